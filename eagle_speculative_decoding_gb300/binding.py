@@ -21,6 +21,7 @@ STATUS = {0: "EAGLE_OK", 1: "EAGLE_ERR_INVALID_ARG", 2: "EAGLE_ERR_UNSUPPORTED",
           6: "EAGLE_ERR_BAD_KV", 7: "EAGLE_ERR_NONFINITE", 8: "EAGLE_ERR_TIMEOUT"}
 
 _P, _I, _F, _Z, _U64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_uint64
+_L, _D = ctypes.c_longlong, ctypes.c_double
 
 _SIGS = {
     "eagle_status_string": (ctypes.c_char_p, [_I]),
@@ -65,6 +66,17 @@ _SIGS = {
                                _I, _P, _P, _P]),
     "eagle_tree_verify_stats": (_I, [_I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _I, _F, _U64, _U64,
                                      _P, _I, _P, _P, _P, _P, _P]),
+    "eagle_rope_table": (_I, [_I, _I, _D, _P, _P]),
+    "eagle_kv_append": (_I, [_P, _P, _P, _L, _L, _L, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _I, _P,
+                             _I, _P, _P]),
+    "eagle_kv_append_kv4": (_I, [_P, _P, _P, _L, _L, _L, _P, _I, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P,
+                                 _F, _F, _I, _P, _I, _P, _P]),
+    "eagle_kv4_read": (_I, [_P, _P, _F, _I, _I, _I, _I, _P, _P]),
+    "eagle_prompt_attn_workspace_size": (_Z, [_I, _I, _I, _I, _I]),
+    "eagle_prompt_attn": (_I, [_P, _L, _P, _P, _I, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P, _Z,
+                               _P, _P]),
+    "eagle_prompt_attn_kv4": (_I, [_P, _L, _P, _P, _P, _P, _F, _F, _I, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I,
+                                   _I, _F, _P, _Z, _P, _P]),
 }
 
 _lib = None
@@ -442,3 +454,113 @@ def eagle_tree_commit(k_tree, v_tree, path_rows, accept_len, k_cache, v_cache, b
         _ptr(accept_len), _ptr(k_cache), _ptr(v_cache), k_cache.shape[0], _ptr(block_table),
         block_table.shape[1], _ptr(ctx_lens), _ptr(features), F, _ptr(features_out),
         _ptr(status), _stream(stream)))
+
+
+# ------------------------------------------------------------------ the prompt path
+# These calls are made once per layer and decoding step, so the marshalling is
+# kept short: plain integers for the pointers, no intermediate objects.
+def _raw_stream(stream):
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _row_stride(name, t, D):
+    """Row stride of a [T, heads, D] array whose heads and channels are contiguous."""
+    st = t.stride()
+    if st[2] != 1 or (st[1] != D and t.shape[1] > 1):
+        raise ValueError(f"{name}: heads and channels must be contiguous, strides {st}")
+    return st[0]
+
+
+def eagle_rope_table(max_pos, D, theta, table=None, stream=None):
+    """cos and sin of pos * theta^(-2i/D): [max_pos, 2, D/2] fp32 on the current device."""
+    if table is None:
+        table = torch.empty((max_pos, 2, D // 2), dtype=torch.float32, device="cuda")
+    _check("eagle_rope_table", lib().eagle_rope_table(max_pos, D, float(theta), _addr(table), _raw_stream(stream)))
+    return table
+
+
+def eagle_kv_append(q, k, v, rope, cu_seqlens, ctx_lens, block_table, k_cache, v_cache, q_out=None, status=None,
+                    stream=None):
+    """Rotate the packed rows to their positions, write q to q_out and k, v into
+    the paged cache (see include/eagle.h).  q and q_out may be None, rope None
+    for no rotation."""
+    T, Hkv, D = k.shape
+    Hq, qs = (0, 0) if q is None else (q.shape[1], _row_stride("q", q, D))
+    if q is not None and (q.shape[0] != T or q.dtype != k.dtype or not q_out.is_contiguous()):
+        raise ValueError("q must have k's rows and dtype, and q_out must be contiguous")
+    if v.shape != k.shape or v.dtype != k.dtype or k_cache.dtype != k.dtype:
+        raise ValueError("k, v and the cache must have one dtype, and k and v one shape")
+    _check("eagle_kv_append", lib().eagle_kv_append(
+        _addr(q), k.data_ptr(), v.data_ptr(), qs, _row_stride("k", k, D), _row_stride("v", v, D), _addr(rope),
+        0 if rope is None else rope.shape[0], cu_seqlens.data_ptr(), ctx_lens.data_ptr(), ctx_lens.shape[0], T, Hq,
+        Hkv, D, _dtype(k), _addr(q_out), k_cache.data_ptr(), v_cache.data_ptr(), k_cache.shape[0],
+        block_table.data_ptr(), block_table.shape[1], _addr(status), _raw_stream(stream)))
+
+
+def eagle_kv_append_kv4(q, k, v, rope, cu_seqlens, ctx_lens, block_table, k_codes, k_scales, v_codes, v_scales,
+                        q_out=None, k_scale=1.0, v_scale=1.0, status=None, stream=None):
+    """eagle_kv_append into 4-bit pages (see include/eagle.h)."""
+    T, Hkv, D = k.shape
+    Hq, qs = (0, 0) if q is None else (q.shape[1], _row_stride("q", q, D))
+    if q is not None and (q.shape[0] != T or q.dtype != k.dtype or not q_out.is_contiguous()):
+        raise ValueError("q must have k's rows and dtype, and q_out must be contiguous")
+    if v.shape != k.shape or v.dtype != k.dtype or k.dtype != torch.bfloat16:
+        raise ValueError("k and v must be bf16 of one shape")
+    _check("eagle_kv_append_kv4", lib().eagle_kv_append_kv4(
+        _addr(q), k.data_ptr(), v.data_ptr(), qs, _row_stride("k", k, D), _row_stride("v", v, D), _addr(rope),
+        0 if rope is None else rope.shape[0], cu_seqlens.data_ptr(), ctx_lens.data_ptr(), ctx_lens.shape[0], T, Hq,
+        Hkv, D, _addr(q_out), k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
+        k_scale, v_scale, k_codes.shape[0], block_table.data_ptr(), block_table.shape[1], _addr(status),
+        _raw_stream(stream)))
+
+
+def eagle_kv4_read(codes, scales, out, scale=1.0, stream=None):
+    """The values of 4-bit pages as an ordinary [pages, 16, Hkv, D] cache."""
+    P, Hkv, _, half = codes.shape
+    _check("eagle_kv4_read", lib().eagle_kv4_read(codes.data_ptr(), scales.data_ptr(), scale, P, Hkv, 2 * half,
+                                                  _dtype(out), out.data_ptr(), _raw_stream(stream)))
+    return out
+
+
+def eagle_prompt_attn_workspace_size(B, T, Hq, Hkv, D):
+    return int(lib().eagle_prompt_attn_workspace_size(B, T, Hq, Hkv, D))
+
+
+def eagle_prompt_attn(q, k_cache, v_cache, block_table, cu_seqlens, ctx_lens, out, lse=None, scale=None, ws=None,
+                      status=None, stream=None):
+    """Causal attention of the packed rows over the paged cache (see include/eagle.h)."""
+    T, Hq, D = q.shape
+    P, page, Hkv, _ = k_cache.shape
+    B = ctx_lens.shape[0]
+    if k_cache.dtype != q.dtype or v_cache.dtype != q.dtype or out.dtype != q.dtype or not out.is_contiguous():
+        raise ValueError("q, the cache and out must have one dtype, and out must be contiguous")
+    if ws is None:
+        ws = workspace(eagle_prompt_attn_workspace_size(B, T, Hq, Hkv, D), q.device)
+    _check("eagle_prompt_attn", lib().eagle_prompt_attn(
+        q.data_ptr(), _row_stride("q", q, D), k_cache.data_ptr(), v_cache.data_ptr(), P, block_table.data_ptr(),
+        block_table.shape[1], cu_seqlens.data_ptr(), ctx_lens.data_ptr(), out.data_ptr(), _addr(lse), B, T, Hq, Hkv,
+        D, page, D ** -0.5 if scale is None else scale, _dtype(q), ws.data_ptr(), ws.numel(), _addr(status),
+        _raw_stream(stream)))
+    return out
+
+
+def eagle_prompt_attn_kv4(q, k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlens, ctx_lens, out, lse=None,
+                          scale=None, k_scale=1.0, v_scale=1.0, ws=None, status=None, stream=None):
+    """eagle_prompt_attn over 4-bit pages (see include/eagle.h)."""
+    T, Hq, D = q.shape
+    P, Hkv, page, _ = k_codes.shape
+    B = ctx_lens.shape[0]
+    if q.dtype != torch.bfloat16 or out.dtype != q.dtype or not out.is_contiguous():
+        raise ValueError("q and out must be bf16, and out must be contiguous")
+    if ws is None:
+        ws = workspace(eagle_prompt_attn_workspace_size(B, T, Hq, Hkv, D), q.device)
+    _check("eagle_prompt_attn_kv4", lib().eagle_prompt_attn_kv4(
+        q.data_ptr(), _row_stride("q", q, D), k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+        v_scales.data_ptr(), k_scale, v_scale, P, block_table.data_ptr(), block_table.shape[1],
+        cu_seqlens.data_ptr(), ctx_lens.data_ptr(), out.data_ptr(), _addr(lse), B, T, Hq, Hkv, D, page,
+        D ** -0.5 if scale is None else scale, ws.data_ptr(), ws.numel(), _addr(status), _raw_stream(stream)))
+    return out

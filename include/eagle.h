@@ -678,6 +678,129 @@ int eagle_tree_verify_noalloc(int B, int R, int V, const int32_t* parent_row,
                               int max_depth, int32_t* accept_len, int32_t* path_rows,
                               int32_t* out_tokens, int32_t* dev_status, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The prompt path: packed rows of many requests against the paged cache.
+ * [M7.5] section 0x03C (the drafter keeps its own K/V for the committed
+ * prefix) and section 0x05D "Feature And KV Commit" (the new frontier token
+ * needs a later target append); [E3] "Stage 2: Verification" starts from a
+ * prefix that is already cached.  These calls put it there and attend to it:
+ * whole prompts, chunks of prompts over a cached context, and single tokens
+ * (n_b = 1) are one form.
+ *   cu_seqlens : [B + 1] int32, cu_seqlens[0] = 0, non-decreasing,
+ *                cu_seqlens[B] = T: request b owns the packed rows
+ *                cu_seqlens[b] .. cu_seqlens[b+1] - 1 (n_b of them, 0 allowed)
+ *   ctx_lens   : [B] int32, the tokens of request b already in the cache; its
+ *                row i stands at position ctx_lens[b] + i.  Not advanced by
+ *                these calls: every layer of a model runs with the same
+ *                ctx_lens, and the caller adds n_b after the last one.
+ *   block_table: [B, max_pages] int32 page ids covering ctx_lens[b] + n_b
+ *                tokens; page_size is 16.
+ * Row arrays q, k, v are [T, heads, D] with heads and channels contiguous and
+ * a stride (in elements, a multiple of 16 bytes) from row to row, so slices
+ * of one fused projection are read in place.
+ *
+ * 4-bit pages ("kv4"): codes [num_pages, Hkv, 16, D/2] uint8 and scales
+ * [num_pages, Hkv, 16, D/16] e4m3 bytes, keys and values alike.  16 channels
+ * of a token and head share one scale byte s; a channel's code c (the even
+ * channel in the low four bits of a byte) has a sign in bit 3 and a magnitude
+ * m in {0, 0.5, 1, 1.5, 2, 3, 4, 6} in bits 0-2, and stands for
+ * k_scale * s * (+-m) (v_scale for values).  k_scale and v_scale are one
+ * number per cache (1 unless the values leave e4m3's range: scales below
+ * 2^-10 read as zero, above 448 saturate).
+ * ---------------------------------------------------------------------- */
+
+/* eagle_rope_table -- cos and sin of pos * theta^(-2 i / D) for positions
+ * 0 .. max_pos - 1 and i < D/2, angles in fp64: table [max_pos, 2, D/2] fp32,
+ * cosines first (16-byte aligned).  Built once per model; any other table of
+ * the same layout (scaled or interpolated frequencies) serves as well.
+ * Limits: D in {64, 128}, max_pos >= 1, theta > 0. */
+int eagle_rope_table(int max_pos, int D, double theta, float* table, void* stream);
+
+/* eagle_kv_append -- rotate and append.  For row t of request b at position
+ * p = ctx_lens[b] + t - cu_seqlens[b], with (c, s) = rope[p] and channel pairs
+ * (i, i + D/2), i < D/2:
+ *   rot(x)_i = x_i c_i - x_{i+D/2} s_i;  rot(x)_{i+D/2} = x_{i+D/2} c_i + x_i s_i
+ *   q_out[t] = rot(q[t]);  k_cache[page, p % 16] = rot(k[t]);
+ *   v_cache[page, p % 16] = v[t],  page = block_table[b, p / 16].
+ * Products and their sum are rounded to fp32 one by one, then once to `dtype`.
+ *   q     : rows of Hq heads, or NULL with Hq = 0 (then q_out is NULL too)
+ *   rope  : [max_pos, 2, D/2] fp32 (eagle_rope_table), or NULL: no rotation
+ *           (max_pos is then ignored)
+ *   q_out : [T, Hq, D]; may be q itself when q_stride = Hq * D
+ *   k_cache, v_cache : [num_pages, 16, Hkv, D] dtype `dtype`, written in place
+ * T = 0 does nothing.  Device-detected: a row outside every request, a
+ * negative ctx_lens or a position past `rope` -> EAGLE_ERR_INVALID_ARG (the
+ * row is skipped); a position past the block table or a page id out of range
+ * -> EAGLE_ERR_BAD_KV (the row's K and V are not written).  Two requests must
+ * not share a page that both append to.
+ * Limits: D in {64, 128}, Hq + 2 Hkv <= 1024; 16-byte aligned arrays. */
+int eagle_kv_append(const void* q, const void* k, const void* v, long long q_stride,
+                    long long k_stride, long long v_stride, const float* rope, int max_pos,
+                    const int32_t* cu_seqlens, const int32_t* ctx_lens, int B, int T, int Hq,
+                    int Hkv, int D, int dtype, void* q_out, void* k_cache, void* v_cache,
+                    int num_pages, const int32_t* block_table, int max_pages,
+                    int32_t* dev_status, void* stream);
+
+/* eagle_kv_append_kv4 -- eagle_kv_append into 4-bit pages (bf16 rows).  With
+ * x = rot(k) or v, unrounded fp32, times the fp32 reciprocal of k_scale or
+ * v_scale, and per group of 16 channels:
+ *   s = e4m3(min(max|x| / 6, 448)) to nearest even; a NaN makes s NaN
+ *   m = the magnitude nearest to |x| / s, ties to the even code (0 if s = 0),
+ * decided by exact comparisons of |x| with s times the midpoints.
+ * Errors and limits as eagle_kv_append; k_scale, v_scale finite and > 0. */
+int eagle_kv_append_kv4(const void* q, const void* k, const void* v, long long q_stride,
+                        long long k_stride, long long v_stride, const float* rope, int max_pos,
+                        const int32_t* cu_seqlens, const int32_t* ctx_lens, int B, int T, int Hq,
+                        int Hkv, int D, void* q_out, uint8_t* k_codes, uint8_t* k_scales,
+                        uint8_t* v_codes, uint8_t* v_scales, float k_scale, float v_scale,
+                        int num_pages, const int32_t* block_table, int max_pages,
+                        int32_t* dev_status, void* stream);
+
+/* eagle_kv4_read -- the values of 4-bit pages, in the layout of an ordinary
+ * cache: out [num_pages, 16, Hkv, D] dtype `dtype` (fp32 product of code,
+ * scale byte and `scale`, rounded once).  For inspection and for handing a
+ * prefix to the calls that read 16- or 32-bit pages.
+ * Limits: D in {64, 128}; 16-byte aligned codes and out. */
+int eagle_kv4_read(const uint8_t* codes, const uint8_t* scales, float scale, int num_pages,
+                   int Hkv, int D, int dtype, void* out, void* stream);
+
+/* eagle_prompt_attn -- causal attention of the packed rows over the paged
+ * cache (their own K/V appended first).  For row t of request b at position p
+ * and query head h (kv head h / (Hq/Hkv)):
+ *   out[t, h] = softmax(scale * q k^T) v over the keys at positions 0 .. p,
+ *   lse[t, h] = natural log of the sum of exp(scale * q k^T).
+ *   q    : rows of Hq heads (positions applied), q_stride elements apart
+ *   out  : [T, Hq, D] dtype `dtype`;  lse : [T, Hq] fp32 or NULL
+ * Keys past a row's position never reach its result, whatever their pages
+ * hold (NaN included), nor do the unused slots of a last page.
+ * T = 0 does nothing.  Device-detected: a malformed cu_seqlens or a negative
+ * ctx_lens -> EAGLE_ERR_INVALID_ARG (the request is skipped, its rows are not
+ * written); more tokens than the block table holds, or a page id out of range
+ * -> EAGLE_ERR_BAD_KV (those keys and values read as zeros).
+ * bf16 runs on the tensor cores with fp32 accumulation and fp32 softmax
+ * statistics; fp32 on the CUDA cores in fp32 arithmetic.
+ * Limits: D in {64, 128}, page_size == 16, Hq % Hkv == 0, Hq / Hkv <= 64,
+ * B <= 65535, scale finite and > 0; q 16-byte aligned, q_stride a multiple of
+ * 16 bytes. */
+size_t eagle_prompt_attn_workspace_size(int B, int T, int Hq, int Hkv, int D);
+int eagle_prompt_attn(const void* q, long long q_stride, const void* k_cache, const void* v_cache,
+                      int num_pages, const int32_t* block_table, int max_pages,
+                      const int32_t* cu_seqlens, const int32_t* ctx_lens, void* out, float* lse,
+                      int B, int T, int Hq, int Hkv, int D, int page_size, float scale, int dtype,
+                      void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/* eagle_prompt_attn_kv4 -- eagle_prompt_attn over 4-bit pages; q and out bf16.
+ * A code times its scale byte is exact in 16 bits, so the products are those
+ * of the values the codes stand for.  Same workspace query; k_scale and
+ * v_scale finite and > 0. */
+int eagle_prompt_attn_kv4(const void* q, long long q_stride, const uint8_t* k_codes,
+                          const uint8_t* k_scales, const uint8_t* v_codes, const uint8_t* v_scales,
+                          float k_scale, float v_scale, int num_pages, const int32_t* block_table,
+                          int max_pages, const int32_t* cu_seqlens, const int32_t* ctx_lens,
+                          void* out, float* lse, int B, int T, int Hq, int Hkv, int D,
+                          int page_size, float scale, void* ws, size_t ws_bytes,
+                          int32_t* dev_status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -53,3 +53,12 @@ from .eagle_oracle import (  # noqa: F401
 )
 from .philox import (  # noqa: F401
     accept_uniforms, bits_to_uniform, philox4x32_10, race_uniforms, race_uniforms_batch)
+from .prompt_oracle import (  # noqa: F401,E402
+    e4m3_byte,
+    e4m3_value,
+    kv4_pack,
+    kv4_unpack,
+    prompt_attn,
+    rotate,
+    row_places,
+)
