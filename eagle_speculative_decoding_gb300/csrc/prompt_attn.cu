@@ -1,11 +1,20 @@
-// Causal attention of the packed rows of many requests over the paged cache.
+// Causal attention of the packed rows of many requests over the paged cache,
+// in 16-bit, 32-bit or 4-bit pages.
 //
 // Source: "M7.5 - EAGLE Feature Drafting: Uncertainty, Dynamic Trees, HASS, and
-// EAGLE-3", section 0x03C (the drafter's committed prefix), 0x05D (rows go to
-// the cache by position).
+// EAGLE-3", section 0x03C (the drafter's committed prefix) and 0x05D (rows go
+// to the cache by position).
 //
-// One warp per (row, query head), the lanes sharing the channels: one pass
-// over the keys with a running maximum and sum.
+// bf16 rows (16- and 4-bit pages): tensor cores.  The rows of a kv head are
+// the (token, grouped query head) pairs of a request in that order, so that
+// all of them share the K/V a CTA stages and a row's last key moves by one
+// every Hq / Hkv rows.  A unit is two tiles of up to 128 such rows of one
+// request and kv head against its 128-key blocks.  Three kernels:
+//   plan    one CTA lists the units from the real lengths; units longer than
+//           a CTA's fair share are cut along the keys; longest pieces first
+//   main    one persistent CTA per SM takes pieces from that list
+//   merge   joins the pieces of cut units
+// fp32 rows: one warp per (row, query head) on the CUDA cores.
 #include <math.h>
 
 #include <algorithm>
@@ -15,6 +24,11 @@
 
 namespace eagle {
 namespace {
+
+constexpr int kBlk = 128;        // keys per block
+constexpr int kTileRows = 128;   // query rows per tile
+constexpr float kRescaleLog2 = 8.f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 struct AttnParams {
   const void* q;
@@ -30,32 +44,1120 @@ struct AttnParams {
   int32_t* status;
 };
 
-enum Source { kF32, kBf16, kKv4 };
+// ------------------------------------------------------------------- plan
+// A piece: key blocks [k0, k1) of unit u of (request b, kv head h); slot >= 0
+// when the unit is cut (its partial result goes there).
+struct __align__(16) Piece {
+  int b, h, u, k0, k1, slot, c0, n, ctx, pad0, pad1, pad2;
+};
+struct __align__(16) Cut {  // a cut unit: its pieces are slots slot .. slot + pieces - 1
+  int h, u, slot, pieces, c0, n, pad0, pad1;
+};
+struct PlanHeader {
+  int pieces, cuts, next, pad;
+};
 
-template <int D, Source S>
-__device__ __forceinline__ void load_row(const void* base, const uint8_t* scales, int page, int slot, int h, int Hkv,
-                                         float* f) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  if (S == kKv4) {
-    const size_t row = ((size_t)page * Hkv + h) * 16 + slot;
-    const uint8_t* c = static_cast<const uint8_t*>(base) + row * (D / 2);
+constexpr int kCand = 6;       // candidate cuts of the plan
+constexpr int kMaxShare = 6;   // pieces per CTA at the finest cut
+__device__ __constant__ const int kShares[kCand] = {0, 1, 2, 3, 4, 6};  // 0: no unit is cut
+
+struct Shape {  // of the bf16 path, on the host and the device
+  int g, tpt, tpu, rows;  // heads per kv head, tokens per tile and unit, rows per slot
+  int ctas, cap_units, cap_pieces, cap_slots;
+  size_t off_pieces, off_cuts, off_ml, off_o, total;
+};
+Shape attn_shape(int B, int T, int Hq, int Hkv, int D) {
+  Shape s;
+  s.g = Hq / Hkv;
+  s.tpt = kTileRows / s.g;
+  s.tpu = 2 * s.tpt;
+  s.rows = std::min(s.tpu, T) * s.g;
+  const int sms = sm_count();
+  s.ctas = sms > 0 ? sms : 152;
+  s.cap_units = T / s.tpu + std::min(B, T);
+  // a unit of L > C blocks makes ceil(L / C) < 2 L / C pieces and the finest C
+  // is total / (kMaxShare * ctas)
+  s.cap_slots = 2 * kMaxShare * s.ctas;
+  s.cap_pieces = s.cap_units * Hkv + s.cap_slots;
+  s.off_pieces = 256;
+  s.off_cuts = round_up(s.off_pieces + sizeof(Piece) * (size_t)s.cap_pieces, 256);
+  s.off_ml = round_up(s.off_cuts + sizeof(Cut) * (size_t)s.cap_slots, 256);
+  s.off_o = round_up(s.off_ml + sizeof(float2) * (size_t)s.cap_slots * s.rows, 256);
+  s.total = s.off_o + sizeof(float) * (size_t)s.cap_slots * s.rows * D + 256;
+  return s;
+}
+
+struct PlanParams {
+  const int32_t *cu, *ctx;
+  int B, T, Hkv, max_pages, tpu, g, ctas, cap_pieces, cap_slots;
+  PlanHeader* hdr;
+  Piece* pieces;
+  Cut* cuts;
+  int32_t* status;
+};
+
+constexpr int kPlanThreads = 1024;
+
+// One CTA.  Warp w takes the requests 32 w .. 32 w + 31 (and so on by 1024);
+// its lanes share the units of those requests.  Sweeps over all units: the
+// total of key blocks, the cost of each candidate cut, the lengths' histogram,
+// and the list.
+__global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanParams p) {
+  __shared__ unsigned long long s_total;
+  __shared__ int s_longest, s_n[kCand], s_cut[kCand], s_units, s_hist[32], s_cursor[32], s_c, s_slots, s_cuts, s_class;
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x < 32) s_hist[threadIdx.x] = 0;
+  if (threadIdx.x < kCand) s_n[threadIdx.x] = s_cut[threadIdx.x] = 0;
+  if (threadIdx.x == 0) {
+    s_total = 0;
+    s_longest = s_units = s_slots = s_cuts = 0;
+  }
+  __syncthreads();
+
+  // f(b, c0, n, ctx, u, key blocks) for every unit; all lanes of a warp call together, `live` lanes have one
+  auto sweep = [&](bool report, auto&& f) {
+    for (int base = warp * 32; base < p.B; base += kPlanThreads) {
+      const int b = base + lane;
+      int c0 = 0, n = 0, ctx = 0;
+      if (b < p.B) {
+        c0 = p.cu[b];
+        const int c1 = p.cu[b + 1];
+        ctx = p.ctx[b];
+        n = c1 - c0;
+        if (c0 < 0 || c1 < c0 || c1 > p.T || ctx < 0) {
+          if (report) set_status(p.status, EAGLE_ERR_INVALID_ARG);
+          n = 0;
+        } else if ((long long)ctx + n > 16ll * p.max_pages) {
+          if (report) set_status(p.status, EAGLE_ERR_BAD_KV);
+          n = 0;
+        }
+      }
+      const int nu = (n + p.tpu - 1) / p.tpu;
+      int end = nu;  // inclusive prefix over the lanes
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int ch = lane + 32 * e;
-      f[e] = kv4_code_value((c[ch >> 1] >> (4 * (ch & 1))) & 15u) * kv4_scale_value(scales[row * (D / 16) + ch / 16]);
+      for (int d = 1; d < 32; d <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, end, d);
+        if (lane >= d) end += x;
+      }
+      const int total = __shfl_sync(0xffffffffu, end, 31);
+      for (int i0 = 0; i0 < total; i0 += 32) {
+        const int i = i0 + lane;
+        int o = 0;  // the lane whose request holds unit i: the first with end > i
+#pragma unroll
+        for (int d = 16; d; d >>= 1)
+          if (__shfl_sync(0xffffffffu, end, o + d - 1) <= i) o += d;
+        o = min(o, 31);
+        const int oc0 = __shfl_sync(0xffffffffu, c0, o), on = __shfl_sync(0xffffffffu, n, o);
+        const int octx = __shfl_sync(0xffffffffu, ctx, o);
+        const int u = i - (__shfl_sync(0xffffffffu, end, o) - __shfl_sync(0xffffffffu, nu, o));
+        const int keys = octx + min(on, (u + 1) * p.tpu);
+        f(i < total, base + o, oc0, on, octx, u, (keys + kBlk - 1) / kBlk);
+      }
     }
-  } else {
-    const size_t at = (((size_t)page * 16 + slot) * Hkv + h) * D + lane;
+  };
+  auto warp_sum = [&](int v) {
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      f[e] = S == kF32 ? static_cast<const float*>(base)[at + 32 * e]
-                       : __bfloat162float(static_cast<const __nv_bfloat16*>(base)[at + 32 * e]);
+    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
+  };
+
+  {
+    unsigned long long sum = 0;
+    int longest = 0, units = 0;
+    sweep(true, [&](bool live, int, int, int, int, int, int L) {
+      if (!live) return;
+      sum += L;
+      longest = max(longest, L);
+      ++units;
+    });
+    if (units) {
+      atomicAdd(&s_total, sum);
+      atomicMax(&s_longest, longest);
+      atomicAdd(&s_units, units);
+    }
+  }
+  __syncthreads();
+  const long long all = (long long)s_total * p.Hkv;  // key blocks of all units
+  // candidate x cuts units longer than C_x = all / (share x ctas)
+  auto cand = [&](int x) -> int {
+    if (kShares[x] == 0) return 0x7fffffff;
+    const long long c = (all + (long long)kShares[x] * p.ctas - 1) / ((long long)kShares[x] * p.ctas);
+    return (int)max(2ll, c);
+  };
+  {
+    int n[kCand] = {}, cut[kCand] = {};
+    sweep(false, [&](bool live, int, int, int, int, int, int L) {
+      if (!live) return;
+#pragma unroll
+      for (int x = 0; x < kCand; ++x) {
+        const int C = cand(x), k = L > C ? (L + C - 1) / C : 1;
+        n[x] += k;
+        cut[x] += k > 1 ? k : 0;
+      }
+    });
+#pragma unroll
+    for (int x = 0; x < kCand; ++x) {
+      const int a = warp_sum(n[x]), b = warp_sum(cut[x]);
+      if (lane == 0 && a) {
+        atomicAdd(&s_n[x], a);
+        atomicAdd(&s_cut[x], b);
+      }
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    // estimated time in blocks per CTA: whole waves of pieces of the mean
+    // length (at least the longest piece), and for each cut piece its
+    // partial result (a block's worth of traffic per 64 rows, written and
+    // read) and a block for its start
+    float best = 3e38f;
+    int C = 0x7fffffff;
+    const float per_cut = 1.f + (float)min(p.tpu, p.T) * (float)p.g / 64.f;
+    for (int x = 0; x < kCand; ++x) {
+      const float N = (float)s_n[x] * p.Hkv;
+      if (N < 1.f || (long long)s_cut[x] * p.Hkv > p.cap_slots) continue;
+      float t = ceilf(N / p.ctas) * ((float)all / N);
+      t = fmaxf(t, (float)min(s_longest, cand(x))) + (float)s_cut[x] * p.Hkv * per_cut / p.ctas;
+      if (t < best) {
+        best = t;
+        C = cand(x);
+      }
+    }
+    s_c = C;
+    s_class = max(1, min(s_longest, C));
+  }
+  __syncthreads();
+  const int C = s_c, top = s_class;
+  auto klass = [&](int len) { return 31 - min(31, (int)((long long)(len - 1) * 32 / top)); };  // 0: the longest
+  sweep(false, [&](bool live, int, int, int, int, int, int L) {
+    if (!live) return;
+    const int k = L > C ? (L + C - 1) / C : 1;
+    atomicAdd(&s_hist[klass((L + k - 1) / k)], k * p.Hkv);
+  });
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int v = s_hist[threadIdx.x];
+    int end = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, end, d);
+      if (lane >= d) end += x;
+    }
+    s_cursor[threadIdx.x] = end - v;
+    if (threadIdx.x == 31) {
+      // a malformed cu_seqlens can list rows twice: what does not fit is left out
+      p.hdr->pieces = min(end, p.cap_pieces);
+      p.hdr->next = 0;
+      if (end > p.cap_pieces) set_status(p.status, EAGLE_ERR_INVALID_ARG);
+    }
+  }
+  __syncthreads();
+  sweep(false, [&](bool live, int b, int c0, int n, int ctx, int u, int L) {
+    if (!live) return;
+    const int k = L > C ? (L + C - 1) / C : 1;
+    int at = atomicAdd(&s_cursor[klass((L + k - 1) / k)], k * p.Hkv);
+    int slot = -1, cut = 0;
+    if (k > 1) {
+      slot = atomicAdd(&s_slots, k * p.Hkv);
+      cut = atomicAdd(&s_cuts, p.Hkv);
+    }
+    for (int h = 0; h < p.Hkv; ++h) {
+      if (k > 1 && slot + k <= p.cap_slots) p.cuts[cut + h] = Cut{h, u, slot, k, c0, n, 0, 0};
+      for (int x = 0; x < k; ++x, ++at)
+        if (at < p.cap_pieces)
+          p.pieces[at] = Piece{b, h, u, (int)((long long)L * x / k), (int)((long long)L * (x + 1) / k),
+                               k > 1 ? slot + x : -1, c0, n, ctx, 0, 0, 0};
+      if (k > 1) slot += k;
+    }
+  });
+  __syncthreads();
+  if (threadIdx.x == 0) p.hdr->cuts = min(s_cuts, p.cap_slots);
+}
+
+// ------------------------------------------------------------------- main
+// 512 threads, one CTA per SM:
+//   warps 0-3    K/V producers: 16-byte asynchronous copies from the pages to
+//                128-byte-swizzled stages (16 tokens of a page are 16 rows
+//                Hkv D apart: copies by threads reach what boxes of a tensor
+//                map, 2 KB each, do not), or, for 4-bit pages, copies of
+//                the codes to a raw ring and from there exact fp16 values to
+//                the stages
+//   warp 4       issues the MMAs (one thread)
+//   warp 5       takes pieces from the list, ahead of the others
+//   warps 6-7    Q loaders
+//   warps 8-11   softmax of tile 0, warps 12-15 of tile 1: a thread is a row
+//                (a TMEM lane) and holds the block's 128 scores
+// S of a tile (fp32, 128 columns), its weights P (16-bit, over S) and O (D
+// columns) live in TMEM; P is the A operand of P V from there.  Per tile the
+// MMA thread issues P V(i), then S(i + 1): while one tile's softmax runs, the
+// other tile's MMAs do.  S(i + 1) follows P V(i) in the pipe, so that the
+// softmax that sees S(i + 1) complete may rescale O.
+// A unit of at most 128 rows (single tokens, short chunks) would leave one
+// tile idle and the chain S - softmax - P V exposed: then both tiles hold the
+// same rows, tile 0 takes the even blocks and tile 1 the odd ones, and tile
+// 0's warps join the two at the end (same TMEM lanes).
+constexpr int kThreads = 512;
+constexpr int kSlots = 4;  // pieces known ahead
+
+template <int D, bool KV4>
+struct Cfg {
+  static constexpr uint32_t kHalf = kTileRows * 128u;        // 64 columns of 128 rows
+  static constexpr uint32_t kTile = kHalf * (D / 64);         // one Q, K or V tile
+  static constexpr int kStages = KV4 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
+  static constexpr uint32_t kRawCodes = kBlk * D / 2, kRaw = kRawCodes + kBlk * D / 16;
+  static constexpr int kRawRing = 6;
+  static constexpr uint32_t kSmem = 2 * kTile + kStages * kTile + (KV4 ? kRawRing * kRaw : 0) + 1024;
+  static constexpr uint32_t kColO = 256;  // S of tile t at t * 128, O at kColO + t * D
+};
+
+struct MainParams {
+  AttnParams a;
+  float scale_log2;
+  int g, tpt, tpu, slot_rows;
+  const PlanHeader* hdr;
+  int* next;
+  const Piece* pieces;
+  float2* part_ml;
+  float* part_o;
+};
+
+template <int ST, bool KV4>
+struct Bars {
+  uint64_t kv_full[ST], kv_empty[ST], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], x_stat, x_done;
+  uint64_t slot_full[kSlots], slot_empty[kSlots], drain;
+  uint32_t tmem_base;
+  int abort_flag;
+  Piece piece[kSlots];      // b < 0: no more work
+  int bad_v[kSlots];        // a masked block of the piece holds non-finite values
+  float q_fac[2][2][KV4 ? kTileRows : 1];  // 4-bit: the rows' powers of two, by a tile's use parity and tile
+  float2 x_ml[kTileRows];
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// at most n of the newest groups may still be in flight
+__device__ __forceinline__ void cp_async_wait_n(int n) {
+  switch (n) {
+    case 0: cp_async_wait<0>(); break;
+    case 1: cp_async_wait<1>(); break;
+    case 2: cp_async_wait<2>(); break;
+    case 3: cp_async_wait<3>(); break;
+    case 4: cp_async_wait<4>(); break;
+    default: cp_async_wait<5>(); break;
+  }
+}
+// O += P V with P in tensor memory (A operand: 16 keys = 8 columns of pairs).
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t pack16(float a, float b) {
+  if (F16) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Blocks of a piece that tile t takes, and the block its i-th one is.
+struct TileWork {
+  int rows0, rows1;  // valid rows of the tiles
+  int n0, n1;        // blocks of the tiles
+  bool twin;         // both tiles hold the same rows and take alternate blocks
+  __device__ __forceinline__ int n(int t) const { return t ? n1 : n0; }
+  __device__ __forceinline__ int rows(int t) const { return t ? rows1 : rows0; }
+  __device__ __forceinline__ int blk(int t, int i) const { return twin ? 2 * i + t : i; }
+};
+__device__ __forceinline__ TileWork tile_work(const Piece& w, int tpt, int tpu, int g) {
+  TileWork r;
+  const int t0 = w.u * tpu, left = w.n - t0, nblk = w.k1 - w.k0;
+  r.twin = left <= tpt;
+  r.rows0 = min(left, tpt) * g;
+  if (r.twin) {
+    r.rows1 = r.rows0;
+    r.n0 = (nblk + 1) / 2;
+    r.n1 = nblk / 2;
+  } else {
+    r.rows1 = min(left - tpt, tpt) * g;
+    // tile 0's last token may need fewer blocks than tile 1's
+    r.n0 = max(0, min(nblk, (w.ctx + t0 + tpt - 1) / kBlk + 1 - w.k0));
+    r.n1 = nblk;
+  }
+  return r;
+}
+
+// Adds to a row's written result the non-finite values it sees in the masked
+// blocks, which the stages held as zeros (cold: only when there are any).
+template <int D, bool KV4, typename T>
+__device__ __noinline__ void add_nonfinite(const AttnParams& a, const Piece& w, int first, int pos, T* row) {
+  for (int k = max(first, w.k0 * kBlk); k <= pos && k < w.k1 * kBlk; ++k) {
+    const int page = a.table[(size_t)w.b * a.max_pages + k / 16];
+    if (page < 0 || page >= a.num_pages) continue;
+    for (int d = 0; d < D; ++d) {
+      float v;
+      if (KV4)
+        v = kv4_scale_value(a.vs[(((size_t)page * a.Hkv + w.h) * 16 + (k & 15)) * (D / 16) + d / 16]);
+      else
+        v = __bfloat162float(
+            static_cast<const __nv_bfloat16*>(a.vc)[(((size_t)page * 16 + (k & 15)) * a.Hkv + w.h) * D + d]);
+      if (!isfinite(v)) row[d] = (T)((float)row[d] + v);
+    }
   }
 }
 
-template <int D, Source S>
-__global__ void __launch_bounds__(128) prompt_attn_kernel(const AttnParams p) {
+template <int D, bool KV4>
+__global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainParams p) {
+  using C = Cfg<D, KV4>;
+  using Sb = Bars<C::kStages, KV4>;
+  constexpr int ST = C::kStages;
+  constexpr uint32_t kFmt = KV4 ? 0u : 1u;  // fp16 or bf16 operands
+  static_assert(C::kSmem + sizeof(Sb) <= 232448, "shared memory of a CTA");
+  __shared__ Sb sb;
+  extern __shared__ unsigned char dsm[];
+  const uint32_t base = (smem_u32(dsm) + 1023u) & ~1023u;
+  unsigned char* gbase = dsm + (base - smem_u32(dsm));
+  const uint32_t sQ = 0, sKV = 2 * C::kTile, sRaw = sKV + ST * C::kTile;  // offsets from base
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &sb.abort_flag;
+  const AttnParams& a = p.a;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(smem_u32(&sb.kv_full[i]), 4);
+      mbar_init(smem_u32(&sb.kv_empty[i]), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(smem_u32(&sb.q_full[t]), 2);
+      mbar_init(smem_u32(&sb.q_empty[t]), 1);
+      mbar_init(smem_u32(&sb.s_full[t]), 1);
+      mbar_init(smem_u32(&sb.p_full[t]), 4);
+      mbar_init(smem_u32(&sb.o_full[t]), 1);
+    }
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(smem_u32(&sb.slot_full[i]), 1);
+      mbar_init(smem_u32(&sb.slot_empty[i]), 15);  // warps 0-4 and 6-15
+    }
+    mbar_init(smem_u32(&sb.x_stat), 4);
+    mbar_init(smem_u32(&sb.x_done), 4);
+    mbar_init(smem_u32(&sb.drain), 1);
+    sb.abort_flag = 0;
+    fence_mbar_init();
+  }
+  pdl_wait();  // the plan is complete, and the previous grid's TMEM is free
+  if (warp == 4) {
+    tmem_alloc(smem_u32(&sb.tmem_base), 512u);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_trigger();
+  const uint32_t tmem = sb.tmem_base;
+
+  auto warp_wait = [&](uint64_t& bar, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), parity, abort_flag)) != 0;
+  };
+  // The ps-th piece: false at the end of the list (or on abort).
+  auto get_piece = [&](int ps, Piece& w) -> bool {
+    if (!warp_wait(sb.slot_full[ps % kSlots], (uint32_t)(ps / kSlots) & 1u)) return false;
+    w = sb.piece[ps % kSlots];
+    return w.b >= 0;
+  };
+  auto release_piece = [&](int ps) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sb.slot_empty[ps % kSlots]));
+  };
+
+  if (warp < 4) {
+    // ------------------------------------------------------ K/V producers
+    // registers move from the copying and issuing warps to the softmax:
+    // 256 x 64 + 256 x 192 = the 512 x 128 of the launch
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    const int tid = threadIdx.x;
+    int st = 0;
+    uint32_t ph = 0;  // stage and phase of the next tile to be filled
+    bool ok = true;
+    if constexpr (!KV4) {
+      constexpr int CPR = D / 8, RPI = 128 / CPR, IT = kBlk / RPI;  // chunks per row, rows per iteration
+      const int row0 = tid / CPR, c = tid % CPR;
+      const uint32_t dst0 = (uint32_t)(c / 8) * C::kHalf + (uint32_t)row0 * 128u + (uint32_t)(((c % 8) ^ (row0 & 7)) << 4);
+      const size_t tok_bytes = (size_t)a.Hkv * D * 2, page_bytes = tok_bytes * 16;
+      int pending = 0, ast = 0;  // tiles issued but not handed on, and the stage of the oldest
+      uint32_t info = 0;         // per stage: bits 0-1 piece slot, bit 3 V tile of a masked block
+      auto hand_on = [&]() {
+        const uint32_t x = (info >> (4 * ast)) & 15u;
+        if (x & 8u) {
+          // V of a masked block: a weight of zero does not silence a NaN or
+          // an infinity in the matrix product, so they are taken out here
+          // and added at the end to the rows that see them
+          bool found = false;
+#pragma unroll 4
+          for (int i = 0; i < IT; ++i) {
+            uint4* q = reinterpret_cast<uint4*>(gbase + sKV + ast * C::kTile + dst0 + (uint32_t)i * (RPI * 128u));
+            uint4 v = *q;
+            uint32_t* e = &v.x;
+            bool hit = false;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if ((e[k] & 0x7f80u) == 0x7f80u) e[k] &= 0xffff0000u, hit = true;
+              if ((e[k] & 0x7f800000u) == 0x7f800000u) e[k] &= 0x0000ffffu, hit = true;
+            }
+            if (hit) *q = v, found = true;
+          }
+          if (found) *(volatile int*)&sb.bad_v[x & 3u] = 1;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sb.kv_full[ast]));
+        if (++ast == ST) ast = 0;
+        --pending;
+      };
+      // before a wait that may block, everything issued is handed on: what
+      // this wait is for may depend on it
+      auto flush = [&]() {
+        cp_async_wait<0>();
+        while (pending) hand_on();
+      };
+      Piece w;
+      for (int ps = 0;; ++ps) {
+        if (!__all_sync(0xffffffffu, mbar_try_wait(smem_u32(&sb.slot_full[ps % kSlots]), (uint32_t)(ps / kSlots) & 1u)))
+          flush();
+        if (!get_piece(ps, w)) break;
+        const int n_keys = w.ctx + w.n, masked_from = w.ctx + w.u * p.tpu;  // the first row's position
+        const char* kb_ = static_cast<const char*>(a.kc) + (size_t)w.h * D * 2 + c * 16;
+        const char* vb_ = static_cast<const char*>(a.vc) + (size_t)w.h * D * 2 + c * 16;
+        const int32_t* tab = a.table + (size_t)w.b * a.max_pages;
+        auto page_of = [&](int blk) -> int {  // lane q < 8: page q of the block, -1 past the keys or out of range
+          const int k = blk * kBlk + (lane & 7) * 16;
+          if (blk >= w.k1 || k >= n_keys) return -1;
+          const int pg = tab[k / 16];
+          if (pg < 0 || pg >= a.num_pages) {
+            set_status(a.status, EAGLE_ERR_BAD_KV);
+            return -1;
+          }
+          return pg;
+        };
+        int pg_next = page_of(w.k0);
+        for (int blk = w.k0; ok && blk < w.k1; ++blk) {
+          const int pg = pg_next;
+          pg_next = page_of(blk + 1);
+          const int key0 = blk * kBlk;
+          const bool masked = key0 + kBlk - 1 > masked_from;
+#pragma unroll
+          for (int o = 0; o < 2; ++o) {
+            if (!__all_sync(0xffffffffu, mbar_try_wait(smem_u32(&sb.kv_empty[st]), ph ^ 1u))) {
+              flush();
+              ok = warp_wait(sb.kv_empty[st], ph ^ 1u);
+              if (!ok) break;
+            }
+            const uint32_t dst = base + sKV + st * C::kTile + dst0;
+            const char* src = o ? vb_ : kb_;
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+              const int r = i * RPI + row0;
+              const int pq = __shfl_sync(0xffffffffu, pg, (i * RPI) / 16);
+              const bool live = pq >= 0 && key0 + r < n_keys;
+              cp_async16(dst + (uint32_t)i * (RPI * 128u),
+                         live ? src + (size_t)pq * page_bytes + (size_t)(r & 15) * tok_bytes : src, live);
+            }
+            cp_async_commit();
+            info = (info & ~(15u << (4 * st))) | ((uint32_t)(ps % kSlots) | (o && masked ? 8u : 0u)) << (4 * st);
+            if (++st == ST) {
+              st = 0;
+              ph ^= 1u;
+            }
+            if (++pending == ST) {
+              cp_async_wait<ST - 1>();
+              hand_on();
+            }
+          }
+        }
+        if (!ok) break;
+        release_piece(ps);
+      }
+      if (ok) flush();
+      cp_async_wait<0>();
+    } else {
+      constexpr int R = C::kRawRing;
+      constexpr int CC = 32 * (D / 2) / 16 / 32;       // code copies per lane: a warp has 32 rows
+      constexpr int SCH = 32 * (D / 16) / 16;          // 16-byte scale chunks of 32 rows
+      constexpr int PC = 16 * (D / 2) / 16;            // code chunks of a page and head
+      constexpr int PS = 16 * (D / 16) / 16;           // scale chunks of a page and head
+      int issued = 0, consumed = 0;
+      // the cursor of the copies runs ahead of that of the conversion
+      Piece iw;
+      int ips = 0, iblk = 0, iop = 0, ipg = -1;
+      bool have = false, last = false;
+      auto issue = [&](bool must) -> bool {
+        if (!have) {
+          if (last) return false;
+          if (!must && !__all_sync(0xffffffffu, mbar_try_wait(smem_u32(&sb.slot_full[ips % kSlots]),
+                                                              (uint32_t)(ips / kSlots) & 1u)))
+            return false;
+          if (!get_piece(ips, iw)) {
+            last = true;
+            return false;
+          }
+          have = true;
+          iblk = iw.k0;
+          iop = 0;
+        }
+        const int n_keys = iw.ctx + iw.n, key0 = iblk * kBlk;
+        if (iop == 0) {
+          // lane q < 2: page q of this warp's 32 keys
+          const int k = key0 + warp * 32 + (lane & 1) * 16;
+          ipg = -1;
+          if (k < n_keys) {
+            ipg = a.table[(size_t)iw.b * a.max_pages + k / 16];
+            if (ipg < 0 || ipg >= a.num_pages) {
+              set_status(a.status, EAGLE_ERR_BAD_KV);
+              ipg = -1;
+            }
+          }
+        }
+        const uint8_t* codes = static_cast<const uint8_t*>(iop ? a.vc : a.kc);
+        const uint8_t* scales = iop ? a.vs : a.ks;
+        const uint32_t dst = base + sRaw + (uint32_t)(issued % R) * C::kRaw;
+#pragma unroll
+        for (int i = 0; i < CC; ++i) {
+          const int ch = i * 32 + lane, q = ch / PC;  // chunk of the warp's rows, its page
+          const int pq = __shfl_sync(0xffffffffu, ipg, q);
+          const bool live = pq >= 0;
+          cp_async16(dst + (uint32_t)(warp * 32 * (D / 2) + ch * 16),
+                     live ? codes + ((size_t)pq * a.Hkv + iw.h) * (16 * D / 2) + (ch % PC) * 16 : codes, live);
+        }
+        {
+          const int ch = lane % SCH, q = ch / PS;
+          const int pq = __shfl_sync(0xffffffffu, ipg, q);
+          const bool live = pq >= 0;
+          if (lane < SCH)
+            cp_async16(dst + C::kRawCodes + (uint32_t)(warp * 32 * (D / 16) + ch * 16),
+                       live ? scales + ((size_t)pq * a.Hkv + iw.h) * (16 * D / 16) + (ch % PS) * 16 : scales, live);
+        }
+        cp_async_commit();
+        ++issued;
+        if (++iop == 2) {
+          iop = 0;
+          if (++iblk == iw.k1) {
+            have = false;
+            ++ips;
+          }
+        }
+        return true;
+      };
+      Piece w;
+      for (int ps = 0; ok; ++ps) {
+        if (!get_piece(ps, w)) break;
+        const int n_keys = w.ctx + w.n, masked_from = w.ctx + w.u * p.tpu;
+        for (int blk = w.k0; ok && blk < w.k1; ++blk) {
+          const int key0 = blk * kBlk;
+          const bool masked = key0 + kBlk - 1 > masked_from;
+#pragma unroll 1
+          for (int o = 0; o < 2; ++o) {
+            while (issued - consumed < R && issue(issued == consumed)) {
+            }
+            cp_async_wait_n(issued - consumed - 1);
+            __syncwarp();
+            ok = warp_wait(sb.kv_empty[st], ph ^ 1u);
+            if (!ok) break;
+            const unsigned char* raw = gbase + sRaw + (uint32_t)(consumed % R) * C::kRaw;
+            unsigned char* stage = gbase + sKV + st * C::kTile;
+            bool found = false;
+            // a lane takes 32 channels of a row: eight lanes at a time write
+            // 4 rows x 2 chunks, whose swizzled places are all different
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+              const int r = warp * 32 + (D == 128 ? (i >> 1) * 16 : i * 16) + (lane >> 1);
+              const int ch = (D == 128 ? (i & 1) * 2 : 0) + (lane & 1);
+              const uint4 cw = *reinterpret_cast<const uint4*>(raw + r * (D / 2) + ch * 16);
+              uint32_t sc = *reinterpret_cast<const uint16_t*>(raw + C::kRawCodes + r * (D / 16) + ch * 2);
+              if (key0 + r >= n_keys) sc = 0;
+              if (o && masked) {
+                if ((sc & 0x7fu) == 0x7fu) sc &= 0xff00u, found = true;
+                if ((sc & 0x7f00u) == 0x7f00u) sc &= 0x00ffu, found = true;
+              }
+              uint32_t s2;
+              asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(s2) : "r"(sc));
+              const uint32_t sl = __byte_perm(s2, s2, 0x1010), sh = __byte_perm(s2, s2, 0x3232);
+              const uint32_t cwv[4] = {cw.x, cw.y, cw.z, cw.w};
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                uint32_t v[4];
+                asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+                    "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+                    "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+                    : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                    : "r"(cwv[x]));
+                const uint32_t m = x < 2 ? sl : sh;
+#pragma unroll
+                for (int y = 0; y < 4; ++y)  // exact: at most six significant bits, all multiples of 2^-10
+                  asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(v[y]) : "r"(m));
+                *reinterpret_cast<uint4*>(stage + (uint32_t)(ch / 2) * C::kHalf + r * 128 +
+                                          ((((ch & 1) * 4 + x) ^ (r & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+              }
+            }
+            if (found) *(volatile int*)&sb.bad_v[ps % kSlots] = 1;
+            fence_proxy_async_smem();
+            __syncwarp();  // also: the raw slot may be filled again
+            if (lane == 0) mbar_arrive(smem_u32(&sb.kv_full[st]));
+            ++consumed;
+            if (++st == ST) {
+              st = 0;
+              ph ^= 1u;
+            }
+          }
+        }
+        if (!ok) break;
+        release_piece(ps);
+      }
+      cp_async_wait<0>();
+    }
+  } else if (warp < 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == 4) {
+    // ---------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = mma_idesc(kFmt, 128, kBlk), idesc_pv = mma_idesc_bmn(kFmt, 128, D);
+      const uint64_t dq0 = smem_desc_sw128(base + sQ), dk0 = smem_desc_sw128(base + sKV);
+      const uint64_t dv0 = smem_desc_sw128_mn(base + sKV, C::kHalf);
+      uint32_t pph[2] = {0, 0}, qph[2] = {0, 0};
+      int tile0 = 0;  // number of K/V tiles before this piece
+      auto bar_wait = [&](uint64_t& b, uint32_t parity) { return mbar_wait(smem_u32(&b), parity, abort_flag); };
+      bool ok = true;
+      for (int ps = 0; ok; ++ps) {
+        if (!bar_wait(sb.slot_full[ps % kSlots], (uint32_t)(ps / kSlots) & 1u)) break;
+        const Piece w = sb.piece[ps % kSlots];
+        if (w.b < 0) break;
+        const TileWork tw = tile_work(w, p.tpt, p.tpu, p.g);
+        // S_t(i) = Q_t K^T
+        auto issue_s = [&](int t, int i) -> bool {
+          const int kt = tile0 + 2 * tw.blk(t, i), st = kt % ST;
+          if (i == 0) {
+            if (!bar_wait(sb.q_full[t], qph[t])) return false;
+            qph[t] ^= 1u;
+          }
+          if (!bar_wait(sb.kv_full[st], (uint32_t)(kt / ST) & 1u)) return false;
+          tc_fence_after();
+          const uint64_t dq = dq0 + (uint64_t)((t * C::kTile) >> 4), dk = dk0 + (uint64_t)((st * C::kTile) >> 4);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = ((uint32_t)(k >> 2) * C::kHalf + (uint32_t)(k & 3) * 32u) >> 4;
+            mma_bf16(tmem + (uint32_t)(t * kBlk), dq + off, dk + off, idesc_s, k > 0 ? 1u : 0u);
+          }
+          mma_commit(smem_u32(&sb.s_full[t]));
+          // the tile that reads a K stage last frees it
+          if (tw.twin || t == 1) mma_commit(smem_u32(&sb.kv_empty[st]));
+          if (i + 1 == tw.n(t)) mma_commit(smem_u32(&sb.q_empty[t]));
+          return true;
+        };
+        auto issue_pv = [&](int t, int i) -> bool {
+          const int vt = tile0 + 2 * tw.blk(t, i) + 1, st = vt % ST;
+          if (!bar_wait(sb.kv_full[st], (uint32_t)(vt / ST) & 1u) || !bar_wait(sb.p_full[t], pph[t])) return false;
+          pph[t] ^= 1u;
+          tc_fence_after();
+          const uint64_t dv = dv0 + (uint64_t)((st * C::kTile) >> 4);
+#pragma unroll
+          for (int k = 0; k < kBlk / 16; ++k)
+            mma_f16_ts(tmem + C::kColO + (uint32_t)(t * D), tmem + (uint32_t)(t * kBlk + k * 8), dv + (uint32_t)k * 128u,
+                       idesc_pv, (i > 0 || k > 0) ? 1u : 0u);
+          if (tw.twin || t == 1) mma_commit(smem_u32(&sb.kv_empty[st]));
+          if (i + 1 == tw.n(t)) mma_commit(smem_u32(&sb.o_full[t]));
+          return true;
+        };
+        for (int t = 0; t < 2 && ok; ++t)
+          if (tw.n(t) > 0) ok = issue_s(t, 0);
+        const int iters = max(tw.n0, tw.n1);
+        for (int i = 0; i < iters && ok; ++i)
+          for (int t = 0; t < 2 && ok; ++t) {
+            if (i < tw.n(t)) ok = issue_pv(t, i);
+            if (ok && i + 1 < tw.n(t)) ok = issue_s(t, i + 1);
+          }
+        if (!ok) break;
+        tile0 += 2 * (w.k1 - w.k0);
+        mbar_arrive(smem_u32(&sb.slot_empty[ps % kSlots]));
+      }
+      // every MMA completes before tensor memory is freed
+      mma_commit(smem_u32(&sb.drain));
+      const unsigned long long t0 = globaltimer_ns();
+      while (!mbar_try_wait(smem_u32(&sb.drain), 0) && globaltimer_ns() - t0 < 100000000ull) {
+      }
+    }
+    __syncwarp();
+    } else if (warp == 5) {
+    // ----------------------------------------------------------- scheduler
+    if (lane == 0) {
+      const int total = p.hdr->pieces;
+      for (int ps = 0;; ++ps) {
+        const int slot = ps % kSlots;
+        if (!mbar_wait(smem_u32(&sb.slot_empty[slot]), ((uint32_t)(ps / kSlots) & 1u) ^ 1u, abort_flag)) break;
+        const int i = atomicAdd(p.next, 1);
+        if (i < total)
+          sb.piece[slot] = p.pieces[i];
+        else
+          sb.piece[slot].b = -1;
+        sb.bad_v[slot] = 0;
+        mbar_arrive(smem_u32(&sb.slot_full[slot]));
+        if (i >= total) break;
+      }
+    }
+    __syncwarp();
+    } else {
+    // ----------------------------------------------------------- Q loaders
+    constexpr int CPR = D / 8, RPI = 64 / CPR;  // rows per iteration of the 64 threads
+    const int tid = threadIdx.x - 192, row0 = tid / CPR, c = tid % CPR;
+    int uses[2] = {0, 0};
+    bool ok = true;
+    Piece w;
+    for (int ps = 0; ok; ++ps) {
+      if (!get_piece(ps, w)) break;
+      const TileWork tw = tile_work(w, p.tpt, p.tpu, p.g);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (!ok || tw.n(t) == 0) continue;
+        ok = warp_wait(sb.q_empty[t], ((uint32_t)uses[t] & 1u) ^ 1u);
+        if (!ok) break;
+        const int rows = tw.rows(t);
+        const size_t tok0 = (size_t)w.c0 + (size_t)w.u * p.tpu + (tw.twin ? 0 : t * p.tpt);
+        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + tok0 * a.q_stride + (size_t)w.h * p.g * D + c * 8;
+        for (int r0 = 0; r0 < rows; r0 += 4 * RPI) {
+          uint4 v[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int r = r0 + x * RPI + row0;
+            const bool live = r < rows;
+            const __nv_bfloat16* src = live ? q + (size_t)(r / p.g) * a.q_stride + (size_t)(r % p.g) * D : q;
+            const uint32_t off = sQ + t * C::kTile + (uint32_t)(c / 8) * C::kHalf + (uint32_t)r * 128u +
+                                 (uint32_t)(((c % 8) ^ (r & 7)) << 4);
+            if constexpr (KV4)
+              v[x] = live ? *reinterpret_cast<const uint4*>(src) : make_uint4(0u, 0u, 0u, 0u);
+            else if (live)
+              cp_async16(base + off, src, true);
+          }
+          if constexpr (KV4) {
+            // rows as fp16, each scaled by a power of two to [1, 2) at its
+            // largest: bf16's 8 bits fit fp16's 11, and what is below 2^-14
+            // of the row's largest keeps an absolute error of 2^-25 of it
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int r = r0 + x * RPI + row0;
+              const uint32_t e[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+              uint32_t mx = 0;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) mx = max(mx, max(e[k] & 0x7fffu, (e[k] >> 16) & 0x7fffu));
+#pragma unroll
+              for (int d = CPR / 2; d; d >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+              const int k2 = min(126, max(-126, (int)(mx >> 7) - 127));
+              const float down = __uint_as_float((uint32_t)(127 - k2) << 23);
+              uint32_t h[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                h[k] = pack16<true>(__uint_as_float(e[k] << 16) * down, __uint_as_float(e[k] & 0xffff0000u) * down);
+              if (r < rows) {
+                *reinterpret_cast<uint4*>(gbase + sQ + t * C::kTile + (uint32_t)(c / 8) * C::kHalf + (uint32_t)r * 128u +
+                                          (uint32_t)(((c % 8) ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                if (c == 0) sb.q_fac[uses[t] & 1][t][r] = __uint_as_float((uint32_t)(127 + k2) << 23);
+              }
+            }
+          }
+        }
+        if constexpr (!KV4) {
+          cp_async_commit();
+          cp_async_wait<0>();
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sb.q_full[t]));
+        ++uses[t];
+      }
+      if (!ok) break;
+      release_piece(ps);
+    }
+    }
+  } else {
+    // ------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    const int t = (warp - 8) >> 2, q4 = warp & 3, row = q4 * 32 + lane;
+    const uint32_t lane_addr = (uint32_t)(q4 * 32) << 16;
+    const uint32_t s_addr = tmem + lane_addr + (uint32_t)(t * kBlk);
+    const uint32_t o_addr = tmem + lane_addr + C::kColO + (uint32_t)(t * D);
+    uint32_t sph = 0, oph = 0, xph = 0;
+    int uses = 0;
+    bool ok = true;
+    Piece w;
+    for (int ps = 0; ok; ++ps) {
+      if (!get_piece(ps, w)) break;
+      const TileWork tw = tile_work(w, p.tpt, p.tpu, p.g);
+      const int n = tw.n(t), rows = tw.rows(t);
+      const bool quad_live = q4 * 32 < rows, row_ok = row < rows;
+      const int tok = w.u * p.tpu + (tw.twin ? 0 : t * p.tpt) + row / p.g;
+      const int pos = row_ok ? w.ctx + tok : 0x7fffffff;
+      float m = -INFINITY, l = 0.f, sl2 = p.scale_log2;
+      for (int i = 0; i < n; ++i) {
+        ok = warp_wait(sb.s_full[t], sph);
+        if (!ok) break;
+        sph ^= 1u;
+        tc_fence_after();
+        if (quad_live) {
+          if (KV4 && i == 0) sl2 *= row_ok ? sb.q_fac[uses & 1][t][row] : 1.f;
+          uint32_t r[kBlk];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32_issue(s_addr + (uint32_t)(c * 32), r + c * 32);
+          tmem_wait_ld();
+          const int lim = pos - (w.k0 + tw.blk(t, i)) * kBlk;  // the last visible column
+          if (!__all_sync(0xffffffffu, lim >= kBlk - 1)) {
+#pragma unroll
+            for (int c = 0; c < kBlk; ++c) r[c] = c <= lim ? r[c] : 0xff800000u;
+          }
+          float mx[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) mx[c] = fmaxf(__uint_as_float(r[c]), __uint_as_float(r[c + 4]));
+#pragma unroll
+          for (int c = 8; c < kBlk; c += 8)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              mx[x] = fmaxf(fmaxf(mx[x], __uint_as_float(r[c + x])), __uint_as_float(r[c + x + 4]));
+          const float bm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+          // m is the reference of O and l: it moves, and both are rescaled,
+          // only when a block's maximum exceeds it by 2^8
+          const bool need = bm > m + kRescaleLog2;
+          const bool resc = need && m != -INFINITY;
+          if (__any_sync(0xffffffffu, resc)) {
+            const float alpha = resc ? ex2_approx(m - bm) : 1.f;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32_issue(o_addr + (uint32_t)(c * 32), o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+              tmem_st32(o_addr + (uint32_t)(c * 32), o);
+            }
+            l *= alpha;
+          }
+          if (need) m = bm;
+          const float neg_m = m == -INFINITY ? 0.f : -m;
+          const uint64_t sc2 = pack2(sl2, sl2), nm2 = pack2(neg_m, neg_m);
+          uint64_t ls[2] = {0ull, 0ull};
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              float e0, e1;
+              unpack2(fma2(pack2(__uint_as_float(r[hf * 64 + 2 * k]), __uint_as_float(r[hf * 64 + 2 * k + 1])), sc2, nm2),
+                      e0, e1);
+              e0 = ex2_approx(e0);
+              e1 = ex2_approx(e1);
+              ls[k & 1] = add2(ls[k & 1], pack2(e0, e1));
+              pk[k] = pack16<KV4>(e0, e1);
+            }
+            tmem_st32(s_addr + (uint32_t)(hf * 32), pk);
+          }
+          float l0, l1;
+          unpack2(add2(ls[0], ls[1]), l0, l1);
+          l += l0 + l1;
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sb.p_full[t]));
+      }
+      if (!ok) break;
+      if (n > 0) {
+        ++uses;
+        ok = warp_wait(sb.o_full[t], oph);
+        if (!ok) break;
+        oph ^= 1u;
+        tc_fence_after();
+      }
+      float w0 = 1.f, w1 = 0.f;  // weights of this tile's O and of the other's
+      const bool join = tw.twin && tw.n1 > 0;
+      if (join) {
+        if (t == 1) {
+          sb.x_ml[row] = make_float2(m, l);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sb.x_stat));
+        } else {
+          ok = warp_wait(sb.x_stat, xph);
+          if (!ok) break;
+          tc_fence_after();
+          const float2 x = sb.x_ml[row];
+          const float mm = fmaxf(m, x.x);
+          w0 = mm == -INFINITY ? 1.f : ex2_approx(m - mm);
+          w1 = mm == -INFINITY ? 1.f : ex2_approx(x.x - mm);
+          l = l * w0 + x.y * w1;
+          m = mm;
+        }
+      }
+      if (quad_live && !(tw.twin && t == 1)) {
+        const int head = w.h * p.g + row % p.g;
+        const size_t orow = ((size_t)w.c0 + tok) * a.Hq + head;
+        const int urow = (tw.twin ? 0 : t * p.tpt * p.g) + row;
+        const bool whole = w.slot < 0;
+        const size_t prow = (size_t)max(w.slot, 0) * p.slot_rows + urow;
+        const float inv = whole ? (l == 0.f ? 0.f : a.v_scale / l) : 1.f;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          if (n > 0) {
+            tmem_ld32_issue(o_addr + (uint32_t)(c * 32), o);
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = 0u;
+          }
+          if (join) {
+            uint32_t o2[32];
+            tmem_ld32_issue(o_addr + (uint32_t)(D + c * 32), o2);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              o[k] = __float_as_uint(__uint_as_float(o[k]) * w0 + __uint_as_float(o2[k]) * w1);
+          }
+          if (!row_ok) continue;
+          const float* f = reinterpret_cast<const float*>(o);
+          if (whole) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + c * 32);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              dst[u] = make_uint4(pack16<false>(f[8 * u] * inv, f[8 * u + 1] * inv),
+                                  pack16<false>(f[8 * u + 2] * inv, f[8 * u + 3] * inv),
+                                  pack16<false>(f[8 * u + 4] * inv, f[8 * u + 5] * inv),
+                                  pack16<false>(f[8 * u + 6] * inv, f[8 * u + 7] * inv));
+          } else {
+            float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + c * 32);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) dst[u] = make_float4(f[4 * u], f[4 * u + 1], f[4 * u + 2], f[4 * u + 3]);
+          }
+        }
+        if (row_ok) {
+          if (whole) {
+            if (a.lse) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+          } else {
+            p.part_ml[prow] = make_float2(m, l);
+          }
+          if (*(volatile int*)&sb.bad_v[ps % kSlots]) {
+            const int first = (w.ctx + w.u * p.tpu) / kBlk * kBlk;  // the first masked block
+            if (whole)
+              add_nonfinite<D, KV4>(a, w, first, pos, static_cast<__nv_bfloat16*>(a.out) + orow * D);
+            else
+              add_nonfinite<D, KV4>(a, w, first, pos, p.part_o + prow * D);
+          }
+        }
+      }
+      if (join) {
+        // tile 1's O may be overwritten once tile 0's warps have read it
+        tc_fence_before();
+        __syncwarp();
+        if (t == 0) {
+          if (lane == 0) mbar_arrive(smem_u32(&sb.x_done));
+        } else {
+          ok = warp_wait(sb.x_done, xph);
+          if (!ok) break;
+        }
+        xph ^= 1u;
+      }
+      release_piece(ps);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (sb.abort_flag && threadIdx.x == 0) set_status(a.status, EAGLE_ERR_TIMEOUT);
+  if (warp == 4) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512u);
+  }
+}
+
+// ------------------------------------------------------------------ merge
+// out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s over the pieces s of a
+// cut unit, a warp per row.
+struct MergeParams {
+  const PlanHeader* hdr;
+  const Cut* cuts;
+  const float2* ml;
+  const float* o;
+  __nv_bfloat16* out;
+  float* lse;
+  float v_scale;
+  int Hq, g, tpu, slot_rows;
+};
+template <int D>
+__global__ void __launch_bounds__(256) prompt_merge_kernel(const MergeParams p) {
+  constexpr int E = D / 32;
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, warps = gridDim.x * 8;
+  const long long items = (long long)p.hdr->cuts * p.slot_rows;
+  for (long long it = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); it < items; it += warps) {
+    const Cut c = p.cuts[it / p.slot_rows];
+    const int r = (int)(it % p.slot_rows), tok = c.u * p.tpu + r / p.g;
+    if (r >= p.tpu * p.g || tok >= c.n) continue;
+    const size_t row0 = (size_t)c.slot * p.slot_rows + r;
+    float M = -INFINITY;
+    for (int s = lane; s < c.pieces; s += 32) M = fmaxf(M, p.ml[row0 + (size_t)s * p.slot_rows].x);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    float l = 0.f, o[E] = {};
+#pragma unroll 4
+    for (int s = 0; s < c.pieces; ++s) {
+      const size_t row = row0 + (size_t)s * p.slot_rows;
+      const float2 x = p.ml[row];
+      const float w = M == -INFINITY ? 1.f : ex2_approx(x.x - M);
+      l = fmaf(w, x.y, l);
+      float f[E];
+      if constexpr (E == 4)
+        *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(p.o + row * D + lane * 4);
+      else
+        *reinterpret_cast<float2*>(f) = *reinterpret_cast<const float2*>(p.o + row * D + lane * 2);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(w, f[e], o[e]);
+    }
+    const float inv = l == 0.f ? 0.f : p.v_scale / l;
+    const size_t orow = ((size_t)c.c0 + tok) * p.Hq + c.h * p.g + r % p.g;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + orow * D) + lane * (E / 2);
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) dst[e] = pack16<false>(o[2 * e] * inv, o[2 * e + 1] * inv);
+    if (p.lse && lane == 0) p.lse[orow] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+  }
+}
+
+// ------------------------------------------------------------------- fp32
+// One warp per (row, query head), the lanes sharing the channels: one pass
+// over the keys with a running maximum and sum.
+template <int D>
+__global__ void __launch_bounds__(128) prompt_attn_f32_kernel(const AttnParams p) {
   constexpr int E = D / 32;
   pdl_wait();
   pdl_trigger();
@@ -63,55 +1165,54 @@ __global__ void __launch_bounds__(128) prompt_attn_kernel(const AttnParams p) {
   if (h >= p.Hq) return;
   const int b = warp_find_request(p.cu, p.B, t);
   const int c0 = p.cu[b], c1 = p.cu[b + 1], ctx = p.ctx[b];
-  if (t < c0 || t >= c1 || ctx < 0) {
+  if (t < c0 || t >= c1 || c0 < 0 || c1 > p.T || ctx < 0) {
     set_status(p.status, EAGLE_ERR_INVALID_ARG);
     return;
   }
-  const int hk = h / (p.Hq / p.Hkv);
-  const long long n = (long long)ctx + (t - c0) + 1;
+  if ((long long)ctx + (c1 - c0) > 16ll * p.max_pages) {
+    set_status(p.status, EAGLE_ERR_BAD_KV);
+    return;
+  }
+  const int hk = h / (p.Hq / p.Hkv), n = ctx + (t - c0) + 1;
+  const float* qr = static_cast<const float*>(p.q) + (size_t)t * p.q_stride + (size_t)h * D + lane;
   float q[E], o[E], m = -INFINITY, l = 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    const size_t at = (size_t)t * p.q_stride + (size_t)h * D + lane + 32 * e;
-    q[e] = S == kF32 ? static_cast<const float*>(p.q)[at]
-                     : __bfloat162float(static_cast<const __nv_bfloat16*>(p.q)[at]);
+    q[e] = qr[32 * e];
     o[e] = 0.f;
   }
-  const float scale = p.scale * p.k_scale;
-  for (long long j = 0; j < n; ++j) {
-    const long long pi = j / 16;
-    const int page = pi < p.max_pages ? p.table[(size_t)b * p.max_pages + pi] : -1;
+  for (int j = 0; j < n; ++j) {
+    const int page = p.table[(size_t)b * p.max_pages + j / 16];
     float k[E], v[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) k[e] = v[e] = 0.f;
     if (page >= 0 && page < p.num_pages) {
-      load_row<D, S>(p.kc, p.ks, page, (int)(j & 15), hk, p.Hkv, k);
-      load_row<D, S>(p.vc, p.vs, page, (int)(j & 15), hk, p.Hkv, v);
+      const size_t at = (((size_t)page * 16 + (j & 15)) * p.Hkv + hk) * D + lane;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        k[e] = static_cast<const float*>(p.kc)[at + 32 * e];
+        v[e] = static_cast<const float*>(p.vc)[at + 32 * e];
+      }
     } else {
       set_status(p.status, EAGLE_ERR_BAD_KV);
+#pragma unroll
+      for (int e = 0; e < E; ++e) k[e] = v[e] = 0.f;
     }
     float z = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) z = fmaf(q[e], k[e], z);
 #pragma unroll
     for (int d = 16; d; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
-    z *= scale;
-    const float mn = fmaxf(m, z), a = m == -INFINITY ? 0.f : expf(m - mn), w = z == -INFINITY ? 0.f : expf(z - mn);
-    l = fmaf(l, a, w);
+    z *= p.scale;
+    const float mn = fmaxf(m, z), a = m == -INFINITY ? 0.f : expf(m - mn), x = z == -INFINITY ? 0.f : expf(z - mn);
+    l = fmaf(l, a, x);
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], a, w * v[e]);
+    for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], a, x * v[e]);
     m = mn;
   }
-  const float inv = p.v_scale / l;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const size_t orow = (size_t)t * p.Hq + h;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const size_t at = ((size_t)t * p.Hq + h) * D + lane + 32 * e;
-    if (S == kF32)
-      static_cast<float*>(p.out)[at] = o[e] * inv;
-    else
-      static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16(o[e] * inv);
-  }
-  if (p.lse && lane == 0) p.lse[(size_t)t * p.Hq + h] = m + logf(l);
+  for (int e = 0; e < E; ++e) static_cast<float*>(p.out)[orow * D + lane + 32 * e] = o[e] * inv;
+  if (p.lse && lane == 0) p.lse[orow] = m + logf(l);
 }
 
 int attn_check(const AttnParams& p, int D, int page_size, size_t es) {
@@ -128,18 +1229,36 @@ int attn_check(const AttnParams& p, int D, int page_size, size_t es) {
   return EAGLE_OK;
 }
 
-template <Source S>
-int attn_launch(const AttnParams& p, int D, void* ws, size_t ws_bytes, void* stream) {
-  if (p.T == 0) return EAGLE_OK;
-  if (!ws || ws_bytes < eagle_prompt_attn_workspace_size(p.B, p.T, p.Hq, p.Hkv, D)) return EAGLE_ERR_WORKSPACE;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const dim3 grid(p.T, (p.Hq + 3) / 4);
-  if (D == 128)
-    launch(prompt_attn_kernel<128, S>, grid, 128, 0, s, p);
-  else
-    launch(prompt_attn_kernel<64, S>, grid, 128, 0, s, p);
-  note_launch();
+template <int D, bool KV4>
+int attn_launch_tc(const AttnParams& a, void* ws, cudaStream_t s) {
+  using C = Cfg<D, KV4>;
+  const Shape sh = attn_shape(a.B, a.T, a.Hq, a.Hkv, D);
+  char* w = reinterpret_cast<char*>(round_up(reinterpret_cast<size_t>(ws), 256));
+  PlanHeader* hdr = reinterpret_cast<PlanHeader*>(w);
+  Piece* pieces = reinterpret_cast<Piece*>(w + sh.off_pieces);
+  Cut* cuts = reinterpret_cast<Cut*>(w + sh.off_cuts);
+  float2* ml = reinterpret_cast<float2*>(w + sh.off_ml);
+  float* po = reinterpret_cast<float*>(w + sh.off_o);
+  auto kern = prompt_attn_tc_kernel<D, KV4>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem) != cudaSuccess) {
+    cudaGetLastError();
+    return EAGLE_ERR_CUDA;
+  }
+  const PlanParams pp = {a.cu, a.ctx, a.B, a.T, a.Hkv, a.max_pages, sh.tpu, sh.g, sh.ctas, sh.cap_pieces, sh.cap_slots,
+                         hdr, pieces, cuts, a.status};
+  launch(prompt_plan_kernel, 1, kPlanThreads, 0, s, pp);
+  const MainParams mp = {a, a.scale * a.k_scale * 1.4426950408889634f, sh.g, sh.tpt, sh.tpu, sh.rows, hdr, &hdr->next,
+                         pieces, ml, po};
+  launch(kern, sh.ctas, kThreads, C::kSmem, s, mp);
+  const MergeParams gp = {hdr, cuts, ml, po, static_cast<__nv_bfloat16*>(a.out), a.lse, a.v_scale, a.Hq, sh.g, sh.tpu,
+                          sh.rows};
+  launch(prompt_merge_kernel<D>, 2 * sh.ctas, 256, 0, s, gp);
+  note_launch(3);
   return last_launch_status();
+}
+
+int attn_ws_check(const AttnParams& a, int D, void* ws, size_t ws_bytes) {
+  return !ws || ws_bytes < eagle_prompt_attn_workspace_size(a.B, a.T, a.Hq, a.Hkv, D) ? EAGLE_ERR_WORKSPACE : EAGLE_OK;
 }
 
 }  // namespace
@@ -148,8 +1267,8 @@ int attn_launch(const AttnParams& p, int D, void* ws, size_t ws_bytes, void* str
 using namespace eagle;
 
 extern "C" size_t eagle_prompt_attn_workspace_size(int B, int T, int Hq, int Hkv, int D) {
-  if (B <= 0 || T < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || (D != 64 && D != 128)) return 0;
-  return 256;
+  if (B <= 0 || T < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || Hq / Hkv > 64 || (D != 64 && D != 128)) return 0;
+  return attn_shape(B, T, Hq, Hkv, D).total + 256;
 }
 
 extern "C" int eagle_prompt_attn(const void* q, long long q_stride, const void* k_cache, const void* v_cache,
@@ -162,7 +1281,18 @@ extern "C" int eagle_prompt_attn(const void* q, long long q_stride, const void* 
                         block_table, cu_seqlens, ctx_lens, out, lse, scale, dev_status};
   const int rc = attn_check(p, D, page_size, dtype == EAGLE_BF16 ? 2 : 4);
   if (rc != EAGLE_OK) return rc;
-  return dtype == EAGLE_BF16 ? attn_launch<kBf16>(p, D, ws, ws_bytes, stream) : attn_launch<kF32>(p, D, ws, ws_bytes, stream);
+  if (T == 0) return EAGLE_OK;
+  const int wrc = attn_ws_check(p, D, ws, ws_bytes);
+  if (wrc != EAGLE_OK) return wrc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (dtype == EAGLE_BF16) return D == 128 ? attn_launch_tc<128, false>(p, ws, s) : attn_launch_tc<64, false>(p, ws, s);
+  const dim3 grid(T, (Hq + 3) / 4);
+  if (D == 128)
+    launch(prompt_attn_f32_kernel<128>, grid, 128, 0, s, p);
+  else
+    launch(prompt_attn_f32_kernel<64>, grid, 128, 0, s, p);
+  note_launch();
+  return last_launch_status();
 }
 
 extern "C" int eagle_prompt_attn_kv4(const void* q, long long q_stride, const uint8_t* k_codes,
@@ -173,8 +1303,12 @@ extern "C" int eagle_prompt_attn_kv4(const void* q, long long q_stride, const ui
                                      void* ws, size_t ws_bytes, int32_t* dev_status, void* stream) {
   const AttnParams p = {q, q_stride, k_codes, v_codes, k_scales, v_scales, k_scale, v_scale, num_pages, max_pages, B, T,
                         Hq, Hkv, block_table, cu_seqlens, ctx_lens, out, lse, scale, dev_status};
-  if (!k_scales || !v_scales) return EAGLE_ERR_INVALID_ARG;
+  if (!k_scales || !v_scales || !aligned16(k_scales) || !aligned16(v_scales)) return EAGLE_ERR_INVALID_ARG;
   const int rc = attn_check(p, D, page_size, 2);
   if (rc != EAGLE_OK) return rc;
-  return attn_launch<kKv4>(p, D, ws, ws_bytes, stream);
+  if (T == 0) return EAGLE_OK;
+  const int wrc = attn_ws_check(p, D, ws, ws_bytes);
+  if (wrc != EAGLE_OK) return wrc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return D == 128 ? attn_launch_tc<128, true>(p, ws, s) : attn_launch_tc<64, true>(p, ws, s);
 }

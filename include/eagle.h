@@ -774,9 +774,9 @@ int eagle_kv4_read(const uint8_t* codes, const uint8_t* scales, float scale, int
  * Keys past a row's position never reach its result, whatever their pages
  * hold (NaN included), nor do the unused slots of a last page.
  * T = 0 does nothing.  Device-detected: a malformed cu_seqlens or a negative
- * ctx_lens -> EAGLE_ERR_INVALID_ARG (the request is skipped, its rows are not
- * written); more tokens than the block table holds, or a page id out of range
- * -> EAGLE_ERR_BAD_KV (those keys and values read as zeros).
+ * ctx_lens -> EAGLE_ERR_INVALID_ARG, more tokens than the block table holds
+ * -> EAGLE_ERR_BAD_KV (the request is skipped, its rows are not written); a
+ * page id out of range -> EAGLE_ERR_BAD_KV (its keys and values read as zeros).
  * bf16 runs on the tensor cores with fp32 accumulation and fp32 softmax
  * statistics; fp32 on the CUDA cores in fp32 arithmetic.
  * Limits: D in {64, 128}, page_size == 16, Hq % Hkv == 0, Hq / Hkv <= 64,
@@ -792,7 +792,7 @@ int eagle_prompt_attn(const void* q, long long q_stride, const void* k_cache, co
 /* eagle_prompt_attn_kv4 -- eagle_prompt_attn over 4-bit pages; q and out bf16.
  * A code times its scale byte is exact in 16 bits, so the products are those
  * of the values the codes stand for.  Same workspace query; k_scale and
- * v_scale finite and > 0. */
+ * v_scale finite and > 0; codes and scales 16-byte aligned. */
 int eagle_prompt_attn_kv4(const void* q, long long q_stride, const uint8_t* k_codes,
                           const uint8_t* k_scales, const uint8_t* v_codes, const uint8_t* v_scales,
                           float k_scale, float v_scale, int num_pages, const int32_t* block_table,
