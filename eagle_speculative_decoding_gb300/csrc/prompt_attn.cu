@@ -343,6 +343,11 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// This thread's arrival on `bar` once all its copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
+}
 // at most n of the newest groups may still be in flight
 __device__ __forceinline__ void cp_async_wait_n(int n) {
   switch (n) {
@@ -454,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
-      mbar_init(smem_u32(&sb.kv_full[i]), 4);
+      mbar_init(smem_u32(&sb.kv_full[i]), KV4 ? 4 : 128);
       mbar_init(smem_u32(&sb.kv_empty[i]), 1);
     }
     for (int t = 0; t < 2; ++t) {
@@ -513,46 +518,28 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
       const int row0 = tid / CPR, c = tid % CPR;
       const uint32_t dst0 = (uint32_t)(c / 8) * C::kHalf + (uint32_t)row0 * 128u + (uint32_t)(((c % 8) ^ (row0 & 7)) << 4);
       const size_t tok_bytes = (size_t)a.Hkv * D * 2, page_bytes = tok_bytes * 16;
-      int pending = 0, ast = 0;  // tiles issued but not handed on, and the stage of the oldest
-      uint32_t info = 0;         // per stage: bits 0-1 piece slot, bit 3 V tile of a masked block
-      auto hand_on = [&]() {
-        const uint32_t x = (info >> (4 * ast)) & 15u;
-        if (x & 8u) {
-          // V of a masked block: a weight of zero does not silence a NaN or
-          // an infinity in the matrix product, so they are taken out here
-          // and added at the end to the rows that see them
-          bool found = false;
+      // V of a masked block: a weight of zero does not silence a NaN or an
+      // infinity in the matrix product, so they are taken out of the stage
+      // and added at the end to the rows that see them
+      auto take_out_nonfinite = [&](int slot) {
+        bool found = false;
 #pragma unroll 4
-          for (int i = 0; i < IT; ++i) {
-            uint4* q = reinterpret_cast<uint4*>(gbase + sKV + ast * C::kTile + dst0 + (uint32_t)i * (RPI * 128u));
-            uint4 v = *q;
-            uint32_t* e = &v.x;
-            bool hit = false;
+        for (int i = 0; i < IT; ++i) {
+          uint4* q = reinterpret_cast<uint4*>(gbase + sKV + st * C::kTile + dst0 + (uint32_t)i * (RPI * 128u));
+          uint4 v = *q;
+          uint32_t e[4] = {v.x, v.y, v.z, v.w};
+          bool hit = false;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if ((e[k] & 0x7f80u) == 0x7f80u) e[k] &= 0xffff0000u, hit = true;
-              if ((e[k] & 0x7f800000u) == 0x7f800000u) e[k] &= 0x0000ffffu, hit = true;
-            }
-            if (hit) *q = v, found = true;
+          for (int k = 0; k < 4; ++k) {
+            if ((e[k] & 0x7f80u) == 0x7f80u) e[k] &= 0xffff0000u, hit = true;
+            if ((e[k] & 0x7f800000u) == 0x7f800000u) e[k] &= 0x0000ffffu, hit = true;
           }
-          if (found) *(volatile int*)&sb.bad_v[x & 3u] = 1;
+          if (hit) *q = make_uint4(e[0], e[1], e[2], e[3]), found = true;
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sb.kv_full[ast]));
-        if (++ast == ST) ast = 0;
-        --pending;
-      };
-      // before a wait that may block, everything issued is handed on: what
-      // this wait is for may depend on it
-      auto flush = [&]() {
-        cp_async_wait<0>();
-        while (pending) hand_on();
+        if (found) *(volatile int*)&sb.bad_v[slot] = 1;
       };
       Piece w;
       for (int ps = 0;; ++ps) {
-        if (!__all_sync(0xffffffffu, mbar_try_wait(smem_u32(&sb.slot_full[ps % kSlots]), (uint32_t)(ps / kSlots) & 1u)))
-          flush();
         if (!get_piece(ps, w)) break;
         const int n_keys = w.ctx + w.n, masked_from = w.ctx + w.u * p.tpu;  // the first row's position
         const char* kb_ = static_cast<const char*>(a.kc) + (size_t)w.h * D * 2 + c * 16;
@@ -576,11 +563,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
           const bool masked = key0 + kBlk - 1 > masked_from;
 #pragma unroll
           for (int o = 0; o < 2; ++o) {
-            if (!__all_sync(0xffffffffu, mbar_try_wait(smem_u32(&sb.kv_empty[st]), ph ^ 1u))) {
-              flush();
-              ok = warp_wait(sb.kv_empty[st], ph ^ 1u);
-              if (!ok) break;
-            }
+            ok = warp_wait(sb.kv_empty[st], ph ^ 1u);
+            if (!ok) break;
             const uint32_t dst = base + sKV + st * C::kTile + dst0;
             const char* src = o ? vb_ : kb_;
 #pragma unroll
@@ -591,23 +575,24 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
               cp_async16(dst + (uint32_t)i * (RPI * 128u),
                          live ? src + (size_t)pq * page_bytes + (size_t)(r & 15) * tok_bytes : src, live);
             }
-            cp_async_commit();
-            info = (info & ~(15u << (4 * st))) | ((uint32_t)(ps % kSlots) | (o && masked ? 8u : 0u)) << (4 * st);
+            if (o && masked) {
+              cp_async_commit();
+              cp_async_wait<0>();
+              take_out_nonfinite(ps % kSlots);
+              mbar_arrive(smem_u32(&sb.kv_full[st]));
+            } else {
+              cp_async_arrive(smem_u32(&sb.kv_full[st]));
+            }
             if (++st == ST) {
               st = 0;
               ph ^= 1u;
-            }
-            if (++pending == ST) {
-              cp_async_wait<ST - 1>();
-              hand_on();
             }
           }
         }
         if (!ok) break;
         release_piece(ps);
       }
-      if (ok) flush();
-      cp_async_wait<0>();
+      cp_async_wait_all();
     } else {
       constexpr int R = C::kRawRing;
       constexpr int CC = 32 * (D / 2) / 16 / 32;       // code copies per lane: a warp has 32 rows
@@ -728,7 +713,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
               }
             }
             if (found) *(volatile int*)&sb.bad_v[ps % kSlots] = 1;
-            fence_proxy_async_smem();
             __syncwarp();  // also: the raw slot may be filled again
             if (lane == 0) mbar_arrive(smem_u32(&sb.kv_full[st]));
             ++consumed;
@@ -741,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
         if (!ok) break;
         release_piece(ps);
       }
-      cp_async_wait<0>();
+      cp_async_wait_all();
     }
   } else if (warp < 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
@@ -768,6 +752,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
             qph[t] ^= 1u;
           }
           if (!bar_wait(sb.kv_full[st], (uint32_t)(kt / ST) & 1u)) return false;
+          // the producers' writes, seen here, become the tensor core's: the
+          // fence stands on this side because in a copying thread it would
+          // wait for all its copies in flight
+          fence_proxy_async_smem();
           tc_fence_after();
           const uint64_t dq = dq0 + (uint64_t)((t * C::kTile) >> 4), dk = dk0 + (uint64_t)((st * C::kTile) >> 4);
 #pragma unroll
@@ -785,6 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
           const int vt = tile0 + 2 * tw.blk(t, i) + 1, st = vt % ST;
           if (!bar_wait(sb.kv_full[st], (uint32_t)(vt / ST) & 1u) || !bar_wait(sb.p_full[t], pph[t])) return false;
           pph[t] ^= 1u;
+          fence_proxy_async_smem();
           tc_fence_after();
           const uint64_t dv = dv0 + (uint64_t)((st * C::kTile) >> 4);
 #pragma unroll
