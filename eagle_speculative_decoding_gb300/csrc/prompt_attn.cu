@@ -359,12 +359,29 @@ __device__ __forceinline__ void cp_async_wait_n(int n) {
     default: cp_async_wait<5>(); break;
   }
 }
-// O += P V with P in tensor memory (A operand: 16 keys = 8 columns of pairs).
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+// MMAs and commits predicated on `one` (set in one lane of the warp).
+// D += A B, both operands in shared memory.
+__device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc), "r"(one)
+      : "memory");
+}
+// The same with A in tensor memory (16 keys = 8 columns of pairs).
+__device__ __forceinline__ void mma_ts(uint32_t one, uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                       bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"((uint32_t)acc), "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t one, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(one)
       : "memory");
 }
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
@@ -488,7 +505,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
   __syncthreads();
   tc_fence_after();
   pdl_trigger();
-  const uint32_t tmem = sb.tmem_base;
+  // all 512 columns are this CTA's: its tensor memory starts at 0
+  constexpr uint32_t tmem = 0;
 
   auto warp_wait = [&](uint64_t& bar, uint32_t parity) -> bool {
     return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), parity, abort_flag)) != 0;
@@ -730,79 +748,111 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
   } else if (warp < 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 4) {
-    // ---------------------------------------------------------- MMA issuer
-    if (lane == 0) {
+      // -------------------------------------------------------- MMA issuer
+      // The whole warp runs this, every value the same in its lanes (so that
+      // descriptors and addresses stay in uniform registers) and only the
+      // MMAs and commits predicated on one lane: with the loop inside a
+      // one-lane branch an MMA took 80-110 cycles to issue.
       constexpr uint32_t idesc_s = mma_idesc(kFmt, 128, kBlk), idesc_pv = mma_idesc_bmn(kFmt, 128, D);
+      const uint32_t one = lane == 0;
       const uint64_t dq0 = smem_desc_sw128(base + sQ), dk0 = smem_desc_sw128(base + sKV);
       const uint64_t dv0 = smem_desc_sw128_mn(base + sKV, C::kHalf);
-      uint32_t pph[2] = {0, 0}, qph[2] = {0, 0};
-      int tile0 = 0;  // number of K/V tiles before this piece
-      auto bar_wait = [&](uint64_t& b, uint32_t parity) { return mbar_wait(smem_u32(&b), parity, abort_flag); };
+      uint32_t pph = 0, qph = 0;  // a bit per tile
+      int st0 = 0;                // stage of the piece's first K tile
+      uint32_t ph0 = 0;           // and its phase
       bool ok = true;
       for (int ps = 0; ok; ++ps) {
-        if (!bar_wait(sb.slot_full[ps % kSlots], (uint32_t)(ps / kSlots) & 1u)) break;
-        const Piece w = sb.piece[ps % kSlots];
-        if (w.b < 0) break;
+        Piece w;
+        if (!get_piece(ps, w)) break;
         const TileWork tw = tile_work(w, p.tpt, p.tpu, p.g);
-        // S_t(i) = Q_t K^T
-        auto issue_s = [&](int t, int i) -> bool {
-          const int kt = tile0 + 2 * tw.blk(t, i), st = kt % ST;
-          if (i == 0) {
-            if (!bar_wait(sb.q_full[t], qph[t])) return false;
-            qph[t] ^= 1u;
+        const int n0 = __shfl_sync(0xffffffffu, tw.n0, 0), n1 = __shfl_sync(0xffffffffu, tw.n1, 0);
+        const int twin = __shfl_sync(0xffffffffu, (int)tw.twin, 0), nblk = __shfl_sync(0xffffffffu, w.k1 - w.k0, 0);
+        // stage and phase of the K tile that tile t reads next, advanced by
+        // two tiles per block; V's is the one after
+        int kst[2], vst[2];
+        uint32_t kph[2], vph[2];
+        auto advance = [&](int& st, uint32_t& ph, int by) {
+          st += by;
+          if (st >= ST) {
+            st -= ST;
+            ph ^= 1u;
           }
-          if (!bar_wait(sb.kv_full[st], (uint32_t)(kt / ST) & 1u)) return false;
+          if (st >= ST) {  // by = 4 of 3 stages
+            st -= ST;
+            ph ^= 1u;
+          }
+        };
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          kst[t] = st0, kph[t] = ph0;
+          if (t && twin) advance(kst[t], kph[t], 2);
+          vst[t] = kst[t], vph[t] = kph[t];
+          advance(vst[t], vph[t], 1);
+        }
+        const int by = twin ? 4 : 2;
+        // S_t(i) = Q_t K^T
+        auto issue_s = [&](int t, bool first, bool last) -> bool {
+          if (first) {
+            if (!warp_wait(sb.q_full[t], (qph >> t) & 1u)) return false;
+            qph ^= 1u << t;
+          }
+          const int st = kst[t];
+          if (!warp_wait(sb.kv_full[st], kph[t])) return false;
           // the producers' writes, seen here, become the tensor core's: the
           // fence stands on this side because in a copying thread it would
           // wait for all its copies in flight
           fence_proxy_async_smem();
           tc_fence_after();
-          const uint64_t dq = dq0 + (uint64_t)((t * C::kTile) >> 4), dk = dk0 + (uint64_t)((st * C::kTile) >> 4);
+          const uint64_t dq = dq0 + (uint64_t)((t * C::kTile) >> 4), dk = dk0 + (uint64_t)((uint32_t)(st * C::kTile) >> 4);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint32_t off = ((uint32_t)(k >> 2) * C::kHalf + (uint32_t)(k & 3) * 32u) >> 4;
-            mma_bf16(tmem + (uint32_t)(t * kBlk), dq + off, dk + off, idesc_s, k > 0 ? 1u : 0u);
+            mma_ss(one, (uint32_t)(t * kBlk), dq + off, dk + off, idesc_s, k > 0);
           }
-          mma_commit(smem_u32(&sb.s_full[t]));
+          commit(one, smem_u32(&sb.s_full[t]));
           // the tile that reads a K stage last frees it
-          if (tw.twin || t == 1) mma_commit(smem_u32(&sb.kv_empty[st]));
-          if (i + 1 == tw.n(t)) mma_commit(smem_u32(&sb.q_empty[t]));
+          if (twin || t == 1) commit(one, smem_u32(&sb.kv_empty[st]));
+          if (last) commit(one, smem_u32(&sb.q_empty[t]));
+          advance(kst[t], kph[t], by);
           return true;
         };
-        auto issue_pv = [&](int t, int i) -> bool {
-          const int vt = tile0 + 2 * tw.blk(t, i) + 1, st = vt % ST;
-          if (!bar_wait(sb.kv_full[st], (uint32_t)(vt / ST) & 1u) || !bar_wait(sb.p_full[t], pph[t])) return false;
-          pph[t] ^= 1u;
+        auto issue_pv = [&](int t, bool first, bool last) -> bool {
+          const int st = vst[t];
+          if (!warp_wait(sb.kv_full[st], vph[t]) || !warp_wait(sb.p_full[t], (pph >> t) & 1u)) return false;
+          pph ^= 1u << t;
           fence_proxy_async_smem();
           tc_fence_after();
-          const uint64_t dv = dv0 + (uint64_t)((st * C::kTile) >> 4);
+          const uint64_t dv = dv0 + (uint64_t)((uint32_t)(st * C::kTile) >> 4);
 #pragma unroll
           for (int k = 0; k < kBlk / 16; ++k)
-            mma_f16_ts(tmem + C::kColO + (uint32_t)(t * D), tmem + (uint32_t)(t * kBlk + k * 8), dv + (uint32_t)k * 128u,
-                       idesc_pv, (i > 0 || k > 0) ? 1u : 0u);
-          if (tw.twin || t == 1) mma_commit(smem_u32(&sb.kv_empty[st]));
-          if (i + 1 == tw.n(t)) mma_commit(smem_u32(&sb.o_full[t]));
+            mma_ts(one, C::kColO + (uint32_t)(t * D), (uint32_t)(t * kBlk + k * 8), dv + (uint32_t)k * 128u, idesc_pv,
+                   !first || k > 0);
+          if (twin || t == 1) commit(one, smem_u32(&sb.kv_empty[st]));
+          if (last) commit(one, smem_u32(&sb.o_full[t]));
+          advance(vst[t], vph[t], by);
           return true;
         };
-        for (int t = 0; t < 2 && ok; ++t)
-          if (tw.n(t) > 0) ok = issue_s(t, 0);
-        const int iters = max(tw.n0, tw.n1);
-        for (int i = 0; i < iters && ok; ++i)
-          for (int t = 0; t < 2 && ok; ++t) {
-            if (i < tw.n(t)) ok = issue_pv(t, i);
-            if (ok && i + 1 < tw.n(t)) ok = issue_s(t, i + 1);
-          }
+        if (n0 > 0) ok = issue_s(0, true, n0 == 1);
+        if (ok && n1 > 0) ok = issue_s(1, true, n1 == 1);
+        const int iters = max(n0, n1);
+        for (int i = 0; i < iters && ok; ++i) {
+          if (i < n0) ok = issue_pv(0, i == 0, i + 1 == n0);
+          if (ok && i + 1 < n0) ok = issue_s(0, false, i + 2 == n0);
+          if (ok && i < n1) ok = issue_pv(1, i == 0, i + 1 == n1);
+          if (ok && i + 1 < n1) ok = issue_s(1, false, i + 2 == n1);
+        }
         if (!ok) break;
-        tile0 += 2 * (w.k1 - w.k0);
-        mbar_arrive(smem_u32(&sb.slot_empty[ps % kSlots]));
+        const int tiles = st0 + 2 * nblk;
+        st0 = tiles % ST;
+        ph0 ^= (uint32_t)(tiles / ST) & 1u;
+        release_piece(ps);
       }
       // every MMA completes before tensor memory is freed
-      mma_commit(smem_u32(&sb.drain));
+      commit(one, smem_u32(&sb.drain));
       const unsigned long long t0 = globaltimer_ns();
       while (!mbar_try_wait(smem_u32(&sb.drain), 0) && globaltimer_ns() - t0 < 100000000ull) {
       }
-    }
-    __syncwarp();
+      __syncwarp();
     } else if (warp == 5) {
     // ----------------------------------------------------------- scheduler
     if (lane == 0) {
