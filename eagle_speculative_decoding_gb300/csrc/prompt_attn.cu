@@ -26,6 +26,7 @@ namespace eagle {
 namespace {
 
 constexpr int kBlk = 128;        // keys per block
+constexpr int kHb = 64;          // keys per softmax step (half a block)
 constexpr int kTileRows = 128;   // query rows per tile
 constexpr float kRescaleLog2 = 8.f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -284,14 +285,14 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanPar
 //                map, 2 KB each, do not), or, for 4-bit pages, copies of
 //                the codes to a raw ring and from there exact fp16 values to
 //                the stages
-//   warp 4       issues the MMAs (one thread)
-//   warp 5       takes pieces from the list, ahead of the others
-//   warps 6-7    Q loaders
+//   warps 4, 5   issue the MMAs of tile 0 and 1
+//   warp 6       takes pieces from the list, ahead of the others
+//   warp 7       Q loader
 //   warps 8-11   softmax of tile 0, warps 12-15 of tile 1: a thread is a row
 //                (a TMEM lane) and holds the block's 128 scores
 // S of a tile (fp32, 128 columns), its weights P (16-bit, over S) and O (D
 // columns) live in TMEM; P is the A operand of P V from there.  Per tile the
-// MMA thread issues P V(i), then S(i + 1): while one tile's softmax runs, the
+// issuing warp issues P V(i), then S(i + 1): while one tile's softmax runs, the
 // other tile's MMAs do.  S(i + 1) follows P V(i) in the pipe, so that the
 // softmax that sees S(i + 1) complete may rescale O.
 // A unit of at most 128 rows (single tokens, short chunks) would leave one
@@ -325,8 +326,9 @@ struct MainParams {
 
 template <int ST, bool KV4>
 struct Bars {
-  uint64_t kv_full[ST], kv_empty[ST], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], x_stat, x_done;
-  uint64_t slot_full[kSlots], slot_empty[kSlots], drain;
+  uint64_t kv_full[ST], kv_empty[ST], q_full[2], q_empty[2], o_full[2], x_stat, x_done;
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // by tile and half
+  uint64_t slot_full[kSlots], slot_empty[kSlots], drain[2];
   uint32_t tmem_base;
   int abort_flag;
   Piece piece[kSlots];      // b < 0: no more work
@@ -335,7 +337,10 @@ struct Bars {
   float2 x_ml[kTileRows];
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -359,7 +364,17 @@ __device__ __forceinline__ void cp_async_wait_n(int n) {
     default: cp_async_wait<5>(); break;
   }
 }
-// MMAs and commits predicated on `one` (set in one lane of the warp).
+// 1 in one lane of the converged warp, 0 in the others.  MMAs are predicated
+// on it: a predicate by elect.sync lets the compiler issue them once (64.5
+// cycles per M 128 N 128 K 16, the tensor core's own rate, 10-30 to issue),
+// any other predicate or a one-lane branch makes it loop over the lanes
+// (100-135 cycles per MMA, 65-82 to issue).
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+// MMAs and commits predicated on `one` (elect_one).
 // D += A B, both operands in shared memory.
 __device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile(
@@ -400,6 +415,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 template <bool F16>
@@ -477,22 +497,26 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(smem_u32(&sb.kv_full[i]), KV4 ? 4 : 128);
-      mbar_init(smem_u32(&sb.kv_empty[i]), 1);
+      mbar_init(smem_u32(&sb.kv_empty[i]), 2);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(smem_u32(&sb.q_full[t]), 2);
+      mbar_init(smem_u32(&sb.q_full[t]), 1);
       mbar_init(smem_u32(&sb.q_empty[t]), 1);
-      mbar_init(smem_u32(&sb.s_full[t]), 1);
-      mbar_init(smem_u32(&sb.p_full[t]), 4);
+      for (int x = 0; x < 2; ++x) {
+        mbar_init(smem_u32(&sb.s_full[t][x]), 1);
+        mbar_init(smem_u32(&sb.p_full[t][x]), 4);
+        mbar_init(smem_u32(&sb.pv_done[t][x]), 1);
+      }
       mbar_init(smem_u32(&sb.o_full[t]), 1);
     }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(smem_u32(&sb.slot_full[i]), 1);
-      mbar_init(smem_u32(&sb.slot_empty[i]), 15);  // warps 0-4 and 6-15
+      mbar_init(smem_u32(&sb.slot_empty[i]), 15);  // warps 0-5 and 7-15
     }
     mbar_init(smem_u32(&sb.x_stat), 4);
     mbar_init(smem_u32(&sb.x_done), 4);
-    mbar_init(smem_u32(&sb.drain), 1);
+    mbar_init(smem_u32(&sb.drain[0]), 1);
+    mbar_init(smem_u32(&sb.drain[1]), 1);
     sb.abort_flag = 0;
     fence_mbar_init();
   }
@@ -524,9 +548,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
 
   if (warp < 4) {
     // ------------------------------------------------------ K/V producers
-    // registers move from the copying and issuing warps to the softmax:
-    // 256 x 64 + 256 x 192 = the 512 x 128 of the launch
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     const int tid = threadIdx.x;
     int st = 0;
     uint32_t ph = 0;  // stage and phase of the next tile to be filled
@@ -579,19 +600,31 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
           pg_next = page_of(blk + 1);
           const int key0 = blk * kBlk;
           const bool masked = key0 + kBlk - 1 > masked_from;
+          // the block's pages, all before the first copy: a copy that waits
+          // for a shuffle of its own cost 89 cycles each
+          int pq[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) pq[q] = __shfl_sync(0xffffffffu, pg, q);
+          const bool whole = __all_sync(0xffffffffu, pg >= 0) && key0 + kBlk <= n_keys;
 #pragma unroll
           for (int o = 0; o < 2; ++o) {
             ok = warp_wait(sb.kv_empty[st], ph ^ 1u);
             if (!ok) break;
             const uint32_t dst = base + sKV + st * C::kTile + dst0;
-            const char* src = o ? vb_ : kb_;
+            const char* src = (o ? vb_ : kb_) + (size_t)(row0 & 15) * tok_bytes;
+            if (whole) {
 #pragma unroll
-            for (int i = 0; i < IT; ++i) {
-              const int r = i * RPI + row0;
-              const int pq = __shfl_sync(0xffffffffu, pg, (i * RPI) / 16);
-              const bool live = pq >= 0 && key0 + r < n_keys;
-              cp_async16(dst + (uint32_t)i * (RPI * 128u),
-                         live ? src + (size_t)pq * page_bytes + (size_t)(r & 15) * tok_bytes : src, live);
+              for (int i = 0; i < IT; ++i)
+                cp_async16(dst + (uint32_t)i * (RPI * 128u),
+                           src + (size_t)pq[i * RPI / 16] * page_bytes + (size_t)(i * RPI & 15) * tok_bytes);
+            } else {
+#pragma unroll
+              for (int i = 0; i < IT; ++i) {
+                const int q = pq[i * RPI / 16];
+                const bool live = q >= 0 && key0 + i * RPI + row0 < n_keys;
+                cp_async16_or_zero(dst + (uint32_t)i * (RPI * 128u),
+                                   live ? src + (size_t)q * page_bytes + (size_t)(i * RPI & 15) * tok_bytes : src, live);
+              }
             }
             if (o && masked) {
               cp_async_commit();
@@ -657,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
           const int ch = i * 32 + lane, q = ch / PC;  // chunk of the warp's rows, its page
           const int pq = __shfl_sync(0xffffffffu, ipg, q);
           const bool live = pq >= 0;
-          cp_async16(dst + (uint32_t)(warp * 32 * (D / 2) + ch * 16),
+          cp_async16_or_zero(dst + (uint32_t)(warp * 32 * (D / 2) + ch * 16),
                      live ? codes + ((size_t)pq * a.Hkv + iw.h) * (16 * D / 2) + (ch % PC) * 16 : codes, live);
         }
         {
@@ -665,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
           const int pq = __shfl_sync(0xffffffffu, ipg, q);
           const bool live = pq >= 0;
           if (lane < SCH)
-            cp_async16(dst + C::kRawCodes + (uint32_t)(warp * 32 * (D / 16) + ch * 16),
+            cp_async16_or_zero(dst + C::kRawCodes + (uint32_t)(warp * 32 * (D / 16) + ch * 16),
                        live ? scales + ((size_t)pq * a.Hkv + iw.h) * (16 * D / 16) + (ch % PS) * 16 : scales, live);
         }
         cp_async_commit();
@@ -746,114 +779,138 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
       cp_async_wait_all();
     }
   } else if (warp < 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if (warp == 4) {
-      // -------------------------------------------------------- MMA issuer
-      // The whole warp runs this, every value the same in its lanes (so that
-      // descriptors and addresses stay in uniform registers) and only the
-      // MMAs and commits predicated on one lane: with the loop inside a
-      // one-lane branch an MMA took 80-110 cycles to issue.
-      constexpr uint32_t idesc_s = mma_idesc(kFmt, 128, kBlk), idesc_pv = mma_idesc_bmn(kFmt, 128, D);
-      const uint32_t one = lane == 0;
-      const uint64_t dq0 = smem_desc_sw128(base + sQ), dk0 = smem_desc_sw128(base + sKV);
+    if (warp < 6) {
+      // ------------------------------------------------------- MMA issuers
+      // One warp per tile, so that one's waits and commits stand beside the
+      // other's MMAs.  Each runs converged, every value the same in its lanes
+      // (descriptors and addresses stay in uniform registers), only the MMAs
+      // and commits predicated on the elected lane.
+      constexpr uint32_t idesc_s = mma_idesc(kFmt, 128, kHb), idesc_pv = mma_idesc_bmn(kFmt, 128, D);
+      const int t = __shfl_sync(0xffffffffu, warp - 4, 0);
+      const uint64_t dq = smem_desc_sw128(base + sQ + t * C::kTile), dk0 = smem_desc_sw128(base + sKV);
       const uint64_t dv0 = smem_desc_sw128_mn(base + sKV, C::kHalf);
-      uint32_t pph = 0, qph = 0;  // a bit per tile
-      int st0 = 0;                // stage of the piece's first K tile
-      uint32_t ph0 = 0;           // and its phase
+      const uint32_t s_col = (uint32_t)(t * kBlk), o_col = C::kColO + (uint32_t)(t * D);
+      uint32_t pph = 0, qph = 0;
+      int st = 0;  // stage and phase of the next K/V tile
+      uint32_t ph = 0;
       bool ok = true;
+      auto next_tile = [&]() {
+        if (++st == ST) {
+          st = 0;
+          ph ^= 1u;
+        }
+      };
+      // both warps free every K/V tile; this one does not read this one
+      auto skip = [&](int tiles) {
+        for (int x = 0; x < tiles && ok; ++x) {
+          ok = warp_wait(sb.kv_full[st], ph);
+          if (ok && lane == 0) mbar_arrive(smem_u32(&sb.kv_empty[st]));
+          next_tile();
+        }
+      };
+      // the next K/V tile, written by the copying threads, becomes the tensor
+      // core's: the fence stands on this side because in a copying thread it
+      // would wait for all its copies in flight
+      auto take = [&]() {
+        ok = ok && warp_wait(sb.kv_full[st], ph);
+        fence_proxy_async_smem();
+        tc_fence_after();
+      };
       for (int ps = 0; ok; ++ps) {
         Piece w;
         if (!get_piece(ps, w)) break;
         const TileWork tw = tile_work(w, p.tpt, p.tpu, p.g);
-        const int n0 = __shfl_sync(0xffffffffu, tw.n0, 0), n1 = __shfl_sync(0xffffffffu, tw.n1, 0);
-        const int twin = __shfl_sync(0xffffffffu, (int)tw.twin, 0), nblk = __shfl_sync(0xffffffffu, w.k1 - w.k0, 0);
-        // stage and phase of the K tile that tile t reads next, advanced by
-        // two tiles per block; V's is the one after
-        int kst[2], vst[2];
-        uint32_t kph[2], vph[2];
-        auto advance = [&](int& st, uint32_t& ph, int by) {
-          st += by;
-          if (st >= ST) {
-            st -= ST;
-            ph ^= 1u;
-          }
-          if (st >= ST) {  // by = 4 of 3 stages
-            st -= ST;
-            ph ^= 1u;
-          }
-        };
+        const int n = __shfl_sync(0xffffffffu, tw.n(t), 0), nblk = __shfl_sync(0xffffffffu, w.k1 - w.k0, 0);
+        const int twin = __shfl_sync(0xffffffffu, (int)tw.twin, 0);
+        if (n == 0) {
+          skip(2 * nblk);
+        } else {
+          if (twin && t) skip(2);  // the other tile's block
+          ok = ok && warp_wait(sb.q_full[t], qph);
+          qph ^= 1u;
+          int kst = 0, vst = 0;
+          // S of one half of a K tile: 64 keys, columns x * 64 ..
+          auto issue_s = [&](int x, bool last) {
+            const uint64_t dk = dk0 + (uint64_t)((uint32_t)(kst * C::kTile + x * 8192) >> 4);
+            const uint32_t one = elect_one();
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          kst[t] = st0, kph[t] = ph0;
-          if (t && twin) advance(kst[t], kph[t], 2);
-          vst[t] = kst[t], vph[t] = kph[t];
-          advance(vst[t], vph[t], 1);
-        }
-        const int by = twin ? 4 : 2;
-        // S_t(i) = Q_t K^T
-        auto issue_s = [&](int t, bool first, bool last) -> bool {
-          if (first) {
-            if (!warp_wait(sb.q_full[t], (qph >> t) & 1u)) return false;
-            qph ^= 1u << t;
-          }
-          const int st = kst[t];
-          if (!warp_wait(sb.kv_full[st], kph[t])) return false;
-          // the producers' writes, seen here, become the tensor core's: the
-          // fence stands on this side because in a copying thread it would
-          // wait for all its copies in flight
-          fence_proxy_async_smem();
-          tc_fence_after();
-          const uint64_t dq = dq0 + (uint64_t)((t * C::kTile) >> 4), dk = dk0 + (uint64_t)((uint32_t)(st * C::kTile) >> 4);
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t off = ((uint32_t)(k >> 2) * C::kHalf + (uint32_t)(k & 3) * 32u) >> 4;
+              mma_ss(one, s_col + (uint32_t)(x * kHb), dq + off, dk + off, idesc_s, k > 0);
+            }
+            commit(one, smem_u32(&sb.s_full[t][x]));
+            if (x == 1) {
+              commit(one, smem_u32(&sb.kv_empty[kst]));
+              if (last) commit(one, smem_u32(&sb.q_empty[t]));
+            }
+          };
+          // O += P V of one half of a V tile, once its P is there
+          auto issue_pv = [&](int x, bool first, bool last) {
+            ok = ok && warp_wait(sb.p_full[t][x], pph);
+            if (!ok) return;
+            tc_fence_after();
+            const uint64_t dv = dv0 + (uint64_t)((uint32_t)(vst * C::kTile + x * 8192) >> 4);
+            const uint32_t one = elect_one();
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = ((uint32_t)(k >> 2) * C::kHalf + (uint32_t)(k & 3) * 32u) >> 4;
-            mma_ss(one, (uint32_t)(t * kBlk), dq + off, dk + off, idesc_s, k > 0);
+            for (int k = 0; k < kHb / 16; ++k)
+              mma_ts(one, o_col, s_col + (uint32_t)(x * kHb + k * 8), dv + (uint32_t)k * 128u, idesc_pv,
+                     !first || k > 0);
+            commit(one, smem_u32(&sb.pv_done[t][x]));
+            if (x == 1) {
+              commit(one, smem_u32(&sb.kv_empty[vst]));
+              if (last) commit(one, smem_u32(&sb.o_full[t]));
+            }
+          };
+          auto take_k = [&]() {
+            take();
+            kst = st;
+            next_tile();
+          };
+          take_k();
+          if (!ok) break;
+          issue_s(0, n == 1);
+          issue_s(1, n == 1);
+          for (int i = 0; i < n && ok; ++i) {
+            const bool last = i + 1 == n;
+            take();
+            vst = st;
+            next_tile();
+            issue_pv(0, i == 0, last);
+            if (twin) {
+              // the next K tile lies past the other tile's two: it may need
+              // this V tile's stage, so V goes first
+              issue_pv(1, false, last);
+              if (ok && !last) {
+                skip(2);
+                take_k();
+                if (!ok) break;
+                issue_s(0, i + 2 == n);
+                issue_s(1, i + 2 == n);
+              }
+            } else {
+              if (ok && !last) {
+                take_k();
+                if (!ok) break;
+                issue_s(0, i + 2 == n);
+              }
+              issue_pv(1, false, last);
+              if (ok && !last) issue_s(1, i + 2 == n);
+            }
+            pph ^= 1u;
           }
-          commit(one, smem_u32(&sb.s_full[t]));
-          // the tile that reads a K stage last frees it
-          if (twin || t == 1) commit(one, smem_u32(&sb.kv_empty[st]));
-          if (last) commit(one, smem_u32(&sb.q_empty[t]));
-          advance(kst[t], kph[t], by);
-          return true;
-        };
-        auto issue_pv = [&](int t, bool first, bool last) -> bool {
-          const int st = vst[t];
-          if (!warp_wait(sb.kv_full[st], vph[t]) || !warp_wait(sb.p_full[t], (pph >> t) & 1u)) return false;
-          pph ^= 1u << t;
-          fence_proxy_async_smem();
-          tc_fence_after();
-          const uint64_t dv = dv0 + (uint64_t)((uint32_t)(st * C::kTile) >> 4);
-#pragma unroll
-          for (int k = 0; k < kBlk / 16; ++k)
-            mma_ts(one, C::kColO + (uint32_t)(t * D), (uint32_t)(t * kBlk + k * 8), dv + (uint32_t)k * 128u, idesc_pv,
-                   !first || k > 0);
-          if (twin || t == 1) commit(one, smem_u32(&sb.kv_empty[st]));
-          if (last) commit(one, smem_u32(&sb.o_full[t]));
-          advance(vst[t], vph[t], by);
-          return true;
-        };
-        if (n0 > 0) ok = issue_s(0, true, n0 == 1);
-        if (ok && n1 > 0) ok = issue_s(1, true, n1 == 1);
-        const int iters = max(n0, n1);
-        for (int i = 0; i < iters && ok; ++i) {
-          if (i < n0) ok = issue_pv(0, i == 0, i + 1 == n0);
-          if (ok && i + 1 < n0) ok = issue_s(0, false, i + 2 == n0);
-          if (ok && i < n1) ok = issue_pv(1, i == 0, i + 1 == n1);
-          if (ok && i + 1 < n1) ok = issue_s(1, false, i + 2 == n1);
+          // what follows this tile's last block in the piece
+          if (ok) skip(2 * (twin ? nblk - (2 * (n - 1) + t + 1) : nblk - n));
         }
         if (!ok) break;
-        const int tiles = st0 + 2 * nblk;
-        st0 = tiles % ST;
-        ph0 ^= (uint32_t)(tiles / ST) & 1u;
         release_piece(ps);
       }
       // every MMA completes before tensor memory is freed
-      commit(one, smem_u32(&sb.drain));
+      commit(elect_one(), smem_u32(&sb.drain[t]));
       const unsigned long long t0 = globaltimer_ns();
-      while (!mbar_try_wait(smem_u32(&sb.drain), 0) && globaltimer_ns() - t0 < 100000000ull) {
+      while (!mbar_try_wait(smem_u32(&sb.drain[t]), 0) && globaltimer_ns() - t0 < 100000000ull) {
       }
       __syncwarp();
-    } else if (warp == 5) {
+    } else if (warp == 6) {
     // ----------------------------------------------------------- scheduler
     if (lane == 0) {
       const int total = p.hdr->pieces;
@@ -872,9 +929,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
     }
     __syncwarp();
     } else {
-    // ----------------------------------------------------------- Q loaders
-    constexpr int CPR = D / 8, RPI = 64 / CPR;  // rows per iteration of the 64 threads
-    const int tid = threadIdx.x - 192, row0 = tid / CPR, c = tid % CPR;
+    // ----------------------------------------------------------- Q loader
+    constexpr int CPR = D / 8, RPI = 32 / CPR;  // rows per iteration of the warp
+    const int tid = lane, row0 = tid / CPR, c = tid % CPR;
     int uses[2] = {0, 0};
     bool ok = true;
     Piece w;
@@ -901,7 +958,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
             if constexpr (KV4)
               v[x] = live ? *reinterpret_cast<const uint4*>(src) : make_uint4(0u, 0u, 0u, 0u);
             else if (live)
-              cp_async16(base + off, src, true);
+              cp_async16(base + off, src);
           }
           if constexpr (KV4) {
             // rows as fp16, each scaled by a power of two to [1, 2) at its
@@ -945,7 +1002,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
     }
   } else {
     // ------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     const int t = (warp - 8) >> 2, q4 = warp & 3, row = q4 * 32 + lane;
     const uint32_t lane_addr = (uint32_t)(q4 * 32) << 16;
     const uint32_t s_addr = tmem + lane_addr + (uint32_t)(t * kBlk);
@@ -962,75 +1018,77 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
       const int tok = w.u * p.tpu + (tw.twin ? 0 : t * p.tpt) + row / p.g;
       const int pos = row_ok ? w.ctx + tok : 0x7fffffff;
       float m = -INFINITY, l = 0.f, sl2 = p.scale_log2;
-      for (int i = 0; i < n; ++i) {
-        ok = warp_wait(sb.s_full[t], sph);
-        if (!ok) break;
-        sph ^= 1u;
-        tc_fence_after();
-        if (quad_live) {
-          if (KV4 && i == 0) sl2 *= row_ok ? sb.q_fac[uses & 1][t][row] : 1.f;
-          uint32_t r[kBlk];
+      for (int i = 0; i < n && ok; ++i) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32_issue(s_addr + (uint32_t)(c * 32), r + c * 32);
-          tmem_wait_ld();
-          const int lim = pos - (w.k0 + tw.blk(t, i)) * kBlk;  // the last visible column
-          if (!__all_sync(0xffffffffu, lim >= kBlk - 1)) {
+        for (int x = 0; x < 2; ++x) {
+          ok = ok && warp_wait(sb.s_full[t][x], sph);
+          if (!ok) break;
+          tc_fence_after();
+          if (quad_live) {
+            if (KV4 && i == 0 && x == 0) sl2 *= row_ok ? sb.q_fac[uses & 1][t][row] : 1.f;
+            uint32_t r[kHb];
+            tmem_ld32_issue(s_addr + (uint32_t)(x * kHb), r);
+            tmem_ld32_issue(s_addr + (uint32_t)(x * kHb + 32), r + 32);
+            tmem_wait_ld();
+            const int lim = pos - (w.k0 + tw.blk(t, i)) * kBlk - x * kHb;  // the last visible column
+            if (!__all_sync(0xffffffffu, lim >= kHb - 1)) {
 #pragma unroll
-            for (int c = 0; c < kBlk; ++c) r[c] = c <= lim ? r[c] : 0xff800000u;
-          }
-          float mx[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) mx[c] = fmaxf(__uint_as_float(r[c]), __uint_as_float(r[c + 4]));
-#pragma unroll
-          for (int c = 8; c < kBlk; c += 8)
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              mx[x] = fmaxf(fmaxf(mx[x], __uint_as_float(r[c + x])), __uint_as_float(r[c + x + 4]));
-          const float bm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
-          // m is the reference of O and l: it moves, and both are rescaled,
-          // only when a block's maximum exceeds it by 2^8
-          const bool need = bm > m + kRescaleLog2;
-          const bool resc = need && m != -INFINITY;
-          if (__any_sync(0xffffffffu, resc)) {
-            const float alpha = resc ? ex2_approx(m - bm) : 1.f;
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32_issue(o_addr + (uint32_t)(c * 32), o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-              tmem_st32(o_addr + (uint32_t)(c * 32), o);
+              for (int c = 0; c < kHb; ++c) r[c] = c <= lim ? r[c] : 0xff800000u;
             }
-            l *= alpha;
-          }
-          if (need) m = bm;
-          const float neg_m = m == -INFINITY ? 0.f : -m;
-          const uint64_t sc2 = pack2(sl2, sl2), nm2 = pack2(neg_m, neg_m);
-          uint64_t ls[2] = {0ull, 0ull};
+            float mx[4];
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
+            for (int c = 0; c < 4; ++c) mx[c] = fmaxf(__uint_as_float(r[c]), __uint_as_float(r[c + 4]));
+#pragma unroll
+            for (int c = 8; c < kHb; c += 8)
+#pragma unroll
+              for (int y = 0; y < 4; ++y) mx[y] = max3(mx[y], __uint_as_float(r[c + y]), __uint_as_float(r[c + y + 4]));
+            const float bm = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * sl2;
+            // m is the reference of O and l: it moves, and both are rescaled,
+            // only when a half block's maximum exceeds it by 2^8
+            const bool need = bm > m + kRescaleLog2;
+            const bool resc = need && m != -INFINITY;
+            if (__any_sync(0xffffffffu, resc)) {
+              // O must be still: every earlier P V complete
+              ok = warp_wait(sb.pv_done[t][x ^ 1], x ? sph : sph ^ 1u);
+              if (!ok) break;
+              tc_fence_after();
+              const float alpha = resc ? ex2_approx(m - bm) : 1.f;
+#pragma unroll 1
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32_issue(o_addr + (uint32_t)(c * 32), o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                tmem_st32(o_addr + (uint32_t)(c * 32), o);
+              }
+              l *= alpha;
+            }
+            if (need) m = bm;
+            const float neg_m = m == -INFINITY ? 0.f : -m;
+            const uint64_t sc2 = pack2(sl2, sl2), nm2 = pack2(neg_m, neg_m);
+            uint64_t ls[2] = {0ull, 0ull};
             uint32_t pk[32];
 #pragma unroll
             for (int k = 0; k < 32; ++k) {
               float e0, e1;
-              unpack2(fma2(pack2(__uint_as_float(r[hf * 64 + 2 * k]), __uint_as_float(r[hf * 64 + 2 * k + 1])), sc2, nm2),
-                      e0, e1);
+              unpack2(fma2(pack2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])), sc2, nm2), e0, e1);
               e0 = ex2_approx(e0);
               e1 = ex2_approx(e1);
               ls[k & 1] = add2(ls[k & 1], pack2(e0, e1));
               pk[k] = pack16<KV4>(e0, e1);
             }
-            tmem_st32(s_addr + (uint32_t)(hf * 32), pk);
+            tmem_st32(s_addr + (uint32_t)(x * kHb), pk);
+            float l0, l1;
+            unpack2(add2(ls[0], ls[1]), l0, l1);
+            l += l0 + l1;
+            tmem_wait_st();
           }
-          float l0, l1;
-          unpack2(add2(ls[0], ls[1]), l0, l1);
-          l += l0 + l1;
-          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sb.p_full[t][x]));
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sb.p_full[t]));
+        sph ^= 1u;
       }
       if (!ok) break;
       if (n > 0) {
