@@ -301,6 +301,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanPar
 // 0's warps join the two at the end (same TMEM lanes).
 constexpr int kThreads = 512;
 constexpr int kSlots = 4;  // pieces known ahead
+constexpr int kNoPage = -0x7fffffff - 1;  // past the keys (or found out of range): reads as zeros
 
 template <int D, bool KV4>
 struct Cfg {
@@ -584,19 +585,18 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
         const char* kb_ = static_cast<const char*>(a.kc) + (size_t)w.h * D * 2 + c * 16;
         const char* vb_ = static_cast<const char*>(a.vc) + (size_t)w.h * D * 2 + c * 16;
         const int32_t* tab = a.table + (size_t)w.b * a.max_pages;
-        auto page_of = [&](int blk) -> int {  // lane q < 8: page q of the block, -1 past the keys or out of range
+        auto page_of = [&](int blk) -> int {  // lane q < 8: page q of the block
           const int k = blk * kBlk + (lane & 7) * 16;
-          if (blk >= w.k1 || k >= n_keys) return -1;
-          const int pg = tab[k / 16];
-          if (pg < 0 || pg >= a.num_pages) {
-            set_status(a.status, EAGLE_ERR_BAD_KV);
-            return -1;
-          }
-          return pg;
+          return blk < w.k1 && k < n_keys ? tab[k / 16] : kNoPage;
         };
         int pg_next = page_of(w.k0);
         for (int blk = w.k0; ok && blk < w.k1; ++blk) {
-          const int pg = pg_next;
+          // checked a block after it was loaded, so that nothing waits for the load
+          int pg = pg_next;
+          if (pg != kNoPage && (pg < 0 || pg >= a.num_pages)) {
+            set_status(a.status, EAGLE_ERR_BAD_KV);
+            pg = kNoPage;
+          }
           pg_next = page_of(blk + 1);
           const int key0 = blk * kBlk;
           const bool masked = key0 + kBlk - 1 > masked_from;
@@ -653,8 +653,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
       int issued = 0, consumed = 0;
       // the cursor of the copies runs ahead of that of the conversion
       Piece iw;
-      int ips = 0, iblk = 0, iop = 0, ipg = -1;
+      int ips = 0, iblk = 0, iop = 0, ipg_next = kNoPage, ip0 = kNoPage, ip1 = kNoPage;
       bool have = false, last = false;
+      // lane q & 1: page q of this warp's 32 keys of a block
+      auto page_of = [&](int blk) -> int {
+        const int k = blk * kBlk + warp * 32 + (lane & 1) * 16;
+        return blk < iw.k1 && k < iw.ctx + iw.n ? a.table[(size_t)iw.b * a.max_pages + k / 16] : kNoPage;
+      };
       auto issue = [&](bool must) -> bool {
         if (!have) {
           if (last) return false;
@@ -668,34 +673,33 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
           have = true;
           iblk = iw.k0;
           iop = 0;
+          ipg_next = page_of(iblk);
         }
-        const int n_keys = iw.ctx + iw.n, key0 = iblk * kBlk;
         if (iop == 0) {
-          // lane q < 2: page q of this warp's 32 keys
-          const int k = key0 + warp * 32 + (lane & 1) * 16;
-          ipg = -1;
-          if (k < n_keys) {
-            ipg = a.table[(size_t)iw.b * a.max_pages + k / 16];
-            if (ipg < 0 || ipg >= a.num_pages) {
-              set_status(a.status, EAGLE_ERR_BAD_KV);
-              ipg = -1;
-            }
+          // checked a block after it was loaded, so that nothing waits for the load
+          int pg = ipg_next;
+          if (pg != kNoPage && (pg < 0 || pg >= a.num_pages)) {
+            set_status(a.status, EAGLE_ERR_BAD_KV);
+            pg = kNoPage;
           }
+          ip0 = __shfl_sync(0xffffffffu, pg, 0);
+          ip1 = __shfl_sync(0xffffffffu, pg, 1);
+          ipg_next = page_of(iblk + 1);
         }
         const uint8_t* codes = static_cast<const uint8_t*>(iop ? a.vc : a.kc);
         const uint8_t* scales = iop ? a.vs : a.ks;
         const uint32_t dst = base + sRaw + (uint32_t)(issued % R) * C::kRaw;
 #pragma unroll
         for (int i = 0; i < CC; ++i) {
-          const int ch = i * 32 + lane, q = ch / PC;  // chunk of the warp's rows, its page
-          const int pq = __shfl_sync(0xffffffffu, ipg, q);
+          const int ch = i * 32 + lane;  // chunk of the warp's rows
+          const int pq = ch / PC ? ip1 : ip0;
           const bool live = pq >= 0;
           cp_async16_or_zero(dst + (uint32_t)(warp * 32 * (D / 2) + ch * 16),
                      live ? codes + ((size_t)pq * a.Hkv + iw.h) * (16 * D / 2) + (ch % PC) * 16 : codes, live);
         }
         {
-          const int ch = lane % SCH, q = ch / PS;
-          const int pq = __shfl_sync(0xffffffffu, ipg, q);
+          const int ch = lane % SCH;
+          const int pq = ch / PS ? ip1 : ip0;
           const bool live = pq >= 0;
           if (lane < SCH)
             cp_async16_or_zero(dst + C::kRawCodes + (uint32_t)(warp * 32 * (D / 16) + ch * 16),
