@@ -585,27 +585,32 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
         const char* kb_ = static_cast<const char*>(a.kc) + (size_t)w.h * D * 2 + c * 16;
         const char* vb_ = static_cast<const char*>(a.vc) + (size_t)w.h * D * 2 + c * 16;
         const int32_t* tab = a.table + (size_t)w.b * a.max_pages;
-        auto page_of = [&](int blk) -> int {  // lane q < 8: page q of the block
-          const int k = blk * kBlk + (lane & 7) * 16;
-          return blk < w.k1 && k < n_keys ? tab[k / 16] : kNoPage;
+        // page ids of four blocks at a time, lane 8 j + q: page q of block j;
+        // the next four are loaded one group ahead (a wait for a load is also
+        // one for the copies in flight)
+        auto pages_of = [&](int blk) -> int {
+          const int pi = blk * 8 + lane;
+          return pi < w.k1 * 8 && pi * 16 < n_keys ? tab[pi] : kNoPage;
         };
-        int pg_next = page_of(w.k0);
+        int pg = kNoPage, pg_next = pages_of(w.k0);
         for (int blk = w.k0; ok && blk < w.k1; ++blk) {
-          // checked a block after it was loaded, so that nothing waits for the load
-          int pg = pg_next;
-          if (pg != kNoPage && (pg < 0 || pg >= a.num_pages)) {
-            set_status(a.status, EAGLE_ERR_BAD_KV);
-            pg = kNoPage;
+          const int j = (blk - w.k0) & 3;
+          if (j == 0) {
+            pg = pg_next;
+            pg_next = pages_of(blk + 4);
+            if (pg != kNoPage && (pg < 0 || pg >= a.num_pages)) {
+              set_status(a.status, EAGLE_ERR_BAD_KV);
+              pg = kNoPage;
+            }
           }
-          pg_next = page_of(blk + 1);
           const int key0 = blk * kBlk;
           const bool masked = key0 + kBlk - 1 > masked_from;
           // the block's pages, all before the first copy: a copy that waits
           // for a shuffle of its own cost 89 cycles each
           int pq[8];
 #pragma unroll
-          for (int q = 0; q < 8; ++q) pq[q] = __shfl_sync(0xffffffffu, pg, q);
-          const bool whole = __all_sync(0xffffffffu, pg >= 0) && key0 + kBlk <= n_keys;
+          for (int q = 0; q < 8; ++q) pq[q] = __shfl_sync(0xffffffffu, pg, j * 8 + q);
+          const bool whole = __all_sync(0xffffffffu, pg >= 0 || (lane >> 3) != j) && key0 + kBlk <= n_keys;
 #pragma unroll
           for (int o = 0; o < 2; ++o) {
             ok = warp_wait(sb.kv_empty[st], ph ^ 1u);
@@ -650,15 +655,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
       constexpr int SCH = 32 * (D / 16) / 16;          // 16-byte scale chunks of 32 rows
       constexpr int PC = 16 * (D / 2) / 16;            // code chunks of a page and head
       constexpr int PS = 16 * (D / 16) / 16;           // scale chunks of a page and head
-      int issued = 0, consumed = 0;
+      int issued = 0, consumed = 0, islot = 0, cslot = 0;  // tiles, and their raw slots
       // the cursor of the copies runs ahead of that of the conversion
-      Piece iw;
-      int ips = 0, iblk = 0, iop = 0, ipg_next = kNoPage, ip0 = kNoPage, ip1 = kNoPage;
+      int ib = 0, ih = 0, ik1 = 0, ikeys = 0;  // its piece
+      int ips = 0, iblk = 0, iop = 0, igrp = 0, ipg = kNoPage, ipg_next = kNoPage, ip0 = kNoPage, ip1 = kNoPage;
       bool have = false, last = false;
-      // lane q & 1: page q of this warp's 32 keys of a block
-      auto page_of = [&](int blk) -> int {
-        const int k = blk * kBlk + warp * 32 + (lane & 1) * 16;
-        return blk < iw.k1 && k < iw.ctx + iw.n ? a.table[(size_t)iw.b * a.max_pages + k / 16] : kNoPage;
+      // page ids of 16 blocks at a time, lane 2 j + q: page q of this warp's 32
+      // keys of block j; the next are loaded one group ahead (a wait for a
+      // load is also one for the copies in flight)
+      auto pages_of = [&](int blk) -> int {
+        const int bl = blk + (lane >> 1), pi = bl * 8 + warp * 2 + (lane & 1);
+        return bl < ik1 && pi * 16 < ikeys ? a.table[(size_t)ib * a.max_pages + pi] : kNoPage;
       };
       auto issue = [&](bool must) -> bool {
         if (!have) {
@@ -666,36 +673,45 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
           if (!must && !__all_sync(0xffffffffu, mbar_try_wait(smem_u32(&sb.slot_full[ips % kSlots]),
                                                               (uint32_t)(ips / kSlots) & 1u)))
             return false;
-          if (!get_piece(ips, iw)) {
+          Piece w;
+          if (!get_piece(ips, w)) {
             last = true;
             return false;
           }
           have = true;
-          iblk = iw.k0;
+          ib = w.b;
+          ih = w.h;
+          ik1 = w.k1;
+          ikeys = w.ctx + w.n;
+          iblk = w.k0;
           iop = 0;
-          ipg_next = page_of(iblk);
+          igrp = 0;
+          ipg_next = pages_of(iblk);
         }
         if (iop == 0) {
-          // checked a block after it was loaded, so that nothing waits for the load
-          int pg = ipg_next;
-          if (pg != kNoPage && (pg < 0 || pg >= a.num_pages)) {
-            set_status(a.status, EAGLE_ERR_BAD_KV);
-            pg = kNoPage;
+          if (igrp == 0) {
+            ipg = ipg_next;
+            ipg_next = pages_of(iblk + 16);
+            if (ipg != kNoPage && (ipg < 0 || ipg >= a.num_pages)) {
+              set_status(a.status, EAGLE_ERR_BAD_KV);
+              ipg = kNoPage;
+            }
           }
-          ip0 = __shfl_sync(0xffffffffu, pg, 0);
-          ip1 = __shfl_sync(0xffffffffu, pg, 1);
-          ipg_next = page_of(iblk + 1);
+          ip0 = __shfl_sync(0xffffffffu, ipg, 2 * igrp);
+          ip1 = __shfl_sync(0xffffffffu, ipg, 2 * igrp + 1);
+          igrp = (igrp + 1) & 15;
         }
         const uint8_t* codes = static_cast<const uint8_t*>(iop ? a.vc : a.kc);
         const uint8_t* scales = iop ? a.vs : a.ks;
-        const uint32_t dst = base + sRaw + (uint32_t)(issued % R) * C::kRaw;
+        const uint32_t dst = base + sRaw + (uint32_t)islot * C::kRaw;
+        if (++islot == R) islot = 0;
 #pragma unroll
         for (int i = 0; i < CC; ++i) {
           const int ch = i * 32 + lane;  // chunk of the warp's rows
           const int pq = ch / PC ? ip1 : ip0;
           const bool live = pq >= 0;
           cp_async16_or_zero(dst + (uint32_t)(warp * 32 * (D / 2) + ch * 16),
-                     live ? codes + ((size_t)pq * a.Hkv + iw.h) * (16 * D / 2) + (ch % PC) * 16 : codes, live);
+                     live ? codes + ((size_t)pq * a.Hkv + ih) * (16 * D / 2) + (ch % PC) * 16 : codes, live);
         }
         {
           const int ch = lane % SCH;
@@ -703,13 +719,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
           const bool live = pq >= 0;
           if (lane < SCH)
             cp_async16_or_zero(dst + C::kRawCodes + (uint32_t)(warp * 32 * (D / 16) + ch * 16),
-                       live ? scales + ((size_t)pq * a.Hkv + iw.h) * (16 * D / 16) + (ch % PS) * 16 : scales, live);
+                       live ? scales + ((size_t)pq * a.Hkv + ih) * (16 * D / 16) + (ch % PS) * 16 : scales, live);
         }
         cp_async_commit();
         ++issued;
         if (++iop == 2) {
           iop = 0;
-          if (++iblk == iw.k1) {
+          if (++iblk == ik1) {
             have = false;
             ++ips;
           }
@@ -731,7 +747,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
             __syncwarp();
             ok = warp_wait(sb.kv_empty[st], ph ^ 1u);
             if (!ok) break;
-            const unsigned char* raw = gbase + sRaw + (uint32_t)(consumed % R) * C::kRaw;
+            const unsigned char* raw = gbase + sRaw + (uint32_t)cslot * C::kRaw;
+            if (++cslot == R) cslot = 0;
             unsigned char* stage = gbase + sKV + st * C::kTile;
             bool found = false;
             // a lane takes 32 channels of a row: eight lanes at a time write
@@ -1022,10 +1039,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
       const int tok = w.u * p.tpu + (tw.twin ? 0 : t * p.tpt) + row / p.g;
       const int pos = row_ok ? w.ctx + tok : 0x7fffffff;
       float m = -INFINITY, l = 0.f, sl2 = p.scale_log2;
+#pragma unroll 1
       for (int i = 0; i < n && ok; ++i) {
-#pragma unroll
+#pragma unroll 1
         for (int x = 0; x < 2; ++x) {
-          ok = ok && warp_wait(sb.s_full[t][x], sph);
+          ok = warp_wait(sb.s_full[t][x], sph);
           if (!ok) break;
           tc_fence_after();
           if (quad_live) {
@@ -1049,7 +1067,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
             const float bm = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * sl2;
             // m is the reference of O and l: it moves, and both are rescaled,
             // only when a half block's maximum exceeds it by 2^8
-            const bool need = bm > m + kRescaleLog2;
+            const bool need = row_ok && bm > m + kRescaleLog2;
             const bool resc = need && m != -INFINITY;
             if (__any_sync(0xffffffffu, resc)) {
               // O must be still: every earlier P V complete
