@@ -28,7 +28,7 @@ namespace {
 constexpr int kBlk = 128;        // keys per block
 constexpr int kHb = 64;          // keys per softmax step (half a block)
 constexpr int kTileRows = 128;   // query rows per tile
-constexpr float kRescaleLog2 = 8.f;
+constexpr float kSumLimit = 256.f;  // fp16 weights: 64 of them stay below 2^8 each
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct AttnParams {
@@ -327,8 +327,8 @@ struct MainParams {
 
 template <int ST, bool KV4>
 struct Bars {
-  uint64_t kv_full[ST], kv_empty[ST], q_full[2], q_empty[2], o_full[2], x_stat, x_done;
-  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // by tile and half
+  uint64_t kv_full[ST], kv_empty[ST], q_full[2], q_empty[2], o_full[2], x_stat, x_done, s_full[2];
+  uint64_t p_full[2][2], pv_half[2];  // by tile and half of a block's keys; P V of the first half
   uint64_t slot_full[kSlots], slot_empty[kSlots], drain[2];
   uint32_t tmem_base;
   int abort_flag;
@@ -363,6 +363,24 @@ __device__ __forceinline__ void cp_async_wait_n(int n) {
     case 3: cp_async_wait<3>(); break;
     case 4: cp_async_wait<4>(); break;
     default: cp_async_wait<5>(); break;
+  }
+}
+// mbar_wait for the waits of this file, which often fail at first: the clock
+// that bounds the wait is read only after 64 failed tries.
+__device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  unsigned long long t0 = 0;
+#pragma unroll 1
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63u) == 0) {
+      if (*abort_flag) return false;
+      const unsigned long long now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kWaitLimitNs) {
+        *abort_flag = 1;
+        return false;
+      }
+    }
   }
 }
 // 1 in one lane of the converged warp, 0 in the others.  MMAs are predicated
@@ -417,6 +435,14 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+// Stores 16 fp32 columns of this warp's 32 TMEM lanes (complete after tmem_wait_st()).
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+      "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+      : "memory");
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
@@ -480,7 +506,8 @@ __device__ __noinline__ void add_nonfinite(const AttnParams& a, const Piece& w, 
 }
 
 template <int D, bool KV4>
-__global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainParams p) {
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const MainParams p) {
   using C = Cfg<D, KV4>;
   using Sb = Bars<C::kStages, KV4>;
   constexpr int ST = C::kStages;
@@ -503,11 +530,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
     for (int t = 0; t < 2; ++t) {
       mbar_init(smem_u32(&sb.q_full[t]), 1);
       mbar_init(smem_u32(&sb.q_empty[t]), 1);
-      for (int x = 0; x < 2; ++x) {
-        mbar_init(smem_u32(&sb.s_full[t][x]), 1);
-        mbar_init(smem_u32(&sb.p_full[t][x]), 4);
-        mbar_init(smem_u32(&sb.pv_done[t][x]), 1);
-      }
+      mbar_init(smem_u32(&sb.s_full[t]), 1);
+      mbar_init(smem_u32(&sb.p_full[t][0]), 4);
+      mbar_init(smem_u32(&sb.p_full[t][1]), 4);
+      mbar_init(smem_u32(&sb.pv_half[t]), 1);
       mbar_init(smem_u32(&sb.o_full[t]), 1);
     }
     for (int i = 0; i < kSlots; ++i) {
@@ -534,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
   constexpr uint32_t tmem = 0;
 
   auto warp_wait = [&](uint64_t& bar, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), parity, abort_flag)) != 0;
+    return __all_sync(0xffffffffu, mbar_wait_short(smem_u32(&bar), parity, abort_flag)) != 0;
   };
   // The ps-th piece: false at the end of the list (or on abort).
   auto get_piece = [&](int ps, Piece& w) -> bool {
@@ -549,6 +575,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
 
   if (warp < 4) {
     // ------------------------------------------------------ K/V producers
+    // registers move from the copying and issuing warps to the softmax:
+    // 256 x 64 + 256 x 192 = the 512 x 128 of the launch
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     const int tid = threadIdx.x;
     int st = 0;
     uint32_t ph = 0;  // stage and phase of the next tile to be filled
@@ -611,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
 #pragma unroll
           for (int q = 0; q < 8; ++q) pq[q] = __shfl_sync(0xffffffffu, pg, j * 8 + q);
           const bool whole = __all_sync(0xffffffffu, pg >= 0 || (lane >> 3) != j) && key0 + kBlk <= n_keys;
-#pragma unroll
+#pragma unroll 1
           for (int o = 0; o < 2; ++o) {
             ok = warp_wait(sb.kv_empty[st], ph ^ 1u);
             if (!ok) break;
@@ -624,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
                            src + (size_t)pq[i * RPI / 16] * page_bytes + (size_t)(i * RPI & 15) * tok_bytes);
             } else {
 #pragma unroll
-              for (int i = 0; i < IT; ++i) {
+              for (int i = 0; i < IT; ++i) {  // a block with a tail or a page out of range
                 const int q = pq[i * RPI / 16];
                 const bool live = q >= 0 && key0 + i * RPI + row0 < n_keys;
                 cp_async16_or_zero(dst + (uint32_t)i * (RPI * 128u),
@@ -800,13 +829,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
       cp_async_wait_all();
     }
   } else if (warp < 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp < 6) {
       // ------------------------------------------------------- MMA issuers
       // One warp per tile, so that one's waits and commits stand beside the
       // other's MMAs.  Each runs converged, every value the same in its lanes
       // (descriptors and addresses stay in uniform registers), only the MMAs
       // and commits predicated on the elected lane.
-      constexpr uint32_t idesc_s = mma_idesc(kFmt, 128, kHb), idesc_pv = mma_idesc_bmn(kFmt, 128, D);
+      constexpr uint32_t idesc_s = mma_idesc(kFmt, 128, kBlk), idesc_pv = mma_idesc_bmn(kFmt, 128, D);
       const int t = __shfl_sync(0xffffffffu, warp - 4, 0);
       const uint64_t dq = smem_desc_sw128(base + sQ + t * C::kTile), dk0 = smem_desc_sw128(base + sKV);
       const uint64_t dv0 = smem_desc_sw128_mn(base + sKV, C::kHalf);
@@ -823,6 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
       };
       // both warps free every K/V tile; this one does not read this one
       auto skip = [&](int tiles) {
+#pragma unroll 1
         for (int x = 0; x < tiles && ok; ++x) {
           ok = warp_wait(sb.kv_full[st], ph);
           if (ok && lane == 0) mbar_arrive(smem_u32(&sb.kv_empty[st]));
@@ -850,74 +881,60 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
           ok = ok && warp_wait(sb.q_full[t], qph);
           qph ^= 1u;
           int kst = 0, vst = 0;
-          // S of one half of a K tile: 64 keys, columns x * 64 ..
-          auto issue_s = [&](int x, bool last) {
-            const uint64_t dk = dk0 + (uint64_t)((uint32_t)(kst * C::kTile + x * 8192) >> 4);
-            const uint32_t one = elect_one();
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint32_t off = ((uint32_t)(k >> 2) * C::kHalf + (uint32_t)(k & 3) * 32u) >> 4;
-              mma_ss(one, s_col + (uint32_t)(x * kHb), dq + off, dk + off, idesc_s, k > 0);
-            }
-            commit(one, smem_u32(&sb.s_full[t][x]));
-            if (x == 1) {
-              commit(one, smem_u32(&sb.kv_empty[kst]));
-              if (last) commit(one, smem_u32(&sb.q_empty[t]));
-            }
-          };
-          // O += P V of one half of a V tile, once its P is there
-          auto issue_pv = [&](int x, bool first, bool last) {
-            ok = ok && warp_wait(sb.p_full[t][x], pph);
-            if (!ok) return;
-            tc_fence_after();
-            const uint64_t dv = dv0 + (uint64_t)((uint32_t)(vst * C::kTile + x * 8192) >> 4);
-            const uint32_t one = elect_one();
-#pragma unroll
-            for (int k = 0; k < kHb / 16; ++k)
-              mma_ts(one, o_col, s_col + (uint32_t)(x * kHb + k * 8), dv + (uint32_t)k * 128u, idesc_pv,
-                     !first || k > 0);
-            commit(one, smem_u32(&sb.pv_done[t][x]));
-            if (x == 1) {
-              commit(one, smem_u32(&sb.kv_empty[vst]));
-              if (last) commit(one, smem_u32(&sb.o_full[t]));
-            }
-          };
           auto take_k = [&]() {
             take();
             kst = st;
             next_tile();
           };
-          take_k();
-          if (!ok) break;
-          issue_s(0, n == 1);
-          issue_s(1, n == 1);
-          for (int i = 0; i < n && ok; ++i) {
-            const bool last = i + 1 == n;
-            take();
-            vst = st;
-            next_tile();
-            issue_pv(0, i == 0, last);
-            if (twin) {
-              // the next K tile lies past the other tile's two: it may need
-              // this V tile's stage, so V goes first
-              issue_pv(1, false, last);
-              if (ok && !last) {
-                skip(2);
-                take_k();
-                if (!ok) break;
-                issue_s(0, i + 2 == n);
-                issue_s(1, i + 2 == n);
+          // One loop with one place for each kind of MMA, started a step
+          // early, keeps the code small (the roles share an instruction cache
+          // that they overfill).
+#pragma unroll 1
+          for (int h = -1; h < 2 * n && ok; ++h) {
+            const int x = h & 1;
+            if (h >= 0) {  // O += P V of half a block, once its P is there
+              if (x == 0) {
+                take();
+                vst = st;
+                next_tile();
               }
-            } else {
-              if (ok && !last) {
-                take_k();
-                if (!ok) break;
-                issue_s(0, i + 2 == n);
+              ok = ok && warp_wait(sb.p_full[t][x], pph);
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t dv = dv0 + (uint64_t)((uint32_t)(vst * C::kTile + x * (kHb * 128)) >> 4);
+              const uint32_t one = elect_one();
+#pragma unroll
+              for (int k = 0; k < kHb / 16; ++k)
+                mma_ts(one, o_col, s_col + (uint32_t)(x * (kHb / 2) + k * 8), dv + (uint32_t)k * 128u, idesc_pv,
+                       h > 0 || k > 0);
+              if (x == 0) {
+                commit(one, smem_u32(&sb.pv_half[t]));
+                // with alternate blocks the next K tile lies past the other
+                // tile's two and may need this V tile's stage: V goes first
+                if (!twin && h + 2 < 2 * n) take_k();
+              } else {
+                commit(one, smem_u32(&sb.kv_empty[vst]));
+                if (h + 1 == 2 * n) commit(one, smem_u32(&sb.o_full[t]));
+                pph ^= 1u;
               }
-              issue_pv(1, false, last);
-              if (ok && !last) issue_s(1, i + 2 == n);
             }
-            pph ^= 1u;
+            if (x && h + 1 < 2 * n) {  // S = Q K^T of the next block, over the P just read
+              if (twin || h < 0) {
+                if (h > 0) skip(2);
+                if (ok) take_k();
+              }
+              if (!ok) break;
+              const uint64_t dk = dk0 + (uint64_t)((uint32_t)(kst * C::kTile) >> 4);
+              const uint32_t one = elect_one();
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = ((uint32_t)(k >> 2) * C::kHalf + (uint32_t)(k & 3) * 32u) >> 4;
+                mma_ss(one, s_col, dq + off, dk + off, idesc_s, k > 0);
+              }
+              commit(one, smem_u32(&sb.s_full[t]));
+              commit(one, smem_u32(&sb.kv_empty[kst]));
+              if (h + 3 == 2 * n) commit(one, smem_u32(&sb.q_empty[t]));
+            }
           }
           // what follows this tile's last block in the piece
           if (ok) skip(2 * (twin ? nblk - (2 * (n - 1) + t + 1) : nblk - n));
@@ -937,7 +954,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
       const int total = p.hdr->pieces;
       for (int ps = 0;; ++ps) {
         const int slot = ps % kSlots;
-        if (!mbar_wait(smem_u32(&sb.slot_empty[slot]), ((uint32_t)(ps / kSlots) & 1u) ^ 1u, abort_flag)) break;
+        if (!mbar_wait_short(smem_u32(&sb.slot_empty[slot]), ((uint32_t)(ps / kSlots) & 1u) ^ 1u, abort_flag)) break;
         const int i = atomicAdd(p.next, 1);
         if (i < total)
           sb.piece[slot] = p.pieces[i];
@@ -952,42 +969,53 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
     } else {
     // ----------------------------------------------------------- Q loader
     constexpr int CPR = D / 8, RPI = 32 / CPR;  // rows per iteration of the warp
-    const int tid = lane, row0 = tid / CPR, c = tid % CPR;
+    constexpr int QU = 8;                       // rows a lane has in flight
+    const int row0 = lane / CPR, c = lane % CPR;
+    const uint32_t g_inv = (65536u + (uint32_t)p.g - 1) / (uint32_t)p.g;  // r / g = r * g_inv >> 16 for r < 128
+    const uint64_t pol = l2_policy_evict_first();
     int uses[2] = {0, 0};
     bool ok = true;
     Piece w;
     for (int ps = 0; ok; ++ps) {
       if (!get_piece(ps, w)) break;
       const TileWork tw = tile_work(w, p.tpt, p.tpu, p.g);
-#pragma unroll
+#pragma unroll 1
       for (int t = 0; t < 2; ++t) {
-        if (!ok || tw.n(t) == 0) continue;
+        if (tw.n(t) == 0) continue;
         ok = warp_wait(sb.q_empty[t], ((uint32_t)uses[t] & 1u) ^ 1u);
         if (!ok) break;
-        const int rows = tw.rows(t);
-        const size_t tok0 = (size_t)w.c0 + (size_t)w.u * p.tpu + (tw.twin ? 0 : t * p.tpt);
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + tok0 * a.q_stride + (size_t)w.h * p.g * D + c * 8;
-        for (int r0 = 0; r0 < rows; r0 += 4 * RPI) {
-          uint4 v[4];
+        const int tok0 = w.c0 + w.u * p.tpu + (tw.twin ? 0 : t * p.tpt);
+        if constexpr (!KV4) {
+          // one box per 64 columns: tokens x the kv head's query heads, in
+          // the tile's row order (rows past the request's end are another's
+          // or zeros: nothing of them is written)
+          if (lane == 0) {
+            const uint32_t bar = smem_u32(&sb.q_full[t]);
+            mbar_arrive_expect_tx(bar, (uint32_t)(p.tpt * p.g) * 128u * (D / 64));
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int r = r0 + x * RPI + row0;
-            const bool live = r < rows;
-            const __nv_bfloat16* src = live ? q + (size_t)(r / p.g) * a.q_stride + (size_t)(r % p.g) * D : q;
-            const uint32_t off = sQ + t * C::kTile + (uint32_t)(c / 8) * C::kHalf + (uint32_t)r * 128u +
-                                 (uint32_t)(((c % 8) ^ (r & 7)) << 4);
-            if constexpr (KV4)
-              v[x] = live ? *reinterpret_cast<const uint4*>(src) : make_uint4(0u, 0u, 0u, 0u);
-            else if (live)
-              cp_async16(base + off, src);
+            for (int h = 0; h < D / 64; ++h)
+              tma_load_3d(base + sQ + t * C::kTile + h * C::kHalf, &map_q, bar, h * 64, w.h * p.g, tok0, pol);
           }
-          if constexpr (KV4) {
-            // rows as fp16, each scaled by a power of two to [1, 2) at its
-            // largest: bf16's 8 bits fit fp16's 11, and what is below 2^-14
-            // of the row's largest keeps an absolute error of 2^-25 of it
+          __syncwarp();
+        } else {
+          // rows as fp16, each scaled by a power of two to [1, 2) at its
+          // largest: bf16's 8 bits fit fp16's 11, and what is below 2^-14
+          // of the row's largest keeps an absolute error of 2^-25 of it
+          const int rows = tw.rows(t);
+          const __nv_bfloat16* q =
+              static_cast<const __nv_bfloat16*>(a.q) + (size_t)tok0 * a.q_stride + (size_t)w.h * p.g * D + c * 8;
+#pragma unroll 1
+          for (int r0 = row0; r0 < rows + row0; r0 += QU * RPI) {
+            uint4 v[QU];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const int r = r0 + x * RPI + row0;
+            for (int x = 0; x < QU; ++x) {
+              const int r = r0 + x * RPI, tk = (int)((uint32_t)r * g_inv >> 16);
+              v[x] = r < rows ? *reinterpret_cast<const uint4*>(q + (size_t)tk * a.q_stride + (size_t)(r - tk * p.g) * D)
+                              : make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int x = 0; x < QU; ++x) {
+              const int r = r0 + x * RPI;
               const uint32_t e[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
               uint32_t mx = 0;
 #pragma unroll
@@ -1007,14 +1035,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
               }
             }
           }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sb.q_full[t]));
         }
-        if constexpr (!KV4) {
-          cp_async_commit();
-          cp_async_wait<0>();
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sb.q_full[t]));
         ++uses[t];
       }
       if (!ok) break;
@@ -1023,6 +1047,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
     }
   } else {
     // ------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     const int t = (warp - 8) >> 2, q4 = warp & 3, row = q4 * 32 + lane;
     const uint32_t lane_addr = (uint32_t)(q4 * 32) << 16;
     const uint32_t s_addr = tmem + lane_addr + (uint32_t)(t * kBlk);
@@ -1038,72 +1063,94 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_tc_kernel(const MainP
       const bool quad_live = q4 * 32 < rows, row_ok = row < rows;
       const int tok = w.u * p.tpu + (tw.twin ? 0 : t * p.tpt) + row / p.g;
       const int pos = row_ok ? w.ctx + tok : 0x7fffffff;
+      const int pos0 = __shfl_sync(0xffffffffu, pos, 0);  // the warp's first row sees least
       float m = -INFINITY, l = 0.f, sl2 = p.scale_log2;
 #pragma unroll 1
       for (int i = 0; i < n && ok; ++i) {
 #pragma unroll 1
         for (int x = 0; x < 2; ++x) {
-          ok = warp_wait(sb.s_full[t][x], sph);
-          if (!ok) break;
-          tc_fence_after();
+          if (x == 0) {
+            ok = warp_wait(sb.s_full[t], sph);
+            if (!ok) break;
+            tc_fence_after();
+          }
           if (quad_live) {
             if (KV4 && i == 0 && x == 0) sl2 *= row_ok ? sb.q_fac[uses & 1][t][row] : 1.f;
             uint32_t r[kHb];
             tmem_ld32_issue(s_addr + (uint32_t)(x * kHb), r);
             tmem_ld32_issue(s_addr + (uint32_t)(x * kHb + 32), r + 32);
             tmem_wait_ld();
-            const int lim = pos - (w.k0 + tw.blk(t, i)) * kBlk - x * kHb;  // the last visible column
-            if (!__all_sync(0xffffffffu, lim >= kHb - 1)) {
+            const int key0 = (w.k0 + tw.blk(t, i)) * kBlk + x * kHb;
+            if (__builtin_expect(key0 + kHb - 1 > pos0, 0)) {
+              const int lim = pos - key0;  // the last visible column
 #pragma unroll
               for (int c = 0; c < kHb; ++c) r[c] = c <= lim ? r[c] : 0xff800000u;
             }
-            float mx[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) mx[c] = fmaxf(__uint_as_float(r[c]), __uint_as_float(r[c + 4]));
-#pragma unroll
-            for (int c = 8; c < kHb; c += 8)
-#pragma unroll
-              for (int y = 0; y < 4; ++y) mx[y] = max3(mx[y], __uint_as_float(r[c + y]), __uint_as_float(r[c + y + 4]));
-            const float bm = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * sl2;
-            // m is the reference of O and l: it moves, and both are rescaled,
-            // only when a half block's maximum exceeds it by 2^8
-            const bool need = row_ok && bm > m + kRescaleLog2;
-            const bool resc = need && m != -INFINITY;
-            if (__any_sync(0xffffffffu, resc)) {
-              // O must be still: every earlier P V complete
-              ok = warp_wait(sb.pv_done[t][x ^ 1], x ? sph : sph ^ 1u);
-              if (!ok) break;
-              tc_fence_after();
-              const float alpha = resc ? ex2_approx(m - bm) : 1.f;
-#pragma unroll 1
-              for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld32_issue(o_addr + (uint32_t)(c * 32), o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-                tmem_st32(o_addr + (uint32_t)(c * 32), o);
-              }
-              l *= alpha;
-            }
-            if (need) m = bm;
-            const float neg_m = m == -INFINITY ? 0.f : -m;
-            const uint64_t sc2 = pack2(sl2, sl2), nm2 = pack2(neg_m, neg_m);
-            uint64_t ls[2] = {0ull, 0ull};
+            // m is the reference of O and l.  It need not be the maximum: the
+            // weights' type only has to hold 2^(z - m).  So a row takes the
+            // maximum of the first keys it sees and keeps it until a half
+            // block's weights add up to more than kSumLimit; then (and for
+            // NaN) the maximum is looked for, and O and l are rescaled.
+            // (Only the row itself decides, so its result does not depend on the
+            // rows beside it.)
+            bool mine = row_ok && m == -INFINITY, renew = __any_sync(0xffffffffu, mine);
             uint32_t pk[32];
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              float e0, e1;
-              unpack2(fma2(pack2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])), sc2, nm2), e0, e1);
-              e0 = ex2_approx(e0);
-              e1 = ex2_approx(e1);
-              ls[k & 1] = add2(ls[k & 1], pack2(e0, e1));
-              pk[k] = pack16<KV4>(e0, e1);
-            }
-            tmem_st32(s_addr + (uint32_t)(x * kHb), pk);
             float l0, l1;
-            unpack2(add2(ls[0], ls[1]), l0, l1);
-            l += l0 + l1;
+#pragma unroll 1
+            for (int pass = 0;; ++pass) {
+              if (__builtin_expect(renew, 0)) {
+                float mx[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) mx[c] = fmaxf(__uint_as_float(r[c]), __uint_as_float(r[c + 4]));
+#pragma unroll
+                for (int c = 8; c < kHb; c += 8)
+#pragma unroll
+                  for (int y = 0; y < 4; ++y) mx[y] = max3(mx[y], __uint_as_float(r[c + y]), __uint_as_float(r[c + y + 4]));
+                const float bm = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * sl2;
+                const bool resc = mine && bm > m && m != -INFINITY;
+                if (__any_sync(0xffffffffu, resc)) {
+                  // O must be still.  S of this block was issued after P V of
+                  // the one before; its own first half may be under way.
+                  if (x) {
+                    ok = warp_wait(sb.pv_half[t], sph);
+                    if (!ok) break;
+                    tc_fence_after();
+                  }
+                  const float alpha = resc ? ex2_approx(m - bm) : 1.f;
+#pragma unroll 1
+                  for (int c = 0; c < D / 16; ++c) {
+                    float o[16];
+                    tmem_ld16(o_addr + (uint32_t)(c * 16), o);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) o[k] *= alpha;
+                    tmem_st16(o_addr + (uint32_t)(c * 16), o);
+                  }
+                  l *= alpha;
+                }
+                if (mine && bm > m) m = bm;
+              }
+              const float neg_m = m == -INFINITY ? 0.f : -m;
+              const uint64_t sc2 = pack2(sl2, sl2), nm2 = pack2(neg_m, neg_m);
+              uint64_t ls[2] = {0ull, 0ull};
+#pragma unroll
+              for (int k = 0; k < 32; ++k) {
+                float e0, e1;
+                unpack2(fma2(pack2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])), sc2, nm2), e0, e1);
+                e0 = ex2_approx(e0);
+                e1 = ex2_approx(e1);
+                ls[k & 1] = add2(ls[k & 1], pack2(e0, e1));
+                pk[k] = pack16<KV4>(e0, e1);
+              }
+              unpack2(add2(ls[0], ls[1]), l0, l1);
+              l0 += l1;
+              if (pass) break;
+              mine = row_ok && !(l0 <= kSumLimit);
+              renew = __any_sync(0xffffffffu, mine);
+              if (!renew) break;
+            }
+            if (!ok) break;
+            tmem_st32(s_addr + (uint32_t)(x * (kHb / 2)), pk);
+            l += l0;
             tmem_wait_st();
           }
           tc_fence_before();
@@ -1363,12 +1410,16 @@ int attn_launch_tc(const AttnParams& a, void* ws, cudaStream_t s) {
     cudaGetLastError();
     return EAGLE_ERR_CUDA;
   }
+  CUtensorMap map_q = {};
+  if (!KV4 && !make_tmap_3d_bf16(&map_q, a.q, D, (uint64_t)a.Hq, (uint64_t)a.T, (uint64_t)D * 2, (uint64_t)a.q_stride * 2,
+                                 64, (uint32_t)sh.g, (uint32_t)sh.tpt))
+    return EAGLE_ERR_CUDA;
   const PlanParams pp = {a.cu, a.ctx, a.B, a.T, a.Hkv, a.max_pages, sh.tpu, sh.g, sh.ctas, sh.cap_pieces, sh.cap_slots,
                          hdr, pieces, cuts, a.status};
   launch(prompt_plan_kernel, 1, kPlanThreads, 0, s, pp);
   const MainParams mp = {a, a.scale * a.k_scale * 1.4426950408889634f, sh.g, sh.tpt, sh.tpu, sh.rows, hdr, &hdr->next,
                          pieces, ml, po};
-  launch(kern, sh.ctas, kThreads, C::kSmem, s, mp);
+  launch(kern, sh.ctas, kThreads, C::kSmem, s, map_q, mp);
   const MergeParams gp = {hdr, cuts, ml, po, static_cast<__nv_bfloat16*>(a.out), a.lse, a.v_scale, a.Hq, sh.g, sh.tpu,
                           sh.rows};
   launch(prompt_merge_kernel<D>, 2 * sh.ctas, 256, 0, s, gp);
