@@ -26,9 +26,8 @@ namespace eagle {
 namespace {
 
 constexpr int kBlk = 128;        // keys per block
-constexpr int kHb = 64;          // keys per softmax step (half a block)
 constexpr int kTileRows = 128;   // query rows per tile
-constexpr float kSumLimit = 256.f;  // fp16 weights: 64 of them stay below 2^8 each
+constexpr float kSumLimit = 256.f;  // of a block's weights: far below fp16's 65504
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct AttnParams {
@@ -328,7 +327,8 @@ struct MainParams {
 template <int ST, bool KV4>
 struct Bars {
   uint64_t kv_full[ST], kv_empty[ST], q_full[2], q_empty[2], o_full[2], x_stat, x_done, s_full[2];
-  uint64_t p_full[2][2], pv_half[2];  // by tile and half of a block's keys; P V of the first half
+  uint64_t turn[2][4];  // by tile and quarter: the other tile's softmax has done its block
+  uint64_t p_full[2];
   uint64_t slot_full[kSlots], slot_empty[kSlots], drain[2];
   uint32_t tmem_base;
   int abort_flag;
@@ -489,17 +489,17 @@ __device__ __forceinline__ TileWork tile_work(const Piece& w, int tpt, int tpu, 
 // Adds to a row's written result the non-finite values it sees in the masked
 // blocks, which the stages held as zeros (cold: only when there are any).
 template <int D, bool KV4, typename T>
-__device__ __noinline__ void add_nonfinite(const AttnParams& a, const Piece& w, int first, int pos, T* row) {
-  for (int k = max(first, w.k0 * kBlk); k <= pos && k < w.k1 * kBlk; ++k) {
-    const int page = a.table[(size_t)w.b * a.max_pages + k / 16];
+__device__ __noinline__ void add_nonfinite(const AttnParams& a, int req, int h, int first, int last, T* row) {
+  for (int k = first; k <= last; ++k) {
+    const int page = a.table[(size_t)req * a.max_pages + k / 16];
     if (page < 0 || page >= a.num_pages) continue;
     for (int d = 0; d < D; ++d) {
       float v;
       if (KV4)
-        v = kv4_scale_value(a.vs[(((size_t)page * a.Hkv + w.h) * 16 + (k & 15)) * (D / 16) + d / 16]);
+        v = kv4_scale_value(a.vs[(((size_t)page * a.Hkv + h) * 16 + (k & 15)) * (D / 16) + d / 16]);
       else
         v = __bfloat162float(
-            static_cast<const __nv_bfloat16*>(a.vc)[(((size_t)page * 16 + (k & 15)) * a.Hkv + w.h) * D + d]);
+            static_cast<const __nv_bfloat16*>(a.vc)[(((size_t)page * 16 + (k & 15)) * a.Hkv + h) * D + d]);
       if (!isfinite(v)) row[d] = (T)((float)row[d] + v);
     }
   }
@@ -531,9 +531,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&sb.q_full[t]), 1);
       mbar_init(smem_u32(&sb.q_empty[t]), 1);
       mbar_init(smem_u32(&sb.s_full[t]), 1);
-      mbar_init(smem_u32(&sb.p_full[t][0]), 4);
-      mbar_init(smem_u32(&sb.p_full[t][1]), 4);
-      mbar_init(smem_u32(&sb.pv_half[t]), 1);
+      mbar_init(smem_u32(&sb.p_full[t]), 4);
+      for (int q = 0; q < 4; ++q) mbar_init(smem_u32(&sb.turn[t][q]), 1);
       mbar_init(smem_u32(&sb.o_full[t]), 1);
     }
     for (int i = 0; i < kSlots; ++i) {
@@ -886,41 +885,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             kst = st;
             next_tile();
           };
-          // One loop with one place for each kind of MMA, started a step
-          // early, keeps the code small (the roles share an instruction cache
-          // that they overfill).
+          // Block i: P V(i), then S(i + 1) over the P just read (one loop with
+          // one place for each, started a step early, keeps the code small).
 #pragma unroll 1
-          for (int h = -1; h < 2 * n && ok; ++h) {
-            const int x = h & 1;
-            if (h >= 0) {  // O += P V of half a block, once its P is there
-              if (x == 0) {
-                take();
-                vst = st;
-                next_tile();
-              }
-              ok = ok && warp_wait(sb.p_full[t][x], pph);
+          for (int i = -1; i < n && ok; ++i) {
+            const bool more = i + 1 < n;
+            if (i >= 0) {
+              take();
+              vst = st;
+              next_tile();
+              // with alternate blocks the next K tile lies past the other
+              // tile's two and may need this V tile's stage: V goes first
+              if (more && !twin) take_k();
+              ok = ok && warp_wait(sb.p_full[t], pph);
               if (!ok) break;
+              pph ^= 1u;
               tc_fence_after();
-              const uint64_t dv = dv0 + (uint64_t)((uint32_t)(vst * C::kTile + x * (kHb * 128)) >> 4);
+              const uint64_t dv = dv0 + (uint64_t)((uint32_t)(vst * C::kTile) >> 4);
               const uint32_t one = elect_one();
 #pragma unroll
-              for (int k = 0; k < kHb / 16; ++k)
-                mma_ts(one, o_col, s_col + (uint32_t)(x * (kHb / 2) + k * 8), dv + (uint32_t)k * 128u, idesc_pv,
-                       h > 0 || k > 0);
-              if (x == 0) {
-                commit(one, smem_u32(&sb.pv_half[t]));
-                // with alternate blocks the next K tile lies past the other
-                // tile's two and may need this V tile's stage: V goes first
-                if (!twin && h + 2 < 2 * n) take_k();
-              } else {
-                commit(one, smem_u32(&sb.kv_empty[vst]));
-                if (h + 1 == 2 * n) commit(one, smem_u32(&sb.o_full[t]));
-                pph ^= 1u;
-              }
+              for (int k = 0; k < kBlk / 16; ++k)
+                mma_ts(one, o_col, s_col + (uint32_t)(k * 8), dv + (uint32_t)k * 128u, idesc_pv, i > 0 || k > 0);
+              commit(one, smem_u32(&sb.kv_empty[vst]));
+              if (!more) commit(one, smem_u32(&sb.o_full[t]));
             }
-            if (x && h + 1 < 2 * n) {  // S = Q K^T of the next block, over the P just read
-              if (twin || h < 0) {
-                if (h > 0) skip(2);
+            if (more) {
+              if (twin || i < 0) {
+                if (i >= 0) skip(2);
                 if (ok) take_k();
               }
               if (!ok) break;
@@ -933,7 +924,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               commit(one, smem_u32(&sb.s_full[t]));
               commit(one, smem_u32(&sb.kv_empty[kst]));
-              if (h + 3 == 2 * n) commit(one, smem_u32(&sb.q_empty[t]));
+              if (i + 2 == n) commit(one, smem_u32(&sb.q_empty[t]));
             }
           }
           // what follows this tile's last block in the piece
@@ -1052,7 +1043,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_addr = (uint32_t)(q4 * 32) << 16;
     const uint32_t s_addr = tmem + lane_addr + (uint32_t)(t * kBlk);
     const uint32_t o_addr = tmem + lane_addr + C::kColO + (uint32_t)(t * D);
-    uint32_t sph = 0, oph = 0, xph = 0;
+    uint32_t sph = 0, oph = 0, xph = 0, tph = 0;
     int uses = 0;
     bool ok = true;
     Piece w;
@@ -1063,101 +1054,108 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool quad_live = q4 * 32 < rows, row_ok = row < rows;
       const int tok = w.u * p.tpu + (tw.twin ? 0 : t * p.tpt) + row / p.g;
       const int pos = row_ok ? w.ctx + tok : 0x7fffffff;
+      // Two warps of a scheduler, one per tile, take turns at a block's
+      // softmax: left alone the tiles fall into step, both in their softmax
+      // and then both waiting for their MMAs.  (Not with alternate blocks,
+      // where the MMAs are few.)  Tile 0 goes first; a turn is passed on only
+      // where the other tile has a block to take it.
+      const bool turns = !tw.twin && q4 * 32 < min(tw.rows0, tw.rows1);
+      const int n_wait = !turns ? 0 : t ? min(tw.n0, tw.n1) : min(tw.n0 - 1, tw.n1);  // turns waited for
+      const int n_pass = !turns ? 0 : t ? min(tw.n0 - 1, tw.n1) : min(tw.n0, tw.n1);  // turns passed on
       const int pos0 = __shfl_sync(0xffffffffu, pos, 0);  // the warp's first row sees least
       float m = -INFINITY, l = 0.f, sl2 = p.scale_log2;
+      bool fresh = true;  // some row has seen no key yet
+      int key0 = (w.k0 + tw.blk(t, 0)) * kBlk;
+      const int key_step = tw.twin ? 2 * kBlk : kBlk;
 #pragma unroll 1
-      for (int i = 0; i < n && ok; ++i) {
-#pragma unroll 1
-        for (int x = 0; x < 2; ++x) {
-          if (x == 0) {
-            ok = warp_wait(sb.s_full[t], sph);
+      for (int i = 0; i < n; ++i, key0 += key_step) {
+        ok = warp_wait(sb.s_full[t], sph);
+        if (!ok) break;
+        sph ^= 1u;
+        tc_fence_after();
+        if (quad_live) {
+          if (KV4 && i == 0) sl2 *= row_ok ? sb.q_fac[uses & 1][t][row] : 1.f;
+          if (i >= 1 - t && i < n_wait + 1 - t) {
+            ok = warp_wait(sb.turn[t][q4], tph);
             if (!ok) break;
-            tc_fence_after();
+            tph ^= 1u;
           }
-          if (quad_live) {
-            if (KV4 && i == 0 && x == 0) sl2 *= row_ok ? sb.q_fac[uses & 1][t][row] : 1.f;
-            uint32_t r[kHb];
-            tmem_ld32_issue(s_addr + (uint32_t)(x * kHb), r);
-            tmem_ld32_issue(s_addr + (uint32_t)(x * kHb + 32), r + 32);
+          // m is the reference of O and l.  It need not be the maximum: the
+          // weights' type only has to hold 2^(z - m).  So a row takes the
+          // maximum of the first keys it sees and keeps it until a block's
+          // weights add up to more than kSumLimit; then (and for NaN) the
+          // block's maximum is looked for, and O and l are rescaled.  (Only
+          // the row itself decides, so its result does not depend on the rows
+          // beside it.)
+          bool mine = row_ok && m == -INFINITY, renew = fresh;
+          uint32_t pk[64];
+          float l0;
+#pragma unroll 1
+          for (int pass = 0;; ++pass) {
+            uint32_t r[kBlk];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32_issue(s_addr + (uint32_t)(c * 32), r + c * 32);
             tmem_wait_ld();
-            const int key0 = (w.k0 + tw.blk(t, i)) * kBlk + x * kHb;
-            if (__builtin_expect(key0 + kHb - 1 > pos0, 0)) {
+            if (__builtin_expect(key0 + kBlk - 1 > pos0, 0)) {
               const int lim = pos - key0;  // the last visible column
 #pragma unroll
-              for (int c = 0; c < kHb; ++c) r[c] = c <= lim ? r[c] : 0xff800000u;
+              for (int c = 0; c < kBlk; ++c) r[c] = c <= lim ? r[c] : 0xff800000u;
             }
-            // m is the reference of O and l.  It need not be the maximum: the
-            // weights' type only has to hold 2^(z - m).  So a row takes the
-            // maximum of the first keys it sees and keeps it until a half
-            // block's weights add up to more than kSumLimit; then (and for
-            // NaN) the maximum is looked for, and O and l are rescaled.
-            // (Only the row itself decides, so its result does not depend on the
-            // rows beside it.)
-            bool mine = row_ok && m == -INFINITY, renew = __any_sync(0xffffffffu, mine);
-            uint32_t pk[32];
-            float l0, l1;
+            if (__builtin_expect(renew, 0)) {
+              float mx[4];
+#pragma unroll
+              for (int c = 0; c < 4; ++c) mx[c] = fmaxf(__uint_as_float(r[c]), __uint_as_float(r[c + 4]));
+#pragma unroll
+              for (int c = 8; c < kBlk; c += 8)
+#pragma unroll
+                for (int y = 0; y < 4; ++y) mx[y] = max3(mx[y], __uint_as_float(r[c + y]), __uint_as_float(r[c + y + 4]));
+              const float bm = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * sl2;
+              const bool resc = mine && bm > m && m != -INFINITY;
+              if (__any_sync(0xffffffffu, resc)) {
+                // S(i) was issued after P V(i - 1): O is still
+                const float alpha = resc ? ex2_approx(m - bm) : 1.f;
 #pragma unroll 1
-            for (int pass = 0;; ++pass) {
-              if (__builtin_expect(renew, 0)) {
-                float mx[4];
+                for (int c = 0; c < D / 16; ++c) {
+                  float o[16];
+                  tmem_ld16(o_addr + (uint32_t)(c * 16), o);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) mx[c] = fmaxf(__uint_as_float(r[c]), __uint_as_float(r[c + 4]));
-#pragma unroll
-                for (int c = 8; c < kHb; c += 8)
-#pragma unroll
-                  for (int y = 0; y < 4; ++y) mx[y] = max3(mx[y], __uint_as_float(r[c + y]), __uint_as_float(r[c + y + 4]));
-                const float bm = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * sl2;
-                const bool resc = mine && bm > m && m != -INFINITY;
-                if (__any_sync(0xffffffffu, resc)) {
-                  // O must be still.  S of this block was issued after P V of
-                  // the one before; its own first half may be under way.
-                  if (x) {
-                    ok = warp_wait(sb.pv_half[t], sph);
-                    if (!ok) break;
-                    tc_fence_after();
-                  }
-                  const float alpha = resc ? ex2_approx(m - bm) : 1.f;
-#pragma unroll 1
-                  for (int c = 0; c < D / 16; ++c) {
-                    float o[16];
-                    tmem_ld16(o_addr + (uint32_t)(c * 16), o);
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) o[k] *= alpha;
-                    tmem_st16(o_addr + (uint32_t)(c * 16), o);
-                  }
-                  l *= alpha;
+                  for (int k = 0; k < 16; ++k) o[k] *= alpha;
+                  tmem_st16(o_addr + (uint32_t)(c * 16), o);
                 }
-                if (mine && bm > m) m = bm;
+                l *= alpha;
               }
-              const float neg_m = m == -INFINITY ? 0.f : -m;
-              const uint64_t sc2 = pack2(sl2, sl2), nm2 = pack2(neg_m, neg_m);
-              uint64_t ls[2] = {0ull, 0ull};
-#pragma unroll
-              for (int k = 0; k < 32; ++k) {
-                float e0, e1;
-                unpack2(fma2(pack2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])), sc2, nm2), e0, e1);
-                e0 = ex2_approx(e0);
-                e1 = ex2_approx(e1);
-                ls[k & 1] = add2(ls[k & 1], pack2(e0, e1));
-                pk[k] = pack16<KV4>(e0, e1);
-              }
-              unpack2(add2(ls[0], ls[1]), l0, l1);
-              l0 += l1;
-              if (pass) break;
-              mine = row_ok && !(l0 <= kSumLimit);
-              renew = __any_sync(0xffffffffu, mine);
-              if (!renew) break;
+              if (mine && bm > m) m = bm;
+              if (fresh) fresh = __any_sync(0xffffffffu, row_ok && m == -INFINITY);
             }
-            if (!ok) break;
-            tmem_st32(s_addr + (uint32_t)(x * (kHb / 2)), pk);
-            l += l0;
-            tmem_wait_st();
+            const float neg_m = m == -INFINITY ? 0.f : -m;
+            const uint64_t sc2 = pack2(sl2, sl2), nm2 = pack2(neg_m, neg_m);
+            uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+            for (int k = 0; k < 64; ++k) {
+              float e0, e1;
+              unpack2(fma2(pack2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])), sc2, nm2), e0, e1);
+              e0 = ex2_approx(e0);
+              e1 = ex2_approx(e1);
+              ls[k & 3] = add2(ls[k & 3], pack2(e0, e1));
+              pk[k] = pack16<KV4>(e0, e1);
+            }
+            float l1;
+            unpack2(add2(add2(ls[0], ls[1]), add2(ls[2], ls[3])), l0, l1);
+            l0 += l1;
+            if (pass) break;
+            mine = row_ok && !(l0 <= kSumLimit);
+            renew = __any_sync(0xffffffffu, mine);
+            if (!renew) break;
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sb.p_full[t][x]));
+          if (i < n_pass && lane == 0) mbar_arrive(smem_u32(&sb.turn[t ^ 1][q4]));
+          tmem_st32(s_addr, pk);
+          tmem_st32(s_addr + 32u, pk + 32);
+          l += l0;
+          tmem_wait_st();
         }
-        sph ^= 1u;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sb.p_full[t]));
       }
       if (!ok) break;
       if (n > 0) {
@@ -1234,11 +1232,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             p.part_ml[prow] = make_float2(m, l);
           }
           if (*(volatile int*)&sb.bad_v[ps % kSlots]) {
-            const int first = (w.ctx + w.u * p.tpu) / kBlk * kBlk;  // the first masked block
+            // the keys it sees from the first masked block on, in this piece
+            const int first = max((w.ctx + w.u * p.tpu) / kBlk, w.k0) * kBlk, last = min(pos, w.k1 * kBlk - 1);
             if (whole)
-              add_nonfinite<D, KV4>(a, w, first, pos, static_cast<__nv_bfloat16*>(a.out) + orow * D);
+              add_nonfinite<D, KV4>(a, w.b, w.h, first, last, static_cast<__nv_bfloat16*>(a.out) + orow * D);
             else
-              add_nonfinite<D, KV4>(a, w, first, pos, p.part_o + prow * D);
+              add_nonfinite<D, KV4>(a, w.b, w.h, first, last, p.part_o + prow * D);
           }
         }
       }
