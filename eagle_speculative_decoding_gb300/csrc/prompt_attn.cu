@@ -365,23 +365,18 @@ __device__ __forceinline__ void cp_async_wait_n(int n) {
     default: cp_async_wait<5>(); break;
   }
 }
-// mbar_wait for the waits of this file, which often fail at first: the clock
-// that bounds the wait is read only after 64 failed tries.
+// The bounded wait of this file's kernel: a failed try suspends the thread for
+// about 4 us, so 2^19 of them are the 2 s of mbar_wait, without its clock
+// reads (some thirty waits are in line here, and the roles share an
+// instruction cache).
 __device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  unsigned long long t0 = 0;
 #pragma unroll 1
-  for (uint32_t i = 1;; ++i) {
+  for (int i = 0; i < (1 << 19); ++i) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 63u) == 0) {
-      if (*abort_flag) return false;
-      const unsigned long long now = globaltimer_ns();
-      if (t0 == 0) t0 = now;
-      if (now - t0 > kWaitLimitNs) {
-        *abort_flag = 1;
-        return false;
-      }
-    }
+    if (*abort_flag) return false;
   }
+  *abort_flag = 1;
+  return false;
 }
 // 1 in one lane of the converged warp, 0 in the others.  MMAs are predicated
 // on it: a predicate by elect.sync lets the compiler issue them once (64.5
@@ -679,22 +674,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       cp_async_wait_all();
     } else {
       constexpr int R = C::kRawRing;
-      constexpr int CC = 32 * (D / 2) / 16 / 32;       // code copies per lane: a warp has 32 rows
-      constexpr int SCH = 32 * (D / 16) / 16;          // 16-byte scale chunks of 32 rows
-      constexpr int PC = 16 * (D / 2) / 16;            // code chunks of a page and head
-      constexpr int PS = 16 * (D / 16) / 16;           // scale chunks of a page and head
+      constexpr int CP = 16 * (D / 2) / 16 / 32;  // code copies per lane and page (16 tokens of a head)
+      constexpr int SP = 16 * (D / 16) / 16;      // 16-byte scale copies per page
       int issued = 0, consumed = 0, islot = 0, cslot = 0;  // tiles, and their raw slots
       // the cursor of the copies runs ahead of that of the conversion
-      int ib = 0, ih = 0, ik1 = 0, ikeys = 0;  // its piece
-      int ips = 0, iblk = 0, iop = 0, igrp = 0, ipg = kNoPage, ipg_next = kNoPage, ip0 = kNoPage, ip1 = kNoPage;
+      int ips = 0, iblk = 0, ik1 = 0, ikeys = 0, iop = 0, igrp = 0, ipg = kNoPage, ipg_next = kNoPage;
+      const int32_t* itab = nullptr;
+      size_t ihead = 0;  // the kv head's 16 x D channels in a page
       bool have = false, last = false;
+      const size_t page_ch = (size_t)a.Hkv * 16 * D;  // channels of a page
+      const uint32_t raw0 = base + sRaw + (uint32_t)(warp * 32 * (D / 2) + lane * 16);
+      const uint32_t raws0 = base + sRaw + C::kRawCodes + (uint32_t)(warp * 32 * (D / 16) + lane * 16);
       // page ids of 16 blocks at a time, lane 2 j + q: page q of this warp's 32
       // keys of block j; the next are loaded one group ahead (a wait for a
       // load is also one for the copies in flight)
       auto pages_of = [&](int blk) -> int {
         const int bl = blk + (lane >> 1), pi = bl * 8 + warp * 2 + (lane & 1);
-        return bl < ik1 && pi * 16 < ikeys ? a.table[(size_t)ib * a.max_pages + pi] : kNoPage;
+        return bl < ik1 && pi * 16 < ikeys ? itab[pi] : kNoPage;
       };
+      int ip0 = kNoPage, ip1 = kNoPage;
       auto issue = [&](bool must) -> bool {
         if (!have) {
           if (last) return false;
@@ -707,8 +705,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             return false;
           }
           have = true;
-          ib = w.b;
-          ih = w.h;
+          itab = a.table + (size_t)w.b * a.max_pages;
+          ihead = (size_t)w.h * (16 * D);
           ik1 = w.k1;
           ikeys = w.ctx + w.n;
           iblk = w.k0;
@@ -729,25 +727,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           ip1 = __shfl_sync(0xffffffffu, ipg, 2 * igrp + 1);
           igrp = (igrp + 1) & 15;
         }
-        const uint8_t* codes = static_cast<const uint8_t*>(iop ? a.vc : a.kc);
+        const uint8_t* codes = static_cast<const uint8_t*>(iop ? a.vc : a.kc) + lane * 16;
         const uint8_t* scales = iop ? a.vs : a.ks;
-        const uint32_t dst = base + sRaw + (uint32_t)islot * C::kRaw;
+        const uint32_t slot_off = (uint32_t)islot * C::kRaw;
         if (++islot == R) islot = 0;
+        const bool live0 = ip0 >= 0, live1 = ip1 >= 0;
+        const size_t ch0 = live0 ? (size_t)ip0 * page_ch + ihead : 0, ch1 = live1 ? (size_t)ip1 * page_ch + ihead : 0;
 #pragma unroll
-        for (int i = 0; i < CC; ++i) {
-          const int ch = i * 32 + lane;  // chunk of the warp's rows
-          const int pq = ch / PC ? ip1 : ip0;
-          const bool live = pq >= 0;
-          cp_async16_or_zero(dst + (uint32_t)(warp * 32 * (D / 2) + ch * 16),
-                     live ? codes + ((size_t)pq * a.Hkv + ih) * (16 * D / 2) + (ch % PC) * 16 : codes, live);
-        }
-        {
-          const int ch = lane % SCH;
-          const int pq = ch / PS ? ip1 : ip0;
-          const bool live = pq >= 0;
-          if (lane < SCH)
-            cp_async16_or_zero(dst + C::kRawCodes + (uint32_t)(warp * 32 * (D / 16) + ch * 16),
-                       live ? scales + ((size_t)pq * a.Hkv + ih) * (16 * D / 16) + (ch % PS) * 16 : scales, live);
+        for (int i = 0; i < CP; ++i) cp_async16_or_zero(raw0 + slot_off + i * 512u, codes + (ch0 >> 1) + i * 512, live0);
+#pragma unroll
+        for (int i = 0; i < CP; ++i)
+          cp_async16_or_zero(raw0 + slot_off + (CP + i) * 512u, codes + (ch1 >> 1) + i * 512, live1);
+        if (lane < 2 * SP) {
+          const bool second = lane >= SP;
+          cp_async16_or_zero(raws0 + slot_off, scales + ((second ? ch1 : ch0) >> 4) + (lane & (SP - 1)) * 16,
+                             second ? live1 : live0);
         }
         cp_async_commit();
         ++issued;
