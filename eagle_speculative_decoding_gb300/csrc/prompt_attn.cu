@@ -14,7 +14,7 @@
 //           a CTA's fair share are cut along the keys; longest pieces first
 //   main    one persistent CTA per SM takes pieces from that list
 //   merge   joins the pieces of cut units
-// fp32 rows: one warp per (row, query head) on the CUDA cores.
+// fp32 rows: the same list and merge around a kernel on the CUDA cores.
 #include <math.h>
 
 #include <algorithm>
@@ -27,8 +27,9 @@ namespace {
 
 constexpr int kBlk = 128;        // keys per block
 constexpr int kTileRows = 128;   // query rows per tile
+constexpr int kF32Rows = 64;     // query rows per unit of the fp32 path
 constexpr float kSumLimit = 256.f;  // of a block's weights: far below fp16's 65504
-constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 
 struct AttnParams {
   const void* q;
@@ -61,16 +62,17 @@ constexpr int kCand = 6;       // candidate cuts of the plan
 constexpr int kMaxShare = 6;   // pieces per CTA at the finest cut
 __device__ __constant__ const int kShares[kCand] = {0, 1, 2, 3, 4, 6};  // 0: no unit is cut
 
-struct Shape {  // of the bf16 path, on the host and the device
+struct Shape {
   int g, tpt, tpu, rows;  // heads per kv head, tokens per tile and unit, rows per slot
   int ctas, cap_units, cap_pieces, cap_slots;
   size_t off_pieces, off_cuts, off_ml, off_o, total;
 };
-Shape attn_shape(int B, int T, int Hq, int Hkv, int D) {
+// unit_rows: 256 (two tensor-core tiles) or 64 (fp32)
+Shape attn_shape(int B, int T, int Hq, int Hkv, int D, int unit_rows) {
   Shape s;
   s.g = Hq / Hkv;
-  s.tpt = kTileRows / s.g;
-  s.tpu = 2 * s.tpt;
+  s.tpt = (unit_rows == kF32Rows ? kF32Rows : kTileRows) / s.g;
+  s.tpu = unit_rows == kF32Rows ? s.tpt : 2 * s.tpt;
   s.rows = std::min(s.tpu, T) * s.g;
   const int sms = sm_count();
   s.ctas = sms > 0 ? sms : 152;
@@ -1267,12 +1269,12 @@ struct MergeParams {
   const Cut* cuts;
   const float2* ml;
   const float* o;
-  __nv_bfloat16* out;
+  void* out;  // bf16 or fp32
   float* lse;
   float v_scale;
   int Hq, g, tpu, slot_rows;
 };
-template <int D>
+template <int D, bool F32>
 __global__ void __launch_bounds__(256) prompt_merge_kernel(const MergeParams p) {
   constexpr int E = D / 32;
   pdl_wait();
@@ -1305,73 +1307,203 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const MergeParams p) 
     }
     const float inv = l == 0.f ? 0.f : p.v_scale / l;
     const size_t orow = ((size_t)c.c0 + tok) * p.Hq + c.h * p.g + r % p.g;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + orow * D) + lane * (E / 2);
+    if constexpr (F32) {
+      float* dst = static_cast<float*>(p.out) + orow * D + lane * E;
 #pragma unroll
-    for (int e = 0; e < E / 2; ++e) dst[e] = pack16<false>(o[2 * e] * inv, o[2 * e + 1] * inv);
+      for (int e = 0; e < E; ++e) dst[e] = o[e] * inv;
+    } else {
+      uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + orow * D) + lane * (E / 2);
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) dst[e] = pack16<false>(o[2 * e] * inv, o[2 * e + 1] * inv);
+    }
     if (p.lse && lane == 0) p.lse[orow] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
   }
 }
 
 // ------------------------------------------------------------------- fp32
-// One warp per (row, query head), the lanes sharing the channels: one pass
-// over the keys with a running maximum and sum.
+// Units of 64 rows against 128-key blocks on the CUDA cores, from the same
+// list of pieces.  256 threads: thread (ty, tx) holds scores of rows 4 ty ..
+// against keys tx + 16 j, and of O the same rows' columns 4 tx .. (and 64 + 4
+// tx ..): 128 FMAs for every 12 16-byte shared loads, rows padded so that 16
+// keys' loads touch all banks evenly.  K of the next block is copied while the
+// weights and P V of this one are computed, V of the next during its scores.
 template <int D>
-__global__ void __launch_bounds__(128) prompt_attn_f32_kernel(const AttnParams p) {
-  constexpr int E = D / 32;
+struct CfgF32 {
+  static constexpr int kLd = D + 4, kLdP = kBlk + 4;  // floats per shared row
+  static constexpr int kSmem = (kF32Rows * kLd + 2 * kBlk * kLd + kF32Rows * kLdP) * 4;
+};
+struct F32Params {
+  AttnParams a;
+  float scale_log2;
+  int g, tpu, slot_rows;
+  const PlanHeader* hdr;
+  int* next;
+  const Piece* pieces;
+  float2* part_ml;
+  float* part_o;
+};
+template <int D>
+__global__ void __launch_bounds__(256, 1) prompt_attn_f32_kernel(const F32Params p) {
+  using C = CfgF32<D>;
+  constexpr int CPR = D / 4, NC = D / 64;  // 16-byte chunks per row, 64-column groups
+  extern __shared__ __align__(16) float sm[];
+  float *sq = sm, *sk = sq + kF32Rows * C::kLd, *sv = sk + kBlk * C::kLd, *sp = sv + kBlk * C::kLd;
+  __shared__ int s_piece;
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, t = blockIdx.x, h = blockIdx.y * 4 + (threadIdx.x >> 5);
-  if (h >= p.Hq) return;
-  const int b = warp_find_request(p.cu, p.B, t);
-  const int c0 = p.cu[b], c1 = p.cu[b + 1], ctx = p.ctx[b];
-  if (t < c0 || t >= c1 || c0 < 0 || c1 > p.T || ctx < 0) {
-    set_status(p.status, EAGLE_ERR_INVALID_ARG);
-    return;
-  }
-  if ((long long)ctx + (c1 - c0) > 16ll * p.max_pages) {
-    set_status(p.status, EAGLE_ERR_BAD_KV);
-    return;
-  }
-  const int hk = h / (p.Hq / p.Hkv), n = ctx + (t - c0) + 1;
-  const float* qr = static_cast<const float*>(p.q) + (size_t)t * p.q_stride + (size_t)h * D + lane;
-  float q[E], o[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = qr[32 * e];
-    o[e] = 0.f;
-  }
-  for (int j = 0; j < n; ++j) {
-    const int page = p.table[(size_t)b * p.max_pages + j / 16];
-    float k[E], v[E];
-    if (page >= 0 && page < p.num_pages) {
-      const size_t at = (((size_t)page * 16 + (j & 15)) * p.Hkv + hk) * D + lane;
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        k[e] = static_cast<const float*>(p.kc)[at + 32 * e];
-        v[e] = static_cast<const float*>(p.vc)[at + 32 * e];
+  const AttnParams& a = p.a;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  for (;;) {
+    __syncthreads();
+    if (tid == 0) s_piece = atomicAdd(p.next, 1);
+    __syncthreads();
+    if (s_piece >= p.hdr->pieces) break;
+    const Piece w = p.pieces[s_piece];
+    const int rows = min(w.n - w.u * p.tpu, p.tpu) * p.g, n_keys = w.ctx + w.n;
+    const int32_t* tab = a.table + (size_t)w.b * a.max_pages;
+    auto copy = [&](float* dst, const void* src, int blk) {
+      if (blk < w.k1) {
+#pragma unroll 8
+        for (int i = tid; i < kBlk * CPR; i += 256) {
+          const int r = i / CPR, c = i % CPR, k = blk * kBlk + r;
+          const int pg = k < n_keys ? tab[k / 16] : -1;
+          const bool live = pg >= 0 && pg < a.num_pages;
+          if (k < n_keys && !live) set_status(a.status, EAGLE_ERR_BAD_KV);
+          const float* from = static_cast<const float*>(src) +
+                              (live ? (((size_t)pg * 16 + (k & 15)) * a.Hkv + w.h) * D + c * 4 : 0);
+          cp_async16_or_zero(smem_u32(dst + r * C::kLd + c * 4), from, live);
+        }
       }
-    } else {
-      set_status(p.status, EAGLE_ERR_BAD_KV);
-#pragma unroll
-      for (int e = 0; e < E; ++e) k[e] = v[e] = 0.f;
+      cp_async_commit();
+    };
+    copy(sk, a.kc, w.k0);
+    copy(sv, a.vc, w.k0);
+    for (int i = tid; i < kF32Rows * CPR; i += 256) {
+      const int r = i / CPR, c = i % CPR;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < rows)
+        v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) +
+                                             ((size_t)w.c0 + w.u * p.tpu + r / p.g) * a.q_stride +
+                                             (size_t)(w.h * p.g + r % p.g) * D + c * 4);
+      *reinterpret_cast<float4*>(sq + r * C::kLd + c * 4) = v;
     }
-    float z = 0.f;
+    int pos[4];
+    float m[4], l[4], o[4][4 * NC];
 #pragma unroll
-    for (int e = 0; e < E; ++e) z = fmaf(q[e], k[e], z);
+    for (int i = 0; i < 4; ++i) {
+      const int r = ty * 4 + i;
+      pos[i] = r < rows ? w.ctx + w.u * p.tpu + r / p.g : 0x7fffffff;
+      m[i] = -INFINITY;
+      l[i] = 0.f;
 #pragma unroll
-    for (int d = 16; d; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
-    z *= p.scale;
-    const float mn = fmaxf(m, z), a = m == -INFINITY ? 0.f : expf(m - mn), x = z == -INFINITY ? 0.f : expf(z - mn);
-    l = fmaf(l, a, x);
+      for (int c = 0; c < 4 * NC; ++c) o[i][c] = 0.f;
+    }
+    for (int blk = w.k0; blk < w.k1; ++blk) {
+      const bool masked = blk * kBlk + kBlk - 1 > w.ctx + w.u * p.tpu;
+      cp_async_wait<1>();
+      __syncthreads();
+      float z[4][8];
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], a, x * v[e]);
-    m = mn;
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[i][j] = 0.f;
+#pragma unroll 4
+      for (int c = 0; c < CPR; ++c) {
+        float4 q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const float4*>(sq + (ty * 4 + i) * C::kLd + c * 4);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float4 k = *reinterpret_cast<const float4*>(sk + (tx + 16 * j) * C::kLd + c * 4);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            z[i][j] = fmaf(q[i].x, k.x, fmaf(q[i].y, k.y, fmaf(q[i].z, k.z, fmaf(q[i].w, k.w, z[i][j]))));
+        }
+      }
+      __syncthreads();
+      copy(sk, a.kc, blk + 1);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float bm = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          z[i][j] = blk * kBlk + tx + 16 * j <= pos[i] ? z[i][j] * p.scale_log2 : -INFINITY;
+          bm = fmaxf(bm, z[i][j]);
+        }
+#pragma unroll
+        for (int d = 8; d; d >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, d));
+        const float mn = fmaxf(m[i], bm), ref = mn == -INFINITY ? 0.f : mn;
+        const float al = ex2_approx(m[i] - ref);
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float e = ex2_approx(z[i][j] - ref);
+          sum += e;
+          sp[(ty * 4 + i) * C::kLdP + tx + 16 * j] = e;
+        }
+#pragma unroll
+        for (int d = 8; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        l[i] = fmaf(l[i], al, sum);
+        m[i] = mn;
+#pragma unroll
+        for (int c = 0; c < 4 * NC; ++c) o[i][c] *= al;
+      }
+      cp_async_wait<1>();
+      __syncthreads();
+      // in a masked block a key adds only to the rows that see it: a weight
+      // of zero would not silence a NaN or an infinity
+      auto weigh = [&](auto keep) {
+#pragma unroll 2
+        for (int k = 0; k < kBlk; k += 4) {
+          float4 e[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) e[i] = *reinterpret_cast<const float4*>(sp + (ty * 4 + i) * C::kLdP + k);
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+              const float4 v = *reinterpret_cast<const float4*>(sv + (k + y) * C::kLd + c * 64 + tx * 4);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float ey = y == 0 ? e[i].x : y == 1 ? e[i].y : y == 2 ? e[i].z : e[i].w;
+                if (!keep(i, k + y)) continue;
+                o[i][4 * c] = fmaf(ey, v.x, o[i][4 * c]);
+                o[i][4 * c + 1] = fmaf(ey, v.y, o[i][4 * c + 1]);
+                o[i][4 * c + 2] = fmaf(ey, v.z, o[i][4 * c + 2]);
+                o[i][4 * c + 3] = fmaf(ey, v.w, o[i][4 * c + 3]);
+              }
+            }
+        }
+      };
+      if (masked)
+        weigh([&](int i, int k) { return blk * kBlk + k <= pos[i]; });
+      else
+        weigh([](int, int) { return true; });
+      __syncthreads();
+      copy(sv, a.vc, blk + 1);
+    }
+    cp_async_wait<0>();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = ty * 4 + i;
+      if (r >= rows) continue;
+      const bool whole = w.slot < 0;
+      const size_t orow = ((size_t)w.c0 + w.u * p.tpu + r / p.g) * a.Hq + w.h * p.g + r % p.g;
+      const size_t prow = (size_t)max(w.slot, 0) * p.slot_rows + r;
+      const float f = whole ? (l[i] == 0.f ? 0.f : 1.f / l[i]) : 1.f;
+      float* dst = whole ? static_cast<float*>(a.out) + orow * D : p.part_o + prow * D;
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+        *reinterpret_cast<float4*>(dst + c * 64 + tx * 4) =
+            make_float4(o[i][4 * c] * f, o[i][4 * c + 1] * f, o[i][4 * c + 2] * f, o[i][4 * c + 3] * f);
+      if (tx == 0) {
+        if (!whole)
+          p.part_ml[prow] = make_float2(m[i], l[i]);
+        else if (a.lse)
+          a.lse[orow] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
+      }
+    }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const size_t orow = (size_t)t * p.Hq + h;
-#pragma unroll
-  for (int e = 0; e < E; ++e) static_cast<float*>(p.out)[orow * D + lane + 32 * e] = o[e] * inv;
-  if (p.lse && lane == 0) p.lse[orow] = m + logf(l);
 }
 
 int attn_check(const AttnParams& p, int D, int page_size, size_t es) {
@@ -1388,36 +1520,63 @@ int attn_check(const AttnParams& p, int D, int page_size, size_t es) {
   return EAGLE_OK;
 }
 
+struct Ws {
+  PlanHeader* hdr;
+  Piece* pieces;
+  Cut* cuts;
+  float2* ml;
+  float* po;
+};
+Ws attn_ws(const Shape& sh, void* ws) {
+  char* w = reinterpret_cast<char*>(round_up(reinterpret_cast<size_t>(ws), 256));
+  return {reinterpret_cast<PlanHeader*>(w), reinterpret_cast<Piece*>(w + sh.off_pieces),
+          reinterpret_cast<Cut*>(w + sh.off_cuts), reinterpret_cast<float2*>(w + sh.off_ml),
+          reinterpret_cast<float*>(w + sh.off_o)};
+}
+void launch_plan(const AttnParams& a, const Shape& sh, const Ws& w, cudaStream_t s) {
+  const PlanParams pp = {a.cu, a.ctx, a.B, a.T, a.Hkv, a.max_pages, sh.tpu, sh.g, sh.ctas, sh.cap_pieces, sh.cap_slots,
+                         w.hdr, w.pieces, w.cuts, a.status};
+  launch(prompt_plan_kernel, 1, kPlanThreads, 0, s, pp);
+}
+template <int D, bool F32>
+int launch_merge(const AttnParams& a, const Shape& sh, const Ws& w, cudaStream_t s) {
+  const MergeParams gp = {w.hdr, w.cuts, w.ml, w.po, a.out, a.lse, a.v_scale, a.Hq, sh.g, sh.tpu, sh.rows};
+  launch(prompt_merge_kernel<D, F32>, 2 * sh.ctas, 256, 0, s, gp);
+  note_launch(3);
+  return last_launch_status();
+}
+template <typename K>
+bool allow_smem(K kern, int bytes) {
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess) return true;
+  cudaGetLastError();
+  return false;
+}
+
 template <int D, bool KV4>
 int attn_launch_tc(const AttnParams& a, void* ws, cudaStream_t s) {
   using C = Cfg<D, KV4>;
-  const Shape sh = attn_shape(a.B, a.T, a.Hq, a.Hkv, D);
-  char* w = reinterpret_cast<char*>(round_up(reinterpret_cast<size_t>(ws), 256));
-  PlanHeader* hdr = reinterpret_cast<PlanHeader*>(w);
-  Piece* pieces = reinterpret_cast<Piece*>(w + sh.off_pieces);
-  Cut* cuts = reinterpret_cast<Cut*>(w + sh.off_cuts);
-  float2* ml = reinterpret_cast<float2*>(w + sh.off_ml);
-  float* po = reinterpret_cast<float*>(w + sh.off_o);
-  auto kern = prompt_attn_tc_kernel<D, KV4>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem) != cudaSuccess) {
-    cudaGetLastError();
-    return EAGLE_ERR_CUDA;
-  }
+  const Shape sh = attn_shape(a.B, a.T, a.Hq, a.Hkv, D, 2 * kTileRows);
+  const Ws w = attn_ws(sh, ws);
   CUtensorMap map_q = {};
   if (!KV4 && !make_tmap_3d_bf16(&map_q, a.q, D, (uint64_t)a.Hq, (uint64_t)a.T, (uint64_t)D * 2, (uint64_t)a.q_stride * 2,
                                  64, (uint32_t)sh.g, (uint32_t)sh.tpt))
     return EAGLE_ERR_CUDA;
-  const PlanParams pp = {a.cu, a.ctx, a.B, a.T, a.Hkv, a.max_pages, sh.tpu, sh.g, sh.ctas, sh.cap_pieces, sh.cap_slots,
-                         hdr, pieces, cuts, a.status};
-  launch(prompt_plan_kernel, 1, kPlanThreads, 0, s, pp);
-  const MainParams mp = {a, a.scale * a.k_scale * 1.4426950408889634f, sh.g, sh.tpt, sh.tpu, sh.rows, hdr, &hdr->next,
-                         pieces, ml, po};
-  launch(kern, sh.ctas, kThreads, C::kSmem, s, map_q, mp);
-  const MergeParams gp = {hdr, cuts, ml, po, static_cast<__nv_bfloat16*>(a.out), a.lse, a.v_scale, a.Hq, sh.g, sh.tpu,
-                          sh.rows};
-  launch(prompt_merge_kernel<D>, 2 * sh.ctas, 256, 0, s, gp);
-  note_launch(3);
-  return last_launch_status();
+  if (!allow_smem(prompt_attn_tc_kernel<D, KV4>, (int)C::kSmem)) return EAGLE_ERR_CUDA;
+  launch_plan(a, sh, w, s);
+  const MainParams mp = {a, a.scale * a.k_scale * kLog2e, sh.g, sh.tpt, sh.tpu, sh.rows, w.hdr, &w.hdr->next, w.pieces,
+                         w.ml, w.po};
+  launch(prompt_attn_tc_kernel<D, KV4>, sh.ctas, kThreads, C::kSmem, s, map_q, mp);
+  return launch_merge<D, false>(a, sh, w, s);
+}
+template <int D>
+int attn_launch_f32(const AttnParams& a, void* ws, cudaStream_t s) {
+  const Shape sh = attn_shape(a.B, a.T, a.Hq, a.Hkv, D, kF32Rows);
+  const Ws w = attn_ws(sh, ws);
+  if (!allow_smem(prompt_attn_f32_kernel<D>, CfgF32<D>::kSmem)) return EAGLE_ERR_CUDA;
+  launch_plan(a, sh, w, s);
+  const F32Params fp = {a, a.scale * kLog2e, sh.g, sh.tpu, sh.rows, w.hdr, &w.hdr->next, w.pieces, w.ml, w.po};
+  launch(prompt_attn_f32_kernel<D>, sh.ctas, 256, CfgF32<D>::kSmem, s, fp);
+  return launch_merge<D, true>(a, sh, w, s);
 }
 
 int attn_ws_check(const AttnParams& a, int D, void* ws, size_t ws_bytes) {
@@ -1431,7 +1590,7 @@ using namespace eagle;
 
 extern "C" size_t eagle_prompt_attn_workspace_size(int B, int T, int Hq, int Hkv, int D) {
   if (B <= 0 || T < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || Hq / Hkv > 64 || (D != 64 && D != 128)) return 0;
-  return attn_shape(B, T, Hq, Hkv, D).total + 256;
+  return std::max(attn_shape(B, T, Hq, Hkv, D, 2 * kTileRows).total, attn_shape(B, T, Hq, Hkv, D, kF32Rows).total) + 256;
 }
 
 extern "C" int eagle_prompt_attn(const void* q, long long q_stride, const void* k_cache, const void* v_cache,
@@ -1449,13 +1608,7 @@ extern "C" int eagle_prompt_attn(const void* q, long long q_stride, const void* 
   if (wrc != EAGLE_OK) return wrc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dtype == EAGLE_BF16) return D == 128 ? attn_launch_tc<128, false>(p, ws, s) : attn_launch_tc<64, false>(p, ws, s);
-  const dim3 grid(T, (Hq + 3) / 4);
-  if (D == 128)
-    launch(prompt_attn_f32_kernel<128>, grid, 128, 0, s, p);
-  else
-    launch(prompt_attn_f32_kernel<64>, grid, 128, 0, s, p);
-  note_launch();
-  return last_launch_status();
+  return D == 128 ? attn_launch_f32<128>(p, ws, s) : attn_launch_f32<64>(p, ws, s);
 }
 
 extern "C" int eagle_prompt_attn_kv4(const void* q, long long q_stride, const uint8_t* k_codes,
