@@ -98,110 +98,131 @@ struct PlanParams {
   int32_t* status;
 };
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 512;
 
-// One CTA.  Warp w takes the requests 32 w .. 32 w + 31 (and so on by 1024);
-// its lanes share the units of those requests.  Sweeps over all units: the
-// total of key blocks, the cost of each candidate cut, the lengths' histogram,
-// and the list.
+// One CTA.  The requests are taken 512 at a time (up to that many are loaded
+// once): a block scan of their unit counts, then every thread finds the request
+// of its units by bisection.  Sweeps over all units: the total of key blocks,
+// the cost of each candidate cut, the lengths' histogram, and the list, which
+// whole warps write.
 __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanParams p) {
   __shared__ unsigned long long s_total;
-  __shared__ int s_longest, s_n[kCand], s_cut[kCand], s_units, s_hist[32], s_cursor[32], s_c, s_slots, s_cuts, s_class;
+  __shared__ int s_longest, s_C[kCand], s_n[kCand], s_cut[kCand], s_hist[32], s_cursor[32], s_c, s_slots, s_cuts;
+  __shared__ int s_c0[kPlanThreads], s_len[kPlanThreads], s_ctx[kPlanThreads], s_end[kPlanThreads], s_warp[kPlanThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid < 32) s_hist[tid] = 0;
+  if (tid < kCand) s_n[tid] = s_cut[tid] = 0;
+  if (tid == 0) {
+    s_total = 0;
+    s_longest = s_slots = s_cuts = 0;
+  }
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (threadIdx.x < 32) s_hist[threadIdx.x] = 0;
-  if (threadIdx.x < kCand) s_n[threadIdx.x] = s_cut[threadIdx.x] = 0;
-  if (threadIdx.x == 0) {
-    s_total = 0;
-    s_longest = s_units = s_slots = s_cuts = 0;
-  }
-  __syncthreads();
 
-  // f(b, c0, n, ctx, u, key blocks) for every unit; all lanes of a warp call together, `live` lanes have one
+  // requests base .. base + 511 into shared memory; s_end: inclusive prefix of their units
+  auto load = [&](int base, bool report) {
+    int c0 = 0, n = 0, ctx = 0;
+    const int b = base + tid;
+    if (b < p.B) {
+      c0 = p.cu[b];
+      const int c1 = p.cu[b + 1];
+      ctx = p.ctx[b];
+      n = c1 - c0;
+      if (c0 < 0 || c1 < c0 || c1 > p.T || ctx < 0) {
+        if (report) set_status(p.status, EAGLE_ERR_INVALID_ARG);
+        n = 0;
+      } else if ((long long)ctx + n > 16ll * p.max_pages) {
+        if (report) set_status(p.status, EAGLE_ERR_BAD_KV);
+        n = 0;
+      }
+    }
+    int end = (n + p.tpu - 1) / p.tpu;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, end, d);
+      if (lane >= d) end += x;
+    }
+    if (lane == 31) s_warp[warp] = end;
+    __syncthreads();
+    int before = lane < warp ? s_warp[lane] : 0;  // warps are fewer than lanes
+    before = (int)__reduce_add_sync(0xffffffffu, (unsigned)before);
+    s_c0[tid] = c0;
+    s_len[tid] = n;
+    s_ctx[tid] = ctx;
+    s_end[tid] = end + before;
+    __syncthreads();
+  };
+  const bool once = p.B <= kPlanThreads;
+  if (once) load(0, true);
+
+  // f(live, b, c0, n, ctx, u, key blocks): whole warps call it, `live` lanes have a unit
   auto sweep = [&](bool report, auto&& f) {
-    for (int base = warp * 32; base < p.B; base += kPlanThreads) {
-      const int b = base + lane;
-      int c0 = 0, n = 0, ctx = 0;
-      if (b < p.B) {
-        c0 = p.cu[b];
-        const int c1 = p.cu[b + 1];
-        ctx = p.ctx[b];
-        n = c1 - c0;
-        if (c0 < 0 || c1 < c0 || c1 > p.T || ctx < 0) {
-          if (report) set_status(p.status, EAGLE_ERR_INVALID_ARG);
-          n = 0;
-        } else if ((long long)ctx + n > 16ll * p.max_pages) {
-          if (report) set_status(p.status, EAGLE_ERR_BAD_KV);
-          n = 0;
-        }
+#pragma unroll 1
+    for (int base = 0; base < p.B; base += kPlanThreads) {
+      if (!once) {
+        __syncthreads();
+        load(base, report);
       }
-      const int nu = (n + p.tpu - 1) / p.tpu;
-      int end = nu;  // inclusive prefix over the lanes
+      const int total = s_end[kPlanThreads - 1];
+#pragma unroll 1
+      for (int i0 = warp * 32; i0 < total; i0 += kPlanThreads) {
+        const int i = min(i0 + lane, total - 1);
+        int o = 0;  // the first request with s_end > i
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, end, d);
-        if (lane >= d) end += x;
-      }
-      const int total = __shfl_sync(0xffffffffu, end, 31);
-      for (int i0 = 0; i0 < total; i0 += 32) {
-        const int i = i0 + lane;
-        int o = 0;  // the lane whose request holds unit i: the first with end > i
-#pragma unroll
-        for (int d = 16; d; d >>= 1)
-          if (__shfl_sync(0xffffffffu, end, o + d - 1) <= i) o += d;
-        o = min(o, 31);
-        const int oc0 = __shfl_sync(0xffffffffu, c0, o), on = __shfl_sync(0xffffffffu, n, o);
-        const int octx = __shfl_sync(0xffffffffu, ctx, o);
-        const int u = i - (__shfl_sync(0xffffffffu, end, o) - __shfl_sync(0xffffffffu, nu, o));
-        const int keys = octx + min(on, (u + 1) * p.tpu);
-        f(i < total, base + o, oc0, on, octx, u, (keys + kBlk - 1) / kBlk);
+        for (int d = kPlanThreads / 2; d; d >>= 1)
+          if (s_end[o + d - 1] <= i) o += d;
+        const int n = s_len[o], u = i - (s_end[o] - (n + p.tpu - 1) / p.tpu);
+        const int keys = s_ctx[o] + min(n, (u + 1) * p.tpu);
+        f(i0 + lane < total, base + o, s_c0[o], n, s_ctx[o], u, (keys + kBlk - 1) / kBlk);
       }
     }
   };
-  auto warp_sum = [&](int v) {
-#pragma unroll
-    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    return v;
-  };
 
   {
-    unsigned long long sum = 0;
-    int longest = 0, units = 0;
+    unsigned sum = 0;  // of this lane's units: below 2^32 key blocks
+    int longest = 0;
     sweep(true, [&](bool live, int, int, int, int, int, int L) {
       if (!live) return;
-      sum += L;
+      sum += (unsigned)L;
       longest = max(longest, L);
-      ++units;
     });
-    if (units) {
-      atomicAdd(&s_total, sum);
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    unsigned long long all = sum;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
+    if (lane == 0 && longest) {
+      atomicAdd(&s_total, all);
       atomicMax(&s_longest, longest);
-      atomicAdd(&s_units, units);
     }
   }
   __syncthreads();
   const long long all = (long long)s_total * p.Hkv;  // key blocks of all units
+  const int longest = s_longest;
   // candidate x cuts units longer than C_x = all / (share x ctas)
-  auto cand = [&](int x) -> int {
-    if (kShares[x] == 0) return 0x7fffffff;
-    const long long c = (all + (long long)kShares[x] * p.ctas - 1) / ((long long)kShares[x] * p.ctas);
-    return (int)max(2ll, c);
-  };
+  if (tid < kCand) {
+    const long long f = (long long)kShares[tid] * p.ctas;
+    s_C[tid] = f ? (int)max(2ll, (all + f - 1) / f) : 0x7fffffff;
+  }
+  __syncthreads();
   {
-    int n[kCand] = {}, cut[kCand] = {};
+    int C[kCand], n[kCand], cut[kCand];
+#pragma unroll
+    for (int x = 0; x < kCand; ++x) {
+      C[x] = s_C[x];
+      n[x] = cut[x] = 0;
+    }
     sweep(false, [&](bool live, int, int, int, int, int, int L) {
       if (!live) return;
 #pragma unroll
       for (int x = 0; x < kCand; ++x) {
-        const int C = cand(x), k = L > C ? (L + C - 1) / C : 1;
+        const int k = L > C[x] ? (L + C[x] - 1) / C[x] : 1;
         n[x] += k;
         cut[x] += k > 1 ? k : 0;
       }
     });
 #pragma unroll
     for (int x = 0; x < kCand; ++x) {
-      const int a = warp_sum(n[x]), b = warp_sum(cut[x]);
+      const int a = __reduce_add_sync(0xffffffffu, n[x]), b = __reduce_add_sync(0xffffffffu, cut[x]);
       if (lane == 0 && a) {
         atomicAdd(&s_n[x], a);
         atomicAdd(&s_cut[x], b);
@@ -209,73 +230,82 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanPar
     }
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
+  if (warp == 0) {
     // estimated time in blocks per CTA: whole waves of pieces of the mean
     // length (at least the longest piece), and for each cut piece its
     // partial result (a block's worth of traffic per 64 rows, written and
-    // read) and a block for its start
-    float best = 3e38f;
-    int C = 0x7fffffff;
+    // read) and a block for its start; a lane per candidate, the least wins
+    // (the lower candidate of equals)
+    const int x = min(lane, kCand - 1), C = s_C[x];
     const float per_cut = 1.f + (float)min(p.tpu, p.T) * (float)p.g / 64.f;
-    for (int x = 0; x < kCand; ++x) {
-      const float N = (float)s_n[x] * p.Hkv;
-      if (N < 1.f || (long long)s_cut[x] * p.Hkv > p.cap_slots) continue;
-      float t = ceilf(N / p.ctas) * ((float)all / N);
-      t = fmaxf(t, (float)min(s_longest, cand(x))) + (float)s_cut[x] * p.Hkv * per_cut / p.ctas;
-      if (t < best) {
-        best = t;
-        C = cand(x);
-      }
-    }
-    s_c = C;
-    s_class = max(1, min(s_longest, C));
+    const float N = (float)s_n[x] * p.Hkv;
+    float t = 3e38f;
+    if (lane < kCand && N >= 1.f && (long long)s_cut[x] * p.Hkv <= p.cap_slots)
+      t = fmaxf(ceilf(N / p.ctas) * ((float)all / N), (float)min(longest, C)) + (float)s_cut[x] * p.Hkv * per_cut / p.ctas;
+    const unsigned best = __reduce_min_sync(0xffffffffu, __float_as_uint(t));  // non-negative: ordered as integers
+    const int who = __ffs(__ballot_sync(0xffffffffu, __float_as_uint(t) == best)) - 1;
+    if (lane == who) s_c = C;
   }
   __syncthreads();
-  const int C = s_c, top = s_class;
-  auto klass = [&](int len) { return 31 - min(31, (int)((long long)(len - 1) * 32 / top)); };  // 0: the longest
+  const int C = s_c, top = max(1, min(longest, C));
+  const float per_class = 32.f / (float)top;
+  auto klass = [&](int len) { return 31 - min(31, (int)((float)(len - 1) * per_class)); };  // 0: the longest
   sweep(false, [&](bool live, int, int, int, int, int, int L) {
     if (!live) return;
     const int k = L > C ? (L + C - 1) / C : 1;
     atomicAdd(&s_hist[klass((L + k - 1) / k)], k * p.Hkv);
   });
   __syncthreads();
-  if (threadIdx.x < 32) {
-    const int v = s_hist[threadIdx.x];
+  if (warp == 0) {
+    const int v = s_hist[lane];
     int end = v;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, end, d);
       if (lane >= d) end += x;
     }
-    s_cursor[threadIdx.x] = end - v;
-    if (threadIdx.x == 31) {
+    s_cursor[lane] = end - v;
+    if (lane == 31) {
       // a malformed cu_seqlens can list rows twice: what does not fit is left out
       p.hdr->pieces = min(end, p.cap_pieces);
-      p.hdr->next = 0;
+      p.hdr->next = p.ctas;  // the first piece of each CTA is its own index
       if (end > p.cap_pieces) set_status(p.status, EAGLE_ERR_INVALID_ARG);
     }
   }
   __syncthreads();
   sweep(false, [&](bool live, int b, int c0, int n, int ctx, int u, int L) {
-    if (!live) return;
-    const int k = L > C ? (L + C - 1) / C : 1;
-    int at = atomicAdd(&s_cursor[klass((L + k - 1) / k)], k * p.Hkv);
-    int slot = -1, cut = 0;
-    if (k > 1) {
-      slot = atomicAdd(&s_slots, k * p.Hkv);
-      cut = atomicAdd(&s_cuts, p.Hkv);
+    int k = 1, at = 0, slot = -1, cut = 0, len = L, extra = 0;  // the first `extra` pieces have len + 1 blocks
+    if (live) {
+      if (L > C) {
+        k = (L + C - 1) / C;
+        len = L / k;
+        extra = L - len * k;
+      }
+      at = atomicAdd(&s_cursor[klass((L + k - 1) / k)], k * p.Hkv);
+      if (k > 1) {
+        slot = atomicAdd(&s_slots, k * p.Hkv);
+        cut = atomicAdd(&s_cuts, p.Hkv);
+      }
     }
-    for (int h = 0; h < p.Hkv; ++h) {
-      if (k > 1 && slot + k <= p.cap_slots) p.cuts[cut + h] = Cut{h, u, slot, k, c0, n, 0, 0};
-      for (int x = 0; x < k; ++x, ++at)
-        if (at < p.cap_pieces)
-          p.pieces[at] = Piece{b, h, u, (int)((long long)L * x / k), (int)((long long)L * (x + 1) / k),
-                               k > 1 ? slot + x : -1, c0, n, ctx, 0, 0, 0};
-      if (k > 1) slot += k;
+    // the warp writes the pieces of its lanes' units one unit after another
+    const unsigned units = __ballot_sync(0xffffffffu, live);
+#pragma unroll 1
+    for (unsigned left = units; left; left &= left - 1) {
+      const int o = __ffs(left) - 1;
+      auto of = [&](int v) { return __shfl_sync(0xffffffffu, v, o); };
+      const int kk = of(k), oat = of(at), oslot = of(slot), ocut = of(cut), ob = of(b), oc0 = of(c0), on = of(n);
+      const int octx = of(ctx), ou = of(u), olen = of(len), oextra = of(extra);
+      for (int j = lane; j < kk * p.Hkv; j += 32) {
+        const int h = kk > 1 ? j / kk : j, x = j - h * kk, k0 = x * olen + min(x, oextra);
+        if (oat + j < p.cap_pieces)
+          p.pieces[oat + j] = Piece{ob, h, ou, k0, k0 + olen + (x < oextra ? 1 : 0), kk > 1 ? oslot + j : -1, oc0, on, octx,
+                                    0, 0, 0};
+        if (kk > 1 && x == 0) p.cuts[ocut + h] = Cut{h, ou, oslot + j, kk, oc0, on, 0, 0};
+      }
     }
   });
   __syncthreads();
-  if (threadIdx.x == 0) p.hdr->cuts = min(s_cuts, p.cap_slots);
+  if (tid == 0) p.hdr->cuts = s_cuts;
 }
 
 // ------------------------------------------------------------------- main
@@ -942,7 +972,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int ps = 0;; ++ps) {
         const int slot = ps % kSlots;
         if (!mbar_wait_short(smem_u32(&sb.slot_empty[slot]), ((uint32_t)(ps / kSlots) & 1u) ^ 1u, abort_flag)) break;
-        const int i = atomicAdd(p.next, 1);
+        const int i = ps == 0 ? (int)blockIdx.x : atomicAdd(p.next, 1);
         if (i < total)
           sb.piece[slot] = p.pieces[i];
         else
@@ -1353,9 +1383,9 @@ __global__ void __launch_bounds__(256, 1) prompt_attn_f32_kernel(const F32Params
   pdl_trigger();
   const AttnParams& a = p.a;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  for (;;) {
+  for (bool first = true;; first = false) {
     __syncthreads();
-    if (tid == 0) s_piece = atomicAdd(p.next, 1);
+    if (tid == 0) s_piece = first ? (int)blockIdx.x : atomicAdd(p.next, 1);
     __syncthreads();
     if (s_piece >= p.hdr->pieces) break;
     const Piece w = p.pieces[s_piece];
