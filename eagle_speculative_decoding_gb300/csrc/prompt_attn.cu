@@ -67,15 +67,15 @@ struct Shape {
   int ctas, cap_units, cap_pieces, cap_slots;
   size_t off_pieces, off_cuts, off_ml, off_o, total;
 };
-// unit_rows: 256 (two tensor-core tiles) or 64 (fp32)
-Shape attn_shape(int B, int T, int Hq, int Hkv, int D, int unit_rows) {
+enum Path { kTensor, kFew, kFp32 };
+Shape attn_shape(int B, int T, int Hq, int Hkv, int D, Path path) {
   Shape s;
   s.g = Hq / Hkv;
-  s.tpt = (unit_rows == kF32Rows ? kF32Rows : kTileRows) / s.g;
-  s.tpu = unit_rows == kF32Rows ? s.tpt : 2 * s.tpt;
+  s.tpt = path == kTensor ? kTileRows / s.g : path == kFew ? 1 : kF32Rows / s.g;
+  s.tpu = path == kTensor ? 2 * s.tpt : s.tpt;
   s.rows = std::min(s.tpu, T) * s.g;
   const int sms = sm_count();
-  s.ctas = sms > 0 ? sms : 152;
+  s.ctas = (sms > 0 ? sms : 152) * (path == kFew ? 2 : 1);
   s.cap_units = T / s.tpu + std::min(B, T);
   // a unit of L > C blocks makes ceil(L / C) < 2 L / C pieces and the finest C
   // is total / (kMaxShare * ctas)
@@ -88,10 +88,14 @@ Shape attn_shape(int B, int T, int Hq, int Hkv, int D, int unit_rows) {
   s.total = s.off_o + sizeof(float) * (size_t)s.cap_slots * s.rows * D + 256;
   return s;
 }
+// Single tokens (at most one new row per request on average) with at most 16
+// query heads per kv head take the few-rows kernel, everything else the
+// two-tile kernel.
+bool few_rows(int B, int T, int Hq, int Hkv) { return T <= B && Hq / Hkv <= 16; }
 
 struct PlanParams {
   const int32_t *cu, *ctx;
-  int B, T, Hkv, max_pages, tpu, g, ctas, cap_pieces, cap_slots;
+  int B, T, Hkv, max_pages, tpu, g, ctas, cap_pieces, cap_slots, min_cut;
   PlanHeader* hdr;
   Piece* pieces;
   Cut* cuts;
@@ -201,7 +205,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanPar
   // candidate x cuts units longer than C_x = all / (share x ctas)
   if (tid < kCand) {
     const long long f = (long long)kShares[tid] * p.ctas;
-    s_C[tid] = f ? (int)max(2ll, (all + f - 1) / f) : 0x7fffffff;
+    s_C[tid] = f ? (int)max((long long)p.min_cut, (all + f - 1) / f) : 0x7fffffff;
   }
   __syncthreads();
   {
@@ -287,21 +291,27 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanPar
         cut = atomicAdd(&s_cuts, p.Hkv);
       }
     }
-    // the warp writes the pieces of its lanes' units one unit after another
-    const unsigned units = __ballot_sync(0xffffffffu, live);
+    auto put = [&](int j, int kk, int oat, int oslot, int ocut, int ob, int oc0, int on, int octx, int ou, int olen,
+                   int oextra) {
+      const int h = kk > 1 ? j / kk : j, x = j - h * kk, k0 = x * olen + min(x, oextra);
+      if (oat + j < p.cap_pieces)
+        p.pieces[oat + j] = Piece{ob, h, ou, k0, k0 + olen + (x < oextra ? 1 : 0), kk > 1 ? oslot + j : -1, oc0, on, octx,
+                                  0, 0, 0};
+      if (kk > 1 && x == 0) p.cuts[ocut + h] = Cut{h, ou, oslot + j, kk, oc0, on, 0, 0};
+    };
+    const int mine = live ? k * p.Hkv : 0;
+    if (__reduce_max_sync(0xffffffffu, (unsigned)mine) <= 16) {
+      for (int j = 0; j < mine; ++j) put(j, k, at, slot, cut, b, c0, n, ctx, u, len, extra);
+      return;
+    }
+    // many pieces each: the warp writes its lanes' units one after another
 #pragma unroll 1
-    for (unsigned left = units; left; left &= left - 1) {
+    for (unsigned left = __ballot_sync(0xffffffffu, live); left; left &= left - 1) {
       const int o = __ffs(left) - 1;
       auto of = [&](int v) { return __shfl_sync(0xffffffffu, v, o); };
       const int kk = of(k), oat = of(at), oslot = of(slot), ocut = of(cut), ob = of(b), oc0 = of(c0), on = of(n);
       const int octx = of(ctx), ou = of(u), olen = of(len), oextra = of(extra);
-      for (int j = lane; j < kk * p.Hkv; j += 32) {
-        const int h = kk > 1 ? j / kk : j, x = j - h * kk, k0 = x * olen + min(x, oextra);
-        if (oat + j < p.cap_pieces)
-          p.pieces[oat + j] = Piece{ob, h, ou, k0, k0 + olen + (x < oextra ? 1 : 0), kk > 1 ? oslot + j : -1, oc0, on, octx,
-                                    0, 0, 0};
-        if (kk > 1 && x == 0) p.cuts[ocut + h] = Cut{h, ou, oslot + j, kk, oc0, on, 0, 0};
-      }
+      for (int j = lane; j < kk * p.Hkv; j += 32) put(j, kk, oat, oslot, ocut, ob, oc0, on, octx, ou, olen, oextra);
     }
   });
   __syncthreads();
@@ -1350,6 +1360,396 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const MergeParams p) 
   }
 }
 
+// --------------------------------------------------------------- few rows
+// Single tokens: one unit per (token, kv head), its at most 16 rows the
+// query heads of the group, every key up to the token's own visible to all of
+// them.  The call is bound by the cache's bytes, and the path through shared
+// memory above costs more than they do (4-bit pages: staging and converting a
+// 128-key tile takes four warps 1,700 cycles, its bytes arrive in 400), so here
+// a warp takes a page at a time from global memory to the fragments of
+// mma.sync in registers: no stage, no barrier, 16 x 8 x 16 MMAs whose idle
+// rows cost nothing that is short.  128 threads, two CTAs per SM; warp w takes
+// pages w and w + 4 of each 128-key block, with its own m, l and O; the warps
+// are joined in shared memory at the end of a piece.
+//
+// The channels of a fragment may stand in any order, as long as Q's and K's
+// agree and O is stored by V's: a lane's registers are then consecutive
+// channels in memory.  With t = lane % 4, j = lane / 4:
+//   K (B operand of S = Q K^T): keys j and j + 8; 16-bit: 16-byte loads
+//     i = 0 .. D/32 - 1 at channel 32 i + 8 t; 4-bit: D/4 channels at t D/4
+//   V (B operand of O = P V): keys 2t, 2t + 1, 2t + 8, 2t + 9; 16-bit: loads
+//     i = 0 .. D/64 - 1 at channel 64 i + 8 j; 4-bit: D/8 channels at j D/8
+constexpr int kFewThreads = 128;
+constexpr int kFewRows = 16;
+
+struct FewParams {
+  AttnParams a;
+  float scale_log2;
+  int g, slot_rows;
+  const PlanHeader* hdr;
+  int* next;
+  const Piece* pieces;
+  float2* part_ml;
+  float* part_o;
+};
+
+template <bool F16>
+__device__ __forceinline__ void mma_16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  if (F16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Eight 4-bit codes as four fp16 pairs times the pair `s`.
+__device__ __forceinline__ void kv4_expand(uint32_t w, uint32_t s, uint32_t* v) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+      : "r"(w));
+#pragma unroll
+  for (int y = 0; y < 4; ++y)  // exact: at most six significant bits, all multiples of 2^-10
+    asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(v[y]) : "r"(s));
+}
+__device__ __forceinline__ uint32_t e4m3_pair_as_f16(uint32_t two) {
+  uint32_t s2;
+  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(s2) : "r"(two));
+  return s2;
+}
+
+template <int D, bool KV4>
+__global__ void __launch_bounds__(kFewThreads, 2) prompt_attn_few_kernel(const FewParams p) {
+  constexpr int KS = D / 16, NT = D / 8;  // k steps of S, 8-column tiles of O
+  constexpr int KW = KV4 ? D / 32 : D / 8;   // 32-bit words of K per key and lane
+  constexpr int VW = KV4 ? D / 64 : D / 16;  // of V
+  constexpr int kAhead = KV4 ? 3 : 1;        // pages in flight per warp
+  extern __shared__ __align__(16) float fm[];  // [4 warps][16 rows][D], then [4][16] (m, l)
+  float2* s_ml = reinterpret_cast<float2*>(fm + 4 * kFewRows * D);
+  __shared__ int s_piece;
+  pdl_wait();
+  pdl_trigger();
+  const AttnParams& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, t = lane & 3, j = lane >> 2;
+  for (bool first = true;; first = false) {
+    __syncthreads();
+    if (tid == 0) s_piece = first ? (int)blockIdx.x : atomicAdd(p.next, 1);
+    __syncthreads();
+    if (s_piece >= p.hdr->pieces) break;
+    const Piece w = p.pieces[s_piece];
+    const int tok = w.c0 + w.u, pos = w.ctx + w.u, n_keys = pos + 1;
+    const int page_end = min(w.k1 * 8, (n_keys + 15) / 16);
+    const int32_t* tab = a.table + (size_t)w.b * a.max_pages;
+    // Q as the A operand of each k step, the lane's two rows j and j + 8
+    uint32_t q[KS][4];
+    float fac[2] = {p.scale_log2, p.scale_log2};
+    {
+      uint32_t raw[2][D / 8];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = j + 8 * r;
+        const __nv_bfloat16* src =
+            static_cast<const __nv_bfloat16*>(a.q) + (size_t)tok * a.q_stride + (size_t)(w.h * p.g + row) * D;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          // 16-bit: channels 32 i + 8 t ..; 4-bit: t D/4 + 8 i ..
+          const uint4 v = row < p.g ? *reinterpret_cast<const uint4*>(src + (KV4 ? t * (D / 4) + 8 * i : 32 * i + 8 * t))
+                                    : make_uint4(0u, 0u, 0u, 0u);
+          raw[r][4 * i] = v.x, raw[r][4 * i + 1] = v.y, raw[r][4 * i + 2] = v.z, raw[r][4 * i + 3] = v.w;
+        }
+        if constexpr (KV4) {
+          // fp16, scaled by a power of two to [1, 2) at the row's largest
+          uint32_t mx = 0;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) mx = max(mx, max(raw[r][i] & 0x7fffu, (raw[r][i] >> 16) & 0x7fffu));
+          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const int k2 = min(126, max(-126, (int)(mx >> 7) - 127));
+          const float down = __uint_as_float((uint32_t)(127 - k2) << 23);
+          fac[r] *= __uint_as_float((uint32_t)(127 + k2) << 23);
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i)
+            raw[r][i] = pack16<true>(__uint_as_float(raw[r][i] << 16) * down, __uint_as_float(raw[r][i] & 0xffff0000u) * down);
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        q[s][0] = raw[0][2 * s];
+        q[s][1] = raw[1][2 * s];
+        q[s][2] = raw[0][2 * s + 1];
+        q[s][3] = raw[1][2 * s + 1];
+      }
+    }
+    float o[NT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+
+    struct Page {
+      uint32_t k[2][KW], v[4][VW], ks[2], vs[4];
+    };
+    // page ids of this warp, 32 at a time: lane x holds page k0 * 8 + warp + 4 (32 G + x)
+    int ids = 0, group = -1;
+    const int page0 = w.k0 * 8 + warp;
+    auto page_id = [&](int i) -> int {  // the i-th page of this warp (in order)
+      if ((i >> 5) != group) {
+        group = i >> 5;
+        const int pi = page0 + 4 * (group * 32 + lane);
+        ids = pi < page_end ? tab[pi] : -1;
+      }
+      int id = __shfl_sync(0xffffffffu, ids, i & 31);
+      if (id < 0 || id >= a.num_pages) {
+        if (page0 + 4 * i < page_end) set_status(a.status, EAGLE_ERR_BAD_KV);
+        id = -1;
+      }
+      return id;
+    };
+    auto load = [&](Page& g, int i) {
+      const int id = page_id(i), key0 = (page0 + 4 * i) * 16;
+      if constexpr (KV4) {
+        const size_t row0 = ((size_t)max(id, 0) * a.Hkv + w.h) * 16;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int r = j + 8 * x;
+          const bool live = id >= 0 && key0 + r < n_keys;
+          const uint8_t* c = static_cast<const uint8_t*>(a.kc) + (row0 + r) * (D / 2) + t * (D / 8);
+          g.ks[x] = 0;
+          if constexpr (D == 128) {
+            const uint4 v = live ? __ldg(reinterpret_cast<const uint4*>(c)) : make_uint4(0u, 0u, 0u, 0u);
+            g.k[x][0] = v.x, g.k[x][1] = v.y, g.k[x][2] = v.z, g.k[x][3] = v.w;
+            if (live) g.ks[x] = __ldg(reinterpret_cast<const uint16_t*>(a.ks + (row0 + r) * 8 + 2 * t));
+          } else {
+            const uint2 v = live ? __ldg(reinterpret_cast<const uint2*>(c)) : make_uint2(0u, 0u);
+            g.k[x][0] = v.x, g.k[x][1] = v.y;
+            if (live) g.ks[x] = __ldg(a.ks + (row0 + r) * 4 + t);
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int r = 2 * t + (x & 1) + 8 * (x >> 1);
+          const bool live = id >= 0 && key0 + r < n_keys;
+          const uint8_t* c = static_cast<const uint8_t*>(a.vc) + (row0 + r) * (D / 2) + j * (D / 16);
+          g.vs[x] = 0;
+          if constexpr (D == 128) {
+            const uint2 v = live ? __ldg(reinterpret_cast<const uint2*>(c)) : make_uint2(0u, 0u);
+            g.v[x][0] = v.x, g.v[x][1] = v.y;
+            if (live) g.vs[x] = __ldg(a.vs + (row0 + r) * 8 + j);
+          } else {
+            g.v[x][0] = live ? __ldg(reinterpret_cast<const uint32_t*>(c)) : 0u;
+            if (live) g.vs[x] = __ldg(a.vs + (row0 + r) * 4 + (j >> 1));
+          }
+        }
+      } else {
+        const size_t tok_ch = (size_t)a.Hkv * D, at0 = (size_t)max(id, 0) * 16 * tok_ch + (size_t)w.h * D;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int r = j + 8 * x;
+          const bool live = id >= 0 && key0 + r < n_keys;
+          const __nv_bfloat16* c = static_cast<const __nv_bfloat16*>(a.kc) + at0 + r * tok_ch + 8 * t;
+#pragma unroll
+          for (int y = 0; y < D / 32; ++y) {
+            const uint4 v = live ? __ldg(reinterpret_cast<const uint4*>(c + 32 * y)) : make_uint4(0u, 0u, 0u, 0u);
+            g.k[x][4 * y] = v.x, g.k[x][4 * y + 1] = v.y, g.k[x][4 * y + 2] = v.z, g.k[x][4 * y + 3] = v.w;
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int r = 2 * t + (x & 1) + 8 * (x >> 1);
+          const bool live = id >= 0 && key0 + r < n_keys;
+          const __nv_bfloat16* c = static_cast<const __nv_bfloat16*>(a.vc) + at0 + r * tok_ch + 8 * j;
+#pragma unroll
+          for (int y = 0; y < D / 64; ++y) {
+            const uint4 v = live ? __ldg(reinterpret_cast<const uint4*>(c + 64 * y)) : make_uint4(0u, 0u, 0u, 0u);
+            g.v[x][4 * y] = v.x, g.v[x][4 * y + 1] = v.y, g.v[x][4 * y + 2] = v.z, g.v[x][4 * y + 3] = v.w;
+          }
+        }
+      }
+    };
+    auto use = [&](const Page& g, int i) {
+      float s[2][4];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
+        if constexpr (KV4) {
+          const uint32_t s2 = e4m3_pair_as_f16(D == 128 ? g.ks[x] : g.ks[x] * 0x101u);
+          const uint32_t sl = __byte_perm(s2, s2, 0x1010), sh = __byte_perm(s2, s2, 0x3232);
+#pragma unroll
+          for (int y = 0; y < KW; ++y) {
+            uint32_t e[4];
+            kv4_expand(g.k[x][y], y < KW / 2 ? sl : sh, e);
+            mma_16816<true>(s[x], q[2 * y], e[0], e[1]);
+            mma_16816<true>(s[x], q[2 * y + 1], e[2], e[3]);
+          }
+        } else {
+#pragma unroll
+          for (int y = 0; y < KS; ++y) mma_16816<false>(s[x], q[y], g.k[x][2 * y], g.k[x][2 * y + 1]);
+        }
+      }
+      // s[x][2 r + e]: row j + 8 r, key 8 x + 2 t + e
+      const int key0 = (page0 + 4 * i) * 16;
+      if (key0 + 16 > n_keys) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (key0 + 8 * x + 2 * t + (e & 1) >= n_keys) s[x][e] = -INFINITY;
+      }
+      // the reference of a row is the maximum of the first page; it is renewed
+      // when a weight passes kSumLimit (or is NaN), see the kernel above
+      float w_[2][4];
+      bool renew = i == 0, mine[2] = {true, true};  // by row, the same in its four lanes
+#pragma unroll 1
+      for (int pass = 0;; ++pass) {
+        if (renew) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            float bm = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+            bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 1));
+            bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 2)) * fac[r];
+            if (mine[r] && bm > m[r]) {
+              const float alpha = m[r] == -INFINITY ? 0.f : ex2_approx(m[r] - bm);
+              l[r] *= alpha;
+              if (m[r] != -INFINITY) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                  o[n][2 * r] *= alpha;
+                  o[n][2 * r + 1] *= alpha;
+                }
+              }
+              m[r] = bm;
+            }
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float ref = m[r] == -INFINITY ? 0.f : -m[r];
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) w_[x][2 * r + e] = ex2_approx(fmaf(s[x][2 * r + e], fac[r], ref));
+        }
+        float sum[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) sum[r] = (w_[0][2 * r] + w_[0][2 * r + 1]) + (w_[1][2 * r] + w_[1][2 * r + 1]);
+        const bool over0 = !(sum[0] <= kSumLimit), over1 = !(sum[1] <= kSumLimit);
+        if (pass || !__any_sync(0xffffffffu, over0 || over1)) {
+          l[0] += sum[0];
+          l[1] += sum[1];
+          break;
+        }
+        renew = true;
+        mine[0] = (__ballot_sync(0xffffffffu, over0) >> (lane & 28) & 15u) != 0;
+        mine[1] = (__ballot_sync(0xffffffffu, over1) >> (lane & 28) & 15u) != 0;
+      }
+      const uint32_t pa[4] = {pack16<KV4>(w_[0][0], w_[0][1]), pack16<KV4>(w_[0][2], w_[0][3]),
+                              pack16<KV4>(w_[1][0], w_[1][1]), pack16<KV4>(w_[1][2], w_[1][3])};
+      // V: pairs of keys (2t, 2t + 1) and (2t + 8, 2t + 9) of each channel
+      if constexpr (KV4) {
+        uint32_t sc[4];
+        {
+          const uint32_t s01 = e4m3_pair_as_f16(g.vs[0] | g.vs[1] << 8), s23 = e4m3_pair_as_f16(g.vs[2] | g.vs[3] << 8);
+          sc[0] = __byte_perm(s01, s01, 0x1010), sc[1] = __byte_perm(s01, s01, 0x3232);
+          sc[2] = __byte_perm(s23, s23, 0x1010), sc[3] = __byte_perm(s23, s23, 0x3232);
+        }
+#pragma unroll
+        for (int y = 0; y < VW; ++y) {
+          uint32_t e[4][4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) kv4_expand(g.v[x][y], sc[x], e[x]);
+#pragma unroll
+          for (int z = 0; z < 4; ++z)
+#pragma unroll
+            for (int hl = 0; hl < 2; ++hl) {
+              const uint32_t sel = hl ? 0x7632u : 0x5410u;
+              mma_16816<true>(o[8 * y + 2 * z + hl], pa, __byte_perm(e[0][z], e[1][z], sel),
+                              __byte_perm(e[2][z], e[3][z], sel));
+            }
+        }
+      } else {
+#pragma unroll
+        for (int y = 0; y < VW; ++y)
+#pragma unroll
+          for (int hl = 0; hl < 2; ++hl) {
+            const uint32_t sel = hl ? 0x7632u : 0x5410u;
+            mma_16816<false>(o[2 * y + hl], pa, __byte_perm(g.v[0][y], g.v[1][y], sel),
+                             __byte_perm(g.v[2][y], g.v[3][y], sel));
+          }
+      }
+    };
+    const int n_pages = page0 < page_end ? (page_end - page0 + 3) / 4 : 0;
+    Page ring[kAhead];
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x)
+      if (x < n_pages) load(ring[x], x);
+#pragma unroll 1
+    for (int i = 0; i < n_pages; i += kAhead) {
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) {
+        if (i + x >= n_pages) break;
+        if constexpr (kAhead == 1) {
+          // 16-bit pages: 64 registers of loads; the next page's are issued
+          // as soon as this one's have been taken
+          const Page cur = ring[0];
+          if (i + 1 < n_pages) load(ring[0], i + 1);
+          use(cur, i);
+        } else {
+          use(ring[x], i + x);
+          if (i + x + kAhead < n_pages) load(ring[x], i + x + kAhead);
+        }
+      }
+    }
+    // join the warps: rows < g of (m, l) and O
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      const int row = j + 8 * r;
+      if (t == 0) s_ml[warp * kFewRows + row] = make_float2(m[r], l[r]);
+      if (row < p.g) {
+        float* dst = fm + (warp * kFewRows + row) * D;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            // column 2 t + e of tile n: lane index j' = 2 t + e of V's order
+            const int jj = 2 * t + e;
+            dst[KV4 ? jj * (D / 8) + n : 64 * (n / 8) + 8 * jj + (n & 7)] = o[n][2 * r + e];
+          }
+      }
+    }
+    __syncthreads();
+    const bool whole = w.slot < 0;
+    for (int i = tid; i < p.g * (D / 4); i += kFewThreads) {
+      const int row = i / (D / 4), c = (i % (D / 4)) * 4;
+      float mm = -INFINITY;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) mm = fmaxf(mm, s_ml[x * kFewRows + row].x);
+      float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+      float ll = 0.f;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float2 ml = s_ml[x * kFewRows + row];
+        const float wt = mm == -INFINITY ? 1.f : ex2_approx(ml.x - mm);
+        const float4 v = *reinterpret_cast<const float4*>(fm + (x * kFewRows + row) * D + c);
+        ll = fmaf(wt, ml.y, ll);
+        f = make_float4(fmaf(wt, v.x, f.x), fmaf(wt, v.y, f.y), fmaf(wt, v.z, f.z), fmaf(wt, v.w, f.w));
+      }
+      const size_t orow = (size_t)tok * a.Hq + w.h * p.g + row, prow = (size_t)max(w.slot, 0) * p.slot_rows + row;
+      if (whole) {
+        const float inv = ll == 0.f ? 0.f : a.v_scale / ll;
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + c) =
+            make_uint2(pack16<false>(f.x * inv, f.y * inv), pack16<false>(f.z * inv, f.w * inv));
+        if (c == 0 && a.lse) a.lse[orow] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+      } else {
+        *reinterpret_cast<float4*>(p.part_o + prow * D + c) = f;
+        if (c == 0) p.part_ml[prow] = make_float2(mm, ll);
+      }
+    }
+  }
+}
+
 // ------------------------------------------------------------------- fp32
 // Units of 64 rows against 128-key blocks on the CUDA cores, from the same
 // list of pieces.  256 threads: thread (ty, tx) holds scores of rows 4 ty ..
@@ -1563,8 +1963,8 @@ Ws attn_ws(const Shape& sh, void* ws) {
           reinterpret_cast<Cut*>(w + sh.off_cuts), reinterpret_cast<float2*>(w + sh.off_ml),
           reinterpret_cast<float*>(w + sh.off_o)};
 }
-void launch_plan(const AttnParams& a, const Shape& sh, const Ws& w, cudaStream_t s) {
-  const PlanParams pp = {a.cu, a.ctx, a.B, a.T, a.Hkv, a.max_pages, sh.tpu, sh.g, sh.ctas, sh.cap_pieces, sh.cap_slots,
+void launch_plan(const AttnParams& a, const Shape& sh, const Ws& w, int min_cut, cudaStream_t s) {
+  const PlanParams pp = {a.cu, a.ctx, a.B, a.T, a.Hkv, a.max_pages, sh.tpu, sh.g, sh.ctas, sh.cap_pieces, sh.cap_slots, min_cut,
                          w.hdr, w.pieces, w.cuts, a.status};
   launch(prompt_plan_kernel, 1, kPlanThreads, 0, s, pp);
 }
@@ -1585,14 +1985,23 @@ bool allow_smem(K kern, int bytes) {
 template <int D, bool KV4>
 int attn_launch_tc(const AttnParams& a, void* ws, cudaStream_t s) {
   using C = Cfg<D, KV4>;
-  const Shape sh = attn_shape(a.B, a.T, a.Hq, a.Hkv, D, 2 * kTileRows);
+  if (few_rows(a.B, a.T, a.Hq, a.Hkv)) {
+    const Shape sh = attn_shape(a.B, a.T, a.Hq, a.Hkv, D, kFew);
+    const Ws w = attn_ws(sh, ws);
+    constexpr int kSmem = 4 * kFewRows * (D * 4 + 8);
+    launch_plan(a, sh, w, 2, s);
+    const FewParams fp = {a, a.scale * a.k_scale * kLog2e, sh.g, sh.rows, w.hdr, &w.hdr->next, w.pieces, w.ml, w.po};
+    launch(prompt_attn_few_kernel<D, KV4>, sh.ctas, kFewThreads, kSmem, s, fp);
+    return launch_merge<D, false>(a, sh, w, s);
+  }
+  const Shape sh = attn_shape(a.B, a.T, a.Hq, a.Hkv, D, kTensor);
   const Ws w = attn_ws(sh, ws);
   CUtensorMap map_q = {};
   if (!KV4 && !make_tmap_3d_bf16(&map_q, a.q, D, (uint64_t)a.Hq, (uint64_t)a.T, (uint64_t)D * 2, (uint64_t)a.q_stride * 2,
                                  64, (uint32_t)sh.g, (uint32_t)sh.tpt))
     return EAGLE_ERR_CUDA;
   if (!allow_smem(prompt_attn_tc_kernel<D, KV4>, (int)C::kSmem)) return EAGLE_ERR_CUDA;
-  launch_plan(a, sh, w, s);
+  launch_plan(a, sh, w, 2, s);
   const MainParams mp = {a, a.scale * a.k_scale * kLog2e, sh.g, sh.tpt, sh.tpu, sh.rows, w.hdr, &w.hdr->next, w.pieces,
                          w.ml, w.po};
   launch(prompt_attn_tc_kernel<D, KV4>, sh.ctas, kThreads, C::kSmem, s, map_q, mp);
@@ -1600,10 +2009,10 @@ int attn_launch_tc(const AttnParams& a, void* ws, cudaStream_t s) {
 }
 template <int D>
 int attn_launch_f32(const AttnParams& a, void* ws, cudaStream_t s) {
-  const Shape sh = attn_shape(a.B, a.T, a.Hq, a.Hkv, D, kF32Rows);
+  const Shape sh = attn_shape(a.B, a.T, a.Hq, a.Hkv, D, kFp32);
   const Ws w = attn_ws(sh, ws);
   if (!allow_smem(prompt_attn_f32_kernel<D>, CfgF32<D>::kSmem)) return EAGLE_ERR_CUDA;
-  launch_plan(a, sh, w, s);
+  launch_plan(a, sh, w, 1, s);
   const F32Params fp = {a, a.scale * kLog2e, sh.g, sh.tpu, sh.rows, w.hdr, &w.hdr->next, w.pieces, w.ml, w.po};
   launch(prompt_attn_f32_kernel<D>, sh.ctas, 256, CfgF32<D>::kSmem, s, fp);
   return launch_merge<D, true>(a, sh, w, s);
@@ -1620,7 +2029,9 @@ using namespace eagle;
 
 extern "C" size_t eagle_prompt_attn_workspace_size(int B, int T, int Hq, int Hkv, int D) {
   if (B <= 0 || T < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || Hq / Hkv > 64 || (D != 64 && D != 128)) return 0;
-  return std::max(attn_shape(B, T, Hq, Hkv, D, 2 * kTileRows).total, attn_shape(B, T, Hq, Hkv, D, kF32Rows).total) + 256;
+  size_t most = 0;
+  for (const Path path : {kTensor, kFew, kFp32}) most = std::max(most, attn_shape(B, T, Hq, Hkv, D, path).total);
+  return most + 256;
 }
 
 extern "C" int eagle_prompt_attn(const void* q, long long q_stride, const void* k_cache, const void* v_cache,

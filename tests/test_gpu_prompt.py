@@ -315,3 +315,74 @@ def test_graph_and_side_stream():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(1, 1, 64), (4, 4, 128), (16, 1, 64), (16, 1, 128), (32, 8, 128), (14, 2, 64), (9, 3, 128),
+                                      (17, 1, 64)])
+@pytest.mark.parametrize("new,ctx", [
+    ([1], [0]), ([1], [15]), ([1], [16]), ([1], [3000]), ([1, 0, 2, 1], [5, 9, 126, 1023]), ([0, 0, 3], [1, 1, 500]),
+    ([1] * 33, [7 * i * i % 911 for i in range(33)]), ([1] * 600, [i % 200 for i in range(600)]),
+])
+@pytest.mark.parametrize("kind", ["bf16", "kv4"])
+def test_attn_single_tokens(new, ctx, Hq, Hkv, D, kind):
+    b = need_gpu()
+    s = make(sum(ctx) + Hq, new, ctx, Hq, Hkv, D, "bf16", kv4=kind == "kv4", pad=2)
+    out, lse = run_attn(b, s, kind == "kv4")
+    check_attn(s, out, lse, dict(bf16=HALF["bf16"], kv4=HALF["fp16"])[kind])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "kv4"])
+@pytest.mark.parametrize("new", [[1], [40]])
+def test_attn_growing_scores(new, kind):
+    """Scores that rise along the keys, by more than the weights' type can hold
+    against the first maximum: the reference has to move."""
+    b = need_gpu()
+    s = make(12, new, [2000], 8, 2, 64, "bf16", kv4=kind == "kv4")
+    n = 2000 + new[0]
+    k = torch.randn(n, 2, 64)
+    u = torch.randn(2, 64)
+    u /= u.norm(dim=-1, keepdim=True)
+    k = 0.1 * k + u * torch.linspace(-12, 12, n)[:, None, None]
+    s["q"] = (u.repeat_interleave(4, 0)[None] * 20 + torch.randn(new[0], 8, 64)).bfloat16().cuda()
+    pages = s["table"][0].long().cpu()
+    pos = torch.arange(n)
+    if kind == "kv4":
+        full = torch.from_numpy(s["kc_np"]).float()
+        full[pages[pos // 16], pos % 16] = k
+        codes, scales = oracle.kv4_pack(full.transpose(1, 2).numpy())
+        s["k4"], s["ks"] = torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda()
+        s["kc_np"] = oracle.kv4_unpack(codes, scales).transpose(0, 2, 1, 3)
+    else:
+        s["kc"][pages[pos // 16].cuda(), pos.cuda() % 16] = k.bfloat16().cuda()
+        s["kc_np"] = f64(s["kc"])
+    out, lse = run_attn(b, s, kind == "kv4")
+    check_attn(s, out, lse, dict(bf16=HALF["bf16"], kv4=HALF["fp16"])[kind])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "kv4"])
+def test_attn_single_token_nan_and_bad_page(kind):
+    b = need_gpu()
+    s = make(13, [1, 1], [40, 60], 8, 2, 128, "bf16", kv4=kind == "kv4")
+    clean, clse = run_attn(b, s, kind == "kv4")
+    names = ("ks", "vs") if kind == "kv4" else ("kc", "vc")
+    bad = 127 if kind == "kv4" else float("nan")
+    page = s["table"][0, 41 // 16].item()
+    for n in names:  # past request 0's end
+        if kind == "kv4":
+            s[n][page, :, 41 % 16] = bad
+        else:
+            s[n][page, 41 % 16] = bad
+    out, lse = run_attn(b, s, kind == "kv4")
+    assert torch.equal(out, clean) and torch.equal(lse, clse)
+    page = s["table"][1, 0].item()
+    for n in names:
+        if kind == "kv4":
+            s[n][page, 0, 3] = bad
+        else:
+            s[n][page, 3, 0] = bad
+    out, lse = run_attn(b, s, kind == "kv4")
+    assert torch.equal(out[0], clean[0]) and out[1, :4].isnan().all() and torch.equal(out[1, 4:], clean[1, 4:])
+    assert s["st"].item() == 0
+    s["table"][1, 0] = -7
+    out, _ = run_attn(b, s, kind == "kv4")
+    assert s["st"].item() == 6 and out.isfinite().all() and torch.equal(out[0], clean[0])
