@@ -60,22 +60,24 @@ struct PlanHeader {
 
 constexpr int kCand = 6;       // candidate cuts of the plan
 constexpr int kMaxShare = 6;   // pieces per CTA at the finest cut
-__device__ __constant__ const int kShares[kCand] = {0, 1, 2, 3, 4, 6};  // 0: no unit is cut
+// In sixteenths of a piece per CTA (0: no unit is cut); a little under whole
+// numbers, so that rounding a unit's pieces up does not start another wave.
+__device__ __constant__ const int kShares[kCand] = {0, 14, 29, 45, 62, 96};
 
 struct Shape {
   int g, tpt, tpu, rows;  // heads per kv head, tokens per tile and unit, rows per slot
   int ctas, cap_units, cap_pieces, cap_slots;
   size_t off_pieces, off_cuts, off_ml, off_o, total;
 };
-enum Path { kTensor, kFew, kFp32 };
+enum Path { kTensor, kFew, kFew4, kFp32 };
 Shape attn_shape(int B, int T, int Hq, int Hkv, int D, Path path) {
   Shape s;
   s.g = Hq / Hkv;
-  s.tpt = path == kTensor ? kTileRows / s.g : path == kFew ? 1 : kF32Rows / s.g;
+  s.tpt = path == kTensor ? kTileRows / s.g : path == kFp32 ? kF32Rows / s.g : 1;
   s.tpu = path == kTensor ? 2 * s.tpt : s.tpt;
   s.rows = std::min(s.tpu, T) * s.g;
   const int sms = sm_count();
-  s.ctas = (sms > 0 ? sms : 152) * (path == kFew ? 2 : 1);
+  s.ctas = (sms > 0 ? sms : 152) * (path == kFew4 ? 3 : path == kFew ? 2 : 1);
   s.cap_units = T / s.tpu + std::min(B, T);
   // a unit of L > C blocks makes ceil(L / C) < 2 L / C pieces and the finest C
   // is total / (kMaxShare * ctas)
@@ -205,7 +207,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanPar
   // candidate x cuts units longer than C_x = all / (share x ctas)
   if (tid < kCand) {
     const long long f = (long long)kShares[tid] * p.ctas;
-    s_C[tid] = f ? (int)max((long long)p.min_cut, (all + f - 1) / f) : 0x7fffffff;
+    s_C[tid] = f ? (int)max((long long)p.min_cut, (16 * all + f - 1) / f) : 0x7fffffff;
   }
   __syncthreads();
   {
@@ -1422,11 +1424,23 @@ __device__ __forceinline__ uint32_t e4m3_pair_as_f16(uint32_t two) {
 }
 
 template <int D, bool KV4>
-__global__ void __launch_bounds__(kFewThreads, 2) prompt_attn_few_kernel(const FewParams p) {
+struct CfgFew {
+  // CTAs per SM; pages per step (their chains of latencies run side by side)
+  static constexpr int kCtas = KV4 ? 3 : 2, NP = KV4 ? 2 : 1;
+  // 4-bit: steps in flight per warp, copied to shared memory (2.3 KB a page:
+  // held in registers, three pages a warp left the loads' latency exposed)
+  static constexpr int kRing = 3;
+  static constexpr int kCodes = 16 * D / 2, kPage = 2 * (kCodes + D);  // bytes: K and V codes, K and V scales
+  static constexpr int kJoin = 4 * kFewRows * (D * 4 + 8);             // the warps' O, m and l at the end (over the ring)
+  static constexpr int kSmem = KV4 && 4 * kRing * NP * kPage > kJoin ? 4 * kRing * NP * kPage : kJoin;
+};
+template <int D, bool KV4>
+__global__ void __launch_bounds__(kFewThreads, (CfgFew<D, KV4>::kCtas)) prompt_attn_few_kernel(const FewParams p) {
+  using C = CfgFew<D, KV4>;
   constexpr int KS = D / 16, NT = D / 8;  // k steps of S, 8-column tiles of O
   constexpr int KW = KV4 ? D / 32 : D / 8;   // 32-bit words of K per key and lane
   constexpr int VW = KV4 ? D / 64 : D / 16;  // of V
-  constexpr int kAhead = KV4 ? 3 : 1;        // pages in flight per warp
+  constexpr int NP = C::NP;
   extern __shared__ __align__(16) float fm[];  // [4 warps][16 rows][D], then [4][16] (m, l)
   float2* s_ml = reinterpret_cast<float2*>(fm + 4 * kFewRows * D);
   __shared__ int s_piece;
@@ -1441,7 +1455,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) prompt_attn_few_kernel(const F
     if (s_piece >= p.hdr->pieces) break;
     const Piece w = p.pieces[s_piece];
     const int tok = w.c0 + w.u, pos = w.ctx + w.u, n_keys = pos + 1;
-    const int page_end = min(w.k1 * 8, (n_keys + 15) / 16);
+    const int lim = min(n_keys, w.k1 * kBlk), page_end = (lim + 15) / 16;  // the piece's keys end at lim
     const int32_t* tab = a.table + (size_t)w.b * a.max_pages;
     // Q as the A operand of each k step, the lane's two rows j and j + 8
     uint32_t q[KS][4];
@@ -1488,7 +1502,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) prompt_attn_few_kernel(const F
     for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
     struct Page {
-      uint32_t k[2][KW], v[4][VW], ks[2], vs[4];
+      uint32_t k[2][KW], v[4][VW];
     };
     // page ids of this warp, 32 at a time: lane x holds page k0 * 8 + warp + 4 (32 G + x)
     int ids = 0, group = -1;
@@ -1506,47 +1520,35 @@ __global__ void __launch_bounds__(kFewThreads, 2) prompt_attn_few_kernel(const F
       }
       return id;
     };
+    unsigned char* wring = reinterpret_cast<unsigned char*>(fm) + warp * C::kRing * NP * C::kPage;
+    // 4-bit: page i of this warp to its ring, a 16-byte chunk c of V's key r at
+    // chunk c ^ (r / 2 & 3), so that the reads below meet fewer bank conflicts
+    auto copy_page = [&](unsigned char* to, int i) {
+      const int id = page_id(i), key0 = (page0 + 4 * i) * 16;
+      const size_t ch = ((size_t)max(id, 0) * a.Hkv + w.h) * (16 * D);  // channels before the page's head
+      constexpr int CK = D / 32;                                        // chunks per key
+#pragma unroll
+      for (int x = 0; x < 16 * CK / 32; ++x) {
+        const int c = x * 32 + lane, r = c / CK;
+        const bool live = id >= 0 && key0 + r < lim;
+        cp_async16_or_zero(smem_u32(to + c * 16), static_cast<const uint8_t*>(a.kc) + ch / 2 + c * 16, live);
+        cp_async16_or_zero(smem_u32(to + C::kCodes + (r * CK + ((c % CK) ^ ((r >> 1) & (CK - 1)))) * 16),
+                           static_cast<const uint8_t*>(a.vc) + ch / 2 + c * 16, live);
+      }
+      if (lane < 2 * D / 16) {
+        const bool v = lane >= D / 16;
+        cp_async16_or_zero(smem_u32(to + 2 * C::kCodes + lane * 16),
+                           (v ? a.vs : a.ks) + ch / 16 + (lane & (D / 16 - 1)) * 16, id >= 0);
+      }
+    };
     auto load = [&](Page& g, int i) {
       const int id = page_id(i), key0 = (page0 + 4 * i) * 16;
-      if constexpr (KV4) {
-        const size_t row0 = ((size_t)max(id, 0) * a.Hkv + w.h) * 16;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int r = j + 8 * x;
-          const bool live = id >= 0 && key0 + r < n_keys;
-          const uint8_t* c = static_cast<const uint8_t*>(a.kc) + (row0 + r) * (D / 2) + t * (D / 8);
-          g.ks[x] = 0;
-          if constexpr (D == 128) {
-            const uint4 v = live ? __ldg(reinterpret_cast<const uint4*>(c)) : make_uint4(0u, 0u, 0u, 0u);
-            g.k[x][0] = v.x, g.k[x][1] = v.y, g.k[x][2] = v.z, g.k[x][3] = v.w;
-            if (live) g.ks[x] = __ldg(reinterpret_cast<const uint16_t*>(a.ks + (row0 + r) * 8 + 2 * t));
-          } else {
-            const uint2 v = live ? __ldg(reinterpret_cast<const uint2*>(c)) : make_uint2(0u, 0u);
-            g.k[x][0] = v.x, g.k[x][1] = v.y;
-            if (live) g.ks[x] = __ldg(a.ks + (row0 + r) * 4 + t);
-          }
-        }
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int r = 2 * t + (x & 1) + 8 * (x >> 1);
-          const bool live = id >= 0 && key0 + r < n_keys;
-          const uint8_t* c = static_cast<const uint8_t*>(a.vc) + (row0 + r) * (D / 2) + j * (D / 16);
-          g.vs[x] = 0;
-          if constexpr (D == 128) {
-            const uint2 v = live ? __ldg(reinterpret_cast<const uint2*>(c)) : make_uint2(0u, 0u);
-            g.v[x][0] = v.x, g.v[x][1] = v.y;
-            if (live) g.vs[x] = __ldg(a.vs + (row0 + r) * 8 + j);
-          } else {
-            g.v[x][0] = live ? __ldg(reinterpret_cast<const uint32_t*>(c)) : 0u;
-            if (live) g.vs[x] = __ldg(a.vs + (row0 + r) * 4 + (j >> 1));
-          }
-        }
-      } else {
+      if constexpr (!KV4) {
         const size_t tok_ch = (size_t)a.Hkv * D, at0 = (size_t)max(id, 0) * 16 * tok_ch + (size_t)w.h * D;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int r = j + 8 * x;
-          const bool live = id >= 0 && key0 + r < n_keys;
+          const bool live = id >= 0 && key0 + r < lim;
           const __nv_bfloat16* c = static_cast<const __nv_bfloat16*>(a.kc) + at0 + r * tok_ch + 8 * t;
 #pragma unroll
           for (int y = 0; y < D / 32; ++y) {
@@ -1557,7 +1559,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) prompt_attn_few_kernel(const F
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const int r = 2 * t + (x & 1) + 8 * (x >> 1);
-          const bool live = id >= 0 && key0 + r < n_keys;
+          const bool live = id >= 0 && key0 + r < lim;
           const __nv_bfloat16* c = static_cast<const __nv_bfloat16*>(a.vc) + at0 + r * tok_ch + 8 * j;
 #pragma unroll
           for (int y = 0; y < D / 64; ++y) {
@@ -1567,45 +1569,68 @@ __global__ void __launch_bounds__(kFewThreads, 2) prompt_attn_few_kernel(const F
         }
       }
     };
-    auto use = [&](const Page& g, int i) {
-      float s[2][4];
+    // the step of pages i .. i + NP - 1
+    auto use = [&](const Page* pg, const unsigned char* raw, int i) {
+      const bool tail = (page0 + 4 * (i + NP - 1)) * 16 + 16 > lim;
+      float s[NP][2][4];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
-        if constexpr (KV4) {
-          const uint32_t s2 = e4m3_pair_as_f16(D == 128 ? g.ks[x] : g.ks[x] * 0x101u);
-          const uint32_t sl = __byte_perm(s2, s2, 0x1010), sh = __byte_perm(s2, s2, 0x3232);
+      for (int z = 0; z < NP; ++z)
 #pragma unroll
-          for (int y = 0; y < KW; ++y) {
-            uint32_t e[4];
-            kv4_expand(g.k[x][y], y < KW / 2 ? sl : sh, e);
-            mma_16816<true>(s[x], q[2 * y], e[0], e[1]);
-            mma_16816<true>(s[x], q[2 * y + 1], e[2], e[3]);
+        for (int x = 0; x < 2; ++x) {
+          float part[2][4] = {};  // two chains of MMAs
+          if constexpr (KV4) {
+            const unsigned char* pr = raw + z * C::kPage;
+            const int r = j + 8 * x;
+            uint32_t kw[KW], sb;
+            if constexpr (D == 128) {
+              const uint4 v = *reinterpret_cast<const uint4*>(pr + r * 64 + t * 16);
+              kw[0] = v.x, kw[1] = v.y, kw[2] = v.z, kw[3] = v.w;
+              sb = *reinterpret_cast<const uint16_t*>(pr + 2 * C::kCodes + r * 8 + 2 * t);
+            } else {
+              const uint2 v = *reinterpret_cast<const uint2*>(pr + r * 32 + t * 8);
+              kw[0] = v.x, kw[1] = v.y;
+              sb = pr[2 * C::kCodes + r * 4 + t] * 0x101u;
+            }
+            // (a dead key's score is masked below, whatever its scale)
+            const uint32_t s2 = e4m3_pair_as_f16(sb);
+            const uint32_t sl = __byte_perm(s2, s2, 0x1010), sh = __byte_perm(s2, s2, 0x3232);
+#pragma unroll
+            for (int y = 0; y < KW; ++y) {
+              uint32_t e[4];
+              kv4_expand(kw[y], y < KW / 2 ? sl : sh, e);
+              mma_16816<true>(part[0], q[2 * y], e[0], e[1]);
+              mma_16816<true>(part[1], q[2 * y + 1], e[2], e[3]);
+            }
+          } else {
+#pragma unroll
+            for (int y = 0; y < KS; ++y) mma_16816<false>(part[y & 1], q[y], pg[z].k[x][2 * y], pg[z].k[x][2 * y + 1]);
           }
-        } else {
 #pragma unroll
-          for (int y = 0; y < KS; ++y) mma_16816<false>(s[x], q[y], g.k[x][2 * y], g.k[x][2 * y + 1]);
+          for (int e = 0; e < 4; ++e) s[z][x][e] = part[0][e] + part[1][e];
         }
-      }
-      // s[x][2 r + e]: row j + 8 r, key 8 x + 2 t + e
-      const int key0 = (page0 + 4 * i) * 16;
-      if (key0 + 16 > n_keys) {
+      // s[z][x][2 r + e]: row j + 8 r, key 8 x + 2 t + e of page z
+      if (tail) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int z = 0; z < NP; ++z)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (key0 + 8 * x + 2 * t + (e & 1) >= n_keys) s[x][e] = -INFINITY;
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if ((page0 + 4 * (i + z)) * 16 + 8 * x + 2 * t + (e & 1) >= lim) s[z][x][e] = -INFINITY;
       }
-      // the reference of a row is the maximum of the first page; it is renewed
-      // when a weight passes kSumLimit (or is NaN), see the kernel above
-      float w_[2][4];
+      // the reference of a row is the maximum of the first step; it is renewed
+      // when a step's weights pass kSumLimit (or are NaN), see the kernel above
+      float wt[NP][2][4];
       bool renew = i == 0, mine[2] = {true, true};  // by row, the same in its four lanes
 #pragma unroll 1
       for (int pass = 0;; ++pass) {
         if (renew) {
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            float bm = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+            float bm = -INFINITY;
+#pragma unroll
+            for (int z = 0; z < NP; ++z)
+              bm = fmaxf(bm, fmaxf(fmaxf(s[z][0][2 * r], s[z][0][2 * r + 1]), fmaxf(s[z][1][2 * r], s[z][1][2 * r + 1])));
             bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 1));
             bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 2)) * fac[r];
             if (mine[r] && bm > m[r]) {
@@ -1622,17 +1647,21 @@ __global__ void __launch_bounds__(kFewThreads, 2) prompt_attn_few_kernel(const F
             }
           }
         }
+        float sum[2] = {0.f, 0.f};
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const float ref = m[r] == -INFINITY ? 0.f : -m[r];
 #pragma unroll
-          for (int x = 0; x < 2; ++x)
+          for (int z = 0; z < NP; ++z)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) w_[x][2 * r + e] = ex2_approx(fmaf(s[x][2 * r + e], fac[r], ref));
+            for (int x = 0; x < 2; ++x) {
+              const float e0 = ex2_approx(fmaf(s[z][x][2 * r], fac[r], ref));
+              const float e1 = ex2_approx(fmaf(s[z][x][2 * r + 1], fac[r], ref));
+              wt[z][x][2 * r] = e0;
+              wt[z][x][2 * r + 1] = e1;
+              sum[r] += e0 + e1;
+            }
         }
-        float sum[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) sum[r] = (w_[0][2 * r] + w_[0][2 * r + 1]) + (w_[1][2 * r] + w_[1][2 * r + 1]);
         const bool over0 = !(sum[0] <= kSumLimit), over1 = !(sum[1] <= kSumLimit);
         if (pass || !__any_sync(0xffffffffu, over0 || over1)) {
           l[0] += sum[0];
@@ -1643,61 +1672,90 @@ __global__ void __launch_bounds__(kFewThreads, 2) prompt_attn_few_kernel(const F
         mine[0] = (__ballot_sync(0xffffffffu, over0) >> (lane & 28) & 15u) != 0;
         mine[1] = (__ballot_sync(0xffffffffu, over1) >> (lane & 28) & 15u) != 0;
       }
-      const uint32_t pa[4] = {pack16<KV4>(w_[0][0], w_[0][1]), pack16<KV4>(w_[0][2], w_[0][3]),
-                              pack16<KV4>(w_[1][0], w_[1][1]), pack16<KV4>(w_[1][2], w_[1][3])};
-      // V: pairs of keys (2t, 2t + 1) and (2t + 8, 2t + 9) of each channel
-      if constexpr (KV4) {
-        uint32_t sc[4];
-        {
-          const uint32_t s01 = e4m3_pair_as_f16(g.vs[0] | g.vs[1] << 8), s23 = e4m3_pair_as_f16(g.vs[2] | g.vs[3] << 8);
+#pragma unroll
+      for (int z = 0; z < NP; ++z) {
+        const uint32_t pa[4] = {pack16<KV4>(wt[z][0][0], wt[z][0][1]), pack16<KV4>(wt[z][0][2], wt[z][0][3]),
+                                pack16<KV4>(wt[z][1][0], wt[z][1][1]), pack16<KV4>(wt[z][1][2], wt[z][1][3])};
+        // V: pairs of keys (2t, 2t + 1) and (2t + 8, 2t + 9) of each channel
+        if constexpr (KV4) {
+          const unsigned char* pr = raw + z * C::kPage;
+          uint32_t vw[4][VW], vs[4], sc[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int r = 2 * t + (x & 1) + 8 * (x >> 1), at = (r >> 1) & (D / 32 - 1);
+            if constexpr (D == 128) {
+              const uint2 v = *reinterpret_cast<const uint2*>(pr + C::kCodes + r * 64 + (((j >> 1) ^ at) << 4) + (j & 1) * 8);
+              vw[x][0] = v.x, vw[x][1] = v.y;
+              vs[x] = pr[2 * C::kCodes + D + r * 8 + j];
+            } else {
+              vw[x][0] = *reinterpret_cast<const uint32_t*>(pr + C::kCodes + r * 32 + (((j >> 2) ^ at) << 4) + (j & 3) * 4);
+              vs[x] = pr[2 * C::kCodes + D + r * 4 + (j >> 1)];
+            }
+            // a dead key's scale may be anything; its codes are zeros
+            if (tail && (page0 + 4 * (i + z)) * 16 + r >= lim) vs[x] = 0;
+          }
+          const uint32_t s01 = e4m3_pair_as_f16(vs[0] | vs[1] << 8);
+          const uint32_t s23 = e4m3_pair_as_f16(vs[2] | vs[3] << 8);
           sc[0] = __byte_perm(s01, s01, 0x1010), sc[1] = __byte_perm(s01, s01, 0x3232);
           sc[2] = __byte_perm(s23, s23, 0x1010), sc[3] = __byte_perm(s23, s23, 0x3232);
-        }
 #pragma unroll
-        for (int y = 0; y < VW; ++y) {
-          uint32_t e[4][4];
+          for (int y = 0; y < VW; ++y) {
+            uint32_t e[4][4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) kv4_expand(g.v[x][y], sc[x], e[x]);
+            for (int x = 0; x < 4; ++x) kv4_expand(vw[x][y], sc[x], e[x]);
 #pragma unroll
-          for (int z = 0; z < 4; ++z)
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int hl = 0; hl < 2; ++hl) {
+                const uint32_t sel = hl ? 0x7632u : 0x5410u;
+                mma_16816<true>(o[8 * y + 2 * c + hl], pa, __byte_perm(e[0][c], e[1][c], sel),
+                                __byte_perm(e[2][c], e[3][c], sel));
+              }
+          }
+        } else {
+#pragma unroll
+          for (int y = 0; y < VW; ++y)
 #pragma unroll
             for (int hl = 0; hl < 2; ++hl) {
               const uint32_t sel = hl ? 0x7632u : 0x5410u;
-              mma_16816<true>(o[8 * y + 2 * z + hl], pa, __byte_perm(e[0][z], e[1][z], sel),
-                              __byte_perm(e[2][z], e[3][z], sel));
+              mma_16816<false>(o[2 * y + hl], pa, __byte_perm(pg[z].v[0][y], pg[z].v[1][y], sel),
+                               __byte_perm(pg[z].v[2][y], pg[z].v[3][y], sel));
             }
         }
-      } else {
-#pragma unroll
-        for (int y = 0; y < VW; ++y)
-#pragma unroll
-          for (int hl = 0; hl < 2; ++hl) {
-            const uint32_t sel = hl ? 0x7632u : 0x5410u;
-            mma_16816<false>(o[2 * y + hl], pa, __byte_perm(g.v[0][y], g.v[1][y], sel),
-                             __byte_perm(g.v[2][y], g.v[3][y], sel));
-          }
       }
     };
     const int n_pages = page0 < page_end ? (page_end - page0 + 3) / 4 : 0;
-    Page ring[kAhead];
+    if constexpr (KV4) {
+      auto copy_step = [&](int slot, int i) {  // a page past the end is masked: its slot's old bytes do
+        if (i < n_pages) {
 #pragma unroll
-    for (int x = 0; x < kAhead; ++x)
-      if (x < n_pages) load(ring[x], x);
-#pragma unroll 1
-    for (int i = 0; i < n_pages; i += kAhead) {
-#pragma unroll
-      for (int x = 0; x < kAhead; ++x) {
-        if (i + x >= n_pages) break;
-        if constexpr (kAhead == 1) {
-          // 16-bit pages: 64 registers of loads; the next page's are issued
-          // as soon as this one's have been taken
-          const Page cur = ring[0];
-          if (i + 1 < n_pages) load(ring[0], i + 1);
-          use(cur, i);
-        } else {
-          use(ring[x], i + x);
-          if (i + x + kAhead < n_pages) load(ring[x], i + x + kAhead);
+          for (int z = 0; z < NP; ++z) copy_page(wring + (slot * NP + z) * C::kPage, i + z);
         }
+        cp_async_commit();
+      };
+#pragma unroll
+      for (int x = 0; x < C::kRing; ++x) copy_step(x, x * NP);
+      int slot = 0;
+#pragma unroll 1
+      for (int i = 0; i < n_pages; i += NP) {
+        cp_async_wait<C::kRing - 1>();
+        __syncwarp();
+        use(nullptr, wring + slot * NP * C::kPage, i);
+        __syncwarp();
+        copy_step(slot, i + C::kRing * NP);
+        if (++slot == C::kRing) slot = 0;
+      }
+      cp_async_wait_all();
+      __syncthreads();  // the join below takes the rings' place
+    } else {
+      // the next page's loads are issued as soon as this one's have been taken
+      Page next;
+      if (n_pages > 0) load(next, 0);
+#pragma unroll 1
+      for (int i = 0; i < n_pages; ++i) {
+        const Page cur = next;
+        if (i + 1 < n_pages) load(next, i + 1);
+        use(&cur, nullptr, i);
       }
     }
     // join the warps: rows < g of (m, l) and O
@@ -1986,12 +2044,12 @@ template <int D, bool KV4>
 int attn_launch_tc(const AttnParams& a, void* ws, cudaStream_t s) {
   using C = Cfg<D, KV4>;
   if (few_rows(a.B, a.T, a.Hq, a.Hkv)) {
-    const Shape sh = attn_shape(a.B, a.T, a.Hq, a.Hkv, D, kFew);
+    const Shape sh = attn_shape(a.B, a.T, a.Hq, a.Hkv, D, KV4 ? kFew4 : kFew);
     const Ws w = attn_ws(sh, ws);
-    constexpr int kSmem = 4 * kFewRows * (D * 4 + 8);
+    if (!allow_smem(prompt_attn_few_kernel<D, KV4>, CfgFew<D, KV4>::kSmem)) return EAGLE_ERR_CUDA;
     launch_plan(a, sh, w, 2, s);
     const FewParams fp = {a, a.scale * a.k_scale * kLog2e, sh.g, sh.rows, w.hdr, &w.hdr->next, w.pieces, w.ml, w.po};
-    launch(prompt_attn_few_kernel<D, KV4>, sh.ctas, kFewThreads, kSmem, s, fp);
+    launch(prompt_attn_few_kernel<D, KV4>, sh.ctas, kFewThreads, CfgFew<D, KV4>::kSmem, s, fp);
     return launch_merge<D, false>(a, sh, w, s);
   }
   const Shape sh = attn_shape(a.B, a.T, a.Hq, a.Hkv, D, kTensor);
@@ -2030,7 +2088,7 @@ using namespace eagle;
 extern "C" size_t eagle_prompt_attn_workspace_size(int B, int T, int Hq, int Hkv, int D) {
   if (B <= 0 || T < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || Hq / Hkv > 64 || (D != 64 && D != 128)) return 0;
   size_t most = 0;
-  for (const Path path : {kTensor, kFew, kFp32}) most = std::max(most, attn_shape(B, T, Hq, Hkv, D, path).total);
+  for (const Path path : {kTensor, kFew, kFew4, kFp32}) most = std::max(most, attn_shape(B, T, Hq, Hkv, D, path).total);
   return most + 256;
 }
 
