@@ -77,6 +77,9 @@ _SIGS = {
                                _P, _P]),
     "eagle_prompt_attn_kv4": (_I, [_P, _L, _P, _P, _P, _P, _F, _F, _I, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I,
                                    _I, _F, _P, _Z, _P, _P]),
+    "eagle_draft_prompt_workspace_size": (_Z, [_I, _I, _I, _I, _I, _I, _I, _I]),
+    "eagle_draft_prompt": (_I, [_P, _P, _P, _P, _P, _P, _P, _F, _P, _I, _P, _P, _P, _P, _P, _P, _F, _F, _I, _P, _I, _P,
+                                _I, _I, _I, _I, _I, _I, _I, _I, _P, _Z, _P, _P]),
 }
 
 _lib = None
@@ -563,4 +566,29 @@ def eagle_prompt_attn_kv4(q, k_codes, k_scales, v_codes, v_scales, block_table, 
         v_scales.data_ptr(), k_scale, v_scale, P, block_table.data_ptr(), block_table.shape[1],
         cu_seqlens.data_ptr(), ctx_lens.data_ptr(), out.data_ptr(), _addr(lse), B, T, Hq, Hkv, D, page,
         D ** -0.5 if scale is None else scale, ws.data_ptr(), ws.numel(), _addr(status), _raw_stream(stream)))
+    return out
+
+
+def eagle_draft_prompt_workspace_size(B, T, d, Hq, Hkv, D, I, dtype):
+    return int(lib().eagle_draft_prompt_workspace_size(B, T, d, Hq, Hkv, D, I, dtype))
+
+
+def eagle_draft_prompt(x, weights, rope, cu_seqlens, ctx_lens, k_cache, v_cache, block_table, out, eps=1e-5,
+                       k_scales=None, v_scales=None, k_scale=1.0, v_scale=1.0, ws=None, status=None, stream=None):
+    """The drafter's decoder layer over packed prompt rows, filling its paged
+    cache (with k_scales and v_scales: 4-bit pages).  weights as eagle_draft_layer."""
+    T, d = x.shape
+    B, D = ctx_lens.shape[0], 2 * rope.shape[2]
+    Hq = weights["o"].shape[1] // D
+    Hkv = (weights["qkv"].shape[0] // D - Hq) // 2
+    I = weights["down"].shape[1]
+    dt = _dtype(x)
+    if ws is None:
+        ws = workspace(eagle_draft_prompt_workspace_size(B, T, d, Hq, Hkv, D, I, dt), x.device)
+    _check("eagle_draft_prompt", lib().eagle_draft_prompt(
+        x.data_ptr(), _addr(weights["norm1"]), _addr(weights["qkv"]), _addr(weights["o"]), _addr(weights["norm2"]),
+        _addr(weights["gu"]), _addr(weights["down"]), eps, rope.data_ptr(), rope.shape[0], cu_seqlens.data_ptr(),
+        ctx_lens.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scales), _addr(v_scales), k_scale, v_scale,
+        k_cache.shape[0], block_table.data_ptr(), block_table.shape[1], out.data_ptr(), B, T, d, Hq, Hkv, D, I, dt,
+        ws.data_ptr(), ws.numel(), _addr(status), _raw_stream(stream)))
     return out

@@ -382,6 +382,137 @@ extern "C" int eagle_draft_layer(const void* x, const void* w_norm1, const void*
   return last_launch_status();
 }
 
+namespace {
+constexpr int kPromptRows = 4096;  // rows per projection call (eagle_linear's limit)
+
+struct PromptWs {
+  size_t h, qkv, q, a, x1, gu, act, lin, att, total;
+};
+PromptWs prompt_ws(int B, int T, int d, int Hq, int Hkv, int D, int I, int dtype) {
+  const size_t es = dtype == EAGLE_BF16 ? 2 : 4, M = (size_t)std::min(T, kPromptRows);
+  PromptWs L;
+  L.h = round_up(M * d * es, 256);
+  L.qkv = round_up((size_t)T * (Hq + 2 * Hkv) * D * es, 256);
+  L.q = L.a = round_up((size_t)T * Hq * D * es, 256);
+  L.x1 = round_up(M * d * es, 256);
+  L.gu = round_up(M * 2 * I * es, 256);
+  L.act = round_up(M * I * es, 256);
+  size_t lin = 0;
+  for (const int rows : {std::min(T, kPromptRows), T % kPromptRows}) {
+    if (rows == 0) continue;
+    lin = std::max(lin, eagle_linear_workspace_size(rows, (Hq + 2 * Hkv) * D, d, dtype));
+    lin = std::max(lin, eagle_linear_workspace_size(rows, d, Hq * D, dtype));
+    lin = std::max(lin, eagle_linear_workspace_size(rows, 2 * I, d, dtype));
+    lin = std::max(lin, eagle_linear_workspace_size(rows, d, I, dtype));
+  }
+  L.lin = round_up(lin, 256);
+  L.att = round_up(eagle_prompt_attn_workspace_size(B, T, Hq, Hkv, D), 256);
+  L.total = L.h + L.qkv + L.q + L.a + L.x1 + L.gu + L.act + L.lin + L.att + 10 * 256;
+  return L;
+}
+bool prompt_shape_ok(int d, int Hq, int Hkv, int D, int I) {
+  return layer_shape_ok(1, 1, d, Hq, Hkv, D, I, 1, 0) && (long long)Hq + 2ll * Hkv <= 1024 && Hq / Hkv <= 64;
+}
+}  // namespace
+
+extern "C" size_t eagle_draft_prompt_workspace_size(int B, int T, int d, int Hq, int Hkv, int D, int I, int dtype) {
+  if (B <= 0 || T < 0 || (dtype != EAGLE_BF16 && dtype != EAGLE_FP32) || !prompt_shape_ok(d, Hq, Hkv, D, I)) return 0;
+  return prompt_ws(B, T, d, Hq, Hkv, D, I, dtype).total;
+}
+
+extern "C" int eagle_draft_prompt(const void* x, const void* w_norm1, const void* w_qkv, const void* w_o,
+                                  const void* w_norm2, const void* w_gu, const void* w_down, float eps,
+                                  const float* rope, int max_pos, const int32_t* cu_seqlens, const int32_t* ctx_lens,
+                                  void* k_cache, void* v_cache, uint8_t* k_scales, uint8_t* v_scales, float k_scale,
+                                  float v_scale, int num_pages, const int32_t* block_table, int max_pages, void* out,
+                                  int B, int T, int d, int Hq, int Hkv, int D, int I, int dtype, void* ws,
+                                  size_t ws_bytes, int32_t* dev_status, void* stream) {
+  if (!x || !w_norm1 || !w_qkv || !w_o || !w_norm2 || !w_gu || !w_down || !rope || !cu_seqlens || !ctx_lens ||
+      !k_cache || !v_cache || !block_table || !out)
+    return EAGLE_ERR_INVALID_ARG;
+  if (dtype != EAGLE_BF16 && dtype != EAGLE_FP32) return EAGLE_ERR_INVALID_ARG;
+  const bool bf = dtype == EAGLE_BF16, kv4 = k_scales || v_scales;
+  if (kv4 && (!k_scales || !v_scales || !bf)) return EAGLE_ERR_INVALID_ARG;
+  if (!(eps >= 0.f) || x == out || B <= 0 || T < 0 || max_pos <= 0 || num_pages <= 0 || max_pages <= 0)
+    return EAGLE_ERR_INVALID_ARG;
+  if (!prompt_shape_ok(d, Hq, Hkv, D, I) || B > 65535) return EAGLE_ERR_UNSUPPORTED;
+  if (!aligned16(rope) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scales) || !aligned16(v_scales))
+    return EAGLE_ERR_INVALID_ARG;
+  if (T == 0) return EAGLE_OK;
+  const PromptWs L = prompt_ws(B, T, d, Hq, Hkv, D, I, dtype);
+  if (!ws || ws_bytes < L.total) return EAGLE_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  char* cur = static_cast<char*>(ws);
+  void* h = ws_carve(cur, L.h);
+  char* qkv = static_cast<char*>(ws_carve(cur, L.qkv));
+  void* q = ws_carve(cur, L.q);
+  char* a = static_cast<char*>(ws_carve(cur, L.a));
+  void* x1 = ws_carve(cur, L.x1);
+  void* gu = ws_carve(cur, L.gu);
+  void* act = ws_carve(cur, L.act);
+  void* lin_ws = ws_carve(cur, L.lin);
+  void* att_ws = ws_carve(cur, L.att);
+  const size_t es = bf ? 2 : 4;
+  const int nqkv = (Hq + 2 * Hkv) * D;
+  auto norm = [&](const void* in, const void* w, void* o, int rows) {
+    if (bf)
+      launch(rmsnorm_kernel<__nv_bfloat16>, rows, kRowThreads, 0, s, (const __nv_bfloat16*)in, (const __nv_bfloat16*)w,
+             eps, (__nv_bfloat16*)o, d);
+    else
+      launch(rmsnorm_kernel<float>, rows, kRowThreads, 0, s, (const float*)in, (const float*)w, eps, (float*)o, d);
+    note_launch();
+  };
+  int rc;
+#define EAGLE_TRY(call)            \
+  do {                             \
+    rc = (call);                   \
+    if (rc != EAGLE_OK) return rc; \
+  } while (0)
+  for (int r0 = 0; r0 < T; r0 += kPromptRows) {
+    const int M = std::min(kPromptRows, T - r0);
+    norm(static_cast<const char*>(x) + (size_t)r0 * d * es, w_norm1, h, M);
+    EAGLE_TRY(eagle_linear(h, w_qkv, nullptr, nullptr, qkv + (size_t)r0 * nqkv * es, M, nqkv, d, dtype, lin_ws, L.lin,
+                           dev_status, stream));
+  }
+  const char *k = qkv + (size_t)Hq * D * es, *v = k + (size_t)Hkv * D * es;
+  const float scale = 1.f / sqrtf((float)D);
+  if (kv4) {
+    uint8_t *kc = static_cast<uint8_t*>(k_cache), *vc = static_cast<uint8_t*>(v_cache);
+    EAGLE_TRY(eagle_kv_append_kv4(qkv, k, v, nqkv, nqkv, nqkv, rope, max_pos, cu_seqlens, ctx_lens, B, T, Hq, Hkv, D, q,
+                                  kc, k_scales, vc, v_scales, k_scale, v_scale, num_pages, block_table, max_pages,
+                                  dev_status, stream));
+    EAGLE_TRY(eagle_prompt_attn_kv4(q, (long long)Hq * D, kc, k_scales, vc, v_scales, k_scale, v_scale, num_pages,
+                                    block_table, max_pages, cu_seqlens, ctx_lens, a, nullptr, B, T, Hq, Hkv, D, 16,
+                                    scale, att_ws, L.att, dev_status, stream));
+  } else {
+    EAGLE_TRY(eagle_kv_append(qkv, k, v, nqkv, nqkv, nqkv, rope, max_pos, cu_seqlens, ctx_lens, B, T, Hq, Hkv, D, dtype, q,
+                              k_cache, v_cache, num_pages, block_table, max_pages, dev_status, stream));
+    EAGLE_TRY(eagle_prompt_attn(q, (long long)Hq * D, k_cache, v_cache, num_pages, block_table, max_pages, cu_seqlens,
+                                ctx_lens, a, nullptr, B, T, Hq, Hkv, D, 16, scale, dtype, att_ws, L.att, dev_status,
+                                stream));
+  }
+  for (int r0 = 0; r0 < T; r0 += kPromptRows) {
+    const int M = std::min(kPromptRows, T - r0);
+    const size_t at = (size_t)r0 * d * es;
+    EAGLE_TRY(eagle_linear(a + (size_t)r0 * Hq * D * es, w_o, nullptr, static_cast<const char*>(x) + at, x1, M, d, Hq * D,
+                           dtype, lin_ws, L.lin, dev_status, stream));
+    norm(x1, w_norm2, h, M);
+    EAGLE_TRY(eagle_linear(h, w_gu, nullptr, nullptr, gu, M, 2 * I, d, dtype, lin_ws, L.lin, dev_status, stream));
+    const long long n = (long long)M * I;
+    const long long blocks = std::min((n + kRowThreads - 1) / kRowThreads, 4LL * std::max(1, sm_count()));
+    if (bf)
+      launch(swiglu_kernel<__nv_bfloat16>, (unsigned)blocks, kRowThreads, 0, s, (const __nv_bfloat16*)gu, I, n,
+             (__nv_bfloat16*)act);
+    else
+      launch(swiglu_kernel<float>, (unsigned)blocks, kRowThreads, 0, s, (const float*)gu, I, n, (float*)act);
+    note_launch();
+    EAGLE_TRY(eagle_linear(act, w_down, nullptr, x1, static_cast<char*>(out) + at, M, d, I, dtype, lin_ws, L.lin,
+                           dev_status, stream));
+  }
+#undef EAGLE_TRY
+  return last_launch_status();
+}
+
 extern "C" int eagle_draft_rows(int B, int step, int width, int Rmax, int max_nodes, int d, int dtype,
                                 const int32_t* root_token, const int32_t* frontier, const int32_t* n_frontier,
                                 const int32_t* node_parent, const int32_t* node_token,

@@ -6,7 +6,9 @@
  * serve stochastic verification without materialised logits, eagle_tree_commit
  * which publishes the accepted path, and the drafter step: eagle_draft_input,
  * the token-embedding input FC, and eagle_draft_layer, its decoder layer,
- * built on eagle_linear):
+ * built on eagle_linear; before the first round the prompt path fills the
+ * paged caches: eagle_kv_append, eagle_prompt_attn and eagle_draft_prompt,
+ * their 4-bit-page forms beside them):
  *   eagle_fuse_proj             EAGLE-3 fused feature g = W_proj [h_low; h_mid; h_high]
  *   eagle_tree_attn             tree-masked attention vs a paged KV cache + the tree rows
  *   eagle_lmhead_topk           LM-head GEMM with fused per-row top-k and log-softmax
@@ -800,6 +802,34 @@ int eagle_prompt_attn_kv4(const void* q, long long q_stride, const uint8_t* k_co
                           void* out, float* lse, int B, int T, int Hq, int Hkv, int D,
                           int page_size, float scale, void* ws, size_t ws_bytes,
                           int32_t* dev_status, void* stream);
+
+/* eagle_draft_prompt -- the drafter's decoder layer (eagle_draft_layer) over
+ * packed prompt rows: it fills the drafter's paged cache and gives the rows'
+ * outputs, so that the first eagle_draft_layer call of a round finds its
+ * prefix.  [M7.5] section 0x03C (the drafter's own K/V of the committed
+ * prefix); [E3] section 3.4 "The transformer decoder layer".
+ *   h = RMSNorm(x) * w_norm1;  q, k, v = split(h W_qkv^T)
+ *   eagle_kv_append(q, k, v), then a = eagle_prompt_attn, scale 1/sqrt(D)
+ *   x1 = x + a W_o^T;  h2 = RMSNorm(x1) * w_norm2
+ *   out = x1 + (silu(h2 Wg^T) * (h2 Wu^T)) W_down^T
+ *   x, out : [T, d] dtype `dtype` (must not alias);  weights as
+ *            eagle_draft_layer;  rope as eagle_kv_append (not NULL)
+ *   k_cache, v_cache : an ordinary cache, or with k_scales and v_scales not
+ *            NULL the codes of 4-bit pages (bf16 rows only; k_scale and
+ *            v_scale are read then)
+ * Errors, cu_seqlens, ctx_lens (not advanced) and block_table as above.
+ * Limits: those of eagle_kv_append, eagle_prompt_attn and eagle_draft_layer's
+ * shapes; any T (the projections run 4096 rows at a time). */
+size_t eagle_draft_prompt_workspace_size(int B, int T, int d, int Hq, int Hkv, int D, int I,
+                                         int dtype);
+int eagle_draft_prompt(const void* x, const void* w_norm1, const void* w_qkv, const void* w_o,
+                       const void* w_norm2, const void* w_gu, const void* w_down, float eps,
+                       const float* rope, int max_pos, const int32_t* cu_seqlens,
+                       const int32_t* ctx_lens, void* k_cache, void* v_cache, uint8_t* k_scales,
+                       uint8_t* v_scales, float k_scale, float v_scale, int num_pages,
+                       const int32_t* block_table, int max_pages, void* out, int B, int T, int d,
+                       int Hq, int Hkv, int D, int I, int dtype, void* ws, size_t ws_bytes,
+                       int32_t* dev_status, void* stream);
 
 #ifdef __cplusplus
 }

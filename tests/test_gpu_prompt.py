@@ -386,3 +386,74 @@ def test_attn_single_token_nan_and_bad_page(kind):
     s["table"][1, 0] = -7
     out, _ = run_attn(b, s, kind == "kv4")
     assert s["st"].item() == 6 and out.isfinite().all() and torch.equal(out[0], clean[0])
+
+
+@pytest.mark.parametrize("kind,new,ctx", [("bf16", [37, 0, 5], [0, 20, 16]), ("fp32", [9, 4], [0, 30]), ("kv4", [37, 5], [0, 16]),
+                                          ("bf16", [4100], [0])])
+def test_draft_prompt(kind, new, ctx):
+    """The layer over the prompt against the oracle's pieces, storing where the
+    call stores; the cache then holds what the oracle's append gives."""
+    b = need_gpu()
+    dt = torch.float32 if kind == "fp32" else torch.bfloat16
+    d, Hq, Hkv, D, I = 256, 4, 2, 64, 128
+    s = make(21, new, ctx, Hq, Hkv, D, "fp32" if kind == "fp32" else "bf16", kv4=kind == "kv4")
+    g = torch.Generator().manual_seed(3)
+    rn = lambda *sh, k=0.05: (torch.randn(*sh, generator=g) * k).to(dt)  # noqa: E731
+    W = dict(norm1=1 + rn(d), qkv=rn((Hq + 2 * Hkv) * D, d), o=rn(d, Hq * D), norm2=1 + rn(d), gu=rn(2 * I, d), down=rn(d, I))
+    x = rn(s["T"], d, k=1.0)
+    rope = b.eagle_rope_table(max(n + c for n, c in zip(new, ctx)), D, 1e4)
+    out = torch.empty(s["T"], d, dtype=dt, device="cuda")
+    Wc = {k: v.cuda() for k, v in W.items()}
+    kw = dict(k_scales=s["ks"], v_scales=s["vs"]) if kind == "kv4" else {}
+    names = ("k4", "v4") if kind == "kv4" else ("kc", "vc")
+    b.eagle_draft_prompt(x.cuda(), Wc, rope, s["cu"], s["ctx"], s[names[0]], s[names[1]], s["table"], out, status=s["st"], **kw)
+    st = (lambda a: torch.from_numpy(a).to(dt).double().numpy()) if dt != torch.float32 else (lambda a: a.astype(np.float32).astype(np.float64))
+    w = {k: v.double().numpy() for k, v in W.items()}
+    cu = s["cu"].cpu().numpy()
+    places = oracle.row_places(cu, ctx, s["table"].cpu().numpy())
+    qkv = st(oracle.linear(st(oracle.rms_norm(x.double().numpy(), w["norm1"], 1e-5)), w["qkv"])).reshape(s["T"], -1, D)
+    r = f64(rope)[[p[1] for p in places]]
+    q, k, v = st(oracle.rotate(qkv[:, :Hq], r)), oracle.rotate(qkv[:, Hq:Hq + Hkv], r), qkv[:, Hq + Hkv:]
+    if kind == "kv4":
+        k, v = (oracle.kv4_unpack(*oracle.kv4_pack(a.astype(np.float32))) for a in (k, v))
+    else:
+        k = st(k)
+    for t, (_, _, page, slot) in enumerate(places):
+        s["kc_np"][page, slot], s["vc_np"][page, slot] = k[t], v[t]
+    a = st(oracle.prompt_attn(q, gathered(s, s["kc_np"]), gathered(s, s["vc_np"]), cu, ctx, D ** -0.5)[0]).reshape(s["T"], -1)
+    x1 = st(oracle.linear(a, w["o"], residual=x.double().numpy()))
+    gu = st(oracle.linear(st(oracle.rms_norm(x1, w["norm2"], 1e-5)), w["gu"]))
+    want = oracle.linear(st(oracle.silu(gu[:, :I]) * gu[:, I:]), w["down"], residual=x1)
+    # each stored intermediate may round the other way by one step where the
+    # sums differ in fp32: a handful of roundings of the output's size, and for
+    # 4-bit pages a code may fall the other side of a midpoint
+    tol = {"fp32": 1e-5, "bf16": 4 * 2.0 ** -8, "kv4": 6 * 2.0 ** -8}[kind]
+    err = np.abs(f64(out) - want)
+    print(f"{kind}: worst {float((err / (np.abs(want) + 1)).max()):.2e} of {tol:.2e}")
+    assert (err <= tol * (np.abs(want) + 1)).all() and s["st"].item() == 0
+
+
+def test_prompt_then_draft_layer():
+    """A prompt through eagle_draft_prompt, then the next row through
+    eagle_draft_layer over the cache it filled, equals the whole prompt with
+    that row through eagle_draft_prompt."""
+    b = need_gpu()
+    d, Hq, Hkv, D, I, n = 256, 4, 2, 64, 128, 50
+    s = make(22, [n + 1], [0], Hq, Hkv, D, "bf16")
+    g = torch.Generator().manual_seed(4)
+    rn = lambda *sh, k=0.05: (torch.randn(*sh, generator=g) * k).bfloat16().cuda()  # noqa: E731
+    W = dict(norm1=1 + rn(d), qkv=rn((Hq + 2 * Hkv) * D, d), o=rn(d, Hq * D), norm2=1 + rn(d), gu=rn(2 * I, d), down=rn(d, I))
+    x, rope = rn(n + 1, d, k=1.0), b.eagle_rope_table(64, D, 1e4)
+    whole = torch.empty_like(x)
+    b.eagle_draft_prompt(x, W, rope, s["cu"], s["ctx"], s["kc"], s["vc"], s["table"], whole)
+    s["kc"].fill_(float("nan"))
+    part = torch.empty(n, d, dtype=x.dtype, device="cuda")
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    b.eagle_draft_prompt(x[:n].contiguous(), W, rope, cu, s["ctx"], s["kc"], s["vc"], s["table"], part)
+    assert torch.equal(part[:32], whole[:32]) or (part - whole[:n]).abs().max() < 0.05
+    z = lambda *sh: torch.zeros(*sh, dtype=x.dtype, device="cuda")  # noqa: E731
+    out = torch.empty(1, d, dtype=x.dtype, device="cuda")
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    b.eagle_draft_layer(x[n:].contiguous(), W, i32([n]).view(1, 1), s["kc"], s["vc"], s["table"], i32(n), z(1, 8, Hq, D),
+                        z(1, 8, Hkv, D), z(1, 8, Hkv, D), (1 << torch.arange(8)).view(1, 8).cuda(), 0, out, theta=1e4)
+    assert (out[0].float() - whole[n].float()).abs().max() <= 4 * 2.0 ** -8 * (1 + whole[n].float().abs().max())

@@ -105,3 +105,17 @@ def test_binding_refuses_strided_heads():
     with pytest.raises(ValueError):
         eb._row_stride("q", q, 128)
     assert eb._row_stride("q", torch.zeros(4, 6, 128)[:, :4], 128) == 6 * 128
+
+
+def test_draft_prompt_refusals(L):
+    def call(x=P, out=ctypes.c_void_p(512), rope=P, ks=N, vs=N, d=256, D=64, I=256, dtype=1, T=4, max_pos=8, eps=1e-5):
+        return L.eagle_draft_prompt(x, P, P, P, P, P, P, eps, rope, max_pos, P, P, P, P, ks, vs, 1.0, 1.0, 8, P, 4, out, 2,
+                                    T, d, 4, 2, D, I, dtype, N, 0, N, N)
+    assert call(T=0) == OK and call() == WORKSPACE
+    for kw in (dict(x=N), dict(out=P), dict(rope=N), dict(ks=P), dict(ks=P, vs=P, dtype=0), dict(dtype=5), dict(max_pos=0),
+               dict(eps=-1.0), dict(T=-1)):
+        assert call(**kw) == INVALID, kw
+    for kw in (dict(d=100), dict(D=96), dict(I=100)):
+        assert call(**kw) == UNSUPPORTED, kw
+    assert L.eagle_draft_prompt_workspace_size(2, 5000, 256, 4, 2, 64, 256, 1) > 0
+    assert L.eagle_draft_prompt_workspace_size(2, 4, 100, 4, 2, 64, 256, 1) == 0
