@@ -462,8 +462,15 @@ def eagle_tree_commit(k_tree, v_tree, path_rows, accept_len, k_cache, v_cache, b
 # ------------------------------------------------------------------ the prompt path
 # These calls are made once per layer and decoding step, so the marshalling is
 # kept short: plain integers for the pointers, no intermediate objects.
-def _raw_stream(stream):
-    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream(stream, device):
+    if stream is not None:
+        return stream.cuda_stream
+    if _current_raw_stream is not None:
+        return _current_raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _addr(t):
@@ -472,17 +479,31 @@ def _addr(t):
 
 def _row_stride(name, t, D):
     """Row stride of a [T, heads, D] array whose heads and channels are contiguous."""
-    st = t.stride()
-    if st[2] != 1 or (st[1] != D and t.shape[1] > 1):
-        raise ValueError(f"{name}: heads and channels must be contiguous, strides {st}")
-    return st[0]
+    rows, heads, last = t.stride()
+    if last != 1 or (heads != D and t.shape[1] > 1):
+        raise ValueError(f"{name}: heads and channels must be contiguous, strides {t.stride()}")
+    return rows
+
+
+def _append_rows(q, k, v, q_out):
+    """Checks of the row arrays and their strides: (Hq, q stride, k stride, v stride)."""
+    T, _, D = k.shape
+    if v.shape != k.shape or v.dtype != k.dtype:
+        raise ValueError("k and v must have one dtype and one shape")
+    ks, vs = _row_stride("k", k, D), _row_stride("v", v, D)
+    if q is None:
+        return 0, 0, ks, vs
+    if q.shape[0] != T or q.dtype != k.dtype or q_out is None or not q_out.is_contiguous():
+        raise ValueError("q must have k's rows and dtype, and q_out must be contiguous")
+    return q.shape[1], _row_stride("q", q, D), ks, vs
 
 
 def eagle_rope_table(max_pos, D, theta, table=None, stream=None):
     """cos and sin of pos * theta^(-2i/D): [max_pos, 2, D/2] fp32 on the current device."""
     if table is None:
         table = torch.empty((max_pos, 2, D // 2), dtype=torch.float32, device="cuda")
-    _check("eagle_rope_table", lib().eagle_rope_table(max_pos, D, float(theta), _addr(table), _raw_stream(stream)))
+    _check("eagle_rope_table", lib().eagle_rope_table(max_pos, D, float(theta), _addr(table),
+                                                      _raw_stream(stream, table.device)))
     return table
 
 
@@ -492,40 +513,36 @@ def eagle_kv_append(q, k, v, rope, cu_seqlens, ctx_lens, block_table, k_cache, v
     the paged cache (see include/eagle.h).  q and q_out may be None, rope None
     for no rotation."""
     T, Hkv, D = k.shape
-    Hq, qs = (0, 0) if q is None else (q.shape[1], _row_stride("q", q, D))
-    if q is not None and (q.shape[0] != T or q.dtype != k.dtype or not q_out.is_contiguous()):
-        raise ValueError("q must have k's rows and dtype, and q_out must be contiguous")
-    if v.shape != k.shape or v.dtype != k.dtype or k_cache.dtype != k.dtype:
-        raise ValueError("k, v and the cache must have one dtype, and k and v one shape")
+    Hq, qs, ks, vs = _append_rows(q, k, v, q_out)
+    if k_cache.dtype != k.dtype or v_cache.dtype != k.dtype:
+        raise ValueError("the cache must have k's dtype")
     _check("eagle_kv_append", lib().eagle_kv_append(
-        _addr(q), k.data_ptr(), v.data_ptr(), qs, _row_stride("k", k, D), _row_stride("v", v, D), _addr(rope),
+        _addr(q), k.data_ptr(), v.data_ptr(), qs, ks, vs, _addr(rope),
         0 if rope is None else rope.shape[0], cu_seqlens.data_ptr(), ctx_lens.data_ptr(), ctx_lens.shape[0], T, Hq,
         Hkv, D, _dtype(k), _addr(q_out), k_cache.data_ptr(), v_cache.data_ptr(), k_cache.shape[0],
-        block_table.data_ptr(), block_table.shape[1], _addr(status), _raw_stream(stream)))
+        block_table.data_ptr(), block_table.shape[1], _addr(status), _raw_stream(stream, k.device)))
 
 
 def eagle_kv_append_kv4(q, k, v, rope, cu_seqlens, ctx_lens, block_table, k_codes, k_scales, v_codes, v_scales,
                         q_out=None, k_scale=1.0, v_scale=1.0, status=None, stream=None):
     """eagle_kv_append into 4-bit pages (see include/eagle.h)."""
     T, Hkv, D = k.shape
-    Hq, qs = (0, 0) if q is None else (q.shape[1], _row_stride("q", q, D))
-    if q is not None and (q.shape[0] != T or q.dtype != k.dtype or not q_out.is_contiguous()):
-        raise ValueError("q must have k's rows and dtype, and q_out must be contiguous")
-    if v.shape != k.shape or v.dtype != k.dtype or k.dtype != torch.bfloat16:
-        raise ValueError("k and v must be bf16 of one shape")
+    Hq, qs, ks, vs = _append_rows(q, k, v, q_out)
+    if k.dtype != torch.bfloat16:
+        raise ValueError("k and v must be bf16")
     _check("eagle_kv_append_kv4", lib().eagle_kv_append_kv4(
-        _addr(q), k.data_ptr(), v.data_ptr(), qs, _row_stride("k", k, D), _row_stride("v", v, D), _addr(rope),
+        _addr(q), k.data_ptr(), v.data_ptr(), qs, ks, vs, _addr(rope),
         0 if rope is None else rope.shape[0], cu_seqlens.data_ptr(), ctx_lens.data_ptr(), ctx_lens.shape[0], T, Hq,
         Hkv, D, _addr(q_out), k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
         k_scale, v_scale, k_codes.shape[0], block_table.data_ptr(), block_table.shape[1], _addr(status),
-        _raw_stream(stream)))
+        _raw_stream(stream, k.device)))
 
 
 def eagle_kv4_read(codes, scales, out, scale=1.0, stream=None):
     """The values of 4-bit pages as an ordinary [pages, 16, Hkv, D] cache."""
     P, Hkv, _, half = codes.shape
     _check("eagle_kv4_read", lib().eagle_kv4_read(codes.data_ptr(), scales.data_ptr(), scale, P, Hkv, 2 * half,
-                                                  _dtype(out), out.data_ptr(), _raw_stream(stream)))
+                                                  _dtype(out), out.data_ptr(), _raw_stream(stream, out.device)))
     return out
 
 
@@ -547,7 +564,7 @@ def eagle_prompt_attn(q, k_cache, v_cache, block_table, cu_seqlens, ctx_lens, ou
         q.data_ptr(), _row_stride("q", q, D), k_cache.data_ptr(), v_cache.data_ptr(), P, block_table.data_ptr(),
         block_table.shape[1], cu_seqlens.data_ptr(), ctx_lens.data_ptr(), out.data_ptr(), _addr(lse), B, T, Hq, Hkv,
         D, page, D ** -0.5 if scale is None else scale, _dtype(q), ws.data_ptr(), ws.numel(), _addr(status),
-        _raw_stream(stream)))
+        _raw_stream(stream, q.device)))
     return out
 
 
@@ -565,7 +582,7 @@ def eagle_prompt_attn_kv4(q, k_codes, k_scales, v_codes, v_scales, block_table, 
         q.data_ptr(), _row_stride("q", q, D), k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
         v_scales.data_ptr(), k_scale, v_scale, P, block_table.data_ptr(), block_table.shape[1],
         cu_seqlens.data_ptr(), ctx_lens.data_ptr(), out.data_ptr(), _addr(lse), B, T, Hq, Hkv, D, page,
-        D ** -0.5 if scale is None else scale, ws.data_ptr(), ws.numel(), _addr(status), _raw_stream(stream)))
+        D ** -0.5 if scale is None else scale, ws.data_ptr(), ws.numel(), _addr(status), _raw_stream(stream, q.device)))
     return out
 
 
@@ -590,5 +607,5 @@ def eagle_draft_prompt(x, weights, rope, cu_seqlens, ctx_lens, k_cache, v_cache,
         _addr(weights["gu"]), _addr(weights["down"]), eps, rope.data_ptr(), rope.shape[0], cu_seqlens.data_ptr(),
         ctx_lens.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scales), _addr(v_scales), k_scale, v_scale,
         k_cache.shape[0], block_table.data_ptr(), block_table.shape[1], out.data_ptr(), B, T, d, Hq, Hkv, D, I, dt,
-        ws.data_ptr(), ws.numel(), _addr(status), _raw_stream(stream)))
+        ws.data_ptr(), ws.numel(), _addr(status), _raw_stream(stream, x.device)))
     return out

@@ -427,13 +427,13 @@ extern "C" int eagle_draft_prompt(const void* x, const void* w_norm1, const void
                                   float v_scale, int num_pages, const int32_t* block_table, int max_pages, void* out,
                                   int B, int T, int d, int Hq, int Hkv, int D, int I, int dtype, void* ws,
                                   size_t ws_bytes, int32_t* dev_status, void* stream) {
-  if (!x || !w_norm1 || !w_qkv || !w_o || !w_norm2 || !w_gu || !w_down || !rope || !cu_seqlens || !ctx_lens ||
-      !k_cache || !v_cache || !block_table || !out)
+  if (!w_norm1 || !w_qkv || !w_o || !w_norm2 || !w_gu || !w_down || !rope || !cu_seqlens || !ctx_lens || !k_cache ||
+      !v_cache || !block_table || (T > 0 && (!x || !out || x == out)))
     return EAGLE_ERR_INVALID_ARG;
   if (dtype != EAGLE_BF16 && dtype != EAGLE_FP32) return EAGLE_ERR_INVALID_ARG;
   const bool bf = dtype == EAGLE_BF16, kv4 = k_scales || v_scales;
   if (kv4 && (!k_scales || !v_scales || !bf)) return EAGLE_ERR_INVALID_ARG;
-  if (!(eps >= 0.f) || x == out || B <= 0 || T < 0 || max_pos <= 0 || num_pages <= 0 || max_pages <= 0)
+  if (!(eps >= 0.f) || B <= 0 || T < 0 || max_pos <= 0 || num_pages <= 0 || max_pages <= 0)
     return EAGLE_ERR_INVALID_ARG;
   if (!prompt_shape_ok(d, Hq, Hkv, D, I) || B > 65535) return EAGLE_ERR_UNSUPPORTED;
   if (!aligned16(rope) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scales) || !aligned16(v_scales))

@@ -253,8 +253,10 @@ __global__ void __launch_bounds__(256)
 int append_check(const AppendParams& p, int D, size_t es) {
   if (p.B <= 0 || p.T < 0 || p.Hq < 0 || p.Hkv <= 0 || p.num_pages <= 0 || p.max_pages <= 0)
     return EAGLE_ERR_INVALID_ARG;
-  if (!p.k || !p.v || !p.kc || !p.vc || !p.cu || !p.ctx || !p.table) return EAGLE_ERR_INVALID_ARG;
-  if ((p.Hq > 0) != (p.q != nullptr) || (p.Hq > 0) != (p.q_out != nullptr)) return EAGLE_ERR_INVALID_ARG;
+  if (!p.kc || !p.vc || !p.cu || !p.ctx || !p.table) return EAGLE_ERR_INVALID_ARG;
+  // (arrays of no rows may have no address)
+  if (p.T > 0 && (!p.k || !p.v || (p.Hq > 0) != (p.q != nullptr) || (p.Hq > 0) != (p.q_out != nullptr)))
+    return EAGLE_ERR_INVALID_ARG;
   if (p.rope && p.max_pos <= 0) return EAGLE_ERR_INVALID_ARG;
   if ((D != 64 && D != 128) || (long long)p.Hq + 2ll * p.Hkv > 1024 || p.num_pages > (1 << 26))
     return EAGLE_ERR_UNSUPPORTED;

@@ -18,6 +18,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "kv4.cuh"
@@ -483,6 +484,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
       "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
       : "memory");
 }
+template <int N, bool INC>
+__device__ __forceinline__ void set_max_regs() {
+  if (INC)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -614,8 +622,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < 4) {
     // ------------------------------------------------------ K/V producers
     // registers move from the copying and issuing warps to the softmax:
-    // 256 x 64 + 256 x 192 = the 512 x 128 of the launch
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    // 256 x 56 + 256 x 200 (4-bit, whose producers convert: 64 and 192) = the
+    // 512 x 128 of the launch
+    set_max_regs<KV4 ? 64 : 56, false>();
     const int tid = threadIdx.x;
     int st = 0;
     uint32_t ph = 0;  // stage and phase of the next tile to be filled
@@ -866,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       cp_async_wait_all();
     }
   } else if (warp < 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    set_max_regs<KV4 ? 64 : 56, false>();
     if (warp < 6) {
       // ------------------------------------------------------- MMA issuers
       // One warp per tile, so that one's waits and commits stand beside the
@@ -1076,7 +1085,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    set_max_regs<KV4 ? 192 : 200, true>();
     const int t = (warp - 8) >> 2, q4 = warp & 3, row = q4 * 32 + lane;
     const uint32_t lane_addr = (uint32_t)(q4 * 32) << 16;
     const uint32_t s_addr = tmem + lane_addr + (uint32_t)(t * kBlk);
@@ -1170,6 +1179,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
             for (int k = 0; k < 64; ++k) {
+              // half of them issued: the other tile's may start to fill the gaps
+              if (k == 32 && !pass && i < n_pass && lane == 0) mbar_arrive(smem_u32(&sb.turn[t ^ 1][q4]));
               float e0, e1;
               unpack2(fma2(pack2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])), sc2, nm2), e0, e1);
               e0 = ex2_approx(e0);
@@ -1185,7 +1196,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             renew = __any_sync(0xffffffffu, mine);
             if (!renew) break;
           }
-          if (i < n_pass && lane == 0) mbar_arrive(smem_u32(&sb.turn[t ^ 1][q4]));
           tmem_st32(s_addr, pk);
           tmem_st32(s_addr + 32u, pk + 32);
           l += l0;
@@ -1997,7 +2007,8 @@ __global__ void __launch_bounds__(256, 1) prompt_attn_f32_kernel(const F32Params
 int attn_check(const AttnParams& p, int D, int page_size, size_t es) {
   if (p.B <= 0 || p.T < 0 || p.Hq <= 0 || p.Hkv <= 0 || p.num_pages <= 0 || p.max_pages <= 0 || p.Hq % p.Hkv)
     return EAGLE_ERR_INVALID_ARG;
-  if (!p.q || !p.kc || !p.vc || !p.table || !p.cu || !p.ctx || !p.out) return EAGLE_ERR_INVALID_ARG;
+  if (!p.kc || !p.vc || !p.table || !p.cu || !p.ctx) return EAGLE_ERR_INVALID_ARG;
+  if (p.T > 0 && (!p.q || !p.out)) return EAGLE_ERR_INVALID_ARG;  // (arrays of no rows may have no address)
   if (!(p.scale > 0.f) || !isfinite(p.scale) || !(p.k_scale > 0.f) || !(p.v_scale > 0.f) || !isfinite(p.k_scale) ||
       !isfinite(p.v_scale))
     return EAGLE_ERR_INVALID_ARG;
@@ -2033,11 +2044,20 @@ int launch_merge(const AttnParams& a, const Shape& sh, const Ws& w, cudaStream_t
   note_launch(3);
   return last_launch_status();
 }
-template <typename K>
-bool allow_smem(K kern, int bytes) {
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess) return true;
-  cudaGetLastError();
-  return false;
+// Opens a kernel's dynamic shared memory, once per device.
+template <auto kern>
+bool allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return false;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return true;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return true;
 }
 
 template <int D, bool KV4>
@@ -2046,7 +2066,7 @@ int attn_launch_tc(const AttnParams& a, void* ws, cudaStream_t s) {
   if (few_rows(a.B, a.T, a.Hq, a.Hkv)) {
     const Shape sh = attn_shape(a.B, a.T, a.Hq, a.Hkv, D, KV4 ? kFew4 : kFew);
     const Ws w = attn_ws(sh, ws);
-    if (!allow_smem(prompt_attn_few_kernel<D, KV4>, CfgFew<D, KV4>::kSmem)) return EAGLE_ERR_CUDA;
+    if (!allow_smem<prompt_attn_few_kernel<D, KV4>>(CfgFew<D, KV4>::kSmem)) return EAGLE_ERR_CUDA;
     launch_plan(a, sh, w, 2, s);
     const FewParams fp = {a, a.scale * a.k_scale * kLog2e, sh.g, sh.rows, w.hdr, &w.hdr->next, w.pieces, w.ml, w.po};
     launch(prompt_attn_few_kernel<D, KV4>, sh.ctas, kFewThreads, CfgFew<D, KV4>::kSmem, s, fp);
@@ -2058,7 +2078,7 @@ int attn_launch_tc(const AttnParams& a, void* ws, cudaStream_t s) {
   if (!KV4 && !make_tmap_3d_bf16(&map_q, a.q, D, (uint64_t)a.Hq, (uint64_t)a.T, (uint64_t)D * 2, (uint64_t)a.q_stride * 2,
                                  64, (uint32_t)sh.g, (uint32_t)sh.tpt))
     return EAGLE_ERR_CUDA;
-  if (!allow_smem(prompt_attn_tc_kernel<D, KV4>, (int)C::kSmem)) return EAGLE_ERR_CUDA;
+  if (!allow_smem<prompt_attn_tc_kernel<D, KV4>>((int)C::kSmem)) return EAGLE_ERR_CUDA;
   launch_plan(a, sh, w, 2, s);
   const MainParams mp = {a, a.scale * a.k_scale * kLog2e, sh.g, sh.tpt, sh.tpu, sh.rows, w.hdr, &w.hdr->next, w.pieces,
                          w.ml, w.po};
@@ -2069,7 +2089,7 @@ template <int D>
 int attn_launch_f32(const AttnParams& a, void* ws, cudaStream_t s) {
   const Shape sh = attn_shape(a.B, a.T, a.Hq, a.Hkv, D, kFp32);
   const Ws w = attn_ws(sh, ws);
-  if (!allow_smem(prompt_attn_f32_kernel<D>, CfgF32<D>::kSmem)) return EAGLE_ERR_CUDA;
+  if (!allow_smem<prompt_attn_f32_kernel<D>>(CfgF32<D>::kSmem)) return EAGLE_ERR_CUDA;
   launch_plan(a, sh, w, 1, s);
   const F32Params fp = {a, a.scale * kLog2e, sh.g, sh.tpu, sh.rows, w.hdr, &w.hdr->next, w.pieces, w.ml, w.po};
   launch(prompt_attn_f32_kernel<D>, sh.ctas, 256, CfgF32<D>::kSmem, s, fp);

@@ -119,3 +119,8 @@ def test_draft_prompt_refusals(L):
         assert call(**kw) == UNSUPPORTED, kw
     assert L.eagle_draft_prompt_workspace_size(2, 5000, 256, 4, 2, 64, 256, 1) > 0
     assert L.eagle_draft_prompt_workspace_size(2, 4, 100, 4, 2, 64, 256, 1) == 0
+
+
+def test_no_rows_need_no_addresses(L):
+    assert append(L, T=0, q=N, k=N, v=N, q_out=N) == OK
+    assert attn(L, T=0, q=N, out=N) == OK
