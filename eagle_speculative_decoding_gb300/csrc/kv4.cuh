@@ -20,17 +20,25 @@ __device__ __forceinline__ uint8_t kv4_scale(float amax) {
 __device__ __forceinline__ float kv4_scale_value(uint8_t s) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(s, __NV_E4M3)));
 }
-// Code of x under the scale s: the magnitude nearest to |x| / s.  The
-// comparisons with s times the midpoints are exact (a midpoint has three
-// significant bits, s four), so no division decides a code; a tie goes to the
-// even code.
-__device__ __forceinline__ uint32_t kv4_code(float x, float s) {
-  const float a = fabsf(x);
-  uint32_t c = 0;
-  if (s > 0.f)
-    c = (a > 0.25f * s) + (a >= 0.75f * s) + (a > 1.25f * s) + (a >= 1.75f * s) + (a > 2.5f * s) + (a >= 3.5f * s) +
-        (a > 5.f * s);
-  return c | (__float_as_uint(x) >> 31 << 3);
+// Codes of eight values under the scale s, the first in the low bits: the
+// magnitude nearest to |x| / s, a tie to the even code (0 if s is 0 or NaN).
+// The rounded quotient decides as the exact one would: a midpoint times s has at
+// most seven significant bits, so an x that is not on it is off by 2^-24 of
+// itself or more, and the quotient then rounds to the same side of the midpoint.
+// (Comparisons with s times the seven midpoints instead: 54 us against 48 us for
+// 8125 rows of 32 + 2 x 8 heads.)
+__device__ __forceinline__ uint32_t kv4_codes(const float* x, float s) {
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = s > 0.f ? __fdiv_rn(x[i], s) : copysignf(0.f, x[i]);
+  uint32_t w;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(w)
+      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+  return w;
 }
 __device__ __forceinline__ float kv4_code_value(uint32_t c) {
   // magnitudes 0, 0.5 (no leading one), then 2^(e-1) (1 + m/2), e = c >> 1

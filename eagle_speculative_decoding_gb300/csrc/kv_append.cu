@@ -84,10 +84,7 @@ __device__ __forceinline__ void store4(const float* x, float inv, bool live, uin
   }
   a = fmax_nan(a, __shfl_xor_sync(0xffffffffu, a, 1));
   const uint8_t sb = kv4_scale(a);
-  const float s = kv4_scale_value(sb);
-  uint32_t w = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w |= kv4_code(y[i], s) << (4 * i);
+  const uint32_t w = kv4_codes(y, kv4_scale_value(sb));
   if (!live) return;
   *reinterpret_cast<uint32_t*>(codes + vec * 4) = w;
   if ((vec & 1) == 0) scales[vec >> 1] = sb;

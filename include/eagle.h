@@ -747,8 +747,7 @@ int eagle_kv_append(const void* q, const void* k, const void* v, long long q_str
  * x = rot(k) or v, unrounded fp32, times the fp32 reciprocal of k_scale or
  * v_scale, and per group of 16 channels:
  *   s = e4m3(min(max|x| / 6, 448)) to nearest even; a NaN makes s NaN
- *   m = the magnitude nearest to |x| / s, ties to the even code (0 if s = 0),
- * decided by exact comparisons of |x| with s times the midpoints.
+ *   m = the magnitude nearest to |x| / s, ties to the even code (0 if s = 0).
  * Errors and limits as eagle_kv_append; k_scale, v_scale finite and > 0. */
 int eagle_kv_append_kv4(const void* q, const void* k, const void* v, long long q_stride,
                         long long k_stride, long long v_stride, const float* rope, int max_pos,
