@@ -18,7 +18,6 @@
 #include <math.h>
 
 #include <algorithm>
-#include <atomic>
 
 #include "common.cuh"
 #include "kv4.cuh"
@@ -56,7 +55,7 @@ struct __align__(16) Cut {  // a cut unit: its pieces are slots slot .. slot + p
   int h, u, slot, pieces, c0, n, pad0, pad1;
 };
 struct PlanHeader {
-  int pieces, cuts, next, pad;
+  int pieces, cuts, next, most;  // most: pieces of the most cut unit
 };
 
 constexpr int kCand = 6;       // candidate cuts of the plan
@@ -114,14 +113,19 @@ constexpr int kPlanThreads = 512;
 // whole warps write.
 __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanParams p) {
   __shared__ unsigned long long s_total;
-  __shared__ int s_longest, s_C[kCand], s_n[kCand], s_cut[kCand], s_hist[32], s_cursor[32], s_c, s_slots, s_cuts;
+  __shared__ int s_longest, s_C[kCand], s_n[kCand], s_cut[kCand], s_hist[32], s_cursor[32], s_c, s_slots, s_cuts, s_most;
   __shared__ int s_c0[kPlanThreads], s_len[kPlanThreads], s_ctx[kPlanThreads], s_end[kPlanThreads], s_warp[kPlanThreads / 32];
+  struct Unit {
+    int at, k, slot, cut, o, u, len, extra;
+  };
+  __shared__ Unit s_unit[kPlanThreads];
+  __shared__ int s_pend[kPlanThreads];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid < 32) s_hist[tid] = 0;
   if (tid < kCand) s_n[tid] = s_cut[tid] = 0;
   if (tid == 0) {
     s_total = 0;
-    s_longest = s_slots = s_cuts = 0;
+    s_longest = s_slots = s_cuts = s_most = 0;
   }
   pdl_wait();
   pdl_trigger();
@@ -162,7 +166,17 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanPar
   const bool once = p.B <= kPlanThreads;
   if (once) load(0, true);
 
-  // f(live, b, c0, n, ctx, u, key blocks): whole warps call it, `live` lanes have a unit
+  // unit i of the loaded requests: its request's place o, its index u there; returns its key blocks
+  auto find = [&](int i, int& o, int& u) -> int {
+    o = 0;  // the first request with s_end > i
+#pragma unroll
+    for (int d = kPlanThreads / 2; d; d >>= 1)
+      if (s_end[o + d - 1] <= i) o += d;
+    const int n = s_len[o];
+    u = i - (s_end[o] - (n + p.tpu - 1) / p.tpu);
+    return (s_ctx[o] + min(n, (u + 1) * p.tpu) + kBlk - 1) / kBlk;
+  };
+  // f(live, key blocks) for every unit: whole warps call it, `live` lanes have one
   auto sweep = [&](bool report, auto&& f) {
 #pragma unroll 1
     for (int base = 0; base < p.B; base += kPlanThreads) {
@@ -173,14 +187,8 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanPar
       const int total = s_end[kPlanThreads - 1];
 #pragma unroll 1
       for (int i0 = warp * 32; i0 < total; i0 += kPlanThreads) {
-        const int i = min(i0 + lane, total - 1);
-        int o = 0;  // the first request with s_end > i
-#pragma unroll
-        for (int d = kPlanThreads / 2; d; d >>= 1)
-          if (s_end[o + d - 1] <= i) o += d;
-        const int n = s_len[o], u = i - (s_end[o] - (n + p.tpu - 1) / p.tpu);
-        const int keys = s_ctx[o] + min(n, (u + 1) * p.tpu);
-        f(i0 + lane < total, base + o, s_c0[o], n, s_ctx[o], u, (keys + kBlk - 1) / kBlk);
+        int o, u;
+        f(i0 + lane < total, find(min(i0 + lane, total - 1), o, u));
       }
     }
   };
@@ -188,7 +196,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanPar
   {
     unsigned sum = 0;  // of this lane's units: below 2^32 key blocks
     int longest = 0;
-    sweep(true, [&](bool live, int, int, int, int, int, int L) {
+    sweep(true, [&](bool live, int L) {
       if (!live) return;
       sum += (unsigned)L;
       longest = max(longest, L);
@@ -218,7 +226,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanPar
       C[x] = s_C[x];
       n[x] = cut[x] = 0;
     }
-    sweep(false, [&](bool live, int, int, int, int, int, int L) {
+    sweep(false, [&](bool live, int L) {
       if (!live) return;
 #pragma unroll
       for (int x = 0; x < kCand; ++x) {
@@ -257,7 +265,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanPar
   const int C = s_c, top = max(1, min(longest, C));
   const float per_class = 32.f / (float)top;
   auto klass = [&](int len) { return 31 - min(31, (int)((float)(len - 1) * per_class)); };  // 0: the longest
-  sweep(false, [&](bool live, int, int, int, int, int, int L) {
+  sweep(false, [&](bool live, int L) {
     if (!live) return;
     const int k = L > C ? (L + C - 1) / C : 1;
     atomicAdd(&s_hist[klass((L + k - 1) / k)], k * p.Hkv);
@@ -280,45 +288,66 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanPar
     }
   }
   __syncthreads();
-  sweep(false, [&](bool live, int b, int c0, int n, int ctx, int u, int L) {
-    int k = 1, at = 0, slot = -1, cut = 0, len = L, extra = 0;  // the first `extra` pieces have len + 1 blocks
-    if (live) {
-      if (L > C) {
-        k = (L + C - 1) / C;
-        len = L / k;
-        extra = L - len * k;
-      }
-      at = atomicAdd(&s_cursor[klass((L + k - 1) / k)], k * p.Hkv);
-      if (k > 1) {
-        slot = atomicAdd(&s_slots, k * p.Hkv);
-        cut = atomicAdd(&s_cuts, p.Hkv);
-      }
-    }
-    auto put = [&](int j, int kk, int oat, int oslot, int ocut, int ob, int oc0, int on, int octx, int ou, int olen,
-                   int oextra) {
-      const int h = kk > 1 ? j / kk : j, x = j - h * kk, k0 = x * olen + min(x, oextra);
-      if (oat + j < p.cap_pieces)
-        p.pieces[oat + j] = Piece{ob, h, ou, k0, k0 + olen + (x < oextra ? 1 : 0), kk > 1 ? oslot + j : -1, oc0, on, octx,
-                                  0, 0, 0};
-      if (kk > 1 && x == 0) p.cuts[ocut + h] = Cut{h, ou, oslot + j, kk, oc0, on, 0, 0};
-    };
-    const int mine = live ? k * p.Hkv : 0;
-    if (__reduce_max_sync(0xffffffffu, (unsigned)mine) <= 16) {
-      for (int j = 0; j < mine; ++j) put(j, k, at, slot, cut, b, c0, n, ctx, u, len, extra);
-      return;
-    }
-    // many pieces each: the warp writes its lanes' units one after another
+  // the list: 512 units at a time into shared memory, then their pieces over
+  // all threads, each finding its unit by bisection
 #pragma unroll 1
-    for (unsigned left = __ballot_sync(0xffffffffu, live); left; left &= left - 1) {
-      const int o = __ffs(left) - 1;
-      auto of = [&](int v) { return __shfl_sync(0xffffffffu, v, o); };
-      const int kk = of(k), oat = of(at), oslot = of(slot), ocut = of(cut), ob = of(b), oc0 = of(c0), on = of(n);
-      const int octx = of(ctx), ou = of(u), olen = of(len), oextra = of(extra);
-      for (int j = lane; j < kk * p.Hkv; j += 32) put(j, kk, oat, oslot, ocut, ob, oc0, on, octx, ou, olen, oextra);
+  for (int base = 0; base < p.B; base += kPlanThreads) {
+    if (!once) {
+      __syncthreads();
+      load(base, false);
     }
-  });
+    const int total = s_end[kPlanThreads - 1];
+#pragma unroll 1
+    for (int i0 = 0; i0 < total; i0 += kPlanThreads) {
+      int k = 0;
+      if (i0 + tid < total) {
+        int o, u;
+        const int L = find(i0 + tid, o, u);
+        k = 1;
+        int slot = -1, cut = 0, len = L, extra = 0;  // the first `extra` pieces have len + 1 blocks
+        if (L > C) {
+          k = (L + C - 1) / C;
+          len = L / k;
+          extra = L - len * k;
+          slot = atomicAdd(&s_slots, k * p.Hkv);
+          cut = atomicAdd(&s_cuts, p.Hkv);
+          atomicMax(&s_most, k);
+        }
+        s_unit[tid] = Unit{atomicAdd(&s_cursor[klass((L + k - 1) / k)], k * p.Hkv), k, slot, cut, o, u, len, extra};
+      }
+      int end = k * p.Hkv;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, end, d);
+        if (lane >= d) end += x;
+      }
+      if (lane == 31) s_warp[warp] = end;
+      __syncthreads();
+      const int before = (int)__reduce_add_sync(0xffffffffu, (unsigned)(lane < warp ? s_warp[lane] : 0));
+      s_pend[tid] = end + before;
+      __syncthreads();
+      const int pieces = s_pend[kPlanThreads - 1];
+      for (int q = tid; q < pieces; q += kPlanThreads) {
+        int i = 0;  // the first unit with s_pend > q
+#pragma unroll
+        for (int d = kPlanThreads / 2; d; d >>= 1)
+          if (s_pend[i + d - 1] <= q) i += d;
+        const Unit w = s_unit[i];
+        const int j = q - (s_pend[i] - w.k * p.Hkv), h = w.k > 1 ? j / w.k : j, x = j - h * w.k;
+        const int k0 = x * w.len + min(x, w.extra), c0 = s_c0[w.o], n = s_len[w.o];
+        if (w.at + j < p.cap_pieces)
+          p.pieces[w.at + j] = Piece{base + w.o, h, w.u, k0, k0 + w.len + (x < w.extra ? 1 : 0), w.k > 1 ? w.slot + j : -1,
+                                     c0, n, s_ctx[w.o], 0, 0, 0};
+        if (w.k > 1 && x == 0) p.cuts[w.cut + h] = Cut{h, w.u, w.slot + j, w.k, c0, n, 0, 0};
+      }
+      __syncthreads();
+    }
+  }
   __syncthreads();
-  if (tid == 0) p.hdr->cuts = s_cuts;
+  if (tid == 0) {
+    p.hdr->cuts = s_cuts;
+    p.hdr->most = s_most;
+  }
 }
 
 // ------------------------------------------------------------------- main
@@ -1315,7 +1344,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------ merge
 // out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s over the pieces s of a
-// cut unit, a warp per row.
+// cut unit.  A CTA takes eight rows, a warp each, or, of a unit with many pieces,
+// one row with all its warps.
 struct MergeParams {
   const PlanHeader* hdr;
   const Cut* cuts;
@@ -1329,22 +1359,28 @@ struct MergeParams {
 template <int D, bool F32>
 __global__ void __launch_bounds__(256) prompt_merge_kernel(const MergeParams p) {
   constexpr int E = D / 32;
+  __shared__ float s_o[8][D], s_l[8];
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, warps = gridDim.x * 8;
-  const long long items = (long long)p.hdr->cuts * p.slot_rows;
-  for (long long it = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); it < items; it += warps) {
-    const Cut c = p.cuts[it / p.slot_rows];
-    const int r = (int)(it % p.slot_rows), tok = c.u * p.tpu + r / p.g;
-    if (r >= p.tpu * p.g || tok >= c.n) continue;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, groups = (p.slot_rows + 7) / 8;
+  const int per = p.hdr->most > 8 ? 8 : 1;  // items per eight rows
+  const long long items = (long long)p.hdr->cuts * groups * per;
+  for (long long it = blockIdx.x; it < items; it += gridDim.x) {
+    const int i = (int)(it / per), y = (int)(it % per);
+    const Cut c = p.cuts[i / groups];
+    const bool shared = c.pieces > 8;  // the warps share row y's pieces
+    if (!shared && y) continue;
+    const int r = i % groups * 8 + (shared ? y : warp), tok = c.u * p.tpu + r / p.g;
+    if (r >= min(min(p.tpu, c.n - c.u * p.tpu) * p.g, p.slot_rows)) continue;  // shared: the whole CTA
     const size_t row0 = (size_t)c.slot * p.slot_rows + r;
     float M = -INFINITY;
     for (int s = lane; s < c.pieces; s += 32) M = fmaxf(M, p.ml[row0 + (size_t)s * p.slot_rows].x);
 #pragma unroll
     for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
     float l = 0.f, o[E] = {};
+    const int step = shared ? 8 : 1;
 #pragma unroll 4
-    for (int s = 0; s < c.pieces; ++s) {
+    for (int s = shared ? warp : 0; s < c.pieces; s += step) {
       const size_t row = row0 + (size_t)s * p.slot_rows;
       const float2 x = p.ml[row];
       const float w = M == -INFINITY ? 1.f : ex2_approx(x.x - M);
@@ -1356,6 +1392,21 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const MergeParams p) 
         *reinterpret_cast<float2*>(f) = *reinterpret_cast<const float2*>(p.o + row * D + lane * 2);
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] = fmaf(w, f[e], o[e]);
+    }
+    if (shared) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
+      if (lane == 0) s_l[warp] = l;
+      __syncthreads();
+      if (warp == 0) {
+        for (int x = 1; x < 8; ++x) {
+          l += s_l[x];
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] += s_o[x][lane * E + e];
+        }
+      }
+      __syncthreads();
+      if (warp != 0) continue;
     }
     const float inv = l == 0.f ? 0.f : p.v_scale / l;
     const size_t orow = ((size_t)c.c0 + tok) * p.Hq + c.h * p.g + r % p.g;
@@ -2044,20 +2095,11 @@ int launch_merge(const AttnParams& a, const Shape& sh, const Ws& w, cudaStream_t
   note_launch(3);
   return last_launch_status();
 }
-// Opens a kernel's dynamic shared memory, once per device.
-template <auto kern>
-bool allow_smem(int bytes) {
-  static std::atomic<uint64_t> done{0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return false;
-  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-  if (done.load(std::memory_order_relaxed) & bit) return true;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
-    cudaGetLastError();
-    return false;
-  }
-  done.fetch_or(bit, std::memory_order_relaxed);
-  return true;
+template <typename K>
+bool allow_smem(K kern, int bytes) {
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess) return true;
+  cudaGetLastError();
+  return false;
 }
 
 template <int D, bool KV4>
@@ -2066,7 +2108,7 @@ int attn_launch_tc(const AttnParams& a, void* ws, cudaStream_t s) {
   if (few_rows(a.B, a.T, a.Hq, a.Hkv)) {
     const Shape sh = attn_shape(a.B, a.T, a.Hq, a.Hkv, D, KV4 ? kFew4 : kFew);
     const Ws w = attn_ws(sh, ws);
-    if (!allow_smem<prompt_attn_few_kernel<D, KV4>>(CfgFew<D, KV4>::kSmem)) return EAGLE_ERR_CUDA;
+    if (!allow_smem(prompt_attn_few_kernel<D, KV4>, CfgFew<D, KV4>::kSmem)) return EAGLE_ERR_CUDA;
     launch_plan(a, sh, w, 2, s);
     const FewParams fp = {a, a.scale * a.k_scale * kLog2e, sh.g, sh.rows, w.hdr, &w.hdr->next, w.pieces, w.ml, w.po};
     launch(prompt_attn_few_kernel<D, KV4>, sh.ctas, kFewThreads, CfgFew<D, KV4>::kSmem, s, fp);
@@ -2078,7 +2120,7 @@ int attn_launch_tc(const AttnParams& a, void* ws, cudaStream_t s) {
   if (!KV4 && !make_tmap_3d_bf16(&map_q, a.q, D, (uint64_t)a.Hq, (uint64_t)a.T, (uint64_t)D * 2, (uint64_t)a.q_stride * 2,
                                  64, (uint32_t)sh.g, (uint32_t)sh.tpt))
     return EAGLE_ERR_CUDA;
-  if (!allow_smem<prompt_attn_tc_kernel<D, KV4>>((int)C::kSmem)) return EAGLE_ERR_CUDA;
+  if (!allow_smem(prompt_attn_tc_kernel<D, KV4>, (int)C::kSmem)) return EAGLE_ERR_CUDA;
   launch_plan(a, sh, w, 2, s);
   const MainParams mp = {a, a.scale * a.k_scale * kLog2e, sh.g, sh.tpt, sh.tpu, sh.rows, w.hdr, &w.hdr->next, w.pieces,
                          w.ml, w.po};
@@ -2089,7 +2131,7 @@ template <int D>
 int attn_launch_f32(const AttnParams& a, void* ws, cudaStream_t s) {
   const Shape sh = attn_shape(a.B, a.T, a.Hq, a.Hkv, D, kFp32);
   const Ws w = attn_ws(sh, ws);
-  if (!allow_smem<prompt_attn_f32_kernel<D>>(CfgF32<D>::kSmem)) return EAGLE_ERR_CUDA;
+  if (!allow_smem(prompt_attn_f32_kernel<D>, CfgF32<D>::kSmem)) return EAGLE_ERR_CUDA;
   launch_plan(a, sh, w, 1, s);
   const F32Params fp = {a, a.scale * kLog2e, sh.g, sh.tpu, sh.rows, w.hdr, &w.hdr->next, w.pieces, w.ml, w.po};
   launch(prompt_attn_f32_kernel<D>, sh.ctas, 256, CfgF32<D>::kSmem, s, fp);
