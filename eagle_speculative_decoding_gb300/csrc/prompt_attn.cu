@@ -69,6 +69,8 @@ struct Shape {
   int ctas, cap_units, cap_pieces, cap_slots;
   size_t off_pieces, off_cuts, off_ml, off_o, total;
 };
+// CTAs per SM of the few-rows kernel with NG groups of eight rows
+constexpr int few_ctas(bool kv4, int ng) { return kv4 ? (ng == 1 ? 4 : 3) : 2; }
 enum Path { kTensor, kFew, kFew4, kFp32 };
 Shape attn_shape(int B, int T, int Hq, int Hkv, int D, Path path) {
   Shape s;
@@ -77,7 +79,7 @@ Shape attn_shape(int B, int T, int Hq, int Hkv, int D, Path path) {
   s.tpu = path == kTensor ? 2 * s.tpt : s.tpt;
   s.rows = std::min(s.tpu, T) * s.g;
   const int sms = sm_count();
-  s.ctas = (sms > 0 ? sms : 152) * (path == kFew4 ? 3 : path == kFew ? 2 : 1);
+  s.ctas = (sms > 0 ? sms : 152) * (path == kFew4 || path == kFew ? few_ctas(path == kFew4, s.g > 8 ? 2 : 1) : 1);
   s.cap_units = T / s.tpu + std::min(B, T);
   // a unit of L > C blocks makes ceil(L / C) < 2 L / C pieces and the finest C
   // is total / (kMaxShare * ctas)
@@ -1443,7 +1445,6 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const MergeParams p) 
 //   V (B operand of O = P V): keys 2t, 2t + 1, 2t + 8, 2t + 9; 16-bit: loads
 //     i = 0 .. D/64 - 1 at channel 64 i + 8 j; 4-bit: D/8 channels at j D/8
 constexpr int kFewThreads = 128;
-constexpr int kFewRows = 16;
 
 struct FewParams {
   AttnParams a;
@@ -1457,15 +1458,22 @@ struct FewParams {
 };
 
 template <bool F16>
-__device__ __forceinline__ void mma_16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_16816(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
   if (F16)
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The transposed 8 x 8 of 16-bit elements (a lane holds elements 2 (lane % 4),
+// + 1 of row lane / 4).
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %0;" : "+r"(v));
+  return v;
 }
 // Eight 4-bit codes as four fp16 pairs times the pair `s`.
 __device__ __forceinline__ void kv4_expand(uint32_t w, uint32_t s, uint32_t* v) {
@@ -1484,26 +1492,26 @@ __device__ __forceinline__ uint32_t e4m3_pair_as_f16(uint32_t two) {
   return s2;
 }
 
-template <int D, bool KV4>
+template <int D, bool KV4, int NG>
 struct CfgFew {
-  // CTAs per SM; pages per step (their chains of latencies run side by side)
-  static constexpr int kCtas = KV4 ? 3 : 2, NP = KV4 ? 2 : 1;
+  // pages per step (their chains of latencies run side by side)
+  static constexpr int NP = KV4 ? 2 : 1, kRows = 8 * NG;
   // 4-bit: steps in flight per warp, copied to shared memory (2.3 KB a page:
   // held in registers, three pages a warp left the loads' latency exposed)
   static constexpr int kRing = 3;
   static constexpr int kCodes = 16 * D / 2, kPage = 2 * (kCodes + D);  // bytes: K and V codes, K and V scales
-  static constexpr int kJoin = 4 * kFewRows * (D * 4 + 8);             // the warps' O, m and l at the end (over the ring)
+  static constexpr int kJoin = 4 * kRows * (D * 4 + 8);             // the warps' O, m and l at the end (over the ring)
   static constexpr int kSmem = KV4 && 4 * kRing * NP * kPage > kJoin ? 4 * kRing * NP * kPage : kJoin;
 };
-template <int D, bool KV4>
-__global__ void __launch_bounds__(kFewThreads, (CfgFew<D, KV4>::kCtas)) prompt_attn_few_kernel(const FewParams p) {
-  using C = CfgFew<D, KV4>;
-  constexpr int KS = D / 16, NT = D / 8;  // k steps of S, 8-column tiles of O
+template <int D, bool KV4, int NG>
+__global__ void __launch_bounds__(kFewThreads, few_ctas(KV4, NG)) prompt_attn_few_kernel(const FewParams p) {
+  using C = CfgFew<D, KV4, NG>;
+  constexpr int KS = D / 16, NT = D / 16;  // k steps of S, 16-channel tiles of O
   constexpr int KW = KV4 ? D / 32 : D / 8;   // 32-bit words of K per key and lane
   constexpr int VW = KV4 ? D / 64 : D / 16;  // of V
-  constexpr int NP = C::NP;
-  extern __shared__ __align__(16) float fm[];  // [4 warps][16 rows][D], then [4][16] (m, l)
-  float2* s_ml = reinterpret_cast<float2*>(fm + 4 * kFewRows * D);
+  constexpr int NP = C::NP, R = C::kRows;
+  extern __shared__ __align__(16) float fm[];  // [4 warps][R rows][D], then [4][R] (m, l)
+  float2* s_ml = reinterpret_cast<float2*>(fm + 4 * R * D);
   __shared__ int s_piece;
   pdl_wait();
   pdl_trigger();
@@ -1518,49 +1526,47 @@ __global__ void __launch_bounds__(kFewThreads, (CfgFew<D, KV4>::kCtas)) prompt_a
     const int tok = w.c0 + w.u, pos = w.ctx + w.u, n_keys = pos + 1;
     const int lim = min(n_keys, w.k1 * kBlk), page_end = (lim + 15) / 16;  // the piece's keys end at lim
     const int32_t* tab = a.table + (size_t)w.b * a.max_pages;
-    // Q as the A operand of each k step, the lane's two rows j and j + 8
-    uint32_t q[KS][4];
-    float fac[2] = {p.scale_log2, p.scale_log2};
-    {
-      uint32_t raw[2][D / 8];
+    // Q as the B operand of each k step: rows j of the NG groups
+    uint32_t q[NG][D / 8];
+    float fac[NG][2];  // of rows 2 t, 2 t + 1 of each group
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int row = j + 8 * r;
-        const __nv_bfloat16* src =
-            static_cast<const __nv_bfloat16*>(a.q) + (size_t)tok * a.q_stride + (size_t)(w.h * p.g + row) * D;
+    for (int n = 0; n < NG; ++n) {
+      const int row = j + 8 * n;
+      const __nv_bfloat16* src =
+          static_cast<const __nv_bfloat16*>(a.q) + (size_t)tok * a.q_stride + (size_t)(w.h * p.g + row) * D;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          // 16-bit: channels 32 i + 8 t ..; 4-bit: t D/4 + 8 i ..
-          const uint4 v = row < p.g ? *reinterpret_cast<const uint4*>(src + (KV4 ? t * (D / 4) + 8 * i : 32 * i + 8 * t))
-                                    : make_uint4(0u, 0u, 0u, 0u);
-          raw[r][4 * i] = v.x, raw[r][4 * i + 1] = v.y, raw[r][4 * i + 2] = v.z, raw[r][4 * i + 3] = v.w;
-        }
-        if constexpr (KV4) {
-          // fp16, scaled by a power of two to [1, 2) at the row's largest
-          uint32_t mx = 0;
+      for (int i = 0; i < D / 32; ++i) {
+        // 16-bit: channels 32 i + 8 t ..; 4-bit: t D/4 + 8 i ..
+        const uint4 v = row < p.g ? *reinterpret_cast<const uint4*>(src + (KV4 ? t * (D / 4) + 8 * i : 32 * i + 8 * t))
+                                  : make_uint4(0u, 0u, 0u, 0u);
+        q[n][4 * i] = v.x, q[n][4 * i + 1] = v.y, q[n][4 * i + 2] = v.z, q[n][4 * i + 3] = v.w;
+      }
+      float up = p.scale_log2;
+      if constexpr (KV4) {
+        // fp16, scaled by a power of two to [1, 2) at the row's largest
+        uint32_t mx = 0;
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) mx = max(mx, max(raw[r][i] & 0x7fffu, (raw[r][i] >> 16) & 0x7fffu));
-          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const int k2 = min(126, max(-126, (int)(mx >> 7) - 127));
-          const float down = __uint_as_float((uint32_t)(127 - k2) << 23);
-          fac[r] *= __uint_as_float((uint32_t)(127 + k2) << 23);
+        for (int i = 0; i < D / 8; ++i) mx = max(mx, max(q[n][i] & 0x7fffu, (q[n][i] >> 16) & 0x7fffu));
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const int k2 = min(126, max(-126, (int)(mx >> 7) - 127));
+        const float down = __uint_as_float((uint32_t)(127 - k2) << 23);
+        up *= __uint_as_float((uint32_t)(127 + k2) << 23);
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i)
-            raw[r][i] = pack16<true>(__uint_as_float(raw[r][i] << 16) * down, __uint_as_float(raw[r][i] & 0xffff0000u) * down);
-        }
+        for (int i = 0; i < D / 8; ++i)
+          q[n][i] = pack16<true>(__uint_as_float(q[n][i] << 16) * down, __uint_as_float(q[n][i] & 0xffff0000u) * down);
       }
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        q[s][0] = raw[0][2 * s];
-        q[s][1] = raw[1][2 * s];
-        q[s][2] = raw[0][2 * s + 1];
-        q[s][3] = raw[1][2 * s + 1];
-      }
+      for (int e = 0; e < 2; ++e) fac[n][e] = __shfl_sync(0xffffffffu, up, 4 * (2 * t + e));
     }
-    float o[NT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float o[NG][NT][4], m[NG][2], l[NG][2];  // row 2 t + e of group n: o[n][..][e], o[n][..][2 + e]
 #pragma unroll
-    for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    for (int n = 0; n < NG; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
+    }
 
     struct Page {
       uint32_t k[2][KW], v[4][VW];
@@ -1633,114 +1639,142 @@ __global__ void __launch_bounds__(kFewThreads, (CfgFew<D, KV4>::kCtas)) prompt_a
     // the step of pages i .. i + NP - 1
     auto use = [&](const Page* pg, const unsigned char* raw, int i) {
       const bool tail = (page0 + 4 * (i + NP - 1)) * 16 + 16 > lim;
-      float s[NP][2][4];
+      float s[NP][NG][4];  // s[z][n][2 x + e]: key j + 8 x of page z, row 2 t + e of group n
 #pragma unroll
-      for (int z = 0; z < NP; ++z)
+      for (int z = 0; z < NP; ++z) {
+        float part[NG][2][4] = {};  // two chains of MMAs each
+        if constexpr (KV4) {
+          const unsigned char* pr = raw + z * C::kPage;
+          uint32_t kw[2][KW], sl[2], sh[2];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float part[2][4] = {};  // two chains of MMAs
-          if constexpr (KV4) {
-            const unsigned char* pr = raw + z * C::kPage;
+          for (int x = 0; x < 2; ++x) {
             const int r = j + 8 * x;
-            uint32_t kw[KW], sb;
+            uint32_t sb;
             if constexpr (D == 128) {
               const uint4 v = *reinterpret_cast<const uint4*>(pr + r * 64 + t * 16);
-              kw[0] = v.x, kw[1] = v.y, kw[2] = v.z, kw[3] = v.w;
+              kw[x][0] = v.x, kw[x][1] = v.y, kw[x][2] = v.z, kw[x][3] = v.w;
               sb = *reinterpret_cast<const uint16_t*>(pr + 2 * C::kCodes + r * 8 + 2 * t);
             } else {
               const uint2 v = *reinterpret_cast<const uint2*>(pr + r * 32 + t * 8);
-              kw[0] = v.x, kw[1] = v.y;
+              kw[x][0] = v.x, kw[x][1] = v.y;
               sb = pr[2 * C::kCodes + r * 4 + t] * 0x101u;
             }
             // (a dead key's score is masked below, whatever its scale)
             const uint32_t s2 = e4m3_pair_as_f16(sb);
-            const uint32_t sl = __byte_perm(s2, s2, 0x1010), sh = __byte_perm(s2, s2, 0x3232);
-#pragma unroll
-            for (int y = 0; y < KW; ++y) {
-              uint32_t e[4];
-              kv4_expand(kw[y], y < KW / 2 ? sl : sh, e);
-              mma_16816<true>(part[0], q[2 * y], e[0], e[1]);
-              mma_16816<true>(part[1], q[2 * y + 1], e[2], e[3]);
-            }
-          } else {
-#pragma unroll
-            for (int y = 0; y < KS; ++y) mma_16816<false>(part[y & 1], q[y], pg[z].k[x][2 * y], pg[z].k[x][2 * y + 1]);
+            sl[x] = __byte_perm(s2, s2, 0x1010), sh[x] = __byte_perm(s2, s2, 0x3232);
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[z][x][e] = part[0][e] + part[1][e];
+          for (int y = 0; y < KW; ++y) {
+            uint32_t e[2][4];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) kv4_expand(kw[x][y], y < KW / 2 ? sl[x] : sh[x], e[x]);
+#pragma unroll
+            for (int n = 0; n < NG; ++n)
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+                mma_16816<true>(part[n][c], e[0][2 * c], e[1][2 * c], e[0][2 * c + 1], e[1][2 * c + 1], q[n][4 * y + 2 * c],
+                                q[n][4 * y + 2 * c + 1]);
+          }
+        } else {
+#pragma unroll
+          for (int y = 0; y < KS; ++y)
+#pragma unroll
+            for (int n = 0; n < NG; ++n)
+              mma_16816<false>(part[n][y & 1], pg[z].k[0][2 * y], pg[z].k[1][2 * y], pg[z].k[0][2 * y + 1],
+                               pg[z].k[1][2 * y + 1], q[n][2 * y], q[n][2 * y + 1]);
         }
-      // s[z][x][2 r + e]: row j + 8 r, key 8 x + 2 t + e of page z
+#pragma unroll
+        for (int n = 0; n < NG; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[z][n][e] = part[n][0][e] + part[n][1][e];
+      }
       if (tail) {
 #pragma unroll
         for (int z = 0; z < NP; ++z)
 #pragma unroll
-          for (int x = 0; x < 2; ++x)
+          for (int n = 0; n < NG; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if ((page0 + 4 * (i + z)) * 16 + 8 * x + 2 * t + (e & 1) >= lim) s[z][x][e] = -INFINITY;
+              if ((page0 + 4 * (i + z)) * 16 + 8 * (e >> 1) + j >= lim) s[z][n][e] = -INFINITY;
       }
       // the reference of a row is the maximum of the first step; it is renewed
       // when a step's weights pass kSumLimit (or are NaN), see the kernel above
-      float wt[NP][2][4];
-      bool renew = i == 0, mine[2] = {true, true};  // by row, the same in its four lanes
+      float wt[NP][NG][4];
+      bool renew = i == 0, mine[NG][2];  // by row, the same in its eight lanes
+#pragma unroll
+      for (int n = 0; n < NG; ++n) mine[n][0] = mine[n][1] = true;
 #pragma unroll 1
       for (int pass = 0;; ++pass) {
         if (renew) {
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            float bm = -INFINITY;
+          for (int n = 0; n < NG; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float bm = -INFINITY;
+#pragma unroll
+              for (int z = 0; z < NP; ++z) bm = fmaxf(bm, fmaxf(s[z][n][e], s[z][n][2 + e]));
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, d));
+              bm *= fac[n][e];
+              if (mine[n][e] && bm > m[n][e]) {
+                if (m[n][e] != -INFINITY) {
+                  const float alpha = ex2_approx(m[n][e] - bm);
+                  l[n][e] *= alpha;
+#pragma unroll
+                  for (int y = 0; y < NT; ++y) {
+                    o[n][y][e] *= alpha;
+                    o[n][y][2 + e] *= alpha;
+                  }
+                }
+                m[n][e] = bm;
+              }
+            }
+        }
+        float sum[NG][2];
+        bool over = false;
+#pragma unroll
+        for (int n = 0; n < NG; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float ref = m[n][e] == -INFINITY ? 0.f : -m[n][e];
+            sum[n][e] = 0.f;
 #pragma unroll
             for (int z = 0; z < NP; ++z)
-              bm = fmaxf(bm, fmaxf(fmaxf(s[z][0][2 * r], s[z][0][2 * r + 1]), fmaxf(s[z][1][2 * r], s[z][1][2 * r + 1])));
-            bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 1));
-            bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 2)) * fac[r];
-            if (mine[r] && bm > m[r]) {
-              const float alpha = m[r] == -INFINITY ? 0.f : ex2_approx(m[r] - bm);
-              l[r] *= alpha;
-              if (m[r] != -INFINITY) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                  o[n][2 * r] *= alpha;
-                  o[n][2 * r + 1] *= alpha;
-                }
+              for (int x = 0; x < 2; ++x) {
+                const float f = ex2_approx(fmaf(s[z][n][2 * x + e], fac[n][e], ref));
+                wt[z][n][2 * x + e] = f;
+                sum[n][e] += f;
               }
-              m[r] = bm;
-            }
+            over = over || !(sum[n][e] <= kSumLimit);
           }
-        }
-        float sum[2] = {0.f, 0.f};
+        if (pass || !__any_sync(0xffffffffu, over)) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float ref = m[r] == -INFINITY ? 0.f : -m[r];
-#pragma unroll
-          for (int z = 0; z < NP; ++z)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const float e0 = ex2_approx(fmaf(s[z][x][2 * r], fac[r], ref));
-              const float e1 = ex2_approx(fmaf(s[z][x][2 * r + 1], fac[r], ref));
-              wt[z][x][2 * r] = e0;
-              wt[z][x][2 * r + 1] = e1;
-              sum[r] += e0 + e1;
-            }
-        }
-        const bool over0 = !(sum[0] <= kSumLimit), over1 = !(sum[1] <= kSumLimit);
-        if (pass || !__any_sync(0xffffffffu, over0 || over1)) {
-          l[0] += sum[0];
-          l[1] += sum[1];
+          for (int n = 0; n < NG; ++n) {
+            l[n][0] += sum[n][0];
+            l[n][1] += sum[n][1];
+          }
           break;
         }
         renew = true;
-        mine[0] = (__ballot_sync(0xffffffffu, over0) >> (lane & 28) & 15u) != 0;
-        mine[1] = (__ballot_sync(0xffffffffu, over1) >> (lane & 28) & 15u) != 0;
+#pragma unroll
+        for (int n = 0; n < NG; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            mine[n][e] = (__ballot_sync(0xffffffffu, !(sum[n][e] <= kSumLimit)) >> t & 0x11111111u) != 0;
       }
 #pragma unroll
       for (int z = 0; z < NP; ++z) {
-        const uint32_t pa[4] = {pack16<KV4>(wt[z][0][0], wt[z][0][1]), pack16<KV4>(wt[z][0][2], wt[z][0][3]),
-                                pack16<KV4>(wt[z][1][0], wt[z][1][1]), pack16<KV4>(wt[z][1][2], wt[z][1][3])};
+        uint32_t pb[NG][2];  // the weights as the B operand: keys 2 t, 2 t + 1 (+ 8) of row j
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+          pb[n][0] = transpose8(pack16<KV4>(wt[z][n][0], wt[z][n][1]));
+          pb[n][1] = transpose8(pack16<KV4>(wt[z][n][2], wt[z][n][3]));
+        }
         // V: pairs of keys (2t, 2t + 1) and (2t + 8, 2t + 9) of each channel
         if constexpr (KV4) {
           const unsigned char* pr = raw + z * C::kPage;
-          uint32_t vw[4][VW], vs[4], sc[4];
+          uint32_t vw[4][VW], vs[4], sc[2];
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const int r = 2 * t + (x & 1) + 8 * (x >> 1), at = (r >> 1) & (D / 32 - 1);
@@ -1755,33 +1789,35 @@ __global__ void __launch_bounds__(kFewThreads, (CfgFew<D, KV4>::kCtas)) prompt_a
             // a dead key's scale may be anything; its codes are zeros
             if (tail && (page0 + 4 * (i + z)) * 16 + r >= lim) vs[x] = 0;
           }
-          const uint32_t s01 = e4m3_pair_as_f16(vs[0] | vs[1] << 8);
-          const uint32_t s23 = e4m3_pair_as_f16(vs[2] | vs[3] << 8);
-          sc[0] = __byte_perm(s01, s01, 0x1010), sc[1] = __byte_perm(s01, s01, 0x3232);
-          sc[2] = __byte_perm(s23, s23, 0x1010), sc[3] = __byte_perm(s23, s23, 0x3232);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) sc[x] = e4m3_pair_as_f16(vs[2 * x] | vs[2 * x + 1] << 8);
 #pragma unroll
           for (int y = 0; y < VW; ++y) {
-            uint32_t e[4][4];
+            uint32_t e[2][2][4];  // [pair of keys][channel's parity]
 #pragma unroll
-            for (int x = 0; x < 4; ++x) kv4_expand(vw[x][y], sc[x], e[x]);
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t lo = vw[2 * x][y], hi = vw[2 * x + 1][y];  // a byte: the pair's codes of one channel
+              kv4_expand((lo & 0x0f0f0f0fu) | (hi << 4 & 0xf0f0f0f0u), sc[x], e[x][0]);
+              kv4_expand((lo >> 4 & 0x0f0f0f0fu) | (hi & 0xf0f0f0f0u), sc[x], e[x][1]);
+            }
 #pragma unroll
             for (int c = 0; c < 4; ++c)
 #pragma unroll
-              for (int hl = 0; hl < 2; ++hl) {
-                const uint32_t sel = hl ? 0x7632u : 0x5410u;
-                mma_16816<true>(o[8 * y + 2 * c + hl], pa, __byte_perm(e[0][c], e[1][c], sel),
-                                __byte_perm(e[2][c], e[3][c], sel));
-              }
+              for (int n = 0; n < NG; ++n)
+                mma_16816<true>(o[n][4 * y + c], e[0][0][c], e[0][1][c], e[1][0][c], e[1][1][c], pb[n][0], pb[n][1]);
           }
         } else {
 #pragma unroll
-          for (int y = 0; y < VW; ++y)
+          for (int y = 0; y < VW; ++y) {
+            uint32_t e[2][2];
 #pragma unroll
-            for (int hl = 0; hl < 2; ++hl) {
-              const uint32_t sel = hl ? 0x7632u : 0x5410u;
-              mma_16816<false>(o[2 * y + hl], pa, __byte_perm(pg[z].v[0][y], pg[z].v[1][y], sel),
-                               __byte_perm(pg[z].v[2][y], pg[z].v[3][y], sel));
+            for (int x = 0; x < 2; ++x) {
+              e[x][0] = __byte_perm(pg[z].v[2 * x][y], pg[z].v[2 * x + 1][y], 0x5410u);
+              e[x][1] = __byte_perm(pg[z].v[2 * x][y], pg[z].v[2 * x + 1][y], 0x7632u);
             }
+#pragma unroll
+            for (int n = 0; n < NG; ++n) mma_16816<false>(o[n][y], e[0][0], e[0][1], e[1][0], e[1][1], pb[n][0], pb[n][1]);
+          }
         }
       }
     };
@@ -1821,37 +1857,36 @@ __global__ void __launch_bounds__(kFewThreads, (CfgFew<D, KV4>::kCtas)) prompt_a
     }
     // join the warps: rows < g of (m, l) and O
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      const int row = j + 8 * r;
-      if (t == 0) s_ml[warp * kFewRows + row] = make_float2(m[r], l[r]);
-      if (row < p.g) {
-        float* dst = fm + (warp * kFewRows + row) * D;
+    for (int n = 0; n < NG; ++n)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+      for (int e = 0; e < 2; ++e) {
+        const int row = 8 * n + 2 * t + e;
+        float sum = l[n][e];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            // column 2 t + e of tile n: lane index j' = 2 t + e of V's order
-            const int jj = 2 * t + e;
-            dst[KV4 ? jj * (D / 8) + n : 64 * (n / 8) + 8 * jj + (n & 7)] = o[n][2 * r + e];
-          }
+        for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (j == 0) s_ml[warp * R + row] = make_float2(m[n][e], sum);
+        if (row < p.g) {
+          float* dst = fm + (warp * R + row) * D;
+#pragma unroll
+          for (int y = 0; y < NT; ++y)  // the lane's channels 2 y, 2 y + 1 in V's order
+            *reinterpret_cast<float2*>(dst + (KV4 ? j * (D / 8) + 2 * y : 64 * (y / 4) + 8 * j + 2 * (y & 3))) =
+                make_float2(o[n][y][e], o[n][y][2 + e]);
+        }
       }
-    }
     __syncthreads();
     const bool whole = w.slot < 0;
     for (int i = tid; i < p.g * (D / 4); i += kFewThreads) {
       const int row = i / (D / 4), c = (i % (D / 4)) * 4;
       float mm = -INFINITY;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) mm = fmaxf(mm, s_ml[x * kFewRows + row].x);
+      for (int x = 0; x < 4; ++x) mm = fmaxf(mm, s_ml[x * R + row].x);
       float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
       float ll = 0.f;
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        const float2 ml = s_ml[x * kFewRows + row];
+        const float2 ml = s_ml[x * R + row];
         const float wt = mm == -INFINITY ? 1.f : ex2_approx(ml.x - mm);
-        const float4 v = *reinterpret_cast<const float4*>(fm + (x * kFewRows + row) * D + c);
+        const float4 v = *reinterpret_cast<const float4*>(fm + (x * R + row) * D + c);
         ll = fmaf(wt, ml.y, ll);
         f = make_float4(fmaf(wt, v.x, f.x), fmaf(wt, v.y, f.y), fmaf(wt, v.z, f.z), fmaf(wt, v.w, f.w));
       }
@@ -2102,18 +2137,22 @@ bool allow_smem(K kern, int bytes) {
   return false;
 }
 
+template <int D, bool KV4, int NG>
+int attn_launch_few(const AttnParams& a, void* ws, cudaStream_t s) {
+  const Shape sh = attn_shape(a.B, a.T, a.Hq, a.Hkv, D, KV4 ? kFew4 : kFew);
+  const Ws w = attn_ws(sh, ws);
+  constexpr int smem = CfgFew<D, KV4, NG>::kSmem;
+  if (!allow_smem(prompt_attn_few_kernel<D, KV4, NG>, smem)) return EAGLE_ERR_CUDA;
+  launch_plan(a, sh, w, 2, s);
+  const FewParams fp = {a, a.scale * a.k_scale * kLog2e, sh.g, sh.rows, w.hdr, &w.hdr->next, w.pieces, w.ml, w.po};
+  launch(prompt_attn_few_kernel<D, KV4, NG>, sh.ctas, kFewThreads, smem, s, fp);
+  return launch_merge<D, false>(a, sh, w, s);
+}
 template <int D, bool KV4>
 int attn_launch_tc(const AttnParams& a, void* ws, cudaStream_t s) {
   using C = Cfg<D, KV4>;
-  if (few_rows(a.B, a.T, a.Hq, a.Hkv)) {
-    const Shape sh = attn_shape(a.B, a.T, a.Hq, a.Hkv, D, KV4 ? kFew4 : kFew);
-    const Ws w = attn_ws(sh, ws);
-    if (!allow_smem(prompt_attn_few_kernel<D, KV4>, CfgFew<D, KV4>::kSmem)) return EAGLE_ERR_CUDA;
-    launch_plan(a, sh, w, 2, s);
-    const FewParams fp = {a, a.scale * a.k_scale * kLog2e, sh.g, sh.rows, w.hdr, &w.hdr->next, w.pieces, w.ml, w.po};
-    launch(prompt_attn_few_kernel<D, KV4>, sh.ctas, kFewThreads, CfgFew<D, KV4>::kSmem, s, fp);
-    return launch_merge<D, false>(a, sh, w, s);
-  }
+  if (few_rows(a.B, a.T, a.Hq, a.Hkv))
+    return a.Hq / a.Hkv > 8 ? attn_launch_few<D, KV4, 2>(a, ws, s) : attn_launch_few<D, KV4, 1>(a, ws, s);
   const Shape sh = attn_shape(a.B, a.T, a.Hq, a.Hkv, D, kTensor);
   const Ws w = attn_ws(sh, ws);
   CUtensorMap map_q = {};
