@@ -1498,7 +1498,7 @@ struct CfgFew {
   static constexpr int NP = KV4 ? 2 : 1, kRows = 8 * NG;
   // 4-bit: steps in flight per warp, copied to shared memory (2.3 KB a page:
   // held in registers, three pages a warp left the loads' latency exposed)
-  static constexpr int kRing = 3;
+  static constexpr int kRing = 2;
   static constexpr int kCodes = 16 * D / 2, kPage = 2 * (kCodes + D);  // bytes: K and V codes, K and V scales
   static constexpr int kJoin = 4 * kRows * (D * 4 + 8);             // the warps' O, m and l at the end (over the ring)
   static constexpr int kSmem = KV4 && 4 * kRing * NP * kPage > kJoin ? 4 * kRing * NP * kPage : kJoin;
@@ -1590,23 +1590,27 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas(KV4, NG)) prompt_attn_fe
     unsigned char* wring = reinterpret_cast<unsigned char*>(fm) + warp * C::kRing * NP * C::kPage;
     // 4-bit: page i of this warp to its ring, a 16-byte chunk c of V's key r at
     // chunk c ^ (r / 2 & 3), so that the reads below meet fewer bank conflicts
+    constexpr int CK = D / 32, CX = 16 * CK / 32;  // chunks per key, and per lane
+    const uint8_t *lane_k, *lane_v, *lane_s;       // of page 0
+    uint32_t to_v;
+    if constexpr (KV4) {
+      const int r = lane / CK;  // chunk lane + 32 x: key r + 32 x / CK
+      lane_k = static_cast<const uint8_t*>(a.kc) + (size_t)w.h * (8 * D) + lane * 16;
+      lane_v = static_cast<const uint8_t*>(a.vc) + (size_t)w.h * (8 * D) + lane * 16;
+      lane_s = (lane < D / 16 ? a.ks : a.vs) + (size_t)w.h * D + (lane & (D / 16 - 1)) * 16;
+      to_v = C::kCodes + (r * CK + ((lane % CK) ^ ((r >> 1) & (CK - 1)))) * 16;
+    }
     auto copy_page = [&](unsigned char* to, int i) {
       const int id = page_id(i), key0 = (page0 + 4 * i) * 16;
-      const size_t ch = ((size_t)max(id, 0) * a.Hkv + w.h) * (16 * D);  // channels before the page's head
-      constexpr int CK = D / 32;                                        // chunks per key
+      const size_t page = (size_t)max(id, 0) * ((size_t)a.Hkv * D);  // scales before the page
+      const uint32_t dst = smem_u32(to);
 #pragma unroll
-      for (int x = 0; x < 16 * CK / 32; ++x) {
-        const int c = x * 32 + lane, r = c / CK;
-        const bool live = id >= 0 && key0 + r < lim;
-        cp_async16_or_zero(smem_u32(to + c * 16), static_cast<const uint8_t*>(a.kc) + ch / 2 + c * 16, live);
-        cp_async16_or_zero(smem_u32(to + C::kCodes + (r * CK + ((c % CK) ^ ((r >> 1) & (CK - 1)))) * 16),
-                           static_cast<const uint8_t*>(a.vc) + ch / 2 + c * 16, live);
+      for (int x = 0; x < CX; ++x) {
+        const bool live = id >= 0 && key0 + (lane + 32 * x) / CK < lim;
+        cp_async16_or_zero(dst + lane * 16 + x * 512, lane_k + page * 8 + x * 512, live);
+        cp_async16_or_zero(dst + to_v + x * 512, lane_v + page * 8 + x * 512, live);
       }
-      if (lane < 2 * D / 16) {
-        const bool v = lane >= D / 16;
-        cp_async16_or_zero(smem_u32(to + 2 * C::kCodes + lane * 16),
-                           (v ? a.vs : a.ks) + ch / 16 + (lane & (D / 16 - 1)) * 16, id >= 0);
-      }
+      if (lane < 2 * D / 16) cp_async16_or_zero(dst + 2 * C::kCodes + lane * 16, lane_s + page, id >= 0);
     };
     auto load = [&](Page& g, int i) {
       const int id = page_id(i), key0 = (page0 + 4 * i) * 16;
