@@ -5,6 +5,14 @@
 // EAGLE-3", section 0x03C (the drafter's committed prefix) and 0x05D (rows go
 // to the cache by position).
 //
+//   out = sum_k 2^(z_k - m) v_k / sum_k 2^(z_k - m),
+//   z_k = scale log2(e) q . k_k over the keys k up to the row's position,
+// for any reference m; one pass over the keys keeps m, l = sum_k 2^(z_k - m) and
+// O = sum_k 2^(z_k - m) v_k in fp32 and rescales the two when m changes.  The
+// weights 2^(z - m) are rounded to the operand type for the product with V (l
+// sums them unrounded): bf16 for 16-bit pages, whose values bf16 holds, and
+// fp16 for 4-bit pages, whose values fp16 holds exactly.
+//
 // bf16 rows (16- and 4-bit pages): tensor cores.  The rows of a kv head are
 // the (token, grouped query head) pairs of a request in that order, so that
 // all of them share the K/V a CTA stages and a row's last key moves by one
@@ -12,7 +20,8 @@
 // request and kv head against its 128-key blocks.  Three kernels:
 //   plan    one CTA lists the units from the real lengths; units longer than
 //           a CTA's fair share are cut along the keys; longest pieces first
-//   main    one persistent CTA per SM takes pieces from that list
+//   main    persistent CTAs take pieces from that list: the two-tile kernel
+//           (one CTA per SM, tcgen05), or for single tokens the few-rows kernel
 //   merge   joins the pieces of cut units
 // fp32 rows: the same list and merge around a kernel on the CUDA cores.
 #include <math.h>
@@ -69,7 +78,8 @@ struct Shape {
   int ctas, cap_units, cap_pieces, cap_slots;
   size_t off_pieces, off_cuts, off_ml, off_o, total;
 };
-// CTAs per SM of the few-rows kernel with NG groups of eight rows
+// CTAs per SM of the few-rows kernel with NG groups of eight rows: as many as
+// the registers allow (4-bit, one group: 4 CTAs 62 us, 3 71 us, 5 69 us)
 constexpr int few_ctas(bool kv4, int ng) { return kv4 ? (ng == 1 ? 4 : 3) : 2; }
 enum Path { kTensor, kFew, kFew4, kFp32 };
 Shape attn_shape(int B, int T, int Hq, int Hkv, int D, Path path) {
@@ -92,10 +102,16 @@ Shape attn_shape(int B, int T, int Hq, int Hkv, int D, Path path) {
   s.total = s.off_o + sizeof(float) * (size_t)s.cap_slots * s.rows * D + 256;
   return s;
 }
-// Single tokens (at most one new row per request on average) with at most 16
-// query heads per kv head take the few-rows kernel, everything else the
-// two-tile kernel.
-bool few_rows(int B, int T, int Hq, int Hkv) { return T <= B && Hq / Hkv <= 16; }
+// Single tokens take the few-rows kernel, everything else the two-tile kernel.
+// The lengths are on the device, so the rule goes by their mean.  Measured, us,
+// few rows / two tiles, 64 requests over 1024 .. 4096 keys, D 128:
+//   16-bit, 32 heads over 8: 1 token 121 / 130, 2 tokens 195 / 131;
+//     64 over 8: 122 / 130; 64 over 4 (16 rows): 84 / 76
+//   4-bit, 32 over 8: 1 token 61 / 140, 2 tokens 88 / 143, 3 tokens 121 / 143,
+//     4 tokens 159 / 146; 64 over 4: 1 token 50 / 86, 2 tokens 89 / 90, 3 tokens 99 / 97
+bool few_rows(bool kv4, int B, int T, int Hq, int Hkv) {
+  return kv4 ? T <= 2 * B && Hq / Hkv <= 16 : T <= B && Hq / Hkv <= 8;
+}
 
 struct PlanParams {
   const int32_t *cu, *ctx;
@@ -111,8 +127,9 @@ constexpr int kPlanThreads = 512;
 // One CTA.  The requests are taken 512 at a time (up to that many are loaded
 // once): a block scan of their unit counts, then every thread finds the request
 // of its units by bisection.  Sweeps over all units: the total of key blocks,
-// the cost of each candidate cut, the lengths' histogram, and the list, which
-// whole warps write.
+// the cost of each candidate cut, the lengths' histogram, and the list.  It is
+// bound by its chain of block-wide steps: 8.5 us from cold caches for one
+// prompt, 12.7 us for 64 requests cut into some 1,700 pieces.
 __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanParams p) {
   __shared__ unsigned long long s_total;
   __shared__ int s_longest, s_C[kCand], s_n[kCand], s_cut[kCand], s_hist[32], s_cursor[32], s_c, s_slots, s_cuts, s_most;
@@ -362,7 +379,8 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanPar
 //                the stages
 //   warps 4, 5   issue the MMAs of tile 0 and 1
 //   warp 6       takes pieces from the list, ahead of the others
-//   warp 7       Q loader
+//   warp 7       loads Q: TMA boxes of tokens x grouped heads, or, for 4-bit
+//                pages, whose MMAs are fp16, loads and converts it
 //   warps 8-11   softmax of tile 0, warps 12-15 of tile 1: a thread is a row
 //                (a TMEM lane) and holds the block's 128 scores
 // S of a tile (fp32, 128 columns), its weights P (16-bit, over S) and O (D
@@ -374,6 +392,14 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanPar
 // tile idle and the chain S - softmax - P V exposed: then both tiles hold the
 // same rows, tile 0 takes the even blocks and tile 1 the odd ones, and tile
 // 0's warps join the two at the end (same TMEM lanes).
+//
+// Bound by each tile's chain S - softmax - P V: about 3,300 cycles per block
+// and two tiles (D 128), while the MMAs take 2,048 and the 32,768 exponentials,
+// at 16 a cycle and SM, 2,048 beside them.  Causal FLOPs at
+// 64 heads over 8, 8192 tokens: 825 us, 1.33 PFLOP/s; chunks of 256 .. 512
+// tokens over 32k keys, 32 over 8: 656 us, 1.21 PFLOP/s; one prompt of 2048
+// tokens: 50-55 us.  On 4-bit pages the producers' conversions take issue slots
+// from the softmax: chunks over 8k keys 262 us, 205 us on 16-bit pages.
 constexpr int kThreads = 512;
 constexpr int kSlots = 4;  // pieces known ahead
 constexpr int kNoPage = -0x7fffffff - 1;  // past the keys (or found out of range): reads as zeros
@@ -382,9 +408,9 @@ template <int D, bool KV4>
 struct Cfg {
   static constexpr uint32_t kHalf = kTileRows * 128u;        // 64 columns of 128 rows
   static constexpr uint32_t kTile = kHalf * (D / 64);         // one Q, K or V tile
-  static constexpr int kStages = KV4 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
+  static constexpr int kStages = KV4 ? (D == 128 ? 4 : 6) : (D == 128 ? 5 : 8);
   static constexpr uint32_t kRawCodes = kBlk * D / 2, kRaw = kRawCodes + kBlk * D / 16;
-  static constexpr int kRawRing = 6;
+  static constexpr int kRawRing = 3;
   static constexpr uint32_t kSmem = 2 * kTile + kStages * kTile + (KV4 ? kRawRing * kRaw : 0) + 1024;
   static constexpr uint32_t kColO = 256;  // S of tile t at t * 128, O at kColO + t * D
 };
@@ -430,15 +456,12 @@ __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wai
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
 }
-// at most n of the newest groups may still be in flight
+// at most n (0 .. 2) of the newest groups may still be in flight
 __device__ __forceinline__ void cp_async_wait_n(int n) {
   switch (n) {
     case 0: cp_async_wait<0>(); break;
     case 1: cp_async_wait<1>(); break;
-    case 2: cp_async_wait<2>(); break;
-    case 3: cp_async_wait<3>(); break;
-    case 4: cp_async_wait<4>(); break;
-    default: cp_async_wait<5>(); break;
+    default: cp_async_wait<2>(); break;
   }
 }
 // The bounded wait of this file's kernel: a failed try suspends the thread for
@@ -535,6 +558,23 @@ __device__ __forceinline__ uint32_t pack16(float a, float b) {
   }
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Eight 4-bit codes as four fp16 pairs times the pair `s`.
+__device__ __forceinline__ void kv4_expand(uint32_t w, uint32_t s, uint32_t* v) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+      : "r"(w));
+#pragma unroll
+  for (int y = 0; y < 4; ++y)  // exact: at most six significant bits, all multiples of 2^-10
+    asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(v[y]) : "r"(s));
+}
+__device__ __forceinline__ uint32_t e4m3_pair_as_f16(uint32_t two) {
+  uint32_t s2;
+  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(s2) : "r"(two));
+  return s2;
 }
 
 // Blocks of a piece that tile t takes, and the block its i-th one is.
@@ -758,6 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       cp_async_wait_all();
     } else {
       constexpr int R = C::kRawRing;
+      static_assert(R <= 3, "cp_async_wait_n");
       constexpr int CP = 16 * (D / 2) / 16 / 32;  // code copies per lane and page (16 tokens of a head)
       constexpr int SP = 16 * (D / 16) / 16;      // 16-byte scale copies per page
       int issued = 0, consumed = 0, islot = 0, cslot = 0;  // tiles, and their raw slots
@@ -870,22 +911,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if ((sc & 0x7fu) == 0x7fu) sc &= 0xff00u, found = true;
                 if ((sc & 0x7f00u) == 0x7f00u) sc &= 0x00ffu, found = true;
               }
-              uint32_t s2;
-              asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(s2) : "r"(sc));
+              const uint32_t s2 = e4m3_pair_as_f16(sc);
               const uint32_t sl = __byte_perm(s2, s2, 0x1010), sh = __byte_perm(s2, s2, 0x3232);
               const uint32_t cwv[4] = {cw.x, cw.y, cw.z, cw.w};
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
                 uint32_t v[4];
-                asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
-                    "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-                    "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-                    : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                    : "r"(cwv[x]));
-                const uint32_t m = x < 2 ? sl : sh;
-#pragma unroll
-                for (int y = 0; y < 4; ++y)  // exact: at most six significant bits, all multiples of 2^-10
-                  asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(v[y]) : "r"(m));
+                kv4_expand(cwv[x], x < 2 ? sl : sh, v);
                 *reinterpret_cast<uint4*>(stage + (uint32_t)(ch / 2) * C::kHalf + r * 128 +
                                           ((((ch & 1) * 4 + x) ^ (r & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
               }
@@ -1018,101 +1050,110 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     } else if (warp == 6) {
-    // ----------------------------------------------------------- scheduler
-    if (lane == 0) {
-      const int total = p.hdr->pieces;
-      for (int ps = 0;; ++ps) {
-        const int slot = ps % kSlots;
-        if (!mbar_wait_short(smem_u32(&sb.slot_empty[slot]), ((uint32_t)(ps / kSlots) & 1u) ^ 1u, abort_flag)) break;
-        const int i = ps == 0 ? (int)blockIdx.x : atomicAdd(p.next, 1);
-        if (i < total)
-          sb.piece[slot] = p.pieces[i];
-        else
-          sb.piece[slot].b = -1;
-        sb.bad_v[slot] = 0;
-        mbar_arrive(smem_u32(&sb.slot_full[slot]));
-        if (i >= total) break;
+      // ----------------------------------------------------------- scheduler
+      if (lane == 0) {
+        const int total = p.hdr->pieces;
+        for (int ps = 0;; ++ps) {
+          const int slot = ps % kSlots;
+          if (!mbar_wait_short(smem_u32(&sb.slot_empty[slot]), ((uint32_t)(ps / kSlots) & 1u) ^ 1u, abort_flag)) break;
+          const int i = ps == 0 ? (int)blockIdx.x : atomicAdd(p.next, 1);
+          if (i < total)
+            sb.piece[slot] = p.pieces[i];
+          else
+            sb.piece[slot].b = -1;
+          sb.bad_v[slot] = 0;
+          mbar_arrive(smem_u32(&sb.slot_full[slot]));
+          if (i >= total) break;
+        }
       }
-    }
-    __syncwarp();
+      __syncwarp();
     } else {
-    // ----------------------------------------------------------- Q loader
-    constexpr int CPR = D / 8, RPI = 32 / CPR;  // rows per iteration of the warp
-    constexpr int QU = 8;                       // rows a lane has in flight
-    const int row0 = lane / CPR, c = lane % CPR;
-    const uint32_t g_inv = (65536u + (uint32_t)p.g - 1) / (uint32_t)p.g;  // r / g = r * g_inv >> 16 for r < 128
-    const uint64_t pol = l2_policy_evict_first();
-    int uses[2] = {0, 0};
-    bool ok = true;
-    Piece w;
-    for (int ps = 0; ok; ++ps) {
-      if (!get_piece(ps, w)) break;
-      const TileWork tw = tile_work(w, p.tpt, p.tpu, p.g);
+      // ----------------------------------------------------------- Q loader
+      constexpr int CPR = D / 8, RPI = 32 / CPR;  // rows per iteration of the warp
+      constexpr int QU = 8;                       // rows a lane has in flight
+      const int row0 = lane / CPR, c = lane % CPR;
+      const uint32_t g_inv = (65536u + (uint32_t)p.g - 1) / (uint32_t)p.g;  // r / g = r * g_inv >> 16 for r < 128
+      const uint64_t pol = l2_policy_evict_first();
+      int uses[2] = {0, 0};
+      bool ok = true;
+      Piece w;
+      for (int ps = 0; ok; ++ps) {
+        if (!get_piece(ps, w)) break;
+        const TileWork tw = tile_work(w, p.tpt, p.tpu, p.g);
 #pragma unroll 1
-      for (int t = 0; t < 2; ++t) {
-        if (tw.n(t) == 0) continue;
-        ok = warp_wait(sb.q_empty[t], ((uint32_t)uses[t] & 1u) ^ 1u);
-        if (!ok) break;
-        const int tok0 = w.c0 + w.u * p.tpu + (tw.twin ? 0 : t * p.tpt);
-        if constexpr (!KV4) {
-          // one box per 64 columns: tokens x the kv head's query heads, in
-          // the tile's row order (rows past the request's end are another's
-          // or zeros: nothing of them is written)
-          if (lane == 0) {
-            const uint32_t bar = smem_u32(&sb.q_full[t]);
-            mbar_arrive_expect_tx(bar, (uint32_t)(p.tpt * p.g) * 128u * (D / 64));
+        for (int t = 0; t < 2; ++t) {
+          if (tw.n(t) == 0) continue;
+          ok = warp_wait(sb.q_empty[t], ((uint32_t)uses[t] & 1u) ^ 1u);
+          if (!ok) break;
+          const int tok0 = w.c0 + w.u * p.tpu + (tw.twin ? 0 : t * p.tpt);
+          if constexpr (!KV4) {
+            // one box per 64 columns: tokens x the kv head's query heads, in
+            // the tile's row order (rows past the request's end are another's
+            // or zeros: nothing of them is written)
+            if (lane == 0) {
+              const uint32_t bar = smem_u32(&sb.q_full[t]);
+              mbar_arrive_expect_tx(bar, (uint32_t)(p.tpt * p.g) * 128u * (D / 64));
 #pragma unroll
-            for (int h = 0; h < D / 64; ++h)
-              tma_load_3d(base + sQ + t * C::kTile + h * C::kHalf, &map_q, bar, h * 64, w.h * p.g, tok0, pol);
-          }
-          __syncwarp();
-        } else {
-          // rows as fp16, each scaled by a power of two to [1, 2) at its
-          // largest: bf16's 8 bits fit fp16's 11, and what is below 2^-14
-          // of the row's largest keeps an absolute error of 2^-25 of it
-          const int rows = tw.rows(t);
-          const __nv_bfloat16* q =
-              static_cast<const __nv_bfloat16*>(a.q) + (size_t)tok0 * a.q_stride + (size_t)w.h * p.g * D + c * 8;
-#pragma unroll 1
-          for (int r0 = row0; r0 < rows + row0; r0 += QU * RPI) {
-            uint4 v[QU];
-#pragma unroll
-            for (int x = 0; x < QU; ++x) {
-              const int r = r0 + x * RPI, tk = (int)((uint32_t)r * g_inv >> 16);
-              v[x] = r < rows ? *reinterpret_cast<const uint4*>(q + (size_t)tk * a.q_stride + (size_t)(r - tk * p.g) * D)
-                              : make_uint4(0u, 0u, 0u, 0u);
+              for (int h = 0; h < D / 64; ++h)
+                tma_load_3d(base + sQ + t * C::kTile + h * C::kHalf, &map_q, bar, h * 64, w.h * p.g, tok0, pol);
             }
+            __syncwarp();
+          } else {
+            // rows as fp16, each scaled by a power of two to [1, 2) at its
+            // largest: bf16's 8 bits fit fp16's 11, and what is below 2^-14
+            // of the row's largest keeps an absolute error of 2^-25 of it
+            const int rows = tw.rows(t);
+            const __nv_bfloat16* q =
+                static_cast<const __nv_bfloat16*>(a.q) + (size_t)tok0 * a.q_stride + (size_t)w.h * p.g * D + c * 8;
+#pragma unroll 1
+            for (int r0 = row0; r0 < rows + row0; r0 += QU * RPI) {
+              uint4 v[QU];
 #pragma unroll
-            for (int x = 0; x < QU; ++x) {
-              const int r = r0 + x * RPI;
-              const uint32_t e[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
-              uint32_t mx = 0;
+              for (int x = 0; x < QU; ++x) {
+                const int r = r0 + x * RPI, tk = (int)((uint32_t)r * g_inv >> 16);
+                v[x] = r < rows ? *reinterpret_cast<const uint4*>(q + (size_t)tk * a.q_stride + (size_t)(r - tk * p.g) * D)
+                                : make_uint4(0u, 0u, 0u, 0u);
+              }
 #pragma unroll
-              for (int k = 0; k < 4; ++k) mx = max(mx, max(e[k] & 0x7fffu, (e[k] >> 16) & 0x7fffu));
+              for (int x = 0; x < QU; ++x) {
+                const int r = r0 + x * RPI;
+                const uint32_t e[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+                uint32_t mx = 0;
 #pragma unroll
-              for (int d = CPR / 2; d; d >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-              const int k2 = min(126, max(-126, (int)(mx >> 7) - 127));
-              const float down = __uint_as_float((uint32_t)(127 - k2) << 23);
-              uint32_t h[4];
+                for (int k = 0; k < 4; ++k) mx = max(mx, max(e[k] & 0x7fffu, (e[k] >> 16) & 0x7fffu));
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                h[k] = pack16<true>(__uint_as_float(e[k] << 16) * down, __uint_as_float(e[k] & 0xffff0000u) * down);
-              if (r < rows) {
-                *reinterpret_cast<uint4*>(gbase + sQ + t * C::kTile + (uint32_t)(c / 8) * C::kHalf + (uint32_t)r * 128u +
-                                          (uint32_t)(((c % 8) ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-                if (c == 0) sb.q_fac[uses[t] & 1][t][r] = __uint_as_float((uint32_t)(127 + k2) << 23);
+                for (int d = CPR / 2; d; d >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                const int k2 = min(126, max(-126, (int)(mx >> 7) - 127));
+                const float down = __uint_as_float((uint32_t)(127 - k2) << 23);
+                uint32_t h[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  h[k] = pack16<true>(__uint_as_float(e[k] << 16) * down, __uint_as_float(e[k] & 0xffff0000u) * down);
+                if (r < rows) {
+                  *reinterpret_cast<uint4*>(gbase + sQ + t * C::kTile + (uint32_t)(c / 8) * C::kHalf + (uint32_t)r * 128u +
+                                            (uint32_t)(((c % 8) ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                  if (c == 0) sb.q_fac[uses[t] & 1][t][r] = __uint_as_float((uint32_t)(127 + k2) << 23);
+                }
               }
             }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sb.q_full[t]));
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sb.q_full[t]));
+          ++uses[t];
         }
-        ++uses[t];
+        if (!ok) break;
+        release_piece(ps);
       }
-      if (!ok) break;
-      release_piece(ps);
-    }
+      // (on abort) no box may land in the memory of the SM's next CTA
+      if (!KV4 && !ok) {
+        const unsigned long long t0 = globaltimer_ns();
+        for (int t = 0; t < 2; ++t)
+          while (uses[t] && !mbar_try_wait(smem_u32(&sb.q_full[t]), (uint32_t)(uses[t] - 1) & 1u) &&
+                 globaltimer_ns() - t0 < 100000000ull) {
+          }
+        __syncwarp();
+      }
     }
   } else {
     // ------------------------------------------------------------- softmax
@@ -1347,7 +1388,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------------------ merge
 // out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s over the pieces s of a
 // cut unit.  A CTA takes eight rows, a warp each, or, of a unit with many pieces,
-// one row with all its warps.
+// one row with all its warps (128 rows of some 50 pieces: 6.4 us, 15 us with a
+// warp each).  Bound by latency: 2.5-7 us.
 struct MergeParams {
   const PlanHeader* hdr;
   const Cut* cuts;
@@ -1428,22 +1470,31 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const MergeParams p) 
 // --------------------------------------------------------------- few rows
 // Single tokens: one unit per (token, kv head), its at most 16 rows the
 // query heads of the group, every key up to the token's own visible to all of
-// them.  The call is bound by the cache's bytes, and the path through shared
-// memory above costs more than they do (4-bit pages: staging and converting a
-// 128-key tile takes four warps 1,700 cycles, its bytes arrive in 400), so here
-// a warp takes a page at a time from global memory to the fragments of
-// mma.sync in registers: no stage, no barrier, 16 x 8 x 16 MMAs whose idle
-// rows cost nothing that is short.  128 threads, two CTAs per SM; warp w takes
-// pages w and w + 4 of each 128-key block, with its own m, l and O; the warps
-// are joined in shared memory at the end of a piece.
+// them.  The call is bound by the cache's bytes, and the path through stages
+// above costs more than they do (4-bit pages: staging and converting a 128-key
+// tile takes four warps 1,700 cycles, its bytes arrive in 400), so here a warp
+// takes a page at a time to the fragments of mma.sync: no stage that others
+// wait for, no barrier.  128 threads; warp w takes pages w and w + 4 of each
+// 128-key block, with its own m, l and O; the warps are joined in shared memory
+// at the end of a piece.
 //
-// The channels of a fragment may stand in any order, as long as Q's and K's
-// agree and O is stored by V's: a lane's registers are then consecutive
-// channels in memory.  With t = lane % 4, j = lane / 4:
-//   K (B operand of S = Q K^T): keys j and j + 8; 16-bit: 16-byte loads
+// The products are transposed, S^T = K Q^T and O^T = V^T P^T: an m16n8k16 MMA
+// then has 16 keys or channels and eight rows, so that a group of eight heads or
+// fewer costs half of what it did as 16 rows (4-bit pages: 62 us as one group
+// of eight, 80 us as two), and an 8 x 8 transpose turns the weights' layout
+// into an operand's.  The channels of a fragment may stand in any order, as
+// long as Q's and K's agree and O is stored by V's: a lane's registers are then
+// consecutive channels in memory.  With t = lane % 4, j = lane / 4:
+//   K (A operand of S^T): keys j and j + 8; 16-bit: 16-byte loads
 //     i = 0 .. D/32 - 1 at channel 32 i + 8 t; 4-bit: D/4 channels at t D/4
-//   V (B operand of O = P V): keys 2t, 2t + 1, 2t + 8, 2t + 9; 16-bit: loads
+//   V (A operand of O^T): keys 2t, 2t + 1, 2t + 8, 2t + 9; 16-bit: loads
 //     i = 0 .. D/64 - 1 at channel 64 i + 8 j; 4-bit: D/8 channels at j D/8
+//
+// 64 requests over 1024 .. 4096 keys, 32 heads over 8, D 128, with plan and
+// merge: 16-bit pages 120 us, 5.6 TB/s of K and V (bound by HBM: the copy rate
+// here is 6.8); 4-bit pages 62 us, 3.1 TB/s (bound by instructions: some 370 a
+// page and head, issue slots 59 % and the integer pipe 51 % busy in this
+// kernel's 47 us).  Four requests over 32k keys, 4-bit: 49 us.
 constexpr int kFewThreads = 128;
 
 struct FewParams {
@@ -1475,29 +1526,13 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %0;" : "+r"(v));
   return v;
 }
-// Eight 4-bit codes as four fp16 pairs times the pair `s`.
-__device__ __forceinline__ void kv4_expand(uint32_t w, uint32_t s, uint32_t* v) {
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-      : "r"(w));
-#pragma unroll
-  for (int y = 0; y < 4; ++y)  // exact: at most six significant bits, all multiples of 2^-10
-    asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(v[y]) : "r"(s));
-}
-__device__ __forceinline__ uint32_t e4m3_pair_as_f16(uint32_t two) {
-  uint32_t s2;
-  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(s2) : "r"(two));
-  return s2;
-}
-
 template <int D, bool KV4, int NG>
 struct CfgFew {
   // pages per step (their chains of latencies run side by side)
   static constexpr int NP = KV4 ? 2 : 1, kRows = 8 * NG;
   // 4-bit: steps in flight per warp, copied to shared memory (2.3 KB a page:
-  // held in registers, three pages a warp left the loads' latency exposed)
+  // held in registers, three pages a warp left the loads' latency exposed).
+  // Two pages a step, two steps: 62 us; three steps 64, one page a step 68.
   static constexpr int kRing = 2;
   static constexpr int kCodes = 16 * D / 2, kPage = 2 * (kCodes + D);  // bytes: K and V codes, K and V scales
   static constexpr int kJoin = 4 * kRows * (D * 4 + 8);             // the warps' O, m and l at the end (over the ring)
@@ -1915,6 +1950,10 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas(KV4, NG)) prompt_attn_fe
 // tx ..): 128 FMAs for every 12 16-byte shared loads, rows padded so that 16
 // keys' loads touch all banks evenly.  K of the next block is copied while the
 // weights and P V of this one are computed, V of the next during its scores.
+// Bound by the FMA and shared-memory pipes: a prompt of 2048 tokens, 32 heads
+// over 8, D 128: 991 us, 35 TFLOP/s causal.  Units of fewer rows pay for 64:
+// 64 single tokens over 1024 .. 4096 keys take 1,200 us (1.1 TB/s).  Three
+// prompts of up to 130 tokens, 4 heads over 2, D 64: 24 us, 17.5 in this kernel.
 template <int D>
 struct CfgF32 {
   static constexpr int kLd = D + 4, kLdP = kBlk + 4;  // floats per shared row
@@ -2155,8 +2194,12 @@ int attn_launch_few(const AttnParams& a, void* ws, cudaStream_t s) {
 template <int D, bool KV4>
 int attn_launch_tc(const AttnParams& a, void* ws, cudaStream_t s) {
   using C = Cfg<D, KV4>;
-  if (few_rows(a.B, a.T, a.Hq, a.Hkv))
-    return a.Hq / a.Hkv > 8 ? attn_launch_few<D, KV4, 2>(a, ws, s) : attn_launch_few<D, KV4, 1>(a, ws, s);
+  if (few_rows(KV4, a.B, a.T, a.Hq, a.Hkv)) {
+    if constexpr (KV4) {
+      if (a.Hq / a.Hkv > 8) return attn_launch_few<D, KV4, 2>(a, ws, s);
+    }
+    return attn_launch_few<D, KV4, 1>(a, ws, s);
+  }
   const Shape sh = attn_shape(a.B, a.T, a.Hq, a.Hkv, D, kTensor);
   const Ws w = attn_ws(sh, ws);
   CUtensorMap map_q = {};

@@ -331,6 +331,17 @@ def test_attn_single_tokens(new, ctx, Hq, Hkv, D, kind):
     check_attn(s, out, lse, dict(bf16=HALF["bf16"], kv4=HALF["fp16"])[kind])
 
 
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 1, 128), (12, 1, 64), (4, 4, 128)])
+@pytest.mark.parametrize("new,ctx", [([2, 2], [700, 15]), ([4, 0], [100, 5]), ([3, 2], [127, 300]), ([1, 1, 4], [0, 2000, 31])])
+@pytest.mark.parametrize("kind", ["bf16", "kv4"])
+def test_attn_two_tokens_on_average(new, ctx, Hq, Hkv, D, kind):
+    """Around two tokens per request, where 4-bit pages change kernels."""
+    b = need_gpu()
+    s = make(sum(new) + 3 * Hq, new, ctx, Hq, Hkv, D, "bf16", kv4=kind == "kv4", pad=1)
+    out, lse = run_attn(b, s, kind == "kv4")
+    check_attn(s, out, lse, dict(bf16=HALF["bf16"], kv4=HALF["fp16"])[kind])
+
+
 @pytest.mark.parametrize("kind", ["bf16", "kv4"])
 @pytest.mark.parametrize("new", [[1], [40]])
 def test_attn_growing_scores(new, kind):
