@@ -15,11 +15,12 @@
 // heads, so that no thread idles).  Its loads of q, k and v do not depend on
 // the row's request, so they are in flight while a warp looks up the request,
 // the position and the page.
-// Bound by HBM for many rows: 9061 rows of 32 + 2 x 8 heads, D 128, bf16: 44 us,
-// 5.1 TB/s; 8125 rows into 4-bit pages, whose elements take a division and a
-// conversion as well: 48 us in the kernel.  One row of each of 64 requests is
+// Bound by HBM for many rows: 9061 rows of 32 + 2 x 8 heads, D 128, bf16: 40 us,
+// 5.6 TB/s; 8125 rows into 4-bit pages, whose elements take a division and a
+// conversion as well: 45 us in the kernel (bound by its latencies: with a plain
+// multiplication for the division it takes as long).  One row of each of 64 requests is
 // bound by the launch: 3.6 us in a graph.  Reading 4-bit pages back
-// (eagle_kv4_read): 9.4 us for one cache of these rows.
+// (eagle_kv4_read): 8.2 us for one cache of these rows.
 #include <math.h>
 
 #include <algorithm>
@@ -31,7 +32,10 @@ namespace eagle {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kUnroll = 4;    // items a thread has in flight
+// items a thread has in flight: 3 hold fewer registers than 4 (9061 rows of 32 +
+// 2 x 8 heads: 40 us, 44 us; of 64 + 2 x 8: 63, 70; of 16 + 2 x 2: 19, 19), with 2
+// the rows take another round of loads (43, 63, 23)
+constexpr int kUnroll = 3;
 constexpr int kMaxRows = 64;  // rows per CTA
 
 struct AppendParams {
@@ -224,31 +228,36 @@ __global__ void __launch_bounds__(256) rope_table_kernel(int max_pos, int half, 
 }
 
 // 16 channels (8 code bytes, one scale byte) per thread; a warp reads 256
-// contiguous code bytes and writes whole rows of the token-major layout.
+// contiguous code bytes and writes whole rows of the token-major layout.  A CTA
+// takes `ppc` whole pages, so that the places are 32-bit divisions within them
+// (with 64-bit quotients per thread 9.4 us, now 8.2 us, for the
+// 566 pages of 8 heads, D 128, of 8125 rows).
 template <typename T>
 __global__ void __launch_bounds__(256)
     kv4_read_kernel(const uint2* __restrict__ codes, const uint8_t* __restrict__ scales, float scale, int Hkv, int D,
-                    long long groups, T* __restrict__ out) {
+                    int num_pages, int ppc, T* __restrict__ out) {
   pdl_wait();
   pdl_trigger();
-  const int gpr = D / 16;  // groups per row
+  const int gpr = D / 16, per_page = Hkv * 16 * gpr;  // groups per row and page
   const T* tag = nullptr;
-  for (long long g = (long long)blockIdx.x * 256 + threadIdx.x; g < groups; g += (long long)gridDim.x * 256) {
-    const uint2 c = codes[g];
-    const float s = kv4_scale_value(scales[g]);
-    const long long row = g / gpr;  // (page * Hkv + head) * 16 + slot
-    const int slot = (int)(row & 15), h = (int)((row >> 4) % Hkv);
-    const long long page = (row >> 4) / Hkv;
-    T* o = out + ((page * 16 + slot) * Hkv + h) * D + (g % gpr) * 16;
-    float f[16];
+  for (int p0 = blockIdx.x * ppc; p0 < num_pages; p0 += gridDim.x * ppc) {
+    const int n = min(ppc, num_pages - p0) * per_page;
+    const size_t g0 = (size_t)p0 * per_page;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < n; i += 256) {
+      const uint2 c = codes[g0 + i];
+      const float s = kv4_scale_value(scales[g0 + i]);
+      const int row = i / gpr, slot = row & 15, ph = row >> 4, page = ph / Hkv, h = ph - page * Hkv;
+      T* o = out + (((size_t)(p0 + page) * 16 + slot) * Hkv + h) * D + (i - row * gpr) * 16;
+      float f[16];
+      kv4_values(c.x, f);
+      kv4_values(c.y, f + 8);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const uint32_t w = i < 8 ? c.x : c.y;
-      f[i] = __fmul_rn(__fmul_rn(kv4_code_value((w >> (4 * (i & 7))) & 15u), s), scale);
+      for (int x = 0; x < 16; ++x) f[x] = __fmul_rn(__fmul_rn(f[x], s), scale);
+      constexpr int kV = Vec<T>::N;
+#pragma unroll
+      for (int x = 0; x < 16; x += kV) *reinterpret_cast<uint4*>(o + x) = pack(f + x, tag);
     }
-    constexpr int kV = Vec<T>::N;
-#pragma unroll
-    for (int i = 0; i < 16; i += kV) *reinterpret_cast<uint4*>(o + i) = pack(f + i, tag);
   }
 }
 
@@ -341,16 +350,16 @@ extern "C" int eagle_kv4_read(const uint8_t* codes, const uint8_t* scales, float
   if (!codes || !scales || !out || num_pages <= 0 || Hkv <= 0 || !(scale > 0.f) || !isfinite(scale))
     return EAGLE_ERR_INVALID_ARG;
   if (dtype != EAGLE_BF16 && dtype != EAGLE_FP32) return EAGLE_ERR_INVALID_ARG;
-  if ((D != 64 && D != 128) || num_pages > (1 << 26)) return EAGLE_ERR_UNSUPPORTED;
+  if ((D != 64 && D != 128) || Hkv > 1024 || num_pages > (1 << 26)) return EAGLE_ERR_UNSUPPORTED;
   if (!aligned16(codes) || !aligned16(out)) return EAGLE_ERR_INVALID_ARG;
-  const long long groups = (long long)num_pages * 16 * Hkv * (D / 16);
-  const int grid = (int)std::min<long long>((groups + 255) / 256, 16ll * std::max(1, sm_count()));
+  const int ppc = std::max(1, 1024 / (Hkv * D));  // four groups per thread
+  const int grid = (int)std::min<long long>((num_pages + ppc - 1) / ppc, 16ll * std::max(1, sm_count()));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dtype == EAGLE_BF16)
-    launch(kv4_read_kernel<__nv_bfloat16>, grid, 256, 0, s, (const uint2*)codes, scales, scale, Hkv, D, groups,
+    launch(kv4_read_kernel<__nv_bfloat16>, grid, 256, 0, s, (const uint2*)codes, scales, scale, Hkv, D, num_pages, ppc,
            (__nv_bfloat16*)out);
   else
-    launch(kv4_read_kernel<float>, grid, 256, 0, s, (const uint2*)codes, scales, scale, Hkv, D, groups, (float*)out);
+    launch(kv4_read_kernel<float>, grid, 256, 0, s, (const uint2*)codes, scales, scale, Hkv, D, num_pages, ppc, (float*)out);
   note_launch();
   return last_launch_status();
 }

@@ -761,7 +761,7 @@ int eagle_kv_append_kv4(const void* q, const void* k, const void* v, long long q
  * cache: out [num_pages, 16, Hkv, D] dtype `dtype` (fp32 product of code,
  * scale byte and `scale`, rounded once).  For inspection and for handing a
  * prefix to the calls that read 16- or 32-bit pages.
- * Limits: D in {64, 128}; 16-byte aligned codes and out. */
+ * Limits: D in {64, 128}; Hkv <= 1024; 16-byte aligned codes and out. */
 int eagle_kv4_read(const uint8_t* codes, const uint8_t* scales, float scale, int num_pages,
                    int Hkv, int D, int dtype, void* out, void* stream);
 

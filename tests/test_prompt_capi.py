@@ -90,6 +90,7 @@ def test_table_and_read_refusals(L):
     assert L.eagle_kv4_read(P, P, 0.0, 4, 2, 128, 1, P, N) == INVALID
     assert L.eagle_kv4_read(P, P, 1.0, 4, 2, 128, 3, P, N) == INVALID
     assert L.eagle_kv4_read(P, P, 1.0, 4, 2, 80, 1, P, N) == UNSUPPORTED
+    assert L.eagle_kv4_read(P, P, 1.0, 4, 1025, 128, 1, P, N) == UNSUPPORTED
 
 
 def test_workspace_query(L):
