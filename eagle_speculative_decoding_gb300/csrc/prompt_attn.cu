@@ -22,7 +22,7 @@
 //           a CTA's fair share are cut along the keys; longest pieces first
 //   main    persistent CTAs take pieces from that list: the two-tile kernel
 //           (one CTA per SM, tcgen05), or for single tokens the few-rows kernel
-//   merge   joins the pieces of cut units
+//   merge   joins the pieces of cut units (few rows: their last CTA does)
 // fp32 rows: the same list and merge around a kernel on the CUDA cores.
 #include <math.h>
 
@@ -58,10 +58,12 @@ struct AttnParams {
 // A piece: key blocks [k0, k1) of unit u of (request b, kv head h); slot >= 0
 // when the unit is cut (its partial result goes there).
 struct __align__(16) Piece {
-  int b, h, u, k0, k1, slot, c0, n, ctx, pad0, pad1, pad2;
+  int b, h, u, k0, k1, slot, c0, n, ctx;
+  int cut, first, pieces;  // of a cut unit: its index, its pieces' first slot and their number
 };
 struct __align__(16) Cut {  // a cut unit: its pieces are slots slot .. slot + pieces - 1
-  int h, u, slot, pieces, c0, n, pad0, pad1;
+  int h, u, slot, pieces, c0, n;
+  int done, pad;  // pieces whose results are written (few rows)
 };
 struct PlanHeader {
   int pieces, cuts, next, most;  // most: pieces of the most cut unit
@@ -356,7 +358,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanPar
         const int k0 = x * w.len + min(x, w.extra), c0 = s_c0[w.o], n = s_len[w.o];
         if (w.at + j < p.cap_pieces)
           p.pieces[w.at + j] = Piece{base + w.o, h, w.u, k0, k0 + w.len + (x < w.extra ? 1 : 0), w.k > 1 ? w.slot + j : -1,
-                                     c0, n, s_ctx[w.o], 0, 0, 0};
+                                     c0, n, s_ctx[w.o], w.cut + h, w.slot + h * w.k, w.k};
         if (w.k > 1 && x == 0) p.cuts[w.cut + h] = Cut{h, w.u, w.slot + j, w.k, c0, n, 0, 0};
       }
       __syncthreads();
@@ -1389,18 +1391,89 @@ __global__ void __launch_bounds__(kThreads, 1)
 // out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s over the pieces s of a
 // cut unit.  A CTA takes eight rows, a warp each, or, of a unit with many pieces,
 // one row with all its warps (128 rows of some 50 pieces: 6.4 us, 15 us with a
-// warp each).  Bound by latency: 2.5-7 us.
+// warp each).  Bound by latency: 2.5-5.5 us.
 struct MergeParams {
   const PlanHeader* hdr;
   const Cut* cuts;
   const float2* ml;
   const float* o;
-  void* out;  // bf16 or fp32
+  void* out;
   float* lse;
   float v_scale;
   int Hq, g, tpu, slot_rows;
 };
-template <int D, bool F32>
+// A warp sums the pieces s0, s0 + step, .. of the row at row0 (its next piece
+// slot_rows further on), a lane D / 32 channels; returns the maximum M over all.
+template <int D>
+__device__ __forceinline__ float merge_row(const float2* ml, const float* part, size_t row0, int slot_rows, int pieces,
+                                           int s0, int step, float& l, float* o) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  float M = -INFINITY;
+  for (int s = lane; s < pieces; s += 32) M = fmaxf(M, __ldcg(ml + row0 + (size_t)s * slot_rows).x);
+#pragma unroll
+  for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+  l = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll 4
+  for (int s = s0; s < pieces; s += step) {
+    const size_t row = row0 + (size_t)s * slot_rows;
+    const float2 x = __ldcg(ml + row);
+    const float w = M == -INFINITY ? 1.f : ex2_approx(x.x - M);
+    l = fmaf(w, x.y, l);
+    float f[E];
+    if constexpr (E == 4)
+      *reinterpret_cast<float4*>(f) = __ldcg(reinterpret_cast<const float4*>(part + row * D + lane * 4));
+    else
+      *reinterpret_cast<float2*>(f) = __ldcg(reinterpret_cast<const float2*>(part + row * D + lane * 2));
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = fmaf(w, f[e], o[e]);
+  }
+  return M;
+}
+template <int D, typename T>
+__device__ __forceinline__ void merge_store(T* out, float* lse, size_t orow, float M, float l, const float* o,
+                                            float v_scale) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const float inv = l == 0.f ? 0.f : v_scale / l;
+#pragma unroll
+  for (int e = 0; e < E; e += 2) {
+    T* dst = out + orow * D + lane * E + e;
+    if constexpr (sizeof(T) == 4)
+      *reinterpret_cast<float2*>(dst) = make_float2(o[e] * inv, o[e + 1] * inv);
+    else
+      *reinterpret_cast<uint32_t*>(dst) = pack16<false>(o[e] * inv, o[e + 1] * inv);
+  }
+  if (lse && lane == 0) lse[orow] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+}
+// Few rows: the last CTA of a cut unit to write its partial result joins them
+// all, in the pieces' order, which saves the merge's launch: one token over 100
+// keys takes 9.8 us from the host, 12.1 with a merge kernel (10.4 and 11.1 in a
+// graph); 64 requests 119 and 121 us, on 4-bit pages 62.5 and 61.5.  Not for
+// fp32's 64 rows (166 rows: 30 us, with the merge kernel 23).  The whole CTA
+// calls it.
+template <int D>
+__device__ __forceinline__ void join_if_last(const AttnParams& a, const Piece& w, int g, int tpu, int slot_rows, Cut* cuts,
+                                             const float2* ml, const float* part, int* s_last) {
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    *s_last = atomicAdd(&cuts[w.cut].done, 1) == w.pieces - 1;
+    __threadfence();
+  }
+  __syncthreads();
+  if (!*s_last) return;
+  const int rows = min(tpu, w.n - w.u * tpu) * g;
+  for (int r = threadIdx.x >> 5; r < rows; r += blockDim.x >> 5) {
+    float l, o[D / 32];
+    const float M = merge_row<D>(ml, part, (size_t)w.first * slot_rows + r, slot_rows, w.pieces, 0, 1, l, o);
+    merge_store<D>(static_cast<__nv_bfloat16*>(a.out), a.lse, ((size_t)w.c0 + w.u * tpu + r / g) * a.Hq + w.h * g + r % g, M, l, o,
+                   a.v_scale);
+  }
+}
+template <int D, typename T>
 __global__ void __launch_bounds__(256) prompt_merge_kernel(const MergeParams p) {
   constexpr int E = D / 32;
   __shared__ float s_o[8][D], s_l[8];
@@ -1416,27 +1489,9 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const MergeParams p) 
     if (!shared && y) continue;
     const int r = i % groups * 8 + (shared ? y : warp), tok = c.u * p.tpu + r / p.g;
     if (r >= min(min(p.tpu, c.n - c.u * p.tpu) * p.g, p.slot_rows)) continue;  // shared: the whole CTA
-    const size_t row0 = (size_t)c.slot * p.slot_rows + r;
-    float M = -INFINITY;
-    for (int s = lane; s < c.pieces; s += 32) M = fmaxf(M, p.ml[row0 + (size_t)s * p.slot_rows].x);
-#pragma unroll
-    for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-    float l = 0.f, o[E] = {};
-    const int step = shared ? 8 : 1;
-#pragma unroll 4
-    for (int s = shared ? warp : 0; s < c.pieces; s += step) {
-      const size_t row = row0 + (size_t)s * p.slot_rows;
-      const float2 x = p.ml[row];
-      const float w = M == -INFINITY ? 1.f : ex2_approx(x.x - M);
-      l = fmaf(w, x.y, l);
-      float f[E];
-      if constexpr (E == 4)
-        *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(p.o + row * D + lane * 4);
-      else
-        *reinterpret_cast<float2*>(f) = *reinterpret_cast<const float2*>(p.o + row * D + lane * 2);
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf(w, f[e], o[e]);
-    }
+    float l, o[E];
+    const float M = merge_row<D>(p.ml, p.o, (size_t)c.slot * p.slot_rows + r, p.slot_rows, c.pieces, shared ? warp : 0,
+                                 shared ? 8 : 1, l, o);
     if (shared) {
 #pragma unroll
       for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
@@ -1452,18 +1507,8 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const MergeParams p) 
       __syncthreads();
       if (warp != 0) continue;
     }
-    const float inv = l == 0.f ? 0.f : p.v_scale / l;
-    const size_t orow = ((size_t)c.c0 + tok) * p.Hq + c.h * p.g + r % p.g;
-    if constexpr (F32) {
-      float* dst = static_cast<float*>(p.out) + orow * D + lane * E;
-#pragma unroll
-      for (int e = 0; e < E; ++e) dst[e] = o[e] * inv;
-    } else {
-      uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + orow * D) + lane * (E / 2);
-#pragma unroll
-      for (int e = 0; e < E / 2; ++e) dst[e] = pack16<false>(o[2 * e] * inv, o[2 * e + 1] * inv);
-    }
-    if (p.lse && lane == 0) p.lse[orow] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+    merge_store<D>(static_cast<T*>(p.out), p.lse, ((size_t)c.c0 + tok) * p.Hq + c.h * p.g + r % p.g, M, l, o,
+                   p.v_scale);
   }
 }
 
@@ -1490,8 +1535,8 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const MergeParams p) 
 //   V (A operand of O^T): keys 2t, 2t + 1, 2t + 8, 2t + 9; 16-bit: loads
 //     i = 0 .. D/64 - 1 at channel 64 i + 8 j; 4-bit: D/8 channels at j D/8
 //
-// 64 requests over 1024 .. 4096 keys, 32 heads over 8, D 128, with plan and
-// merge: 16-bit pages 120 us, 5.6 TB/s of K and V (bound by HBM: the copy rate
+// 64 requests over 1024 .. 4096 keys, 32 heads over 8, D 128, with the plan:
+// 16-bit pages 120 us, 5.6 TB/s of K and V (bound by HBM: the copy rate
 // here is 6.8); 4-bit pages 62 us, 3.1 TB/s (bound by instructions: some 370 a
 // page and head, issue slots 59 % and the integer pipe 51 % busy in this
 // kernel's 47 us).  Four requests over 32k keys, 4-bit: 49 us.
@@ -1504,6 +1549,7 @@ struct FewParams {
   const PlanHeader* hdr;
   int* next;
   const Piece* pieces;
+  Cut* cuts;
   float2* part_ml;
   float* part_o;
 };
@@ -1547,7 +1593,7 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas(KV4, NG)) prompt_attn_fe
   constexpr int NP = C::NP, R = C::kRows;
   extern __shared__ __align__(16) float fm[];  // [4 warps][R rows][D], then [4][R] (m, l)
   float2* s_ml = reinterpret_cast<float2*>(fm + 4 * R * D);
-  __shared__ int s_piece;
+  __shared__ int s_piece, s_last;
   pdl_wait();
   pdl_trigger();
   const AttnParams& a = p.a;
@@ -1940,6 +1986,7 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas(KV4, NG)) prompt_attn_fe
         if (c == 0) p.part_ml[prow] = make_float2(mm, ll);
       }
     }
+    if (!whole) join_if_last<D>(a, w, p.g, 1, p.slot_rows, p.cuts, p.part_ml, p.part_o, &s_last);
   }
 }
 
@@ -2166,10 +2213,10 @@ void launch_plan(const AttnParams& a, const Shape& sh, const Ws& w, int min_cut,
                          w.hdr, w.pieces, w.cuts, a.status};
   launch(prompt_plan_kernel, 1, kPlanThreads, 0, s, pp);
 }
-template <int D, bool F32>
+template <int D, typename T>
 int launch_merge(const AttnParams& a, const Shape& sh, const Ws& w, cudaStream_t s) {
   const MergeParams gp = {w.hdr, w.cuts, w.ml, w.po, a.out, a.lse, a.v_scale, a.Hq, sh.g, sh.tpu, sh.rows};
-  launch(prompt_merge_kernel<D, F32>, 2 * sh.ctas, 256, 0, s, gp);
+  launch(prompt_merge_kernel<D, T>, 2 * sh.ctas, 256, 0, s, gp);
   note_launch(3);
   return last_launch_status();
 }
@@ -2187,9 +2234,10 @@ int attn_launch_few(const AttnParams& a, void* ws, cudaStream_t s) {
   constexpr int smem = CfgFew<D, KV4, NG>::kSmem;
   if (!allow_smem(prompt_attn_few_kernel<D, KV4, NG>, smem)) return EAGLE_ERR_CUDA;
   launch_plan(a, sh, w, 2, s);
-  const FewParams fp = {a, a.scale * a.k_scale * kLog2e, sh.g, sh.rows, w.hdr, &w.hdr->next, w.pieces, w.ml, w.po};
+  const FewParams fp = {a, a.scale * a.k_scale * kLog2e, sh.g, sh.rows, w.hdr, &w.hdr->next, w.pieces, w.cuts, w.ml, w.po};
   launch(prompt_attn_few_kernel<D, KV4, NG>, sh.ctas, kFewThreads, smem, s, fp);
-  return launch_merge<D, false>(a, sh, w, s);
+  note_launch(2);
+  return last_launch_status();
 }
 template <int D, bool KV4>
 int attn_launch_tc(const AttnParams& a, void* ws, cudaStream_t s) {
@@ -2211,7 +2259,7 @@ int attn_launch_tc(const AttnParams& a, void* ws, cudaStream_t s) {
   const MainParams mp = {a, a.scale * a.k_scale * kLog2e, sh.g, sh.tpt, sh.tpu, sh.rows, w.hdr, &w.hdr->next, w.pieces,
                          w.ml, w.po};
   launch(prompt_attn_tc_kernel<D, KV4>, sh.ctas, kThreads, C::kSmem, s, map_q, mp);
-  return launch_merge<D, false>(a, sh, w, s);
+  return launch_merge<D, __nv_bfloat16>(a, sh, w, s);
 }
 template <int D>
 int attn_launch_f32(const AttnParams& a, void* ws, cudaStream_t s) {
@@ -2221,7 +2269,7 @@ int attn_launch_f32(const AttnParams& a, void* ws, cudaStream_t s) {
   launch_plan(a, sh, w, 1, s);
   const F32Params fp = {a, a.scale * kLog2e, sh.g, sh.tpu, sh.rows, w.hdr, &w.hdr->next, w.pieces, w.ml, w.po};
   launch(prompt_attn_f32_kernel<D>, sh.ctas, 256, CfgF32<D>::kSmem, s, fp);
-  return launch_merge<D, true>(a, sh, w, s);
+  return launch_merge<D, float>(a, sh, w, s);
 }
 
 int attn_ws_check(const AttnParams& a, int D, void* ws, size_t ws_bytes) {
