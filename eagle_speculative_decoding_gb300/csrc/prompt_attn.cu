@@ -36,7 +36,8 @@ namespace {
 
 constexpr int kBlk = 128;        // keys per block
 constexpr int kTileRows = 128;   // query rows per tile
-constexpr int kF32Rows = 64;     // query rows per unit of the fp32 path
+constexpr int kF32Rows = 64, kF32Few = 16;  // query rows per unit of the fp32 path, and when they are few
+constexpr int kF32FewCtas = 2;               // CTAs per SM then
 constexpr float kSumLimit = 256.f;  // of a block's weights: far below fp16's 65504
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 
@@ -83,15 +84,15 @@ struct Shape {
 // CTAs per SM of the few-rows kernel with NG groups of eight rows: as many as
 // the registers allow (4-bit, one group: 4 CTAs 62 us, 3 71 us, 5 69 us)
 constexpr int few_ctas(bool kv4, int ng) { return kv4 ? (ng == 1 ? 4 : 3) : 2; }
-enum Path { kTensor, kFew, kFew4, kFp32 };
+enum Path { kTensor, kFew, kFew4, kFp32, kFp32Few };
 Shape attn_shape(int B, int T, int Hq, int Hkv, int D, Path path) {
   Shape s;
   s.g = Hq / Hkv;
-  s.tpt = path == kTensor ? kTileRows / s.g : path == kFp32 ? kF32Rows / s.g : 1;
+  s.tpt = path == kTensor ? kTileRows / s.g : path == kFp32 ? kF32Rows / s.g : path == kFp32Few ? std::max(1, kF32Few / s.g) : 1;
   s.tpu = path == kTensor ? 2 * s.tpt : s.tpt;
   s.rows = std::min(s.tpu, T) * s.g;
   const int sms = sm_count();
-  s.ctas = (sms > 0 ? sms : 152) * (path == kFew4 || path == kFew ? few_ctas(path == kFew4, s.g > 8 ? 2 : 1) : 1);
+  s.ctas = (sms > 0 ? sms : 152) * (path == kFew4 || path == kFew ? few_ctas(path == kFew4, s.g > 8 ? 2 : 1) : path == kFp32Few ? kF32FewCtas : 1);
   s.cap_units = T / s.tpu + std::min(B, T);
   // a unit of L > C blocks makes ceil(L / C) < 2 L / C pieces and the finest C
   // is total / (kMaxShare * ctas)
@@ -113,6 +114,13 @@ Shape attn_shape(int B, int T, int Hq, int Hkv, int D, Path path) {
 //     4 tokens 159 / 146; 64 over 4: 1 token 50 / 86, 2 tokens 89 / 90, 3 tokens 99 / 97
 bool few_rows(bool kv4, int B, int T, int Hq, int Hkv) {
   return kv4 ? T <= 2 * B && Hq / Hkv <= 16 : T <= B && Hq / Hkv <= 8;
+}
+// fp32: at most 16 rows per request and kv head on average take units of 16.
+// us, 16 / 64 rows a unit, 32 heads over 8, D 128, 64 requests over 1024 ..
+// 4096 keys: 1 to 4 tokens 802 / 1,200, 6 tokens 1,680 / 1,207; 8 heads of 16
+// requests over 300 .. 500 keys, D 64: 16 tokens 36 / 48, 20 tokens 57 / 49.
+bool few_rows_f32(int B, int T, int Hq, int Hkv) {
+  return Hq / Hkv <= kF32Few && (long long)T * (Hq / Hkv) <= (long long)kF32Few * B;
 }
 
 struct PlanParams {
@@ -1992,19 +2000,23 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas(KV4, NG)) prompt_attn_fe
 
 // ------------------------------------------------------------------- fp32
 // Units of 64 rows against 128-key blocks on the CUDA cores, from the same
-// list of pieces.  256 threads: thread (ty, tx) holds scores of rows 4 ty ..
-// against keys tx + 16 j, and of O the same rows' columns 4 tx .. (and 64 + 4
-// tx ..): 128 FMAs for every 12 16-byte shared loads, rows padded so that 16
-// keys' loads touch all banks evenly.  K of the next block is copied while the
-// weights and P V of this one are computed, V of the next during its scores.
+// list of pieces.  256 threads: thread (ty, tx) holds scores of RT = 4 rows,
+// RT ty .., against keys tx + 16 j, and of O the same rows' columns 4 tx ..
+// (and 64 + 4 tx ..): 128 FMAs for every 12 16-byte shared loads, rows padded
+// so that 16 keys' loads touch all banks evenly.  K of the next block is copied
+// while the weights and P V of this one are computed, V of the next during its
+// scores.  Few rows: units of 16, one row per thread, and half blocks, so that
+// two CTAs fit an SM (64 single tokens 802 us; whole blocks, one CTA 902).
 // Bound by the FMA and shared-memory pipes: a prompt of 2048 tokens, 32 heads
-// over 8, D 128: 991 us, 35 TFLOP/s causal.  Units of fewer rows pay for 64:
-// 64 single tokens over 1024 .. 4096 keys take 1,200 us (1.1 TB/s).  Three
-// prompts of up to 130 tokens, 4 heads over 2, D 64: 24 us, 17.5 in this kernel.
-template <int D>
+// over 8, D 128: 991 us, 35 TFLOP/s causal; 64 single tokens over 1024 .. 4096
+// keys 802 us, 1.7 TB/s (a key's shared loads serve one row).  Three prompts of
+// up to 130 tokens, 4 heads over 2, D 64: 24 us, 17.5 in this kernel.
+template <int D, int RT>
 struct CfgF32 {
-  static constexpr int kLd = D + 4, kLdP = kBlk + 4;  // floats per shared row
-  static constexpr int kSmem = (kF32Rows * kLd + 2 * kBlk * kLd + kF32Rows * kLdP) * 4;
+  static constexpr int kRows = 16 * RT, kKeys = RT == 1 ? 64 : 128;  // per unit, per step
+  static constexpr int kCtas = RT == 1 ? kF32FewCtas : 1;            // per SM
+  static constexpr int kLd = D + 4, kLdP = kKeys + 4;  // floats per shared row
+  static constexpr int kSmem = (kRows * kLd + 2 * kKeys * kLd + kRows * kLdP) * 4;
 };
 struct F32Params {
   AttnParams a;
@@ -2016,12 +2028,13 @@ struct F32Params {
   float2* part_ml;
   float* part_o;
 };
-template <int D>
-__global__ void __launch_bounds__(256, 1) prompt_attn_f32_kernel(const F32Params p) {
-  using C = CfgF32<D>;
+template <int D, int RT>
+__global__ void __launch_bounds__(256, (CfgF32<D, RT>::kCtas)) prompt_attn_f32_kernel(const F32Params p) {
+  using C = CfgF32<D, RT>;
   constexpr int CPR = D / 4, NC = D / 64;  // 16-byte chunks per row, 64-column groups
+  constexpr int KB = C::kKeys, NJ = KB / 16;
   extern __shared__ __align__(16) float sm[];
-  float *sq = sm, *sk = sq + kF32Rows * C::kLd, *sv = sk + kBlk * C::kLd, *sp = sv + kBlk * C::kLd;
+  float *sq = sm, *sk = sq + C::kRows * C::kLd, *sv = sk + KB * C::kLd, *sp = sv + KB * C::kLd;
   __shared__ int s_piece;
   pdl_wait();
   pdl_trigger();
@@ -2035,11 +2048,12 @@ __global__ void __launch_bounds__(256, 1) prompt_attn_f32_kernel(const F32Params
     const Piece w = p.pieces[s_piece];
     const int rows = min(w.n - w.u * p.tpu, p.tpu) * p.g, n_keys = w.ctx + w.n;
     const int32_t* tab = a.table + (size_t)w.b * a.max_pages;
+    const int b0 = w.k0 * (kBlk / KB), b1 = min(w.k1 * (kBlk / KB), (n_keys + KB - 1) / KB);  // in steps
     auto copy = [&](float* dst, const void* src, int blk) {
-      if (blk < w.k1) {
+      if (blk < b1) {
 #pragma unroll 8
-        for (int i = tid; i < kBlk * CPR; i += 256) {
-          const int r = i / CPR, c = i % CPR, k = blk * kBlk + r;
+        for (int i = tid; i < KB * CPR; i += 256) {
+          const int r = i / CPR, c = i % CPR, k = blk * KB + r;
           const int pg = k < n_keys ? tab[k / 16] : -1;
           const bool live = pg >= 0 && pg < a.num_pages;
           if (k < n_keys && !live) set_status(a.status, EAGLE_ERR_BAD_KV);
@@ -2050,9 +2064,9 @@ __global__ void __launch_bounds__(256, 1) prompt_attn_f32_kernel(const F32Params
       }
       cp_async_commit();
     };
-    copy(sk, a.kc, w.k0);
-    copy(sv, a.vc, w.k0);
-    for (int i = tid; i < kF32Rows * CPR; i += 256) {
+    copy(sk, a.kc, b0);
+    copy(sv, a.vc, b0);
+    for (int i = tid; i < C::kRows * CPR; i += 256) {
       const int r = i / CPR, c = i % CPR;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < rows)
@@ -2061,47 +2075,47 @@ __global__ void __launch_bounds__(256, 1) prompt_attn_f32_kernel(const F32Params
                                              (size_t)(w.h * p.g + r % p.g) * D + c * 4);
       *reinterpret_cast<float4*>(sq + r * C::kLd + c * 4) = v;
     }
-    int pos[4];
-    float m[4], l[4], o[4][4 * NC];
+    int pos[RT];
+    float m[RT], l[RT], o[RT][4 * NC];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = ty * 4 + i;
+    for (int i = 0; i < RT; ++i) {
+      const int r = ty * RT + i;
       pos[i] = r < rows ? w.ctx + w.u * p.tpu + r / p.g : 0x7fffffff;
       m[i] = -INFINITY;
       l[i] = 0.f;
 #pragma unroll
       for (int c = 0; c < 4 * NC; ++c) o[i][c] = 0.f;
     }
-    for (int blk = w.k0; blk < w.k1; ++blk) {
-      const bool masked = blk * kBlk + kBlk - 1 > w.ctx + w.u * p.tpu;
+    for (int blk = b0; blk < b1; ++blk) {
+      const bool masked = blk * KB + KB - 1 > w.ctx + w.u * p.tpu;
       cp_async_wait<1>();
       __syncthreads();
-      float z[4][8];
+      float z[RT][NJ];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < RT; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) z[i][j] = 0.f;
+        for (int j = 0; j < NJ; ++j) z[i][j] = 0.f;
 #pragma unroll 4
       for (int c = 0; c < CPR; ++c) {
-        float4 q[4];
+        float4 q[RT];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const float4*>(sq + (ty * 4 + i) * C::kLd + c * 4);
+        for (int i = 0; i < RT; ++i) q[i] = *reinterpret_cast<const float4*>(sq + (ty * RT + i) * C::kLd + c * 4);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < NJ; ++j) {
           const float4 k = *reinterpret_cast<const float4*>(sk + (tx + 16 * j) * C::kLd + c * 4);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < RT; ++i)
             z[i][j] = fmaf(q[i].x, k.x, fmaf(q[i].y, k.y, fmaf(q[i].z, k.z, fmaf(q[i].w, k.w, z[i][j]))));
         }
       }
       __syncthreads();
       copy(sk, a.kc, blk + 1);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < RT; ++i) {
         float bm = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          z[i][j] = blk * kBlk + tx + 16 * j <= pos[i] ? z[i][j] * p.scale_log2 : -INFINITY;
+        for (int j = 0; j < NJ; ++j) {
+          z[i][j] = blk * KB + tx + 16 * j <= pos[i] ? z[i][j] * p.scale_log2 : -INFINITY;
           bm = fmaxf(bm, z[i][j]);
         }
 #pragma unroll
@@ -2110,10 +2124,10 @@ __global__ void __launch_bounds__(256, 1) prompt_attn_f32_kernel(const F32Params
         const float al = ex2_approx(m[i] - ref);
         float sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < NJ; ++j) {
           const float e = ex2_approx(z[i][j] - ref);
           sum += e;
-          sp[(ty * 4 + i) * C::kLdP + tx + 16 * j] = e;
+          sp[(ty * RT + i) * C::kLdP + tx + 16 * j] = e;
         }
 #pragma unroll
         for (int d = 8; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
@@ -2128,17 +2142,17 @@ __global__ void __launch_bounds__(256, 1) prompt_attn_f32_kernel(const F32Params
       // of zero would not silence a NaN or an infinity
       auto weigh = [&](auto keep) {
 #pragma unroll 2
-        for (int k = 0; k < kBlk; k += 4) {
-          float4 e[4];
+        for (int k = 0; k < KB; k += 4) {
+          float4 e[RT];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) e[i] = *reinterpret_cast<const float4*>(sp + (ty * 4 + i) * C::kLdP + k);
+          for (int i = 0; i < RT; ++i) e[i] = *reinterpret_cast<const float4*>(sp + (ty * RT + i) * C::kLdP + k);
 #pragma unroll
           for (int y = 0; y < 4; ++y)
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
               const float4 v = *reinterpret_cast<const float4*>(sv + (k + y) * C::kLd + c * 64 + tx * 4);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
+              for (int i = 0; i < RT; ++i) {
                 const float ey = y == 0 ? e[i].x : y == 1 ? e[i].y : y == 2 ? e[i].z : e[i].w;
                 if (!keep(i, k + y)) continue;
                 o[i][4 * c] = fmaf(ey, v.x, o[i][4 * c]);
@@ -2150,7 +2164,7 @@ __global__ void __launch_bounds__(256, 1) prompt_attn_f32_kernel(const F32Params
         }
       };
       if (masked)
-        weigh([&](int i, int k) { return blk * kBlk + k <= pos[i]; });
+        weigh([&](int i, int k) { return blk * KB + k <= pos[i]; });
       else
         weigh([](int, int) { return true; });
       __syncthreads();
@@ -2158,8 +2172,8 @@ __global__ void __launch_bounds__(256, 1) prompt_attn_f32_kernel(const F32Params
     }
     cp_async_wait<0>();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = ty * 4 + i;
+    for (int i = 0; i < RT; ++i) {
+      const int r = ty * RT + i;
       if (r >= rows) continue;
       const bool whole = w.slot < 0;
       const size_t orow = ((size_t)w.c0 + w.u * p.tpu + r / p.g) * a.Hq + w.h * p.g + r % p.g;
@@ -2261,15 +2275,20 @@ int attn_launch_tc(const AttnParams& a, void* ws, cudaStream_t s) {
   launch(prompt_attn_tc_kernel<D, KV4>, sh.ctas, kThreads, C::kSmem, s, map_q, mp);
   return launch_merge<D, __nv_bfloat16>(a, sh, w, s);
 }
-template <int D>
+template <int D, int RT>
 int attn_launch_f32(const AttnParams& a, void* ws, cudaStream_t s) {
-  const Shape sh = attn_shape(a.B, a.T, a.Hq, a.Hkv, D, kFp32);
+  const Shape sh = attn_shape(a.B, a.T, a.Hq, a.Hkv, D, RT == 1 ? kFp32Few : kFp32);
   const Ws w = attn_ws(sh, ws);
-  if (!allow_smem(prompt_attn_f32_kernel<D>, CfgF32<D>::kSmem)) return EAGLE_ERR_CUDA;
+  constexpr int smem = CfgF32<D, RT>::kSmem;
+  if (!allow_smem(prompt_attn_f32_kernel<D, RT>, smem)) return EAGLE_ERR_CUDA;
   launch_plan(a, sh, w, 1, s);
   const F32Params fp = {a, a.scale * kLog2e, sh.g, sh.tpu, sh.rows, w.hdr, &w.hdr->next, w.pieces, w.ml, w.po};
-  launch(prompt_attn_f32_kernel<D>, sh.ctas, 256, CfgF32<D>::kSmem, s, fp);
+  launch(prompt_attn_f32_kernel<D, RT>, sh.ctas, 256, smem, s, fp);
   return launch_merge<D, float>(a, sh, w, s);
+}
+template <int D>
+int attn_launch_f32(const AttnParams& a, void* ws, cudaStream_t s) {
+  return few_rows_f32(a.B, a.T, a.Hq, a.Hkv) ? attn_launch_f32<D, 1>(a, ws, s) : attn_launch_f32<D, 4>(a, ws, s);
 }
 
 int attn_ws_check(const AttnParams& a, int D, void* ws, size_t ws_bytes) {
@@ -2284,7 +2303,7 @@ using namespace eagle;
 extern "C" size_t eagle_prompt_attn_workspace_size(int B, int T, int Hq, int Hkv, int D) {
   if (B <= 0 || T < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || Hq / Hkv > 64 || (D != 64 && D != 128)) return 0;
   size_t most = 0;
-  for (const Path path : {kTensor, kFew, kFew4, kFp32}) most = std::max(most, attn_shape(B, T, Hq, Hkv, D, path).total);
+  for (const Path path : {kTensor, kFew, kFew4, kFp32, kFp32Few}) most = std::max(most, attn_shape(B, T, Hq, Hkv, D, path).total);
   return most + 256;
 }
 
