@@ -404,8 +404,8 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanPar
 // 0's warps join the two at the end (same TMEM lanes).
 //
 // Bound by each tile's chain S - softmax - P V: about 3,300 cycles per block
-// and two tiles (D 128), while the MMAs take 2,048 and the 32,768 exponentials,
-// at 16 a cycle and SM, 2,048 beside them.  Causal FLOPs at
+// and two tiles (D 128), while the MMAs take 2,048 and the exponentials, at 32
+// a cycle and SM, 1,024 beside them.  Causal FLOPs at
 // 64 heads over 8, 8192 tokens: 825 us, 1.33 PFLOP/s; chunks of 256 .. 512
 // tokens over 32k keys, 32 over 8: 656 us, 1.21 PFLOP/s; one prompt of 2048
 // tokens: 50-55 us.  On 4-bit pages the producers' conversions take issue slots
@@ -1546,8 +1546,8 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const MergeParams p) 
 // 64 requests over 1024 .. 4096 keys, 32 heads over 8, D 128, with the plan:
 // 16-bit pages 120 us, 5.6 TB/s of K and V (bound by HBM: the copy rate
 // here is 6.8); 4-bit pages 62 us, 3.1 TB/s (bound by instructions: some 370 a
-// page and head, issue slots 59 % and the integer pipe 51 % busy in this
-// kernel's 47 us).  Four requests over 32k keys, 4-bit: 49 us.
+// page and head, issue slots 55-59 % and the integer pipe 46-51 % busy in this
+// kernel).  Four requests over 32k keys, 4-bit: 49 us.
 constexpr int kFewThreads = 128;
 
 struct FewParams {
