@@ -27,6 +27,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kv4.cuh"
@@ -117,8 +118,8 @@ bool few_rows(bool kv4, int B, int T, int Hq, int Hkv) {
 }
 // fp32: at most 16 rows per request and kv head on average take units of 16.
 // us, 16 / 64 rows a unit, 32 heads over 8, D 128, 64 requests over 1024 ..
-// 4096 keys: 1 to 4 tokens 802 / 1,200, 6 tokens 1,680 / 1,207; 8 heads of 16
-// requests over 300 .. 500 keys, D 64: 16 tokens 36 / 48, 20 tokens 57 / 49.
+// 4096 keys: 1 to 4 tokens 800 / 1,200, 6 tokens 1,680 / 985; 8 heads of 16
+// requests over 300 .. 500 keys, D 64: 16 tokens 36 / 48, 20 tokens 57 / 40.
 bool few_rows_f32(int B, int T, int Hq, int Hkv) {
   return Hq / Hkv <= kF32Few && (long long)T * (Hq / Hkv) <= (long long)kF32Few * B;
 }
@@ -2001,16 +2002,18 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas(KV4, NG)) prompt_attn_fe
 // ------------------------------------------------------------------- fp32
 // Units of 64 rows against 128-key blocks on the CUDA cores, from the same
 // list of pieces.  256 threads: thread (ty, tx) holds scores of RT = 4 rows,
-// RT ty .., against keys tx + 16 j, and of O the same rows' columns 4 tx ..
+// ty + 16 i, against keys tx + 16 j, and of O the same rows' columns 4 tx ..
 // (and 64 + 4 tx ..): 128 FMAs for every 12 16-byte shared loads, rows padded
 // so that 16 keys' loads touch all banks evenly.  K of the next block is copied
 // while the weights and P V of this one are computed, V of the next during its
-// scores.  Few rows: units of 16, one row per thread, and half blocks, so that
-// two CTAs fit an SM (64 single tokens 802 us; whole blocks, one CTA 902).
-// Bound by the FMA and shared-memory pipes: a prompt of 2048 tokens, 32 heads
-// over 8, D 128: 991 us, 35 TFLOP/s causal; 64 single tokens over 1024 .. 4096
-// keys 802 us, 1.7 TB/s (a key's shared loads serve one row).  Three prompts of
-// up to 130 tokens, 4 heads over 2, D 64: 24 us, 17.5 in this kernel.
+// scores.  Units of at most 32 rows compute those alone (64 requests of 8
+// tokens, 32 rows each: 988 us, 1,203 with all 64; a long prompt pays 4 % for
+// the larger kernel).  Few rows: units of 16, one row per thread, and half
+// blocks, so that two CTAs fit an SM (64 single tokens 800 us; whole blocks, one
+// CTA 902).  Bound by the FMA and shared-memory pipes: a prompt of 2048 tokens,
+// 32 heads over 8, D 128: 1,027 us, 33 TFLOP/s causal; 64 single tokens over
+// 1024 .. 4096 keys 800 us, 1.7 TB/s (a key's shared loads serve one row).  Three
+// prompts of up to 130 tokens, 4 heads over 2, D 64: 24 us, 17.5 in this kernel.
 template <int D, int RT>
 struct CfgF32 {
   static constexpr int kRows = 16 * RT, kKeys = RT == 1 ? 64 : 128;  // per unit, per step
@@ -2079,39 +2082,41 @@ __global__ void __launch_bounds__(256, (CfgF32<D, RT>::kCtas)) prompt_attn_f32_k
     float m[RT], l[RT], o[RT][4 * NC];
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
-      const int r = ty * RT + i;
+      const int r = ty + 16 * i;
       pos[i] = r < rows ? w.ctx + w.u * p.tpu + r / p.g : 0x7fffffff;
       m[i] = -INFINITY;
       l[i] = 0.f;
 #pragma unroll
       for (int c = 0; c < 4 * NC; ++c) o[i][c] = 0.f;
     }
-    for (int blk = b0; blk < b1; ++blk) {
+    // a block for the first 16 R rows
+    auto step = [&](int blk, auto r_) {
+      constexpr int R = decltype(r_)::value;
       const bool masked = blk * KB + KB - 1 > w.ctx + w.u * p.tpu;
       cp_async_wait<1>();
       __syncthreads();
-      float z[RT][NJ];
+      float z[R][NJ];
 #pragma unroll
-      for (int i = 0; i < RT; ++i)
+      for (int i = 0; i < R; ++i)
 #pragma unroll
         for (int j = 0; j < NJ; ++j) z[i][j] = 0.f;
 #pragma unroll 4
       for (int c = 0; c < CPR; ++c) {
-        float4 q[RT];
+        float4 q[R];
 #pragma unroll
-        for (int i = 0; i < RT; ++i) q[i] = *reinterpret_cast<const float4*>(sq + (ty * RT + i) * C::kLd + c * 4);
+        for (int i = 0; i < R; ++i) q[i] = *reinterpret_cast<const float4*>(sq + (ty + 16 * i) * C::kLd + c * 4);
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
           const float4 k = *reinterpret_cast<const float4*>(sk + (tx + 16 * j) * C::kLd + c * 4);
 #pragma unroll
-          for (int i = 0; i < RT; ++i)
+          for (int i = 0; i < R; ++i)
             z[i][j] = fmaf(q[i].x, k.x, fmaf(q[i].y, k.y, fmaf(q[i].z, k.z, fmaf(q[i].w, k.w, z[i][j]))));
         }
       }
       __syncthreads();
       copy(sk, a.kc, blk + 1);
 #pragma unroll
-      for (int i = 0; i < RT; ++i) {
+      for (int i = 0; i < R; ++i) {
         float bm = -INFINITY;
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
@@ -2127,7 +2132,7 @@ __global__ void __launch_bounds__(256, (CfgF32<D, RT>::kCtas)) prompt_attn_f32_k
         for (int j = 0; j < NJ; ++j) {
           const float e = ex2_approx(z[i][j] - ref);
           sum += e;
-          sp[(ty * RT + i) * C::kLdP + tx + 16 * j] = e;
+          sp[(ty + 16 * i) * C::kLdP + tx + 16 * j] = e;
         }
 #pragma unroll
         for (int d = 8; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
@@ -2143,16 +2148,16 @@ __global__ void __launch_bounds__(256, (CfgF32<D, RT>::kCtas)) prompt_attn_f32_k
       auto weigh = [&](auto keep) {
 #pragma unroll 2
         for (int k = 0; k < KB; k += 4) {
-          float4 e[RT];
+          float4 e[R];
 #pragma unroll
-          for (int i = 0; i < RT; ++i) e[i] = *reinterpret_cast<const float4*>(sp + (ty * RT + i) * C::kLdP + k);
+          for (int i = 0; i < R; ++i) e[i] = *reinterpret_cast<const float4*>(sp + (ty + 16 * i) * C::kLdP + k);
 #pragma unroll
           for (int y = 0; y < 4; ++y)
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
               const float4 v = *reinterpret_cast<const float4*>(sv + (k + y) * C::kLd + c * 64 + tx * 4);
 #pragma unroll
-              for (int i = 0; i < RT; ++i) {
+              for (int i = 0; i < R; ++i) {
                 const float ey = y == 0 ? e[i].x : y == 1 ? e[i].y : y == 2 ? e[i].z : e[i].w;
                 if (!keep(i, k + y)) continue;
                 o[i][4 * c] = fmaf(ey, v.x, o[i][4 * c]);
@@ -2169,11 +2174,17 @@ __global__ void __launch_bounds__(256, (CfgF32<D, RT>::kCtas)) prompt_attn_f32_k
         weigh([](int, int) { return true; });
       __syncthreads();
       copy(sv, a.vc, blk + 1);
+    };
+    for (int blk = b0; blk < b1; ++blk) {
+      if (RT > 1 && rows <= 32)
+        step(blk, std::integral_constant<int, (RT + 1) / 2>());
+      else
+        step(blk, std::integral_constant<int, RT>());
     }
     cp_async_wait<0>();
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
-      const int r = ty * RT + i;
+      const int r = ty + 16 * i;
       if (r >= rows) continue;
       const bool whole = w.slot < 0;
       const size_t orow = ((size_t)w.c0 + w.u * p.tpu + r / p.g) * a.Hq + w.h * p.g + r % p.g;
