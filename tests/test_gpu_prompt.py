@@ -342,6 +342,36 @@ def test_attn_two_tokens_on_average(new, ctx, Hq, Hkv, D, kind):
     check_attn(s, out, lse, dict(bf16=HALF["bf16"], kv4=HALF["fp16"])[kind])
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp32", "kv4"])
+@pytest.mark.parametrize("new,ctx", [([1, 1], [300, 17]), ([70, 3], [0, 40])])
+def test_offsets_past_32_bits(kind, new, ctx):
+    """The same pages far into a large pool: the same bits, appended and attended to."""
+    b = need_gpu()
+    far = {"bf16": 2 ** 18, "fp32": 2 ** 17, "kv4": 2 ** 19}[kind] + 5  # 2^31 elements or 2^32 code bytes
+    kv4 = kind == "kv4"
+    s = make(14, new, ctx, 16, 8, 128, "fp32" if kind == "fp32" else "bf16", kv4=kv4)
+    names = ("k4", "ks", "v4", "vs") if kv4 else ("kc", "vc")
+    big = dict(s, table=torch.where(s["table"] >= 0, s["table"] + far, s["table"]))
+    for n in names:
+        big[n] = torch.empty((far + s["P"],) + tuple(s[n].shape[1:]), dtype=s[n].dtype, device="cuda")
+        big[n][far:] = s[n]
+    rope = b.eagle_rope_table(512, 128, 500000.0)
+    res = []
+    for x in (s, big):
+        q = torch.empty((x["T"], 16, 128), dtype=x["q"].dtype, device="cuda")
+        if kv4:
+            b.eagle_kv_append_kv4(x["q"], x["k"], x["v"], rope, x["cu"], x["ctx"], x["table"], x["k4"], x["ks"], x["v4"],
+                                  x["vs"], q_out=q, status=x["st"])
+        else:
+            b.eagle_kv_append(x["q"], x["k"], x["v"], rope, x["cu"], x["ctx"], x["table"], x["kc"], x["vc"], q_out=q,
+                              status=x["st"])
+        res.append(run_attn(b, dict(x, q=q), kv4))
+    for n in names:
+        assert torch.equal(big[n][far:].view(torch.uint8), s[n].view(torch.uint8))
+    assert torch.equal(res[0][0], res[1][0]) and torch.equal(res[0][1], res[1][1])
+    assert s["st"].item() == 0
+
+
 @pytest.mark.parametrize("kind", ["bf16", "kv4"])
 @pytest.mark.parametrize("new", [[1], [40]])
 def test_attn_growing_scores(new, kind):
