@@ -126,7 +126,8 @@ bool few_rows_f32(int B, int T, int Hq, int Hkv) {
 
 struct PlanParams {
   const int32_t *cu, *ctx;
-  int B, T, Hkv, max_pages, tpu, g, ctas, cap_pieces, cap_slots, min_cut;
+  int B, T, Hkv, max_pages, tpu, g, ctas, cap_pieces, cap_slots;
+  int min_cut, min_cut_short;  // blocks of a piece at least; the latter if no unit has over 16 blocks
   PlanHeader* hdr;
   Piece* pieces;
   Cut* cuts;
@@ -246,7 +247,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanPar
   // candidate x cuts units longer than C_x = all / (share x ctas)
   if (tid < kCand) {
     const long long f = (long long)kShares[tid] * p.ctas;
-    s_C[tid] = f ? (int)max((long long)p.min_cut, (16 * all + f - 1) / f) : 0x7fffffff;
+    s_C[tid] = f ? (int)max((long long)(longest > 16 ? p.min_cut : p.min_cut_short), (16 * all + f - 1) / f) : 0x7fffffff;
   }
   __syncthreads();
   {
@@ -2233,8 +2234,8 @@ Ws attn_ws(const Shape& sh, void* ws) {
           reinterpret_cast<Cut*>(w + sh.off_cuts), reinterpret_cast<float2*>(w + sh.off_ml),
           reinterpret_cast<float*>(w + sh.off_o)};
 }
-void launch_plan(const AttnParams& a, const Shape& sh, const Ws& w, int min_cut, cudaStream_t s) {
-  const PlanParams pp = {a.cu, a.ctx, a.B, a.T, a.Hkv, a.max_pages, sh.tpu, sh.g, sh.ctas, sh.cap_pieces, sh.cap_slots, min_cut,
+void launch_plan(const AttnParams& a, const Shape& sh, const Ws& w, int min_cut, int min_cut_short, cudaStream_t s) {
+  const PlanParams pp = {a.cu, a.ctx, a.B, a.T, a.Hkv, a.max_pages, sh.tpu, sh.g, sh.ctas, sh.cap_pieces, sh.cap_slots, min_cut, min_cut_short,
                          w.hdr, w.pieces, w.cuts, a.status};
   launch(prompt_plan_kernel, 1, kPlanThreads, 0, s, pp);
 }
@@ -2258,7 +2259,9 @@ int attn_launch_few(const AttnParams& a, void* ws, cudaStream_t s) {
   const Ws w = attn_ws(sh, ws);
   constexpr int smem = CfgFew<D, KV4, NG>::kSmem;
   if (!allow_smem(prompt_attn_few_kernel<D, KV4, NG>, smem)) return EAGLE_ERR_CUDA;
-  launch_plan(a, sh, w, 2, s);
+  // a token over 300 keys: 13.7 us in single blocks, 15.2 in pairs; over 1000:
+  // 13.9, 14.9; over 4000, whose 32 pieces are joined: 18.4, 17.5
+  launch_plan(a, sh, w, 2, 1, s);
   const FewParams fp = {a, a.scale * a.k_scale * kLog2e, sh.g, sh.rows, w.hdr, &w.hdr->next, w.pieces, w.cuts, w.ml, w.po};
   launch(prompt_attn_few_kernel<D, KV4, NG>, sh.ctas, kFewThreads, smem, s, fp);
   note_launch(2);
@@ -2280,7 +2283,7 @@ int attn_launch_tc(const AttnParams& a, void* ws, cudaStream_t s) {
                                  64, (uint32_t)sh.g, (uint32_t)sh.tpt))
     return EAGLE_ERR_CUDA;
   if (!allow_smem(prompt_attn_tc_kernel<D, KV4>, (int)C::kSmem)) return EAGLE_ERR_CUDA;
-  launch_plan(a, sh, w, 2, s);
+  launch_plan(a, sh, w, 2, 2, s);
   const MainParams mp = {a, a.scale * a.k_scale * kLog2e, sh.g, sh.tpt, sh.tpu, sh.rows, w.hdr, &w.hdr->next, w.pieces,
                          w.ml, w.po};
   launch(prompt_attn_tc_kernel<D, KV4>, sh.ctas, kThreads, C::kSmem, s, map_q, mp);
@@ -2292,7 +2295,7 @@ int attn_launch_f32(const AttnParams& a, void* ws, cudaStream_t s) {
   const Ws w = attn_ws(sh, ws);
   constexpr int smem = CfgF32<D, RT>::kSmem;
   if (!allow_smem(prompt_attn_f32_kernel<D, RT>, smem)) return EAGLE_ERR_CUDA;
-  launch_plan(a, sh, w, 1, s);
+  launch_plan(a, sh, w, 1, 1, s);
   const F32Params fp = {a, a.scale * kLog2e, sh.g, sh.tpu, sh.rows, w.hdr, &w.hdr->next, w.pieces, w.ml, w.po};
   launch(prompt_attn_f32_kernel<D, RT>, sh.ctas, 256, smem, s, fp);
   return launch_merge<D, float>(a, sh, w, s);
