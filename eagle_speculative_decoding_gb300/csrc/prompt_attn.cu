@@ -1175,6 +1175,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_addr = tmem + lane_addr + (uint32_t)(t * kBlk);
     const uint32_t o_addr = tmem + lane_addr + C::kColO + (uint32_t)(t * D);
     uint32_t sph = 0, oph = 0, xph = 0, tph = 0;
+    bool my_turn_comes = t != 0;  // the other tile's warp passes before this one's next turn (not before tile 0's first)
     int uses = 0;
     bool ok = true;
     Piece w;
@@ -1188,11 +1189,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Two warps of a scheduler, one per tile, take turns at a block's
       // softmax: left alone the tiles fall into step, both in their softmax
       // and then both waiting for their MMAs.  (Not with alternate blocks,
-      // where the MMAs are few.)  Tile 0 goes first; a turn is passed on only
-      // where the other tile has a block to take it.
-      const bool turns = !tw.twin && q4 * 32 < min(tw.rows0, tw.rows1);
-      const int n_wait = !turns ? 0 : t ? min(tw.n0, tw.n1) : min(tw.n0 - 1, tw.n1);  // turns waited for
-      const int n_pass = !turns ? 0 : t ? min(tw.n0 - 1, tw.n1) : min(tw.n0, tw.n1);  // turns passed on
+      // where the MMAs are few.)  Tile 0 goes first, and the turns run on
+      // from piece to piece: each warp waits for the other's last pass before
+      // it passes again, so that no barrier is ever two phases ahead of the
+      // warp that waits on it by parity.  (With a waiting of its own in every
+      // piece, tile 0 could pass at the last block of a piece and at the first
+      // of the next before tile 1 had seen either.)
+      const int turns = !tw.twin && q4 * 32 < min(tw.rows0, tw.rows1) ? min(tw.n0, tw.n1) : 0;
       const int pos0 = __shfl_sync(0xffffffffu, pos, 0);  // the warp's first row sees least
       float m = -INFINITY, l = 0.f, sl2 = p.scale_log2;
       bool fresh = true;  // some row has seen no key yet
@@ -1206,11 +1209,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if (quad_live) {
           if (KV4 && i == 0) sl2 *= row_ok ? sb.q_fac[uses & 1][t][row] : 1.f;
-          if (i >= 1 - t && i < n_wait + 1 - t) {
+          if (i < turns && my_turn_comes) {
             ok = warp_wait(sb.turn[t][q4], tph);
             if (!ok) break;
             tph ^= 1u;
           }
+          my_turn_comes = my_turn_comes || i < turns;
           // m is the reference of O and l.  It need not be the maximum: the
           // weights' type only has to hold 2^(z - m).  So a row takes the
           // maximum of the first keys it sees and keeps it until a block's
@@ -1264,7 +1268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 64; ++k) {
               // half of them issued: the other tile's may start to fill the gaps
-              if (k == 32 && !pass && i < n_pass && lane == 0) mbar_arrive(smem_u32(&sb.turn[t ^ 1][q4]));
+              if (k == 32 && !pass && i < turns && lane == 0) mbar_arrive(smem_u32(&sb.turn[t ^ 1][q4]));
               float e0, e1;
               unpack2(fma2(pack2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])), sc2, nm2), e0, e1);
               e0 = ex2_approx(e0);
