@@ -1655,6 +1655,7 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas(KV4, NG)) prompt_attn_fe
       for (int e = 0; e < 2; ++e) fac[n][e] = __shfl_sync(0xffffffffu, up, 4 * (2 * t + e));
     }
     float o[NG][NT][4], m[NG][2], l[NG][2];  // row 2 t + e of group n: o[n][..][e], o[n][..][2 + e]
+    bool fresh = true;                       // some row has no reference yet
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
       m[n][0] = m[n][1] = -INFINITY;
@@ -1796,12 +1797,15 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas(KV4, NG)) prompt_attn_fe
             for (int e = 0; e < 4; ++e)
               if ((page0 + 4 * (i + z)) * 16 + 8 * (e >> 1) + j >= lim) s[z][n][e] = -INFINITY;
       }
-      // the reference of a row is the maximum of the first step; it is renewed
-      // when a step's weights pass kSumLimit (or are NaN), see the kernel above
+      // the reference of a row is the maximum of the first step that has a
+      // finite score for it; it is renewed when a step's weights pass kSumLimit
+      // (or are NaN), see the kernel above
       float wt[NP][NG][4];
-      bool renew = i == 0, mine[NG][2];  // by row, the same in its eight lanes
+      bool renew = fresh, mine[NG][2];  // by row, the same in its eight lanes
 #pragma unroll
-      for (int n = 0; n < NG; ++n) mine[n][0] = mine[n][1] = true;
+      for (int n = 0; n < NG; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) mine[n][e] = m[n][e] == -INFINITY;
 #pragma unroll 1
       for (int pass = 0;; ++pass) {
         if (renew) {
@@ -1828,6 +1832,12 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas(KV4, NG)) prompt_attn_fe
                 m[n][e] = bm;
               }
             }
+          if (fresh) {
+            bool none = false;
+#pragma unroll
+            for (int n = 0; n < NG; ++n) none = none || m[n][0] == -INFINITY || m[n][1] == -INFINITY;
+            fresh = __any_sync(0xffffffffu, none);
+          }
         }
         float sum[NG][2];
         bool over = false;

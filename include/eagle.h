@@ -774,6 +774,8 @@ int eagle_kv4_read(const uint8_t* codes, const uint8_t* scales, float scale, int
  *   out  : [T, Hq, D] dtype `dtype`;  lse : [T, Hq] fp32 or NULL
  * Keys past a row's position never reach its result, whatever their pages
  * hold (NaN included), nor do the unused slots of a last page.
+ * A row whose scores are all minus infinity gives zeros and an lse of minus
+ * infinity; scores of minus infinity beside finite ones weigh nothing.
  * T = 0 does nothing.  Device-detected: a malformed cu_seqlens or a negative
  * ctx_lens -> EAGLE_ERR_INVALID_ARG, more tokens than the block table holds
  * -> EAGLE_ERR_BAD_KV (the request is skipped, its rows are not written); a

@@ -1,6 +1,7 @@
 """GPU parity of the prompt path where it is easily got wrong: many pieces per
 CTA, scores at the ends of their range, malformed lengths.  Helpers and
 tolerances are those of test_gpu_prompt."""
+import numpy as np
 import pytest
 import torch
 
@@ -62,3 +63,58 @@ def test_attn_many_two_tile_pieces_per_cta(kind, D, back):
     check_attn(s, out, lse, WEIGHT_HALF[kind])
     again, lse2 = run_attn(b, s, kind == "kv4")
     assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16", "kv4"])
+@pytest.mark.parametrize("n,count,ctx", [(1, 40, 600), (1, 3, 3000), (2, 5, 700), (40, 3, 500)])
+def test_attn_first_keys_of_minus_infinity(kind, n, count, ctx):
+    """Scores of minus infinity over the first 128 + 64 keys, a plain softmax
+    over the others: a row has no reference until it meets a finite score."""
+    b = need_gpu()
+    Hq, Hkv, D, low = 16, 8, 64, 192
+    s = make(41 + n, [n] * count, [ctx] * count, Hq, Hkv, D, "fp32" if kind == "fp32" else "bf16", kv4=kind == "kv4")
+    # channel 0 alone carries the scores: 2^119 * 2 * -6 overflows to minus
+    # infinity, and the other keys have 0 there
+    q = torch.zeros(s["T"], Hq, D)
+    q[..., 0] = 2.0
+    s["q"] = q.to(s["q"].dtype).cuda()
+    key = torch.zeros(ctx + n, Hkv, D)
+    key[:low, :, 0] = -2688.0
+    set_keys(s, kind, [key] * count)
+    assert (s["kc_np"][s["table"][0, 0].item(), 0, :, 0] < -2000).all()
+    out, lse = run_attn(b, s, kind == "kv4", scale=2.0 ** 119)
+    # the softmax over what is left, all scores 0
+    v = [x[low:] for x in (s["vc_np"][t].reshape(-1, Hkv, D) for t in s["table"].cpu().numpy())]
+    half = HALF["fp32"] if kind == "fp32" else HALF["bf16"]
+    for r in range(s["T"]):
+        seen = ctx + r % n + 1 - low
+        x = np.repeat(v[r // n][:seen], Hq // Hkv, 1)
+        want, mag = x.mean(0), np.abs(x).mean(0)
+        err = np.abs(f64(out[r]) - want)
+        assert (err <= half * np.abs(want) + (WEIGHT_HALF[kind] + (ctx + 16) * 2.0 ** -24) * mag).all()
+        assert np.abs(f64(lse[r]) - np.log(seen)).max() <= 2.0 ** -20
+    assert s["st"].item() == 0
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16", "kv4"])
+@pytest.mark.parametrize("new,ctx", [([1] * 3, [5, 300, 2500]), ([40, 3, 70], [0, 300, 260])])
+def test_attn_rows_whose_scores_are_all_minus_infinity(kind, new, ctx):
+    """Such a row gives zeros and an lse of minus infinity; its neighbours are as they were."""
+    b = need_gpu()
+    Hq, Hkv, D = 8, 4, 128
+    s = make(43, new, ctx, Hq, Hkv, D, "fp32" if kind == "fp32" else "bf16", kv4=kind == "kv4")
+    key = [torch.randn(c + n, Hkv, D, generator=torch.Generator().manual_seed(c)) for n, c in zip(new, ctx)]
+    for k in key:
+        k[..., 0] = 8.0
+    set_keys(s, kind, key)
+    clean, clse = run_attn(b, s, kind == "kv4")
+    dead = torch.zeros(s["T"], Hq, dtype=torch.bool, device="cuda")
+    dead[1::3, 2] = dead[0, 7] = dead[2, :] = True
+    q = s["q"].clone()
+    q[dead] = 0
+    q[..., 0] = torch.where(dead, torch.full_like(q[..., 0], -float("inf")), q[..., 0])
+    s["q"] = q
+    # every dead row's score is -inf * 8 + 0 * k = -inf: no NaN among its products
+    out, lse = run_attn(b, s, kind == "kv4")
+    assert (out[dead] == 0).all() and (lse[dead] == -float("inf")).all()
+    assert torch.equal(out[~dead], clean[~dead]) and torch.equal(lse[~dead], clse[~dead])
