@@ -572,6 +572,15 @@ __device__ __forceinline__ uint32_t pack16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// 4-bit pages: a row of q goes to fp16 divided by 2^row_exponent, which brings
+// its largest magnitude (the bits `mx` of a bf16) to [1, 2); 0 for a row of zeros.
+__device__ __forceinline__ int row_exponent(uint32_t mx) {
+  return mx ? min(126, max(-126, (int)(mx >> 7) - 127)) : 0;
+}
+// What its scores are then multiplied by: never 0, which would make NaN of a
+// masked score (no score of a row with a factor this small leaves a weight of 1).
+__device__ __forceinline__ float row_factor(float scale_log2, float power) { return fmaxf(scale_log2 * power, 1.17549435e-38f); }
+
 // Eight 4-bit codes as four fp16 pairs times the pair `s`.
 __device__ __forceinline__ void kv4_expand(uint32_t w, uint32_t s, uint32_t* v) {
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
@@ -1135,7 +1144,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int k = 0; k < 4; ++k) mx = max(mx, max(e[k] & 0x7fffu, (e[k] >> 16) & 0x7fffu));
 #pragma unroll
                 for (int d = CPR / 2; d; d >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                const int k2 = min(126, max(-126, (int)(mx >> 7) - 127));
+                const int k2 = row_exponent(mx);
                 const float down = __uint_as_float((uint32_t)(127 - k2) << 23);
                 uint32_t h[4];
 #pragma unroll
@@ -1208,7 +1217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         sph ^= 1u;
         tc_fence_after();
         if (quad_live) {
-          if (KV4 && i == 0) sl2 *= row_ok ? sb.q_fac[uses & 1][t][row] : 1.f;
+          if (KV4 && i == 0) sl2 = row_factor(sl2, row_ok ? sb.q_fac[uses & 1][t][row] : 1.f);
           if (i < turns && my_turn_comes) {
             ok = warp_wait(sb.turn[t][q4], tph);
             if (!ok) break;
@@ -1644,9 +1653,9 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas(KV4, NG)) prompt_attn_fe
         for (int i = 0; i < D / 8; ++i) mx = max(mx, max(q[n][i] & 0x7fffu, (q[n][i] >> 16) & 0x7fffu));
         mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const int k2 = min(126, max(-126, (int)(mx >> 7) - 127));
+        const int k2 = row_exponent(mx);
         const float down = __uint_as_float((uint32_t)(127 - k2) << 23);
-        up *= __uint_as_float((uint32_t)(127 + k2) << 23);
+        up = row_factor(up, __uint_as_float((uint32_t)(127 + k2) << 23));
 #pragma unroll
         for (int i = 0; i < D / 8; ++i)
           q[n][i] = pack16<true>(__uint_as_float(q[n][i] << 16) * down, __uint_as_float(q[n][i] & 0xffff0000u) * down);

@@ -118,3 +118,18 @@ def test_attn_rows_whose_scores_are_all_minus_infinity(kind, new, ctx):
     out, lse = run_attn(b, s, kind == "kv4")
     assert (out[dead] == 0).all() and (lse[dead] == -float("inf")).all()
     assert torch.equal(out[~dead], clean[~dead]) and torch.equal(lse[~dead], clse[~dead])
+
+
+@pytest.mark.parametrize("new,ctx", [([1] * 5, [3, 40, 300, 200, 1000]), ([40, 9, 150], [100, 0, 260])])
+@pytest.mark.parametrize("k_scale", [1.0, 2.0 ** -24, 2.0 ** -60])
+def test_attn_kv4_rows_of_zeros(new, ctx, k_scale):
+    """A query of zeros, or one whose factor leaves fp32's range, weighs every key alike."""
+    b = need_gpu()
+    s = make(47, new, ctx, 8, 2, 128, "bf16", kv4=True)
+    q = s["q"].clone()
+    q[::2, 1::2] = 0.0
+    q[1::2, ::3] *= 2.0 ** -120
+    q[0, 0] = 2.0 ** -130  # below bf16's normal numbers
+    s["q"] = q
+    out, lse = run_attn(b, s, True, ks=k_scale)
+    check_attn(s, out, lse, HALF["fp16"], ks=k_scale)
