@@ -144,7 +144,7 @@ constexpr int kPlanThreads = 512;
 // prompt, 12.7 us for 64 requests cut into some 1,700 pieces.
 __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanParams p) {
   __shared__ unsigned long long s_total;
-  __shared__ int s_longest, s_C[kCand], s_n[kCand], s_cut[kCand], s_hist[32], s_cursor[32], s_c, s_slots, s_cuts, s_most;
+  __shared__ int s_longest, s_C[kCand], s_n[kCand], s_cut[kCand], s_hist[32], s_cursor[32], s_c, s_slots, s_cuts, s_most, s_falls;
   __shared__ int s_c0[kPlanThreads], s_len[kPlanThreads], s_ctx[kPlanThreads], s_end[kPlanThreads], s_warp[kPlanThreads / 32];
   struct Unit {
     int at, k, slot, cut, o, u, len, extra;
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanPar
   if (tid < kCand) s_n[tid] = s_cut[tid] = 0;
   if (tid == 0) {
     s_total = 0;
-    s_longest = s_slots = s_cuts = s_most = 0;
+    s_longest = s_slots = s_cuts = s_most = s_falls = 0;
   }
   pdl_wait();
   pdl_trigger();
@@ -164,13 +164,15 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanPar
   // requests base .. base + 511 into shared memory; s_end: inclusive prefix of their units
   auto load = [&](int base, bool report) {
     int c0 = 0, n = 0, ctx = 0;
+    bool falls = false;
     const int b = base + tid;
     if (b < p.B) {
       c0 = p.cu[b];
       const int c1 = p.cu[b + 1];
       ctx = p.ctx[b];
       n = c1 - c0;
-      if (c0 < 0 || c1 < c0 || c1 > p.T || ctx < 0) {
+      falls = c1 < c0;
+      if (c0 < 0 || falls || c1 > p.T || ctx < 0) {
         if (report) set_status(p.status, EAGLE_ERR_INVALID_ARG);
         n = 0;
       } else if ((long long)ctx + n > 16ll * p.max_pages) {
@@ -185,7 +187,9 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanPar
       if (lane >= d) end += x;
     }
     if (lane == 31) s_warp[warp] = end;
-    __syncthreads();
+    // where cu_seqlens falls, requests may claim the same rows again and again:
+    // no room is laid out for that, and nothing is listed
+    if (__syncthreads_or(falls) && tid == 0) s_falls = 1;
     int before = lane < warp ? s_warp[lane] : 0;  // warps are fewer than lanes
     before = (int)__reduce_add_sync(0xffffffffu, (unsigned)before);
     s_c0[tid] = c0;
@@ -242,6 +246,10 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanPar
     }
   }
   __syncthreads();
+  if (s_falls) {
+    if (tid == 0) *p.hdr = PlanHeader{0, 0, p.ctas, 0};
+    return;
+  }
   const long long all = (long long)s_total * p.Hkv;  // key blocks of all units
   const int longest = s_longest;
   // candidate x cuts units longer than C_x = all / (share x ctas)
@@ -312,10 +320,8 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanPar
     }
     s_cursor[lane] = end - v;
     if (lane == 31) {
-      // a malformed cu_seqlens can list rows twice: what does not fit is left out
       p.hdr->pieces = min(end, p.cap_pieces);
       p.hdr->next = p.ctas;  // the first piece of each CTA is its own index
-      if (end > p.cap_pieces) set_status(p.status, EAGLE_ERR_INVALID_ARG);
     }
   }
   __syncthreads();
@@ -366,7 +372,9 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanPar
         const Unit w = s_unit[i];
         const int j = q - (s_pend[i] - w.k * p.Hkv), h = w.k > 1 ? j / w.k : j, x = j - h * w.k;
         const int k0 = x * w.len + min(x, w.extra), c0 = s_c0[w.o], n = s_len[w.o];
-        if (w.at + j < p.cap_pieces)
+        // (the list has room for every cu_seqlens that does not fall; this is for
+        // one that is overwritten during the call)
+        if ((unsigned)(w.at + j) < (unsigned)p.cap_pieces)
           p.pieces[w.at + j] = Piece{base + w.o, h, w.u, k0, k0 + w.len + (x < w.extra ? 1 : 0), w.k > 1 ? w.slot + j : -1,
                                      c0, n, s_ctx[w.o], w.cut + h, w.slot + h * w.k, w.k};
         if (w.k > 1 && x == 0) p.cuts[w.cut + h] = Cut{h, w.u, w.slot + j, w.k, c0, n, 0, 0};

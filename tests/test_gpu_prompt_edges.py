@@ -133,3 +133,21 @@ def test_attn_kv4_rows_of_zeros(new, ctx, k_scale):
     s["q"] = q
     out, lse = run_attn(b, s, True, ks=k_scale)
     check_attn(s, out, lse, HALF["fp16"], ks=k_scale)
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16", "kv4"])
+@pytest.mark.parametrize("cu,per", [([0, 6, 3, 8], 0), ([0, 8, 0, 8], 0), ([3, 0, 8, 8], 0), (None, 1), (None, 30)])
+def test_attn_lists_nothing_where_cu_seqlens_falls(kind, cu, per):
+    """A cu_seqlens that falls lets requests claim rows many times over: nothing is
+    listed (the longest here would be 4096 requests of all rows), nothing written."""
+    b = need_gpu()
+    B = 3 if cu else 8192
+    s = make(61, [3, 3, 2], [20, 300, 0], 8, 8, 64, "fp32" if kind == "fp32" else "bf16", kv4=kind == "kv4")
+    if cu is None:
+        T = per * B
+        cu = [T * (i % 2) for i in range(B + 1)]
+        s.update(T=T, q=torch.zeros(T, 8, 64, dtype=s["q"].dtype, device="cuda"), ctx=torch.zeros(B, dtype=torch.int32).cuda(),
+                 table=torch.zeros(B, -(-T // 16), dtype=torch.int32).cuda())
+    s["cu"] = torch.tensor(cu, dtype=torch.int32).cuda()
+    out, lse = run_attn(b, s, kind == "kv4")
+    assert s["st"].item() == 1 and (out == 7.0).all() and (lse == 7.0).all()
