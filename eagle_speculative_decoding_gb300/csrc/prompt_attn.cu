@@ -179,6 +179,8 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanPar
         if (report) set_status(p.status, EAGLE_ERR_BAD_KV);
         n = 0;
       }
+      // rows in front of the first request or behind the last belong to none
+      if (report && ((b == 0 && c0 != 0) || (b == p.B - 1 && c1 != p.T))) set_status(p.status, EAGLE_ERR_INVALID_ARG);
     }
     int end = (n + p.tpu - 1) / p.tpu;
 #pragma unroll

@@ -780,8 +780,10 @@ int eagle_kv4_read(const uint8_t* codes, const uint8_t* scales, float scale, int
  * -> EAGLE_ERR_INVALID_ARG (no row is written); one with an entry outside
  * 0 .. T or a negative ctx_lens -> EAGLE_ERR_INVALID_ARG, more tokens than the
  * block table holds -> EAGLE_ERR_BAD_KV (the request is skipped, its rows are
- * not written); a page id out of range -> EAGLE_ERR_BAD_KV (its keys and
- * values read as zeros).
+ * not written); cu_seqlens[0] != 0 or cu_seqlens[B] != T ->
+ * EAGLE_ERR_INVALID_ARG (the rows of no request are not written, the others
+ * are); a page id out of range -> EAGLE_ERR_BAD_KV (its keys and values read
+ * as zeros).
  * bf16 runs on the tensor cores with fp32 accumulation and fp32 softmax
  * statistics; fp32 on the CUDA cores in fp32 arithmetic.
  * Limits: D in {64, 128}, page_size == 16, Hq % Hkv == 0, Hq / Hkv <= 64,

@@ -136,6 +136,26 @@ def test_attn_kv4_rows_of_zeros(new, ctx, k_scale):
 
 
 @pytest.mark.parametrize("kind", ["fp32", "bf16", "kv4"])
+@pytest.mark.parametrize("n", [1, 30])
+@pytest.mark.parametrize("lead,trail", [(2, 0), (0, 3), (1, 1)])
+def test_attn_reports_rows_outside_every_request(kind, n, lead, trail):
+    """cu_seqlens that starts late or ends early: reported, the requests' own rows are right, the others left alone."""
+    b = need_gpu()
+    Hkv = 2
+    s = make(59, [n, n, n], [20, 300, 0], 8, Hkv, 64, "fp32" if kind == "fp32" else "bf16", kv4=kind == "kv4")
+    pad = lambda k: torch.zeros(k, *s["q"].shape[1:], dtype=s["q"].dtype, device="cuda")  # noqa: E731
+    x = dict(s, T=3 * n + lead + trail, q=torch.cat([pad(lead), s["q"], pad(trail)]), cu=s["cu"] + lead)
+    out, lse = run_attn(b, x, kind == "kv4")
+    assert s["st"].item() == 1
+    s["st"].zero_()
+    rows = slice(lead, lead + 3 * n)
+    check_attn(s, out[rows], lse[rows], WEIGHT_HALF[kind])
+    outside = torch.ones(x["T"], dtype=torch.bool)
+    outside[rows] = False
+    assert (out[outside.cuda()] == 7.0).all() and (lse[outside.cuda()] == 7.0).all()
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16", "kv4"])
 @pytest.mark.parametrize("cu,per", [([0, 6, 3, 8], 0), ([0, 8, 0, 8], 0), ([3, 0, 8, 8], 0), (None, 1), (None, 30)])
 def test_attn_lists_nothing_where_cu_seqlens_falls(kind, cu, per):
     """A cu_seqlens that falls lets requests claim rows many times over: nothing is
