@@ -37,6 +37,7 @@ namespace {
 
 constexpr int kBlk = 128;        // keys per block
 constexpr int kTileRows = 128;   // query rows per tile
+constexpr int kMaxPages = 1 << 26;  // of a cache, and of a request
 constexpr int kF32Rows = 64, kF32Few = 16;  // query rows per unit of the fp32 path, and when they are few
 constexpr int kF32FewCtas = 2;               // CTAs per SM then
 constexpr float kSumLimit = 256.f;  // of a block's weights: far below fp16's 65504
@@ -2247,7 +2248,7 @@ int attn_check(const AttnParams& p, int D, int page_size, size_t es) {
   if (!(p.scale > 0.f) || !isfinite(p.scale) || !(p.k_scale > 0.f) || !(p.v_scale > 0.f) || !isfinite(p.k_scale) ||
       !isfinite(p.v_scale))
     return EAGLE_ERR_INVALID_ARG;
-  if ((D != 64 && D != 128) || page_size != 16 || p.Hq / p.Hkv > 64 || p.B > 65535 || p.num_pages > (1 << 26))
+  if ((D != 64 && D != 128) || page_size != 16 || p.Hq / p.Hkv > 64 || p.B > 65535 || p.num_pages > kMaxPages)
     return EAGLE_ERR_UNSUPPORTED;
   if (p.q_stride < (long long)p.Hq * D || p.q_stride % (long long)(16 / es)) return EAGLE_ERR_INVALID_ARG;
   if (!aligned16(p.q) || !aligned16(p.kc) || !aligned16(p.vc) || !aligned16(p.out)) return EAGLE_ERR_INVALID_ARG;
@@ -2268,7 +2269,10 @@ Ws attn_ws(const Shape& sh, void* ws) {
           reinterpret_cast<float*>(w + sh.off_o)};
 }
 void launch_plan(const AttnParams& a, const Shape& sh, const Ws& w, int min_cut, int min_cut_short, cudaStream_t s) {
-  const PlanParams pp = {a.cu, a.ctx, a.B, a.T, a.Hkv, a.max_pages, sh.tpu, sh.g, sh.ctas, sh.cap_pieces, sh.cap_slots, min_cut, min_cut_short,
+  // a request ends at 2^30 tokens (the pages that ids can name), so that
+  // positions and their blocks' ends stay below 2^31
+  const int max_pages = std::min(a.max_pages, kMaxPages);
+  const PlanParams pp = {a.cu, a.ctx, a.B, a.T, a.Hkv, max_pages, sh.tpu, sh.g, sh.ctas, sh.cap_pieces, sh.cap_slots, min_cut, min_cut_short,
                          w.hdr, w.pieces, w.cuts, a.status};
   launch(prompt_plan_kernel, 1, kPlanThreads, 0, s, pp);
 }

@@ -779,8 +779,8 @@ int eagle_kv4_read(const uint8_t* codes, const uint8_t* scales, float scale, int
  * T = 0 does nothing.  Device-detected: a cu_seqlens that falls somewhere
  * -> EAGLE_ERR_INVALID_ARG (no row is written); one with an entry outside
  * 0 .. T or a negative ctx_lens -> EAGLE_ERR_INVALID_ARG, more tokens than the
- * block table holds -> EAGLE_ERR_BAD_KV (the request is skipped, its rows are
- * not written); cu_seqlens[0] != 0 or cu_seqlens[B] != T ->
+ * block table holds or than 2^30 -> EAGLE_ERR_BAD_KV (the request is skipped,
+ * its rows are not written); cu_seqlens[0] != 0 or cu_seqlens[B] != T ->
  * EAGLE_ERR_INVALID_ARG (the rows of no request are not written, the others
  * are); a page id out of range -> EAGLE_ERR_BAD_KV (its keys and values read
  * as zeros).

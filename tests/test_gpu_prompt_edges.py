@@ -171,3 +171,19 @@ def test_attn_lists_nothing_where_cu_seqlens_falls(kind, cu, per):
     s["cu"] = torch.tensor(cu, dtype=torch.int32).cuda()
     out, lse = run_attn(b, s, kind == "kv4")
     assert s["st"].item() == 1 and (out == 7.0).all() and (lse == 7.0).all()
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16", "kv4"])
+@pytest.mark.parametrize("n,ctx", [(1, 2 ** 31 - 1), (20, 2 ** 31 - 8), (20, 2 ** 30 - 10), (1, 2 ** 30)])
+def test_attn_refuses_positions_past_its_range(kind, n, ctx):
+    """A block table wide enough for more positions than 32 bits count."""
+    b = need_gpu()
+    s = make(67, [n, 3], [0, 40], 8, 2, 64, "fp32" if kind == "fp32" else "bf16", kv4=kind == "kv4")
+    wide = torch.zeros(2, 2 ** 27 + 2, dtype=torch.int32, device="cuda")
+    wide[:, :s["table"].shape[1]] = s["table"]
+    clean, _ = run_attn(b, s, kind == "kv4")
+    s["table"] = wide
+    s["ctx"][0] = ctx
+    out, lse = run_attn(b, s, kind == "kv4")
+    assert s["st"].item() == 6 and (out[:n] == 7.0).all() and (lse[:n] == 7.0).all()
+    assert torch.equal(out[n:], clean[n:])
