@@ -1177,8 +1177,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         release_piece(ps);
       }
-      // (on abort) no box may land in the memory of the SM's next CTA
-      if (!KV4 && !ok) {
+      // no box may land in the memory of the SM's next CTA: done already, but
+      // after an abort, which may show as a failed wait here or as a list
+      // that ends early
+      if (!KV4) {
         const unsigned long long t0 = globaltimer_ns();
         for (int t = 0; t < 2; ++t)
           while (uses[t] && !mbar_try_wait(smem_u32(&sb.q_full[t]), (uint32_t)(uses[t] - 1) & 1u) &&
