@@ -1328,6 +1328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (join) {
         if (t == 1) {
           sb.x_ml[row] = make_float2(m, l);
+          tc_fence_before();  // tile 0's warps read this tile's O after their fence
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sb.x_stat));
         } else {
