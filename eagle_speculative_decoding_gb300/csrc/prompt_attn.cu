@@ -40,7 +40,17 @@ constexpr int kTileRows = 128;   // query rows per tile
 constexpr int kMaxPages = 1 << 26;  // of a cache, and of a request
 constexpr int kF32Rows = 64, kF32Few = 16;  // query rows per unit of the fp32 path, and when they are few
 constexpr int kF32FewCtas = 2;               // CTAs per SM then
-constexpr float kSumLimit = 256.f;  // of a block's weights: far below fp16's 65504
+// A row's reference lies kBelow under the maximum that it is taken from, and holds
+// until a block's weights add up to more than kSumLimit.  fp16 (4-bit pages) ends
+// at 65504 and loses bits below 2^-14: references 7 under the maximum put those
+// at 2^-21 of the largest weight and the smallest step's half at 2^-32, so that a
+// long tail of small weights behind one large key still counts (with kBelow 0 and
+// a limit of 256, weights under 2^-25 were zeros beside a sum that had them).
+// 128 first weights add up to 2^14 at most.  bf16 keeps its 8 bits anywhere.
+template <bool F16>
+constexpr float kBelow = F16 ? 7.f : 0.f;
+template <bool F16>
+constexpr float kSumLimit = F16 ? 32768.f : 256.f;
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 
 struct AttnParams {
@@ -1238,8 +1248,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           my_turn_comes = my_turn_comes || i < turns;
           // m is the reference of O and l.  It need not be the maximum: the
-          // weights' type only has to hold 2^(z - m).  So a row takes the
-          // maximum of the first keys it sees and keeps it until a block's
+          // weights' type only has to hold 2^(z - m).  So a row takes (kBelow
+          // under) the maximum of the first keys it sees and keeps it until a block's
           // weights add up to more than kSumLimit; then (and for NaN) the
           // block's maximum is looked for, and O and l are rescaled.  (Only
           // the row itself decides, so its result does not depend on the rows
@@ -1266,7 +1276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int c = 8; c < kBlk; c += 8)
 #pragma unroll
                 for (int y = 0; y < 4; ++y) mx[y] = max3(mx[y], __uint_as_float(r[c + y]), __uint_as_float(r[c + y + 4]));
-              const float bm = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * sl2;
+              const float bm = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * sl2 - kBelow<KV4>;
               const bool resc = mine && bm > m && m != -INFINITY;
               if (__any_sync(0xffffffffu, resc)) {
                 // S(i) was issued after P V(i - 1): O is still
@@ -1302,7 +1312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             unpack2(add2(add2(ls[0], ls[1]), add2(ls[2], ls[3])), l0, l1);
             l0 += l1;
             if (pass) break;
-            mine = row_ok && !(l0 <= kSumLimit);
+            mine = row_ok && !(l0 <= kSumLimit<KV4>);
             renew = __any_sync(0xffffffffu, mine);
             if (!renew) break;
           }
@@ -1841,7 +1851,7 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas(KV4, NG)) prompt_attn_fe
               for (int z = 0; z < NP; ++z) bm = fmaxf(bm, fmaxf(s[z][n][e], s[z][n][2 + e]));
 #pragma unroll
               for (int d = 4; d < 32; d <<= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, d));
-              bm *= fac[n][e];
+              bm = bm * fac[n][e] - kBelow<KV4>;
               if (mine[n][e] && bm > m[n][e]) {
                 if (m[n][e] != -INFINITY) {
                   const float alpha = ex2_approx(m[n][e] - bm);
@@ -1878,7 +1888,7 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas(KV4, NG)) prompt_attn_fe
                 wt[z][n][2 * x + e] = f;
                 sum[n][e] += f;
               }
-            over = over || !(sum[n][e] <= kSumLimit);
+            over = over || !(sum[n][e] <= kSumLimit<KV4>);
           }
         if (pass || !__any_sync(0xffffffffu, over)) {
 #pragma unroll
@@ -1893,7 +1903,7 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas(KV4, NG)) prompt_attn_fe
         for (int n = 0; n < NG; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            mine[n][e] = (__ballot_sync(0xffffffffu, !(sum[n][e] <= kSumLimit)) >> t & 0x11111111u) != 0;
+            mine[n][e] = (__ballot_sync(0xffffffffu, !(sum[n][e] <= kSumLimit<KV4>)) >> t & 0x11111111u) != 0;
       }
 #pragma unroll
       for (int z = 0; z < NP; ++z) {

@@ -785,7 +785,9 @@ int eagle_kv4_read(const uint8_t* codes, const uint8_t* scales, float scale, int
  * are); a page id out of range -> EAGLE_ERR_BAD_KV (its keys and values read
  * as zeros).
  * bf16 runs on the tensor cores with fp32 accumulation and fp32 softmax
- * statistics; fp32 on the CUDA cores in fp32 arithmetic.
+ * statistics; the weights are rounded to bf16 for the product with V (2^-8 of
+ * sum w |v| at most), the statistics take them unrounded.  fp32 runs on the
+ * CUDA cores in fp32 arithmetic.
  * Limits: D in {64, 128}, page_size == 16, Hq % Hkv == 0, Hq / Hkv <= 64,
  * B <= 65535, scale finite and > 0; q 16-byte aligned, q_stride a multiple of
  * 16 bytes. */
@@ -797,8 +799,11 @@ int eagle_prompt_attn(const void* q, long long q_stride, const void* k_cache, co
                       void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
 
 /* eagle_prompt_attn_kv4 -- eagle_prompt_attn over 4-bit pages; q and out bf16.
- * A code times its scale byte is exact in 16 bits, so the products are those
- * of the values the codes stand for.  Same workspace query; k_scale and
+ * A code times its scale byte is exact in fp16, so the products are those of
+ * the values the codes stand for.  Rounded to fp16: a row of q, divided by a
+ * power of two (nothing is lost above 2^-14 of its largest element, 2^-25 of
+ * that below), and the weights (2^-11 of each; 2^-32 of the row's sum for those
+ * below 2^-21 of the first maximum).  Same workspace query; k_scale and
  * v_scale finite and > 0; codes and scales 16-byte aligned. */
 int eagle_prompt_attn_kv4(const void* q, long long q_stride, const uint8_t* k_codes,
                           const uint8_t* k_scales, const uint8_t* v_codes, const uint8_t* v_scales,

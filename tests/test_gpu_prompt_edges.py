@@ -135,6 +135,40 @@ def test_attn_kv4_rows_of_zeros(new, ctx, k_scale):
     check_attn(s, out, lse, HALF["fp16"], ks=k_scale)
 
 
+@pytest.mark.parametrize("n,count,ctx", [(1, 20, 16383), (40, 8, 16300)])
+@pytest.mark.parametrize("kind", ["bf16", "kv4"])
+@pytest.mark.parametrize("down", [20.3, 25.7])
+def test_attn_leading_key_over_a_flat_tail(kind, n, count, ctx, down):
+    """One key outweighs each of a long tail by 2^down, and its value is zero:
+    the output is the tail's.  fp16 holds a weight 2^(z - m) with m 7 below the
+    first maximum, so beside its 2^-11 a weight is off by at most half of
+    fp16's smallest step, 2^-25, relative to a sum of at least 2^7."""
+    b = need_gpu()
+    Hq, Hkv, D = 16, 8, 64
+    s = make(53, [n], [ctx], Hq, Hkv, D, "bf16", kv4=kind == "kv4")
+    k, v = torch.zeros(ctx + n, Hkv, D), torch.randn(ctx + n, Hkv, D, generator=torch.Generator().manual_seed(3)) + 1
+    k[0], v[0] = 1.0, 0.0
+    set_keys(s, kind, [k])
+    set_keys(s, kind, [v], "v")
+    # the same pages for every request, so that the pieces are long
+    T = n * count
+    near = 1 + 0.002 * torch.randn(T, Hq, D, generator=torch.Generator().manual_seed(4))
+    s.update(T=T, q=(near * down * float(np.log(2)) / (D ** 0.5 * s["kc_np"][s["table"][0, 0].item(), 0, 0, 0])).bfloat16().cuda(),
+             table=s["table"].repeat(count, 1).contiguous(), cu=torch.arange(count + 1, dtype=torch.int32).cuda() * n,
+             ctx=s["ctx"].repeat(count))
+    out, lse = run_attn(b, s, kind == "kv4")
+    keys, values = (f64(torch.from_numpy(s[x]))[s["table"][0].cpu().numpy()].reshape(-1, Hkv, D) for x in ("kc_np", "vc_np"))
+    want, wl, mag, dot = oracle.prompt_attn(f64(s["q"]), [keys] * count, [values] * count, s["cu"].cpu().numpy(),
+                                            s["ctx"].cpu().numpy(), D ** -0.5)
+    dz = (D + 8) * 2.0 ** -24 * dot
+    arith = 2 * dz + (ctx + 16) * 2.0 ** -24
+    small = 0.0 if kind == "bf16" else 2.0 ** -32 * np.abs(values).sum(0).max()
+    err = np.abs(f64(out) - want)
+    bound = HALF["bf16"] * np.abs(want) + (WEIGHT_HALF[kind] + arith)[..., None] * mag + small
+    print(f"worst error / bound {float((err / bound).max()):.3f}, of the output {float((err / np.abs(want).max()).max()):.2e}")
+    assert (err <= bound).all() and s["st"].item() == 0
+
+
 @pytest.mark.parametrize("kind", ["fp32", "bf16", "kv4"])
 @pytest.mark.parametrize("n", [1, 30])
 @pytest.mark.parametrize("lead,trail", [(2, 0), (0, 3), (1, 1)])
