@@ -485,23 +485,107 @@ def _row_stride(name, t, D):
     return rows
 
 
+# The kernels check lengths and page ids, but take the arrays' own shapes, types
+# and layouts from the arguments that are derived below; an array that is not as
+# those say would be read, or its neighbours written, out of place.  Every
+# attribute of a tensor costs some 60 ns or more, so each is taken once, and the
+# conditions stand in line.
+_I32, _F32 = torch.int32, torch.float32
+_BYTES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _lengths(rows, cu_seqlens, ctx_lens, block_table, status):
+    """Last of a call's checks, those of the index arrays, and that they (the
+    ones that are built on the host) and the rows are on the GPU: (B, max_pages)."""
+    if not (cu_seqlens.dtype is _I32 and ctx_lens.dtype is _I32 and block_table.dtype is _I32
+            and cu_seqlens.is_contiguous() and ctx_lens.is_contiguous() and block_table.is_contiguous()):
+        raise ValueError("cu_seqlens, ctx_lens and block_table must be contiguous int32")
+    B, pages = block_table.shape
+    if ctx_lens.shape != (B,) or cu_seqlens.shape != (B + 1,):
+        raise ValueError("cu_seqlens must be [B + 1], ctx_lens [B] and block_table [B, max_pages]")
+    if status is not None and status.dtype is not _I32:
+        raise ValueError("status must be int32")
+    if not (rows.is_cuda and cu_seqlens.is_cuda and ctx_lens.is_cuda and block_table.is_cuda):
+        raise ValueError("the arrays must be on the GPU")
+    return B, pages
+
+
+def _pages16(k_cache, v_cache, Hkv, D, dtype):
+    """Checks of 16- or 32-bit pages: their number."""
+    shape = k_cache.shape
+    if v_cache.shape != shape or shape != (shape[0], 16, Hkv, D):
+        raise ValueError("k_cache and v_cache must be [pages, 16, Hkv, D]")
+    if not (k_cache.dtype is dtype and v_cache.dtype is dtype and k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError("k_cache and v_cache must be contiguous, with the rows' dtype")
+    return shape[0]
+
+
+def _pages4(k_codes, k_scales, v_codes, v_scales, Hkv, D):
+    """Checks of 4-bit pages: their number."""
+    shape, scales = k_codes.shape, k_scales.shape
+    P = shape[0]
+    if (v_codes.shape != shape or v_scales.shape != scales or shape != (P, Hkv, 16, D // 2)
+            or scales != (P, Hkv, 16, D // 16)):
+        raise ValueError("codes must be [pages, Hkv, 16, D / 2], scales [pages, Hkv, 16, D / 16]")
+    if not (k_codes.dtype is torch.uint8 and v_codes.dtype is torch.uint8 and k_scales.dtype in _BYTES
+            and v_scales.dtype in _BYTES):
+        raise ValueError("codes must be uint8, scales uint8 or float8_e4m3fn")
+    if not (k_codes.is_contiguous() and k_scales.is_contiguous() and v_codes.is_contiguous()
+            and v_scales.is_contiguous()):
+        raise ValueError("codes and scales must be contiguous")
+    return P
+
+
+def _rope_rows(rope, D):
+    """Checks of a rotation table (or None): its positions."""
+    if rope is None:
+        return 0
+    shape = rope.shape
+    if shape != (shape[0], 2, D // 2) or rope.dtype is not _F32 or not rope.is_contiguous():
+        raise ValueError("rope must be contiguous fp32 [max_pos, 2, D / 2]")
+    return shape[0]
+
+
 def _append_rows(q, k, v, q_out):
-    """Checks of the row arrays and their strides: (Hq, q stride, k stride, v stride)."""
-    T, _, D = k.shape
-    if v.shape != k.shape or v.dtype != k.dtype:
+    """Checks of the row arrays and their strides: (T, Hkv, D, Hq, q stride, k stride, v stride)."""
+    shape, dtype = k.shape, k.dtype
+    T, Hkv, D = shape
+    if v.shape != shape or v.dtype is not dtype:
         raise ValueError("k and v must have one dtype and one shape")
     ks, vs = _row_stride("k", k, D), _row_stride("v", v, D)
     if q is None:
-        return 0, 0, ks, vs
-    if q.shape[0] != T or q.dtype != k.dtype or q_out is None or not q_out.is_contiguous():
-        raise ValueError("q must have k's rows and dtype, and q_out must be contiguous")
-    return q.shape[1], _row_stride("q", q, D), ks, vs
+        if q_out is not None:
+            raise ValueError("q_out without q")
+        return T, Hkv, D, 0, 0, ks, vs
+    shape = q.shape
+    rows, Hq, last = shape
+    if rows != T or last != D or q.dtype is not dtype:
+        raise ValueError("q must have k's rows, D and dtype")
+    if q_out is None or q_out.shape != shape or q_out.dtype is not dtype or not q_out.is_contiguous():
+        raise ValueError("q_out must be contiguous, with q's shape and dtype")
+    return T, Hkv, D, Hq, _row_stride("q", q, D), ks, vs
+
+
+def _attn_rows(q, out, lse):
+    """Checks of the attention's row arrays: (T, Hq, D, q stride)."""
+    shape = q.shape
+    T, Hq, D = shape
+    if out.shape != shape or out.dtype is not q.dtype or not out.is_contiguous():
+        raise ValueError("out must be contiguous, with q's shape and dtype")
+    if lse is not None and not (lse.shape == (T, Hq) and lse.dtype is _F32 and lse.is_contiguous()):
+        raise ValueError("lse must be contiguous fp32 [T, Hq]")
+    return T, Hq, D, _row_stride("q", q, D)
 
 
 def eagle_rope_table(max_pos, D, theta, table=None, stream=None):
     """cos and sin of pos * theta^(-2i/D): [max_pos, 2, D/2] fp32 on the current device."""
     if table is None:
         table = torch.empty((max_pos, 2, D // 2), dtype=torch.float32, device="cuda")
+    else:
+        if _rope_rows(table, D) != max_pos:
+            raise ValueError("table must be [max_pos, 2, D / 2]")
+        if not table.is_cuda:
+            raise ValueError("the table must be on the GPU")
     _check("eagle_rope_table", lib().eagle_rope_table(max_pos, D, float(theta), _addr(table),
                                                       _raw_stream(stream, table.device)))
     return table
@@ -512,35 +596,38 @@ def eagle_kv_append(q, k, v, rope, cu_seqlens, ctx_lens, block_table, k_cache, v
     """Rotate the packed rows to their positions, write q to q_out and k, v into
     the paged cache (see include/eagle.h).  q and q_out may be None, rope None
     for no rotation."""
-    T, Hkv, D = k.shape
-    Hq, qs, ks, vs = _append_rows(q, k, v, q_out)
-    if k_cache.dtype != k.dtype or v_cache.dtype != k.dtype:
-        raise ValueError("the cache must have k's dtype")
+    T, Hkv, D, Hq, qs, ks, vs = _append_rows(q, k, v, q_out)
+    P, max_pos = _pages16(k_cache, v_cache, Hkv, D, k.dtype), _rope_rows(rope, D)
+    B, pages = _lengths(k, cu_seqlens, ctx_lens, block_table, status)
     _check("eagle_kv_append", lib().eagle_kv_append(
-        _addr(q), k.data_ptr(), v.data_ptr(), qs, ks, vs, _addr(rope),
-        0 if rope is None else rope.shape[0], cu_seqlens.data_ptr(), ctx_lens.data_ptr(), ctx_lens.shape[0], T, Hq,
-        Hkv, D, _dtype(k), _addr(q_out), k_cache.data_ptr(), v_cache.data_ptr(), k_cache.shape[0],
-        block_table.data_ptr(), block_table.shape[1], _addr(status), _raw_stream(stream, k.device)))
+        _addr(q), k.data_ptr(), v.data_ptr(), qs, ks, vs, _addr(rope), max_pos, cu_seqlens.data_ptr(),
+        ctx_lens.data_ptr(), B, T, Hq, Hkv, D, _dtype(k), _addr(q_out), k_cache.data_ptr(), v_cache.data_ptr(), P,
+        block_table.data_ptr(), pages, _addr(status), _raw_stream(stream, k.device)))
 
 
 def eagle_kv_append_kv4(q, k, v, rope, cu_seqlens, ctx_lens, block_table, k_codes, k_scales, v_codes, v_scales,
                         q_out=None, k_scale=1.0, v_scale=1.0, status=None, stream=None):
     """eagle_kv_append into 4-bit pages (see include/eagle.h)."""
-    T, Hkv, D = k.shape
-    Hq, qs, ks, vs = _append_rows(q, k, v, q_out)
+    T, Hkv, D, Hq, qs, ks, vs = _append_rows(q, k, v, q_out)
     if k.dtype != torch.bfloat16:
         raise ValueError("k and v must be bf16")
+    P, max_pos = _pages4(k_codes, k_scales, v_codes, v_scales, Hkv, D), _rope_rows(rope, D)
+    B, pages = _lengths(k, cu_seqlens, ctx_lens, block_table, status)
     _check("eagle_kv_append_kv4", lib().eagle_kv_append_kv4(
-        _addr(q), k.data_ptr(), v.data_ptr(), qs, ks, vs, _addr(rope),
-        0 if rope is None else rope.shape[0], cu_seqlens.data_ptr(), ctx_lens.data_ptr(), ctx_lens.shape[0], T, Hq,
-        Hkv, D, _addr(q_out), k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
-        k_scale, v_scale, k_codes.shape[0], block_table.data_ptr(), block_table.shape[1], _addr(status),
+        _addr(q), k.data_ptr(), v.data_ptr(), qs, ks, vs, _addr(rope), max_pos, cu_seqlens.data_ptr(),
+        ctx_lens.data_ptr(), B, T, Hq, Hkv, D, _addr(q_out), k_codes.data_ptr(), k_scales.data_ptr(),
+        v_codes.data_ptr(), v_scales.data_ptr(), k_scale, v_scale, P, block_table.data_ptr(), pages, _addr(status),
         _raw_stream(stream, k.device)))
 
 
 def eagle_kv4_read(codes, scales, out, scale=1.0, stream=None):
     """The values of 4-bit pages as an ordinary [pages, 16, Hkv, D] cache."""
     P, Hkv, _, half = codes.shape
+    _pages4(codes, scales, codes, scales, Hkv, 2 * half)
+    if out.shape != (P, 16, Hkv, 2 * half) or not out.is_contiguous():
+        raise ValueError("out must be contiguous [pages, 16, Hkv, D]")
+    if not (codes.is_cuda and scales.is_cuda and out.is_cuda):
+        raise ValueError("the arrays must be on the GPU")
     _check("eagle_kv4_read", lib().eagle_kv4_read(codes.data_ptr(), scales.data_ptr(), scale, P, Hkv, 2 * half,
                                                   _dtype(out), out.data_ptr(), _raw_stream(stream, out.device)))
     return out
@@ -553,17 +640,16 @@ def eagle_prompt_attn_workspace_size(B, T, Hq, Hkv, D):
 def eagle_prompt_attn(q, k_cache, v_cache, block_table, cu_seqlens, ctx_lens, out, lse=None, scale=None, ws=None,
                       status=None, stream=None):
     """Causal attention of the packed rows over the paged cache (see include/eagle.h)."""
-    T, Hq, D = q.shape
-    P, page, Hkv, _ = k_cache.shape
-    B = ctx_lens.shape[0]
-    if k_cache.dtype != q.dtype or v_cache.dtype != q.dtype or out.dtype != q.dtype or not out.is_contiguous():
-        raise ValueError("q, the cache and out must have one dtype, and out must be contiguous")
+    T, Hq, D, qs = _attn_rows(q, out, lse)
+    _, page, Hkv, _ = k_cache.shape
+    P = _pages16(k_cache, v_cache, Hkv, D, q.dtype)
+    B, pages = _lengths(q, cu_seqlens, ctx_lens, block_table, status)
     if ws is None:
         ws = workspace(eagle_prompt_attn_workspace_size(B, T, Hq, Hkv, D), q.device)
     _check("eagle_prompt_attn", lib().eagle_prompt_attn(
-        q.data_ptr(), _row_stride("q", q, D), k_cache.data_ptr(), v_cache.data_ptr(), P, block_table.data_ptr(),
-        block_table.shape[1], cu_seqlens.data_ptr(), ctx_lens.data_ptr(), out.data_ptr(), _addr(lse), B, T, Hq, Hkv,
-        D, page, D ** -0.5 if scale is None else scale, _dtype(q), ws.data_ptr(), ws.numel(), _addr(status),
+        q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), P, block_table.data_ptr(), pages,
+        cu_seqlens.data_ptr(), ctx_lens.data_ptr(), out.data_ptr(), _addr(lse), B, T, Hq, Hkv, D, page,
+        D ** -0.5 if scale is None else scale, _dtype(q), ws.data_ptr(), ws.numel(), _addr(status),
         _raw_stream(stream, q.device)))
     return out
 
@@ -571,18 +657,19 @@ def eagle_prompt_attn(q, k_cache, v_cache, block_table, cu_seqlens, ctx_lens, ou
 def eagle_prompt_attn_kv4(q, k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlens, ctx_lens, out, lse=None,
                           scale=None, k_scale=1.0, v_scale=1.0, ws=None, status=None, stream=None):
     """eagle_prompt_attn over 4-bit pages (see include/eagle.h)."""
-    T, Hq, D = q.shape
-    P, Hkv, page, _ = k_codes.shape
-    B = ctx_lens.shape[0]
-    if q.dtype != torch.bfloat16 or out.dtype != q.dtype or not out.is_contiguous():
-        raise ValueError("q and out must be bf16, and out must be contiguous")
+    if q.dtype != torch.bfloat16:
+        raise ValueError("q and out must be bf16")
+    T, Hq, D, qs = _attn_rows(q, out, lse)
+    _, Hkv, page, _ = k_codes.shape
+    P = _pages4(k_codes, k_scales, v_codes, v_scales, Hkv, D)
+    B, pages = _lengths(q, cu_seqlens, ctx_lens, block_table, status)
     if ws is None:
         ws = workspace(eagle_prompt_attn_workspace_size(B, T, Hq, Hkv, D), q.device)
     _check("eagle_prompt_attn_kv4", lib().eagle_prompt_attn_kv4(
-        q.data_ptr(), _row_stride("q", q, D), k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
-        v_scales.data_ptr(), k_scale, v_scale, P, block_table.data_ptr(), block_table.shape[1],
-        cu_seqlens.data_ptr(), ctx_lens.data_ptr(), out.data_ptr(), _addr(lse), B, T, Hq, Hkv, D, page,
-        D ** -0.5 if scale is None else scale, ws.data_ptr(), ws.numel(), _addr(status), _raw_stream(stream, q.device)))
+        q.data_ptr(), qs, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), k_scale,
+        v_scale, P, block_table.data_ptr(), pages, cu_seqlens.data_ptr(), ctx_lens.data_ptr(), out.data_ptr(),
+        _addr(lse), B, T, Hq, Hkv, D, page, D ** -0.5 if scale is None else scale, ws.data_ptr(), ws.numel(),
+        _addr(status), _raw_stream(stream, q.device)))
     return out
 
 
@@ -595,17 +682,32 @@ def eagle_draft_prompt(x, weights, rope, cu_seqlens, ctx_lens, k_cache, v_cache,
     """The drafter's decoder layer over packed prompt rows, filling its paged
     cache (with k_scales and v_scales: 4-bit pages).  weights as eagle_draft_layer."""
     T, d = x.shape
-    B, D = ctx_lens.shape[0], 2 * rope.shape[2]
+    D = 2 * rope.shape[2]
+    max_pos = _rope_rows(rope, D)
     Hq = weights["o"].shape[1] // D
     Hkv = (weights["qkv"].shape[0] // D - Hq) // 2
     I = weights["down"].shape[1]
+    shapes = dict(norm1=(d,), qkv=((Hq + 2 * Hkv) * D, d), o=(d, Hq * D), norm2=(d,), gu=(2 * I, d), down=(d, I))
+    for name, shape in shapes.items():
+        w = weights[name]
+        if w.shape != shape or w.dtype is not x.dtype or not w.is_contiguous():
+            raise ValueError(f"weights[{name!r}] must be contiguous {list(shape)}, with x's dtype")
+    if not (x.is_contiguous() and out.shape == x.shape and out.dtype is x.dtype and out.is_contiguous()):
+        raise ValueError("x and out must be contiguous, with one shape and dtype")
+    if k_scales is None and v_scales is None:
+        P = _pages16(k_cache, v_cache, Hkv, D, x.dtype)
+    elif k_scales is None or v_scales is None or x.dtype != torch.bfloat16:
+        raise ValueError("4-bit pages need k_scales and v_scales, and bf16 rows")
+    else:
+        P = _pages4(k_cache, k_scales, v_cache, v_scales, Hkv, D)
+    B, pages = _lengths(x, cu_seqlens, ctx_lens, block_table, status)
     dt = _dtype(x)
     if ws is None:
         ws = workspace(eagle_draft_prompt_workspace_size(B, T, d, Hq, Hkv, D, I, dt), x.device)
     _check("eagle_draft_prompt", lib().eagle_draft_prompt(
         x.data_ptr(), _addr(weights["norm1"]), _addr(weights["qkv"]), _addr(weights["o"]), _addr(weights["norm2"]),
-        _addr(weights["gu"]), _addr(weights["down"]), eps, rope.data_ptr(), rope.shape[0], cu_seqlens.data_ptr(),
+        _addr(weights["gu"]), _addr(weights["down"]), eps, rope.data_ptr(), max_pos, cu_seqlens.data_ptr(),
         ctx_lens.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scales), _addr(v_scales), k_scale, v_scale,
-        k_cache.shape[0], block_table.data_ptr(), block_table.shape[1], out.data_ptr(), B, T, d, Hq, Hkv, D, I, dt,
+        P, block_table.data_ptr(), pages, out.data_ptr(), B, T, d, Hq, Hkv, D, I, dt,
         ws.data_ptr(), ws.numel(), _addr(status), _raw_stream(stream, x.device)))
     return out
