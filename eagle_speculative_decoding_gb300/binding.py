@@ -129,10 +129,19 @@ def _check(fn, code):
         raise EagleError(fn, code)
 
 
-def workspace(nbytes, device=None):
-    """A caller-owned device buffer of at least ``nbytes`` (torch allocation)."""
-    return torch.empty(max(int(nbytes), 256), dtype=torch.uint8,
-                       device=device if device is not None else "cuda")
+def workspace(nbytes, device=None, stream=None):
+    """A caller-owned device buffer of at least ``nbytes`` (torch allocation).
+    It belongs to ``stream`` if that is given, else to the current stream: the
+    memory is another allocation's again only behind what that stream has been
+    given until the buffer is released."""
+    return _empty((max(int(nbytes), 256),), torch.uint8, device if device is not None else "cuda", stream)
+
+
+def _empty(shape, dtype, device, stream):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def launch_count():
@@ -161,7 +170,7 @@ def eagle_fuse_proj(h_low, h_mid, h_high, w_proj, g, bias=None, ws=None, status=
     M, d = h_low.shape
     dt = _dtype(h_low)
     if ws is None:
-        ws = workspace(eagle_fuse_proj_workspace_size(M, d, dt), h_low.device)
+        ws = workspace(eagle_fuse_proj_workspace_size(M, d, dt), h_low.device, stream)
     _check("eagle_fuse_proj", lib().eagle_fuse_proj(
         _ptr(h_low), _ptr(h_mid), _ptr(h_high), _ptr(w_proj), _ptr(bias), _ptr(g), M, d, dt,
         _ptr(ws), ws.numel(), _ptr(status), _stream(stream)))
@@ -182,7 +191,7 @@ def eagle_fuse_proj_accepted(h_low, h_mid, h_high, w_proj, path_rows, accept_len
     R = h_low.shape[0] // B
     dt = _dtype(h_low)
     if ws is None:
-        ws = workspace(eagle_fuse_proj_accepted_workspace_size(B, slots - 1, d, dt), h_low.device)
+        ws = workspace(eagle_fuse_proj_accepted_workspace_size(B, slots - 1, d, dt), h_low.device, stream)
     _check("eagle_fuse_proj_accepted", lib().eagle_fuse_proj_accepted(
         _ptr(h_low), _ptr(h_mid), _ptr(h_high), _ptr(w_proj), _ptr(bias), _ptr(path_rows), _ptr(accept_len),
         B, R, slots - 1, d, dt, _ptr(g), _ptr(ws), ws.numel(), _ptr(status), _stream(stream)))
@@ -198,7 +207,7 @@ def eagle_draft_input(r, token_ids, embed, w_in, u, bias=None, ws=None, status=N
     M, d = r.shape
     dt = _dtype(r)
     if ws is None:
-        ws = workspace(eagle_draft_input_workspace_size(M, d, dt), r.device)
+        ws = workspace(eagle_draft_input_workspace_size(M, d, dt), r.device, stream)
     _check("eagle_draft_input", lib().eagle_draft_input(
         _ptr(r), _ptr(token_ids), _ptr(embed), embed.shape[0], _ptr(w_in), _ptr(bias), _ptr(u), M, d,
         dt, _ptr(ws), ws.numel(), _ptr(status), _stream(stream)))
@@ -215,7 +224,7 @@ def eagle_linear(x, w, y, bias=None, residual=None, ws=None, status=None, stream
     n_out = w.shape[0]
     dt = _dtype(x)
     if ws is None:
-        ws = workspace(eagle_linear_workspace_size(M, n_out, k_in, dt), x.device)
+        ws = workspace(eagle_linear_workspace_size(M, n_out, k_in, dt), x.device, stream)
     _check("eagle_linear", lib().eagle_linear(
         _ptr(x), _ptr(w), _ptr(bias), _ptr(residual), _ptr(y), M, n_out, k_in, dt, _ptr(ws), ws.numel(),
         _ptr(status), _stream(stream)))
@@ -239,7 +248,7 @@ def eagle_draft_layer(x, weights, positions, k_cache, v_cache, block_table, ctx_
     dt = _dtype(x)
     if ws is None:
         ws = workspace(eagle_draft_layer_workspace_size(B, W, d, Hq, Hkv, D, I, Rmax, block_table.shape[1], dt),
-                       x.device)
+                       x.device, stream)
     _check("eagle_draft_layer", lib().eagle_draft_layer(
         _ptr(x), _ptr(weights["norm1"]), _ptr(weights["qkv"]), _ptr(weights["o"]), _ptr(weights["norm2"]),
         _ptr(weights["gu"]), _ptr(weights["down"]), eps, theta, _ptr(positions), _ptr(k_cache),
@@ -280,7 +289,7 @@ def eagle_tree_attn(q, k_tree, v_tree, k_cache, v_cache, block_table, ctx_lens, 
         scale = D ** -0.5
     if ws is None:
         ws = workspace(eagle_tree_attn_workspace_size(B, R, Hq, Hkv, D, max_pages, page, num_splits,
-                                                      dt), q.device)
+                                                      dt), q.device, stream)
     _check("eagle_tree_attn", lib().eagle_tree_attn(
         _ptr(q), _ptr(k_tree), _ptr(v_tree), _ptr(k_cache), _ptr(v_cache), P, _ptr(block_table),
         max_pages, _ptr(ctx_lens), _ptr(tree_mask), _ptr(out), _ptr(lse), B, R, Hq, Hkv, D, page,
@@ -299,7 +308,7 @@ def eagle_lmhead_topk(x, w_lm, k, topk_ids, topk_logprobs, temperature=1.0, bias
     V = w_lm.shape[0]
     dt = _dtype(x)
     if ws is None:
-        ws = workspace(eagle_lmhead_topk_workspace_size(M, d, V, k, dt), x.device)
+        ws = workspace(eagle_lmhead_topk_workspace_size(M, d, V, k, dt), x.device, stream)
     _check("eagle_lmhead_topk", lib().eagle_lmhead_topk(
         _ptr(x), _ptr(w_lm), _ptr(bias), M, d, V, k, float(temperature), _ptr(topk_ids),
         _ptr(topk_logprobs), _ptr(row_max), _ptr(row_sumexp), dt, _ptr(ws), ws.numel(),
@@ -388,7 +397,7 @@ def eagle_tree_verify(parent_row, token, temperature, max_depth, accept_len, pat
     if V is None:
         V = target_logits.shape[2]
     if ws is None:
-        ws = workspace(eagle_tree_verify_workspace_size(B, R, V), parent_row.device)
+        ws = workspace(eagle_tree_verify_workspace_size(B, R, V), parent_row.device, stream)
     _check("eagle_tree_verify", lib().eagle_tree_verify(
         B, R, V, _ptr(parent_row), _ptr(token), _ptr(n_rows), _ptr(target_logits),
         _ptr(target_argmax), _ptr(draft_logits), float(temperature), proposal_mode, int(seed),
@@ -424,7 +433,7 @@ def eagle_lmhead_verify_stats(x, w_lm, parent_row, token, temperature, race_k, r
     V = w_lm.shape[0]
     dt = _dtype(x)
     if ws is None:
-        ws = workspace(eagle_lmhead_topk_workspace_size(M, d, V, race_k, dt), x.device)
+        ws = workspace(eagle_lmhead_topk_workspace_size(M, d, V, race_k, dt), x.device, stream)
     _check("eagle_lmhead_verify_stats", lib().eagle_lmhead_verify_stats(
         _ptr(x), _ptr(w_lm), _ptr(bias), B, R, d, V, _ptr(parent_row), _ptr(token), _ptr(n_rows),
         float(temperature), int(seed), int(offset), race_k, _ptr(race_ids), _ptr(race_keys),
@@ -580,7 +589,7 @@ def _attn_rows(q, out, lse):
 def eagle_rope_table(max_pos, D, theta, table=None, stream=None):
     """cos and sin of pos * theta^(-2i/D): [max_pos, 2, D/2] fp32 on the current device."""
     if table is None:
-        table = torch.empty((max_pos, 2, D // 2), dtype=torch.float32, device="cuda")
+        table = _empty((max_pos, 2, D // 2), torch.float32, "cuda", stream)
     else:
         if _rope_rows(table, D) != max_pos:
             raise ValueError("table must be [max_pos, 2, D / 2]")
@@ -645,7 +654,7 @@ def eagle_prompt_attn(q, k_cache, v_cache, block_table, cu_seqlens, ctx_lens, ou
     P = _pages16(k_cache, v_cache, Hkv, D, q.dtype)
     B, pages = _lengths(q, cu_seqlens, ctx_lens, block_table, status)
     if ws is None:
-        ws = workspace(eagle_prompt_attn_workspace_size(B, T, Hq, Hkv, D), q.device)
+        ws = workspace(eagle_prompt_attn_workspace_size(B, T, Hq, Hkv, D), q.device, stream)
     _check("eagle_prompt_attn", lib().eagle_prompt_attn(
         q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), P, block_table.data_ptr(), pages,
         cu_seqlens.data_ptr(), ctx_lens.data_ptr(), out.data_ptr(), _addr(lse), B, T, Hq, Hkv, D, page,
@@ -664,7 +673,7 @@ def eagle_prompt_attn_kv4(q, k_codes, k_scales, v_codes, v_scales, block_table, 
     P = _pages4(k_codes, k_scales, v_codes, v_scales, Hkv, D)
     B, pages = _lengths(q, cu_seqlens, ctx_lens, block_table, status)
     if ws is None:
-        ws = workspace(eagle_prompt_attn_workspace_size(B, T, Hq, Hkv, D), q.device)
+        ws = workspace(eagle_prompt_attn_workspace_size(B, T, Hq, Hkv, D), q.device, stream)
     _check("eagle_prompt_attn_kv4", lib().eagle_prompt_attn_kv4(
         q.data_ptr(), qs, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), k_scale,
         v_scale, P, block_table.data_ptr(), pages, cu_seqlens.data_ptr(), ctx_lens.data_ptr(), out.data_ptr(),
@@ -703,7 +712,7 @@ def eagle_draft_prompt(x, weights, rope, cu_seqlens, ctx_lens, k_cache, v_cache,
     B, pages = _lengths(x, cu_seqlens, ctx_lens, block_table, status)
     dt = _dtype(x)
     if ws is None:
-        ws = workspace(eagle_draft_prompt_workspace_size(B, T, d, Hq, Hkv, D, I, dt), x.device)
+        ws = workspace(eagle_draft_prompt_workspace_size(B, T, d, Hq, Hkv, D, I, dt), x.device, stream)
     _check("eagle_draft_prompt", lib().eagle_draft_prompt(
         x.data_ptr(), _addr(weights["norm1"]), _addr(weights["qkv"]), _addr(weights["o"]), _addr(weights["norm2"]),
         _addr(weights["gu"]), _addr(weights["down"]), eps, rope.data_ptr(), max_pos, cu_seqlens.data_ptr(),

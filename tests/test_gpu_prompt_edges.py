@@ -221,3 +221,23 @@ def test_attn_refuses_positions_past_its_range(kind, n, ctx):
     out, lse = run_attn(b, s, kind == "kv4")
     assert s["st"].item() == 6 and (out[:n] == 7.0).all() and (lse[:n] == 7.0).all()
     assert torch.equal(out[n:], clean[n:])
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16", "kv4"])
+def test_attn_on_a_given_stream_without_a_workspace(kind):
+    """The scratch is the given stream's: work of the current stream that takes
+    memory as soon as the call returns does not disturb it."""
+    b = need_gpu()
+    s = make(71, [60, 1, 200] * 6, [700, 3000, 90] * 6, 16, 4, 128, "fp32" if kind == "fp32" else "bf16", kv4=kind == "kv4")
+    want, wl = run_attn(b, s, kind == "kv4")
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        out, lse = torch.zeros_like(want), torch.zeros_like(wl)
+        torch.cuda.synchronize()
+        if kind == "kv4":
+            b.eagle_prompt_attn_kv4(s["q"], s["k4"], s["ks"], s["v4"], s["vs"], s["table"], s["cu"], s["ctx"], out, lse=lse, stream=side)
+        else:
+            b.eagle_prompt_attn(s["q"], s["kc"], s["vc"], s["table"], s["cu"], s["ctx"], out, lse=lse, stream=side)
+        torch.zeros(64 << 20, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, wl)
