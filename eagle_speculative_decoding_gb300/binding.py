@@ -486,12 +486,14 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _row_stride(name, t, D):
-    """Row stride of a [T, heads, D] array whose heads and channels are contiguous."""
+def _row_stride(name, t, D, T=None, H=None):
+    """Row stride of a [T, H, D] array whose heads and channels are contiguous."""
+    if T is None:
+        T, H, _ = t.shape
     rows, heads, last = t.stride()
-    if last != 1 or (heads != D and t.shape[1] > 1):
+    if last != 1 or (heads != D and H > 1):
         raise ValueError(f"{name}: heads and channels must be contiguous, strides {t.stride()}")
-    return rows
+    return rows if T > 1 else H * D  # (a single row's stride leads nowhere and may be anything)
 
 
 # The kernels check lengths and page ids, but take the arrays' own shapes, types
@@ -561,7 +563,7 @@ def _append_rows(q, k, v, q_out):
     T, Hkv, D = shape
     if v.shape != shape or v.dtype is not dtype:
         raise ValueError("k and v must have one dtype and one shape")
-    ks, vs = _row_stride("k", k, D), _row_stride("v", v, D)
+    ks, vs = _row_stride("k", k, D, T, Hkv), _row_stride("v", v, D, T, Hkv)
     if q is None:
         if q_out is not None:
             raise ValueError("q_out without q")
@@ -572,7 +574,7 @@ def _append_rows(q, k, v, q_out):
         raise ValueError("q must have k's rows, D and dtype")
     if q_out is None or q_out.shape != shape or q_out.dtype is not dtype or not q_out.is_contiguous():
         raise ValueError("q_out must be contiguous, with q's shape and dtype")
-    return T, Hkv, D, Hq, _row_stride("q", q, D), ks, vs
+    return T, Hkv, D, Hq, _row_stride("q", q, D, T, Hq), ks, vs
 
 
 def _attn_rows(q, out, lse):
@@ -583,7 +585,7 @@ def _attn_rows(q, out, lse):
         raise ValueError("out must be contiguous, with q's shape and dtype")
     if lse is not None and not (lse.shape == (T, Hq) and lse.dtype is _F32 and lse.is_contiguous()):
         raise ValueError("lse must be contiguous fp32 [T, Hq]")
-    return T, Hq, D, _row_stride("q", q, D)
+    return T, Hq, D, _row_stride("q", q, D, T, Hq)
 
 
 def eagle_rope_table(max_pos, D, theta, table=None, stream=None):

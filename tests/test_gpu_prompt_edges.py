@@ -241,3 +241,14 @@ def test_attn_on_a_given_stream_without_a_workspace(kind):
         torch.zeros(64 << 20, dtype=torch.uint8, device="cuda")
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16", "kv4"])
+def test_attn_single_row_of_any_stride(kind):
+    b = need_gpu()
+    s = make(73, [1], [100], 8, 2, 64, "fp32" if kind == "fp32" else "bf16", kv4=kind == "kv4")
+    want, wl = run_attn(b, s, kind == "kv4")
+    for row in (64, 3, 0, 8 * 64 + 1):
+        q = torch.as_strided(s["q"].contiguous(), (1, 8, 64), (row, 64, 1))
+        out, lse = run_attn(b, dict(s, q=q), kind == "kv4")
+        assert torch.equal(out, want) and torch.equal(lse, wl)

@@ -141,3 +141,13 @@ def test_rope_table_given():
     for bad in (z(7, 2, D // 2, dtype=F32), z(8, 2, D, dtype=F32), z(8, 2, D // 2, dtype=torch.float64)):
         with pytest.raises(ValueError, match="max_pos"):
             eb.eagle_rope_table(8, D, 1e4, table=bad)
+
+
+def test_a_single_row_may_have_any_stride():
+    """A row's stride that no second row uses is not held against it."""
+    one = z(HQ, 1, D).transpose(0, 1)
+    assert one.stride(0) < HQ * D and eb._row_stride("q", one, D) == HQ * D
+    assert eb._row_stride("q", z(1, D).expand(1, HQ, D)[:, :1], D) == D
+    assert eb._row_stride("q", torch.as_strided(z(4000), (1, HQ, D), (4001, D, 1)), D) == HQ * D
+    assert eb._row_stride("q", z(4, 6, D)[:, :HQ], D) == 6 * D
+    assert eb._row_stride("q", z(HQ, D).expand(3, HQ, D), D) == 0  # for the library to refuse
