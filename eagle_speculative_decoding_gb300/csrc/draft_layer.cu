@@ -411,7 +411,9 @@ PromptWs prompt_ws(int B, int T, int d, int Hq, int Hkv, int D, int I, int dtype
   return L;
 }
 bool prompt_shape_ok(int d, int Hq, int Hkv, int D, int I) {
-  return layer_shape_ok(1, 1, d, Hq, Hkv, D, I, 1, 0) && (long long)Hq + 2ll * Hkv <= 1024 && Hq / Hkv <= 64;
+  // (eagle_linear takes 65536 rows of weights)
+  return layer_shape_ok(1, 1, d, Hq, Hkv, D, I, 1, 0) && (long long)Hq + 2ll * Hkv <= 1024 && Hq / Hkv <= 64 &&
+         d <= 65536 && I <= 32768 && (Hq + 2 * Hkv) * D <= 65536;
 }
 }  // namespace
 
@@ -436,8 +438,12 @@ extern "C" int eagle_draft_prompt(const void* x, const void* w_norm1, const void
   if (!(eps >= 0.f) || B <= 0 || T < 0 || max_pos <= 0 || num_pages <= 0 || max_pages <= 0)
     return EAGLE_ERR_INVALID_ARG;
   if (!prompt_shape_ok(d, Hq, Hkv, D, I) || B > 65535) return EAGLE_ERR_UNSUPPORTED;
-  if (!aligned16(rope) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scales) || !aligned16(v_scales))
-    return EAGLE_ERR_INVALID_ARG;
+  if (kv4 && (!(k_scale > 0.f) || !(v_scale > 0.f) || !isfinite(k_scale) || !isfinite(v_scale))) return EAGLE_ERR_INVALID_ARG;
+  // what one of the calls below would refuse is refused before the first has run
+  if (num_pages > (1 << 26)) return EAGLE_ERR_UNSUPPORTED;
+  for (const void* a : {x, (const void*)out, w_qkv, w_o, w_gu, w_down, (const void*)rope, (const void*)k_cache,
+                        (const void*)v_cache, (const void*)k_scales, (const void*)v_scales})
+    if (!aligned16(a)) return EAGLE_ERR_INVALID_ARG;
   if (T == 0) return EAGLE_OK;
   const PromptWs L = prompt_ws(B, T, d, Hq, Hkv, D, I, dtype);
   if (!ws || ws_bytes < L.total) return EAGLE_ERR_WORKSPACE;

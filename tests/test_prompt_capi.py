@@ -125,3 +125,21 @@ def test_draft_prompt_refusals(L):
 def test_no_rows_need_no_addresses(L):
     assert append(L, T=0, q=N, k=N, v=N, q_out=N) == OK
     assert attn(L, T=0, q=N, out=N) == OK
+
+
+@pytest.mark.parametrize("want,kw", [
+    (INVALID, dict(x=ODD)), (INVALID, dict(out=ODD)), (INVALID, dict(qkv=ODD)), (INVALID, dict(o=ODD)), (INVALID, dict(gu=ODD)),
+    (INVALID, dict(down=ODD)), (INVALID, dict(kc=ODD)), (UNSUPPORTED, dict(pages=(1 << 26) + 1)),
+    (INVALID, dict(ks=P, vs=P, k_scale=0.0)), (INVALID, dict(ks=P, vs=P, v_scale=float("inf"))),
+    (INVALID, dict(ks=P, vs=P, k_scale=float("nan"))), (INVALID, dict(ks=P)), (WORKSPACE, dict(k_scale=0.0)),
+    (UNSUPPORTED, dict(I=32832)), (WORKSPACE, dict(I=32768)),
+])
+def test_draft_prompt_refuses_before_its_first_launch(L, want, kw):
+    """What one of its steps would refuse is refused at the entry: the cache is
+    not half filled.  (A refusal behind the entry's checks would come after the
+    workspace's.)"""
+    a = dict(x=P, qkv=P, o=P, gu=P, down=P, kc=P, I=256, ks=N, vs=N, k_scale=1.0, v_scale=1.0, pages=8, out=ctypes.c_void_p(512))
+    a.update(kw)
+    assert L.eagle_draft_prompt(a["x"], P, a["qkv"], a["o"], P, a["gu"], a["down"], 1e-5, P, 8, P, P, a["kc"], P, a["ks"],
+                                a["vs"], a["k_scale"], a["v_scale"], a["pages"], P, 4, a["out"], 2, 4, 256, 4, 2, 64, a["I"], 1,
+                                N, 0, N, N) == want
