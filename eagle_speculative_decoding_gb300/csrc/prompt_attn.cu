@@ -2366,8 +2366,16 @@ using namespace eagle;
 
 extern "C" size_t eagle_prompt_attn_workspace_size(int B, int T, int Hq, int Hkv, int D) {
   if (B <= 0 || T < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || Hq / Hkv > 64 || (D != 64 && D != 128)) return 0;
+  // the largest of the paths that some call of at most these B and T takes, each
+  // at the most rows that it takes: a workspace serves all those calls
+  const long long g = Hq / Hkv;
+  auto rows = [&](long long limit) { return (int)std::min<long long>(T, limit); };
+  const struct {
+    Path path;
+    int T;
+  } calls[] = {{kTensor, T}, {kFew, rows(B)}, {kFew4, rows(2ll * B)}, {kFp32, T}, {kFp32Few, rows((long long)kF32Few * B / g)}};
   size_t most = 0;
-  for (const Path path : {kTensor, kFew, kFew4, kFp32, kFp32Few}) most = std::max(most, attn_shape(B, T, Hq, Hkv, D, path).total);
+  for (const auto& c : calls) most = std::max(most, attn_shape(B, c.T, Hq, Hkv, D, c.path).total);
   return most + 256;
 }
 

@@ -790,7 +790,13 @@ int eagle_kv4_read(const uint8_t* codes, const uint8_t* scales, float scale, int
  * CUDA cores in fp32 arithmetic.
  * Limits: D in {64, 128}, page_size == 16, Hq % Hkv == 0, Hq / Hkv <= 64,
  * B <= 65535, scale finite and > 0; q 16-byte aligned, q_stride a multiple of
- * 16 bytes. */
+ * 16 bytes.
+ * A workspace of B and T serves every call of at most that many requests and
+ * rows, any dtype and 4-bit pages.  Most of it is room for the partial results
+ * of requests that are cut along the keys: with 152 SMs and D 128 243 MB once T
+ * (Hq/Hkv) reaches 256 (64 rows of 32 heads over 8 among them), 123 MB at D 64, and
+ * 16 MB for one row of 32 heads over 8.  The list of work adds some 50 bytes per
+ * request, 256 rows and key head. */
 size_t eagle_prompt_attn_workspace_size(int B, int T, int Hq, int Hkv, int D);
 int eagle_prompt_attn(const void* q, long long q_stride, const void* k_cache, const void* v_cache,
                       int num_pages, const int32_t* block_table, int max_pages,

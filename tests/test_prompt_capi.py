@@ -143,3 +143,20 @@ def test_draft_prompt_refuses_before_its_first_launch(L, want, kw):
     assert L.eagle_draft_prompt(a["x"], P, a["qkv"], a["o"], P, a["gu"], a["down"], 1e-5, P, 8, P, P, a["kc"], P, a["ks"],
                                 a["vs"], a["k_scale"], a["v_scale"], a["pages"], P, 4, a["out"], 2, 4, 256, 4, 2, 64, a["I"], 1,
                                 N, 0, N, N) == want
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(32, 8, 128), (16, 1, 64), (7, 7, 64), (64, 1, 128), (12, 4, 128)])
+def test_workspace_serves_fewer_requests_and_rows(L, Hq, Hkv, D):
+    """Grows with B and with T, and slowly: the paths that only short calls take
+    count at the rows that they take."""
+    size = L.eagle_prompt_attn_workspace_size
+    Bs, Ts = (1, 2, 3, 16, 64, 1000, 65535), (1, 2, 3, 4, 5, 16, 33, 64, 65, 200, 4096, 65536, 1 << 20, 1 << 28)
+    table = [[size(B, T, Hq, Hkv, D) for T in Ts] for B in Bs]
+    for x in range(len(Bs)):
+        for y in range(len(Ts)):
+            assert 0 < table[x][y] and (x == 0 or table[x - 1][y] <= table[x][y]) and (y == 0 or table[x][y - 1] <= table[x][y])
+    g = Hq // Hkv
+    # slots of 256 rows, a cut's description beside them, and 48 bytes a piece;
+    # fp32 units hold 64 rows (64 / g tokens)
+    most = 12 * 160 * 256 * (4 * D + 8 + 48) + 48 * Hkv * (2 * 65535 * 3 + (1 << 28) // (64 // g) + 160 * 12 * 6) + 4096
+    assert table[-1][-1] <= most
