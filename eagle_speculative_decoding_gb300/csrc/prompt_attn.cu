@@ -24,6 +24,7 @@
 //           (one CTA per SM, tcgen05), or for single tokens the few-rows kernel
 //   merge   joins the pieces of cut units (few rows: their last CTA does)
 // fp32 rows: the same list and merge around a kernel on the CUDA cores.
+#include <float.h>
 #include <math.h>
 
 #include <algorithm>
@@ -51,7 +52,7 @@ template <bool F16>
 constexpr float kBelow = F16 ? 7.f : 0.f;
 template <bool F16>
 constexpr float kSumLimit = F16 ? 32768.f : 256.f;
-constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 struct AttnParams {
   const void* q;
@@ -599,8 +600,11 @@ __device__ __forceinline__ int row_exponent(uint32_t mx) {
   return mx ? min(126, max(-126, (int)(mx >> 7) - 127)) : 0;
 }
 // What its scores are then multiplied by: never 0, which would make NaN of a
-// masked score (no score of a row with a factor this small leaves a weight of 1).
-__device__ __forceinline__ float row_factor(float scale_log2, float power) { return fmaxf(scale_log2 * power, 1.17549435e-38f); }
+// masked score (no score of a row with a factor this small leaves a weight of 1),
+// and never infinite, which would make NaN of a score of 0.
+__device__ __forceinline__ float row_factor(float scale_log2, float power) {
+  return fminf(fmaxf(scale_log2 * power, 1.17549435e-38f), 3.40282347e38f);
+}
 
 // Eight 4-bit codes as four fp16 pairs times the pair `s`.
 __device__ __forceinline__ void kv4_expand(uint32_t w, uint32_t s, uint32_t* v) {
@@ -2296,6 +2300,11 @@ int launch_merge(const AttnParams& a, const Shape& sh, const Ws& w, cudaStream_t
   note_launch(3);
   return last_launch_status();
 }
+// The factor of the scores, in fp32's range (as row_factor).
+float scale_log2(const AttnParams& a) {
+  const double f = (double)a.scale * a.k_scale * 1.4426950408889634;
+  return (float)std::min(std::max(f, (double)FLT_MIN), (double)FLT_MAX);
+}
 template <typename K>
 bool allow_smem(K kern, int bytes) {
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess) return true;
@@ -2312,7 +2321,7 @@ int attn_launch_few(const AttnParams& a, void* ws, cudaStream_t s) {
   // a token over 300 keys: 13.7 us in single blocks, 15.2 in pairs; over 1000:
   // 13.9, 14.9; over 4000, whose 32 pieces are joined: 18.4, 17.5
   launch_plan(a, sh, w, 2, 1, s);
-  const FewParams fp = {a, a.scale * a.k_scale * kLog2e, sh.g, sh.rows, w.hdr, &w.hdr->next, w.pieces, w.cuts, w.ml, w.po};
+  const FewParams fp = {a, scale_log2(a), sh.g, sh.rows, w.hdr, &w.hdr->next, w.pieces, w.cuts, w.ml, w.po};
   launch(prompt_attn_few_kernel<D, KV4, NG>, sh.ctas, kFewThreads, smem, s, fp);
   note_launch(2);
   return last_launch_status();
@@ -2334,7 +2343,7 @@ int attn_launch_tc(const AttnParams& a, void* ws, cudaStream_t s) {
     return EAGLE_ERR_CUDA;
   if (!allow_smem(prompt_attn_tc_kernel<D, KV4>, (int)C::kSmem)) return EAGLE_ERR_CUDA;
   launch_plan(a, sh, w, 2, 2, s);
-  const MainParams mp = {a, a.scale * a.k_scale * kLog2e, sh.g, sh.tpt, sh.tpu, sh.rows, w.hdr, &w.hdr->next, w.pieces,
+  const MainParams mp = {a, scale_log2(a), sh.g, sh.tpt, sh.tpu, sh.rows, w.hdr, &w.hdr->next, w.pieces,
                          w.ml, w.po};
   launch(prompt_attn_tc_kernel<D, KV4>, sh.ctas, kThreads, C::kSmem, s, map_q, mp);
   return launch_merge<D, __nv_bfloat16>(a, sh, w, s);
@@ -2346,7 +2355,7 @@ int attn_launch_f32(const AttnParams& a, void* ws, cudaStream_t s) {
   constexpr int smem = CfgF32<D, RT>::kSmem;
   if (!allow_smem(prompt_attn_f32_kernel<D, RT>, smem)) return EAGLE_ERR_CUDA;
   launch_plan(a, sh, w, 1, 1, s);
-  const F32Params fp = {a, a.scale * kLog2e, sh.g, sh.tpu, sh.rows, w.hdr, &w.hdr->next, w.pieces, w.ml, w.po};
+  const F32Params fp = {a, scale_log2(a), sh.g, sh.tpu, sh.rows, w.hdr, &w.hdr->next, w.pieces, w.ml, w.po};
   launch(prompt_attn_f32_kernel<D, RT>, sh.ctas, 256, smem, s, fp);
   return launch_merge<D, float>(a, sh, w, s);
 }

@@ -252,3 +252,31 @@ def test_attn_single_row_of_any_stride(kind):
         q = torch.as_strided(s["q"].contiguous(), (1, 8, 64), (row, 64, 1))
         out, lse = run_attn(b, dict(s, q=q), kind == "kv4")
         assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("kind,q,scale,ks", [
+    ("fp32", 1.0, 3.3e38, 1.0), ("bf16", 1.0, 3.3e38, 1.0), ("kv4", 1.0, 3.3e38, 1.0), ("kv4", 2.0 ** 100, 1.0, 2.0 ** 40),
+    ("kv4", 1.0, 2.0 ** 100, 2.0 ** 100)])
+@pytest.mark.parametrize("n,ctx", [(1, 300), (1, 2600), (50, 300)])
+def test_attn_factors_past_the_range(kind, q, scale, ks, n, ctx):
+    """Where scale, k_scale and a row's power of two leave fp32's range together,
+    scores of 0 stay 0 and those below it weigh nothing."""
+    b = need_gpu()
+    s = make(79, [n], [ctx], 8, 2, 64, "fp32" if kind == "fp32" else "bf16", kv4=kind == "kv4")
+    x = torch.zeros(n, 8, 64)
+    x[..., 3] = q
+    s["q"] = x.to(s["q"].dtype).cuda()
+    key = torch.zeros(ctx + n, 2, 64)
+    key[::3, :, 3] = -40.0
+    set_keys(s, kind, [key])
+    out, lse = run_attn(b, s, kind == "kv4", scale=scale, ks=ks)
+    pages = s["table"][0].cpu().numpy()
+    v = s["vc_np"][pages].reshape(-1, 2, 64)
+    half = HALF["fp32"] if kind == "fp32" else HALF["bf16"]
+    for r in range(n):
+        w = np.arange(ctx + r + 1) % 3 != 0
+        x = np.repeat(v[:ctx + r + 1][w], 4, 1)
+        err = np.abs(f64(out[r]) - x.mean(0))
+        assert (err <= half * np.abs(x.mean(0)) + (WEIGHT_HALF[kind] + (ctx + 16) * 2.0 ** -24) * np.abs(x).mean(0)).all()
+        assert np.abs(f64(lse[r]) - np.log(w.sum())).max() <= 2.0 ** -20
+    assert s["st"].item() == 0
