@@ -21,6 +21,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "kv4.cuh"
 
 namespace eagle {
 namespace {
@@ -438,7 +439,7 @@ extern "C" int eagle_draft_prompt(const void* x, const void* w_norm1, const void
   if (!(eps >= 0.f) || B <= 0 || T < 0 || max_pos <= 0 || num_pages <= 0 || max_pages <= 0)
     return EAGLE_ERR_INVALID_ARG;
   if (!prompt_shape_ok(d, Hq, Hkv, D, I) || B > 65535) return EAGLE_ERR_UNSUPPORTED;
-  if (kv4 && (!(k_scale > 0.f) || !(v_scale > 0.f) || !isfinite(k_scale) || !isfinite(v_scale))) return EAGLE_ERR_INVALID_ARG;
+  if (kv4 && (!kv4_scale_ok(k_scale) || !kv4_scale_ok(v_scale))) return EAGLE_ERR_INVALID_ARG;
   // what one of the calls below would refuse is refused before the first has run
   if (num_pages > (1 << 26)) return EAGLE_ERR_UNSUPPORTED;
   for (const void* a : {x, (const void*)out, w_qkv, w_o, w_gu, w_down, (const void*)rope, (const void*)k_cache,

@@ -7,10 +7,15 @@
 
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
+#include <math.h>
 
 #include "common.cuh"
 
 namespace eagle {
+
+// A cache's k_scale or v_scale that rows can be divided by: finite, positive, and
+// of a finite reciprocal (an infinite one would make NaN of zeros).
+inline bool kv4_scale_ok(float s) { return s > 0.f && isfinite(s) && isfinite(1.f / s); }
 
 // e4m3 scale byte of a group whose largest magnitude is `amax`: amax / 6 to
 // nearest even, at most 448; NaN stays NaN.

@@ -335,8 +335,7 @@ extern "C" int eagle_kv_append_kv4(const void* q, const void* k, const void* v, 
                                    int D, void* q_out, uint8_t* k_codes, uint8_t* k_scales, uint8_t* v_codes,
                                    uint8_t* v_scales, float k_scale, float v_scale, int num_pages,
                                    const int32_t* block_table, int max_pages, int32_t* dev_status, void* stream) {
-  if (!k_scales || !v_scales || !(k_scale > 0.f) || !(v_scale > 0.f) || !isfinite(k_scale) || !isfinite(v_scale))
-    return EAGLE_ERR_INVALID_ARG;
+  if (!k_scales || !v_scales || !kv4_scale_ok(k_scale) || !kv4_scale_ok(v_scale)) return EAGLE_ERR_INVALID_ARG;
   const AppendParams p = {q,  k,   v,         q_stride,  k_stride, v_stride, rope,    max_pos, cu_seqlens, ctx_lens, block_table,
                           B,  T,   Hq,        Hkv,       num_pages, max_pages, 1,     q_out,   k_codes,    v_codes,  k_scales,
                           v_scales, 1.f / k_scale, 1.f / v_scale, dev_status};

@@ -748,7 +748,8 @@ int eagle_kv_append(const void* q, const void* k, const void* v, long long q_str
  * v_scale, and per group of 16 channels:
  *   s = e4m3(min(max|x| / 6, 448)) to nearest even; a NaN makes s NaN
  *   m = the magnitude nearest to |x| / s, ties to the even code (0 if s = 0).
- * Errors and limits as eagle_kv_append; k_scale, v_scale finite and > 0. */
+ * Errors and limits as eagle_kv_append; k_scale, v_scale > 0, they and their
+ * reciprocals finite. */
 int eagle_kv_append_kv4(const void* q, const void* k, const void* v, long long q_stride,
                         long long k_stride, long long v_stride, const float* rope, int max_pos,
                         const int32_t* cu_seqlens, const int32_t* ctx_lens, int B, int T, int Hq,

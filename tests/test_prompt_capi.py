@@ -160,3 +160,17 @@ def test_workspace_serves_fewer_requests_and_rows(L, Hq, Hkv, D):
     # fp32 units hold 64 rows (64 / g tokens)
     most = 12 * 160 * 256 * (4 * D + 8 + 48) + 48 * Hkv * (2 * 65535 * 3 + (1 << 28) // (64 // g) + 160 * 12 * 6) + 4096
     assert table[-1][-1] <= most
+
+
+@pytest.mark.parametrize("name", ["k_scale", "v_scale"])
+def test_cache_scales_without_a_reciprocal(L, name):
+    """1 / 2^-129 is no fp32 number: 0 times it would be NaN."""
+    a = dict(k_scale=1.0, v_scale=1.0)
+    a[name] = 2.0 ** -129
+    assert L.eagle_kv_append_kv4(P, P, P, 512, 256, 256, P, 64, P, P, 2, 0, 4, 2, 128, ctypes.c_void_p(512), P, P, P, P,
+                                 a["k_scale"], a["v_scale"], 8, P, 4, N, N) == INVALID
+    assert L.eagle_draft_prompt(P, P, P, P, P, P, P, 1e-5, P, 8, P, P, P, P, P, P, a["k_scale"], a["v_scale"], 8, P, 4,
+                                ctypes.c_void_p(512), 2, 4, 256, 4, 2, 64, 256, 1, N, 0, N, N) == INVALID
+    a[name] = 2.0 ** -127
+    assert L.eagle_kv_append_kv4(P, P, P, 512, 256, 256, P, 64, P, P, 2, 0, 4, 2, 128, ctypes.c_void_p(512), P, P, P, P,
+                                 a["k_scale"], a["v_scale"], 8, P, 4, N, N) == OK
