@@ -119,11 +119,17 @@ Shape attn_shape(int B, int T, int Hq, int Hkv, int D, Path path) {
   return s;
 }
 // Single tokens take the few-rows kernel, everything else the two-tile kernel.
-// The lengths are on the device, so the rule goes by their mean.  Measured, us,
+// The host does not know the lengths, so the rule goes by their mean, and a
+// batch of unlike requests has one kernel for all of them.  What that costs, us,
+// 32 heads over 8, D 128, one call from a cold L2: a chunk of 512 rows beside 63
+// single tokens 158 on 16-bit pages (the parts alone 67 and 133) and 198 on 4-bit
+// (97 and 74); a chunk of 60 rows among 63 empty requests 70 on 16-bit pages, where
+// each row reads the whole context (30 as a call of its own), 43 on 4-bit (58).
+// Requests of one kind, us,
 // few rows / two tiles, 64 requests over 1024 .. 4096 keys, D 128:
 //   16-bit, 32 heads over 8: 1 token 121 / 130, 2 tokens 195 / 131;
 //     64 over 8: 122 / 130; 64 over 4 (16 rows): 84 / 76
-//   4-bit, 32 over 8: 1 token 61 / 140, 2 tokens 88 / 143, 3 tokens 121 / 143,
+//   4-bit, 32 over 8: 1 token 62 / 140, 2 tokens 88 / 143, 3 tokens 121 / 143,
 //     4 tokens 159 / 146; 64 over 4: 1 token 50 / 86, 2 tokens 89 / 90, 3 tokens 99 / 97
 bool few_rows(bool kv4, int B, int T, int Hq, int Hkv) {
   return kv4 ? T <= 2 * B && Hq / Hkv <= 16 : T <= B && Hq / Hkv <= 8;
@@ -430,10 +436,10 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanPar
 // Bound by each tile's chain S - softmax - P V: about 3,300 cycles per block
 // and two tiles (D 128), while the MMAs take 2,048 and the exponentials, at 32
 // a cycle and SM, 1,024 beside them.  Causal FLOPs at
-// 64 heads over 8, 8192 tokens: 825 us, 1.33 PFLOP/s; chunks of 256 .. 512
+// 64 heads over 8, 8192 tokens: 830 us, 1.32 PFLOP/s; chunks of 256 .. 512
 // tokens over 32k keys, 32 over 8: 656 us, 1.21 PFLOP/s; one prompt of 2048
-// tokens: 50-55 us.  On 4-bit pages the producers' conversions take issue slots
-// from the softmax: chunks over 8k keys 262 us, 205 us on 16-bit pages.
+// tokens: 50-56 us.  On 4-bit pages the producers' conversions take issue slots
+// from the softmax: chunks over 8k keys 272 us, 205 us on 16-bit pages.
 constexpr int kThreads = 512;
 constexpr int kSlots = 4;  // pieces known ahead
 constexpr int kNoPage = -0x7fffffff - 1;  // past the keys (or found out of range): reads as zeros
@@ -1588,9 +1594,11 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const MergeParams p) 
 //
 // 64 requests over 1024 .. 4096 keys, 32 heads over 8, D 128, with the plan:
 // 16-bit pages 120 us, 5.6 TB/s of K and V (bound by HBM: the copy rate
-// here is 6.8); 4-bit pages 62 us, 3.1 TB/s (bound by instructions: some 370 a
-// page and head, issue slots 55-59 % and the integer pipe 46-51 % busy in this
-// kernel).  Four requests over 32k keys, 4-bit: 49 us.
+// here is 6.7); 4-bit pages 62.5 us, 3.0 TB/s: neither issue slots (55-59 %, some
+// 370 instructions a page and head) nor the integer pipe (46-51 %) nor HBM are
+// full in this kernel, 16 warps an SM leave the latencies of a step's chain
+// uncovered, and the plan in front takes 12.7 us.  Four requests over 32k keys,
+// 4-bit: 49.6 us.
 constexpr int kFewThreads = 128;
 
 struct FewParams {

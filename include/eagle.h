@@ -8,7 +8,7 @@
  * the token-embedding input FC, and eagle_draft_layer, its decoder layer,
  * built on eagle_linear; before the first round the prompt path fills the
  * paged caches: eagle_kv_append, eagle_prompt_attn and eagle_draft_prompt,
- * their 4-bit-page forms beside them):
+ * their 4-bit-page forms, which the tree calls do not read, beside them):
  *   eagle_fuse_proj             EAGLE-3 fused feature g = W_proj [h_low; h_mid; h_high]
  *   eagle_tree_attn             tree-masked attention vs a paged KV cache + the tree rows
  *   eagle_lmhead_topk           LM-head GEMM with fused per-row top-k and log-softmax
@@ -708,7 +708,10 @@ int eagle_tree_verify_noalloc(int B, int R, int V, const int32_t* parent_row,
  * m in {0, 0.5, 1, 1.5, 2, 3, 4, 6} in bits 0-2, and stands for
  * k_scale * s * (+-m) (v_scale for values).  k_scale and v_scale are one
  * number per cache (1 unless the values leave e4m3's range: scales below
- * 2^-10 read as zero, above 448 saturate).
+ * 2^-10 read as zero, above 448 saturate).  4-bit pages are for prompts,
+ * chunks and single tokens: eagle_tree_attn, eagle_draft_layer and
+ * eagle_tree_commit read and write 16- and 32-bit pages only (eagle_kv4_read
+ * unpacks a pool for them).
  * ---------------------------------------------------------------------- */
 
 /* eagle_rope_table -- cos and sin of pos * theta^(-2 i / D) for positions
@@ -823,7 +826,8 @@ int eagle_prompt_attn_kv4(const void* q, long long q_stride, const uint8_t* k_co
 /* eagle_draft_prompt -- the drafter's decoder layer (eagle_draft_layer) over
  * packed prompt rows: it fills the drafter's paged cache and gives the rows'
  * outputs, so that the first eagle_draft_layer call of a round finds its
- * prefix.  [M7.5] section 0x03C (the drafter's own K/V of the committed
+ * prefix (in 16- or 32-bit pages; a prefix in 4-bit pages serves further prompt
+ * calls, not the draft rounds).  [M7.5] section 0x03C (the drafter's own K/V of the committed
  * prefix); [E3] section 3.4 "The transformer decoder layer".
  *   h = RMSNorm(x) * w_norm1;  q, k, v = split(h W_qkv^T)
  *   eagle_kv_append(q, k, v), then a = eagle_prompt_attn, scale 1/sqrt(D)
