@@ -563,7 +563,11 @@ def _append_rows(q, k, v, q_out):
     T, Hkv, D = shape
     if v.shape != shape or v.dtype is not dtype:
         raise ValueError("k and v must have one dtype and one shape")
-    ks, vs = _row_stride("k", k, D, T, Hkv), _row_stride("v", v, D, T, Hkv)
+    (ks, kh, k1), (vs, vh, v1) = k.stride(), v.stride()
+    if k1 != 1 or v1 != 1 or ((kh != D or vh != D) and Hkv > 1):
+        raise ValueError(f"k, v: heads and channels must be contiguous, strides {k.stride()}, {v.stride()}")
+    if T <= 1:
+        ks = vs = Hkv * D  # (a single row's stride leads nowhere and may be anything)
     if q is None:
         if q_out is not None:
             raise ValueError("q_out without q")

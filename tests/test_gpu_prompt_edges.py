@@ -280,3 +280,21 @@ def test_attn_factors_past_the_range(kind, q, scale, ks, n, ctx):
         assert (err <= half * np.abs(x.mean(0)) + (WEIGHT_HALF[kind] + (ctx + 16) * 2.0 ** -24) * np.abs(x).mean(0)).all()
         assert np.abs(f64(lse[r]) - np.log(w.sum())).max() <= 2.0 ** -20
     assert s["st"].item() == 0
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16", "kv4"])
+@pytest.mark.parametrize("new,ctx", [([1] * 4, [5, 300, 2500, 130]), ([40, 3, 170], [0, 300, 260])])
+def test_attn_non_finite_query_rows(kind, new, ctx):
+    """A query of NaN or infinities is its own row's matter."""
+    b = need_gpu()
+    s = make(97, new, ctx, 8, 2, 128, "fp32" if kind == "fp32" else "bf16", kv4=kind == "kv4")
+    clean, clse = run_attn(b, s, kind == "kv4")
+    q = s["q"].clone()
+    bad = torch.zeros(s["T"], 8, dtype=torch.bool, device="cuda")
+    bad[0, 3] = bad[2, :] = bad[-1, 5] = bad[1::7, 1] = True
+    q[bad] = torch.tensor([float("nan"), float("inf"), -float("inf"), 1.0], dtype=q.dtype, device="cuda").repeat(32)
+    s["q"] = q
+    out, lse = run_attn(b, s, kind == "kv4")
+    assert out[bad].isnan().all() and lse[bad].isnan().all()
+    assert torch.equal(out[~bad], clean[~bad]) and torch.equal(lse[~bad], clse[~bad])
+    assert s["st"].item() == 0
