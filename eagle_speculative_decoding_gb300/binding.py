@@ -71,6 +71,10 @@ _SIGS = {
                              _I, _P, _P]),
     "eagle_kv_append_kv4": (_I, [_P, _P, _P, _L, _L, _L, _P, _I, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P,
                                  _F, _F, _I, _P, _I, _P, _P]),
+    "eagle_kv_append_axes": (_I, [_P, _P, _P, _L, _L, _L, _P, _I, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P,
+                                  _I, _P, _I, _P, _P]),
+    "eagle_kv_append_axes_kv4": (_I, [_P, _P, _P, _L, _L, _L, _P, _I, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P,
+                                      _P, _P, _F, _F, _I, _P, _I, _P, _P]),
     "eagle_kv4_read": (_I, [_P, _P, _F, _I, _I, _I, _I, _P, _P]),
     "eagle_prompt_attn_workspace_size": (_Z, [_I, _I, _I, _I, _I]),
     "eagle_prompt_attn": (_I, [_P, _L, _P, _P, _I, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P, _Z,
@@ -633,6 +637,49 @@ def eagle_kv_append_kv4(q, k, v, rope, cu_seqlens, ctx_lens, block_table, k_code
         ctx_lens.data_ptr(), B, T, Hq, Hkv, D, _addr(q_out), k_codes.data_ptr(), k_scales.data_ptr(),
         v_codes.data_ptr(), v_scales.data_ptr(), k_scale, v_scale, P, block_table.data_ptr(), pages, _addr(status),
         _raw_stream(stream, k.device)))
+
+
+def _axes(positions, pair_axis, T, D):
+    """Checks of a call's positions and axes: the number of axes."""
+    shape = positions.shape
+    if shape != (shape[0], T) or positions.dtype is not _I32 or not positions.is_contiguous():
+        raise ValueError("positions must be contiguous int32 [axes, T]")
+    if pair_axis is not None and not (pair_axis.shape == (D // 2,) and pair_axis.dtype is _I32 and pair_axis.is_contiguous()):
+        raise ValueError("pair_axis must be contiguous int32 [D / 2]")
+    if not (positions.is_cuda and (pair_axis is None or pair_axis.is_cuda)):
+        raise ValueError("the arrays must be on the GPU")
+    return shape[0]
+
+
+def eagle_kv_append_axes(q, k, v, rope, positions, cu_seqlens, ctx_lens, block_table, k_cache, v_cache, pair_axis=None,
+                         q_out=None, status=None, stream=None):
+    """eagle_kv_append with the rows' positions given, positions [axes, T], and
+    an axis for each channel pair, pair_axis [D / 2] (see include/eagle.h)."""
+    T, Hkv, D, Hq, qs, ks, vs = _append_rows(q, k, v, q_out)
+    P, max_pos = _pages16(k_cache, v_cache, Hkv, D, k.dtype), _rope_rows(rope, D)
+    B, pages = _lengths(k, cu_seqlens, ctx_lens, block_table, status)
+    axes = _axes(positions, pair_axis, T, D)
+    _check("eagle_kv_append_axes", lib().eagle_kv_append_axes(
+        _addr(q), k.data_ptr(), v.data_ptr(), qs, ks, vs, _addr(rope), max_pos, positions.data_ptr(), axes,
+        _addr(pair_axis), cu_seqlens.data_ptr(), ctx_lens.data_ptr(), B, T, Hq, Hkv, D, _dtype(k), _addr(q_out),
+        k_cache.data_ptr(), v_cache.data_ptr(), P, block_table.data_ptr(), pages, _addr(status),
+        _raw_stream(stream, k.device)))
+
+
+def eagle_kv_append_axes_kv4(q, k, v, rope, positions, cu_seqlens, ctx_lens, block_table, k_codes, k_scales, v_codes,
+                             v_scales, pair_axis=None, q_out=None, k_scale=1.0, v_scale=1.0, status=None, stream=None):
+    """eagle_kv_append_axes into 4-bit pages (see include/eagle.h)."""
+    T, Hkv, D, Hq, qs, ks, vs = _append_rows(q, k, v, q_out)
+    if k.dtype != torch.bfloat16:
+        raise ValueError("k and v must be bf16")
+    P, max_pos = _pages4(k_codes, k_scales, v_codes, v_scales, Hkv, D), _rope_rows(rope, D)
+    B, pages = _lengths(k, cu_seqlens, ctx_lens, block_table, status)
+    axes = _axes(positions, pair_axis, T, D)
+    _check("eagle_kv_append_axes_kv4", lib().eagle_kv_append_axes_kv4(
+        _addr(q), k.data_ptr(), v.data_ptr(), qs, ks, vs, _addr(rope), max_pos, positions.data_ptr(), axes,
+        _addr(pair_axis), cu_seqlens.data_ptr(), ctx_lens.data_ptr(), B, T, Hq, Hkv, D, _addr(q_out), k_codes.data_ptr(),
+        k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), k_scale, v_scale, P, block_table.data_ptr(), pages,
+        _addr(status), _raw_stream(stream, k.device)))
 
 
 def eagle_kv4_read(codes, scales, out, scale=1.0, stream=None):

@@ -49,7 +49,11 @@ struct AppendParams {
   uint8_t *ks, *vs;       // 4-bit: the scales
   float k_inv, v_inv;     // 4-bit: 1 / k_scale, 1 / v_scale
   int32_t* status;
+  const int32_t *pos, *axis;  // several axes: [axes, T], and [D/2] or null (every pair on axis 0)
+  int axes;
 };
+constexpr int kMaxAxes = 8;
+constexpr uint32_t kStill = 0x7fc01234u;  // in a cosine's place, a NaN that no table gives: the pair is not turned
 
 template <typename T>
 struct Vec {
@@ -99,10 +103,16 @@ __device__ __forceinline__ void store4(const float* x, float inv, bool live, uin
   if ((vec & 1) == 0) scales[vec >> 1] = sb;
 }
 
-template <typename T, int D, bool KV4>
+// AXES: a row's cosines and sines are gathered pair by pair, each from the table's
+// row at the position on the pair's axis, to shared memory, where all the row's
+// heads read them as vectors: D/2 gathers a row and not (Hq + Hkv) D/2, whatever
+// the order of the axes.  The gathers start with the rows' loads, before the
+// lookup of the request.
+template <typename T, int D, bool KV4, bool AXES>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams p) {
   constexpr int kV = Vec<T>::N, kHalf = D / 2, kVph = kHalf / kV;  // vectors per half head
   __shared__ int s_pos[kMaxRows], s_dst[kMaxRows];  // position (-1: skip), cache row (-1: none)
+  extern __shared__ __align__(16) float s_turn[];   // AXES: [rows][2][D/2]
   pdl_wait();
   pdl_trigger();
   const int t0 = blockIdx.x * p.tpc, rows = min(p.tpc, p.T - t0);
@@ -132,14 +142,46 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
   };
   load(0);
 
+  if constexpr (AXES) {
+    for (int x = threadIdx.x; x < rows * kHalf; x += kThreads) {
+      const int r = x / kHalf, i = x % kHalf;
+      const int ax = p.axis ? p.axis[i] : 0;
+      uint32_t c = kStill;
+      float s = 0.f;
+      if (ax >= 0 && ax < p.axes) {
+        const int at = p.pos[(size_t)ax * p.T + t0 + r];
+        if (at >= 0 && at < p.max_pos) {
+          const float x = p.rope[(size_t)at * D + i];
+          c = x == x ? __float_as_uint(x) : 0x7fffffffu;
+          s = p.rope[(size_t)at * D + kHalf + i];
+        }
+      }
+      s_turn[r * D + i] = __uint_as_float(c);
+      s_turn[r * D + kHalf + i] = s;
+    }
+  }
   for (int r = threadIdx.x >> 5; r < rows; r += kThreads / 32) {
     const int t = t0 + r;
     const int bq = warp_find_request(p.cu, p.B, t);
+    bool bad = false;  // AXES: a position past the table on some axis, or a pair on an axis that is none
+    if constexpr (AXES) {
+      if (lane < p.axes) {
+        const int at = p.pos[(size_t)lane * p.T + t];
+        bad = at < 0 || at >= p.max_pos;
+      }
+      if (p.axis)
+#pragma unroll
+        for (int i = 0; i < kHalf; i += 32) {
+          const int ax = p.axis[i + lane];
+          bad = bad || ax < -1 || ax >= p.axes;
+        }
+      bad = __any_sync(0xffffffffu, bad);
+    }
     if (lane == 0) {
       const int c0 = p.cu[bq], c1 = p.cu[bq + 1], ctx = p.ctx[bq];
       const long long pos = (long long)ctx + (t - c0);
       int dst = -1, at = -1;
-      if (t < c0 || t >= c1 || ctx < 0 || pos > 0x7fffffff || (p.rope && pos >= p.max_pos)) {
+      if (t < c0 || t >= c1 || ctx < 0 || pos > 0x7fffffff || (AXES ? bad : p.rope && pos >= p.max_pos)) {
         set_status(p.status, EAGLE_ERR_INVALID_ARG);
       } else {
         at = (int)pos;
@@ -169,8 +211,9 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
       unpack(a[u], x1, tag);
       unpack(b[u], x2, tag);
       if (!is_v && p.rope && in && pos >= 0) {
-        const float4* cs = reinterpret_cast<const float4*>(p.rope + (size_t)pos * D + i0);
-        const float4* sn = reinterpret_cast<const float4*>(p.rope + (size_t)pos * D + kHalf + i0);
+        const float* turn = AXES ? s_turn + r * D : p.rope + (size_t)pos * D;
+        const float4* cs = reinterpret_cast<const float4*>(turn + i0);
+        const float4* sn = reinterpret_cast<const float4*>(turn + kHalf + i0);
 #pragma unroll
         for (int j = 0; j < kV / 4; ++j) {
           const float4 c4 = cs[j], s4 = sn[j];
@@ -180,6 +223,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
             // rounded one by one: the 4-bit codes are then those of the
             // same three operations anywhere
             const float y1 = x1[4 * j + e], y2 = x2[4 * j + e];
+            if (AXES && __float_as_uint(c[e]) == kStill) continue;
             x1[4 * j + e] = __fsub_rn(__fmul_rn(y1, c[e]), __fmul_rn(y2, s[e]));
             x2[4 * j + e] = __fadd_rn(__fmul_rn(y2, c[e]), __fmul_rn(y1, s[e]));
           }
@@ -283,7 +327,7 @@ int append_check(const AppendParams& p, int D, size_t es) {
   return EAGLE_OK;
 }
 
-template <typename T, bool KV4>
+template <typename T, bool KV4, bool AXES = false>
 int append_launch(AppendParams p, int D, void* stream) {
   if (p.T == 0) return EAGLE_OK;
   const int per_row = (p.Hq + 2 * p.Hkv) * (D / 2 / Vec<T>::N);
@@ -292,12 +336,19 @@ int append_launch(AppendParams p, int D, void* stream) {
   p.tpc = std::max(1, std::min(kMaxRows, kThreads * kUnroll / per_row));
   const int grid = (p.T + p.tpc - 1) / p.tpc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const size_t smem = AXES ? (size_t)p.tpc * D * sizeof(float) : 0;
   if (D == 128)
-    launch(kv_append_kernel<T, 128, KV4>, grid, kThreads, 0, s, p);
+    launch(kv_append_kernel<T, 128, KV4, AXES>, grid, kThreads, smem, s, p);
   else
-    launch(kv_append_kernel<T, 64, KV4>, grid, kThreads, 0, s, p);
+    launch(kv_append_kernel<T, 64, KV4, AXES>, grid, kThreads, smem, s, p);
   note_launch();
   return last_launch_status();
+}
+
+// What several axes need beside append_check().
+int axes_check(const AppendParams& p) {
+  if (p.axes < 1 || !p.rope || (p.T > 0 && !p.pos)) return EAGLE_ERR_INVALID_ARG;
+  return p.axes > kMaxAxes ? EAGLE_ERR_UNSUPPORTED : EAGLE_OK;
 }
 
 }  // namespace
@@ -342,6 +393,41 @@ extern "C" int eagle_kv_append_kv4(const void* q, const void* k, const void* v, 
   const int rc = append_check(p, D, 2);
   if (rc != EAGLE_OK) return rc;
   return append_launch<__nv_bfloat16, true>(p, D, stream);
+}
+
+extern "C" int eagle_kv_append_axes(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
+                                    long long v_stride, const float* rope, int max_pos, const int32_t* positions,
+                                    int axes, const int32_t* pair_axis, const int32_t* cu_seqlens,
+                                    const int32_t* ctx_lens, int B, int T, int Hq, int Hkv, int D, int dtype,
+                                    void* q_out, void* k_cache, void* v_cache, int num_pages,
+                                    const int32_t* block_table, int max_pages, int32_t* dev_status, void* stream) {
+  if (dtype != EAGLE_BF16 && dtype != EAGLE_FP32) return EAGLE_ERR_INVALID_ARG;
+  const AppendParams p = {q,  k,   v,         q_stride,  k_stride, v_stride, rope,    max_pos, cu_seqlens, ctx_lens, block_table,
+                          B,  T,   Hq,        Hkv,       num_pages, max_pages, 1,     q_out,   k_cache,    v_cache,  nullptr,
+                          nullptr, 1.f, 1.f, dev_status, positions, pair_axis, axes};
+  int rc = append_check(p, D, dtype == EAGLE_BF16 ? 2 : 4);
+  if (rc == EAGLE_OK) rc = axes_check(p);
+  if (rc != EAGLE_OK) return rc;
+  return dtype == EAGLE_BF16 ? append_launch<__nv_bfloat16, false, true>(p, D, stream)
+                             : append_launch<float, false, true>(p, D, stream);
+}
+
+extern "C" int eagle_kv_append_axes_kv4(const void* q, const void* k, const void* v, long long q_stride,
+                                        long long k_stride, long long v_stride, const float* rope, int max_pos,
+                                        const int32_t* positions, int axes, const int32_t* pair_axis,
+                                        const int32_t* cu_seqlens, const int32_t* ctx_lens, int B, int T, int Hq,
+                                        int Hkv, int D, void* q_out, uint8_t* k_codes, uint8_t* k_scales,
+                                        uint8_t* v_codes, uint8_t* v_scales, float k_scale, float v_scale,
+                                        int num_pages, const int32_t* block_table, int max_pages,
+                                        int32_t* dev_status, void* stream) {
+  if (!k_scales || !v_scales || !kv4_scale_ok(k_scale) || !kv4_scale_ok(v_scale)) return EAGLE_ERR_INVALID_ARG;
+  const AppendParams p = {q,  k,   v,         q_stride,  k_stride, v_stride, rope,    max_pos, cu_seqlens, ctx_lens, block_table,
+                          B,  T,   Hq,        Hkv,       num_pages, max_pages, 1,     q_out,   k_codes,    v_codes,  k_scales,
+                          v_scales, 1.f / k_scale, 1.f / v_scale, dev_status, positions, pair_axis, axes};
+  int rc = append_check(p, D, 2);
+  if (rc == EAGLE_OK) rc = axes_check(p);
+  if (rc != EAGLE_OK) return rc;
+  return append_launch<__nv_bfloat16, true, true>(p, D, stream);
 }
 
 extern "C" int eagle_kv4_read(const uint8_t* codes, const uint8_t* scales, float scale, int num_pages, int Hkv, int D,

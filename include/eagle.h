@@ -761,6 +761,38 @@ int eagle_kv_append_kv4(const void* q, const void* k, const void* v, long long q
                         int num_pages, const int32_t* block_table, int max_pages,
                         int32_t* dev_status, void* stream);
 
+/* eagle_kv_append_axes -- eagle_kv_append with the rows' positions given, on
+ * several axes: a row's slot in the cache still goes by its number (p =
+ * ctx_lens[b] + t - cu_seqlens[b]), its rotation by positions of its own, such
+ * as time, height and width of an image token, or the place of a row behind a
+ * prefix that several requests share (eagle_prefix_attn), whose slots start at 0.
+ * With a = pair_axis[i] and (c_i, s_i) = entry i of rope[positions[a, t]], pair i
+ * of q and k turns as above; pairs of axis -1 are not turned.
+ *   positions : [axes, T] int32;  rope : [max_pos, 2, D/2] fp32 (not NULL)
+ *   pair_axis : [D/2] int32, each -1 .. axes - 1 (axes in sections, taking turns,
+ *               or in any other order), or NULL: every pair on axis 0
+ * Device-detected, beside what eagle_kv_append detects: a position outside
+ * 0 .. max_pos - 1 on any axis, a pair_axis entry out of range (all rows then)
+ * -> EAGLE_ERR_INVALID_ARG, the row is skipped.  Limits: those of
+ * eagle_kv_append, axes <= 8. */
+int eagle_kv_append_axes(const void* q, const void* k, const void* v, long long q_stride,
+                         long long k_stride, long long v_stride, const float* rope, int max_pos,
+                         const int32_t* positions, int axes, const int32_t* pair_axis,
+                         const int32_t* cu_seqlens, const int32_t* ctx_lens, int B, int T, int Hq,
+                         int Hkv, int D, int dtype, void* q_out, void* k_cache, void* v_cache,
+                         int num_pages, const int32_t* block_table, int max_pages,
+                         int32_t* dev_status, void* stream);
+
+/* eagle_kv_append_axes_kv4 -- the same into 4-bit pages (eagle_kv_append_kv4). */
+int eagle_kv_append_axes_kv4(const void* q, const void* k, const void* v, long long q_stride,
+                             long long k_stride, long long v_stride, const float* rope, int max_pos,
+                             const int32_t* positions, int axes, const int32_t* pair_axis,
+                             const int32_t* cu_seqlens, const int32_t* ctx_lens, int B, int T,
+                             int Hq, int Hkv, int D, void* q_out, uint8_t* k_codes,
+                             uint8_t* k_scales, uint8_t* v_codes, uint8_t* v_scales, float k_scale,
+                             float v_scale, int num_pages, const int32_t* block_table,
+                             int max_pages, int32_t* dev_status, void* stream);
+
 /* eagle_kv4_read -- the values of 4-bit pages, in the layout of an ordinary
  * cache: out [num_pages, 16, Hkv, D] dtype `dtype` (fp32 product of code,
  * scale byte and `scale`, rounded once).  For inspection and for handing a

@@ -1,0 +1,57 @@
+"""What the binding of the calls for a batch behind a shared prompt refuses before
+it calls the library, on CPU tensors (no GPU needed): a call whose arrays agree
+gets as far as the check that asks for a GPU; one changed array does not."""
+import pytest
+import torch
+
+from eagle_speculative_decoding_gb300 import binding as eb
+from test_prompt_binding import BF16, B, CACHE, CODES, D, F32, HKV, HQ, I32, INDEX, ROPE, ROWS, T, lengths, pages4, pages16, rows, z
+
+
+def axes():
+    return dict(positions=z(3, T, dtype=I32), pair_axis=z(D // 2, dtype=I32))
+
+
+CALLS = dict(
+    axes=(eb.eagle_kv_append_axes, lambda: {**rows(), **lengths(), **pages16(), **axes()}),
+    axes4=(eb.eagle_kv_append_axes_kv4, lambda: {**rows(), **lengths(), **pages4(), **axes()}),
+)
+AXES = [dict(positions=z(3, T + 1, dtype=I32)), dict(positions=z(3, T, dtype=torch.long)), dict(positions=z(T, 3, dtype=I32).t()),
+        dict(positions=z(3, 2 * T, dtype=I32)[:, ::2]), dict(pair_axis=z(D, dtype=I32)), dict(pair_axis=z(D // 2, dtype=torch.long)),
+        dict(pair_axis=z(D, dtype=I32)[::2])]
+
+
+def on_gpu(monkeypatch):
+    """Lets CPU tensors pass for the GPU's in the checks."""
+    monkeypatch.setattr(eb, "_lengths", lambda rows, cu, ctx, table, status: table.shape)
+
+
+def cases():
+    both = {"axes": INDEX + CACHE + ROPE + ROWS, "axes4": INDEX + CODES + ROPE + ROWS}
+    return [(name, i, change) for name, changes in both.items() for i, change in enumerate(changes)]
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_arrays_that_agree_pass_every_check_but_the_last(name):
+    call, base = CALLS[name]
+    with pytest.raises(ValueError, match="on the GPU"):
+        call(**base())
+
+
+@pytest.mark.parametrize("name,i,change", cases(), ids=lambda x: "-".join(x) if isinstance(x, dict) else str(x))
+def test_arrays_that_do_not_are_refused(name, i, change):
+    call, base = CALLS[name]
+    with pytest.raises(ValueError) as e:
+        call(**{**base(), **change})
+    assert "on the GPU" not in str(e.value)
+
+
+@pytest.mark.parametrize("name", ["axes", "axes4"])
+@pytest.mark.parametrize("change", AXES, ids=lambda c: "-".join(c))
+def test_positions_that_do_not_agree_are_refused(name, change, monkeypatch):
+    call, base = CALLS[name]
+    on_gpu(monkeypatch)
+    with pytest.raises(ValueError, match="positions must|pair_axis must"):
+        call(**{**base(), **change})
+    with pytest.raises(ValueError, match="on the GPU"):
+        call(**base())

@@ -1,0 +1,51 @@
+"""Refusals of the calls for a batch behind a shared prompt, on the host: every
+case returns before any CUDA call (no GPU needed)."""
+import ctypes
+import os
+
+import pytest
+
+OK, INVALID, UNSUPPORTED, WORKSPACE = 0, 1, 2, 3
+N, P, ODD = None, ctypes.c_void_p(256), ctypes.c_void_p(8)
+
+
+@pytest.fixture(scope="module")
+def L():
+    from eagle_speculative_decoding_gb300 import binding, build
+    if not os.path.exists(binding.LIB_PATH):
+        build.build()
+    return binding.lib()
+
+
+def append(L, **kw):
+    a = dict(q=P, k=P, v=P, qs=512, ks=256, vs=256, rope=P, max_pos=64, pos=P, axes=3, axis=P, cu=P, ctx=P, B=2, T=4, Hq=4,
+             Hkv=2, D=128, dtype=1, q_out=ctypes.c_void_p(512), kc=P, vc=P, pages=8, table=P, width=4)
+    a.update(kw)
+    return L.eagle_kv_append_axes(a["q"], a["k"], a["v"], a["qs"], a["ks"], a["vs"], a["rope"], a["max_pos"], a["pos"],
+                                  a["axes"], a["axis"], a["cu"], a["ctx"], a["B"], a["T"], a["Hq"], a["Hkv"], a["D"],
+                                  a["dtype"], a["q_out"], a["kc"], a["vc"], a["pages"], a["table"], a["width"], N, N)
+
+
+@pytest.mark.parametrize("want,kw", [
+    (OK, dict(T=0)), (OK, dict(T=0, q=N, k=N, v=N, q_out=N, pos=N)), (OK, dict(T=0, axis=N, axes=1)),
+    (INVALID, dict(rope=N)), (INVALID, dict(pos=N)), (INVALID, dict(axes=0)), (INVALID, dict(axes=-1)),
+    (UNSUPPORTED, dict(axes=9)), (INVALID, dict(max_pos=0)), (INVALID, dict(k=N)), (INVALID, dict(vc=N)), (INVALID, dict(cu=N)),
+    (INVALID, dict(ctx=N)), (INVALID, dict(table=N)), (INVALID, dict(q_out=N)), (INVALID, dict(dtype=2)), (INVALID, dict(T=-1)),
+    (UNSUPPORTED, dict(D=96)), (INVALID, dict(qs=511)), (INVALID, dict(rope=ODD)), (INVALID, dict(kc=ODD)),
+    (INVALID, dict(q_out=P, qs=1024)), (UNSUPPORTED, dict(pages=(1 << 26) + 1)),
+])
+def test_append_axes_refusals(L, want, kw):
+    assert append(L, **kw) == want
+
+
+@pytest.mark.parametrize("want,kw", [
+    (OK, dict(T=0)), (INVALID, dict(ks=N)), (INVALID, dict(k_scale=0.0)), (INVALID, dict(v_scale=2.0 ** -129)),
+    (INVALID, dict(rope=N)), (INVALID, dict(pos=N)), (INVALID, dict(axes=0)), (UNSUPPORTED, dict(axes=9)),
+    (UNSUPPORTED, dict(D=32)),
+])
+def test_append_axes_kv4_refusals(L, want, kw):
+    a = dict(T=4, D=128, ks=P, rope=P, pos=P, axes=3, k_scale=1.0, v_scale=1.0)
+    a.update(kw)
+    assert L.eagle_kv_append_axes_kv4(P, P, P, 512, 256, 256, a["rope"], 64, a["pos"], a["axes"], P, P, P, 2, a["T"], 4, 2,
+                                      a["D"], ctypes.c_void_p(512), P, a["ks"], P, P, a["k_scale"], a["v_scale"], 8, P, 4, N,
+                                      N) == want
