@@ -81,6 +81,8 @@ _SIGS = {
                                _P, _P]),
     "eagle_prompt_attn_kv4": (_I, [_P, _L, _P, _P, _P, _P, _F, _F, _I, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I,
                                    _I, _F, _P, _Z, _P, _P]),
+    "eagle_sample": (_I, [_P, _L, _I, _I, _I, _P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P]),
+    "eagle_truncate_logits": (_I, [_P, _L, _I, _I, _I, _P, _P, _P, _P, _I, _P, _L, _P, _P, _P]),
     "eagle_draft_prompt_workspace_size": (_Z, [_I, _I, _I, _I, _I, _I, _I, _I]),
     "eagle_draft_prompt": (_I, [_P, _P, _P, _P, _P, _P, _P, _F, _P, _I, _P, _P, _P, _P, _P, _P, _F, _F, _I, _P, _I, _P,
                                 _I, _I, _I, _I, _I, _I, _I, _I, _P, _Z, _P, _P]),
@@ -772,4 +774,75 @@ def eagle_draft_prompt(x, weights, rope, cu_seqlens, ctx_lens, k_cache, v_cache,
         ctx_lens.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scales), _addr(v_scales), k_scale, v_scale,
         P, block_table.data_ptr(), pages, out.data_ptr(), B, T, d, Hq, Hkv, D, I, dt,
         ws.data_ptr(), ws.numel(), _addr(status), _raw_stream(stream, x.device)))
+    return out
+
+
+# ------------------------------------------------------------------ sampling
+def _logit_rows(name, x):
+    """(M, V, row stride) of rows whose entries are contiguous."""
+    M, V = x.shape
+    rows, last = x.stride()
+    if last != 1 and V > 1:
+        raise ValueError(f"{name}: a row's entries must be contiguous, strides {x.stride()}")
+    return M, V, rows if M > 1 else V  # (a single row's stride leads nowhere and may be anything)
+
+
+def _per_request(settings, M, rows_per_request):
+    """Checks of the settings of each request (None: left out)."""
+    n = -(-M // rows_per_request) if rows_per_request > 0 else 0
+    for (name, dtype), t in zip((("temperature", _F32), ("top_k", _I32), ("top_p", _F32), ("min_p", _F32)), settings):
+        if t is not None and not (t.shape == (n,) and t.dtype is dtype and t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous {dtype} [{n}], an entry per request")
+        if t is not None and not t.is_cuda:
+            raise ValueError("the arrays must be on the GPU")
+
+
+def _per_row(name, t, M, dtype):
+    if t is not None and not (t.shape == (M,) and t.dtype is dtype and t.is_contiguous()):
+        raise ValueError(f"{name} must be contiguous {dtype} [{M}], an entry per row")
+    if t is not None and not t.is_cuda:
+        raise ValueError("the arrays must be on the GPU")
+
+
+def eagle_sample(logits, uniforms, tokens, temperature=None, top_k=None, top_p=None, min_p=None, rows_per_request=1,
+                 logprobs=None, n_kept=None, status=None, stream=None):
+    """A token from each row of logits [M, V] by temperature, top-k, top-p and
+    min-p (one entry per request, each optional), from the uniform numbers given
+    (see include/eagle.h)."""
+    M, V, stride = _logit_rows("logits", logits)
+    if status is not None and status.dtype is not _I32:
+        raise ValueError("status must be int32")
+    if uniforms is None or tokens is None:
+        raise ValueError("uniforms and tokens must be given")
+    _per_row("uniforms", uniforms, M, _F32)
+    _per_row("tokens", tokens, M, _I32)
+    _per_row("logprobs", logprobs, M, _F32)
+    _per_row("n_kept", n_kept, M, _I32)
+    _per_request((temperature, top_k, top_p, min_p), M, rows_per_request)
+    if not logits.is_cuda:
+        raise ValueError("the arrays must be on the GPU")
+    _check("eagle_sample", lib().eagle_sample(
+        logits.data_ptr(), stride, M, V, _dtype(logits), _addr(temperature), _addr(top_k), _addr(top_p), _addr(min_p),
+        rows_per_request, uniforms.data_ptr(), tokens.data_ptr(), _addr(logprobs), _addr(n_kept), _addr(status),
+        _raw_stream(stream, logits.device)))
+    return tokens
+
+
+def eagle_truncate_logits(logits, out, temperature=None, top_k=None, top_p=None, min_p=None, rows_per_request=1, n_kept=None,
+                          status=None, stream=None):
+    """The logits [M, V] that eagle_sample's truncation keeps, the others as
+    minus infinity; out may be logits (see include/eagle.h)."""
+    M, V, stride = _logit_rows("logits", logits)
+    if out.shape != logits.shape or out.dtype is not logits.dtype:
+        raise ValueError("out must have the logits' shape and dtype")
+    _, _, out_stride = _logit_rows("out", out)
+    if status is not None and status.dtype is not _I32:
+        raise ValueError("status must be int32")
+    _per_row("n_kept", n_kept, M, _I32)
+    _per_request((temperature, top_k, top_p, min_p), M, rows_per_request)
+    if not (logits.is_cuda and out.is_cuda):
+        raise ValueError("the arrays must be on the GPU")
+    _check("eagle_truncate_logits", lib().eagle_truncate_logits(
+        logits.data_ptr(), stride, M, V, _dtype(logits), _addr(temperature), _addr(top_k), _addr(top_p), _addr(min_p),
+        rows_per_request, out.data_ptr(), out_stride, _addr(n_kept), _addr(status), _raw_stream(stream, logits.device)))
     return out

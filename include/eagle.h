@@ -884,6 +884,59 @@ int eagle_draft_prompt(const void* x, const void* w_norm1, const void* w_qkv, co
                        int Hq, int Hkv, int D, int I, int dtype, void* ws, size_t ws_bytes,
                        int32_t* dev_status, void* stream);
 
+/* ------------------------------------------------------------------------
+ * eagle_sample -- a token from each row of logits, by temperature, top-k, top-p
+ * and min-p, from a uniform number that the caller gives: the token behind a
+ * prompt, or a step of a target without a draft.  [E1] "Verification Phase:
+ * Multi-Round Speculative Sampling on Trees" (the target's own distribution,
+ * of which verification is lossless).
+ * Entries of row r are ordered by (logit descending, index ascending), with
+ * weights w_i = exp((x_i - max x) / T):
+ *   top-k keeps the first k;
+ *   top-p keeps, of these, an entry while the weights before it add up to less
+ *         than p times the sum of them all (the first entry always);
+ *   min-p keeps w_i >= min_p (the largest weight is 1).
+ *   token = the first index, in the order of indices, at which the running sum of
+ *         the kept weights exceeds u times their sum;
+ *   logprob = log(w_token / sum of the kept weights);  n_kept = entries kept.
+ * T = 0: the first entry (log-prob 0, one kept) whatever the others say.
+ * Entries of minus infinity are never kept.  Weights are whole multiples of 2^-44
+ * (good to 2^-36 of themselves) with exact sums, so a result does not depend on
+ * the order of summation; entries below 2^-45 weigh nothing, nor does one that
+ * lies further below the maximum than fp32 reaches.
+ *   logits : rows of V entries, row_stride elements apart, dtype `dtype`; a row
+ *            may start at any element
+ *   temperature, top_k, top_p, min_p : one entry per request, row r reads entry
+ *            r / rows_per_request; NULL leaves that out (temperature: 1).
+ *            top_k 0 or >= V, top_p >= 1, min_p 0: no truncation
+ *   uniforms : [M] fp32 in [0, 1)
+ *   tokens : [M] int32;  logprobs : [M] fp32 or NULL;  n_kept : [M] int32 or NULL
+ * Device-detected: a NaN or +infinity in a row, or nothing but -infinity ->
+ * EAGLE_ERR_NONFINITE; a temperature that is negative or not finite, a top_k
+ * below 0, a top_p below 0 or NaN, a min_p outside 0 .. 1 or a uniform outside
+ * [0, 1) -> EAGLE_ERR_INVALID_ARG.  Such a row gives token -1, log-prob -infinity
+ * and n_kept 0; the others are not affected.
+ * One kernel, no workspace.  M = 0 does nothing.
+ * Limits: M <= 65535, V <= 262144, rows_per_request >= 1. */
+int eagle_sample(const void* logits, long long row_stride, int M, int V, int dtype,
+                 const float* temperature, const int32_t* top_k, const float* top_p,
+                 const float* min_p, int rows_per_request, const float* uniforms, int32_t* tokens,
+                 float* logprobs, int32_t* n_kept, int32_t* dev_status, void* stream);
+
+/* eagle_truncate_logits -- the logits that eagle_sample's truncation keeps, the
+ * others as minus infinity: with them eagle_tree_verify verifies against the
+ * truncated distribution (target_logits fp32 [B, R, V], M = B R,
+ * rows_per_request = R, and the temperature that the truncation used).
+ *   out : rows of V entries, out_stride elements apart, dtype `dtype`; may be
+ *         `logits` itself (in place, with one stride)
+ * A row in error is not written.  T = 0 keeps the first entry alone.  Everything
+ * else as eagle_sample. */
+int eagle_truncate_logits(const void* logits, long long row_stride, int M, int V, int dtype,
+                          const float* temperature, const int32_t* top_k, const float* top_p,
+                          const float* min_p, int rows_per_request, void* out,
+                          long long out_stride, int32_t* n_kept, int32_t* dev_status,
+                          void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -62,3 +62,4 @@ from .prompt_oracle import (  # noqa: F401,E402
     rotate,
     row_places,
 )
+from .sample_oracle import sample, truncate  # noqa: F401,E402

@@ -55,3 +55,41 @@ def test_positions_that_do_not_agree_are_refused(name, change, monkeypatch):
         call(**{**base(), **change})
     with pytest.raises(ValueError, match="on the GPU"):
         call(**base())
+
+
+def sampling():
+    return dict(logits=z(T, 50, dtype=F32), uniforms=z(T, dtype=F32), tokens=z(T, dtype=I32), temperature=z(3, dtype=F32),
+                top_k=z(3, dtype=I32), top_p=z(3, dtype=F32), min_p=z(3, dtype=F32), rows_per_request=2, logprobs=z(T, dtype=F32),
+                n_kept=z(T, dtype=I32), status=z(1, dtype=I32))
+
+
+def truncating():
+    kw = {k: v for k, v in sampling().items() if k not in ("uniforms", "tokens", "logprobs")}
+    return {**kw, "out": z(T, 50, dtype=F32)}
+
+
+SETTINGS = [dict(temperature=z(2, dtype=F32)), dict(temperature=z(3)), dict(top_k=z(3, dtype=torch.long)), dict(top_k=z(4, dtype=I32)),
+            dict(top_p=z(6, dtype=F32)[::2]), dict(min_p=z(3, 1, dtype=F32)), dict(n_kept=z(T, dtype=torch.long)),
+            dict(n_kept=z(3, dtype=I32)), dict(rows_per_request=1), dict(rows_per_request=0), dict(status=z(1, dtype=torch.long)),
+            dict(logits=z(T, 100, dtype=F32)[:, ::2]), dict(logits=z(50, T, dtype=F32).t())]
+SAMPLE = [dict(uniforms=z(T - 1, dtype=F32)), dict(uniforms=z(T)), dict(uniforms=None), dict(tokens=z(T, dtype=torch.long)),
+          dict(tokens=None), dict(logprobs=z(T)), dict(logprobs=z(2 * T, dtype=F32)[::2])]
+TRUNCATE = [dict(out=z(T, 49, dtype=F32)), dict(out=z(T, 50)), dict(out=z(T, 100, dtype=F32)[:, ::2])]
+
+
+@pytest.mark.parametrize("call,base,change", [(eb.eagle_sample, sampling, c) for c in SETTINGS + SAMPLE]
+                         + [(eb.eagle_truncate_logits, truncating, c) for c in SETTINGS + TRUNCATE],
+                         ids=lambda x: "-".join(x) if isinstance(x, dict) else getattr(x, "__name__", ""))
+def test_settings_that_do_not_agree_are_refused(call, base, change, monkeypatch):
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True)
+    with pytest.raises(ValueError):
+        call(**{**base(), **change})
+
+
+@pytest.mark.parametrize("call,base", [(eb.eagle_sample, sampling), (eb.eagle_truncate_logits, truncating)])
+def test_sampling_asks_for_a_gpu(call, base):
+    with pytest.raises(ValueError, match="on the GPU"):
+        call(**base())
+    some = {k: None if k in ("temperature", "top_k", "top_p", "min_p", "logprobs", "n_kept", "status") else v for k, v in base().items()}
+    with pytest.raises(ValueError, match="on the GPU"):
+        call(**some)

@@ -49,3 +49,29 @@ def test_append_axes_kv4_refusals(L, want, kw):
     assert L.eagle_kv_append_axes_kv4(P, P, P, 512, 256, 256, a["rope"], 64, a["pos"], a["axes"], P, P, P, 2, a["T"], 4, 2,
                                       a["D"], ctypes.c_void_p(512), P, a["ks"], P, P, a["k_scale"], a["v_scale"], 8, P, 4, N,
                                       N) == want
+
+
+def sample(L, **kw):
+    a = dict(x=P, stride=100, M=4, V=100, dtype=1, per=1, u=P, tok=P)
+    a.update(kw)
+    return L.eagle_sample(a["x"], a["stride"], a["M"], a["V"], a["dtype"], N, N, N, N, a["per"], a["u"], a["tok"], N, N, N, N)
+
+
+@pytest.mark.parametrize("want,kw", [
+    (OK, dict(M=0)), (OK, dict(M=0, x=N, u=N, tok=N)), (INVALID, dict(x=N)), (INVALID, dict(u=N)), (INVALID, dict(tok=N)),
+    (INVALID, dict(M=-1)), (INVALID, dict(V=0)), (INVALID, dict(per=0)), (INVALID, dict(stride=99)), (INVALID, dict(dtype=2)),
+    (INVALID, dict(x=ctypes.c_void_p(257))), (INVALID, dict(x=ctypes.c_void_p(258), dtype=0)), (UNSUPPORTED, dict(M=65536)),
+    (UNSUPPORTED, dict(V=262145, stride=262145)),
+])
+def test_sample_refusals(L, want, kw):
+    assert sample(L, **kw) == want
+
+
+@pytest.mark.parametrize("want,kw", [
+    (OK, dict(M=0)), (INVALID, dict(x=N)), (INVALID, dict(out=N)), (INVALID, dict(out_stride=99)), (INVALID, dict(out=P, out_stride=120)),
+    (INVALID, dict(out=ctypes.c_void_p(513))), (INVALID, dict(V=0)), (INVALID, dict(per=-1)), (UNSUPPORTED, dict(M=65536)),
+])
+def test_truncate_refusals(L, want, kw):
+    a = dict(x=P, M=4, V=100, per=1, out=ctypes.c_void_p(512), out_stride=100)
+    a.update(kw)
+    assert L.eagle_truncate_logits(a["x"], 100, a["M"], a["V"], 1, N, N, N, N, a["per"], a["out"], a["out_stride"], N, N, N) == want
