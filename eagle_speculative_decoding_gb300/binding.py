@@ -81,6 +81,11 @@ _SIGS = {
                                _P, _P]),
     "eagle_prompt_attn_kv4": (_I, [_P, _L, _P, _P, _P, _P, _F, _F, _I, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I,
                                    _I, _F, _P, _Z, _P, _P]),
+    "eagle_prefix_attn_workspace_size": (_Z, [_I, _I, _I, _I, _I]),
+    "eagle_prefix_attn": (_I, [_P, _L, _P, _P, _I, _P, _I, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P, _Z,
+                               _P, _P]),
+    "eagle_prefix_attn_kv4": (_I, [_P, _L, _P, _P, _P, _P, _F, _F, _I, _P, _I, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I,
+                                   _I, _F, _P, _Z, _P, _P]),
     "eagle_sample": (_I, [_P, _L, _I, _I, _I, _P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P]),
     "eagle_truncate_logits": (_I, [_P, _L, _I, _I, _I, _P, _P, _P, _P, _I, _P, _L, _P, _P, _P]),
     "eagle_draft_prompt_workspace_size": (_Z, [_I, _I, _I, _I, _I, _I, _I, _I]),
@@ -734,6 +739,61 @@ def eagle_prompt_attn_kv4(q, k_codes, k_scales, v_codes, v_scales, block_table, 
         v_scale, P, block_table.data_ptr(), pages, cu_seqlens.data_ptr(), ctx_lens.data_ptr(), out.data_ptr(),
         _addr(lse), B, T, Hq, Hkv, D, page, D ** -0.5 if scale is None else scale, ws.data_ptr(), ws.numel(),
         _addr(status), _raw_stream(stream, q.device)))
+    return out
+
+
+def eagle_prefix_attn_workspace_size(G, T, Hq, Hkv, D):
+    return int(lib().eagle_prefix_attn_workspace_size(G, T, Hq, Hkv, D))
+
+
+def _own_rows(own_out, own_lse, out, T, Hq):
+    """Checks of the rows' own results, both or neither given."""
+    if own_out is None and own_lse is None:
+        return
+    if own_out is None or own_lse is None:
+        raise ValueError("own_out and own_lse go together")
+    if own_out.shape != out.shape or own_out.dtype is not out.dtype or not own_out.is_contiguous():
+        raise ValueError("own_out must be contiguous, with out's shape and dtype")
+    if not (own_lse.shape == (T, Hq) and own_lse.dtype is _F32 and own_lse.is_contiguous()):
+        raise ValueError("own_lse must be contiguous fp32 [T, Hq]")
+
+
+def eagle_prefix_attn(q, k_cache, v_cache, prefix_table, cu_rows, prefix_lens, out, lse=None, own_out=None, own_lse=None,
+                      scale=None, ws=None, status=None, stream=None):
+    """Attention of groups of rows over the prefix that each group shares,
+    joined with the rows' own attention (own_out, own_lse; see include/eagle.h)."""
+    T, Hq, D, qs = _attn_rows(q, out, lse)
+    _, page, Hkv, _ = k_cache.shape
+    P = _pages16(k_cache, v_cache, Hkv, D, q.dtype)
+    _own_rows(own_out, own_lse, out, T, Hq)
+    G, pages = _lengths(q, cu_rows, prefix_lens, prefix_table, status)
+    if ws is None:
+        ws = workspace(eagle_prefix_attn_workspace_size(G, T, Hq, Hkv, D), q.device, stream)
+    _check("eagle_prefix_attn", lib().eagle_prefix_attn(
+        q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), P, prefix_table.data_ptr(), pages, cu_rows.data_ptr(),
+        prefix_lens.data_ptr(), _addr(own_out), _addr(own_lse), out.data_ptr(), _addr(lse), G, T, Hq, Hkv, D, page,
+        D ** -0.5 if scale is None else scale, _dtype(q), ws.data_ptr(), ws.numel(), _addr(status),
+        _raw_stream(stream, q.device)))
+    return out
+
+
+def eagle_prefix_attn_kv4(q, k_codes, k_scales, v_codes, v_scales, prefix_table, cu_rows, prefix_lens, out, lse=None,
+                          own_out=None, own_lse=None, scale=None, k_scale=1.0, v_scale=1.0, ws=None, status=None, stream=None):
+    """eagle_prefix_attn over 4-bit pages (see include/eagle.h)."""
+    if q.dtype != torch.bfloat16:
+        raise ValueError("q and out must be bf16")
+    T, Hq, D, qs = _attn_rows(q, out, lse)
+    _, Hkv, page, _ = k_codes.shape
+    P = _pages4(k_codes, k_scales, v_codes, v_scales, Hkv, D)
+    _own_rows(own_out, own_lse, out, T, Hq)
+    G, pages = _lengths(q, cu_rows, prefix_lens, prefix_table, status)
+    if ws is None:
+        ws = workspace(eagle_prefix_attn_workspace_size(G, T, Hq, Hkv, D), q.device, stream)
+    _check("eagle_prefix_attn_kv4", lib().eagle_prefix_attn_kv4(
+        q.data_ptr(), qs, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), k_scale,
+        v_scale, P, prefix_table.data_ptr(), pages, cu_rows.data_ptr(), prefix_lens.data_ptr(), _addr(own_out),
+        _addr(own_lse), out.data_ptr(), _addr(lse), G, T, Hq, Hkv, D, page, D ** -0.5 if scale is None else scale,
+        ws.data_ptr(), ws.numel(), _addr(status), _raw_stream(stream, q.device)))
     return out
 
 

@@ -53,6 +53,7 @@ constexpr float kBelow = F16 ? 7.f : 0.f;
 template <bool F16>
 constexpr float kSumLimit = F16 ? 32768.f : 256.f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kMaxGroups = 1024;  // that share prefixes
 
 struct AttnParams {
   const void* q;
@@ -409,6 +410,143 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanPar
   }
 }
 
+// ---------------------------------------------------------- shared prefixes
+// FLAT kernels: attention of groups of rows over a prefix that the group shares
+// (B groups, cu their rows, ctx their prefix's keys, table its pages), every key
+// visible to every row.  A unit's key blocks are all known from a group's two
+// numbers, so nothing is planned: the blocks of all units (by group, kv head and
+// unit) are one line that the CTAs share out evenly, each finding its own part.
+// A unit that lies in one CTA's part is finished there; of the others each CTA
+// leaves a partial result (slot 2 c + 1 for the piece that a unit starts with, at
+// most one per CTA, 2 c for one that it goes on with), joined by flat_join_kernel.
+struct Groups {  // a warp's view: lane i holds group base + i
+  int c0, n, len;  // first row, rows, keys (0 if the group is in error)
+  int units, blocks;
+  long long work;  // blocks of all its units
+  bool falls;
+};
+__device__ __forceinline__ Groups load_groups(const AttnParams& a, int base, int tpu, bool report) {
+  Groups g = {0, 0, 0, 0, 0, 0, false};
+  const int i = base + (int)(threadIdx.x & 31);
+  if (i >= a.B) return g;
+  g.c0 = a.cu[i];
+  const int c1 = a.cu[i + 1], len = a.ctx[i];
+  g.falls = c1 < g.c0;
+  if (g.c0 < 0 || g.falls || c1 > a.T || len < 0) {
+    if (report) set_status(a.status, EAGLE_ERR_INVALID_ARG);
+  } else if (len > 16ll * min(a.max_pages, kMaxPages)) {
+    if (report) set_status(a.status, EAGLE_ERR_BAD_KV);
+  } else {
+    g.n = c1 - g.c0;
+    g.len = len;
+    g.units = (g.n + tpu - 1) / tpu;
+    g.blocks = (len + kBlk - 1) / kBlk;
+    g.work = (long long)g.units * g.blocks * a.Hkv;
+  }
+  // rows in front of the first group or behind the last belong to none
+  if (report && ((i == 0 && g.c0 != 0) || (i == a.B - 1 && c1 != a.T))) set_status(a.status, EAGLE_ERR_INVALID_ARG);
+  return g;
+}
+__device__ __forceinline__ long long warp_sum(long long v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+// Blocks of all units; 0 where cu falls (rows might have two prefixes).
+__device__ __forceinline__ long long flat_total(const AttnParams& a, int tpu, bool report) {
+  long long all = 0;
+  bool falls = false;
+  for (int base = 0; base < a.B; base += 32) {
+    const Groups g = load_groups(a, base, tpu, report);
+    all += warp_sum(g.work);
+    falls = falls || __any_sync(0xffffffffu, g.falls);
+  }
+  return falls ? 0 : all;
+}
+// CTA c of n takes blocks [all c / n, all (c + 1) / n); at least `least` each, so
+// that few blocks are not a piece for every CTA.
+__device__ __forceinline__ int flat_ctas(long long all, int ctas, int least) {
+  return (int)max(1ll, min((long long)ctas, all / least));
+}
+// The pieces of a CTA's part, one after the other; one warp calls it.
+struct FlatWalk {
+  long long left;  // blocks still to be given out
+  int base, src, h, u, k, ctas;
+  Groups g;
+  __device__ __forceinline__ void start(const AttnParams& a, int tpu, int least) {
+    const long long all = flat_total(a, tpu, blockIdx.x == 0);
+    ctas = flat_ctas(all, (int)gridDim.x, least);
+    const int c = (int)blockIdx.x;
+    left = 0;
+    if (c >= ctas || all == 0) return;
+    long long at = all * c / ctas;
+    left = all * (c + 1) / ctas - at;
+    for (base = 0; base < a.B; base += 32) {
+      g = load_groups(a, base, tpu, false);
+      long long end = g.work;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, end, d);
+        if ((int)(threadIdx.x & 31) >= d) end += x;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, end > at);
+      if (past) {
+        src = __ffs((int)past) - 1;
+        at -= __shfl_sync(0xffffffffu, end - g.work, src);
+        break;
+      }
+      at -= __shfl_sync(0xffffffffu, end, 31);
+    }
+    const int blocks = __shfl_sync(0xffffffffu, g.blocks, src), units = __shfl_sync(0xffffffffu, g.units, src);
+    const long long unit = at / blocks;
+    k = (int)(at - unit * blocks);
+    h = (int)(unit / units);
+    u = (int)(unit - (long long)h * units);
+  }
+  __device__ __forceinline__ bool next(const AttnParams& a, int tpu, Piece& w) {
+    if (left <= 0) return false;
+    const int blocks = __shfl_sync(0xffffffffu, g.blocks, src), units = __shfl_sync(0xffffffffu, g.units, src);
+    const int k1 = (int)min((long long)blocks, k + left), c = (int)blockIdx.x;
+    w = Piece{base + src, h, u, k, k1, k1 - k == blocks ? -1 : 2 * c + (k == 0 ? 1 : 0), __shfl_sync(0xffffffffu, g.c0, src),
+              __shfl_sync(0xffffffffu, g.n, src), __shfl_sync(0xffffffffu, g.len, src), 0, 0, 1};
+    left -= k1 - k;
+    k = 0;
+    if (k1 == blocks && ++u == units) {
+      u = 0;
+      if (++h == a.Hkv && left > 0) {
+        h = 0;
+        unsigned more = __ballot_sync(0xffffffffu, g.work > 0) & (src == 31 ? 0u : ~0u << (src + 1));
+        while (!more) {  // (work is left, so some later group has it)
+          base += 32;
+          if (base >= a.B) {
+            left = 0;
+            return true;
+          }
+          g = load_groups(a, base, tpu, false);
+          more = __ballot_sync(0xffffffffu, g.work > 0);
+        }
+        src = __ffs((int)more) - 1;
+      }
+    }
+    return true;
+  }
+};
+// A row's own keys as one more term of its sums: their log-sum-exp L becomes the
+// weight 2^(L log2(e) - M) beside the prefix's sum l 2^(m - M), M the larger of the two
+// references.  L log2(e) is kept in two parts (as one it is off by 2^-24 of itself,
+// which is 2^-20 of a weight).
+struct OwnWeight {
+  float prefix, own, lse;  // factors of O and of own_out, and the joined log-sum-exp
+};
+__device__ __forceinline__ OwnWeight own_weight(float m, float l, const float* own_lse, size_t row) {
+  const float L = own_lse ? own_lse[row] : -INFINITY;
+  if (l == 0.f) return {0.f, L == -INFINITY ? 0.f : 1.f, L};  // the own result as it is
+  if (L == -INFINITY) return {1.f / l, 0.f, (m + log2f(l)) * kLn2};
+  const float hi = L * 1.44269502f, lo = fmaf(L, 1.44269502f, -hi) + L * 1.92596303e-8f, M = fmaxf(m, hi);
+  const float p = ex2_approx(m - M), o = ex2_approx((hi - M) + lo), total = fmaf(l, p, o), f = 1.f / total;
+  return {p * f, o * f, (M + log2f(total)) * kLn2};
+}
+
 // ------------------------------------------------------------------- main
 // 512 threads, one CTA per SM:
 //   warps 0-3    K/V producers: 16-byte asynchronous copies from the pages to
@@ -464,6 +602,9 @@ struct MainParams {
   const Piece* pieces;
   float2* part_ml;
   float* part_o;
+  const void* own_out;  // FLAT: what the rows' own keys gave, or null
+  const float* own_lse;
+  int least;
 };
 
 template <int ST, bool KV4>
@@ -638,6 +779,7 @@ struct TileWork {
   __device__ __forceinline__ int rows(int t) const { return t ? rows1 : rows0; }
   __device__ __forceinline__ int blk(int t, int i) const { return twin ? 2 * i + t : i; }
 };
+template <bool FLAT>
 __device__ __forceinline__ TileWork tile_work(const Piece& w, int tpt, int tpu, int g) {
   TileWork r;
   const int t0 = w.u * tpu, left = w.n - t0, nblk = w.k1 - w.k0;
@@ -650,7 +792,7 @@ __device__ __forceinline__ TileWork tile_work(const Piece& w, int tpt, int tpu, 
   } else {
     r.rows1 = min(left - tpt, tpt) * g;
     // tile 0's last token may need fewer blocks than tile 1's
-    r.n0 = max(0, min(nblk, (w.ctx + t0 + tpt - 1) / kBlk + 1 - w.k0));
+    r.n0 = FLAT ? nblk : max(0, min(nblk, (w.ctx + t0 + tpt - 1) / kBlk + 1 - w.k0));
     r.n1 = nblk;
   }
   return r;
@@ -675,7 +817,7 @@ __device__ __noinline__ void add_nonfinite(const AttnParams& a, int req, int h, 
   }
 }
 
-template <int D, bool KV4>
+template <int D, bool KV4, bool FLAT>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const MainParams p) {
   using C = Cfg<D, KV4>;
@@ -780,7 +922,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Piece w;
       for (int ps = 0;; ++ps) {
         if (!get_piece(ps, w)) break;
-        const int n_keys = w.ctx + w.n, masked_from = w.ctx + w.u * p.tpu;  // the first row's position
+        const int n_keys = w.ctx + (FLAT ? 0 : w.n), masked_from = w.ctx + w.u * p.tpu;  // the first row's position
         const char* kb_ = static_cast<const char*>(a.kc) + (size_t)w.h * D * 2 + c * 16;
         const char* vb_ = static_cast<const char*>(a.vc) + (size_t)w.h * D * 2 + c * 16;
         const int32_t* tab = a.table + (size_t)w.b * a.max_pages;
@@ -803,7 +945,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           const int key0 = blk * kBlk;
-          const bool masked = key0 + kBlk - 1 > masked_from;
+          const bool masked = !FLAT && key0 + kBlk - 1 > masked_from;
           // the block's pages, all before the first copy: a copy that waits
           // for a shuffle of its own cost 89 cycles each
           int pq[8];
@@ -885,7 +1027,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           itab = a.table + (size_t)w.b * a.max_pages;
           ihead = (size_t)w.h * (16 * D);
           ik1 = w.k1;
-          ikeys = w.ctx + w.n;
+          ikeys = w.ctx + (FLAT ? 0 : w.n);
           iblk = w.k0;
           iop = 0;
           igrp = 0;
@@ -934,10 +1076,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       Piece w;
       for (int ps = 0; ok; ++ps) {
         if (!get_piece(ps, w)) break;
-        const int n_keys = w.ctx + w.n, masked_from = w.ctx + w.u * p.tpu;
+        const int n_keys = w.ctx + (FLAT ? 0 : w.n), masked_from = w.ctx + w.u * p.tpu;
         for (int blk = w.k0; ok && blk < w.k1; ++blk) {
           const int key0 = blk * kBlk;
-          const bool masked = key0 + kBlk - 1 > masked_from;
+          const bool masked = !FLAT && key0 + kBlk - 1 > masked_from;
 #pragma unroll 1
           for (int o = 0; o < 2; ++o) {
             while (issued - consumed < R && issue(issued == consumed)) {
@@ -1032,7 +1174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int ps = 0; ok; ++ps) {
         Piece w;
         if (!get_piece(ps, w)) break;
-        const TileWork tw = tile_work(w, p.tpt, p.tpu, p.g);
+        const TileWork tw = tile_work<FLAT>(w, p.tpt, p.tpu, p.g);
         const int n = __shfl_sync(0xffffffffu, tw.n(t), 0), nblk = __shfl_sync(0xffffffffu, w.k1 - w.k0, 0);
         const int twin = __shfl_sync(0xffffffffu, (int)tw.twin, 0);
         if (n == 0) {
@@ -1103,7 +1245,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else if (warp == 6) {
       // ----------------------------------------------------------- scheduler
-      if (lane == 0) {
+      if constexpr (FLAT) {
+        FlatWalk walk;
+        walk.start(a, p.tpu, p.least);
+        for (int ps = 0;; ++ps) {
+          const int slot = ps % kSlots;
+          Piece w;
+          const bool more = walk.next(a, p.tpu, w);
+          if (!warp_wait(sb.slot_empty[slot], ((uint32_t)(ps / kSlots) & 1u) ^ 1u)) break;
+          if (lane == 0) {
+            if (more)
+              sb.piece[slot] = w;
+            else
+              sb.piece[slot].b = -1;
+            sb.bad_v[slot] = 0;
+            mbar_arrive(smem_u32(&sb.slot_full[slot]));
+          }
+          __syncwarp();
+          if (!more) break;
+        }
+      } else if (lane == 0) {
         const int total = p.hdr->pieces;
         for (int ps = 0;; ++ps) {
           const int slot = ps % kSlots;
@@ -1131,7 +1292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Piece w;
       for (int ps = 0; ok; ++ps) {
         if (!get_piece(ps, w)) break;
-        const TileWork tw = tile_work(w, p.tpt, p.tpu, p.g);
+        const TileWork tw = tile_work<FLAT>(w, p.tpt, p.tpu, p.g);
 #pragma unroll 1
         for (int t = 0; t < 2; ++t) {
           if (tw.n(t) == 0) continue;
@@ -1223,11 +1384,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     Piece w;
     for (int ps = 0; ok; ++ps) {
       if (!get_piece(ps, w)) break;
-      const TileWork tw = tile_work(w, p.tpt, p.tpu, p.g);
+      const TileWork tw = tile_work<FLAT>(w, p.tpt, p.tpu, p.g);
       const int n = tw.n(t), rows = tw.rows(t);
       const bool quad_live = q4 * 32 < rows, row_ok = row < rows;
       const int tok = w.u * p.tpu + (tw.twin ? 0 : t * p.tpt) + row / p.g;
-      const int pos = row_ok ? w.ctx + tok : 0x7fffffff;
+      const int pos = row_ok ? (FLAT ? w.ctx - 1 : w.ctx + tok) : 0x7fffffff;
       // Two warps of a scheduler, one per tile, take turns at a block's
       // softmax: left alone the tiles fall into step, both in their softmax
       // and then both waiting for their MMAs.  (Not with alternate blocks,
@@ -1369,7 +1530,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int urow = (tw.twin ? 0 : t * p.tpt * p.g) + row;
         const bool whole = w.slot < 0;
         const size_t prow = (size_t)max(w.slot, 0) * p.slot_rows + urow;
-        const float inv = whole ? (l == 0.f ? 0.f : a.v_scale / l) : 1.f;
+        float inv = whole ? (l == 0.f ? 0.f : a.v_scale / l) : 1.f, own = 0.f;
+        if constexpr (FLAT) {
+          if (whole && row_ok) {
+            const OwnWeight x = own_weight(m, l, p.own_lse, orow);
+            inv = x.prefix * a.v_scale;
+            own = x.own;
+            m = x.lse;
+          }
+        }
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
@@ -1389,15 +1558,35 @@ __global__ void __launch_bounds__(kThreads, 1)
               o[k] = __float_as_uint(__uint_as_float(o[k]) * w0 + __uint_as_float(o2[k]) * w1);
           }
           if (!row_ok) continue;
-          const float* f = reinterpret_cast<const float*>(o);
+          float* f = reinterpret_cast<float*>(o);
           if (whole) {
+            if constexpr (FLAT) {
+              // (a row without keys of its own may hold anything)
+              if (p.own_out && !(own == 0.f)) {
+                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.own_out) + orow * D + c * 32);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                  const uint4 v = src[u];
+                  const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    f[8 * u + 2 * k] = fmaf(__uint_as_float(e[k] << 16), own, f[8 * u + 2 * k] * inv);
+                    f[8 * u + 2 * k + 1] = fmaf(__uint_as_float(e[k] & 0xffff0000u), own, f[8 * u + 2 * k + 1] * inv);
+                  }
+                }
+              } else {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) f[k] *= inv;
+              }
+            }
             uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + c * 32);
+            const float by = FLAT ? 1.f : inv;
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-              dst[u] = make_uint4(pack16<false>(f[8 * u] * inv, f[8 * u + 1] * inv),
-                                  pack16<false>(f[8 * u + 2] * inv, f[8 * u + 3] * inv),
-                                  pack16<false>(f[8 * u + 4] * inv, f[8 * u + 5] * inv),
-                                  pack16<false>(f[8 * u + 6] * inv, f[8 * u + 7] * inv));
+              dst[u] = make_uint4(pack16<false>(f[8 * u] * by, f[8 * u + 1] * by),
+                                  pack16<false>(f[8 * u + 2] * by, f[8 * u + 3] * by),
+                                  pack16<false>(f[8 * u + 4] * by, f[8 * u + 5] * by),
+                                  pack16<false>(f[8 * u + 6] * by, f[8 * u + 7] * by));
           } else {
             float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + c * 32);
 #pragma unroll
@@ -1406,11 +1595,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (row_ok) {
           if (whole) {
-            if (a.lse) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            if (a.lse) a.lse[orow] = FLAT ? m : l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
           } else {
             p.part_ml[prow] = make_float2(m, l);
           }
-          if (*(volatile int*)&sb.bad_v[ps % kSlots]) {
+          if (!FLAT && *(volatile int*)&sb.bad_v[ps % kSlots]) {
             // the keys it sees from the first masked block on, in this piece
             const int first = max((w.ctx + w.u * p.tpu) / kBlk, w.k0) * kBlk, last = min(pos, w.k1 * kBlk - 1);
             if (whole)
@@ -2090,8 +2279,10 @@ struct F32Params {
   const Piece* pieces;
   float2* part_ml;
   float* part_o;
+  const float *own_out, *own_lse;  // FLAT
+  int least;
 };
-template <int D, int RT>
+template <int D, int RT, bool FLAT>
 __global__ void __launch_bounds__(256, (CfgF32<D, RT>::kCtas)) prompt_attn_f32_kernel(const F32Params p) {
   using C = CfgF32<D, RT>;
   constexpr int CPR = D / 4, NC = D / 64;  // 16-byte chunks per row, 64-column groups
@@ -2103,13 +2294,24 @@ __global__ void __launch_bounds__(256, (CfgF32<D, RT>::kCtas)) prompt_attn_f32_k
   pdl_trigger();
   const AttnParams& a = p.a;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  __shared__ Piece s_w;  // FLAT
+  FlatWalk walk;
+  if (FLAT && tid < 32) walk.start(a, p.tpu, p.least);
   for (bool first = true;; first = false) {
     __syncthreads();
-    if (tid == 0) s_piece = first ? (int)blockIdx.x : atomicAdd(p.next, 1);
+    if (FLAT) {
+      if (tid < 32) {
+        Piece w;
+        const bool more = walk.next(a, p.tpu, w);
+        if (tid == 0) s_piece = more, s_w = w;
+      }
+    } else if (tid == 0) {
+      s_piece = first ? (int)blockIdx.x : atomicAdd(p.next, 1);
+    }
     __syncthreads();
-    if (s_piece >= p.hdr->pieces) break;
-    const Piece w = p.pieces[s_piece];
-    const int rows = min(w.n - w.u * p.tpu, p.tpu) * p.g, n_keys = w.ctx + w.n;
+    if (FLAT ? !s_piece : s_piece >= p.hdr->pieces) break;
+    const Piece w = FLAT ? s_w : p.pieces[s_piece];
+    const int rows = min(w.n - w.u * p.tpu, p.tpu) * p.g, n_keys = w.ctx + (FLAT ? 0 : w.n);
     const int32_t* tab = a.table + (size_t)w.b * a.max_pages;
     const int b0 = w.k0 * (kBlk / KB), b1 = min(w.k1 * (kBlk / KB), (n_keys + KB - 1) / KB);  // in steps
     auto copy = [&](float* dst, const void* src, int blk) {
@@ -2143,7 +2345,7 @@ __global__ void __launch_bounds__(256, (CfgF32<D, RT>::kCtas)) prompt_attn_f32_k
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
       const int r = ty + 16 * i;
-      pos[i] = r < rows ? w.ctx + w.u * p.tpu + r / p.g : 0x7fffffff;
+      pos[i] = r < rows ? (FLAT ? w.ctx - 1 : w.ctx + w.u * p.tpu + r / p.g) : 0x7fffffff;
       m[i] = -INFINITY;
       l[i] = 0.f;
 #pragma unroll
@@ -2152,7 +2354,7 @@ __global__ void __launch_bounds__(256, (CfgF32<D, RT>::kCtas)) prompt_attn_f32_k
     // a block for the first 16 R rows
     auto step = [&](int blk, auto r_) {
       constexpr int R = decltype(r_)::value;
-      const bool masked = blk * KB + KB - 1 > w.ctx + w.u * p.tpu;
+      const bool masked = blk * KB + KB - 1 > w.ctx + (FLAT ? -1 : w.u * p.tpu);
       cp_async_wait<1>();
       __syncthreads();
       float z[R][NJ];
@@ -2249,8 +2451,27 @@ __global__ void __launch_bounds__(256, (CfgF32<D, RT>::kCtas)) prompt_attn_f32_k
       const bool whole = w.slot < 0;
       const size_t orow = ((size_t)w.c0 + w.u * p.tpu + r / p.g) * a.Hq + w.h * p.g + r % p.g;
       const size_t prow = (size_t)max(w.slot, 0) * p.slot_rows + r;
-      const float f = whole ? (l[i] == 0.f ? 0.f : 1.f / l[i]) : 1.f;
+      float f = whole ? (l[i] == 0.f ? 0.f : 1.f / l[i]) : 1.f;
       float* dst = whole ? static_cast<float*>(a.out) + orow * D : p.part_o + prow * D;
+      if (FLAT && whole) {
+        const OwnWeight x = own_weight(m[i], l[i], p.own_lse, orow);
+        const float own = x.own;
+        f = 1.f;
+        m[i] = x.lse;
+#pragma unroll
+        for (int c = 0; c < 4 * NC; ++c) o[i][c] *= x.prefix;
+        if (p.own_out && !(own == 0.f)) {
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const float4 v = *reinterpret_cast<const float4*>(p.own_out + orow * D + c * 64 + tx * 4);
+            o[i][4 * c] = fmaf(v.x, own, o[i][4 * c]);
+            o[i][4 * c + 1] = fmaf(v.y, own, o[i][4 * c + 1]);
+            o[i][4 * c + 2] = fmaf(v.z, own, o[i][4 * c + 2]);
+            o[i][4 * c + 3] = fmaf(v.w, own, o[i][4 * c + 3]);
+          }
+        }
+        __syncwarp(0xffffu << (tid & 16));  // own_lse, which lse may be, is read by the row's threads
+      }
 #pragma unroll
       for (int c = 0; c < NC; ++c)
         *reinterpret_cast<float4*>(dst + c * 64 + tx * 4) =
@@ -2259,9 +2480,118 @@ __global__ void __launch_bounds__(256, (CfgF32<D, RT>::kCtas)) prompt_attn_f32_k
         if (!whole)
           p.part_ml[prow] = make_float2(m[i], l[i]);
         else if (a.lse)
-          a.lse[orow] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
+          a.lse[orow] = FLAT ? m[i] : l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
       }
     }
+  }
+}
+
+// ----------------------------------------------- shared prefixes: the join
+// Rows whose unit several CTAs shared: the partial results and the rows' own.  A
+// warp takes a row, a lane D / 32 channels.  Rows of a prefix without keys take
+// their own result over.
+struct JoinParams {
+  AttnParams a;
+  int g, tpu, slot_rows, ctas, least;
+  const float2* ml;
+  const float* o;
+  const void* own_out;
+  const float* own_lse;
+};
+template <int D, typename T>
+__global__ void __launch_bounds__(256) flat_join_kernel(const JoinParams p) {
+  constexpr int E = D / 32;
+  pdl_wait();
+  pdl_trigger();
+  const AttnParams& a = p.a;
+  const int lane = threadIdx.x & 31;
+  const long long all = flat_total(a, p.tpu, false);
+  const int ctas = flat_ctas(all, p.ctas, p.least);
+  const long long rows = (long long)a.T * a.Hq, step = (long long)gridDim.x * 8;
+  // the groups' first block in the line, 32 groups at a time from group `base` on
+  int base = -32;
+  long long end = 0;
+  Groups g = {};
+  bool falls = false;
+  if (all == 0)  // nothing to join but rows of empty prefixes, unless cu falls
+    for (int b = 0; b < a.B; b += 32) falls = falls || __any_sync(0xffffffffu, load_groups(a, b, p.tpu, false).falls);
+  if (falls) return;
+  long long before = 0;  // blocks in front of group base
+  for (long long r = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += step) {
+    const int t = (int)(r / a.Hq), head = (int)(r - (long long)t * a.Hq), h = head / p.g;
+    // the row's group (rows are taken in ascending order)
+    int src = -1;
+    while (true) {
+      const unsigned in = __ballot_sync(0xffffffffu, base >= 0 && t >= g.c0 && t < g.c0 + g.n);
+      if (in) {
+        src = __ffs((int)in) - 1;
+        break;
+      }
+      if (base + 32 >= a.B) break;
+      // later groups only if the row lies behind these
+      if (base >= 0) {
+        if (a.cu[base + 32] > t) break;
+        before += __shfl_sync(0xffffffffu, end, 31);
+      }
+      base += 32;
+      g = load_groups(a, base, p.tpu, false);
+      end = g.work;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, end, d);
+        if (lane >= d) end += x;
+      }
+    }
+    if (src < 0) continue;  // in no group, or in one that is in error
+    const int blocks = __shfl_sync(0xffffffffu, g.blocks, src), units = __shfl_sync(0xffffffffu, g.units, src);
+    const int tok = t - __shfl_sync(0xffffffffu, g.c0, src), u = tok / p.tpu;
+    const long long first = before + __shfl_sync(0xffffffffu, end - g.work, src) + ((long long)h * units + u) * blocks;
+    float l = 0.f, M = -INFINITY, o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+    if (blocks) {
+      // the CTA whose part block x is in: the largest c with all c / ctas (rounded down) <= x
+      const int c0 = (int)(((first + 1) * ctas + all - 1) / all) - 1, c1 = (int)(((first + blocks) * ctas + all - 1) / all) - 1;
+      if (c0 == c1) continue;  // written by that CTA
+      const size_t row = (size_t)(tok - u * p.tpu) * p.g + head % p.g;
+      auto slot = [&](int c) { return (size_t)(2 * c + (c == c0 ? 1 : 0)) * p.slot_rows + row; };
+      for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, __ldcg(p.ml + slot(c)).x);
+#pragma unroll
+      for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+#pragma unroll 4
+      for (int c = c0; c <= c1; ++c) {
+        const float2 x = __ldcg(p.ml + slot(c));
+        const float w = M == -INFINITY ? 1.f : ex2_approx(x.x - M);
+        l = fmaf(w, x.y, l);
+        const float* src_o = p.o + slot(c) * D + lane * E;
+        float f[E];
+        if constexpr (E == 4)
+          *reinterpret_cast<float4*>(f) = __ldcg(reinterpret_cast<const float4*>(src_o));
+        else
+          *reinterpret_cast<float2*>(f) = __ldcg(reinterpret_cast<const float2*>(src_o));
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(w, f[e], o[e]);
+      }
+    }
+    const OwnWeight w = own_weight(M, l, p.own_lse, (size_t)r);
+    float y[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) y[e] = o[e] * (w.prefix * a.v_scale);
+    if (p.own_out && !(w.own == 0.f)) {
+      const T* src_own = static_cast<const T*>(p.own_out) + (size_t)r * D + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; ++e) y[e] = w.prefix == 0.f ? (float)src_own[e] : fmaf((float)src_own[e], w.own, y[e]);
+    }
+    T* dst = static_cast<T*>(a.out) + (size_t)r * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      if constexpr (sizeof(T) == 4)
+        *reinterpret_cast<float2*>(dst + e) = make_float2(y[e], y[e + 1]);
+      else
+        *reinterpret_cast<uint32_t*>(dst + e) = pack16<false>(y[e], y[e + 1]);
+    }
+    __syncwarp();  // lse may be own_lse
+    if (a.lse && lane == 0) a.lse[r] = w.lse;
   }
 }
 
@@ -2349,11 +2679,11 @@ int attn_launch_tc(const AttnParams& a, void* ws, cudaStream_t s) {
   if (!KV4 && !make_tmap_3d_bf16(&map_q, a.q, D, (uint64_t)a.Hq, (uint64_t)a.T, (uint64_t)D * 2, (uint64_t)a.q_stride * 2,
                                  64, (uint32_t)sh.g, (uint32_t)sh.tpt))
     return EAGLE_ERR_CUDA;
-  if (!allow_smem(prompt_attn_tc_kernel<D, KV4>, (int)C::kSmem)) return EAGLE_ERR_CUDA;
+  if (!allow_smem(prompt_attn_tc_kernel<D, KV4, false>, (int)C::kSmem)) return EAGLE_ERR_CUDA;
   launch_plan(a, sh, w, 2, 2, s);
   const MainParams mp = {a, scale_log2(a), sh.g, sh.tpt, sh.tpu, sh.rows, w.hdr, &w.hdr->next, w.pieces,
-                         w.ml, w.po};
-  launch(prompt_attn_tc_kernel<D, KV4>, sh.ctas, kThreads, C::kSmem, s, map_q, mp);
+                         w.ml, w.po, nullptr, nullptr, 0};
+  launch(prompt_attn_tc_kernel<D, KV4, false>, sh.ctas, kThreads, C::kSmem, s, map_q, mp);
   return launch_merge<D, __nv_bfloat16>(a, sh, w, s);
 }
 template <int D, int RT>
@@ -2361,15 +2691,83 @@ int attn_launch_f32(const AttnParams& a, void* ws, cudaStream_t s) {
   const Shape sh = attn_shape(a.B, a.T, a.Hq, a.Hkv, D, RT == 1 ? kFp32Few : kFp32);
   const Ws w = attn_ws(sh, ws);
   constexpr int smem = CfgF32<D, RT>::kSmem;
-  if (!allow_smem(prompt_attn_f32_kernel<D, RT>, smem)) return EAGLE_ERR_CUDA;
+  if (!allow_smem(prompt_attn_f32_kernel<D, RT, false>, smem)) return EAGLE_ERR_CUDA;
   launch_plan(a, sh, w, 1, 1, s);
-  const F32Params fp = {a, scale_log2(a), sh.g, sh.tpu, sh.rows, w.hdr, &w.hdr->next, w.pieces, w.ml, w.po};
-  launch(prompt_attn_f32_kernel<D, RT>, sh.ctas, 256, smem, s, fp);
+  const F32Params fp = {a, scale_log2(a), sh.g, sh.tpu, sh.rows, w.hdr, &w.hdr->next, w.pieces, w.ml, w.po, nullptr, nullptr, 0};
+  launch(prompt_attn_f32_kernel<D, RT, false>, sh.ctas, 256, smem, s, fp);
   return launch_merge<D, float>(a, sh, w, s);
 }
 template <int D>
 int attn_launch_f32(const AttnParams& a, void* ws, cudaStream_t s) {
   return few_rows_f32(a.B, a.T, a.Hq, a.Hkv) ? attn_launch_f32<D, 1>(a, ws, s) : attn_launch_f32<D, 4>(a, ws, s);
+}
+
+// Shared prefixes.  Units are those of the tensor-core or the fp32 path.
+constexpr int kFlatLeast = 2;  // blocks of a CTA's part at least
+struct FlatShape {
+  int g, tpt, tpu, rows, ctas;
+  size_t off_o, total;
+};
+FlatShape flat_shape(int T, int Hq, int Hkv, int D, Path path) {
+  FlatShape s;
+  const Shape x = attn_shape(1, T, Hq, Hkv, D, path);
+  s.g = x.g, s.tpt = x.tpt, s.tpu = x.tpu, s.rows = x.rows, s.ctas = x.ctas;
+  s.off_o = round_up(sizeof(float2) * 2 * (size_t)s.ctas * s.rows, 256);
+  s.total = s.off_o + sizeof(float) * 2 * (size_t)s.ctas * s.rows * D + 256;
+  return s;
+}
+struct Own {
+  const void* out;
+  const float* lse;
+};
+template <int D, typename T>
+int flat_join(const AttnParams& a, const Own& own, const FlatShape& sh, const float2* ml, const float* o, cudaStream_t s) {
+  const JoinParams jp = {a, sh.g, sh.tpu, sh.rows, sh.ctas, kFlatLeast, ml, o, own.out, own.lse};
+  const long long rows = (long long)a.T * a.Hq;
+  launch(flat_join_kernel<D, T>, (int)std::min<long long>((rows + 7) / 8, 8ll * std::max(1, sm_count())), 256, 0, s, jp);
+  note_launch(2);
+  return last_launch_status();
+}
+template <int D, bool KV4>
+int flat_launch_tc(const AttnParams& a, const Own& own, void* ws, cudaStream_t s) {
+  using C = Cfg<D, KV4>;
+  const FlatShape sh = flat_shape(a.T, a.Hq, a.Hkv, D, kTensor);
+  char* w = reinterpret_cast<char*>(round_up(reinterpret_cast<size_t>(ws), 256));
+  float2* ml = reinterpret_cast<float2*>(w);
+  float* o = reinterpret_cast<float*>(w + sh.off_o);
+  CUtensorMap map_q = {};
+  if (!KV4 && !make_tmap_3d_bf16(&map_q, a.q, D, (uint64_t)a.Hq, (uint64_t)a.T, (uint64_t)D * 2, (uint64_t)a.q_stride * 2,
+                                 64, (uint32_t)sh.g, (uint32_t)sh.tpt))
+    return EAGLE_ERR_CUDA;
+  if (!allow_smem(prompt_attn_tc_kernel<D, KV4, true>, (int)C::kSmem)) return EAGLE_ERR_CUDA;
+  const MainParams mp = {a, scale_log2(a), sh.g, sh.tpt, sh.tpu, sh.rows, nullptr, nullptr, nullptr, ml, o, own.out, own.lse, kFlatLeast};
+  launch(prompt_attn_tc_kernel<D, KV4, true>, sh.ctas, kThreads, C::kSmem, s, map_q, mp);
+  return flat_join<D, __nv_bfloat16>(a, own, sh, ml, o, s);
+}
+template <int D, int RT>
+int flat_launch_f32(const AttnParams& a, const Own& own, void* ws, cudaStream_t s) {
+  const FlatShape sh = flat_shape(a.T, a.Hq, a.Hkv, D, RT == 1 ? kFp32Few : kFp32);
+  char* w = reinterpret_cast<char*>(round_up(reinterpret_cast<size_t>(ws), 256));
+  float2* ml = reinterpret_cast<float2*>(w);
+  float* o = reinterpret_cast<float*>(w + sh.off_o);
+  constexpr int smem = CfgF32<D, RT>::kSmem;
+  if (!allow_smem(prompt_attn_f32_kernel<D, RT, true>, smem)) return EAGLE_ERR_CUDA;
+  const F32Params fp = {a, scale_log2(a), sh.g, sh.tpu, sh.rows, nullptr, nullptr, nullptr, ml, o,
+                        static_cast<const float*>(own.out), own.lse, kFlatLeast};
+  launch(prompt_attn_f32_kernel<D, RT, true>, sh.ctas, 256, smem, s, fp);
+  return flat_join<D, float>(a, own, sh, ml, o, s);
+}
+template <int D>
+int flat_launch_f32(const AttnParams& a, const Own& own, void* ws, cudaStream_t s) {
+  return few_rows_f32(a.B, a.T, a.Hq, a.Hkv) ? flat_launch_f32<D, 1>(a, own, ws, s) : flat_launch_f32<D, 4>(a, own, ws, s);
+}
+// What a shared prefix needs beside attn_check().
+int flat_check(const AttnParams& a, const Own& own, int D, void* ws, size_t ws_bytes) {
+  if (a.B > kMaxGroups) return EAGLE_ERR_UNSUPPORTED;
+  if ((own.out != nullptr) != (own.lse != nullptr) && a.T > 0) return EAGLE_ERR_INVALID_ARG;
+  if (!aligned16(own.out)) return EAGLE_ERR_INVALID_ARG;
+  if (a.T > 0 && (!ws || ws_bytes < eagle_prefix_attn_workspace_size(a.B, a.T, a.Hq, a.Hkv, D))) return EAGLE_ERR_WORKSPACE;
+  return EAGLE_OK;
 }
 
 int attn_ws_check(const AttnParams& a, int D, void* ws, size_t ws_bytes) {
@@ -2430,4 +2828,47 @@ extern "C" int eagle_prompt_attn_kv4(const void* q, long long q_stride, const ui
   if (wrc != EAGLE_OK) return wrc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return D == 128 ? attn_launch_tc<128, true>(p, ws, s) : attn_launch_tc<64, true>(p, ws, s);
+}
+
+extern "C" size_t eagle_prefix_attn_workspace_size(int G, int T, int Hq, int Hkv, int D) {
+  if (G <= 0 || G > kMaxGroups || T < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || Hq / Hkv > 64 || (D != 64 && D != 128)) return 0;
+  const int few = (int)std::min<long long>(T, (long long)kF32Few * G / (Hq / Hkv));
+  size_t most = 0;
+  for (const Path path : {kTensor, kFp32}) most = std::max(most, flat_shape(T, Hq, Hkv, D, path).total);
+  return std::max(most, flat_shape(few, Hq, Hkv, D, kFp32Few).total) + 256;
+}
+
+extern "C" int eagle_prefix_attn(const void* q, long long q_stride, const void* k_cache, const void* v_cache, int num_pages,
+                                 const int32_t* prefix_table, int max_pages, const int32_t* cu_rows,
+                                 const int32_t* prefix_lens, const void* own_out, const float* own_lse, void* out,
+                                 float* lse, int G, int T, int Hq, int Hkv, int D, int page_size, float scale, int dtype,
+                                 void* ws, size_t ws_bytes, int32_t* dev_status, void* stream) {
+  if (dtype != EAGLE_BF16 && dtype != EAGLE_FP32) return EAGLE_ERR_INVALID_ARG;
+  const AttnParams p = {q, q_stride, k_cache, v_cache, nullptr, nullptr, 1.f, 1.f, num_pages, max_pages, G, T, Hq, Hkv,
+                        prefix_table, cu_rows, prefix_lens, out, lse, scale, dev_status};
+  const Own own = {own_out, own_lse};
+  int rc = attn_check(p, D, page_size, dtype == EAGLE_BF16 ? 2 : 4);
+  if (rc == EAGLE_OK) rc = flat_check(p, own, D, ws, ws_bytes);
+  if (rc != EAGLE_OK || T == 0) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (dtype == EAGLE_BF16)
+    return D == 128 ? flat_launch_tc<128, false>(p, own, ws, s) : flat_launch_tc<64, false>(p, own, ws, s);
+  return D == 128 ? flat_launch_f32<128>(p, own, ws, s) : flat_launch_f32<64>(p, own, ws, s);
+}
+
+extern "C" int eagle_prefix_attn_kv4(const void* q, long long q_stride, const uint8_t* k_codes, const uint8_t* k_scales,
+                                     const uint8_t* v_codes, const uint8_t* v_scales, float k_scale, float v_scale,
+                                     int num_pages, const int32_t* prefix_table, int max_pages, const int32_t* cu_rows,
+                                     const int32_t* prefix_lens, const void* own_out, const float* own_lse, void* out,
+                                     float* lse, int G, int T, int Hq, int Hkv, int D, int page_size, float scale,
+                                     void* ws, size_t ws_bytes, int32_t* dev_status, void* stream) {
+  const AttnParams p = {q, q_stride, k_codes, v_codes, k_scales, v_scales, k_scale, v_scale, num_pages, max_pages, G, T,
+                        Hq, Hkv, prefix_table, cu_rows, prefix_lens, out, lse, scale, dev_status};
+  if (!k_scales || !v_scales || !aligned16(k_scales) || !aligned16(v_scales)) return EAGLE_ERR_INVALID_ARG;
+  const Own own = {own_out, own_lse};
+  int rc = attn_check(p, D, page_size, 2);
+  if (rc == EAGLE_OK) rc = flat_check(p, own, D, ws, ws_bytes);
+  if (rc != EAGLE_OK || T == 0) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return D == 128 ? flat_launch_tc<128, true>(p, own, ws, s) : flat_launch_tc<64, true>(p, own, ws, s);
 }

@@ -855,6 +855,63 @@ int eagle_prompt_attn_kv4(const void* q, long long q_stride, const uint8_t* k_co
                           int page_size, float scale, void* ws, size_t ws_bytes,
                           int32_t* dev_status, void* stream);
 
+/* eagle_prefix_attn -- attention of groups of rows over a prefix that each group
+ * shares (a system prompt, a document), read once for all of them, joined with
+ * the rows' attention over their own keys.  [E3] "Stage 2: Verification" and
+ * [M7.5] section 0x03C attend to a committed prefix per request; here the part of
+ * it that requests have in common is kept once, in pages of its own, and each
+ * request's own pages and ctx_lens start behind it (their rows' rotation:
+ * eagle_kv_append_axes).  For row t of group g and query head h (kv head
+ * h / (Hq/Hkv)):
+ *   keys = the tokens 0 .. prefix_lens[g] - 1 of the pages in prefix_table[g], all
+ *          of them visible to every row of the group;
+ *   l = sum exp(scale q k^T), O = sum exp(scale q k^T) v over them;
+ *   out[t, h] = (O + exp(own_lse[t, h]) own_out[t, h]) / (l + exp(own_lse[t, h])),
+ *   lse[t, h] = log(l + exp(own_lse[t, h])),
+ * which is the attention over both when own_out and own_lse are the attention of
+ * the same rows, with the same scale, over the keys behind the prefix, as
+ * eagle_prompt_attn, eagle_prompt_attn_kv4 and eagle_tree_attn give it (tree rows
+ * [B, R, Hq, D] are T = B R rows).
+ *   cu_rows : [G + 1] int32, cu_rows[0] = 0, non-decreasing, cu_rows[G] = T: the
+ *             rows cu_rows[g] .. cu_rows[g+1] - 1 are group g's
+ *   prefix_lens : [G] int32 (0 allowed, and no multiple of a page needed)
+ *   prefix_table : [G, max_pages] int32 page ids;  page_size is 16
+ *   q : rows of Hq heads (positions applied), q_stride elements apart
+ *   own_out : [T, Hq, D] dtype `dtype`, own_lse : [T, Hq] fp32; both or, for the
+ *             prefix alone, neither.  A row of own_lse = -infinity has no keys of
+ *             its own (its own_out is not read)
+ *   out, lse (or NULL) : as eagle_prompt_attn; may be own_out and own_lse themselves
+ * A group of an empty prefix takes own_out and own_lse over (zeros and -infinity
+ * without them).  Rows whose keys, own ones included, all score -infinity give
+ * zeros and -infinity.  T = 0 does nothing.
+ * Device-detected: a cu_rows that falls somewhere -> EAGLE_ERR_INVALID_ARG (no
+ * row is written); a group with an entry outside 0 .. T or a negative length ->
+ * EAGLE_ERR_INVALID_ARG, a length beyond the table or 2^30 -> EAGLE_ERR_BAD_KV
+ * (its rows are not written); cu_rows[0] != 0 or cu_rows[G] != T ->
+ * EAGLE_ERR_INVALID_ARG (the rows of no group are not written, the others are);
+ * a page id out of range -> EAGLE_ERR_BAD_KV (its keys and values read as zeros).
+ * Arithmetic and limits as eagle_prompt_attn (own_out is read in `dtype`: where
+ * it was rounded to bf16 by another call, that rounding stays in it); G <= 1024.
+ * A workspace of G and T serves every call of at most that many groups and rows,
+ * any dtype and 4-bit pages: 41 MB at most with 152 SMs and D 128. */
+size_t eagle_prefix_attn_workspace_size(int G, int T, int Hq, int Hkv, int D);
+int eagle_prefix_attn(const void* q, long long q_stride, const void* k_cache, const void* v_cache,
+                      int num_pages, const int32_t* prefix_table, int max_pages,
+                      const int32_t* cu_rows, const int32_t* prefix_lens, const void* own_out,
+                      const float* own_lse, void* out, float* lse, int G, int T, int Hq, int Hkv,
+                      int D, int page_size, float scale, int dtype, void* ws, size_t ws_bytes,
+                      int32_t* dev_status, void* stream);
+
+/* eagle_prefix_attn_kv4 -- the same over 4-bit pages (arithmetic and scales as
+ * eagle_prompt_attn_kv4; q, own_out and out bf16).  Same workspace query. */
+int eagle_prefix_attn_kv4(const void* q, long long q_stride, const uint8_t* k_codes,
+                          const uint8_t* k_scales, const uint8_t* v_codes, const uint8_t* v_scales,
+                          float k_scale, float v_scale, int num_pages, const int32_t* prefix_table,
+                          int max_pages, const int32_t* cu_rows, const int32_t* prefix_lens,
+                          const void* own_out, const float* own_lse, void* out, float* lse, int G,
+                          int T, int Hq, int Hkv, int D, int page_size, float scale, void* ws,
+                          size_t ws_bytes, int32_t* dev_status, void* stream);
+
 /* eagle_draft_prompt -- the drafter's decoder layer (eagle_draft_layer) over
  * packed prompt rows: it fills the drafter's paged cache and gives the rows'
  * outputs, so that the first eagle_draft_layer call of a round finds its

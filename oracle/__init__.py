@@ -58,6 +58,7 @@ from .prompt_oracle import (  # noqa: F401,E402
     e4m3_value,
     kv4_pack,
     kv4_unpack,
+    prefix_attn,
     prompt_attn,
     rotate,
     row_places,

@@ -98,3 +98,35 @@ def prompt_attn(q, keys, values, cu, ctx, scale):
             lse[rows, h] = (m + np.log(l))[:, 0]
             dot[rows, h] = np.where(late, 0, np.abs(qq) @ np.abs(k).T * scale).max(-1)
     return out, lse, mag, dot
+
+
+def prefix_attn(q, keys, values, cu, scale, own_out=None, own_lse=None):
+    """Attention of groups of rows over the keys [n_keys, Hkv, D] of their group,
+    all visible, joined with the rows' own result.  Returns out, lse and, for
+    error bounds, sum_j w_j |v_j| of the prefix alone and with the own part, and the
+    largest scale * sum_c |q_c k_c|."""
+    T, Hq, D = q.shape
+    out, mag, both = np.zeros((T, Hq, D)), np.zeros((T, Hq, D)), np.zeros((T, Hq, D))
+    lse, dot = np.full((T, Hq), -np.inf), np.zeros((T, Hq))
+    for g, (k_all, v_all) in enumerate(zip(keys, values)):
+        rows = slice(int(cu[g]), int(cu[g + 1]))
+        for h in range(Hq):
+            hk = h // (Hq // k_all.shape[1])
+            qq, k, v = (np.asarray(a, np.float64) for a in (q[rows, h], k_all[:, hk], v_all[:, hk]))
+            z = qq @ k.T * scale
+            own = own_lse is not None
+            # the own keys are one more key, of score own_lse and value own_out
+            L = np.asarray(own_lse[rows, h], np.float64)[:, None] if own else np.full((len(qq), 1), -np.inf)
+            o = np.where(np.isneginf(L), 0.0, np.asarray(own_out[rows, h], np.float64)) if own else np.zeros((len(qq), D))
+            m = np.maximum(z.max(-1, keepdims=True, initial=-np.inf), L)
+            ref = np.where(np.isneginf(m), 0.0, m)
+            w, wo = np.exp(z - ref), np.exp(L - ref)
+            l = w.sum(-1, keepdims=True) + wo
+            div = np.where(l == 0, 1.0, l)
+            out[rows, h] = w / div @ v + wo / div * o
+            mag[rows, h] = w / div @ np.abs(v)
+            both[rows, h] = mag[rows, h] + wo / div * np.abs(o)
+            with np.errstate(divide="ignore"):
+                lse[rows, h] = (ref + np.log(l))[:, 0]
+            dot[rows, h] = (np.abs(qq) @ np.abs(k).T * scale).max(-1, initial=0.0)
+    return out, lse, mag, both, dot

@@ -5,14 +5,22 @@ import pytest
 import torch
 
 from eagle_speculative_decoding_gb300 import binding as eb
-from test_prompt_binding import BF16, B, CACHE, CODES, D, F32, HKV, HQ, I32, INDEX, ROPE, ROWS, T, lengths, pages4, pages16, rows, z
+from test_prompt_binding import (B, CACHE, CODES, D, F32, HQ, I32, INDEX, OUT, ROPE, ROWS, T, W, attn_rows, lengths, pages4,
+                                 pages16, rows, z)
 
 
 def axes():
     return dict(positions=z(3, T, dtype=I32), pair_axis=z(D // 2, dtype=I32))
 
 
+def groups():
+    return dict(cu_rows=torch.tensor([0, 2, 5], dtype=I32), prefix_lens=z(B, dtype=I32), prefix_table=z(B, W, dtype=I32),
+                status=z(1, dtype=I32), own_out=z(T, HQ, D), own_lse=z(T, HQ, dtype=F32))
+
+
 CALLS = dict(
+    prefix=(eb.eagle_prefix_attn, lambda: {**attn_rows(), **groups(), **pages16()}),
+    prefix4=(eb.eagle_prefix_attn_kv4, lambda: {**attn_rows(), **groups(), **pages4()}),
     axes=(eb.eagle_kv_append_axes, lambda: {**rows(), **lengths(), **pages16(), **axes()}),
     axes4=(eb.eagle_kv_append_axes_kv4, lambda: {**rows(), **lengths(), **pages4(), **axes()}),
 )
@@ -21,13 +29,20 @@ AXES = [dict(positions=z(3, T + 1, dtype=I32)), dict(positions=z(3, T, dtype=tor
         dict(pair_axis=z(D, dtype=I32)[::2])]
 
 
+OWN = [dict(own_out=None), dict(own_lse=None), dict(own_out=z(T, HQ, D, dtype=F32)), dict(own_out=z(T - 1, HQ, D)),
+       dict(own_out=z(T, HQ, 2 * D)[..., :D]), dict(own_lse=z(T, HQ)), dict(own_lse=z(T, HQ + 1, dtype=F32)),
+       dict(own_lse=z(HQ, T, dtype=F32).t())]
+
+
 def on_gpu(monkeypatch):
     """Lets CPU tensors pass for the GPU's in the checks."""
     monkeypatch.setattr(eb, "_lengths", lambda rows, cu, ctx, table, status: table.shape)
 
 
 def cases():
-    both = {"axes": INDEX + CACHE + ROPE + ROWS, "axes4": INDEX + CODES + ROPE + ROWS}
+    names = dict(cu_seqlens="cu_rows", ctx_lens="prefix_lens", block_table="prefix_table")
+    group = [{names.get(k, k): v for k, v in c.items()} for c in INDEX]
+    both = {"prefix": group + CACHE + OUT + OWN, "prefix4": group + CODES + OUT + OWN, "axes": INDEX + CACHE + ROPE + ROWS, "axes4": INDEX + CODES + ROPE + ROWS}
     return [(name, i, change) for name, changes in both.items() for i, change in enumerate(changes)]
 
 

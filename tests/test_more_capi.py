@@ -75,3 +75,46 @@ def test_truncate_refusals(L, want, kw):
     a = dict(x=P, M=4, V=100, per=1, out=ctypes.c_void_p(512), out_stride=100)
     a.update(kw)
     assert L.eagle_truncate_logits(a["x"], 100, a["M"], a["V"], 1, N, N, N, N, a["per"], a["out"], a["out_stride"], N, N, N) == want
+
+
+def prefix(L, **kw):
+    a = dict(q=P, qs=512, kc=P, vc=P, pages=8, table=P, width=4, cu=P, lens=P, own=P, own_lse=P, out=P, G=2, T=4, Hq=4, Hkv=2,
+             D=128, page=16, scale=0.1, dtype=1, ws=N, wsb=0)
+    a.update(kw)
+    return L.eagle_prefix_attn(a["q"], a["qs"], a["kc"], a["vc"], a["pages"], a["table"], a["width"], a["cu"], a["lens"],
+                               a["own"], a["own_lse"], a["out"], N, a["G"], a["T"], a["Hq"], a["Hkv"], a["D"], a["page"],
+                               a["scale"], a["dtype"], a["ws"], a["wsb"], N, N)
+
+
+@pytest.mark.parametrize("want,kw", [
+    (OK, dict(T=0)), (OK, dict(T=0, q=N, out=N, own=N, own_lse=N)), (WORKSPACE, dict()), (WORKSPACE, dict(ws=P, wsb=16)),
+    (WORKSPACE, dict(own=N, own_lse=N)), (INVALID, dict(own=N)), (INVALID, dict(own_lse=N)), (INVALID, dict(own=ODD)),
+    (INVALID, dict(q=N)), (INVALID, dict(kc=N)), (INVALID, dict(vc=N)), (INVALID, dict(table=N)), (INVALID, dict(cu=N)),
+    (INVALID, dict(lens=N)), (INVALID, dict(out=N)), (INVALID, dict(G=0)), (INVALID, dict(T=-1)), (INVALID, dict(Hq=5)),
+    (INVALID, dict(scale=0.0)), (INVALID, dict(scale=float("nan"))), (INVALID, dict(dtype=7)), (INVALID, dict(qs=500)),
+    (INVALID, dict(qs=516)), (INVALID, dict(q=ODD)), (INVALID, dict(out=ODD)), (UNSUPPORTED, dict(D=96)),
+    (UNSUPPORTED, dict(page=32)), (UNSUPPORTED, dict(Hq=130, qs=130 * 128)), (UNSUPPORTED, dict(G=1025)),
+    (UNSUPPORTED, dict(pages=(1 << 26) + 1)),
+])
+def test_prefix_refusals(L, want, kw):
+    assert prefix(L, **kw) == want
+
+
+@pytest.mark.parametrize("want,ks,k_scale,own", [
+    (INVALID, N, 1.0, P), (INVALID, P, -1.0, P), (INVALID, P, float("nan"), P), (INVALID, P, 1.0, N), (WORKSPACE, P, 1.0, P)])
+def test_prefix_kv4_refusals(L, want, ks, k_scale, own):
+    assert L.eagle_prefix_attn_kv4(P, 512, P, ks, P, P, k_scale, 1.0, 8, P, 4, P, P, own, P, P, N, 2, 4, 4, 2, 128, 16, 0.1, N,
+                                   0, N, N) == want
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(32, 8, 128), (16, 1, 64), (7, 7, 64), (64, 1, 128), (12, 4, 128)])
+def test_prefix_workspace_serves_fewer_groups_and_rows(L, Hq, Hkv, D):
+    size = L.eagle_prefix_attn_workspace_size
+    Gs, Ts = (1, 2, 3, 64, 1024), (0, 1, 2, 5, 16, 33, 64, 200, 4096, 1 << 28)
+    table = [[size(G, T, Hq, Hkv, D) for T in Ts] for G in Gs]
+    for x in range(len(Gs)):
+        for y in range(len(Ts)):
+            assert 0 < table[x][y] and (x == 0 or table[x - 1][y] <= table[x][y]) and (y == 0 or table[x][y - 1] <= table[x][y])
+    assert table[-1][-1] <= 2 * 160 * 256 * (4 * D + 8) + 4096
+    for bad in ((0, 4, 4, 2, 64), (1025, 4, 4, 2, 64), (1, 4, 5, 2, 64), (1, 4, 4, 2, 80), (1, -1, 4, 2, 64)):
+        assert size(*bad) == 0
