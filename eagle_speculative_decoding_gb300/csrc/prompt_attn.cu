@@ -32,6 +32,9 @@
 
 #include "common.cuh"
 #include "kv4.cuh"
+#ifndef FLAT_ONE
+#define FLAT_ONE 256
+#endif
 
 namespace eagle {
 namespace {
@@ -418,7 +421,11 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanPar
 // unit) are one line that the CTAs share out evenly, each finding its own part.
 // A unit that lies in one CTA's part is finished there; of the others each CTA
 // leaves a partial result (slot 2 c + 1 for the piece that a unit starts with, at
-// most one per CTA, 2 c for one that it goes on with), joined by flat_join_kernel.
+// most one per CTA, 2 c for one that it goes on with), and the CTA that it starts in
+// describes it to flat_join_kernel, which joins them.
+struct __align__(16) Split {  // a unit that starts in a CTA's part and ends in CTA `last`'s
+  int rows, last, h, tok0;   // rows: 0 if there is none
+};
 struct Groups {  // a warp's view: lane i holds group base + i
   int c0, n, len;  // first row, rows, keys (0 if the group is in error)
   int units, blocks;
@@ -452,37 +459,49 @@ __device__ __forceinline__ long long warp_sum(long long v) {
   for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
   return v;
 }
-// Blocks of all units; 0 where cu falls (rows might have two prefixes).
-__device__ __forceinline__ long long flat_total(const AttnParams& a, int tpu, bool report) {
-  long long all = 0;
-  bool falls = false;
-  for (int base = 0; base < a.B; base += 32) {
-    const Groups g = load_groups(a, base, tpu, report);
-    all += warp_sum(g.work);
-    falls = falls || __any_sync(0xffffffffu, g.falls);
+// a / b for a >= 0, b > 0 (64-bit quotients are long sequences; most lines are short)
+__device__ __forceinline__ long long quotient(long long a, int b) {
+  return a < (1ll << 32) ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+// The line of all blocks and its parts: CTA c of n has blocks [start(c), start(c + 1)),
+// all c / n rounded down; `least` blocks each or more, so that few blocks are not a
+// piece for every CTA.
+struct FlatLine {
+  long long all, q;  // blocks (0 where cu falls: rows might have two prefixes); all / ctas
+  int ctas, r;
+  bool falls;
+  Groups g;  // groups 0 .. 31
+  __device__ __forceinline__ FlatLine(const AttnParams& a, int tpu, int n, int least, bool report) {
+    g = load_groups(a, 0, tpu, report);
+    all = warp_sum(g.work);
+    falls = __any_sync(0xffffffffu, g.falls);
+    for (int base = 32; base < a.B; base += 32) {
+      const Groups x = load_groups(a, base, tpu, report);
+      all += warp_sum(x.work);
+      falls = falls || __any_sync(0xffffffffu, x.falls);
+    }
+    if (falls) all = 0;
+    ctas = (int)max(1ll, min((long long)n, quotient(all, least)));
+    q = quotient(all, ctas);
+    r = (int)(all - q * ctas);
   }
-  return falls ? 0 : all;
-}
-// CTA c of n takes blocks [all c / n, all (c + 1) / n); at least `least` each, so
-// that few blocks are not a piece for every CTA.
-__device__ __forceinline__ int flat_ctas(long long all, int ctas, int least) {
-  return (int)max(1ll, min((long long)ctas, all / least));
-}
-// The pieces of a CTA's part, one after the other; one warp calls it.
+  __device__ __forceinline__ long long start(int c) const { return q * c + (uint32_t)(r * c) / (uint32_t)ctas; }
+  // the CTA whose part block x is in: the largest c with all c / ctas <= x
+  __device__ __forceinline__ int owner(long long x) const {
+    const long long y = (x + 1) * ctas - 1;
+    return (int)(all < (1ll << 31) ? quotient(y, (int)all) : y / all);
+  }
+};
+// A place in the line, and the way on from it; one warp has it.
 struct FlatWalk {
   long long left;  // blocks still to be given out
-  int base, src, h, u, k, ctas;
+  int base, src, h, u, k;
   Groups g;
-  __device__ __forceinline__ void start(const AttnParams& a, int tpu, int least) {
-    const long long all = flat_total(a, tpu, blockIdx.x == 0);
-    ctas = flat_ctas(all, (int)gridDim.x, least);
-    const int c = (int)blockIdx.x;
-    left = 0;
-    if (c >= ctas || all == 0) return;
-    long long at = all * c / ctas;
-    left = all * (c + 1) / ctas - at;
+  // the unit (h, u) of group base + src, and the block k of it, at `at` < all
+  __device__ __forceinline__ void seek(const AttnParams& a, const FlatLine& line, int tpu, long long at) {
+    g = line.g;
     for (base = 0; base < a.B; base += 32) {
-      g = load_groups(a, base, tpu, false);
+      if (base) g = load_groups(a, base, tpu, false);
       long long end = g.work;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -498,11 +517,30 @@ struct FlatWalk {
       at -= __shfl_sync(0xffffffffu, end, 31);
     }
     const int blocks = __shfl_sync(0xffffffffu, g.blocks, src), units = __shfl_sync(0xffffffffu, g.units, src);
-    const long long unit = at / blocks;
+    const long long unit = quotient(at, blocks);
     k = (int)(at - unit * blocks);
-    h = (int)(unit / units);
+    h = (int)quotient(unit, units);
     u = (int)(unit - (long long)h * units);
   }
+  __device__ __forceinline__ void start(const AttnParams& a, const FlatLine& line, int tpu) {
+    const int c = (int)blockIdx.x;
+    left = 0;
+    if (c >= line.ctas || line.all == 0) return;
+    const long long at = line.start(c);
+    left = line.start(c + 1) - at;
+    seek(a, line, tpu, at);
+  }
+  // what the join needs of piece w, the part's last: the unit may go on in the next CTA's
+  __device__ __forceinline__ Split split(const FlatLine& line, const Piece& w, int tpu, int g_) const {
+    Split s = {0, 0, 0, 0};
+    if (w.slot < 0 || w.k0 > 0) return s;
+    s.rows = min(tpu, w.n - w.u * tpu) * g_;
+    s.last = line.owner(line.start((int)blockIdx.x + 1) + (w.ctx + kBlk - 1) / kBlk - w.k1 - 1);
+    s.h = w.h;
+    s.tok0 = w.c0 + w.u * tpu;
+    return s;
+  }
+  // the next piece of a CTA's part
   __device__ __forceinline__ bool next(const AttnParams& a, int tpu, Piece& w) {
     if (left <= 0) return false;
     const int blocks = __shfl_sync(0xffffffffu, g.blocks, src), units = __shfl_sync(0xffffffffu, g.units, src);
@@ -605,6 +643,7 @@ struct MainParams {
   const void* own_out;  // FLAT: what the rows' own keys gave, or null
   const float* own_lse;
   int least;
+  Split* splits;  // one per CTA
 };
 
 template <int ST, bool KV4>
@@ -782,7 +821,7 @@ struct TileWork {
 template <bool FLAT>
 __device__ __forceinline__ TileWork tile_work(const Piece& w, int tpt, int tpu, int g) {
   TileWork r;
-  const int t0 = w.u * tpu, left = w.n - t0, nblk = w.k1 - w.k0;
+  const int t0 = w.u * tpu, left = FLAT ? min(w.n - t0, tpu) : w.n - t0, nblk = w.k1 - w.k0;
   r.twin = left <= tpt;
   r.rows0 = min(left, tpt) * g;
   if (r.twin) {
@@ -840,7 +879,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&sb.kv_empty[i]), 2);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(smem_u32(&sb.q_full[t]), 1);
+      mbar_init(smem_u32(&sb.q_full[t]), KV4 && FLAT ? 4 : 1);
       mbar_init(smem_u32(&sb.q_empty[t]), 1);
       mbar_init(smem_u32(&sb.s_full[t]), 1);
       mbar_init(smem_u32(&sb.p_full[t]), 4);
@@ -1246,11 +1285,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 6) {
       // ----------------------------------------------------------- scheduler
       if constexpr (FLAT) {
+        const FlatLine line(a, p.tpu, (int)gridDim.x, p.least, blockIdx.x == 0);
         FlatWalk walk;
-        walk.start(a, p.tpu, p.least);
+        walk.start(a, line, p.tpu);
+        Piece w;
+        w.slot = -1;
         for (int ps = 0;; ++ps) {
           const int slot = ps % kSlots;
-          Piece w;
           const bool more = walk.next(a, p.tpu, w);
           if (!warp_wait(sb.slot_empty[slot], ((uint32_t)(ps / kSlots) & 1u) ^ 1u)) break;
           if (lane == 0) {
@@ -1264,6 +1305,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (!more) break;
         }
+        const Split x = walk.split(line, w, p.tpu, p.g);
+        if (lane == 0) p.splits[blockIdx.x] = x;
       } else if (lane == 0) {
         const int total = p.hdr->pieces;
         for (int ps = 0;; ++ps) {
@@ -1295,7 +1338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const TileWork tw = tile_work<FLAT>(w, p.tpt, p.tpu, p.g);
 #pragma unroll 1
         for (int t = 0; t < 2; ++t) {
-          if (tw.n(t) == 0) continue;
+          if (tw.n(t) == 0 || (KV4 && FLAT)) continue;
           ok = warp_wait(sb.q_empty[t], ((uint32_t)uses[t] & 1u) ^ 1u);
           if (!ok) break;
           const int tok0 = w.c0 + w.u * p.tpu + (tw.twin ? 0 : t * p.tpt);
@@ -1402,6 +1445,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int pos0 = __shfl_sync(0xffffffffu, pos, 0);  // the warp's first row sees least
       float m = -INFINITY, l = 0.f, sl2 = p.scale_log2;
       bool fresh = true;  // some row has seen no key yet
+      if constexpr (KV4 && FLAT) {
+        // Pieces are short here, and one warp that brings 256 rows of Q to fp16
+        // would hold up the first block of each: a row's thread does it (as the
+        // Q loader's warp does otherwise).
+        if (n > 0) {
+          ok = warp_wait(sb.q_empty[t], ((uint32_t)uses & 1u) ^ 1u);
+          if (!ok) break;
+          if (row_ok) {
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                              ((size_t)w.c0 + tok) * a.q_stride + (size_t)(w.h * p.g + row % p.g) * D);
+            uint4 v[D / 8];
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) v[c] = src[c];
+            uint32_t mx = 0;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+              const uint32_t e[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) mx = max(mx, max(e[k] & 0x7fffu, (e[k] >> 16) & 0x7fffu));
+            }
+            const int k2 = row_exponent(mx);
+            const float down = __uint_as_float((uint32_t)(127 - k2) << 23);
+            sl2 = row_factor(sl2, __uint_as_float((uint32_t)(127 + k2) << 23));
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+              const uint32_t e[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+              uint32_t x[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                x[k] = pack16<true>(__uint_as_float(e[k] << 16) * down, __uint_as_float(e[k] & 0xffff0000u) * down);
+              *reinterpret_cast<uint4*>(gbase + sQ + t * C::kTile + (uint32_t)(c / 8) * C::kHalf + (uint32_t)row * 128u +
+                                        (uint32_t)(((c % 8) ^ (row & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sb.q_full[t]));
+        }
+      }
       int key0 = (w.k0 + tw.blk(t, 0)) * kBlk;
       const int key_step = tw.twin ? 2 * kBlk : kBlk;
 #pragma unroll 1
@@ -1411,7 +1493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         sph ^= 1u;
         tc_fence_after();
         if (quad_live) {
-          if (KV4 && i == 0) sl2 = row_factor(sl2, row_ok ? sb.q_fac[uses & 1][t][row] : 1.f);
+          if (KV4 && !FLAT && i == 0) sl2 = row_factor(sl2, row_ok ? sb.q_fac[uses & 1][t][row] : 1.f);
           if (i < turns && my_turn_comes) {
             ok = warp_wait(sb.turn[t][q4], tph);
             if (!ok) break;
@@ -2281,6 +2363,7 @@ struct F32Params {
   float* part_o;
   const float *own_out, *own_lse;  // FLAT
   int least;
+  Split* splits;
 };
 template <int D, int RT, bool FLAT>
 __global__ void __launch_bounds__(256, (CfgF32<D, RT>::kCtas)) prompt_attn_f32_kernel(const F32Params p) {
@@ -2296,7 +2379,19 @@ __global__ void __launch_bounds__(256, (CfgF32<D, RT>::kCtas)) prompt_attn_f32_k
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   __shared__ Piece s_w;  // FLAT
   FlatWalk walk;
-  if (FLAT && tid < 32) walk.start(a, p.tpu, p.least);
+  if (FLAT && tid < 32) {
+    // (walked twice: what the join needs is in the part's last piece, and the line
+    // would hold registers all the while)
+    const FlatLine line(a, p.tpu, (int)gridDim.x, p.least, blockIdx.x == 0);
+    Piece w;
+    w.slot = -1;
+    walk.start(a, line, p.tpu);
+    while (walk.next(a, p.tpu, w)) {
+    }
+    const Split x = walk.split(line, w, p.tpu, p.g);
+    if (tid == 0) p.splits[blockIdx.x] = x;
+    walk.start(a, line, p.tpu);
+  }
   for (bool first = true;; first = false) {
     __syncthreads();
     if (FLAT) {
@@ -2487,111 +2582,113 @@ __global__ void __launch_bounds__(256, (CfgF32<D, RT>::kCtas)) prompt_attn_f32_k
 }
 
 // ----------------------------------------------- shared prefixes: the join
-// Rows whose unit several CTAs shared: the partial results and the rows' own.  A
-// warp takes a row, a lane D / 32 channels.  Rows of a prefix without keys take
-// their own result over.
+// The units that several CTAs shared, as those CTAs described them: eight rows of a
+// unit to a CTA, a warp each, a lane D / 32 channels.  The last CTA lets rows of
+// empty prefixes take their own result over.
 struct JoinParams {
   AttnParams a;
-  int g, tpu, slot_rows, ctas, least;
+  int g, tpu, slot_rows, ctas;
+  const Split* splits;
   const float2* ml;
   const float* o;
   const void* own_out;
   const float* own_lse;
 };
 template <int D, typename T>
+__device__ __forceinline__ void join_row(const JoinParams& p, size_t r, float M, float l, const float* o) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const OwnWeight w = own_weight(M, l, p.own_lse, r);
+  float y[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) y[e] = o[e] * (w.prefix * p.a.v_scale);
+  if (p.own_out && !(w.own == 0.f)) {
+    const T* own = static_cast<const T*>(p.own_out) + r * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) y[e] = w.prefix == 0.f ? (float)own[e] : fmaf((float)own[e], w.own, y[e]);
+  }
+  T* dst = static_cast<T*>(p.a.out) + r * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; e += 2) {
+    if constexpr (sizeof(T) == 4)
+      *reinterpret_cast<float2*>(dst + e) = make_float2(y[e], y[e + 1]);
+    else
+      *reinterpret_cast<uint32_t*>(dst + e) = pack16<false>(y[e], y[e + 1]);
+  }
+  __syncwarp();  // lse may be own_lse
+  if (p.a.lse && lane == 0) p.a.lse[r] = w.lse;
+}
+constexpr int kMaxSplits = 512;  // CTAs of a main kernel at most
+template <int D, typename T>
 __global__ void __launch_bounds__(256) flat_join_kernel(const JoinParams p) {
   constexpr int E = D / 32;
+  __shared__ int s_rows[kMaxSplits];
+  const AttnParams& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  float none[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) none[e] = 0.f;
   pdl_wait();
   pdl_trigger();
-  const AttnParams& a = p.a;
-  const int lane = threadIdx.x & 31;
-  const long long all = flat_total(a, p.tpu, false);
-  const int ctas = flat_ctas(all, p.ctas, p.least);
-  const long long rows = (long long)a.T * a.Hq, step = (long long)gridDim.x * 8;
-  // the groups' first block in the line, 32 groups at a time from group `base` on
-  int base = -32;
-  long long end = 0;
-  Groups g = {};
-  bool falls = false;
-  if (all == 0)  // nothing to join but rows of empty prefixes, unless cu falls
-    for (int b = 0; b < a.B; b += 32) falls = falls || __any_sync(0xffffffffu, load_groups(a, b, p.tpu, false).falls);
-  if (falls) return;
-  long long before = 0;  // blocks in front of group base
-  for (long long r = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += step) {
-    const int t = (int)(r / a.Hq), head = (int)(r - (long long)t * a.Hq), h = head / p.g;
-    // the row's group (rows are taken in ascending order)
-    int src = -1;
-    while (true) {
-      const unsigned in = __ballot_sync(0xffffffffu, base >= 0 && t >= g.c0 && t < g.c0 + g.n);
-      if (in) {
-        src = __ffs((int)in) - 1;
-        break;
-      }
-      if (base + 32 >= a.B) break;
-      // later groups only if the row lies behind these
-      if (base >= 0) {
-        if (a.cu[base + 32] > t) break;
-        before += __shfl_sync(0xffffffffu, end, 31);
-      }
-      base += 32;
-      g = load_groups(a, base, p.tpu, false);
-      end = g.work;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, end, d);
-        if (lane >= d) end += x;
+  if (blockIdx.x == gridDim.x - 1) {
+    bool falls = false;
+    for (int base = 0; base < a.B; base += 32) falls = falls || __any_sync(0xffffffffu, load_groups(a, base, p.tpu, false).falls);
+    if (falls) return;
+    for (int base = 0; base < a.B; base += 32) {
+      const Groups g = load_groups(a, base, p.tpu, false);
+      for (unsigned m = __ballot_sync(0xffffffffu, g.n > 0 && g.len == 0); m; m &= m - 1) {
+        const int src = __ffs((int)m) - 1;
+        const long long rows = (long long)__shfl_sync(0xffffffffu, g.n, src) * a.Hq;
+        const size_t r0 = (size_t)__shfl_sync(0xffffffffu, g.c0, src) * a.Hq;
+        for (long long r = warp; r < rows; r += 8) join_row<D, T>(p, r0 + (size_t)r, -INFINITY, 0.f, none);
       }
     }
-    if (src < 0) continue;  // in no group, or in one that is in error
-    const int blocks = __shfl_sync(0xffffffffu, g.blocks, src), units = __shfl_sync(0xffffffffu, g.units, src);
-    const int tok = t - __shfl_sync(0xffffffffu, g.c0, src), u = tok / p.tpu;
-    const long long first = before + __shfl_sync(0xffffffffu, end - g.work, src) + ((long long)h * units + u) * blocks;
-    float l = 0.f, M = -INFINITY, o[E];
+    return;
+  }
+  for (int c = tid; c < p.ctas; c += 256) s_rows[c] = p.splits[c].rows;
+  __syncthreads();
+  // every warp walks the units' chunks of eight rows: this CTA's are numbers
+  // blockIdx.x, + gridDim.x - 1, ..
+  int want = (int)blockIdx.x, before = 0;
+  for (int base = 0; base < p.ctas; base += 32) {
+    const int chunks = base + lane < p.ctas ? (s_rows[base + lane] + 7) / 8 : 0;
+    int end = chunks;
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.f;
-    if (blocks) {
-      // the CTA whose part block x is in: the largest c with all c / ctas (rounded down) <= x
-      const int c0 = (int)(((first + 1) * ctas + all - 1) / all) - 1, c1 = (int)(((first + blocks) * ctas + all - 1) / all) - 1;
-      if (c0 == c1) continue;  // written by that CTA
-      const size_t row = (size_t)(tok - u * p.tpu) * p.g + head % p.g;
-      auto slot = [&](int c) { return (size_t)(2 * c + (c == c0 ? 1 : 0)) * p.slot_rows + row; };
-      for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, __ldcg(p.ml + slot(c)).x);
+    for (int d = 1; d < 32; d <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, end, d);
+      if (lane >= d) end += x;
+    }
+    const int all = __shfl_sync(0xffffffffu, end, 31);
+    while (want < before + all) {
+      const int src = __ffs((int)__ballot_sync(0xffffffffu, before + end > want)) - 1, c0 = base + src;
+      const int row = (want - before - __shfl_sync(0xffffffffu, end - chunks, src)) * 8 + warp;
+      want += (int)gridDim.x - 1;
+      const Split u = p.splits[c0];
+      if (row >= u.rows) continue;
+      auto slot = [&](int x) { return (size_t)(2 * x + (x == c0 ? 1 : 0)) * p.slot_rows + row; };
+      float l = 0.f, M = -INFINITY, o[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = 0.f;
+      for (int x = c0 + lane; x <= u.last; x += 32) M = fmaxf(M, __ldcg(p.ml + slot(x)).x);
 #pragma unroll
       for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-#pragma unroll 4
-      for (int c = c0; c <= c1; ++c) {
-        const float2 x = __ldcg(p.ml + slot(c));
-        const float w = M == -INFINITY ? 1.f : ex2_approx(x.x - M);
-        l = fmaf(w, x.y, l);
-        const float* src_o = p.o + slot(c) * D + lane * E;
+#pragma unroll 8
+      for (int x = c0; x <= u.last; ++x) {
+        const float2 v = __ldcg(p.ml + slot(x));
+        const float w = M == -INFINITY ? 1.f : ex2_approx(v.x - M);
+        l = fmaf(w, v.y, l);
+        const float* part = p.o + slot(x) * D + lane * E;
         float f[E];
         if constexpr (E == 4)
-          *reinterpret_cast<float4*>(f) = __ldcg(reinterpret_cast<const float4*>(src_o));
+          *reinterpret_cast<float4*>(f) = __ldcg(reinterpret_cast<const float4*>(part));
         else
-          *reinterpret_cast<float2*>(f) = __ldcg(reinterpret_cast<const float2*>(src_o));
+          *reinterpret_cast<float2*>(f) = __ldcg(reinterpret_cast<const float2*>(part));
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = fmaf(w, f[e], o[e]);
       }
+      join_row<D, T>(p, ((size_t)u.tok0 + row / p.g) * a.Hq + u.h * p.g + row % p.g, M, l, o);
     }
-    const OwnWeight w = own_weight(M, l, p.own_lse, (size_t)r);
-    float y[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) y[e] = o[e] * (w.prefix * a.v_scale);
-    if (p.own_out && !(w.own == 0.f)) {
-      const T* src_own = static_cast<const T*>(p.own_out) + (size_t)r * D + lane * E;
-#pragma unroll
-      for (int e = 0; e < E; ++e) y[e] = w.prefix == 0.f ? (float)src_own[e] : fmaf((float)src_own[e], w.own, y[e]);
-    }
-    T* dst = static_cast<T*>(a.out) + (size_t)r * D + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      if constexpr (sizeof(T) == 4)
-        *reinterpret_cast<float2*>(dst + e) = make_float2(y[e], y[e + 1]);
-      else
-        *reinterpret_cast<uint32_t*>(dst + e) = pack16<false>(y[e], y[e + 1]);
-    }
-    __syncwarp();  // lse may be own_lse
-    if (a.lse && lane == 0) a.lse[r] = w.lse;
+    before += all;
   }
 }
 
@@ -2682,7 +2779,7 @@ int attn_launch_tc(const AttnParams& a, void* ws, cudaStream_t s) {
   if (!allow_smem(prompt_attn_tc_kernel<D, KV4, false>, (int)C::kSmem)) return EAGLE_ERR_CUDA;
   launch_plan(a, sh, w, 2, 2, s);
   const MainParams mp = {a, scale_log2(a), sh.g, sh.tpt, sh.tpu, sh.rows, w.hdr, &w.hdr->next, w.pieces,
-                         w.ml, w.po, nullptr, nullptr, 0};
+                         w.ml, w.po, nullptr, nullptr, 0, nullptr};
   launch(prompt_attn_tc_kernel<D, KV4, false>, sh.ctas, kThreads, C::kSmem, s, map_q, mp);
   return launch_merge<D, __nv_bfloat16>(a, sh, w, s);
 }
@@ -2693,7 +2790,7 @@ int attn_launch_f32(const AttnParams& a, void* ws, cudaStream_t s) {
   constexpr int smem = CfgF32<D, RT>::kSmem;
   if (!allow_smem(prompt_attn_f32_kernel<D, RT, false>, smem)) return EAGLE_ERR_CUDA;
   launch_plan(a, sh, w, 1, 1, s);
-  const F32Params fp = {a, scale_log2(a), sh.g, sh.tpu, sh.rows, w.hdr, &w.hdr->next, w.pieces, w.ml, w.po, nullptr, nullptr, 0};
+  const F32Params fp = {a, scale_log2(a), sh.g, sh.tpu, sh.rows, w.hdr, &w.hdr->next, w.pieces, w.ml, w.po, nullptr, nullptr, 0, nullptr};
   launch(prompt_attn_f32_kernel<D, RT, false>, sh.ctas, 256, smem, s, fp);
   return launch_merge<D, float>(a, sh, w, s);
 }
@@ -2702,60 +2799,76 @@ int attn_launch_f32(const AttnParams& a, void* ws, cudaStream_t s) {
   return few_rows_f32(a.B, a.T, a.Hq, a.Hkv) ? attn_launch_f32<D, 1>(a, ws, s) : attn_launch_f32<D, 4>(a, ws, s);
 }
 
-// Shared prefixes.  Units are those of the tensor-core or the fp32 path.
-constexpr int kFlatLeast = 2;  // blocks of a CTA's part at least
+// Shared prefixes.  Units are those of the tensor-core or the fp32 path, or of one
+// tile of the former (kTile).
+constexpr int kFlatLeast = 2, kFlatLeastF32 = 1;  // blocks of a CTA's part at least
 struct FlatShape {
   int g, tpt, tpu, rows, ctas;
-  size_t off_o, total;
+  size_t off_ml, off_o, total;  // the splits first
 };
-FlatShape flat_shape(int T, int Hq, int Hkv, int D, Path path) {
+FlatShape flat_shape(int T, int Hq, int Hkv, int D, Path path, bool one_tile = false) {
   FlatShape s;
   const Shape x = attn_shape(1, T, Hq, Hkv, D, path);
-  s.g = x.g, s.tpt = x.tpt, s.tpu = x.tpu, s.rows = x.rows, s.ctas = x.ctas;
-  s.off_o = round_up(sizeof(float2) * 2 * (size_t)s.ctas * s.rows, 256);
+  s.g = x.g, s.tpt = x.tpt, s.ctas = x.ctas;
+  s.tpu = one_tile ? x.tpt : x.tpu;
+  s.rows = std::min(s.tpu, T) * s.g;
+  s.off_ml = round_up(sizeof(Split) * (size_t)s.ctas, 256);
+  s.off_o = round_up(s.off_ml + sizeof(float2) * 2 * (size_t)s.ctas * s.rows, 256);
   s.total = s.off_o + sizeof(float) * 2 * (size_t)s.ctas * s.rows * D + 256;
   return s;
 }
+struct FlatWs {
+  Split* splits;
+  float2* ml;
+  float* o;
+};
+FlatWs flat_ws(const FlatShape& sh, void* ws) {
+  char* w = reinterpret_cast<char*>(round_up(reinterpret_cast<size_t>(ws), 256));
+  return {reinterpret_cast<Split*>(w), reinterpret_cast<float2*>(w + sh.off_ml), reinterpret_cast<float*>(w + sh.off_o)};
+}
+// Few rows of all groups together: units of one tile.
+bool flat_one_tile(int T, int Hq, int Hkv) { return (long long)T * (Hq / Hkv) <= FLAT_ONE; }
 struct Own {
   const void* out;
   const float* lse;
 };
 template <int D, typename T>
-int flat_join(const AttnParams& a, const Own& own, const FlatShape& sh, const float2* ml, const float* o, cudaStream_t s) {
-  const JoinParams jp = {a, sh.g, sh.tpu, sh.rows, sh.ctas, kFlatLeast, ml, o, own.out, own.lse};
-  const long long rows = (long long)a.T * a.Hq;
-  launch(flat_join_kernel<D, T>, (int)std::min<long long>((rows + 7) / 8, 8ll * std::max(1, sm_count())), 256, 0, s, jp);
+int flat_join(const AttnParams& a, const Own& own, const FlatShape& sh, const FlatWs& w, cudaStream_t s) {
+  const JoinParams jp = {a, sh.g, sh.tpu, sh.rows, sh.ctas, w.splits, w.ml, w.o, own.out, own.lse};
+  // as many CTAs as there can be chunks of eight rows, four to an SM at most
+  const int sms = std::max(1, sm_count());
+  const long long units = ((long long)a.T / sh.tpu + std::min(a.B, a.T)) * a.Hkv;
+  const int chunks = (int)std::min<long long>(std::min<long long>(units, sh.ctas) * ((sh.rows + 7) / 8), 4 * sms);
+  launch(flat_join_kernel<D, T>, chunks + 1, 256, 0, s, jp);
   note_launch(2);
   return last_launch_status();
 }
 template <int D, bool KV4>
 int flat_launch_tc(const AttnParams& a, const Own& own, void* ws, cudaStream_t s) {
   using C = Cfg<D, KV4>;
-  const FlatShape sh = flat_shape(a.T, a.Hq, a.Hkv, D, kTensor);
-  char* w = reinterpret_cast<char*>(round_up(reinterpret_cast<size_t>(ws), 256));
-  float2* ml = reinterpret_cast<float2*>(w);
-  float* o = reinterpret_cast<float*>(w + sh.off_o);
+  const FlatShape sh = flat_shape(a.T, a.Hq, a.Hkv, D, kTensor, flat_one_tile(a.T, a.Hq, a.Hkv));
+  const FlatWs w = flat_ws(sh, ws);
+  if (sh.ctas > kMaxSplits) return EAGLE_ERR_UNSUPPORTED;
   CUtensorMap map_q = {};
   if (!KV4 && !make_tmap_3d_bf16(&map_q, a.q, D, (uint64_t)a.Hq, (uint64_t)a.T, (uint64_t)D * 2, (uint64_t)a.q_stride * 2,
                                  64, (uint32_t)sh.g, (uint32_t)sh.tpt))
     return EAGLE_ERR_CUDA;
   if (!allow_smem(prompt_attn_tc_kernel<D, KV4, true>, (int)C::kSmem)) return EAGLE_ERR_CUDA;
-  const MainParams mp = {a, scale_log2(a), sh.g, sh.tpt, sh.tpu, sh.rows, nullptr, nullptr, nullptr, ml, o, own.out, own.lse, kFlatLeast};
+  const MainParams mp = {a, scale_log2(a), sh.g, sh.tpt, sh.tpu, sh.rows, nullptr, nullptr, nullptr, w.ml, w.o, own.out, own.lse, kFlatLeast, w.splits};
   launch(prompt_attn_tc_kernel<D, KV4, true>, sh.ctas, kThreads, C::kSmem, s, map_q, mp);
-  return flat_join<D, __nv_bfloat16>(a, own, sh, ml, o, s);
+  return flat_join<D, __nv_bfloat16>(a, own, sh, w, s);
 }
 template <int D, int RT>
 int flat_launch_f32(const AttnParams& a, const Own& own, void* ws, cudaStream_t s) {
   const FlatShape sh = flat_shape(a.T, a.Hq, a.Hkv, D, RT == 1 ? kFp32Few : kFp32);
-  char* w = reinterpret_cast<char*>(round_up(reinterpret_cast<size_t>(ws), 256));
-  float2* ml = reinterpret_cast<float2*>(w);
-  float* o = reinterpret_cast<float*>(w + sh.off_o);
+  const FlatWs w = flat_ws(sh, ws);
+  if (sh.ctas > kMaxSplits) return EAGLE_ERR_UNSUPPORTED;
   constexpr int smem = CfgF32<D, RT>::kSmem;
   if (!allow_smem(prompt_attn_f32_kernel<D, RT, true>, smem)) return EAGLE_ERR_CUDA;
-  const F32Params fp = {a, scale_log2(a), sh.g, sh.tpu, sh.rows, nullptr, nullptr, nullptr, ml, o,
-                        static_cast<const float*>(own.out), own.lse, kFlatLeast};
+  const F32Params fp = {a, scale_log2(a), sh.g, sh.tpu, sh.rows, nullptr, nullptr, nullptr, w.ml, w.o,
+                        static_cast<const float*>(own.out), own.lse, kFlatLeastF32, w.splits};
   launch(prompt_attn_f32_kernel<D, RT, true>, sh.ctas, 256, smem, s, fp);
-  return flat_join<D, float>(a, own, sh, ml, o, s);
+  return flat_join<D, float>(a, own, sh, w, s);
 }
 template <int D>
 int flat_launch_f32(const AttnParams& a, const Own& own, void* ws, cudaStream_t s) {
