@@ -417,8 +417,12 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanPar
 // FLAT kernels: attention of groups of rows over a prefix that the group shares
 // (B groups, cu their rows, ctx their prefix's keys, table its pages), every key
 // visible to every row.  A unit's key blocks are all known from a group's two
-// numbers, so nothing is planned: the blocks of all units (by group, kv head and
-// unit) are one line that the CTAs share out evenly, each finding its own part.
+// numbers, so nothing is planned in front: the blocks of all units (by group, kv
+// head and unit) are one line, of which CTA c takes blocks c per .. c per + per - 1,
+// and each CTA finds its own part.  Where the units are few, `per` is such that
+// units, rounded up to a multiple of it, have a CTA for every part, and no CTA has
+// parts of two units (a second piece's start costs 3 us: its pages, keys and rows
+// are only then known).
 // A unit that lies in one CTA's part is finished there; of the others each CTA
 // leaves a partial result (slot 2 c + 1 for the piece that a unit starts with, at
 // most one per CTA, 2 c for one that it goes on with), and the CTA that it starts in
@@ -426,15 +430,16 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanPar
 struct __align__(16) Split {  // a unit that starts in a CTA's part and ends in CTA `last`'s
   int rows, last, h, tok0;   // rows: 0 if there is none
 };
-struct Groups {  // a warp's view: lane i holds group base + i
-  int c0, n, len;  // first row, rows, keys (0 if the group is in error)
-  int units, blocks;
-  long long work;  // blocks of all its units
+constexpr int kFlatLeast = 2, kFlatLeastF32 = 1;  // blocks of a part at least
+constexpr int kFlatMore = 3;  // blocks by which a part may grow for whole units
+struct Groups {  // a warp's view: lane i holds group base + i (of one group, all lanes have it)
+  int c0, n, len;     // first row, rows, keys (0 if the group is in error)
+  int units, blocks;  // units: of all kv heads
   bool falls;
 };
 __device__ __forceinline__ Groups load_groups(const AttnParams& a, int base, int tpu, bool report) {
-  Groups g = {0, 0, 0, 0, 0, 0, false};
-  const int i = base + (int)(threadIdx.x & 31);
+  Groups g = {0, 0, 0, 0, 0, false};
+  const int i = a.B == 1 ? 0 : base + (int)(threadIdx.x & 31);
   if (i >= a.B) return g;
   g.c0 = a.cu[i];
   const int c1 = a.cu[i + 1], len = a.ctx[i];
@@ -446,127 +451,132 @@ __device__ __forceinline__ Groups load_groups(const AttnParams& a, int base, int
   } else {
     g.n = c1 - g.c0;
     g.len = len;
-    g.units = (g.n + tpu - 1) / tpu;
+    g.units = (g.n + tpu - 1) / tpu * a.Hkv;
     g.blocks = (len + kBlk - 1) / kBlk;
-    g.work = (long long)g.units * g.blocks * a.Hkv;
   }
   // rows in front of the first group or behind the last belong to none
   if (report && ((i == 0 && g.c0 != 0) || (i == a.B - 1 && c1 != a.T))) set_status(a.status, EAGLE_ERR_INVALID_ARG);
   return g;
 }
-__device__ __forceinline__ long long warp_sum(long long v) {
+// a / b, 0 <= a, 0 < b: by the quotient of floats, put right by the remainder, where
+// a is exact in fp32 (a 64-bit division is a long way round for a CTA's first step)
+__device__ __forceinline__ long long quotient(long long a, int b) {
+  if (a >= (1 << 24)) return a / b;
+  int q = (int)__fdividef((float)(int)a, (float)b);
+  const int r = (int)a - q * b;
+  if (r < 0)
+    --q;
+  else if (r >= b)
+    ++q;
+  return q;
+}
+// The sum of f(group) over all groups; one warp calls it.
+template <typename F>
+__device__ __forceinline__ long long sum_groups(const AttnParams& a, int tpu, const Groups& first, F&& f) {
+  if (a.B == 1) return f(first);
+  long long v = f(first);
+  for (int base = 32; base < a.B; base += 32) v += f(load_groups(a, base, tpu, false));
 #pragma unroll
   for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
   return v;
 }
-// a / b for a >= 0, b > 0 (64-bit quotients are long sequences; most lines are short)
-__device__ __forceinline__ long long quotient(long long a, int b) {
-  return a < (1ll << 32) ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
-}
-// The line of all blocks and its parts: CTA c of n has blocks [start(c), start(c + 1)),
-// all c / n rounded down; `least` blocks each or more, so that few blocks are not a
-// piece for every CTA.
-struct FlatLine {
-  long long all, q;  // blocks (0 where cu falls: rows might have two prefixes); all / ctas
-  int ctas, r;
-  bool falls;
-  Groups g;  // groups 0 .. 31
-  __device__ __forceinline__ FlatLine(const AttnParams& a, int tpu, int n, int least, bool report) {
-    g = load_groups(a, 0, tpu, report);
-    all = warp_sum(g.work);
-    falls = __any_sync(0xffffffffu, g.falls);
-    for (int base = 32; base < a.B; base += 32) {
-      const Groups x = load_groups(a, base, tpu, report);
-      all += warp_sum(x.work);
-      falls = falls || __any_sync(0xffffffffu, x.falls);
-    }
-    if (falls) all = 0;
-    ctas = (int)max(1ll, min((long long)n, quotient(all, least)));
-    q = quotient(all, ctas);
-    r = (int)(all - q * ctas);
-  }
-  __device__ __forceinline__ long long start(int c) const { return q * c + (uint32_t)(r * c) / (uint32_t)ctas; }
-  // the CTA whose part block x is in: the largest c with all c / ctas <= x
-  __device__ __forceinline__ int owner(long long x) const {
-    const long long y = (x + 1) * ctas - 1;
-    return (int)(all < (1ll << 31) ? quotient(y, (int)all) : y / all);
-  }
-};
-// A place in the line, and the way on from it; one warp has it.
+// A CTA's part, piece by piece; one warp has it.
 struct FlatWalk {
+  int per;         // blocks of a part
+  bool snap;       // units are rounded up to whole parts
   long long left;  // blocks still to be given out
   int base, src, h, u, k;
   Groups g;
-  // the unit (h, u) of group base + src, and the block k of it, at `at` < all
-  __device__ __forceinline__ void seek(const AttnParams& a, const FlatLine& line, int tpu, long long at) {
-    g = line.g;
-    for (base = 0; base < a.B; base += 32) {
-      if (base) g = load_groups(a, base, tpu, false);
-      long long end = g.work;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, end, d);
-        if ((int)(threadIdx.x & 31) >= d) end += x;
-      }
-      const unsigned past = __ballot_sync(0xffffffffu, end > at);
-      if (past) {
-        src = __ffs((int)past) - 1;
-        at -= __shfl_sync(0xffffffffu, end - g.work, src);
-        break;
-      }
-      at -= __shfl_sync(0xffffffffu, end, 31);
-    }
-    const int blocks = __shfl_sync(0xffffffffu, g.blocks, src), units = __shfl_sync(0xffffffffu, g.units, src);
-    const long long unit = quotient(at, blocks);
-    k = (int)(at - unit * blocks);
-    h = (int)quotient(unit, units);
-    u = (int)(unit - (long long)h * units);
+  __device__ __forceinline__ int take(int x) const { return __shfl_sync(0xffffffffu, x, src); }
+  __device__ __forceinline__ long long line(const Groups& x) const {  // a group's stretch of it
+    return (long long)x.units * (snap ? (x.blocks + per - 1) / per * per : x.blocks);
   }
-  __device__ __forceinline__ void start(const AttnParams& a, const FlatLine& line, int tpu) {
-    const int c = (int)blockIdx.x;
+  __device__ __forceinline__ void start(const AttnParams& a, int tpu, int least, bool report) {
+    const int ctas = (int)gridDim.x;
+    g = load_groups(a, 0, tpu, report);
     left = 0;
-    if (c >= line.ctas || line.all == 0) return;
-    const long long at = line.start(c);
-    left = line.start(c + 1) - at;
-    seek(a, line, tpu, at);
+    per = least;
+    snap = false;
+    bool falls = g.falls;
+    if (a.B > 1) {
+      for (base = 32; base < a.B; base += 32) falls = load_groups(a, base, tpu, report).falls || falls;
+      falls = __any_sync(0xffffffffu, falls);
+    }
+    if (falls) return;  // rows might have two prefixes: nothing is done
+    const long long all = sum_groups(a, tpu, g, [](const Groups& x) { return (long long)x.units * x.blocks; });
+    const int even = (int)max((long long)least, quotient(all + ctas - 1, ctas));
+    per = even;
+    for (int more = 0; more <= kFlatMore && !snap; ++more) {
+      const int p = even + more;
+      snap = sum_groups(a, tpu, g, [&](const Groups& x) { return x.units * quotient(x.blocks + p - 1, p); }) <= ctas;
+      if (snap) per = p;
+    }
+    long long at = (long long)blockIdx.x * per;
+    base = src = 0;
+    if (a.B == 1) {
+      if (at >= line(g)) return;
+    } else {
+      for (;; base += 32) {
+        if (base >= a.B) return;
+        if (base) g = load_groups(a, base, tpu, false);
+        const long long mine = line(g);
+        long long end = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const long long x = __shfl_up_sync(0xffffffffu, end, d);
+          if ((int)(threadIdx.x & 31) >= d) end += x;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, end > at);
+        if (past) {
+          src = __ffs((int)past) - 1;
+          at -= __shfl_sync(0xffffffffu, end - mine, src);
+          break;
+        }
+        at -= __shfl_sync(0xffffffffu, end, 31);
+      }
+    }
+    const int blocks = take(g.blocks), units = take(g.units), len = snap ? (blocks + per - 1) / per * per : blocks;
+    const int unit = (int)quotient(at, len), of_head = units / a.Hkv;
+    k = (int)(at - (long long)unit * len);
+    h = (int)quotient(unit, of_head);
+    u = unit - h * of_head;
+    left = snap ? min(per, blocks - k) : min((long long)per, all - (long long)blockIdx.x * per);
   }
-  // what the join needs of piece w, the part's last: the unit may go on in the next CTA's
-  __device__ __forceinline__ Split split(const FlatLine& line, const Piece& w, int tpu, int g_) const {
-    Split s = {0, 0, 0, 0};
-    if (w.slot < 0 || w.k0 > 0) return s;
-    s.rows = min(tpu, w.n - w.u * tpu) * g_;
-    s.last = line.owner(line.start((int)blockIdx.x + 1) + (w.ctx + kBlk - 1) / kBlk - w.k1 - 1);
-    s.h = w.h;
-    s.tok0 = w.c0 + w.u * tpu;
-    return s;
-  }
-  // the next piece of a CTA's part
   __device__ __forceinline__ bool next(const AttnParams& a, int tpu, Piece& w) {
     if (left <= 0) return false;
-    const int blocks = __shfl_sync(0xffffffffu, g.blocks, src), units = __shfl_sync(0xffffffffu, g.units, src);
+    const int blocks = take(g.blocks), n = take(g.n);
     const int k1 = (int)min((long long)blocks, k + left), c = (int)blockIdx.x;
-    w = Piece{base + src, h, u, k, k1, k1 - k == blocks ? -1 : 2 * c + (k == 0 ? 1 : 0), __shfl_sync(0xffffffffu, g.c0, src),
-              __shfl_sync(0xffffffffu, g.n, src), __shfl_sync(0xffffffffu, g.len, src), 0, 0, 1};
+    w = Piece{base + src, h, u, k, k1, k1 - k == blocks ? -1 : 2 * c + (k == 0 ? 1 : 0), take(g.c0), n, take(g.len), 0, 0, 1};
     left -= k1 - k;
     k = 0;
-    if (k1 == blocks && ++u == units) {
+    if (left > 0 && ++u * tpu >= n) {
       u = 0;
-      if (++h == a.Hkv && left > 0) {
+      if (++h == a.Hkv) {
         h = 0;
-        unsigned more = __ballot_sync(0xffffffffu, g.work > 0) & (src == 31 ? 0u : ~0u << (src + 1));
-        while (!more) {  // (work is left, so some later group has it)
+        unsigned more = a.B == 1 ? 0u : __ballot_sync(0xffffffffu, g.blocks > 0 && g.units > 0) & (src == 31 ? 0u : ~0u << (src + 1));
+        while (!more) {  // (blocks are left, so some later group has them)
           base += 32;
           if (base >= a.B) {
             left = 0;
             return true;
           }
           g = load_groups(a, base, tpu, false);
-          more = __ballot_sync(0xffffffffu, g.work > 0);
+          more = __ballot_sync(0xffffffffu, g.blocks > 0 && g.units > 0);
         }
         src = __ffs((int)more) - 1;
       }
     }
     return true;
+  }
+  // what the join needs of the part's last piece w, whose unit may go on in the next parts
+  __device__ __forceinline__ Split split(const Piece& w, int tpu, int of_token) const {
+    Split s = {0, 0, 0, 0};
+    if (w.slot < 0 || w.k0 > 0) return s;
+    s.rows = min(tpu, w.n - w.u * tpu) * of_token;
+    s.last = (int)blockIdx.x + 1 + ((w.ctx + kBlk - 1) / kBlk - w.k1 - 1) / per;
+    s.h = w.h;
+    s.tok0 = w.c0 + w.u * tpu;
+    return s;
   }
 };
 // A row's own keys as one more term of its sums: their log-sum-exp L becomes the
@@ -576,8 +586,7 @@ struct FlatWalk {
 struct OwnWeight {
   float prefix, own, lse;  // factors of O and of own_out, and the joined log-sum-exp
 };
-__device__ __forceinline__ OwnWeight own_weight(float m, float l, const float* own_lse, size_t row) {
-  const float L = own_lse ? own_lse[row] : -INFINITY;
+__device__ __forceinline__ OwnWeight own_weight(float m, float l, float L) {
   if (l == 0.f) return {0.f, L == -INFINITY ? 0.f : 1.f, L};  // the own result as it is
   if (L == -INFINITY) return {1.f / l, 0.f, (m + log2f(l)) * kLn2};
   const float hi = L * 1.44269502f, lo = fmaf(L, 1.44269502f, -hi) + L * 1.92596303e-8f, M = fmaxf(m, hi);
@@ -642,7 +651,6 @@ struct MainParams {
   float* part_o;
   const void* own_out;  // FLAT: what the rows' own keys gave, or null
   const float* own_lse;
-  int least;
   Split* splits;  // one per CTA
 };
 
@@ -1285,9 +1293,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 6) {
       // ----------------------------------------------------------- scheduler
       if constexpr (FLAT) {
-        const FlatLine line(a, p.tpu, (int)gridDim.x, p.least, blockIdx.x == 0);
         FlatWalk walk;
-        walk.start(a, line, p.tpu);
+        walk.start(a, p.tpu, kFlatLeast, blockIdx.x == 0);
         Piece w;
         w.slot = -1;
         for (int ps = 0;; ++ps) {
@@ -1305,7 +1312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (!more) break;
         }
-        const Split x = walk.split(line, w, p.tpu, p.g);
+        const Split x = walk.split(w, p.tpu, p.g);
         if (lane == 0) p.splits[blockIdx.x] = x;
       } else if (lane == 0) {
         const int total = p.hdr->pieces;
@@ -1615,7 +1622,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float inv = whole ? (l == 0.f ? 0.f : a.v_scale / l) : 1.f, own = 0.f;
         if constexpr (FLAT) {
           if (whole && row_ok) {
-            const OwnWeight x = own_weight(m, l, p.own_lse, orow);
+            const OwnWeight x = own_weight(m, l, p.own_lse ? p.own_lse[orow] : -INFINITY);
             inv = x.prefix * a.v_scale;
             own = x.own;
             m = x.lse;
@@ -1669,6 +1676,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   pack16<false>(f[8 * u + 2] * by, f[8 * u + 3] * by),
                                   pack16<false>(f[8 * u + 4] * by, f[8 * u + 5] * by),
                                   pack16<false>(f[8 * u + 6] * by, f[8 * u + 7] * by));
+          } else if constexpr (FLAT) {
+            // by channel and row: a warp's rows lie side by side (a row's 16 bytes
+            // each, 32 rows apart, took 5,900 cycles a tile)
+            float* dst = p.part_o + ((size_t)w.slot * D + c * 32) * p.slot_rows + urow;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) dst[(size_t)k * p.slot_rows] = f[k];
           } else {
             float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + c * 32);
 #pragma unroll
@@ -2362,7 +2375,6 @@ struct F32Params {
   float2* part_ml;
   float* part_o;
   const float *own_out, *own_lse;  // FLAT
-  int least;
   Split* splits;
 };
 template <int D, int RT, bool FLAT>
@@ -2380,17 +2392,16 @@ __global__ void __launch_bounds__(256, (CfgF32<D, RT>::kCtas)) prompt_attn_f32_k
   __shared__ Piece s_w;  // FLAT
   FlatWalk walk;
   if (FLAT && tid < 32) {
-    // (walked twice: what the join needs is in the part's last piece, and the line
-    // would hold registers all the while)
-    const FlatLine line(a, p.tpu, (int)gridDim.x, p.least, blockIdx.x == 0);
+    // (walked twice: what the join needs is in the part's last piece)
+    walk.start(a, p.tpu, kFlatLeastF32, blockIdx.x == 0);
+    const FlatWalk from = walk;
     Piece w;
     w.slot = -1;
-    walk.start(a, line, p.tpu);
     while (walk.next(a, p.tpu, w)) {
     }
-    const Split x = walk.split(line, w, p.tpu, p.g);
+    const Split x = walk.split(w, p.tpu, p.g);
     if (tid == 0) p.splits[blockIdx.x] = x;
-    walk.start(a, line, p.tpu);
+    walk = from;
   }
   for (bool first = true;; first = false) {
     __syncthreads();
@@ -2549,7 +2560,7 @@ __global__ void __launch_bounds__(256, (CfgF32<D, RT>::kCtas)) prompt_attn_f32_k
       float f = whole ? (l[i] == 0.f ? 0.f : 1.f / l[i]) : 1.f;
       float* dst = whole ? static_cast<float*>(a.out) + orow * D : p.part_o + prow * D;
       if (FLAT && whole) {
-        const OwnWeight x = own_weight(m[i], l[i], p.own_lse, orow);
+        const OwnWeight x = own_weight(m[i], l[i], p.own_lse ? p.own_lse[orow] : -INFINITY);
         const float own = x.own;
         f = 1.f;
         m[i] = x.lse;
@@ -2583,8 +2594,10 @@ __global__ void __launch_bounds__(256, (CfgF32<D, RT>::kCtas)) prompt_attn_f32_k
 
 // ----------------------------------------------- shared prefixes: the join
 // The units that several CTAs shared, as those CTAs described them: eight rows of a
-// unit to a CTA, a warp each, a lane D / 32 channels.  The last CTA lets rows of
-// empty prefixes take their own result over.
+// unit to a CTA at a time.  16-bit rows' partial results are by channel and row
+// (thread t: row t % 8, channels D/32 (t / 8) ..), fp32 rows' by row (a warp a row, a
+// lane D / 32 channels): what each main kernel writes in whole lines.  The last CTA
+// lets rows of empty prefixes take their own result over.
 struct JoinParams {
   AttnParams a;
   int g, tpu, slot_rows, ctas;
@@ -2595,100 +2608,160 @@ struct JoinParams {
   const float* own_lse;
 };
 template <int D, typename T>
-__device__ __forceinline__ void join_row(const JoinParams& p, size_t r, float M, float l, const float* o) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const OwnWeight w = own_weight(M, l, p.own_lse, r);
-  float y[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) y[e] = o[e] * (w.prefix * p.a.v_scale);
-  if (p.own_out && !(w.own == 0.f)) {
-    const T* own = static_cast<const T*>(p.own_out) + r * D + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) y[e] = w.prefix == 0.f ? (float)own[e] : fmaf((float)own[e], w.own, y[e]);
-  }
-  T* dst = static_cast<T*>(p.a.out) + r * D + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; e += 2) {
-    if constexpr (sizeof(T) == 4)
-      *reinterpret_cast<float2*>(dst + e) = make_float2(y[e], y[e + 1]);
-    else
-      *reinterpret_cast<uint32_t*>(dst + e) = pack16<false>(y[e], y[e + 1]);
-  }
-  __syncwarp();  // lse may be own_lse
-  if (p.a.lse && lane == 0) p.a.lse[r] = w.lse;
-}
-constexpr int kMaxSplits = 512;  // CTAs of a main kernel at most
-template <int D, typename T>
 __global__ void __launch_bounds__(256) flat_join_kernel(const JoinParams p) {
-  constexpr int E = D / 32;
-  __shared__ int s_rows[kMaxSplits];
+  constexpr int E = D / 32, kBatch = 10;  // pieces whose loads are in flight together
+  constexpr bool kByRow = sizeof(T) == 4;
   const AttnParams& a = p.a;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  float none[E];
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int my_row = kByRow ? tid >> 5 : tid & 7, chan = (kByRow ? lane : tid >> 3) * E;
+  auto load_own = [&](size_t r, float* y, float& L) {
+    if (!p.own_lse) {
+      L = -INFINITY;
+      return;
+    }
+    L = p.own_lse[r];
+    const T* own = static_cast<const T*>(p.own_out) + r * D + chan;
 #pragma unroll
-  for (int e = 0; e < E; ++e) none[e] = 0.f;
+    for (int e = 0; e < E; ++e) y[e] = (float)own[e];
+  };
+  // O = o with its statistics, and the own result, to row r of the arrays; the
+  // threads of a row have read own_lse, which lse may be, before one of them writes it
+  auto finish = [&](bool live, size_t r, float M, float l, const float* o, const float* own, float L) {
+    OwnWeight w;
+    if (live) {
+      w = own_weight(M, l, L);
+      const float pre = w.prefix * a.v_scale;
+      float y[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        y[e] = w.own == 0.f ? o[e] * pre : w.prefix == 0.f ? own[e] : fmaf(own[e], w.own, o[e] * pre);
+      T* dst = static_cast<T*>(a.out) + r * D + chan;
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        if constexpr (kByRow)
+          *reinterpret_cast<float2*>(dst + e) = make_float2(y[e], y[e + 1]);
+        else
+          *reinterpret_cast<uint32_t*>(dst + e) = pack16<false>(y[e], y[e + 1]);
+      }
+    }
+    __syncthreads();
+    if (live && a.lse && chan == 0) a.lse[r] = w.lse;
+  };
   pdl_wait();
   pdl_trigger();
   if (blockIdx.x == gridDim.x - 1) {
     bool falls = false;
-    for (int base = 0; base < a.B; base += 32) falls = falls || __any_sync(0xffffffffu, load_groups(a, base, p.tpu, false).falls);
+    for (int base = 0; base < a.B; base += 32) falls = __any_sync(0xffffffffu, load_groups(a, base, p.tpu, false).falls) || falls;
     if (falls) return;
     for (int base = 0; base < a.B; base += 32) {
       const Groups g = load_groups(a, base, p.tpu, false);
-      for (unsigned m = __ballot_sync(0xffffffffu, g.n > 0 && g.len == 0); m; m &= m - 1) {
+      unsigned m = __ballot_sync(0xffffffffu, g.n > 0 && g.len == 0);
+      if (a.B == 1) m &= 1u;
+      for (; m; m &= m - 1) {
         const int src = __ffs((int)m) - 1;
         const long long rows = (long long)__shfl_sync(0xffffffffu, g.n, src) * a.Hq;
         const size_t r0 = (size_t)__shfl_sync(0xffffffffu, g.c0, src) * a.Hq;
-        for (long long r = warp; r < rows; r += 8) join_row<D, T>(p, r0 + (size_t)r, -INFINITY, 0.f, none);
+        for (long long r = 0; r < rows; r += 8) {
+          const bool live = r + my_row < rows;
+          float none[E], own[E], L = 0.f;
+#pragma unroll
+          for (int e = 0; e < E; ++e) none[e] = own[e] = 0.f;
+          if (live) load_own(r0 + (size_t)r + my_row, own, L);
+          finish(live, r0 + (size_t)r + my_row, -INFINITY, 0.f, none, own, L);
+        }
       }
     }
     return;
   }
-  for (int c = tid; c < p.ctas; c += 256) s_rows[c] = p.splits[c].rows;
-  __syncthreads();
   // every warp walks the units' chunks of eight rows: this CTA's are numbers
   // blockIdx.x, + gridDim.x - 1, ..
   int want = (int)blockIdx.x, before = 0;
-  for (int base = 0; base < p.ctas; base += 32) {
-    const int chunks = base + lane < p.ctas ? (s_rows[base + lane] + 7) / 8 : 0;
-    int end = chunks;
+  for (int base0 = 0; base0 < p.ctas; base0 += 160) {
+    Split sp[5];
+    int end[5];
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, end, d);
-      if (lane >= d) end += x;
-    }
-    const int all = __shfl_sync(0xffffffffu, end, 31);
-    while (want < before + all) {
-      const int src = __ffs((int)__ballot_sync(0xffffffffu, before + end > want)) - 1, c0 = base + src;
-      const int row = (want - before - __shfl_sync(0xffffffffu, end - chunks, src)) * 8 + warp;
-      want += (int)gridDim.x - 1;
-      const Split u = p.splits[c0];
-      if (row >= u.rows) continue;
-      auto slot = [&](int x) { return (size_t)(2 * x + (x == c0 ? 1 : 0)) * p.slot_rows + row; };
-      float l = 0.f, M = -INFINITY, o[E];
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = 0.f;
-      for (int x = c0 + lane; x <= u.last; x += 32) M = fmaxf(M, __ldcg(p.ml + slot(x)).x);
-#pragma unroll
-      for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-#pragma unroll 8
-      for (int x = c0; x <= u.last; ++x) {
-        const float2 v = __ldcg(p.ml + slot(x));
-        const float w = M == -INFINITY ? 1.f : ex2_approx(v.x - M);
-        l = fmaf(w, v.y, l);
-        const float* part = p.o + slot(x) * D + lane * E;
-        float f[E];
-        if constexpr (E == 4)
-          *reinterpret_cast<float4*>(f) = __ldcg(reinterpret_cast<const float4*>(part));
-        else
-          *reinterpret_cast<float2*>(f) = __ldcg(reinterpret_cast<const float2*>(part));
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(w, f[e], o[e]);
+    for (int i = 0; i < 5; ++i) {
+      sp[i] = Split{0, 0, 0, 0};
+      if (base0 + 32 * i + lane < p.ctas) {
+        const int4 v = __ldcg(reinterpret_cast<const int4*>(p.splits + base0 + 32 * i + lane));
+        sp[i] = Split{v.x, v.y, v.z, v.w};
       }
-      join_row<D, T>(p, ((size_t)u.tok0 + row / p.g) * a.Hq + u.h * p.g + row % p.g, M, l, o);
+      end[i] = (sp[i].rows + 7) / 8;
     }
-    before += all;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1)
+#pragma unroll
+      for (int i = 0; i < 5; ++i) {
+        const int x = __shfl_up_sync(0xffffffffu, end[i], d);
+        if (lane >= d) end[i] += x;
+      }
+    // (the chunks of sp[0] come first, and so on)
+    int all[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) all[i] = __shfl_sync(0xffffffffu, end[i], 31) + (i ? all[i - 1] : 0);
+#pragma unroll 1
+    while (want < before + all[4]) {
+      Split mine = sp[0];
+      int last = end[0], base = base0, skipped = 0;
+#pragma unroll
+      for (int i = 1; i < 5; ++i)
+        if (want >= before + all[i - 1]) mine = sp[i], last = end[i], base = base0 + 32 * i, skipped = all[i - 1];
+      const int n = want - before - skipped, src = __ffs((int)__ballot_sync(0xffffffffu, last > n)) - 1, c0 = base + src;
+      Split u;
+      u.rows = __shfl_sync(0xffffffffu, mine.rows, src);
+      u.last = __shfl_sync(0xffffffffu, mine.last, src);
+      u.h = __shfl_sync(0xffffffffu, mine.h, src);
+      u.tok0 = __shfl_sync(0xffffffffu, mine.tok0, src);
+      const int row = (n - (__shfl_sync(0xffffffffu, last, src) - (u.rows + 7) / 8)) * 8 + my_row;
+      want += (int)gridDim.x - 1;
+      const bool live = row < u.rows;
+      const size_t r = ((size_t)u.tok0 + row / p.g) * a.Hq + u.h * p.g + row % p.g;
+      float l = 0.f, M = -INFINITY, L = 0.f, o[E], own[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = own[e] = 0.f;
+      if (live) load_own(r, own, L);
+      for (int x0 = c0; live && x0 <= u.last; x0 += kBatch) {
+        float2 ml[kBatch];
+        float f[kBatch][E];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int x = x0 + i;
+          ml[i] = make_float2(-INFINITY, 0.f);
+          if (x > u.last) continue;
+          const size_t slot = (size_t)(2 * x + (x == c0 ? 1 : 0));
+          ml[i] = __ldcg(p.ml + slot * p.slot_rows + row);
+          if constexpr (kByRow) {
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+              const float2 v = __ldcg(reinterpret_cast<const float2*>(p.o + (slot * p.slot_rows + row) * D + chan + e));
+              f[i][e] = v.x, f[i][e + 1] = v.y;
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) f[i][e] = __ldcg(p.o + (slot * D + chan + e) * p.slot_rows + row);
+          }
+        }
+        float top = M;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) top = fmaxf(top, ml[i].x);
+        const float ref = top == -INFINITY ? 0.f : top, down = ex2_approx(M - ref);
+        M = top;
+        l *= down;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] *= down;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          if (x0 + i > u.last) continue;
+          // a piece without a key that counts has zeros, or a NaN to pass on
+          const float w = ml[i].x == -INFINITY ? 1.f : ex2_approx(ml[i].x - ref);
+          l = fmaf(w, ml[i].y, l);
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] = fmaf(w, f[i][e], o[e]);
+        }
+      }
+      finish(live, r, M, l, o, own, L);
+    }
+    before += all[4];
   }
 }
 
@@ -2779,7 +2852,7 @@ int attn_launch_tc(const AttnParams& a, void* ws, cudaStream_t s) {
   if (!allow_smem(prompt_attn_tc_kernel<D, KV4, false>, (int)C::kSmem)) return EAGLE_ERR_CUDA;
   launch_plan(a, sh, w, 2, 2, s);
   const MainParams mp = {a, scale_log2(a), sh.g, sh.tpt, sh.tpu, sh.rows, w.hdr, &w.hdr->next, w.pieces,
-                         w.ml, w.po, nullptr, nullptr, 0, nullptr};
+                         w.ml, w.po, nullptr, nullptr, nullptr};
   launch(prompt_attn_tc_kernel<D, KV4, false>, sh.ctas, kThreads, C::kSmem, s, map_q, mp);
   return launch_merge<D, __nv_bfloat16>(a, sh, w, s);
 }
@@ -2790,7 +2863,7 @@ int attn_launch_f32(const AttnParams& a, void* ws, cudaStream_t s) {
   constexpr int smem = CfgF32<D, RT>::kSmem;
   if (!allow_smem(prompt_attn_f32_kernel<D, RT, false>, smem)) return EAGLE_ERR_CUDA;
   launch_plan(a, sh, w, 1, 1, s);
-  const F32Params fp = {a, scale_log2(a), sh.g, sh.tpu, sh.rows, w.hdr, &w.hdr->next, w.pieces, w.ml, w.po, nullptr, nullptr, 0, nullptr};
+  const F32Params fp = {a, scale_log2(a), sh.g, sh.tpu, sh.rows, w.hdr, &w.hdr->next, w.pieces, w.ml, w.po, nullptr, nullptr, nullptr};
   launch(prompt_attn_f32_kernel<D, RT, false>, sh.ctas, 256, smem, s, fp);
   return launch_merge<D, float>(a, sh, w, s);
 }
@@ -2801,7 +2874,6 @@ int attn_launch_f32(const AttnParams& a, void* ws, cudaStream_t s) {
 
 // Shared prefixes.  Units are those of the tensor-core or the fp32 path, or of one
 // tile of the former (kTile).
-constexpr int kFlatLeast = 2, kFlatLeastF32 = 1;  // blocks of a CTA's part at least
 struct FlatShape {
   int g, tpt, tpu, rows, ctas;
   size_t off_ml, off_o, total;  // the splits first
@@ -2811,7 +2883,7 @@ FlatShape flat_shape(int T, int Hq, int Hkv, int D, Path path, bool one_tile = f
   const Shape x = attn_shape(1, T, Hq, Hkv, D, path);
   s.g = x.g, s.tpt = x.tpt, s.ctas = x.ctas;
   s.tpu = one_tile ? x.tpt : x.tpu;
-  s.rows = std::min(s.tpu, T) * s.g;
+  s.rows = (int)round_up(std::min(s.tpu, T) * s.g, 8);  // (whole sectors of eight rows)
   s.off_ml = round_up(sizeof(Split) * (size_t)s.ctas, 256);
   s.off_o = round_up(s.off_ml + sizeof(float2) * 2 * (size_t)s.ctas * s.rows, 256);
   s.total = s.off_o + sizeof(float) * 2 * (size_t)s.ctas * s.rows * D + 256;
@@ -2838,7 +2910,7 @@ int flat_join(const AttnParams& a, const Own& own, const FlatShape& sh, const Fl
   // as many CTAs as there can be chunks of eight rows, four to an SM at most
   const int sms = std::max(1, sm_count());
   const long long units = ((long long)a.T / sh.tpu + std::min(a.B, a.T)) * a.Hkv;
-  const int chunks = (int)std::min<long long>(std::min<long long>(units, sh.ctas) * ((sh.rows + 7) / 8), 4 * sms);
+  const int chunks = (int)std::min<long long>(std::min<long long>(units, sh.ctas) * (sh.rows / 8), 8 * sms);
   launch(flat_join_kernel<D, T>, chunks + 1, 256, 0, s, jp);
   note_launch(2);
   return last_launch_status();
@@ -2848,13 +2920,12 @@ int flat_launch_tc(const AttnParams& a, const Own& own, void* ws, cudaStream_t s
   using C = Cfg<D, KV4>;
   const FlatShape sh = flat_shape(a.T, a.Hq, a.Hkv, D, kTensor, flat_one_tile(a.T, a.Hq, a.Hkv));
   const FlatWs w = flat_ws(sh, ws);
-  if (sh.ctas > kMaxSplits) return EAGLE_ERR_UNSUPPORTED;
   CUtensorMap map_q = {};
   if (!KV4 && !make_tmap_3d_bf16(&map_q, a.q, D, (uint64_t)a.Hq, (uint64_t)a.T, (uint64_t)D * 2, (uint64_t)a.q_stride * 2,
                                  64, (uint32_t)sh.g, (uint32_t)sh.tpt))
     return EAGLE_ERR_CUDA;
   if (!allow_smem(prompt_attn_tc_kernel<D, KV4, true>, (int)C::kSmem)) return EAGLE_ERR_CUDA;
-  const MainParams mp = {a, scale_log2(a), sh.g, sh.tpt, sh.tpu, sh.rows, nullptr, nullptr, nullptr, w.ml, w.o, own.out, own.lse, kFlatLeast, w.splits};
+  const MainParams mp = {a, scale_log2(a), sh.g, sh.tpt, sh.tpu, sh.rows, nullptr, nullptr, nullptr, w.ml, w.o, own.out, own.lse, w.splits};
   launch(prompt_attn_tc_kernel<D, KV4, true>, sh.ctas, kThreads, C::kSmem, s, map_q, mp);
   return flat_join<D, __nv_bfloat16>(a, own, sh, w, s);
 }
@@ -2862,11 +2933,10 @@ template <int D, int RT>
 int flat_launch_f32(const AttnParams& a, const Own& own, void* ws, cudaStream_t s) {
   const FlatShape sh = flat_shape(a.T, a.Hq, a.Hkv, D, RT == 1 ? kFp32Few : kFp32);
   const FlatWs w = flat_ws(sh, ws);
-  if (sh.ctas > kMaxSplits) return EAGLE_ERR_UNSUPPORTED;
   constexpr int smem = CfgF32<D, RT>::kSmem;
   if (!allow_smem(prompt_attn_f32_kernel<D, RT, true>, smem)) return EAGLE_ERR_CUDA;
   const F32Params fp = {a, scale_log2(a), sh.g, sh.tpu, sh.rows, nullptr, nullptr, nullptr, w.ml, w.o,
-                        static_cast<const float*>(own.out), own.lse, kFlatLeastF32, w.splits};
+                        static_cast<const float*>(own.out), own.lse, w.splits};
   launch(prompt_attn_f32_kernel<D, RT, true>, sh.ctas, 256, smem, s, fp);
   return flat_join<D, float>(a, own, sh, w, s);
 }

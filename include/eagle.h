@@ -879,7 +879,7 @@ int eagle_prompt_attn_kv4(const void* q, long long q_stride, const uint8_t* k_co
  *   q : rows of Hq heads (positions applied), q_stride elements apart
  *   own_out : [T, Hq, D] dtype `dtype`, own_lse : [T, Hq] fp32; both or, for the
  *             prefix alone, neither.  A row of own_lse = -infinity has no keys of
- *             its own (its own_out is not read)
+ *             its own (its own_out may hold anything)
  *   out, lse (or NULL) : as eagle_prompt_attn; may be own_out and own_lse themselves
  * A group of an empty prefix takes own_out and own_lse over (zeros and -infinity
  * without them).  Rows whose keys, own ones included, all score -infinity give
