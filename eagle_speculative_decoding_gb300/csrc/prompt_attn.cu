@@ -458,17 +458,13 @@ __device__ __forceinline__ Groups load_groups(const AttnParams& a, int base, int
   if (report && ((i == 0 && g.c0 != 0) || (i == a.B - 1 && c1 != a.T))) set_status(a.status, EAGLE_ERR_INVALID_ARG);
   return g;
 }
-// a / b, 0 <= a, 0 < b: by the quotient of floats, put right by the remainder, where
-// a is exact in fp32 (a 64-bit division is a long way round for a CTA's first step)
+// a / b, 0 <= a < 2^24, 0 < b: the quotient of floats, put right by the remainder
+__device__ __forceinline__ int quotient(int a, int b) {
+  const int q = (int)__fdividef((float)a, (float)b), r = a - q * b;
+  return q + (r >= b ? 1 : 0) - (r < 0 ? 1 : 0);
+}
 __device__ __forceinline__ long long quotient(long long a, int b) {
-  if (a >= (1 << 24)) return a / b;
-  int q = (int)__fdividef((float)(int)a, (float)b);
-  const int r = (int)a - q * b;
-  if (r < 0)
-    --q;
-  else if (r >= b)
-    ++q;
-  return q;
+  return a < (1 << 24) && b < (1 << 24) ? quotient((int)a, b) : a / b;
 }
 // The sum of f(group) over all groups; one warp calls it.
 template <typename F>
@@ -503,12 +499,35 @@ struct FlatWalk {
       falls = __any_sync(0xffffffffu, falls);
     }
     if (falls) return;  // rows might have two prefixes: nothing is done
+    const int limit = 1 << 23;
+    if (a.B == 1 && g.units < limit && g.blocks < limit && (long long)g.units * g.blocks < limit) {
+      // one group and a short line, as in most calls: the same in plain ints (a CTA's
+      // first loads wait for this: 0.9 us the other way)
+      const int units = g.units, blocks = g.blocks, all = units * blocks;
+      const int even = max(least, quotient(all + ctas - 1, ctas));
+      per = even;
+      int parts = 0;
+      for (int more = 0; more <= kFlatMore && !snap; ++more) {
+        parts = quotient(blocks + even + more - 1, even + more);
+        if (units * (long long)parts <= ctas) snap = true, per = even + more;
+      }
+      base = src = 0;
+      const int c = (int)blockIdx.x, at = c * per;
+      if (snap ? c >= units * parts : at >= all) return;
+      const int unit = snap ? quotient(c, parts) : quotient(at, blocks);
+      k = snap ? (c - unit * parts) * per : at - unit * blocks;
+      const int of_head = units / a.Hkv;
+      h = of_head == 1 ? unit : quotient(unit, of_head);
+      u = unit - h * of_head;
+      left = snap ? min(per, blocks - k) : min(per, all - at);
+      return;
+    }
     const long long all = sum_groups(a, tpu, g, [](const Groups& x) { return (long long)x.units * x.blocks; });
-    const int even = (int)max((long long)least, quotient(all + ctas - 1, ctas));
+    const int even = (int)max((long long)least, quotient(all + ctas - 1, ctas));  // (lines of 2^31 blocks would be 2^38 keys)
     per = even;
     for (int more = 0; more <= kFlatMore && !snap; ++more) {
       const int p = even + more;
-      snap = sum_groups(a, tpu, g, [&](const Groups& x) { return x.units * quotient(x.blocks + p - 1, p); }) <= ctas;
+      snap = sum_groups(a, tpu, g, [&](const Groups& x) { return x.units * quotient((long long)x.blocks + p - 1, p); }) <= ctas;
       if (snap) per = p;
     }
     long long at = (long long)blockIdx.x * per;
@@ -536,9 +555,9 @@ struct FlatWalk {
       }
     }
     const int blocks = take(g.blocks), units = take(g.units), len = snap ? (blocks + per - 1) / per * per : blocks;
-    const int unit = (int)quotient(at, len), of_head = units / a.Hkv;
+    const int unit = (int)quotient(at, len), of_head = units / a.Hkv;  // (at: within the group)
     k = (int)(at - (long long)unit * len);
-    h = (int)quotient(unit, of_head);
+    h = (int)quotient((long long)unit, of_head);
     u = unit - h * of_head;
     left = snap ? min(per, blocks - k) : min((long long)per, all - (long long)blockIdx.x * per);
   }
@@ -656,7 +675,7 @@ struct MainParams {
 
 template <int ST, bool KV4>
 struct Bars {
-  uint64_t kv_full[ST], kv_empty[ST], q_full[2], q_empty[2], o_full[2], x_stat, x_done, s_full[2];
+  uint64_t kv_full[ST], kv_empty[ST], q_full[2], q_empty[2], o_full[2], x_stat, x_back, x_done, s_full[2];
   uint64_t turn[2][4];  // by tile and quarter: the other tile's softmax has done its block
   uint64_t p_full[2];
   uint64_t slot_full[kSlots], slot_empty[kSlots], drain[2];
@@ -899,7 +918,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&sb.slot_empty[i]), 15);  // warps 0-5 and 7-15
     }
     mbar_init(smem_u32(&sb.x_stat), 4);
-    mbar_init(smem_u32(&sb.x_done), 4);
+    mbar_init(smem_u32(&sb.x_back), 4);
+    mbar_init(smem_u32(&sb.x_done), FLAT ? 8 : 4);
     mbar_init(smem_u32(&sb.drain[0]), 1);
     mbar_init(smem_u32(&sb.drain[1]), 1);
     sb.abort_flag = 0;
@@ -1606,14 +1626,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after();
           const float2 x = sb.x_ml[row];
+          if (FLAT) {
+            sb.x_ml[row] = make_float2(m, l);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sb.x_back));
+          }
           const float mm = fmaxf(m, x.x);
           w0 = mm == -INFINITY ? 1.f : ex2_approx(m - mm);
           w1 = mm == -INFINITY ? 1.f : ex2_approx(x.x - mm);
           l = l * w0 + x.y * w1;
           m = mm;
         }
+        if (FLAT && t == 1) {
+          // (pieces are short here, and writing their results a good part of them:
+          // tile 1's warps take the upper half of the channels)
+          ok = warp_wait(sb.x_back, xph);
+          if (!ok) break;
+          tc_fence_after();
+          const float2 x = sb.x_ml[row];
+          const float mm = fmaxf(m, x.x);
+          w1 = mm == -INFINITY ? 1.f : ex2_approx(m - mm);
+          w0 = mm == -INFINITY ? 1.f : ex2_approx(x.x - mm);
+          l = x.y * w0 + l * w1;
+          m = mm;
+        }
       }
-      if (quad_live && !(tw.twin && t == 1)) {
+      const bool halves = FLAT && join;  // of the channels, one for each tile's warps
+      if (quad_live && (halves || !(tw.twin && t == 1))) {
         const int head = w.h * p.g + row % p.g;
         const size_t orow = ((size_t)w.c0 + tok) * a.Hq + head;
         const int urow = (tw.twin ? 0 : t * p.tpt * p.g) + row;
@@ -1628,11 +1668,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             m = x.lse;
           }
         }
+        const uint32_t o_first = halves ? tmem + lane_addr + C::kColO : o_addr;
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
+        for (int c = halves ? t * (D / 64) : 0; c < (halves && t == 0 ? D / 64 : D / 32); ++c) {
           uint32_t o[32];
           if (n > 0) {
-            tmem_ld32_issue(o_addr + (uint32_t)(c * 32), o);
+            tmem_ld32_issue(o_first + (uint32_t)(c * 32), o);
             tmem_wait_ld();
           } else {
 #pragma unroll
@@ -1640,7 +1681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (join) {
             uint32_t o2[32];
-            tmem_ld32_issue(o_addr + (uint32_t)(D + c * 32), o2);
+            tmem_ld32_issue(o_first + (uint32_t)(D + c * 32), o2);
             tmem_wait_ld();
 #pragma unroll
             for (int k = 0; k < 32; ++k)
@@ -1677,18 +1718,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   pack16<false>(f[8 * u + 4] * by, f[8 * u + 5] * by),
                                   pack16<false>(f[8 * u + 6] * by, f[8 * u + 7] * by));
           } else if constexpr (FLAT) {
-            // by channel and row: a warp's rows lie side by side (a row's 16 bytes
-            // each, 32 rows apart, took 5,900 cycles a tile)
-            float* dst = p.part_o + ((size_t)w.slot * D + c * 32) * p.slot_rows + urow;
+            // eight rows by channel: whole sectors (a row's 16 bytes each, 32 rows
+            // apart, took 5,900 cycles a tile)
+            float* dst = p.part_o + (((size_t)w.slot * p.slot_rows + (urow & ~7)) * D + c * 256) + (urow & 7);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) dst[(size_t)k * p.slot_rows] = f[k];
+            for (int k = 0; k < 32; ++k) dst[k * 8] = f[k];
           } else {
             float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + c * 32);
 #pragma unroll
             for (int u = 0; u < 8; ++u) dst[u] = make_float4(f[4 * u], f[4 * u + 1], f[4 * u + 2], f[4 * u + 3]);
           }
         }
-        if (row_ok) {
+        if (row_ok && !(halves && t == 1)) {
           if (whole) {
             if (a.lse) a.lse[orow] = FLAT ? m : l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
           } else {
@@ -1706,11 +1747,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (join) {
         // tile 1's O may be overwritten once tile 0's warps have read it
+        // (where both read both, neither's may before both have)
         tc_fence_before();
         __syncwarp();
-        if (t == 0) {
+        if (FLAT || t == 0) {
           if (lane == 0) mbar_arrive(smem_u32(&sb.x_done));
-        } else {
+        }
+        if (FLAT || t == 1) {
           ok = warp_wait(sb.x_done, xph);
           if (!ok) break;
         }
@@ -2593,11 +2636,12 @@ __global__ void __launch_bounds__(256, (CfgF32<D, RT>::kCtas)) prompt_attn_f32_k
 }
 
 // ----------------------------------------------- shared prefixes: the join
-// The units that several CTAs shared, as those CTAs described them: eight rows of a
-// unit to a CTA at a time.  16-bit rows' partial results are by channel and row
-// (thread t: row t % 8, channels D/32 (t / 8) ..), fp32 rows' by row (a warp a row, a
-// lane D / 32 channels): what each main kernel writes in whole lines.  The last CTA
-// lets rows of empty prefixes take their own result over.
+// The units that several CTAs shared, as those CTAs described them.  A CTA of 2 D
+// threads takes eight rows of a unit at a time, whose partial results are 32 D
+// contiguous bytes of each piece: 16 bytes a thread, of 16-bit rows four rows of a
+// channel, of fp32 rows four channels of a row.  The pieces' weights are worked out
+// once, a thread a piece and row, while those are on their way.  The last CTA lets
+// rows of empty prefixes take their own result over.
 struct JoinParams {
   AttnParams a;
   int g, tpu, slot_rows, ctas;
@@ -2607,45 +2651,44 @@ struct JoinParams {
   const void* own_out;
   const float* own_lse;
 };
-template <int D, typename T>
-__global__ void __launch_bounds__(256) flat_join_kernel(const JoinParams p) {
-  constexpr int E = D / 32, kBatch = 10;  // pieces whose loads are in flight together
+constexpr int kMaxParts = 320;  // CTAs of a main kernel at most
+template <int D, typename T, int kBatch, int kCtas>
+__global__ void __launch_bounds__(2 * D, kCtas) flat_join_kernel(const JoinParams p) {
   constexpr bool kByRow = sizeof(T) == 4;
+  constexpr int kThreads_ = 2 * D, kWarps = kThreads_ / 32;
+  __shared__ Split s_split[kMaxParts];
+  __shared__ int s_first[kMaxParts], s_count[kMaxParts / 32];  // the CTAs that left one, in order
+  __shared__ float s_w[kMaxParts][8];  // the pieces' weights
+  __shared__ float s_top[kWarps][8], s_sum[kWarps][8];
+  __shared__ OwnWeight s_own[8];
   const AttnParams& a = p.a;
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int my_row = kByRow ? tid >> 5 : tid & 7, chan = (kByRow ? lane : tid >> 3) * E;
-  auto load_own = [&](size_t r, float* y, float& L) {
-    if (!p.own_lse) {
-      L = -INFINITY;
-      return;
-    }
-    L = p.own_lse[r];
-    const T* own = static_cast<const T*>(p.own_out) + r * D + chan;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // element e of this thread's four: row and channel
+  auto row_of = [&](int e) { return kByRow ? tid / (D / 4) : (tid & 1) * 4 + e; };
+  auto chan_of = [&](int e) { return kByRow ? tid % (D / 4) * 4 + e : tid >> 1; };
+  // the eight rows from `first` of the unit (rows of the arrays: at(row)), O in o;
+  // s_own holds their factors
+  auto load_own = [&](int first, int rows, auto&& at, float* own) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) y[e] = (float)own[e];
+    for (int e = 0; e < 4; ++e)
+      own[e] = p.own_out && first + row_of(e) < rows ? (float)static_cast<const T*>(p.own_out)[at(first + row_of(e)) * D + chan_of(e)] : 0.f;
   };
-  // O = o with its statistics, and the own result, to row r of the arrays; the
-  // threads of a row have read own_lse, which lse may be, before one of them writes it
-  auto finish = [&](bool live, size_t r, float M, float l, const float* o, const float* own, float L) {
-    OwnWeight w;
-    if (live) {
-      w = own_weight(M, l, L);
-      const float pre = w.prefix * a.v_scale;
-      float y[E];
+  auto store = [&](int first, int rows, auto&& at, const float* o, const float* own) {
+    float y[4];
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        y[e] = w.own == 0.f ? o[e] * pre : w.prefix == 0.f ? own[e] : fmaf(own[e], w.own, o[e] * pre);
-      T* dst = static_cast<T*>(a.out) + r * D + chan;
-#pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        if constexpr (kByRow)
-          *reinterpret_cast<float2*>(dst + e) = make_float2(y[e], y[e + 1]);
-        else
-          *reinterpret_cast<uint32_t*>(dst + e) = pack16<false>(y[e], y[e + 1]);
-      }
+    for (int e = 0; e < 4; ++e) {
+      const int row = row_of(e);
+      if (first + row >= rows) continue;
+      const OwnWeight w = s_own[row];
+      y[e] = o[e] * (w.prefix * a.v_scale);
+      if (w.own != 0.f) y[e] = w.prefix == 0.f ? own[e] : fmaf(own[e], w.own, y[e]);
+      if constexpr (!kByRow) static_cast<T*>(a.out)[at(first + row) * D + chan_of(e)] = (T)y[e];
     }
-    __syncthreads();
-    if (live && a.lse && chan == 0) a.lse[r] = w.lse;
+    if constexpr (kByRow) {
+      if (first + row_of(0) < rows)
+        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at(first + row_of(0)) * D + chan_of(0)) =
+            make_float4(y[0], y[1], y[2], y[3]);
+    }
   };
   pdl_wait();
   pdl_trigger();
@@ -2653,115 +2696,125 @@ __global__ void __launch_bounds__(256) flat_join_kernel(const JoinParams p) {
     bool falls = false;
     for (int base = 0; base < a.B; base += 32) falls = __any_sync(0xffffffffu, load_groups(a, base, p.tpu, false).falls) || falls;
     if (falls) return;
+    const float none[4] = {};
     for (int base = 0; base < a.B; base += 32) {
       const Groups g = load_groups(a, base, p.tpu, false);
       unsigned m = __ballot_sync(0xffffffffu, g.n > 0 && g.len == 0);
       if (a.B == 1) m &= 1u;
       for (; m; m &= m - 1) {
         const int src = __ffs((int)m) - 1;
-        const long long rows = (long long)__shfl_sync(0xffffffffu, g.n, src) * a.Hq;
-        const size_t r0 = (size_t)__shfl_sync(0xffffffffu, g.c0, src) * a.Hq;
-        for (long long r = 0; r < rows; r += 8) {
-          const bool live = r + my_row < rows;
-          float none[E], own[E], L = 0.f;
-#pragma unroll
-          for (int e = 0; e < E; ++e) none[e] = own[e] = 0.f;
-          if (live) load_own(r0 + (size_t)r + my_row, own, L);
-          finish(live, r0 + (size_t)r + my_row, -INFINITY, 0.f, none, own, L);
+        const size_t r0 = (size_t)__shfl_sync(0xffffffffu, g.c0, src) * a.Hq, n = (size_t)__shfl_sync(0xffffffffu, g.n, src) * a.Hq;
+        for (size_t r = r0; r < r0 + n; r += 8) {
+          const int rows = (int)min((size_t)8, r0 + n - r);
+          __syncthreads();
+          if (tid < rows) {
+            s_own[tid] = own_weight(-INFINITY, 0.f, p.own_lse ? p.own_lse[r + tid] : -INFINITY);
+            if (a.lse) a.lse[r + tid] = s_own[tid].lse;
+          }
+          __syncthreads();
+          float own[4];
+          load_own(0, rows, [&](int row) { return r + row; }, own);
+          store(0, rows, [&](int row) { return r + row; }, none, own);
         }
       }
     }
     return;
   }
-  // every warp walks the units' chunks of eight rows: this CTA's are numbers
+  // this CTA's chunks of eight rows, of slot_rows / 8 of each split: numbers
   // blockIdx.x, + gridDim.x - 1, ..
-  int want = (int)blockIdx.x, before = 0;
-  for (int base0 = 0; base0 < p.ctas; base0 += 160) {
-    Split sp[5];
-    int end[5];
-#pragma unroll
-    for (int i = 0; i < 5; ++i) {
-      sp[i] = Split{0, 0, 0, 0};
-      if (base0 + 32 * i + lane < p.ctas) {
-        const int4 v = __ldcg(reinterpret_cast<const int4*>(p.splits + base0 + 32 * i + lane));
-        sp[i] = Split{v.x, v.y, v.z, v.w};
-      }
-      end[i] = (sp[i].rows + 7) / 8;
+  const int of_split = p.slot_rows / 8;
+  const int sets = (p.ctas + 31) / 32;
+  for (int x = warp; x < sets; x += kWarps) {
+    const int c = x * 32 + lane;
+    Split u = {0, 0, 0, 0};
+    if (c < p.ctas) {
+      const int4 v = __ldcg(reinterpret_cast<const int4*>(p.splits + c));
+      u = Split{v.x, v.y, v.z, v.w};
     }
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1)
-#pragma unroll
-      for (int i = 0; i < 5; ++i) {
-        const int x = __shfl_up_sync(0xffffffffu, end[i], d);
-        if (lane >= d) end[i] += x;
-      }
-    // (the chunks of sp[0] come first, and so on)
-    int all[5];
-#pragma unroll
-    for (int i = 0; i < 5; ++i) all[i] = __shfl_sync(0xffffffffu, end[i], 31) + (i ? all[i - 1] : 0);
+    s_split[c] = u;
+    const unsigned has = __ballot_sync(0xffffffffu, u.rows > 0);
+    s_w[x][0] = __uint_as_float(has);
+    if (lane == 0) s_count[x] = __popc(has);
+  }
+  __syncthreads();
+  int splits = 0;
+  for (int x = 0; x < sets; ++x) {
+    if (x % kWarps == warp) {
+      const unsigned has = __float_as_uint(s_w[x][0]);
+      if (has >> lane & 1u) s_first[splits + __popc(has & ((1u << lane) - 1u))] = x * 32 + lane;
+    }
+    splits += s_count[x];
+  }
+  __syncthreads();
 #pragma unroll 1
-    while (want < before + all[4]) {
-      Split mine = sp[0];
-      int last = end[0], base = base0, skipped = 0;
+  for (int it = (int)blockIdx.x; it < splits * of_split; it += (int)gridDim.x - 1) {
+    const int n = it / of_split, chunk = it - n * of_split, c0 = s_first[n];
+    const Split u = s_split[c0];
+    const int rows = u.rows, pieces = u.last - c0 + 1, h = u.h, tok0 = u.tok0;
+    const int row0 = chunk * 8;
+    if (row0 >= rows) continue;
+    auto to = [&](int row) {
+      const int of_token = row / p.g;
+      return ((size_t)tok0 + of_token) * a.Hq + h * p.g + (row - of_token * p.g);
+    };
+    // the unit's first piece is in slot 2 c0 + 1, the others in 2 (c0 + 1), 2 (c0 + 2), ..
+    auto slot = [&](int x) { return (size_t)(2 * (c0 + x) + (x == 0 ? 1 : 0)) * p.slot_rows + row0; };
+    float4 f[kBatch];
 #pragma unroll
-      for (int i = 1; i < 5; ++i)
-        if (want >= before + all[i - 1]) mine = sp[i], last = end[i], base = base0 + 32 * i, skipped = all[i - 1];
-      const int n = want - before - skipped, src = __ffs((int)__ballot_sync(0xffffffffu, last > n)) - 1, c0 = base + src;
-      Split u;
-      u.rows = __shfl_sync(0xffffffffu, mine.rows, src);
-      u.last = __shfl_sync(0xffffffffu, mine.last, src);
-      u.h = __shfl_sync(0xffffffffu, mine.h, src);
-      u.tok0 = __shfl_sync(0xffffffffu, mine.tok0, src);
-      const int row = (n - (__shfl_sync(0xffffffffu, last, src) - (u.rows + 7) / 8)) * 8 + my_row;
-      want += (int)gridDim.x - 1;
-      const bool live = row < u.rows;
-      const size_t r = ((size_t)u.tok0 + row / p.g) * a.Hq + u.h * p.g + row % p.g;
-      float l = 0.f, M = -INFINITY, L = 0.f, o[E], own[E];
+    for (int i = 0; i < kBatch; ++i)
+      if (i < pieces) f[i] = __ldcg(reinterpret_cast<const float4*>(p.o + slot(i) * D) + tid);
+    float L = -INFINITY, own[4];
+    load_own(row0, rows, to, own);
+    if (tid < 8 && row0 + tid < rows && p.own_lse) L = p.own_lse[to(row0 + tid)];
+    // the weights: thread (x, row) = (tid / 8, tid % 8) of pieces x, x + 2 D / 8, ..
+    const int row = tid & 7;
+    float sum = 0.f;
+    const bool mine = tid >> 3 < pieces;
+    const float2 ml = mine ? __ldcg(p.ml + slot(tid >> 3) + row) : make_float2(-INFINITY, 0.f);
+    float top = ml.x;
+    for (int x = (tid >> 3) + 2 * D / 8; x < pieces; x += 2 * D / 8) top = fmaxf(top, __ldcg(p.ml + slot(x) + row).x);
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+    if (lane < 8) s_top[warp][lane] = top;
+    __syncthreads();
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = own[e] = 0.f;
-      if (live) load_own(r, own, L);
-      for (int x0 = c0; live && x0 <= u.last; x0 += kBatch) {
-        float2 ml[kBatch];
-        float f[kBatch][E];
+    for (int x = 0; x < kWarps; ++x) top = fmaxf(top, s_top[x][row]);
+    auto weigh = [&](int x, float2 v) {
+      // a piece without a key that counts has zeros, or a NaN to pass on
+      const float w = v.x == -INFINITY ? 1.f : ex2_approx(v.x - top);
+      s_w[x][row] = w;
+      sum = fmaf(w, v.y, sum);
+    };
+    if (mine) weigh(tid >> 3, ml);
+    for (int x = (tid >> 3) + 2 * D / 8; x < pieces; x += 2 * D / 8) weigh(x, __ldcg(p.ml + slot(x) + row));
+    sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+    if (lane < 8) s_sum[warp][lane] = sum;
+    __syncthreads();
+    if (tid < 8 && row0 + tid < rows) {
+      sum = s_sum[0][tid];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int x = x0 + i;
-          ml[i] = make_float2(-INFINITY, 0.f);
-          if (x > u.last) continue;
-          const size_t slot = (size_t)(2 * x + (x == c0 ? 1 : 0));
-          ml[i] = __ldcg(p.ml + slot * p.slot_rows + row);
-          if constexpr (kByRow) {
-#pragma unroll
-            for (int e = 0; e < E; e += 2) {
-              const float2 v = __ldcg(reinterpret_cast<const float2*>(p.o + (slot * p.slot_rows + row) * D + chan + e));
-              f[i][e] = v.x, f[i][e + 1] = v.y;
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < E; ++e) f[i][e] = __ldcg(p.o + (slot * D + chan + e) * p.slot_rows + row);
-          }
-        }
-        float top = M;
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) top = fmaxf(top, ml[i].x);
-        const float ref = top == -INFINITY ? 0.f : top, down = ex2_approx(M - ref);
-        M = top;
-        l *= down;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] *= down;
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          if (x0 + i > u.last) continue;
-          // a piece without a key that counts has zeros, or a NaN to pass on
-          const float w = ml[i].x == -INFINITY ? 1.f : ex2_approx(ml[i].x - ref);
-          l = fmaf(w, ml[i].y, l);
-#pragma unroll
-          for (int e = 0; e < E; ++e) o[e] = fmaf(w, f[i][e], o[e]);
-        }
-      }
-      finish(live, r, M, l, o, own, L);
+      for (int x = 1; x < kWarps; ++x) sum += s_sum[x][tid];
+      s_own[tid] = own_weight(top, sum, L);
+      if (a.lse) a.lse[to(row0 + tid)] = s_own[tid].lse;  // (this thread alone read own_lse, which it may be)
     }
-    before += all[4];
+    float o[4] = {};
+    for (int x0 = 0; x0 < pieces; x0 += kBatch) {
+      if (x0) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+          if (x0 + i < pieces) f[i] = __ldcg(reinterpret_cast<const float4*>(p.o + slot(x0 + i) * D) + tid);
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (x0 + i < pieces) {
+          const float v[4] = {f[i].x, f[i].y, f[i].z, f[i].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[e] = fmaf(s_w[x0 + i][row_of(e)], v[e], o[e]);
+        }
+    }
+    __syncthreads();
+    store(row0, rows, to, o, own);
   }
 }
 
@@ -2883,7 +2936,7 @@ FlatShape flat_shape(int T, int Hq, int Hkv, int D, Path path, bool one_tile = f
   const Shape x = attn_shape(1, T, Hq, Hkv, D, path);
   s.g = x.g, s.tpt = x.tpt, s.ctas = x.ctas;
   s.tpu = one_tile ? x.tpt : x.tpu;
-  s.rows = (int)round_up(std::min(s.tpu, T) * s.g, 8);  // (whole sectors of eight rows)
+  s.rows = (int)round_up(std::min(s.tpu, T) * s.g, 8);  // (the join takes eight at a time)
   s.off_ml = round_up(sizeof(Split) * (size_t)s.ctas, 256);
   s.off_o = round_up(s.off_ml + sizeof(float2) * 2 * (size_t)s.ctas * s.rows, 256);
   s.total = s.off_o + sizeof(float) * 2 * (size_t)s.ctas * s.rows * D + 256;
@@ -2907,11 +2960,15 @@ struct Own {
 template <int D, typename T>
 int flat_join(const AttnParams& a, const Own& own, const FlatShape& sh, const FlatWs& w, cudaStream_t s) {
   const JoinParams jp = {a, sh.g, sh.tpu, sh.rows, sh.ctas, w.splits, w.ml, w.o, own.out, own.lse};
-  // as many CTAs as there can be chunks of eight rows, four to an SM at most
+  // CTAs for the chunks of eight rows that there can be
   const int sms = std::max(1, sm_count());
-  const long long units = ((long long)a.T / sh.tpu + std::min(a.B, a.T)) * a.Hkv;
-  const int chunks = (int)std::min<long long>(std::min<long long>(units, sh.ctas) * (sh.rows / 8), 8 * sms);
-  launch(flat_join_kernel<D, T>, chunks + 1, 256, 0, s, jp);
+  const long long units = ((long long)a.T + (long long)std::min(a.B, a.T) * (sh.tpu - 1)) / sh.tpu * a.Hkv;
+  const long long chunks = std::min<long long>(units, sh.ctas) * (sh.rows / 8);
+  constexpr int kFew = 2, kMany = 640 / D;
+  if (chunks <= (long long)kFew * sms)
+    launch(flat_join_kernel<D, T, 20, 256 / D>, (int)chunks + 1, 2 * D, 0, s, jp);
+  else
+    launch(flat_join_kernel<D, T, 2, kMany>, (int)std::min<long long>(chunks, kMany * sms) + 1, 2 * D, 0, s, jp);
   note_launch(2);
   return last_launch_status();
 }
@@ -2920,6 +2977,7 @@ int flat_launch_tc(const AttnParams& a, const Own& own, void* ws, cudaStream_t s
   using C = Cfg<D, KV4>;
   const FlatShape sh = flat_shape(a.T, a.Hq, a.Hkv, D, kTensor, flat_one_tile(a.T, a.Hq, a.Hkv));
   const FlatWs w = flat_ws(sh, ws);
+  if (sh.ctas > kMaxParts) return EAGLE_ERR_UNSUPPORTED;
   CUtensorMap map_q = {};
   if (!KV4 && !make_tmap_3d_bf16(&map_q, a.q, D, (uint64_t)a.Hq, (uint64_t)a.T, (uint64_t)D * 2, (uint64_t)a.q_stride * 2,
                                  64, (uint32_t)sh.g, (uint32_t)sh.tpt))
@@ -2933,6 +2991,7 @@ template <int D, int RT>
 int flat_launch_f32(const AttnParams& a, const Own& own, void* ws, cudaStream_t s) {
   const FlatShape sh = flat_shape(a.T, a.Hq, a.Hkv, D, RT == 1 ? kFp32Few : kFp32);
   const FlatWs w = flat_ws(sh, ws);
+  if (sh.ctas > kMaxParts) return EAGLE_ERR_UNSUPPORTED;
   constexpr int smem = CfgF32<D, RT>::kSmem;
   if (!allow_smem(prompt_attn_f32_kernel<D, RT, true>, smem)) return EAGLE_ERR_CUDA;
   const F32Params fp = {a, scale_log2(a), sh.g, sh.tpu, sh.rows, nullptr, nullptr, nullptr, w.ml, w.o,
