@@ -15,17 +15,26 @@
 // Where a sum passes a border (p times the sum, u times the sum) decides the
 // result, and with 10^5 entries the borders lie closer than fp32's rounding of
 // such sums.  So weights are whole numbers, w = round(2^44 e^((x - max) / T)), good
-// to 2^-37 of themselves, and their sums are exact 64-bit integers: no order of
+// to 2^-36 of themselves, and their sums are exact 64-bit integers: no order of
 // summation, no atomics' order and no split of a row changes any result.
 //
-// A row belongs to a cluster of 1 to 8 CTAs, which read it once and keep it in
-// shared memory: contiguous ranges by CTA and warp, so that running sums by index
-// are sums over ranges.  The order is never sorted as a whole.  A histogram over
-// the distance from the maximum (64 bins per octave; counts, and for top-p sums of
-// weights) finds the bin in which the k-th entry or the p-th part lies; the entries
-// up to it, when they are at most 1024, are sorted by one CTA, which finishes the
-// row.  Otherwise that bin alone is refined, until its entries are few enough to be
-// sorted or all equal; equal entries are cut by their index.
+// A row belongs to a cluster of 1 to 8 CTAs: contiguous ranges by CTA and warp, so
+// that running sums by index are sums over ranges.  Passes after the first read the
+// row from L2.  What a row costs goes by what it keeps:
+//   few entries  In the first pass every thread finds its largest entry.  With q = k / 8
+//                of a CTA's at or above a value, k entries of the row are at or above
+//                the least of the eight CTAs' values, and not many more: one comparison
+//                each in the second pass collects them.  One CTA works out the order
+//                of up to 256 by comparing all with all, sorts up to 1024, and
+//                finishes the row with their exact weights.  Top-p without top-k needs
+//                the sum over the whole row as well: the second pass adds it up in
+//                fp32, which settles the border unless the sum's error reaches across
+//                it; then the exact sum is taken.
+//   many         For a cut, a histogram over the distance from the maximum (counts, or
+//                sums of exact weights, 40 instructions each) finds the bin that it lies
+//                in, which is refined until its entries are few enough for one CTA, or
+//                equal; equal entries are cut by their index.  After a top-k the CTAs
+//                go on with the entries that they collected, otherwise with the row.
 #include <float.h>
 #include <math.h>
 
@@ -61,13 +70,17 @@ __device__ __constant__ const uint32_t kPow4096[64] = {
     2500439153u, 2546528435u, 2592609919u, 2638683604u, 2684749494u, 2730807589u, 2776857890u, 2822900400u, 2868935118u,
     2914962046u};
 
-constexpr int kNT = 512, kNW = kNT / 32;
-constexpr int kBins = 2048;
+constexpr int kNT = 256, kNW = kNT / 32;
+constexpr int kBins = 512;
 constexpr int kCap = 1024;       // entries that one CTA sorts
+constexpr int kLocal = 1536;     // entries that a CTA collects
 constexpr int kMaxVocab = 1 << 18;
 constexpr int kOne = 44;         // a weight of 1 is 2^kOne: 2^18 of them stay below 2^63
 constexpr int kLimb = 15;        // a weight's limbs in the histogram: 2^16 of them stay below 2^32
 constexpr int kMaxCluster = 8;
+// Of the row's sum in fp32, relative: an entry's exponent y <= 45 in three roundings
+// (0.7 * 3 * 45 * 2^-24), its exponential (2^-22), and up to 128 + 21 additions.
+constexpr float kSumError = 3.0517578125e-5f;
 
 struct SampleParams {
   const void* x;
@@ -88,17 +101,19 @@ struct Entry {  // of the sorted list
   unsigned long long key, w;
 };
 struct Part {  // what a CTA tells the others
-  unsigned long long v, key;
+  unsigned long long v;
   unsigned int n, flags;
 };
-struct Found {  // the bin or entry that a search ends at
+struct Found {  // the bin that a search ends at
   unsigned long long before;  // measure before it
   unsigned int bin, before_n, n, pad;
 };
-struct Cut {  // entries behind (key, idx) in the order are dropped
-  uint32_t key;
+struct Cut {  // entries behind (value, idx) in the order are dropped
+  float value;
   int idx;
 };
+enum Outcome { kDone, kNeedSum, kNeedAll };  // of a list
+enum Source { kList, kRow };                 // where a CTA's entries are
 
 // Order-preserving key of a float that is no NaN; the two zeros are equal.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -134,32 +149,48 @@ struct Weigh {
   }
 };
 
+
+// What a CTA holds of a row.
+struct Shared {
+  uint4 hist[kBins];  // counts, and three limbs of sums of weights
+  uint2 local[kLocal];  // this CTA's collected entries: (order key, index)
+  Entry list[kCap];     // the leader's list
+  float tops[kNT];      // the threads' largest
+  unsigned long long pow64[64], wv[kNW], wkey[kNW];
+  uint32_t pow4096[64], wn[kNW];
+  float wsum[kNW];
+  Part part[2][kMaxCluster];
+  Found found;
+  Cut cut;
+  Weigh weigh;
+  float bins, low, temp, top_p, u;  // bins: per distance
+  int top_k, n;
+};
+
 __device__ __forceinline__ uint32_t remote(const void* p, int rank) {
   uint32_t ra;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(smem_u32(p)), "r"(rank));
   return ra;
 }
-__device__ __forceinline__ uint32_t ld_remote(const uint32_t* p, int rank) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote(p, rank)) : "memory");
+__device__ __forceinline__ uint4 ld_remote(const uint4* p, int rank) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(remote(p, rank))
+               : "memory");
   return v;
 }
-__device__ __forceinline__ uint2 ld_remote2(const uint2* p, int rank) {
-  uint2 v;
-  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(remote(p, rank)) : "memory");
-  return v;
-}
-// 24 or 32 bytes to the same place in the shared memory of CTA `rank`.
+// whole 64-bit words to the same place in the shared memory of CTA `rank`
 template <typename S>
 __device__ __forceinline__ void st_remote(S* p, int rank, const S& v) {
   static_assert(sizeof(S) % 8 == 0, "whole 64-bit words");
-  const unsigned long long* w = reinterpret_cast<const unsigned long long*>(&v);
+  unsigned long long w[sizeof(S) / 8];
+  memcpy(w, &v, sizeof(S));
   const uint32_t ra = remote(p, rank);
 #pragma unroll
   for (int i = 0; i < (int)sizeof(S) / 8; ++i)
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(ra + 8 * i), "l"(w[i]) : "memory");
 }
-
 // barrier of the cluster after code that may have parted a warp
 __device__ __forceinline__ void cluster_sync() {
   __syncwarp();
@@ -210,505 +241,439 @@ __device__ __forceinline__ V warp_scan(V v) {  // inclusive
   }
   return v;
 }
+__device__ __forceinline__ unsigned long long warp_total(unsigned long long v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
 
+// A row, a thread's place in it, and the steps that the paths share.  The cluster is
+// the grid's x, the row its y.
 template <typename T>
-__global__ void __launch_bounds__(kNT) sample_kernel(const SampleParams p) {
-  constexpr int E = Unit<T>::E;
-  extern __shared__ __align__(16) unsigned char sm[];  // histogram, then the row's slice
-  uint32_t* hist_n = reinterpret_cast<uint32_t*>(sm);
-  uint32_t* hist_w = hist_n + kBins;                    // three limbs
-  uint2* local = reinterpret_cast<uint2*>(sm);          // this CTA's entries of the list (over hist_n)
-  Entry* list = reinterpret_cast<Entry*>(hist_w);       // the leader's sorted list
-  const uint4* slice = reinterpret_cast<const uint4*>(sm + 4 * kBins * 4);
-  static_assert(kCap * sizeof(uint2) <= 4 * kBins && kCap * sizeof(Entry) <= 12 * kBins, "the lists lie over the histogram");
-  __shared__ unsigned long long s_pow64[64], s_wv[kNW];
-  __shared__ uint32_t s_pow4096[64], s_wn[kNW];
-  __shared__ Part s_part[2][kMaxCluster];
-  __shared__ Found s_found;
-  __shared__ float s_ch, s_cl, s_low;
-  __shared__ int s_local;
+struct Row {
+  static constexpr int E = Unit<T>::E;
+  const SampleParams& p;
+  Shared& sh;
+  const T* x;
+  int lead, u0, n_units;  // elements in front of the row in its first unit; the warp's units
+  int phase;              // of sh.part: a CTA may write the next while another reads this one
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int C = (int)gridDim.x, rank = (int)blockIdx.x, row = blockIdx.y;  // the cluster is the grid's x
-  const T* tag = nullptr;
-  if (tid < 64) {
-    s_pow64[tid] = kPow64[tid];
-    s_pow4096[tid] = kPow4096[tid];
+  __device__ __forceinline__ Row(const SampleParams& p_, Shared& s, int phase_) : p(p_), sh(s), phase(phase_) {
+    x = static_cast<const T*>(p.x) + (size_t)blockIdx.y * p.stride;
+    lead = (int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
+    u0 = ((int)blockIdx.x * kNW + ((int)threadIdx.x >> 5)) * p.units;
+    n_units = max(0, min(p.units, (p.V + lead + E - 1) / E - u0));
   }
-  // no CTA writes to another's shared memory before that one runs: waited for below
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-  pdl_wait();
-  pdl_trigger();
-
-  const int rq = row / p.per;
-  const float temp = p.temp ? p.temp[rq] : 1.f, top_p = p.top_p ? p.top_p[rq] : 1.f, min_p = p.min_p ? p.min_p[rq] : 0.f;
-  const int top_k = p.top_k ? p.top_k[rq] : 0;
-  const float u = p.out ? 0.f : p.u[row];
-  const bool bad_args = !(temp >= 0.f && temp <= FLT_MAX) || !(top_p >= 0.f) || !(min_p >= 0.f && min_p <= 1.f) ||
-                        top_k < 0 || !(u >= 0.f && u < 1.f);
-
-  // ------------------------------------------------------------ the row, once
-  // 16-byte units of the row, counted from the boundary at or before it
-  const T* x = static_cast<const T*>(p.x) + (size_t)row * p.stride;
-  const int lead = (int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
-  const int u0 = (rank * kNW + warp) * p.units, ul = warp * p.units;  // the warp's first unit: of the row, of the slice
-  const int n_units = max(0, min(p.units, (p.V + lead + E - 1) / E - u0));
-  unsigned long long best = 0;  // (order key, ~index) of the largest
-  bool odd = false;             // NaN or +infinity
-  {
-    uint4* to = const_cast<uint4*>(slice) + ul;
-    float top = -INFINITY;
-    int at = 0x7fffffff;
-#pragma unroll 4
-    for (int j = lane; j < n_units; j += 32) {
-      const int i0 = (u0 + j) * E - lead;
-      uint4 v;
-      float f[E];
-      if (i0 >= 0 && i0 + E <= p.V) {
-        v = __ldcs(reinterpret_cast<const uint4*>(x + i0));
-        open_unit(v, f, tag);
-      } else {  // the row's first or last unit: what is not the row's counts as -infinity
-        alignas(16) T e[E];
+  __device__ __forceinline__ int lane() const { return threadIdx.x & 31; }
+  __device__ __forceinline__ int warp() const { return threadIdx.x >> 5; }
+  __device__ __forceinline__ int C() const { return (int)gridDim.x; }
+  __device__ __forceinline__ bool leader() const { return blockIdx.x == 0; }
+  __device__ __forceinline__ int first_of(int j) const { return (u0 + j) * E - lead; }
+  // unit j of the warp's range; what is not the row's counts as -infinity
+  __device__ __forceinline__ uint4 load(int j) const {
+    const int i0 = first_of(j);
+    if (i0 >= 0 && i0 + E <= p.V) return *reinterpret_cast<const uint4*>(x + i0);
+    alignas(16) T e[E];
 #pragma unroll
-        for (int k = 0; k < E; ++k) {
-          e[k] = i0 + k >= 0 && i0 + k < p.V ? x[i0 + k] : (T)(-INFINITY);
-          f[k] = (float)e[k];
-        }
-        v = *reinterpret_cast<const uint4*>(e);
-      }
-      to[j] = v;
-#pragma unroll
-      for (int k = 0; k < E; ++k) {
-        odd = odd || !(f[k] <= FLT_MAX);
-        if (f[k] > top) top = f[k], at = i0 + k;
-      }
-    }
-    best = (unsigned long long)order_key(top) << 32 | (uint32_t)~at;
+    for (int k = 0; k < E; ++k) e[k] = i0 + k >= 0 && i0 + k < p.V ? x[i0 + k] : (T)(-INFINITY);
+    return *reinterpret_cast<const uint4*>(e);
   }
-  int phase = 0;  // of s_part: a CTA may write the next while another reads this one
-  // Every CTA's part in s_part[..][rank] of all; returns where they are.  A barrier of the cluster.
-  auto tell = [&](const Part& mine) -> const Part* {  // the same value in threads 0 .. C - 1
-    Part* to = s_part[phase & 1];
-    ++phase;
-    if (tid < C) st_remote(&to[rank], tid, mine);
-    cluster_sync();
-    return to;
-  };
-#pragma unroll
-  for (int d = 16; d; d >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, d));
-  if (lane == 0) s_wv[warp] = best;
-  const bool any_odd = __syncthreads_or(odd);
-  {
-    best = s_wv[lane % kNW];
-#pragma unroll
-    for (int d = kNW / 2; d; d >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, d));
-    __syncwarp();
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    const Part* all = tell(Part{0, best, 0, any_odd});
-    odd = false;
-    for (int r = 0; r < C; ++r) {
-      best = max(best, all[r].key);
-      odd = odd || all[r].flags;
-    }
-  }
-  const uint32_t max_key = (uint32_t)(best >> 32);
-  const float xmax = key_value(max_key);
-  const bool leader = rank == 0;
-  if (bad_args || odd || xmax == -INFINITY) {
-    if (leader && tid == 0) {
-      set_status(p.status, bad_args ? EAGLE_ERR_INVALID_ARG : EAGLE_ERR_NONFINITE);
-      if (p.tokens) p.tokens[row] = -1;
-      if (p.logprobs) p.logprobs[row] = -INFINITY;
-      if (p.kept) p.kept[row] = 0;
-    }
-    return;
-  }
-  const bool greedy = temp == 0.f;
-  if (greedy && !p.out) {
-    if (leader && tid == 0) {
-      p.tokens[row] = (int)~(uint32_t)best;
-      if (p.logprobs) p.logprobs[row] = 0.f;
-      if (p.kept) p.kept[row] = 1;
-    }
-    return;
-  }
-  if (tid == 0) {
-    // (a temperature so small that its reciprocal overflows leaves the largest alone)
-    const double c = fmin(1.4426950408889634 / (double)(greedy ? 1.f : temp), 3.0e38);
-    s_ch = (float)c;
-    s_cl = (float)(c - (double)s_ch);
-    // w >= min_p as a border of x: the smallest fp32 number not below max + T log(min_p)
-    float low = -FLT_MAX;
-    if (min_p > 0.f) {
-      const double b = (double)xmax + (double)temp * log((double)min_p);
-      low = b <= -(double)FLT_MAX ? -FLT_MAX : __double2float_ru(b);
-    }
-    s_low = low;
-  }
-  __syncthreads();
-  const Weigh weigh{xmax, s_ch, s_cl};
-  const float low = s_low;
-  Cut cut{0u, 0x7fffffff};
-  if (greedy) cut = Cut{max_key, (int)~(uint32_t)best};
-
-  auto weight = [&](float f) { return weigh(f, s_pow64, s_pow4096); };
-  auto inside = [&](float f, int i) {  // not cut so far
-    const uint32_t k = order_key(f);
-    return f > -INFINITY && (k > cut.key || (k == cut.key && i <= cut.idx));
-  };
-  // f(value, index) for this thread's entries, in the order of indices within a lane
-  auto sweep = [&](auto&& f) {
+  // f(unit j, its values, index of its first entry) for this lane's units, in ascending
+  // order, four loads in flight
+  template <typename F>
+  __device__ __forceinline__ void sweep_units(F&& f) const {
+    constexpr int U = 4;
 #pragma unroll 1
-    for (int j = lane; j < n_units; j += 32) {
+    for (int j0 = lane(); j0 < n_units; j0 += 32 * U) {
+      uint4 v[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (j0 + 32 * i < n_units) v[i] = load(j0 + 32 * i);
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (j0 + 32 * i < n_units) f(v[i], first_of(j0 + 32 * i));
+    }
+  }
+  template <typename F>
+  __device__ __forceinline__ void sweep(F&& f) const {  // f(value, index)
+    sweep_units([&](const uint4& u, int i0) {
       float v[E];
-      open_unit(slice[ul + j], v, tag);
-      const int i0 = (u0 + j) * E - lead;
+      open_unit(u, v, (const T*)nullptr);
 #pragma unroll
       for (int k = 0; k < E; ++k) f(v[k], i0 + k);
+    });
+  }
+  // `mine`, the same in threads 0 .. C - 1, to all CTAs; returns where theirs are
+  __device__ __forceinline__ const Part* tell(const Part& mine) {
+    Part* to = sh.part[phase & 1];
+    ++phase;
+    if ((int)threadIdx.x < C()) st_remote(&to[blockIdx.x], threadIdx.x, mine);
+    cluster_sync();
+    return to;
+  }
+  __device__ __forceinline__ unsigned long long weight(float f) const { return sh.weigh(f, sh.pow64, sh.pow4096); }
+  // bin of an entry by its distance from the maximum: 511 up to where weights vanish
+  __device__ __forceinline__ int bin_of(float f) const { return min((int)((sh.weigh.xmax - f) * sh.bins), kBins - 1); }
+  // keys that bin b's entries lie between, with room for the roundings
+  __device__ __forceinline__ void keys_of(int b, uint32_t& lo, uint32_t& hi) const {
+    const float xmax = sh.weigh.xmax;
+    float from = -FLT_MAX, to = xmax;
+    if (sh.bins > 0.f && sh.bins < INFINITY) {
+      const float d0 = (float)b / sh.bins, d1 = (float)(b + 1) / sh.bins;
+      to = fminf(to, xmax - d0 + 1e-6f * (fabsf(xmax) + d0));
+      if (b < kBins - 1) from = fmaxf(from, xmax - d1 - 1e-6f * (fabsf(xmax) + d1));
     }
-  };
-  // bin of an entry by its distance d from the maximum: 64 per octave from 2^-10 to 2^22
-  auto octave_bin = [&](float f) {
-    const int b = (int)(__float_as_uint(xmax - f) >> 17) - ((127 - 10) << 6);
-    return min(max(b, 0), kBins - 1);
-  };
-  auto clear = [&]() {
-    uint4* h = reinterpret_cast<uint4*>(hist_n);
-    for (int i = tid; i < kBins; i += kNT) h[i] = make_uint4(0u, 0u, 0u, 0u);
-    __syncthreads();
-  };
-  auto add = [&](int b, bool weighted, float f) {
-    atomicAdd(&hist_n[b], 1u);
-    if (weighted) {
-      const unsigned long long w = weight(f);
-      constexpr uint32_t mask = (1u << kLimb) - 1;
-      const uint32_t w0 = (uint32_t)w & mask, w1 = (uint32_t)(w >> kLimb) & mask, w2 = (uint32_t)(w >> (2 * kLimb));
-      if (w0) atomicAdd(&hist_w[b], w0);
-      if (w1) atomicAdd(&hist_w[kBins + b], w1);
-      if (w2) atomicAdd(&hist_w[2 * kBins + b], w2);
-    }
-  };
+    lo = order_key(from);
+    hi = order_key(to);
+  }
   // Exclusive prefixes over the threads of the CTA, and the sums over all.
-  auto block_scan = [&](unsigned long long v, uint32_t n, unsigned long long& before, uint32_t& before_n,
-                        unsigned long long& all, uint32_t& all_n) {
+  __device__ __forceinline__ void block_scan(unsigned long long v, uint32_t n, unsigned long long& before, uint32_t& before_n,
+                                             unsigned long long& all, uint32_t& all_n) {
     const unsigned long long iv = warp_scan(v);
     const uint32_t in = warp_scan(n);
-    __syncthreads();  // s_wv, s_wn are free
-    if (lane == 31) s_wv[warp] = iv, s_wn[warp] = in;
+    __syncthreads();  // sh.wv, sh.wn are free
+    if (lane() == 31) sh.wv[warp()] = iv, sh.wn[warp()] = in;
     __syncthreads();
     unsigned long long o = 0, a = 0;
     uint32_t on = 0, an = 0;
 #pragma unroll
-    for (int x = 0; x < kNW; ++x) {
-      if (x < warp) o += s_wv[x], on += s_wn[x];
-      a += s_wv[x], an += s_wn[x];
+    for (int w = 0; w < kNW; ++w) {
+      if (w < warp()) o += sh.wv[w], on += sh.wn[w];
+      a += sh.wv[w], an += sh.wn[w];
     }
     before = o + iv - v;
     before_n = on + in - n;
     all = a;
     all_n = an;
-  };
-  // The bin at which the histogram's running measure (counts, or sums of weights)
-  // reaches a target: before < target <= before + bin.  target(sum) gives it from
-  // the sum of all; returns false where that is not reached.  Everyone calls it.
-  auto find_bin = [&](bool weighted, auto&& target, unsigned long long& goal, unsigned long long& sum, Found& at) -> bool {
-    cluster_sync();  // the histograms are complete
-    const int nb = kBins / C, per = max(1, nb / kNT);
-    unsigned long long v[kBins / kNT], mine = 0;
-    uint32_t n[kBins / kNT], mine_n = 0;
+  }
+  __device__ __forceinline__ void clear() {
+    for (int i = threadIdx.x; i < kBins; i += kNT) sh.hist[i] = make_uint4(0u, 0u, 0u, 0u);
+    __syncthreads();
+  }
+  __device__ __forceinline__ void add(int b, bool weighted, float f) {
+    atomicAdd(&sh.hist[b].x, 1u);
+    if (weighted) {
+      const unsigned long long w = weight(f);
+      constexpr uint32_t mask = (1u << kLimb) - 1;
+      const uint32_t w0 = (uint32_t)w & mask, w1 = (uint32_t)(w >> kLimb) & mask, w2 = (uint32_t)(w >> (2 * kLimb));
+      if (w0) atomicAdd(&sh.hist[b].y, w0);
+      if (w1) atomicAdd(&sh.hist[b].z, w1);
+      if (w2) atomicAdd(&sh.hist[b].w, w2);
+    }
+  }
+  __device__ __forceinline__ unsigned long long block_sum(unsigned long long v) {
+    v = warp_total(v);
+    __syncthreads();
+    if (lane() == 0) sh.wv[warp()] = v;
+    __syncthreads();
+    v = 0;
 #pragma unroll
-    for (int i = 0; i < kBins / kNT; ++i) {
+    for (int w = 0; w < kNW; ++w) v += sh.wv[w];
+    return v;
+  }
+  // The bin at which the cluster's running measure (counts, or sums of weights) reaches
+  // goal(sum of all): before < goal <= before + bin's.  A CTA adds up an eighth of the
+  // bins over all the histograms.  False if the goal is not reached.
+  template <typename G>
+  __device__ __forceinline__ bool find_bin(bool weighted, G&& goal_of, unsigned long long& goal, Found& at) {
+    cluster_sync();  // the histograms are complete
+    constexpr int B = kBins / kNT;
+    const int nb = kBins / C(), per = max(1, nb / kNT);
+    unsigned long long v[B], mine = 0;
+    uint32_t n[B], mine_n = 0;
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
       v[i] = 0;
       n[i] = 0;
-      const int b = tid * per + i;
-      if (i >= per || b >= nb) continue;
-      for (int r = 0; r < C; ++r) {
-        const uint32_t* h = hist_n + rank * nb + b;
-        n[i] += ld_remote(h, r);
-        if (weighted)
-          v[i] += ld_remote(h + kBins, r) + ((unsigned long long)ld_remote(h + 2 * kBins, r) << kLimb) +
-                  ((unsigned long long)ld_remote(h + 3 * kBins, r) << (2 * kLimb));
+      const int b = (int)threadIdx.x * per + i;
+      if (i < per && b < nb) {
+        uint4 h[kMaxCluster];
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+          if (r < C()) h[r] = ld_remote(&sh.hist[blockIdx.x * nb + b], r);
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+          if (r < C()) {
+            n[i] += h[r].x;
+            v[i] += weighted ? h[r].y + ((unsigned long long)h[r].z << kLimb) + ((unsigned long long)h[r].w << (2 * kLimb)) : h[r].x;
+          }
       }
-      if (!weighted) v[i] = n[i];
       mine += v[i];
       mine_n += n[i];
     }
-    unsigned long long before, all;
+    unsigned long long before, sum;
     uint32_t before_n, all_n;
-    block_scan(mine, mine_n, before, before_n, all, all_n);
-    const Part* parts = tell(Part{all, 0, all_n, 0});
+    block_scan(mine, mine_n, before, before_n, sum, all_n);
+    const Part* parts = tell(Part{sum, all_n, 0});
     sum = 0;
-    for (int r = 0; r < C; ++r) {
-      if (r < rank) before += parts[r].v, before_n += parts[r].n;
+    for (int r = 0; r < C(); ++r) {
+      if (r < (int)blockIdx.x) before += parts[r].v, before_n += parts[r].n;
       sum += parts[r].v;
     }
-    goal = target(sum);
+    goal = goal_of(sum);
     if (goal > sum) return false;
 #pragma unroll
-    for (int i = 0; i < kBins / kNT; ++i) {
+    for (int i = 0; i < B; ++i) {
       if (before < goal && goal <= before + v[i]) {
-        const Found f{before, (uint32_t)(rank * nb + tid * per + i), before_n, n[i], 0};
-        for (int r = 0; r < C; ++r) st_remote(&s_found, r, f);
+        const Found f{before, (uint32_t)(blockIdx.x * nb + threadIdx.x * per + i), before_n, n[i], 0};
+        for (int r = 0; r < C(); ++r) st_remote(&sh.found, r, f);
       }
       before += v[i];
       before_n += n[i];
     }
     cluster_sync();
-    at = s_found;
+    at = sh.found;
     return true;
-  };
-  auto sort_list = [&](int n) {  // the leader's list[0 .. n), by key ascending
+  }
+  // One entry for this CTA's local list.
+  __device__ __forceinline__ void collect(float f, int i) {
+    const int at = atomicAdd(&sh.n, 1);
+    if (at < kLocal) sh.local[at] = make_uint2(order_key(f), (uint32_t)i);
+  }
+  // list[0 .. n) of the leader by key ascending
+  __device__ __forceinline__ void sort_list(int n) {
     int n2 = 32;
     while (n2 < n) n2 <<= 1;
-    for (int i = n + tid; i < n2; i += kNT) list[i] = Entry{~0ull, 0};
+    for (int i = n + threadIdx.x; i < n2; i += kNT) sh.list[i] = Entry{~0ull, 0};
     __syncthreads();
-    for (int k = 2; k <= n2; k <<= 1)
-      for (int j = k >> 1; j; j >>= 1) {
-        for (int i = tid; i < n2 / 2; i += kNT) {
-          const int a = 2 * i - (i & (j - 1)), b = a + j;
-          const Entry ea = list[a], eb = list[b];
-          if ((ea.key > eb.key) == ((a & k) == 0)) list[a] = eb, list[b] = ea;
+    // up to 64 entries one warp does it, without the CTA's barriers
+    const bool alone = n2 <= 64;
+    if (!alone || warp() == 0) {
+      const int step = alone ? 32 : kNT;
+      for (int k = 2; k <= n2; k <<= 1)
+        for (int j = k >> 1; j; j >>= 1) {
+          for (int i = threadIdx.x; i < n2 / 2; i += step) {
+            const int a = 2 * i - (i & (j - 1)), b = a + j;
+            const Entry ea = sh.list[a], eb = sh.list[b];
+            if ((ea.key > eb.key) == ((a & k) == 0)) sh.list[a] = eb, sh.list[b] = ea;
+          }
+          if (alone)
+            __syncwarp();
+          else
+            __syncthreads();
         }
-        __syncthreads();
-      }
-  };
-  // The entries with take(value, index), at most kCap, in this CTA's local list and
-  // then all CTAs' in the leader's, best first.  Everyone calls it; the leader's
-  // result is their number.
-  auto gather = [&](auto&& take) -> int {
+    }
     __syncthreads();
-    if (tid == 0) s_local = 0;
+  }
+  // All CTAs' local lists (sh.n entries each) in the leader's: the number of entries,
+  // in all CTAs; over kCap nothing is sent (most: the largest local list).  Whole CTAs
+  // call it.
+  __device__ __forceinline__ int gather(unsigned long long v, unsigned long long& sum, int& most) {
     __syncthreads();
-    sweep([&](float f, int i) {
-      if (take(f, i)) {
-        const int at = atomicAdd(&s_local, 1);
-        if (at < kCap) local[at] = make_uint2(order_key(f), (uint32_t)i);
-      }
-    });
-    __syncthreads();
-    const Part* parts = tell(Part{0, 0, (unsigned)min(s_local, kCap), 0});
-    int n = 0;
-    if (leader) {
-      for (int r = 0; r < C; ++r) {
-        const int m = (int)parts[r].n;
-        for (int i = tid; i < m && n + i < kCap; i += kNT) {
-          const uint2 e = ld_remote2(&local[i], r);
-          list[n + i] = Entry{(unsigned long long)~e.x << 32 | e.y, weight(key_value(e.x))};
-        }
-        n = min(n + m, kCap);
-      }
+    const int mine = sh.n;
+    const Part* parts = tell(Part{v, (unsigned)mine, 0});
+    int n = 0, at = 0;
+    sum = 0;
+    most = 0;
+    for (int r = 0; r < C(); ++r) {
+      const int m = (int)parts[r].n;
+      if (r < (int)blockIdx.x) at += m;
+      most = max(most, m);
+      n += m;  // (262144 at most)
+      sum += parts[r].v;
+    }
+    if (n > kCap) return n;
+    for (int i = threadIdx.x; i < mine; i += kNT) {
+      const uint2 e = sh.local[i];
+      st_remote(&sh.list[at + i], 0, Entry{(unsigned long long)~e.x << 32 | e.y, weight(key_value(e.x))});
     }
     cluster_sync();
-    if (leader) sort_list(n);
     return n;
-  };
-  auto entry_value = [&](const Entry& e) { return key_value(~(uint32_t)(e.key >> 32)); };
-  auto finish = [&](float f, int i, unsigned long long sum, uint32_t kept) {  // one thread: the drawn token
-    p.tokens[row] = i;
-    if (p.kept) p.kept[row] = (int)kept;
-    if (p.logprobs) {
-      // -(xmax - x) / T - log(sum), the sum as 1 (the largest entry, which is always kept) and the rest
-      p.logprobs[row] = -(xmax - f) / temp - log1pf((float)(sum - (1ull << kOne)) * 5.684341886080802e-14f);
+  }
+  // The leader, of a list of at most kNT entries: `lanes` neighbouring threads have entry
+  // i (< n), and compare it with all.  key is its key with `turn` applied; before: the
+  // measure of the entries of lower keys, rank: their number.
+  template <typename K, typename W>
+  __device__ __forceinline__ void among(int n, int lanes, int i, unsigned long long key, K&& key_of, W&& measure, uint32_t& rank,
+                                        unsigned long long& before) const {
+    rank = 0;
+    before = 0;
+    for (int j = (int)threadIdx.x & (lanes - 1); j < n; j += lanes) {
+      const Entry e = sh.list[j];
+      if (key_of(e.key) < key) {
+        ++rank;
+        before += measure(e);
+      }
     }
-  };
-
-  // ------------------------------------------------------------ top-k, top-p
-  bool done = false;     // the leader has drawn the token
-  bool settled = false;  // the cut is final
-  const bool use_k = !greedy && top_k > 0 && top_k < p.V, use_p = !greedy && top_p < 1.f;
-#pragma unroll 1
-  for (int stage = 0; stage < 2 && !done && !settled; ++stage) {
-    const bool by_w = stage == 1;
-    if (by_w ? !use_p : !use_k) continue;
-    clear();
-    sweep([&](float f, int i) {
-      if (inside(f, i)) add(octave_bin(f), by_w, f);
-    });
-    unsigned long long goal = 0, sum = 0;
-    Found at;
-    auto target = [&](unsigned long long s) -> unsigned long long {
-      if (!by_w) return (unsigned long long)top_k;
-      bool rest;  // kept while before < p s: up to the entry that reaches ceil(p s), the first at least
-      const unsigned long long g = scaled(top_p, s, rest);
-      return max(1ull, g + (rest ? 1 : 0));
-    };
-    if (!find_bin(by_w, target, goal, sum, at)) continue;  // fewer than k entries
-    const int bin1 = (int)at.bin;
-    if (at.before_n + at.n <= kCap) {
-      // the list holds all that is kept: the leader finishes the row
-      const int n = gather([&](float f, int i) { return inside(f, i) && octave_bin(f) <= bin1; });
-      if (leader) {
-        // each thread has two neighbours of the sorted list
-        static_assert(kCap == 2 * kNT, "two entries a thread");
-        unsigned long long w0, w1, before, all;
-        uint32_t bn, an;
-        const bool h0 = 2 * tid < n, h1 = 2 * tid + 1 < n;
-        const float f0 = h0 ? entry_value(list[2 * tid]) : 0.f, f1 = h1 ? entry_value(list[2 * tid + 1]) : 0.f;
-        const bool k0 = h0 && (by_w || 2 * tid < top_k), k1 = h1 && (by_w || 2 * tid + 1 < top_k);
-        w0 = k0 ? list[2 * tid].w : 0;
-        w1 = k1 ? list[2 * tid + 1].w : 0;
-        block_scan(w0 + w1, 0, before, bn, all, an);
-        unsigned long long lim = ~0ull;
-        if (by_w)
-          lim = goal;
-        else if (use_p) {
-          bool rest;
-          const unsigned long long g = scaled(top_p, all, rest);
-          lim = max(1ull, g + (rest ? 1 : 0));
-        }
-        const bool y0 = k0 && before < lim && f0 >= low, y1 = k1 && before + w0 < lim && f1 >= low;
-        block_scan((y0 ? w0 : 0) + (y1 ? w1 : 0), (y0 ? 1u : 0u) + (y1 ? 1u : 0u), before, bn, all, an);
-        const int m = (int)an;  // the first m of the list are kept
-        if (p.out) {
-          if (tid == 0) {
-            const Entry e = list[m - 1];
-            const Cut c{~(uint32_t)(e.key >> 32), (int)(uint32_t)e.key};
-            const Found f{0, c.key, (uint32_t)c.idx, (uint32_t)m, 0};
-            for (int r = 0; r < C; ++r) st_remote(&s_found, r, f);
-          }
-        } else {
-          __syncthreads();
-          for (int i = tid; i < m; i += kNT) list[i].key = list[i].key << 32 | list[i].key >> 32;  // by index
-          sort_list(m);
-          bool rest;
-          const unsigned long long t = scaled(u, all, rest);
-          const unsigned long long a = 2 * tid < m ? list[2 * tid].w : 0, b = 2 * tid + 1 < m ? list[2 * tid + 1].w : 0;
-          unsigned long long s;
-          block_scan(a + b, 0, before, bn, s, an);
-          int hit = -1;
-          if (before <= t && t < before + a) hit = 2 * tid;
-          if (before + a <= t && t < before + a + b) hit = 2 * tid + 1;
-          if (hit >= 0) {
-            const Entry e = list[hit];
-            finish(key_value(~(uint32_t)e.key), (int)(e.key >> 32), all, (uint32_t)m);
-          }
-        }
-      }
-      if (!p.out) {
-        done = true;
-      } else {
-        cluster_sync();
-        cut = Cut{s_found.bin, (int)s_found.before_n};
-        settled = true;
-      }
-      continue;
-    }
-    // refine the bin: keys of its entries lie in [lo, hi], with room for the
-    // rounding of the distance
-    const float d0 = bin1 ? __uint_as_float((uint32_t)(bin1 + ((127 - 10) << 6)) << 17) : 0.f;
-    const float d1 = bin1 < kBins - 1 ? __uint_as_float((uint32_t)(bin1 + 1 + ((127 - 10) << 6)) << 17) : INFINITY;
-    const float slack = (fabsf(xmax) + d0) * 2.4e-7f;
-    uint32_t hi = min(max_key, order_key(fminf(xmax - d0 + slack, FLT_MAX)));
-    uint32_t lo = order_key(fmaxf(xmax - d1 - 2.f * slack, -FLT_MAX));
-    unsigned long long before = at.before;
-    uint32_t n_bin = at.n;
-    auto member = [&](float f, int i) {
-      const uint32_t k = order_key(f);
-      return k >= lo && k <= hi && octave_bin(f) == bin1 && inside(f, i);
-    };
-    while (n_bin > kCap && lo < hi) {
-      const int shift = max(0, 32 - __clz((int)(hi - lo)) - 11);
-      clear();
-      sweep([&](float f, int i) {
-        if (member(f, i)) add((int)((hi - order_key(f)) >> shift), by_w, f);
-      });
-      unsigned long long s;
-      auto rest = [&](unsigned long long) { return goal - before; };
-      unsigned long long g;
-      Found in;
-      find_bin(by_w, rest, g, s, in);
-      before += in.before;
-      n_bin = in.n;
-      const uint32_t top = hi - (in.bin << shift);
-      const uint32_t width = (1u << shift) - 1;
-      lo = top - lo > width ? top - width : lo;
-      hi = top;
-    }
-    if (n_bin <= kCap) {
-      const int n = gather(member);
-      if (leader) {
-        const unsigned long long w0 = 2 * tid < n ? (by_w ? list[2 * tid].w : 1) : 0;
-        const unsigned long long w1 = 2 * tid + 1 < n ? (by_w ? list[2 * tid + 1].w : 1) : 0;
-        unsigned long long b, all;
-        uint32_t bn, an;
-        block_scan(w0 + w1, 0, b, bn, all, an);
-        b += before;
-        int hit = -1;
-        if (b < goal && goal <= b + w0) hit = 2 * tid;
-        if (b + w0 < goal && goal <= b + w0 + w1) hit = 2 * tid + 1;
-        if (hit >= 0) {
-          const Entry e = list[hit];
-          const Found f{0, ~(uint32_t)(e.key >> 32), (uint32_t)e.key, 0, 0};
-          for (int r = 0; r < C; ++r) st_remote(&s_found, r, f);
-        }
-      }
-      cluster_sync();
-      cut = Cut{s_found.bin, (int)s_found.before_n};
-    } else {
-      // equal entries: the c-th by index is the last
-      const unsigned long long each = by_w ? weight(key_value(lo)) : 1ull;
-      const unsigned long long c = (goal - before + each - 1) / each;
-      uint32_t n = 0;
-      sweep([&](float f, int i) { n += member(f, i) ? 1u : 0u; });
-      n = __reduce_add_sync(0xffffffffu, n);
-      __syncthreads();
-      if (lane == 0) s_wn[warp] = n;
-      __syncthreads();
-      uint32_t all = 0, off = 0;
-      for (int x = 0; x < kNW; ++x) {
-        if (x < warp) off += s_wn[x];
-        all += s_wn[x];
-      }
-      const Part* parts = tell(Part{0, 0, all, 0});
-      for (int r = 0; r < rank; ++r) off += parts[r].n;
-      if (off < c && c <= (unsigned long long)off + n) {  // this warp's range holds it
-#pragma unroll 1
-        for (int j0 = 0; j0 < n_units; j0 += 32) {
-          const int j = j0 + lane;
-          float v[E];
-          uint32_t m = 0;
-          const int i0 = (u0 + j) * E - lead;
-          if (j < n_units) {
-            open_unit(slice[ul + j], v, tag);
-#pragma unroll
-            for (int k = 0; k < E; ++k) m += member(v[k], i0 + k) ? 1u : 0u;
-          }
-          const uint32_t in = warp_scan(m);
-          uint32_t at_ = off + in - m;
-          if (j < n_units && at_ < c && c <= (unsigned long long)at_ + m) {
-#pragma unroll
-            for (int k = 0; k < E; ++k)
-              if (member(v[k], i0 + k) && ++at_ == c) {
-                const Found f{0, lo, (uint32_t)(i0 + k), 0, 0};
-                for (int r = 0; r < C; ++r) st_remote(&s_found, r, f);
-              }
-          }
-          off += __shfl_sync(0xffffffffu, in, 31);
-        }
-      }
-      cluster_sync();
-      cut = Cut{s_found.bin, (int)s_found.before_n};
+    for (int d = 1; d < lanes; d <<= 1) {
+      rank += __shfl_xor_sync(0xffffffffu, rank, d);
+      before += __shfl_xor_sync(0xffffffffu, before, d);
     }
   }
-  if (done) return;
-
-  // ------------------------------------------------------------ the whole row
-  auto keep = [&](float f, int i) { return f >= low && inside(f, i); };
-  if (p.out) {
+  __device__ __forceinline__ int lanes_of(int n) const { return n <= kNT / 8 ? 8 : n <= kNT / 4 ? 4 : n <= kNT / 2 ? 2 : 1; }
+  __device__ __forceinline__ Cut cut_of(unsigned long long key) const {
+    return Cut{key_value(~(uint32_t)(key >> 32)), (int)(uint32_t)key};
+  }
+  __device__ __forceinline__ void send_cut(const Cut& c) {
+    for (int r = 0; r < C(); ++r) st_remote(&sh.cut, r, c);
+  }
+  // The leader: the entry of its list at which the measure, from `before` on, reaches
+  // goal, as the cut in all CTAs.
+  __device__ __forceinline__ void cut_list(int n, bool weighted, unsigned long long before, unsigned long long goal) {
+    if (n <= kNT) {
+      const int lanes = lanes_of(n), i = (int)threadIdx.x / lanes;
+      const Entry e = i < n ? sh.list[i] : Entry{0, 0};
+      uint32_t rank;
+      unsigned long long b;
+      among(n, lanes, i, e.key, [](unsigned long long k) { return k; },
+            [&](const Entry& x) { return weighted ? x.w : 1ull; }, rank, b);
+      b += before;
+      if (i < n && threadIdx.x % lanes == 0 && b < goal && goal <= b + (weighted ? e.w : 1ull)) send_cut(cut_of(e.key));
+      return;
+    }
+    sort_list(n);
+    constexpr int K = kCap / kNT;
+    const int i0 = (int)threadIdx.x * K;
+    unsigned long long w[K], mine = 0, b, all;
+    uint32_t bn, an;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      w[k] = i0 + k < n ? (weighted ? sh.list[i0 + k].w : 1ull) : 0;
+      mine += w[k];
+    }
+    block_scan(mine, 0, b, bn, all, an);
+    b += before;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (b < goal && goal <= b + w[k]) send_cut(cut_of(sh.list[i0 + k].key));
+      b += w[k];
+    }
+  }
+  // one thread: the drawn token
+  __device__ __forceinline__ void finish(float f, int i, unsigned long long sum, uint32_t kept) const {
+    const int row = blockIdx.y;
+    p.tokens[row] = i;
+    if (p.kept) p.kept[row] = (int)kept;
+    // -(xmax - x) / T - log(sum), the sum as 1 (the largest entry, which is always kept) and the rest
+    if (p.logprobs)
+      p.logprobs[row] = -(sh.weigh.xmax - f) / sh.temp - log1pf((float)(sum - (1ull << kOne)) * 5.684341886080802e-14f);
+  }
+  __device__ __forceinline__ unsigned long long part_of(unsigned long long sum) const {
+    bool rest;  // kept while before < p sum: up to the entry that reaches ceil(p sum), the first at least
+    const unsigned long long g = scaled(sh.top_p, sum, rest);
+    return max(1ull, g + (rest ? 1 : 0));
+  }
+  // The leader: what is kept of its list, which holds all that may be, cut by top_k (0:
+  // no cut) and top-p between the limits lo and hi (0: of the list's own sum; ~0: no
+  // cut).  Draws the token, or leaves the cut in all CTAs' sh.cut.
+  __device__ __forceinline__ Outcome use_list(int n, int top_k, unsigned long long lo, unsigned long long hi) {
+    return n <= kNT ? use_short_list(n, top_k, lo, hi) : use_long_list(n, top_k, lo, hi);
+  }
+  __device__ __forceinline__ Outcome use_short_list(int n, int top_k, unsigned long long lo, unsigned long long hi) {
+    const int lanes = lanes_of(n), i = (int)threadIdx.x / lanes;
+    const bool mine = i < n && threadIdx.x % lanes == 0;
+    const Entry e = i < n ? sh.list[i] : Entry{0, 0};
+    uint32_t rank;
+    unsigned long long before;
+    among(n, lanes, i, e.key, [](unsigned long long k) { return k; }, [](const Entry& x) { return x.w; }, rank, before);
+    const bool in = mine && (top_k == 0 || (int)rank < top_k);
+    unsigned long long all = 0;
+    if (hi != ~0ull) {
+      all = block_sum(in ? e.w : 0);
+      if (lo == 0) lo = hi = part_of(all);
+      if (all < hi) return kNeedAll;
+    }
+    const bool above = cut_of(e.key).value >= sh.low;
+    const bool k_lo = in && above && before < lo, k_hi = in && above && before < hi;
+    unsigned long long none, sum;
+    uint32_t bn, an;
+    block_scan(k_lo ? e.w : 0, (k_lo ? 1u : 0u) + (k_hi ? 0x10000u : 0u), none, bn, sum, an);
+    const int m = (int)(an & 0xffffu);
+    if (m != (int)(an >> 16)) return kNeedSum;
+    if (p.out) {
+      if (k_lo && (int)rank == m - 1) {
+        send_cut(cut_of(e.key));
+        if (p.kept) p.kept[blockIdx.y] = m;
+      }
+      return kDone;
+    }
+    // the kept entries by index
+    if (mine && !k_lo) sh.list[i].w = 0;
+    __syncthreads();
+    bool rest;
+    const unsigned long long t = scaled(sh.u, sum, rest);
+    auto index = [](unsigned long long k) { return (unsigned long long)(uint32_t)k; };
+    among(n, lanes, i, index(e.key), index, [](const Entry& x) { return x.w; }, rank, before);
+    if (k_lo && before <= t && t < before + e.w) finish(cut_of(e.key).value, (int)(uint32_t)e.key, sum, (uint32_t)m);
+    return kDone;
+  }
+  __device__ __forceinline__ Outcome use_long_list(int n, int top_k, unsigned long long lo, unsigned long long hi) {
+    sort_list(n);
+    constexpr int K = kCap / kNT;  // neighbours of the list, a thread's
+    unsigned long long w[K], mine = 0, before, all;
+    uint32_t bn, an;
+    const int i0 = (int)threadIdx.x * K;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      w[k] = i0 + k < n && (top_k == 0 || i0 + k < top_k) ? sh.list[i0 + k].w : 0;
+      mine += w[k];
+    }
+    block_scan(mine, 0, before, bn, all, an);
+    if (lo == 0) lo = hi = part_of(all);
+    if (hi != ~0ull && all < hi) return kNeedAll;
+    // kept by the lower and by the upper limit
+    uint32_t m_lo = 0, m_hi = 0;
+    unsigned long long v = 0, b = before;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (i0 + k < n && (top_k == 0 || i0 + k < top_k)) {
+        const bool above = key_value(~(uint32_t)(sh.list[i0 + k].key >> 32)) >= sh.low;
+        if (b < lo && above) ++m_lo, v += w[k];
+        if (b < hi && above) ++m_hi;
+      }
+      b += w[k];
+    }
+    unsigned long long sum, none;
+    block_scan(v, m_lo | m_hi << 16, none, bn, sum, an);
+    const int m = (int)(an & 0xffffu);  // the first m of the list are kept
+    if (m != (int)(an >> 16)) return kNeedSum;
+    if (p.out) {
+      if (threadIdx.x == 0) {
+        send_cut(cut_of(sh.list[m - 1].key));
+        if (p.kept) p.kept[blockIdx.y] = m;
+      }
+      return kDone;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < m; i += kNT) sh.list[i].key = sh.list[i].key << 32 | sh.list[i].key >> 32;  // by index
+    sort_list(m);
+    bool rest;
+    const unsigned long long t = scaled(sh.u, sum, rest);
+    mine = 0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      w[k] = i0 + k < m ? sh.list[i0 + k].w : 0;
+      mine += w[k];
+    }
+    block_scan(mine, 0, before, bn, all, an);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (before <= t && t < before + w[k]) {
+        const Entry e = sh.list[i0 + k];
+        finish(key_value(~(uint32_t)e.key), (int)(e.key >> 32), sum, (uint32_t)m);
+      }
+      before += w[k];
+    }
+    return kDone;
+  }
+  // an entry that the cut, and min-p's border, leave
+  __device__ __forceinline__ bool inside(float f, int i, const Cut& cut) const {
+    return f > cut.value || (f == cut.value && i <= cut.idx);
+  }
+  // out = the entries that `cut` leaves
+  __device__ __forceinline__ uint32_t write(const Cut& cut) const {
     uint32_t n = 0;
-    T* out = static_cast<T*>(p.out) + (size_t)row * p.out_stride;
+    T* out = static_cast<T*>(p.out) + (size_t)blockIdx.y * p.out_stride;
     const bool whole = (reinterpret_cast<uintptr_t>(out) & 15u) == (reinterpret_cast<uintptr_t>(x) & 15u);
-#pragma unroll 2
-    for (int j = lane; j < n_units; j += 32) {
-      const int i0 = (u0 + j) * E - lead;
-      const uint4 raw = slice[ul + j];
+    const float low = sh.low;
+    sweep_units([&](const uint4& raw, int i0) {
       float v[E];
-      open_unit(raw, v, tag);
+      open_unit(raw, v, (const T*)nullptr);
       alignas(16) T e[E];
       *reinterpret_cast<uint4*>(e) = raw;
 #pragma unroll
       for (int k = 0; k < E; ++k) {
-        if (keep(v[k], i0 + k))
+        if (v[k] >= low && inside(v[k], i0 + k, cut))
           ++n;
         else
           e[k] = (T)(-INFINITY);
@@ -720,66 +685,231 @@ __global__ void __launch_bounds__(kNT) sample_kernel(const SampleParams p) {
         for (int k = 0; k < E; ++k)
           if (i0 + k >= 0 && i0 + k < p.V) out[i0 + k] = e[k];
       }
+    });
+    return n;
+  }
+};
+
+// Rows that keep many entries, from what the CTAs have collected (which holds all that
+// may be kept) or from the whole row.  (Out of line: its registers and code are none
+// of the others'.)
+template <typename T, Source kFrom>
+__device__ __noinline__ void many_kept(const SampleParams& p, Shared& sh, int phase) {
+  constexpr int E = Row<T>::E;
+  Row<T> row(p, sh, phase);
+  const int lane = row.lane(), warp = row.warp(), C = row.C(), tid = threadIdx.x;
+  const int n_local = sh.n;
+  Cut cut{-FLT_MAX, 0x7fffffff};
+  auto sweep = [&](auto&& f) {  // f(value, index) for this thread's entries
+    if (kFrom == kRow) {
+      row.sweep(f);
+    } else {
+      for (int i = tid; i < n_local; i += kNT) {
+        const uint2 e = sh.local[i];
+        f(key_value(e.x), (int)e.y);
+      }
     }
-    if (!p.kept) return;
-    n = __reduce_add_sync(0xffffffffu, n);
+  };
+  // the sum of the cluster, and this warp's prefix in it by CTA and warp
+  auto total = [&](unsigned long long v, uint32_t n, unsigned long long& off, uint32_t& off_n, unsigned long long& all,
+                   uint32_t& all_n) {  // v, n: the warp's
     __syncthreads();
-    if (lane == 0) s_wn[warp] = n;
+    if (lane == 0) sh.wv[warp] = v, sh.wn[warp] = n;
     __syncthreads();
-    uint32_t all = 0;
-    for (int x = 0; x < kNW; ++x) all += s_wn[x];
-    const Part* parts = tell(Part{0, 0, all, 0});
-    if (leader && tid == 0) {
-      for (int r = 1; r < C; ++r) all += parts[r].n;
-      p.kept[row] = (int)all;
+    off = all = 0;
+    off_n = all_n = 0;
+    for (int w = 0; w < kNW; ++w) {
+      if (w < warp) off += sh.wv[w], off_n += sh.wn[w];
+      all += sh.wv[w];
+      all_n += sh.wn[w];
     }
+    const Part* parts = row.tell(Part{all, all_n, 0});
+    all = 0;
+    all_n = 0;
+    for (int r = 0; r < C; ++r) {
+      if (r < (int)blockIdx.x) off += parts[r].v, off_n += parts[r].n;
+      all += parts[r].v;
+      all_n += parts[r].n;
+    }
+  };
+  const bool use_k = sh.top_k > 0 && sh.top_k < p.V, use_p = sh.top_p < 1.f;
+#pragma unroll 1
+  for (int stage = 0; stage < 2; ++stage) {
+    const bool by_w = stage == 1;
+    if (by_w ? !use_p : !use_k) continue;
+    cluster_sync();  // (the histogram, and what else the CTAs read of one another, is free)
+    row.clear();
+    {
+      uint32_t far = 0;  // of the last bin, which may be most entries: they weigh nothing
+      sweep([&](float f, int i) {
+        if (row.inside(f, i, cut)) {
+          const int b = row.bin_of(f);
+          if (b == kBins - 1)
+            ++far;
+          else
+            row.add(b, by_w, f);
+        }
+      });
+      far = __reduce_add_sync(0xffffffffu, far);
+      if (lane == 0 && far) atomicAdd(&sh.hist[kBins - 1].x, far);
+    }
+    unsigned long long goal = 0;
+    Found at;
+    auto target = [&](unsigned long long s) { return by_w ? row.part_of(s) : (unsigned long long)sh.top_k; };
+    if (!row.find_bin(by_w, target, goal, at)) continue;  // fewer than k entries
+    const int bin1 = (int)at.bin;
+    uint32_t lo, hi;
+    row.keys_of(bin1, lo, hi);
+    unsigned long long before = at.before;
+    uint32_t n_bin = at.n;
+    auto member = [&](float f, int i) {
+      const uint32_t k = order_key(f);
+      return k >= lo && k <= hi && row.bin_of(f) == bin1 && row.inside(f, i, cut);
+    };
+    while (n_bin > kCap && lo < hi) {
+      const int shift = max(0, 32 - __clz((int)(hi - lo)) - 9);
+      row.clear();
+      sweep([&](float f, int i) {
+        if (member(f, i)) row.add((int)((hi - order_key(f)) >> shift), by_w, f);
+      });
+      unsigned long long g;
+      Found in;
+      row.find_bin(by_w, [&](unsigned long long) { return goal - before; }, g, in);
+      before += in.before;
+      n_bin = in.n;
+      const uint32_t top = hi - (in.bin << shift), width = (1u << shift) - 1;
+      lo = top - lo > width ? top - width : lo;
+      hi = top;
+    }
+    if (n_bin <= kCap) {
+      // to the leader, by their places in order of CTAs
+      uint32_t n = 0;
+      sweep([&](float f, int i) { n += member(f, i) ? 1u : 0u; });
+      const uint32_t in = warp_scan(n);
+      unsigned long long x, y;
+      uint32_t off, all;
+      total(0, __shfl_sync(0xffffffffu, in, 31), x, off, y, all);
+      off += in - n;
+      if (n)
+        sweep([&](float f, int i) {
+          if (member(f, i))
+            st_remote(&sh.list[off++], 0, Entry{(unsigned long long)~order_key(f) << 32 | (uint32_t)i, row.weight(f)});
+        });
+      cluster_sync();
+      if (row.leader()) row.cut_list((int)all, by_w, before, goal);
+    } else {
+      // equal entries: the c-th by index is the last
+      const unsigned long long each = by_w ? row.weight(key_value(lo)) : 1ull;
+      const unsigned long long c = (goal - before + each - 1) / each;
+      uint32_t n = 0;
+      row.sweep([&](float f, int i) { n += member(f, i) ? 1u : 0u; });  // (ranges by index: the row's)
+      n = __reduce_add_sync(0xffffffffu, n);
+      unsigned long long x, y;
+      uint32_t off, all;
+      total(0, n, x, off, y, all);
+      if (off < c && c <= (unsigned long long)off + n) {  // this warp's range holds it
+#pragma unroll 1
+        for (int j0 = 0; j0 < row.n_units; j0 += 32) {
+          const int j = j0 + lane, i0 = row.first_of(j);
+          float v[E];
+          uint32_t m = 0;
+          if (j < row.n_units) {
+            open_unit(row.load(j), v, (const T*)nullptr);
+#pragma unroll
+            for (int k = 0; k < E; ++k) m += member(v[k], i0 + k) ? 1u : 0u;
+          }
+          const uint32_t in = warp_scan(m);
+          uint32_t nth = off + in - m;
+          if (j < row.n_units && nth < c && c <= (unsigned long long)nth + m) {
+#pragma unroll
+            for (int k = 0; k < E; ++k)
+              if (member(v[k], i0 + k) && ++nth == c) row.send_cut(Cut{key_value(lo), i0 + k});
+          }
+          off += __shfl_sync(0xffffffffu, in, 31);
+        }
+      }
+    }
+    cluster_sync();
+    cut = sh.cut;
+  }
+
+  // ---- what is kept
+  const float low = sh.low;
+  uint32_t n = 0;
+  unsigned long long v = 0;
+  if (p.out) {
+    n = row.write(cut);
+  } else {
+    sweep([&](float f, int i) {
+      if (f >= low && row.inside(f, i, cut)) {
+        v += row.weight(f);
+        ++n;
+      }
+    });
+    v = warp_total(v);
+  }
+  n = __reduce_add_sync(0xffffffffu, n);
+  unsigned long long off, all;
+  uint32_t off_n, all_n;
+  total(v, n, off, off_n, all, all_n);
+  if (p.out) {
+    if (p.kept && row.leader() && tid == 0) p.kept[blockIdx.y] = (int)all_n;
     return;
   }
-  unsigned long long v = 0;
-  uint32_t n = 0;
-  sweep([&](float f, int i) {
-    if (keep(f, i)) {
-      v += weight(f);
-      ++n;
-    }
-  });
-#pragma unroll
-  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  n = __reduce_add_sync(0xffffffffu, n);
-  __syncthreads();
-  if (lane == 0) s_wv[warp] = v, s_wn[warp] = n;
-  __syncthreads();
-  unsigned long long off = 0, all = 0;
-  uint32_t all_n = 0;
-  for (int x = 0; x < kNW; ++x) {
-    if (x < warp) off += s_wv[x];
-    all += s_wv[x];
-    all_n += s_wn[x];
-  }
-  const Part* parts = tell(Part{all, 0, all_n, 0});
-  all = 0;
-  all_n = 0;
-  for (int r = 0; r < C; ++r) {
-    if (r < rank) off += parts[r].v;
-    all += parts[r].v;
-    all_n += parts[r].n;
-  }
   bool rest;
-  const unsigned long long t = scaled(u, all, rest);
+  const unsigned long long t = scaled(sh.u, all, rest);
+  if (kFrom == kList) {
+    // the CTA whose range of indices holds the token: its entries by index
+    unsigned long long mine = 0;
+    for (int w = 0; w < kNW; ++w) mine += sh.wv[w];
+    off = 0;
+    for (int r = 0; r < (int)blockIdx.x; ++r) off += sh.part[(row.phase - 1) & 1][r].v;
+    if (!(off <= t && t < off + mine)) return;
+    // their sums over stretches of indices find a stretch of few entries
+    unsigned long long from = (unsigned long long)max(0, ((int)blockIdx.x * kNW) * p.units * E - row.lead);
+    uint32_t width = (uint32_t)kNW * p.units * E;
+    // (a stretch of 1 / kNT of the range at a time: the CTA's threads hold one each)
+    unsigned long long* sums = reinterpret_cast<unsigned long long*>(sh.list);  // [kNT], not the leader's list any more
+    while (width > 1) {
+      const uint32_t step = (width + kNT - 1) / kNT;
+      __syncthreads();
+      sums[tid] = 0;
+      __syncthreads();
+      for (int i = tid; i < n_local; i += kNT) {
+        const uint2 e = sh.local[i];
+        const float f = key_value(e.x);
+        if (f >= low && row.inside(f, (int)e.y, cut) && e.y >= from && e.y - from < width)
+          atomicAdd(&sums[(uint32_t)(e.y - from) / step], row.weight(f));
+      }
+      __syncthreads();
+      unsigned long long before, s;
+      uint32_t bn, an;
+      const unsigned long long w = sums[tid];
+      row.block_scan(w, 0, before, bn, s, an);
+      before += off;
+      if (before <= t && t < before + w) sh.found = Found{before, (uint32_t)tid, 0, 0, 0};
+      __syncthreads();
+      off = sh.found.before;
+      from += (unsigned long long)sh.found.bin * step;
+      width = step;
+    }
+    for (int i = tid; i < n_local; i += kNT)
+      if (sh.local[i].y == (uint32_t)from) row.finish(key_value(sh.local[i].x), (int)from, all, all_n);
+    return;
+  }
   if (!(off <= t && t < off + v)) return;
 #pragma unroll 1
-  for (int j0 = 0; j0 < n_units; j0 += 32) {
-    const int j = j0 + lane;
+  for (int j0 = 0; j0 < row.n_units; j0 += 32) {
+    const int j = j0 + lane, i0 = row.first_of(j);
     float f[E];
     unsigned long long w[E], mine = 0;
-    const int i0 = (u0 + j) * E - lead;
 #pragma unroll
     for (int k = 0; k < E; ++k) w[k] = 0;
-    if (j < n_units) {
-      open_unit(slice[ul + j], f, tag);
+    if (j < row.n_units) {
+      open_unit(row.load(j), f, (const T*)nullptr);
 #pragma unroll
       for (int k = 0; k < E; ++k) {
-        w[k] = keep(f[k], i0 + k) ? weight(f[k]) : 0;
+        w[k] = f[k] >= low && row.inside(f[k], i0 + k, cut) ? row.weight(f[k]) : 0;
         mine += w[k];
       }
     }
@@ -788,7 +918,7 @@ __global__ void __launch_bounds__(kNT) sample_kernel(const SampleParams p) {
     if (at <= t && t < at + mine) {
 #pragma unroll
       for (int k = 0; k < E; ++k) {
-        if (at <= t && t < at + w[k]) finish(f[k], i0 + k, all, all_n);
+        if (at <= t && t < at + w[k]) row.finish(f[k], i0 + k, all, all_n);
         at += w[k];
       }
     }
@@ -798,18 +928,210 @@ __global__ void __launch_bounds__(kNT) sample_kernel(const SampleParams p) {
 }
 
 template <typename T>
+__global__ void __launch_bounds__(kNT, 4) sample_kernel(const SampleParams p) {
+  constexpr int E = Unit<T>::E;
+  __shared__ Shared sh;
+  const int tid = threadIdx.x, at_row = blockIdx.y;
+  if (tid < 64) {
+    sh.pow64[tid] = kPow64[tid];
+    sh.pow4096[tid] = kPow4096[tid];
+  }
+  if (tid == 0) sh.n = 0;
+  // no CTA writes to another's shared memory before that one runs: waited for below
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  pdl_wait();
+  pdl_trigger();
+  Row<T> row(p, sh, 0);
+  const int lane = row.lane(), warp = row.warp();
+  const int rq = at_row / p.per;
+  const float temp = p.temp ? p.temp[rq] : 1.f, top_p = p.top_p ? p.top_p[rq] : 1.f, min_p = p.min_p ? p.min_p[rq] : 0.f;
+  const int top_k = p.top_k ? p.top_k[rq] : 0;
+  const float u = p.out ? 0.f : p.u[at_row];
+  const bool bad_args = !(temp >= 0.f && temp <= FLT_MAX) || !(top_p >= 0.f) || !(min_p >= 0.f && min_p <= 1.f) ||
+                        top_k < 0 || !(u >= 0.f && u < 1.f);
+
+  // ---- first pass: the largest, and what is no logit
+  const bool use_k = top_k > 0 && top_k < p.V, use_p = top_p < 1.f, small = p.V <= kCap;
+  // What may be kept is collected from the q-th largest of a CTA's threads' largest on:
+  // their largest of all entries, or, for a large k, of so many that about half of
+  // them reach the value looked for.  q k-ths of the CTAs' are k entries at least; a
+  // large k's is an estimate, and the entries are counted.
+  int q = 0, group = 0x7fffffff;
+  if (!small && temp != 0.f) {
+    if (use_k) {
+      q = (top_k + row.C() - 1) / row.C();
+      if (q > kNT / 4) {
+        const float share = (1.25f * (float)top_k + 32.f) / (float)p.V, units = (float)((p.units + 31) / 32);
+        const float g = fmaxf(1.f, fminf(units, floorf(1.2f / (share * (float)E))));
+        group = (int)g;
+        q = share < 0.2f ? min(kNT, (int)((1.f - __expf(-share * g * (float)E)) * (float)kNT) + 8) : 0;
+      }
+    } else if (use_p) {
+      q = kNT / 8;
+    }
+  }
+  float top = -INFINITY, group_top = -INFINITY;
+  int at = 0x7fffffff, units = 0;
+  bool odd = false;  // NaN or +infinity
+  row.sweep_units([&](const uint4& v, int i0) {
+    float f[E];
+    open_unit(v, f, (const T*)nullptr);
+#pragma unroll
+    for (int k = 0; k < E; ++k) {
+      odd = odd || !(f[k] <= FLT_MAX);
+      if (f[k] > top) top = f[k], at = i0 + k;
+    }
+    if (units++ < group) group_top = top;
+  });
+  if (q) sh.tops[tid] = group_top;
+  unsigned long long best = (unsigned long long)order_key(top) << 32 | (uint32_t)~at;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, d));
+  if (lane == 0) sh.wkey[warp] = best;
+  const bool any_odd = __syncthreads_or(odd);
+  best = sh.wkey[lane % kNW];
+#pragma unroll
+  for (int d = kNW / 2; d; d >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, d));
+  uint32_t from_key = 0xffffffffu;  // of this CTA's q-th
+  if (q) {
+    int rank = 0;
+#pragma unroll 4
+    for (int j = 0; j < kNT; j += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(&sh.tops[j]);
+      rank += (v.x > group_top || (v.x == group_top && j < tid)) + (v.y > group_top || (v.y == group_top && j + 1 < tid)) +
+              (v.z > group_top || (v.z == group_top && j + 2 < tid)) + (v.w > group_top || (v.w == group_top && j + 3 < tid));
+    }
+    if (rank == q - 1) sh.n = (int)order_key(group_top);
+    __syncthreads();
+    from_key = (uint32_t)sh.n;
+    __syncthreads();
+    if (tid == 0) sh.n = 0;
+  }
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  {
+    const Part* all = row.tell(Part{best, from_key, any_odd});
+    odd = false;
+    for (int r = 0; r < row.C(); ++r) {
+      best = max(best, all[r].v);
+      from_key = min(from_key, all[r].n);
+      odd = odd || all[r].flags;
+    }
+  }
+  const float xmax = key_value((uint32_t)(best >> 32));
+  const int first = (int)~(uint32_t)best;
+  if (bad_args || odd || xmax == -INFINITY) {
+    if (row.leader() && tid == 0) {
+      set_status(p.status, bad_args ? EAGLE_ERR_INVALID_ARG : EAGLE_ERR_NONFINITE);
+      if (p.tokens) p.tokens[at_row] = -1;
+      if (p.logprobs) p.logprobs[at_row] = -INFINITY;
+      if (p.kept) p.kept[at_row] = 0;
+    }
+    return;
+  }
+  if (temp == 0.f) {
+    if (row.leader() && tid == 0) {
+      if (p.tokens) p.tokens[at_row] = first;
+      if (p.logprobs) p.logprobs[at_row] = 0.f;
+      if (p.kept) p.kept[at_row] = 1;
+    }
+    if (!p.out) return;
+    if (tid == 0) sh.low = -FLT_MAX;
+    __syncthreads();
+    row.write(Cut{xmax, first});
+    return;
+  }
+  if (tid == 0) {
+    // (a temperature so small that its reciprocal overflows leaves the largest alone)
+    const double c = fmin(1.4426950408889634 / (double)temp, 3.0e38);
+    const float ch = (float)c;
+    sh.weigh = Weigh{xmax, ch, (float)(c - (double)ch)};
+    sh.bins = (float)(kBins - 1) / ((float)(kOne + 1) + 0.01f) * ch;
+    // w >= min_p as a border of x: the smallest fp32 number not below max + T log(min_p)
+    float low = -FLT_MAX;
+    if (min_p > 0.f) {
+      const double b = (double)xmax + (double)temp * log((double)min_p);
+      low = b <= -(double)FLT_MAX ? -FLT_MAX : __double2float_ru(b);
+    }
+    sh.low = low;
+    sh.temp = temp;
+    sh.top_p = top_p;
+    sh.u = u;
+    sh.top_k = top_k;
+  }
+  __syncthreads();
+
+  // ---- the entries that may be kept, when they are few
+  const bool by_sum = !use_k && use_p && !small;
+  if (small || q || (!use_k && !use_p && min_p > 0.f)) {
+    const float from = q ? fmaxf(key_value(from_key), -FLT_MAX) : small ? -FLT_MAX : sh.low;
+    const bool all_of_them = from == -FLT_MAX;
+    const float c = by_sum ? sh.weigh.ch : 0.f;
+    float sum = 0.f;
+    row.sweep([&](float f, int i) {
+      if (by_sum) sum += ex2_approx((f - xmax) * c);
+      if (f >= from) row.collect(f, i);
+    });
+    if (by_sum) {
+#pragma unroll
+      for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      if (lane == 0) sh.wsum[warp] = sum;
+      __syncthreads();
+      sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kNW; ++w) sum += sh.wsum[w];
+    }
+    unsigned long long around;  // the CTAs' sums, in units of 2^-40
+    int most;
+    const int n = row.gather(by_sum ? __float2ull_rn(sum * 1.099511627776e12f) : 0ull, around, most);
+    const bool enough = all_of_them || !use_k || n >= top_k;
+    if (n <= kCap && enough) {
+      unsigned long long lo = ~0ull, hi = ~0ull;  // top-p's limits
+      if (use_p) lo = hi = 0;
+      if (by_sum && !all_of_them) {
+        const float s = (float)around * 16.f;
+        lo = row.part_of(__float2ull_rd(s * (1.f - kSumError)));
+        hi = row.part_of(__float2ull_ru(s * (1.f + kSumError)));
+      }
+      Outcome result = kDone;
+      if (row.leader()) result = row.use_list(n, use_k ? top_k : 0, lo, hi);
+      if (by_sum && !all_of_them) {
+        result = (Outcome)row.tell(Part{0, (unsigned)result, 0})[0].n;
+        if (result == kNeedSum) {
+          // the border lies within the sum's error: the exact sum
+          unsigned long long v = 0;
+          row.sweep([&](float f, int i) { v += row.weight(f); });
+          const Part* parts = row.tell(Part{row.block_sum(v), 0, 0});
+          v = 0;
+          for (int r = 0; r < row.C(); ++r) v += parts[r].v;
+          lo = row.part_of(v);
+          result = kDone;
+          if (row.leader()) result = row.use_list(n, 0, lo, lo);
+          result = (Outcome)row.tell(Part{0, (unsigned)result, 0})[0].n;
+        }
+      } else if (p.out) {
+        cluster_sync();
+      }
+      if (result == kDone) {
+        if (p.out) row.write(sh.cut);
+        return;
+      }
+    } else if (use_k && enough && most <= kLocal) {
+      many_kept<T, kList>(p, sh, row.phase);
+      return;
+    }
+  }
+  many_kept<T, kRow>(p, sh, row.phase);
+}
+
+template <typename T>
 int sample_launch(SampleParams p, void* stream) {
   if (p.M == 0) return EAGLE_OK;
   const int total = (p.V + Unit<T>::E - 1) / Unit<T>::E + 1;  // and one for a start off its boundary
   int C = 1;
   while (C < kMaxCluster && total > C * kNT * 2) C *= 2;
   p.units = (total + C * kNW - 1) / (C * kNW);
-  const size_t smem = 16 * kBins + 16 * (size_t)p.units * kNW;
-  if (cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
-    cudaGetLastError();
-    return EAGLE_ERR_CUDA;
-  }
-  launch_cluster(sample_kernel<T>, dim3(C, p.M), dim3(kNT), dim3(C, 1, 1), smem, static_cast<cudaStream_t>(stream), p);
+  launch_cluster(sample_kernel<T>, dim3(C, p.M), dim3(kNT), dim3(C, 1, 1), 0, static_cast<cudaStream_t>(stream), p);
   note_launch();
   return last_launch_status();
 }
