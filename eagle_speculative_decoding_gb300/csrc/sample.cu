@@ -155,7 +155,6 @@ struct Shared {
   uint4 hist[kBins];  // counts, and three limbs of sums of weights
   uint2 local[kLocal];  // this CTA's collected entries: (order key, index)
   Entry list[kCap];     // the leader's list
-  float tops[kNT];      // the threads' largest
   unsigned long long pow64[64], wv[kNW], wkey[kNW];
   uint32_t pow4096[64], wn[kNW];
   float wsum[kNW];
@@ -279,10 +278,10 @@ struct Row {
     return *reinterpret_cast<const uint4*>(e);
   }
   // f(unit j, its values, index of its first entry) for this lane's units, in ascending
-  // order, four loads in flight
-  template <typename F>
+  // order, kUnits loads in flight
+  template <int kUnits, typename F>
   __device__ __forceinline__ void sweep_units(F&& f) const {
-    constexpr int U = 4;
+    constexpr int U = kUnits;
 #pragma unroll 1
     for (int j0 = lane(); j0 < n_units; j0 += 32 * U) {
       uint4 v[U];
@@ -294,9 +293,9 @@ struct Row {
         if (j0 + 32 * i < n_units) f(v[i], first_of(j0 + 32 * i));
     }
   }
-  template <typename F>
+  template <int kUnits = 4, typename F>
   __device__ __forceinline__ void sweep(F&& f) const {  // f(value, index)
-    sweep_units([&](const uint4& u, int i0) {
+    sweep_units<kUnits>([&](const uint4& u, int i0) {
       float v[E];
       open_unit(u, v, (const T*)nullptr);
 #pragma unroll
@@ -457,10 +456,18 @@ struct Row {
   }
   // All CTAs' local lists (sh.n entries each) in the leader's: the number of entries,
   // in all CTAs; over kCap nothing is sent (most: the largest local list).  Whole CTAs
-  // call it.
+  // call it.  The entries go with the counts, to a stretch of the list for each CTA,
+  // where that holds them; otherwise behind another barrier.
   __device__ __forceinline__ int gather(unsigned long long v, unsigned long long& sum, int& most) {
     __syncthreads();
-    const int mine = sh.n;
+    const int mine = sh.n, stretch = kCap / C();
+    auto send = [&](int to) {
+      for (int i = threadIdx.x; i < mine; i += kNT) {
+        const uint2 e = sh.local[i];
+        st_remote(&sh.list[to + i], 0, Entry{(unsigned long long)~e.x << 32 | e.y, weight(key_value(e.x))});
+      }
+    };
+    if (mine <= stretch) send((int)blockIdx.x * stretch);
     const Part* parts = tell(Part{v, (unsigned)mine, 0});
     int n = 0, at = 0;
     sum = 0;
@@ -473,11 +480,27 @@ struct Row {
       sum += parts[r].v;
     }
     if (n > kCap) return n;
-    for (int i = threadIdx.x; i < mine; i += kNT) {
-      const uint2 e = sh.local[i];
-      st_remote(&sh.list[at + i], 0, Entry{(unsigned long long)~e.x << 32 | e.y, weight(key_value(e.x))});
+    if (most > stretch) {
+      send(at);
+      cluster_sync();
+    } else if (leader()) {
+      // close the gaps: entry i of all is entry i - at of CTA r
+      constexpr int K = kCap / kNT;
+      Entry e[K];
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int i = (int)threadIdx.x + k * kNT;
+        if (i >= n) continue;
+        int r = 0, from = 0;
+        while (i >= from + (int)parts[r].n) from += (int)parts[r++].n;
+        e[k] = sh.list[r * stretch + i - from];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if ((int)threadIdx.x + k * kNT < n) sh.list[threadIdx.x + k * kNT] = e[k];
+      __syncthreads();
     }
-    cluster_sync();
     return n;
   }
   // The leader, of a list of at most kNT entries: `lanes` neighbouring threads have entry
@@ -507,37 +530,17 @@ struct Row {
   __device__ __forceinline__ void send_cut(const Cut& c) {
     for (int r = 0; r < C(); ++r) st_remote(&sh.cut, r, c);
   }
-  // The leader: the entry of its list at which the measure, from `before` on, reaches
+  // The leader: the entry of its list of at most kNT at which the measure, from `before` on, reaches
   // goal, as the cut in all CTAs.
   __device__ __forceinline__ void cut_list(int n, bool weighted, unsigned long long before, unsigned long long goal) {
-    if (n <= kNT) {
-      const int lanes = lanes_of(n), i = (int)threadIdx.x / lanes;
-      const Entry e = i < n ? sh.list[i] : Entry{0, 0};
-      uint32_t rank;
-      unsigned long long b;
-      among(n, lanes, i, e.key, [](unsigned long long k) { return k; },
-            [&](const Entry& x) { return weighted ? x.w : 1ull; }, rank, b);
-      b += before;
-      if (i < n && threadIdx.x % lanes == 0 && b < goal && goal <= b + (weighted ? e.w : 1ull)) send_cut(cut_of(e.key));
-      return;
-    }
-    sort_list(n);
-    constexpr int K = kCap / kNT;
-    const int i0 = (int)threadIdx.x * K;
-    unsigned long long w[K], mine = 0, b, all;
-    uint32_t bn, an;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      w[k] = i0 + k < n ? (weighted ? sh.list[i0 + k].w : 1ull) : 0;
-      mine += w[k];
-    }
-    block_scan(mine, 0, b, bn, all, an);
+    const int lanes = lanes_of(n), i = (int)threadIdx.x / lanes;
+    const Entry e = i < n ? sh.list[i] : Entry{0, 0};
+    uint32_t rank;
+    unsigned long long b;
+    among(n, lanes, i, e.key, [](unsigned long long k) { return k; },
+          [&](const Entry& x) { return weighted ? x.w : 1ull; }, rank, b);
     b += before;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      if (b < goal && goal <= b + w[k]) send_cut(cut_of(sh.list[i0 + k].key));
-      b += w[k];
-    }
+    if (i < n && threadIdx.x % lanes == 0 && b < goal && goal <= b + (weighted ? e.w : 1ull)) send_cut(cut_of(e.key));
   }
   // one thread: the drawn token
   __device__ __forceinline__ void finish(float f, int i, unsigned long long sum, uint32_t kept) const {
@@ -666,7 +669,7 @@ struct Row {
     T* out = static_cast<T*>(p.out) + (size_t)blockIdx.y * p.out_stride;
     const bool whole = (reinterpret_cast<uintptr_t>(out) & 15u) == (reinterpret_cast<uintptr_t>(x) & 15u);
     const float low = sh.low;
-    sweep_units([&](const uint4& raw, int i0) {
+    sweep_units<4>([&](const uint4& raw, int i0) {
       float v[E];
       open_unit(raw, v, (const T*)nullptr);
       alignas(16) T e[E];
@@ -698,17 +701,19 @@ __device__ __noinline__ void many_kept(const SampleParams& p, Shared& sh, int ph
   constexpr int E = Row<T>::E;
   Row<T> row(p, sh, phase);
   const int lane = row.lane(), warp = row.warp(), C = row.C(), tid = threadIdx.x;
-  const int n_local = sh.n;
+  int n_local = sh.n;
   Cut cut{-FLT_MAX, 0x7fffffff};
-  auto sweep = [&](auto&& f) {  // f(value, index) for this thread's entries
-    if (kFrom == kRow) {
-      row.sweep(f);
-    } else {
-      for (int i = tid; i < n_local; i += kNT) {
-        const uint2 e = sh.local[i];
-        f(key_value(e.x), (int)e.y);
-      }
+  auto sweep_local = [&](auto&& f) {
+    for (int i = tid; i < n_local; i += kNT) {
+      const uint2 e = sh.local[i];
+      f(key_value(e.x), (int)e.y);
     }
+  };
+  auto sweep = [&](auto&& f) {  // f(value, index) for this thread's entries
+    if (kFrom == kRow)
+      row.template sweep<2>(f);
+    else
+      sweep_local(f);
   };
   // the sum of the cluster, and this warp's prefix in it by CTA and warp
   auto total = [&](unsigned long long v, uint32_t n, unsigned long long& off, uint32_t& off_n, unsigned long long& all,
@@ -766,12 +771,34 @@ __device__ __noinline__ void many_kept(const SampleParams& p, Shared& sh, int ph
       const uint32_t k = order_key(f);
       return k >= lo && k <= hi && row.bin_of(f) == bin1 && row.inside(f, i, cut);
     };
-    while (n_bin > kCap && lo < hi) {
+    // (the row's are collected once, and the bin is refined among them)
+    bool collected = kFrom == kList;
+    if (kFrom == kRow && n_bin > kNT) {
+      __syncthreads();
+      if (tid == 0) sh.n = 0;
+      __syncthreads();
+      row.sweep([&](float f, int i) {
+        if (member(f, i)) row.collect(f, i);
+      });
+      __syncthreads();
+      n_local = sh.n;
+      const Part* parts = row.tell(Part{0, (unsigned)n_local, 0});
+      collected = true;
+      for (int r = 0; r < C; ++r) collected = collected && parts[r].n <= kLocal;
+    }
+    auto members = [&](auto&& f) {  // f(value, index) of the bin's entries
+      auto if_member = [&](float x, int i) {
+        if (member(x, i)) f(x, i);
+      };
+      if (kFrom == kRow && !collected)
+        row.sweep(if_member);
+      else
+        sweep_local(if_member);
+    };
+    while (n_bin > kNT && lo < hi) {
       const int shift = max(0, 32 - __clz((int)(hi - lo)) - 9);
       row.clear();
-      sweep([&](float f, int i) {
-        if (member(f, i)) row.add((int)((hi - order_key(f)) >> shift), by_w, f);
-      });
+      members([&](float f, int i) { row.add((int)((hi - order_key(f)) >> shift), by_w, f); });
       unsigned long long g;
       Found in;
       row.find_bin(by_w, [&](unsigned long long) { return goal - before; }, g, in);
@@ -781,19 +808,18 @@ __device__ __noinline__ void many_kept(const SampleParams& p, Shared& sh, int ph
       lo = top - lo > width ? top - width : lo;
       hi = top;
     }
-    if (n_bin <= kCap) {
+    if (n_bin <= kNT) {
       // to the leader, by their places in order of CTAs
       uint32_t n = 0;
-      sweep([&](float f, int i) { n += member(f, i) ? 1u : 0u; });
+      members([&](float, int) { ++n; });
       const uint32_t in = warp_scan(n);
       unsigned long long x, y;
       uint32_t off, all;
       total(0, __shfl_sync(0xffffffffu, in, 31), x, off, y, all);
       off += in - n;
       if (n)
-        sweep([&](float f, int i) {
-          if (member(f, i))
-            st_remote(&sh.list[off++], 0, Entry{(unsigned long long)~order_key(f) << 32 | (uint32_t)i, row.weight(f)});
+        members([&](float f, int i) {
+          st_remote(&sh.list[off++], 0, Entry{(unsigned long long)~order_key(f) << 32 | (uint32_t)i, row.weight(f)});
         });
       cluster_sync();
       if (row.leader()) row.cut_list((int)all, by_w, before, goal);
@@ -967,13 +993,13 @@ __global__ void __launch_bounds__(kNT, 4) sample_kernel(const SampleParams p) {
         q = share < 0.2f ? min(kNT, (int)((1.f - __expf(-share * g * (float)E)) * (float)kNT) + 8) : 0;
       }
     } else if (use_p) {
-      q = kNT / 8;
+      q = kNT / 16;
     }
   }
   float top = -INFINITY, group_top = -INFINITY;
   int at = 0x7fffffff, units = 0;
   bool odd = false;  // NaN or +infinity
-  row.sweep_units([&](const uint4& v, int i0) {
+  row.template sweep_units<8>([&](const uint4& v, int i0) {
     float f[E];
     open_unit(v, f, (const T*)nullptr);
 #pragma unroll
@@ -983,7 +1009,6 @@ __global__ void __launch_bounds__(kNT, 4) sample_kernel(const SampleParams p) {
     }
     if (units++ < group) group_top = top;
   });
-  if (q) sh.tops[tid] = group_top;
   unsigned long long best = (unsigned long long)order_key(top) << 32 | (uint32_t)~at;
 #pragma unroll
   for (int d = 16; d; d >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, d));
@@ -992,20 +1017,15 @@ __global__ void __launch_bounds__(kNT, 4) sample_kernel(const SampleParams p) {
   best = sh.wkey[lane % kNW];
 #pragma unroll
   for (int d = kNW / 2; d; d >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, d));
-  uint32_t from_key = 0xffffffffu;  // of this CTA's q-th
+  uint32_t from_key = 0xffffffffu;  // a value that q of this CTA's threads reach, to 2^-11
   if (q) {
-    int rank = 0;
-#pragma unroll 4
-    for (int j = 0; j < kNT; j += 4) {
-      const float4 v = *reinterpret_cast<const float4*>(&sh.tops[j]);
-      rank += (v.x > group_top || (v.x == group_top && j < tid)) + (v.y > group_top || (v.y == group_top && j + 1 < tid)) +
-              (v.z > group_top || (v.z == group_top && j + 2 < tid)) + (v.w > group_top || (v.w == group_top && j + 3 < tid));
+    const uint32_t mine = order_key(group_top);
+    from_key = 0;
+#pragma unroll 1
+    for (int bit = 31; bit >= 12; --bit) {
+      const uint32_t key = from_key | 1u << bit;
+      if (__syncthreads_count(mine >= key) >= q) from_key = key;
     }
-    if (rank == q - 1) sh.n = (int)order_key(group_top);
-    __syncthreads();
-    from_key = (uint32_t)sh.n;
-    __syncthreads();
-    if (tid == 0) sh.n = 0;
   }
   __syncwarp();
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -1042,10 +1062,11 @@ __global__ void __launch_bounds__(kNT, 4) sample_kernel(const SampleParams p) {
     return;
   }
   if (tid == 0) {
-    // (a temperature so small that its reciprocal overflows leaves the largest alone)
-    const double c = fmin(1.4426950408889634 / (double)temp, 3.0e38);
-    const float ch = (float)c;
-    sh.weigh = Weigh{xmax, ch, (float)(c - (double)ch)};
+    // log2(e) / T in two parts, the second from the remainder (a temperature so small
+    // that its reciprocal overflows leaves the largest alone)
+    const float ch = fminf(1.44269502f / temp, 3.0e38f);
+    const float cl = ch < 3.0e38f ? (fmaf(-ch, temp, 1.44269502f) + 1.92596303e-8f) / temp : 0.f;
+    sh.weigh = Weigh{xmax, ch, isfinite(cl) ? cl : 0.f};
     sh.bins = (float)(kBins - 1) / ((float)(kOne + 1) + 0.01f) * ch;
     // w >= min_p as a border of x: the smallest fp32 number not below max + T log(min_p)
     float low = -FLT_MAX;
@@ -1064,11 +1085,11 @@ __global__ void __launch_bounds__(kNT, 4) sample_kernel(const SampleParams p) {
   // ---- the entries that may be kept, when they are few
   const bool by_sum = !use_k && use_p && !small;
   if (small || q || (!use_k && !use_p && min_p > 0.f)) {
-    const float from = q ? fmaxf(key_value(from_key), -FLT_MAX) : small ? -FLT_MAX : sh.low;
+    const float from = q ? (from_key > order_key(-FLT_MAX) ? key_value(from_key) : -FLT_MAX) : small ? -FLT_MAX : sh.low;
     const bool all_of_them = from == -FLT_MAX;
     const float c = by_sum ? sh.weigh.ch : 0.f;
     float sum = 0.f;
-    row.sweep([&](float f, int i) {
+    row.template sweep<8>([&](float f, int i) {
       if (by_sum) sum += ex2_approx((f - xmax) * c);
       if (f >= from) row.collect(f, i);
     });
