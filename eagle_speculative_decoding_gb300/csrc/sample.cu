@@ -131,9 +131,10 @@ struct Weigh {
   __device__ __forceinline__ unsigned long long operator()(float x, const unsigned long long* pow64,
                                                            const uint32_t* pow4096) const {
     const float dh = xmax - x, b = dh - xmax, dl = (xmax - (dh - b)) - (x + b);
-    const float yh = dh * ch;
-    if (!(yh < (float)kOne + 1.f)) return 0;  // below half a unit (or no difference at all)
-    const float yl = fmaf(dh, ch, -yh) + fmaf(dh, cl, dl * ch);
+    // (no branch, so that a thread's entries are worked out side by side; at 50 the
+    // weight is zero, as it is from 45 on)
+    const float yh = fminf(dh * ch, 50.f);
+    const float yl = yh < 50.f ? fmaf(dh, ch, -yh) + fmaf(dh, cl, dl * ch) : 0.f;
     const float t = fmaf(yh, 4096.f, 12582912.f);  // rounds to a whole number in the low bits
     const int j = __float_as_int(t) - 0x4b400000;
     const float r = fmaf(t - 12582912.f, -1.f / 4096.f, yh) + yl;  // |r| <= 2^-13 and a little
@@ -145,7 +146,7 @@ struct Weigh {
     unsigned long long w = a - (((unsigned long long)a31 * q + (1u << 24)) >> (31 + 38 - kOne));
     w -= (unsigned long long)(((long long)(int)(a31 >> 1) * s) >> (30 + 38 - kOne));
     const int n = j >> 12;
-    return n ? (w + (1ull << (n - 1))) >> n : w;
+    return (2 * w + (1ull << n)) >> (n + 1);  // rounded: 2 w < 2^46
   }
 };
 
@@ -246,6 +247,39 @@ __device__ __forceinline__ unsigned long long warp_total(unsigned long long v) {
   return v;
 }
 
+// A row's first or last unit, what is not the row's as -infinity.  (Rare steps are
+// functions of their own: a row's code runs once or a few times on an SM, and fetching
+// it takes longer than running it.)
+template <typename T>
+__device__ __noinline__ uint4 load_edge(const T* x, int i0, int V) {
+  alignas(16) T e[Unit<T>::E];
+  for (int k = 0; k < Unit<T>::E; ++k) e[k] = i0 + k >= 0 && i0 + k < V ? x[i0 + k] : (T)(-INFINITY);
+  return *reinterpret_cast<const uint4*>(e);
+}
+template <typename T>
+__device__ __noinline__ void store_edge(T* out, uint4 v, int i0, int V) {
+  alignas(16) T e[Unit<T>::E];
+  *reinterpret_cast<uint4*>(e) = v;
+  for (int k = 0; k < Unit<T>::E; ++k)
+    if (i0 + k >= 0 && i0 + k < V) out[i0 + k] = e[k];
+}
+// The entries of a unit within [from, to] to this CTA's local list.
+template <typename T>
+__device__ __noinline__ void collect_unit(Shared& sh, uint4 u, int i0, float from, float to) {
+  float f[Unit<T>::E];
+  open_unit(u, f, (const T*)nullptr);
+  uint32_t n = 0;
+#pragma unroll
+  for (int k = 0; k < Unit<T>::E; ++k) n += (f[k] >= from) & (f[k] <= to);
+  int at = atomicAdd(&sh.n, (int)n);
+#pragma unroll
+  for (int k = 0; k < Unit<T>::E; ++k)
+    if ((f[k] >= from) & (f[k] <= to)) {
+      if (at < kLocal) sh.local[at] = make_uint2(order_key(f[k]), (uint32_t)(i0 + k));
+      ++at;
+    }
+}
+
 // A row, a thread's place in it, and the steps that the paths share.  The cluster is
 // the grid's x, the row its y.
 template <typename T>
@@ -272,10 +306,7 @@ struct Row {
   __device__ __forceinline__ uint4 load(int j) const {
     const int i0 = first_of(j);
     if (i0 >= 0 && i0 + E <= p.V) return *reinterpret_cast<const uint4*>(x + i0);
-    alignas(16) T e[E];
-#pragma unroll
-    for (int k = 0; k < E; ++k) e[k] = i0 + k >= 0 && i0 + k < p.V ? x[i0 + k] : (T)(-INFINITY);
-    return *reinterpret_cast<const uint4*>(e);
+    return load_edge(x, i0, p.V);
   }
   // f(unit j, its values, index of its first entry) for this lane's units, in ascending
   // order, kUnits loads in flight
@@ -293,13 +324,37 @@ struct Row {
         if (j0 + 32 * i < n_units) f(v[i], first_of(j0 + 32 * i));
     }
   }
-  template <int kUnits = 4, typename F>
+  // the same with one copy of f, the next load in flight meanwhile
+  template <typename F>
+  __device__ __forceinline__ void sweep_short(F&& f) const {
+    uint4 next = lane() < n_units ? load(lane()) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+    for (int j = lane(); j < n_units; j += 32) {
+      const uint4 v = next;
+      if (j + 32 < n_units) next = load(j + 32);
+      f(v, first_of(j));
+    }
+  }
+  template <typename F>
   __device__ __forceinline__ void sweep(F&& f) const {  // f(value, index)
-    sweep_units<kUnits>([&](const uint4& u, int i0) {
+    sweep_short([&](const uint4& u, int i0) {
       float v[E];
       open_unit(u, v, (const T*)nullptr);
 #pragma unroll
       for (int k = 0; k < E; ++k) f(v[k], i0 + k);
+    });
+  }
+  // f(value, index, weight)
+  template <typename F>
+  __device__ __forceinline__ void sweep_weights(F&& f) const {
+    sweep_short([&](const uint4& u, int i0) {
+      float v[E];
+      open_unit(u, v, (const T*)nullptr);
+      unsigned long long w[E];
+#pragma unroll
+      for (int k = 0; k < E; ++k) w[k] = weight(v[k]);
+#pragma unroll
+      for (int k = 0; k < E; ++k) f(v[k], i0 + k, w[k]);
     });
   }
   // `mine`, the same in threads 0 .. C - 1, to all CTAs; returns where theirs are
@@ -349,10 +404,9 @@ struct Row {
     for (int i = threadIdx.x; i < kBins; i += kNT) sh.hist[i] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
   }
-  __device__ __forceinline__ void add(int b, bool weighted, float f) {
+  __device__ __forceinline__ void add(int b, bool weighted, unsigned long long w) {
     atomicAdd(&sh.hist[b].x, 1u);
     if (weighted) {
-      const unsigned long long w = weight(f);
       constexpr uint32_t mask = (1u << kLimb) - 1;
       const uint32_t w0 = (uint32_t)w & mask, w1 = (uint32_t)(w >> kLimb) & mask, w2 = (uint32_t)(w >> (2 * kLimb));
       if (w0) atomicAdd(&sh.hist[b].y, w0);
@@ -423,11 +477,6 @@ struct Row {
     cluster_sync();
     at = sh.found;
     return true;
-  }
-  // One entry for this CTA's local list.
-  __device__ __forceinline__ void collect(float f, int i) {
-    const int at = atomicAdd(&sh.n, 1);
-    if (at < kLocal) sh.local[at] = make_uint2(order_key(f), (uint32_t)i);
   }
   // list[0 .. n) of the leader by key ascending
   __device__ __forceinline__ void sort_list(int n) {
@@ -661,7 +710,7 @@ struct Row {
   }
   // an entry that the cut, and min-p's border, leave
   __device__ __forceinline__ bool inside(float f, int i, const Cut& cut) const {
-    return f > cut.value || (f == cut.value && i <= cut.idx);
+    return (f > cut.value) | ((f == cut.value) & (i <= cut.idx));
   }
   // out = the entries that `cut` leaves
   __device__ __forceinline__ uint32_t write(const Cut& cut) const {
@@ -676,17 +725,14 @@ struct Row {
       *reinterpret_cast<uint4*>(e) = raw;
 #pragma unroll
       for (int k = 0; k < E; ++k) {
-        if (v[k] >= low && inside(v[k], i0 + k, cut))
-          ++n;
-        else
-          e[k] = (T)(-INFINITY);
+        const bool in = (v[k] >= low) & inside(v[k], i0 + k, cut);
+        n += in;
+        e[k] = in ? e[k] : (T)(-INFINITY);
       }
       if (whole && i0 >= 0 && i0 + E <= p.V) {
         *reinterpret_cast<uint4*>(out + i0) = *reinterpret_cast<const uint4*>(e);
       } else {
-#pragma unroll
-        for (int k = 0; k < E; ++k)
-          if (i0 + k >= 0 && i0 + k < p.V) out[i0 + k] = e[k];
+        store_edge(out, *reinterpret_cast<const uint4*>(e), i0, p.V);
       }
     });
     return n;
@@ -711,9 +757,15 @@ __device__ __noinline__ void many_kept(const SampleParams& p, Shared& sh, int ph
   };
   auto sweep = [&](auto&& f) {  // f(value, index) for this thread's entries
     if (kFrom == kRow)
-      row.template sweep<2>(f);
+      row.sweep(f);
     else
       sweep_local(f);
+  };
+  auto sweep_weights = [&](auto&& f) {  // f(value, index, weight)
+    if (kFrom == kRow)
+      row.sweep_weights(f);
+    else
+      sweep_local([&](float x, int i) { f(x, i, row.weight(x)); });
   };
   // the sum of the cluster, and this warp's prefix in it by CTA and warp
   auto total = [&](unsigned long long v, uint32_t n, unsigned long long& off, uint32_t& off_n, unsigned long long& all,
@@ -746,15 +798,16 @@ __device__ __noinline__ void many_kept(const SampleParams& p, Shared& sh, int ph
     row.clear();
     {
       uint32_t far = 0;  // of the last bin, which may be most entries: they weigh nothing
-      sweep([&](float f, int i) {
-        if (row.inside(f, i, cut)) {
-          const int b = row.bin_of(f);
-          if (b == kBins - 1)
-            ++far;
-          else
-            row.add(b, by_w, f);
-        }
-      });
+      auto put = [&](float f, int i, unsigned long long w) {
+        const int b = row.bin_of(f);
+        const bool in = row.inside(f, i, cut);
+        if (in & (b == kBins - 1)) ++far;
+        if (in & (b < kBins - 1)) row.add(b, by_w, w);
+      };
+      if (by_w)
+        sweep_weights(put);
+      else
+        sweep([&](float f, int i) { put(f, i, 0); });
       far = __reduce_add_sync(0xffffffffu, far);
       if (lane == 0 && far) atomicAdd(&sh.hist[kBins - 1].x, far);
     }
@@ -769,16 +822,23 @@ __device__ __noinline__ void many_kept(const SampleParams& p, Shared& sh, int ph
     uint32_t n_bin = at.n;
     auto member = [&](float f, int i) {
       const uint32_t k = order_key(f);
-      return k >= lo && k <= hi && row.bin_of(f) == bin1 && row.inside(f, i, cut);
+      return (k >= lo) & (k <= hi) & (row.bin_of(f) == bin1) & row.inside(f, i, cut);
     };
     // (the row's are collected once, and the bin is refined among them)
     bool collected = kFrom == kList;
-    if (kFrom == kRow && n_bin > kNT) {
+    if (kFrom == kRow && (n_bin <= kNT || lo < hi)) {
       __syncthreads();
       if (tid == 0) sh.n = 0;
       __syncthreads();
-      row.sweep([&](float f, int i) {
-        if (member(f, i)) row.collect(f, i);
+      // (by value: `members` looks at the bin and the cut)
+      const float from = key_value(lo), to = key_value(hi);
+      row.sweep_short([&](const uint4& raw, int i0) {
+        float v[E];
+        open_unit(raw, v, (const T*)nullptr);
+        bool any = false;
+#pragma unroll
+        for (int k = 0; k < E; ++k) any |= (v[k] >= from) & (v[k] <= to);
+        if (any) collect_unit<T>(sh, raw, i0, from, to);
       });
       __syncthreads();
       n_local = sh.n;
@@ -798,7 +858,7 @@ __device__ __noinline__ void many_kept(const SampleParams& p, Shared& sh, int ph
     while (n_bin > kNT && lo < hi) {
       const int shift = max(0, 32 - __clz((int)(hi - lo)) - 9);
       row.clear();
-      members([&](float f, int i) { row.add((int)((hi - order_key(f)) >> shift), by_w, f); });
+      members([&](float f, int i) { row.add((int)((hi - order_key(f)) >> shift), by_w, row.weight(f)); });
       unsigned long long g;
       Found in;
       row.find_bin(by_w, [&](unsigned long long) { return goal - before; }, g, in);
@@ -866,11 +926,10 @@ __device__ __noinline__ void many_kept(const SampleParams& p, Shared& sh, int ph
   if (p.out) {
     n = row.write(cut);
   } else {
-    sweep([&](float f, int i) {
-      if (f >= low && row.inside(f, i, cut)) {
-        v += row.weight(f);
-        ++n;
-      }
+    sweep_weights([&](float f, int i, unsigned long long w) {
+      const bool in = (f >= low) & row.inside(f, i, cut);
+      v += in ? w : 0;
+      n += in;
     });
     v = warp_total(v);
   }
@@ -935,7 +994,8 @@ __device__ __noinline__ void many_kept(const SampleParams& p, Shared& sh, int ph
       open_unit(row.load(j), f, (const T*)nullptr);
 #pragma unroll
       for (int k = 0; k < E; ++k) {
-        w[k] = f[k] >= low && row.inside(f[k], i0 + k, cut) ? row.weight(f[k]) : 0;
+        const unsigned long long x = row.weight(f[k]);
+        w[k] = (f[k] >= low) & row.inside(f[k], i0 + k, cut) ? x : 0;
         mine += w[k];
       }
     }
@@ -1089,9 +1149,17 @@ __global__ void __launch_bounds__(kNT, 4) sample_kernel(const SampleParams p) {
     const bool all_of_them = from == -FLT_MAX;
     const float c = by_sum ? sh.weigh.ch : 0.f;
     float sum = 0.f;
-    row.template sweep<8>([&](float f, int i) {
-      if (by_sum) sum += ex2_approx((f - xmax) * c);
-      if (f >= from) row.collect(f, i);
+    row.template sweep_units<8>([&](const uint4& raw, int i0) {
+      float v[E];
+      open_unit(raw, v, (const T*)nullptr);
+      float most = v[0];
+#pragma unroll
+      for (int k = 1; k < E; ++k) most = fmaxf(most, v[k]);
+      if (by_sum) {
+#pragma unroll
+        for (int k = 0; k < E; ++k) sum += ex2_approx((v[k] - xmax) * c);
+      }
+      if (most >= from) collect_unit<T>(sh, raw, i0, from, xmax);
     });
     if (by_sum) {
 #pragma unroll
@@ -1121,7 +1189,7 @@ __global__ void __launch_bounds__(kNT, 4) sample_kernel(const SampleParams p) {
         if (result == kNeedSum) {
           // the border lies within the sum's error: the exact sum
           unsigned long long v = 0;
-          row.sweep([&](float f, int i) { v += row.weight(f); });
+          row.sweep_weights([&](float, int, unsigned long long w) { v += w; });
           const Part* parts = row.tell(Part{row.block_sum(v), 0, 0});
           v = 0;
           for (int r = 0; r < row.C(); ++r) v += parts[r].v;
