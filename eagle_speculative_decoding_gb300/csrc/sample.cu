@@ -153,7 +153,7 @@ struct Weigh {
 
 // What a CTA holds of a row.
 struct Shared {
-  uint4 hist[kBins];  // counts, and three limbs of sums of weights
+  uint32_t hist[4][kBins];  // counts, and three limbs of sums of weights (a bin's four words apart: neighbouring bins in all banks)
   uint2 local[kLocal];  // this CTA's collected entries: (order key, index)
   Entry list[kCap];     // the leader's list
   unsigned long long pow64[64], wv[kNW], wkey[kNW];
@@ -172,12 +172,9 @@ __device__ __forceinline__ uint32_t remote(const void* p, int rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(smem_u32(p)), "r"(rank));
   return ra;
 }
-__device__ __forceinline__ uint4 ld_remote(const uint4* p, int rank) {
-  uint4 v;
-  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(remote(p, rank))
-               : "memory");
+__device__ __forceinline__ uint32_t ld_remote(const uint32_t* p, int rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote(p, rank)) : "memory");
   return v;
 }
 // whole 64-bit words to the same place in the shared memory of CTA `rank`
@@ -401,17 +398,17 @@ struct Row {
     all_n = an;
   }
   __device__ __forceinline__ void clear() {
-    for (int i = threadIdx.x; i < kBins; i += kNT) sh.hist[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = threadIdx.x; i < kBins; i += kNT) reinterpret_cast<uint4*>(sh.hist)[i] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
   }
   __device__ __forceinline__ void add(int b, bool weighted, unsigned long long w) {
-    atomicAdd(&sh.hist[b].x, 1u);
+    atomicAdd(&sh.hist[0][b], 1u);
     if (weighted) {
       constexpr uint32_t mask = (1u << kLimb) - 1;
       const uint32_t w0 = (uint32_t)w & mask, w1 = (uint32_t)(w >> kLimb) & mask, w2 = (uint32_t)(w >> (2 * kLimb));
-      if (w0) atomicAdd(&sh.hist[b].y, w0);
-      if (w1) atomicAdd(&sh.hist[b].z, w1);
-      if (w2) atomicAdd(&sh.hist[b].w, w2);
+      if (w0) atomicAdd(&sh.hist[1][b], w0);
+      if (w1) atomicAdd(&sh.hist[2][b], w1);
+      if (w2) atomicAdd(&sh.hist[3][b], w2);
     }
   }
   __device__ __forceinline__ unsigned long long block_sum(unsigned long long v) {
@@ -432,25 +429,28 @@ struct Row {
     cluster_sync();  // the histograms are complete
     constexpr int B = kBins / kNT;
     const int nb = kBins / C(), per = max(1, nb / kNT);
+    // every word of this CTA's bins over all CTAs
+    static_assert(sizeof(sh.list) >= 4 * kBins * sizeof(unsigned long long), "their sums are where the list will be");
+    unsigned long long* sums = reinterpret_cast<unsigned long long*>(sh.list);
+    for (int x = threadIdx.x; x < (weighted ? 4 : 1) * nb; x += kNT) {
+      const uint32_t* word = &sh.hist[x / nb][blockIdx.x * nb + x % nb];
+      uint32_t h[kMaxCluster];
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) h[r] = r < C() ? ld_remote(word, r) : 0u;
+      unsigned long long a = 0;
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) a += h[r];
+      sums[x] = a;
+    }
+    __syncthreads();
     unsigned long long v[B], mine = 0;
     uint32_t n[B], mine_n = 0;
 #pragma unroll
     for (int i = 0; i < B; ++i) {
-      v[i] = 0;
-      n[i] = 0;
       const int b = (int)threadIdx.x * per + i;
-      if (i < per && b < nb) {
-        uint4 h[kMaxCluster];
-#pragma unroll
-        for (int r = 0; r < kMaxCluster; ++r)
-          if (r < C()) h[r] = ld_remote(&sh.hist[blockIdx.x * nb + b], r);
-#pragma unroll
-        for (int r = 0; r < kMaxCluster; ++r)
-          if (r < C()) {
-            n[i] += h[r].x;
-            v[i] += weighted ? h[r].y + ((unsigned long long)h[r].z << kLimb) + ((unsigned long long)h[r].w << (2 * kLimb)) : h[r].x;
-          }
-      }
+      const bool has = i < per && b < nb;
+      n[i] = has ? (uint32_t)sums[b] : 0u;
+      v[i] = !has ? 0 : weighted ? sums[nb + b] + (sums[2 * nb + b] << kLimb) + (sums[3 * nb + b] << (2 * kLimb)) : n[i];
       mine += v[i];
       mine_n += n[i];
     }
@@ -809,7 +809,7 @@ __device__ __noinline__ void many_kept(const SampleParams& p, Shared& sh, int ph
       else
         sweep([&](float f, int i) { put(f, i, 0); });
       far = __reduce_add_sync(0xffffffffu, far);
-      if (lane == 0 && far) atomicAdd(&sh.hist[kBins - 1].x, far);
+      if (lane == 0 && far) atomicAdd(&sh.hist[0][kBins - 1], far);
     }
     unsigned long long goal = 0;
     Found at;
@@ -1014,7 +1014,7 @@ __device__ __noinline__ void many_kept(const SampleParams& p, Shared& sh, int ph
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kNT, 4) sample_kernel(const SampleParams p) {
+__global__ void __launch_bounds__(kNT, 3) sample_kernel(const SampleParams p) {
   constexpr int E = Unit<T>::E;
   __shared__ Shared sh;
   const int tid = threadIdx.x, at_row = blockIdx.y;
