@@ -2666,14 +2666,16 @@ __global__ void __launch_bounds__(2 * D, kCtas) flat_join_kernel(const JoinParam
   // element e of this thread's four: row and channel
   auto row_of = [&](int e) { return kByRow ? tid / (D / 4) : (tid & 1) * 4 + e; };
   auto chan_of = [&](int e) { return kByRow ? tid % (D / 4) * 4 + e : tid >> 1; };
-  // the eight rows from `first` of the unit (rows of the arrays: at(row)), O in o;
-  // s_own holds their factors
-  auto load_own = [&](int first, int rows, auto&& at, float* own) {
+  // the eight rows from `first` of a unit, whose row 0 is row r0 of the arrays and row
+  // x at(x) rows further; O in o; s_own holds their factors
+  auto load_own = [&](size_t r0, int first, int rows, auto&& at, float* own) {
+    const T* src = static_cast<const T*>(p.own_out) + r0 * D;
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      own[e] = p.own_out && first + row_of(e) < rows ? (float)static_cast<const T*>(p.own_out)[at(first + row_of(e)) * D + chan_of(e)] : 0.f;
+      own[e] = p.own_out && first + row_of(e) < rows ? (float)src[at(first + row_of(e)) * D + chan_of(e)] : 0.f;
   };
-  auto store = [&](int first, int rows, auto&& at, const float* o, const float* own) {
+  auto store = [&](size_t r0, int first, int rows, auto&& at, const float* o, const float* own) {
+    T* dst = static_cast<T*>(a.out) + r0 * D;
     float y[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -2682,12 +2684,11 @@ __global__ void __launch_bounds__(2 * D, kCtas) flat_join_kernel(const JoinParam
       const OwnWeight w = s_own[row];
       y[e] = o[e] * (w.prefix * a.v_scale);
       if (w.own != 0.f) y[e] = w.prefix == 0.f ? own[e] : fmaf(own[e], w.own, y[e]);
-      if constexpr (!kByRow) static_cast<T*>(a.out)[at(first + row) * D + chan_of(e)] = (T)y[e];
+      if constexpr (!kByRow) dst[at(first + row) * D + chan_of(e)] = (T)y[e];
     }
     if constexpr (kByRow) {
       if (first + row_of(0) < rows)
-        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at(first + row_of(0)) * D + chan_of(0)) =
-            make_float4(y[0], y[1], y[2], y[3]);
+        *reinterpret_cast<float4*>(dst + at(first + row_of(0)) * D + chan_of(0)) = make_float4(y[0], y[1], y[2], y[3]);
     }
   };
   pdl_wait();
@@ -2713,8 +2714,9 @@ __global__ void __launch_bounds__(2 * D, kCtas) flat_join_kernel(const JoinParam
           }
           __syncthreads();
           float own[4];
-          load_own(0, rows, [&](int row) { return r + row; }, own);
-          store(0, rows, [&](int row) { return r + row; }, none, own);
+          auto same = [](int row) { return row; };
+          load_own(r, 0, rows, same, own);
+          store(r, 0, rows, same, none, own);
         }
       }
     }
@@ -2746,6 +2748,7 @@ __global__ void __launch_bounds__(2 * D, kCtas) flat_join_kernel(const JoinParam
     splits += s_count[x];
   }
   __syncthreads();
+  const uint32_t g_inv = (65536u + (uint32_t)p.g - 1) / (uint32_t)p.g;
 #pragma unroll 1
   for (int it = (int)blockIdx.x; it < splits * of_split; it += (int)gridDim.x - 1) {
     const int n = it / of_split, chunk = it - n * of_split, c0 = s_first[n];
@@ -2753,9 +2756,12 @@ __global__ void __launch_bounds__(2 * D, kCtas) flat_join_kernel(const JoinParam
     const int rows = u.rows, pieces = u.last - c0 + 1, h = u.h, tok0 = u.tok0;
     const int row0 = chunk * 8;
     if (row0 >= rows) continue;
+    // (rows of a unit are fewer than 2^9, groups of heads no more than 2^6: x / g is
+    // x g_inv >> 16)
+    const size_t r0 = (size_t)tok0 * a.Hq + h * p.g;
     auto to = [&](int row) {
-      const int of_token = row / p.g;
-      return ((size_t)tok0 + of_token) * a.Hq + h * p.g + (row - of_token * p.g);
+      const int of_token = (int)((uint32_t)row * g_inv >> 16);
+      return of_token * a.Hq + (row - of_token * p.g);
     };
     // the unit's first piece is in slot 2 c0 + 1, the others in 2 (c0 + 1), 2 (c0 + 2), ..
     auto slot = [&](int x) { return (size_t)(2 * (c0 + x) + (x == 0 ? 1 : 0)) * p.slot_rows + row0; };
@@ -2764,8 +2770,8 @@ __global__ void __launch_bounds__(2 * D, kCtas) flat_join_kernel(const JoinParam
     for (int i = 0; i < kBatch; ++i)
       if (i < pieces) f[i] = __ldcg(reinterpret_cast<const float4*>(p.o + slot(i) * D) + tid);
     float L = -INFINITY, own[4];
-    load_own(row0, rows, to, own);
-    if (tid < 8 && row0 + tid < rows && p.own_lse) L = p.own_lse[to(row0 + tid)];
+    load_own(r0, row0, rows, to, own);
+    if (tid < 8 && row0 + tid < rows && p.own_lse) L = p.own_lse[r0 + to(row0 + tid)];
     // the weights: thread (x, row) = (tid / 8, tid % 8) of pieces x, x + 2 D / 8, ..
     const int row = tid & 7;
     float sum = 0.f;
@@ -2796,7 +2802,7 @@ __global__ void __launch_bounds__(2 * D, kCtas) flat_join_kernel(const JoinParam
 #pragma unroll
       for (int x = 1; x < kWarps; ++x) sum += s_sum[x][tid];
       s_own[tid] = own_weight(top, sum, L);
-      if (a.lse) a.lse[to(row0 + tid)] = s_own[tid].lse;  // (this thread alone read own_lse, which it may be)
+      if (a.lse) a.lse[r0 + to(row0 + tid)] = s_own[tid].lse;  // (this thread alone read own_lse, which it may be)
     }
     float o[4] = {};
     for (int x0 = 0; x0 < pieces; x0 += kBatch) {
@@ -2814,7 +2820,7 @@ __global__ void __launch_bounds__(2 * D, kCtas) flat_join_kernel(const JoinParam
         }
     }
     __syncthreads();
-    store(row0, rows, to, o, own);
+    store(r0, row0, rows, to, o, own);
   }
 }
 
