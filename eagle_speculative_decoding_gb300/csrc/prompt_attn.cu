@@ -32,9 +32,6 @@
 
 #include "common.cuh"
 #include "kv4.cuh"
-#ifndef FLAT_ONE
-#define FLAT_ONE 256
-#endif
 
 namespace eagle {
 namespace {
@@ -430,8 +427,13 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanPar
 struct __align__(16) Split {  // a unit that starts in a CTA's part and ends in CTA `last`'s
   int rows, last, h, tok0;   // rows: 0 if there is none
 };
-constexpr int kFlatLeast = 2, kFlatLeastF32 = 1;  // blocks of a part at least
-constexpr int kFlatMore = 3;  // blocks by which a part may grow for whole units
+// (A part has one block at least.  With two at least, calls of 300 to 1,000 keys and
+// up to 128 tokens took 0.3 to 2 us more; only units of two blocks, which nobody joins
+// then, 1.2 less.)
+// By how many blocks a part may grow for whole units.  32 + 8 heads, D 128, 3 / none:
+// 64 and 256 tokens over 2,400 keys 15.9 / 17.5 and 26 / 28.5 us, 1,024 over 2,000
+// 41 / 55; with 8, 1,024 over 4,800 is 76 and not 86, but 400 over 8,000 71 and not 64.
+constexpr int kFlatMore = 3;
 struct Groups {  // a warp's view: lane i holds group base + i (of one group, all lanes have it)
   int c0, n, len;     // first row, rows, keys (0 if the group is in error)
   int units, blocks;  // units: of all kv heads
@@ -487,11 +489,11 @@ struct FlatWalk {
   __device__ __forceinline__ long long line(const Groups& x) const {  // a group's stretch of it
     return (long long)x.units * (snap ? (x.blocks + per - 1) / per * per : x.blocks);
   }
-  __device__ __forceinline__ void start(const AttnParams& a, int tpu, int least, bool report) {
+  __device__ __forceinline__ void start(const AttnParams& a, int tpu, bool report) {
     const int ctas = (int)gridDim.x;
     g = load_groups(a, 0, tpu, report);
     left = 0;
-    per = least;
+    per = 1;
     snap = false;
     bool falls = g.falls;
     if (a.B > 1) {
@@ -504,7 +506,7 @@ struct FlatWalk {
       // one group and a short line, as in most calls: the same in plain ints (a CTA's
       // first loads wait for this: 0.9 us the other way)
       const int units = g.units, blocks = g.blocks, all = units * blocks;
-      const int even = max(least, quotient(all + ctas - 1, ctas));
+      const int even = max(1, quotient(all + ctas - 1, ctas));
       per = even;
       int parts = 0;
       for (int more = 0; more <= kFlatMore && !snap; ++more) {
@@ -523,7 +525,7 @@ struct FlatWalk {
       return;
     }
     const long long all = sum_groups(a, tpu, g, [](const Groups& x) { return (long long)x.units * x.blocks; });
-    const int even = (int)max((long long)least, quotient(all + ctas - 1, ctas));  // (lines of 2^31 blocks would be 2^38 keys)
+    const int even = (int)max(1ll, quotient(all + ctas - 1, ctas));  // (lines of 2^31 blocks would be 2^38 keys)
     per = even;
     for (int more = 0; more <= kFlatMore && !snap; ++more) {
       const int p = even + more;
@@ -1314,7 +1316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ----------------------------------------------------------- scheduler
       if constexpr (FLAT) {
         FlatWalk walk;
-        walk.start(a, p.tpu, kFlatLeast, blockIdx.x == 0);
+        walk.start(a, p.tpu, blockIdx.x == 0);
         Piece w;
         w.slot = -1;
         for (int ps = 0;; ++ps) {
@@ -2436,7 +2438,7 @@ __global__ void __launch_bounds__(256, (CfgF32<D, RT>::kCtas)) prompt_attn_f32_k
   FlatWalk walk;
   if (FLAT && tid < 32) {
     // (walked twice: what the join needs is in the part's last piece)
-    walk.start(a, p.tpu, kFlatLeastF32, blockIdx.x == 0);
+    walk.start(a, p.tpu, blockIdx.x == 0);
     const FlatWalk from = walk;
     Piece w;
     w.slot = -1;
@@ -2932,7 +2934,7 @@ int attn_launch_f32(const AttnParams& a, void* ws, cudaStream_t s) {
 }
 
 // Shared prefixes.  Units are those of the tensor-core or the fp32 path, or of one
-// tile of the former (kTile).
+// tile of the former.
 struct FlatShape {
   int g, tpt, tpu, rows, ctas;
   size_t off_ml, off_o, total;  // the splits first
@@ -2957,8 +2959,15 @@ FlatWs flat_ws(const FlatShape& sh, void* ws) {
   char* w = reinterpret_cast<char*>(round_up(reinterpret_cast<size_t>(ws), 256));
   return {reinterpret_cast<Split*>(w), reinterpret_cast<float2*>(w + sh.off_ml), reinterpret_cast<float*>(w + sh.off_o)};
 }
-// Few rows of all groups together: units of one tile.
-bool flat_one_tile(int T, int Hq, int Hkv) { return (long long)T * (Hq / Hkv) <= FLAT_ONE; }
+// Few rows of all groups together: units of one tile, whose key blocks both tiles'
+// warps share, so that there are twice as many, shorter pieces.  32 + 8 heads, D 128,
+// one tile / two, us: 64 tokens (256 rows of a kv head) over 500, 2,000 and 8,000 keys
+// 13.4 / 15.7, 14.3 / 16.3, 19.9 / 20.5, in 4-bit pages 16.9 / 20.0, 17.8 / 21.1, 25.4 /
+// 26.5; 128 tokens 14.8 / 16.9, 17.6 / 18.8, 28.9 / 27.2; 256 tokens over 8,000 46.7 /
+// 44.1, 1,024 over 500 34.6 / 21.2 (keys are read and brought to shared memory twice as
+// often).
+constexpr int kOneTileRows = 256;
+bool flat_one_tile(int T, int Hq, int Hkv) { return (long long)T * (Hq / Hkv) <= kOneTileRows; }
 struct Own {
   const void* out;
   const float* lse;
@@ -2970,6 +2979,10 @@ int flat_join(const AttnParams& a, const Own& own, const FlatShape& sh, const Fl
   const int sms = std::max(1, sm_count());
   const long long units = ((long long)a.T + (long long)std::min(a.B, a.T) * (sh.tpu - 1)) / sh.tpu * a.Hkv;
   const long long chunks = std::min<long long>(units, sh.ctas) * (sh.rows / 8);
+  // Few chunks, two a SM at most: 20 pieces' loads at a time and all their CTAs at once,
+  // since the chain of loads is what they wait for (64 tokens over 8,000 keys 20.0 us,
+  // 4 over 32,768 35.3; the other way 22.0 and 38.6).  More: two pieces at a time, for
+  // more CTAs a SM (2,000 rows in 24 groups 128 us, 158 the first way).
   constexpr int kFew = 2, kMany = 640 / D;
   if (chunks <= (long long)kFew * sms)
     launch(flat_join_kernel<D, T, 20, 256 / D>, (int)chunks + 1, 2 * D, 0, s, jp);
