@@ -31,10 +31,26 @@
 //                fp32, which settles the border unless the sum's error reaches across
 //                it; then the exact sum is taken.
 //   many         For a cut, a histogram over the distance from the maximum (counts, or
-//                sums of exact weights, 40 instructions each) finds the bin that it lies
-//                in, which is refined until its entries are few enough for one CTA, or
-//                equal; equal entries are cut by their index.  After a top-k the CTAs
-//                go on with the entries that they collected, otherwise with the row.
+//                weights to 16 bits of their bin's, one addition each) finds the bin that
+//                it lies in, or the few that it may.  One pass with exact weights adds up
+//                what lies in front of them and the whole, and collects their entries,
+//                among which they are refined until they are few enough for one CTA, or
+//                equal; equal entries are cut by their index.  What lies in front is kept,
+//                so that a token's running sums need no further pass.  After a top-k the
+//                CTAs go on with the entries that they collected, otherwise with the row.
+//
+// What bounds it: one row, the chain of loads, cluster barriers (1 us each) and first
+// fetches of its code: 128,256 entries, bf16, top-k 50 and top-p 0.95 12 us in a graph
+// (first pass 2.5, threshold and barrier 2.5, second pass 2.5, list 5).  Rows that
+// keep many, the instructions of the exact weights (some 75 an entry, a third of the
+// stalls waiting for instructions): a row of 128,256 whose top-p keeps half of it 55
+// us, 64 of them 112.  Copies in flight to shared memory, rings of loads in registers
+// and shorter loops changed none of that, and sums of exact weights in the bins, four
+// additions an entry, took as long.
+// Four CTAs an SM at 64 registers against three at 80: 64 rows of top-p 0.95 112 us and
+// 156, of top-k 50 29 and 35, 256 rows of mixed settings truncated 134 and 152; 17 rows
+// of 50,257 57.4 and 54.5.  Clusters of four CTAs took 16 % less for 256 rows, and a
+// half more for one row that keeps many.
 #include <float.h>
 #include <math.h>
 
@@ -71,7 +87,8 @@ __device__ __constant__ const uint32_t kPow4096[64] = {
     2914962046u};
 
 constexpr int kNT = 256, kNW = kNT / 32;
-constexpr int kBins = 512;
+constexpr int kBins = 512;       // of a bin that is refined
+constexpr int kFine = 2048;      // of a whole row
 constexpr int kCap = 1024;       // entries that one CTA sorts
 constexpr int kLocal = 1536;     // entries that a CTA collects
 constexpr int kMaxVocab = 1 << 18;
@@ -81,6 +98,10 @@ constexpr int kMaxCluster = 8;
 // Of the row's sum in fp32, relative: an entry's exponent y <= 45 in three roundings
 // (0.7 * 3 * 45 * 2^-24), its exponential (2^-22), and up to 128 + 21 additions.
 constexpr float kSumError = 3.0517578125e-5f;
+// Of sums over the row's bins, relative: a weight is the bin's times 16 bits (2^-17, its
+// exponential 2^-22), its place in units of the exponent up to 45 is off by 2^-22 of
+// itself (2^-17), the bin's weight by 2^-24 of that exponent (2^-19).
+constexpr double kBinError = 3.0517578125e-5;
 
 struct SampleParams {
   const void* x;
@@ -103,6 +124,7 @@ struct Entry {  // of the sorted list
 struct Part {  // what a CTA tells the others
   unsigned long long v;
   unsigned int n, flags;
+  unsigned long long w;
 };
 struct Found {  // the bin that a search ends at
   unsigned long long before;  // measure before it
@@ -153,17 +175,21 @@ struct Weigh {
 
 // What a CTA holds of a row.
 struct Shared {
-  uint32_t hist[4][kBins];  // counts, and three limbs of sums of weights (a bin's four words apart: neighbouring bins in all banks)
+  // counts, and three limbs of sums of weights (a bin's four words apart: neighbouring
+  // bins in all banks); or a word each of kFine bins
+  uint32_t hist[4][kBins];
   uint2 local[kLocal];  // this CTA's collected entries: (order key, index)
   Entry list[kCap];     // the leader's list
   unsigned long long pow64[64], wv[kNW], wkey[kNW];
-  uint32_t pow4096[64], wn[kNW];
+  unsigned long long kept_w[kNW];  // of the warps' ranges: what is kept, its weights and number
+  uint32_t pow4096[64], wn[kNW], kept_n[kNW];
   float wsum[kNW];
   Part part[2][kMaxCluster];
   Found found;
+  unsigned long long range[2];  // bins
   Cut cut;
   Weigh weigh;
-  float bins, low, temp, top_p, u;  // bins: per distance
+  float bins, width, low, temp, top_p, u;  // bins per distance, and a bin's width in powers of two
   int top_k, n;
 };
 
@@ -363,16 +389,17 @@ struct Row {
     return to;
   }
   __device__ __forceinline__ unsigned long long weight(float f) const { return sh.weigh(f, sh.pow64, sh.pow4096); }
-  // bin of an entry by its distance from the maximum: 511 up to where weights vanish
-  __device__ __forceinline__ int bin_of(float f) const { return min((int)((sh.weigh.xmax - f) * sh.bins), kBins - 1); }
+  // place of an entry among the kFine bins by its distance from the maximum: in front of
+  // the last up to where weights vanish
+  __device__ __forceinline__ float place(float f) const { return fminf((sh.weigh.xmax - f) * sh.bins, (float)(kFine - 1)); }
   // keys that bin b's entries lie between, with room for the roundings
   __device__ __forceinline__ void keys_of(int b, uint32_t& lo, uint32_t& hi) const {
     const float xmax = sh.weigh.xmax;
     float from = -FLT_MAX, to = xmax;
-    if (sh.bins > 0.f && sh.bins < INFINITY) {
+    if (sh.bins > 0.f) {
       const float d0 = (float)b / sh.bins, d1 = (float)(b + 1) / sh.bins;
       to = fminf(to, xmax - d0 + 1e-6f * (fabsf(xmax) + d0));
-      if (b < kBins - 1) from = fmaxf(from, xmax - d1 - 1e-6f * (fabsf(xmax) + d1));
+      if (b < kFine - 1) from = fmaxf(from, xmax - d1 - 1e-6f * (fabsf(xmax) + d1));
     }
     lo = order_key(from);
     hi = order_key(to);
@@ -476,6 +503,60 @@ struct Row {
     }
     cluster_sync();
     at = sh.found;
+    return true;
+  }
+  // Of the kFine bins those in which the cluster's running measure passes the goal, top_k
+  // or top_p's part of the sum, whose sums of weights are within kBinError of the true
+  // ones.  False if there are fewer than top_k entries.
+  __device__ __forceinline__ bool find_range(bool weighted, int& first, int& last) {
+    cluster_sync();  // the histograms are complete
+    const int nb = kFine / C(), per = nb / kNT, b0 = (int)blockIdx.x * nb;
+    static_assert(kFine % (kMaxCluster * kNT) == 0 && sizeof(sh.hist) >= 4 * kFine && sizeof(sh.list) >= 8 * kFine, "a CTA's bins");
+    unsigned long long* sums = reinterpret_cast<unsigned long long*>(sh.list);
+    const Weigh edge{0.f, sh.width, 0.f};
+#pragma unroll 1
+    for (int x = threadIdx.x; x < nb; x += kNT) {
+      const uint32_t* word = sh.hist[0] + b0 + x;
+      uint32_t h[kMaxCluster];
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) h[r] = r < C() ? ld_remote(word, r) : 0u;
+      unsigned long long a = 0;
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) a += h[r];
+      if (weighted) a = __double2ull_rn((double)a * (double)edge(-(float)(b0 + x), sh.pow64, sh.pow4096) * 0x1p-16);
+      sums[x] = a;
+    }
+    __syncthreads();
+    unsigned long long mine = 0, before, sum;
+    uint32_t bn, an;
+    for (int i = 0; i < per; ++i) mine += sums[(int)threadIdx.x * per + i];
+    block_scan(mine, 0, before, bn, sum, an);
+    const Part* parts = tell(Part{sum, 0, 0, 0});
+    sum = 0;
+    for (int r = 0; r < C(); ++r) {
+      if (r < (int)blockIdx.x) before += parts[r].v;
+      sum += parts[r].v;
+    }
+    unsigned long long from = (unsigned long long)sh.top_k, to = from;
+    if (weighted) {
+      const double g = (double)sh.top_p * (double)sum;
+      from = max(1ull, __double2ull_rd(g * (1.0 - 2 * kBinError)));
+      to = __double2ull_ru(g * (1.0 + 2 * kBinError)) + 1;
+    } else if (to > sum) {
+      return false;
+    }
+    for (int i = 0; i < per; ++i) {
+      const int x = (int)threadIdx.x * per + i;
+      const unsigned long long end = before + sums[x];
+      for (int r = 0; r < C(); ++r) {
+        if (before < from && from <= end) st_remote(&sh.range[0], r, (unsigned long long)(b0 + x));
+        if (before < to && to <= end) st_remote(&sh.range[1], r, (unsigned long long)(b0 + x));
+      }
+      before = end;
+    }
+    cluster_sync();
+    first = (int)sh.range[0];
+    last = to > sum ? kFine - 1 : (int)sh.range[1];
     return true;
   }
   // list[0 .. n) of the leader by key ascending
@@ -755,12 +836,6 @@ __device__ __noinline__ void many_kept(const SampleParams& p, Shared& sh, int ph
       f(key_value(e.x), (int)e.y);
     }
   };
-  auto sweep = [&](auto&& f) {  // f(value, index) for this thread's entries
-    if (kFrom == kRow)
-      row.sweep(f);
-    else
-      sweep_local(f);
-  };
   auto sweep_weights = [&](auto&& f) {  // f(value, index, weight)
     if (kFrom == kRow)
       row.sweep_weights(f);
@@ -790,6 +865,9 @@ __device__ __noinline__ void many_kept(const SampleParams& p, Shared& sh, int ph
     }
   };
   const bool use_k = sh.top_k > 0 && sh.top_k < p.V, use_p = sh.top_p < 1.f;
+  // the values between which a stage by weights has collected the row's entries, with the
+  // sums over those in front in kept_w and kept_n (none: from > to)
+  float col_from = 1.f, col_to = 0.f;
 #pragma unroll 1
   for (int stage = 0; stage < 2; ++stage) {
     const bool by_w = stage == 1;
@@ -798,54 +876,87 @@ __device__ __noinline__ void many_kept(const SampleParams& p, Shared& sh, int ph
     row.clear();
     {
       uint32_t far = 0;  // of the last bin, which may be most entries: they weigh nothing
-      auto put = [&](float f, int i, unsigned long long w) {
-        const int b = row.bin_of(f);
-        const bool in = row.inside(f, i, cut);
-        if (in & (b == kBins - 1)) ++far;
-        if (in & (b < kBins - 1)) row.add(b, by_w, w);
+      uint32_t* hist = sh.hist[0];
+      auto put = [&](float f, int i) {
+        const float at = row.place(f);
+        const int b = (int)at;
+        const bool in = row.inside(f, i, cut), last = b == kFine - 1;
+        far += in & last;
+        // (2^16 entries of a CTA at most)
+        if (in & !last) atomicAdd(&hist[b], by_w ? __float2uint_rn(ex2_approx(((float)b - at) * sh.width) * 65535.f) : 1u);
       };
-      if (by_w)
-        sweep_weights(put);
+      if (kFrom == kRow)
+        row.sweep(put);
       else
-        sweep([&](float f, int i) { put(f, i, 0); });
+        sweep_local(put);
       far = __reduce_add_sync(0xffffffffu, far);
-      if (lane == 0 && far) atomicAdd(&sh.hist[0][kBins - 1], far);
+      if (!by_w && lane == 0 && far) atomicAdd(&hist[kFine - 1], far);
     }
-    unsigned long long goal = 0;
-    Found at;
-    auto target = [&](unsigned long long s) { return by_w ? row.part_of(s) : (unsigned long long)sh.top_k; };
-    if (!row.find_bin(by_w, target, goal, at)) continue;  // fewer than k entries
-    const int bin1 = (int)at.bin;
-    uint32_t lo, hi;
-    row.keys_of(bin1, lo, hi);
-    unsigned long long before = at.before;
-    uint32_t n_bin = at.n;
-    auto member = [&](float f, int i) {
-      const uint32_t k = order_key(f);
-      return (k >= lo) & (k <= hi) & (row.bin_of(f) == bin1) & row.inside(f, i, cut);
+    int b0, b1;
+    if (!row.find_range(by_w, b0, b1)) continue;  // fewer than k entries
+    // Exactly, then: what lies in front of those bins, the sum of all, and the entries
+    // between (the row's are collected once, if they have room).
+    uint32_t lo, hi, none;
+    row.keys_of(b0, none, hi);
+    row.keys_of(b1, lo, none);
+    const float from = key_value(lo), to = key_value(hi);
+    unsigned long long front = 0, sum = 0;
+    uint32_t n_bin = 0, n_front = 0;
+    auto measure = [&](float f, int i, unsigned long long w) {
+      const bool in = row.inside(f, i, cut);
+      front += in & (f > to) ? w : 0;
+      n_front += in & (f > to);
+      sum += in ? w : 0;
+      n_bin += in & (f >= from) & (f <= to);
     };
-    // (the row's are collected once, and the bin is refined among them)
-    bool collected = kFrom == kList;
-    if (kFrom == kRow && (n_bin <= kNT || lo < hi)) {
+    if (kFrom == kRow) {
       __syncthreads();
       if (tid == 0) sh.n = 0;
       __syncthreads();
-      // (by value: `members` looks at the bin and the cut)
-      const float from = key_value(lo), to = key_value(hi);
       row.sweep_short([&](const uint4& raw, int i0) {
         float v[E];
         open_unit(raw, v, (const T*)nullptr);
-        bool any = false;
+        unsigned long long w[E];
 #pragma unroll
-        for (int k = 0; k < E; ++k) any |= (v[k] >= from) & (v[k] <= to);
-        if (any) collect_unit<T>(sh, raw, i0, from, to);
+        for (int k = 0; k < E; ++k) w[k] = by_w ? row.weight(v[k]) : (unsigned long long)(v[k] > -INFINITY);
+        const uint32_t n = n_bin;
+#pragma unroll
+        for (int k = 0; k < E; ++k) measure(v[k], i0 + k, w[k]);
+        if (n_bin != n) collect_unit<T>(sh, raw, i0, from, to);
       });
-      __syncthreads();
-      n_local = sh.n;
-      const Part* parts = row.tell(Part{0, (unsigned)n_local, 0});
-      collected = true;
-      for (int r = 0; r < C; ++r) collected = collected && parts[r].n <= kLocal;
+    } else {
+      sweep_local([&](float f, int i) { measure(f, i, by_w ? row.weight(f) : 1ull); });
     }
+    front = warp_total(front);
+    n_bin = __reduce_add_sync(0xffffffffu, n_bin);
+    n_front = __reduce_add_sync(0xffffffffu, n_front);
+    if (lane == 0) sh.kept_w[warp] = front, sh.kept_n[warp] = n_front;
+    sum = row.block_sum(sum);  // (and all of the row's are collected)
+    if (kFrom == kRow) n_local = sh.n;
+    __syncthreads();
+    if (lane == 0) sh.wv[warp] = front, sh.wn[warp] = n_bin;
+    __syncthreads();
+    front = 0;
+    n_bin = 0;
+#pragma unroll
+    for (int w = 0; w < kNW; ++w) front += sh.wv[w], n_bin += sh.wn[w];
+    const Part* parts = row.tell(Part{front, n_bin, n_local > kLocal, sum});
+    unsigned long long before = 0;
+    sum = 0;
+    n_bin = 0;
+    bool collected = true;
+    for (int r = 0; r < C; ++r) {
+      before += parts[r].v;
+      n_bin += parts[r].n;
+      sum += parts[r].w;
+      collected = collected && !parts[r].flags;
+    }
+    if (kFrom == kRow && by_w && collected) col_from = from, col_to = to;
+    const unsigned long long goal = by_w ? row.part_of(sum) : (unsigned long long)sh.top_k;
+    auto member = [&](float f, int i) {
+      const uint32_t k = order_key(f);
+      return (k >= lo) & (k <= hi) & row.inside(f, i, cut);
+    };
     auto members = [&](auto&& f) {  // f(value, index) of the bin's entries
       auto if_member = [&](float x, int i) {
         if (member(x, i)) f(x, i);
@@ -923,17 +1034,31 @@ __device__ __noinline__ void many_kept(const SampleParams& p, Shared& sh, int ph
   const float low = sh.low;
   uint32_t n = 0;
   unsigned long long v = 0;
-  if (p.out) {
-    n = row.write(cut);
-  } else {
-    sweep_weights([&](float f, int i, unsigned long long w) {
-      const bool in = (f >= low) & row.inside(f, i, cut);
-      v += in ? w : 0;
-      n += in;
+  if (!p.out && col_from <= col_to && low <= col_to) {
+    // those in front of what was collected are summed up already
+    __syncthreads();
+    sweep_local([&](float f, int i) {
+      if ((f >= col_from) & (f >= low) & row.inside(f, i, cut)) {
+        const int w = (i + row.lead) / E / p.units - (int)blockIdx.x * kNW;
+        atomicAdd(&sh.kept_w[w], row.weight(f));
+        atomicAdd(&sh.kept_n[w], 1u);
+      }
     });
+    __syncthreads();
+    v = sh.kept_w[warp];
+    n = sh.kept_n[warp];
+  } else {
+    if (p.out)
+      n = row.write(cut);
+    else
+      sweep_weights([&](float f, int i, unsigned long long w) {
+        const bool in = (f >= low) & row.inside(f, i, cut);
+        v += in ? w : 0;
+        n += in;
+      });
     v = warp_total(v);
+    n = __reduce_add_sync(0xffffffffu, n);
   }
-  n = __reduce_add_sync(0xffffffffu, n);
   unsigned long long off, all;
   uint32_t off_n, all_n;
   total(v, n, off, off_n, all, all_n);
@@ -1014,7 +1139,7 @@ __device__ __noinline__ void many_kept(const SampleParams& p, Shared& sh, int ph
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kNT, 3) sample_kernel(const SampleParams p) {
+__global__ void __launch_bounds__(kNT, 4) sample_kernel(const SampleParams p) {
   constexpr int E = Unit<T>::E;
   __shared__ Shared sh;
   const int tid = threadIdx.x, at_row = blockIdx.y;
@@ -1127,7 +1252,8 @@ __global__ void __launch_bounds__(kNT, 3) sample_kernel(const SampleParams p) {
     const float ch = fminf(1.44269502f / temp, 3.0e38f);
     const float cl = ch < 3.0e38f ? (fmaf(-ch, temp, 1.44269502f) + 1.92596303e-8f) / temp : 0.f;
     sh.weigh = Weigh{xmax, ch, isfinite(cl) ? cl : 0.f};
-    sh.bins = (float)(kBins - 1) / ((float)(kOne + 1) + 0.01f) * ch;
+    sh.bins = fminf((float)(kFine - 1) / ((float)(kOne + 1) + 0.01f) * ch, 3.0e38f);
+    sh.width = ch / sh.bins;
     // w >= min_p as a border of x: the smallest fp32 number not below max + T log(min_p)
     float low = -FLT_MAX;
     if (min_p > 0.f) {

@@ -960,7 +960,9 @@ int eagle_draft_prompt(const void* x, const void* w_norm1, const void* w_qkv, co
  * Entries of minus infinity are never kept.  Weights are whole multiples of 2^-44
  * (good to 2^-36 of themselves) with exact sums, so a result does not depend on
  * the order of summation; entries below 2^-45 weigh nothing, nor does one that
- * lies further below the maximum than fp32 reaches.
+ * lies further below the maximum than fp32 reaches.  (Sums are off by V 2^-45 at
+ * most: where a top_p next to 1 ends among weights as small as that, it may end a
+ * few entries from where the formula does.)
  *   logits : rows of V entries, row_stride elements apart, dtype `dtype`; a row
  *            may start at any element
  *   temperature, top_k, top_p, min_p : one entry per request, row r reads entry

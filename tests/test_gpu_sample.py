@@ -219,3 +219,43 @@ def test_many_rows():
     b.eagle_sample(x, torch.from_numpy(u).cuda(), tok, top_p=torch.full((M,), 0.9, device="cuda"))
     xs = x.double().cpu().numpy()
     assert tok.tolist() == [oracle.sample(xs[r], float(u[r]), top_p=float(F(0.9)))[0] for r in range(M)]
+
+
+@pytest.mark.parametrize("V,dtype", [(20011, "fp32"), (128256, "bf16"), (262144, "fp32"), (262144, "bf16")])
+@pytest.mark.parametrize("kind", ["power", "equal", "few", "spread"])
+def test_many_kept_with_borders_near_one_another(kind, V, dtype):
+    """Top-p cuts of many entries with min-p in front of them, behind them and among them,
+    behind a top-k, at the ends of temperature's range."""
+    b = need_gpu()
+    rows = [(1.3, 0, 0.95, 1e-3), (1.3, 0, 0.95, 1e-12), (1.0, 0, 0.99, 1e-5), (1.0, 0, 1 - 2.0 ** -15, 0.0),
+            (1.0, 20000, 0.97, 0.0), (2.0, 60000, 0.999, 1e-6), (1e-30, 0, 0.9, 0.0), (1e-38, 0, 0.5, 0.0), (3e38, 0, 0.25, 0.0), (40.0, 0, 0.75, 0.0)]
+    x = make(kind, len(rows), V, dtype, V + len(kind)).cuda()
+    check(b, x, rows, uniforms(len(rows), V))
+
+
+@pytest.mark.parametrize("V,dtype", [(20011, "fp32"), (128256, "bf16"), (262144, "fp32"), (262144, "bf16")])
+@pytest.mark.parametrize("kind", ["power", "equal", "few", "spread", "flat"])
+def test_top_p_next_to_one_of_many(kind, V, dtype):
+    """p = 1 - 2^-24, which leaves out 2^-24 of the sum S.  A weight is off by 2^-45 (half a
+    unit) and 2^-36 of itself, so S, and a sum in front of an entry, by at most e = V 2^-45
+    + 2^-36 S, and the two borders, p S and that sum, by 2 e from one another.  What is kept is
+    the head of the order, and its last entry the last in front of p S within 2 e."""
+    b = need_gpu()
+    temps = (0.3, 1.0, 2.5)
+    x = make(kind, len(temps), V, dtype, V + len(kind)).cuda()
+    s = settings_of([(t, 0, 1 - 2.0 ** -24, 0.0) for t in temps])
+    n, st = torch.empty(len(temps), dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32).cuda()
+    out = b.eagle_truncate_logits(x, torch.empty_like(x), n_kept=n, status=st, **s).double().cpu().numpy()
+    tok, n2 = torch.empty_like(n), torch.empty_like(n)
+    b.eagle_sample(x, torch.full((len(temps),), 1 - 2.0 ** -24, device="cuda"), tok, n_kept=n2, status=st, **s)
+    assert st.item() == 0 and torch.equal(n, n2)
+    for r, t in enumerate(temps):
+        row, m = x[r].double().cpu().numpy(), n[r].item()
+        order = np.lexsort((np.arange(V), -row))
+        kept = np.zeros(V, bool)
+        kept[order[:m]] = True
+        assert np.array_equal(out[r], np.where(kept, row, -np.inf)) and kept[tok[r].item()]
+        run = np.concatenate([[0.0], np.cumsum(np.exp((row[order] - row.max()) / float(F(t))))])
+        e = V * 2.0 ** -45 + 2.0 ** -36 * run[-1]
+        border = (1 - 2.0 ** -24) * run[-1]
+        assert run[m - 1] < border + 2 * e and run[m] > border - 2 * e, (t, m, run[m - 1] - border, run[m] - border, e)
