@@ -108,7 +108,7 @@ __device__ __forceinline__ void store4(const float* x, float inv, bool live, uin
 // heads read them as vectors: D/2 gathers a row and not (Hq + Hkv) D/2, whatever
 // the order of the axes.  Their chain of three loads (axis, position, table) is the
 // longest of a row, so it is issued before the rows' loads, and by other warps than
-// the lookup of the request: 8,300 rows of 32 + 2 x 8 heads, D 128, bf16 36 us, 5.6
+// the lookup of the request: 8,085 rows of 32 + 2 x 8 heads, D 128, bf16 36 us, 5.6
 // TB/s (42 us behind the rows' loads and in the lookup's warp, 40 beside it).
 template <typename T, int D, bool KV4, bool AXES>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams p) {

@@ -24,6 +24,9 @@
 //           (one CTA per SM, tcgen05), or for single tokens the few-rows kernel
 //   merge   joins the pieces of cut units (few rows: their last CTA does)
 // fp32 rows: the same list and merge around a kernel on the CUDA cores.
+//
+// Rows that share a prefix (FLAT): the two-tile and the fp32 kernel without a plan in
+// front, and a join that brings in the rows' own attention (below).
 #include <float.h>
 #include <math.h>
 
@@ -424,6 +427,15 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PlanPar
 // leaves a partial result (slot 2 c + 1 for the piece that a unit starts with, at
 // most one per CTA, 2 c for one that it goes on with), and the CTA that it starts in
 // describes it to flat_join_kernel, which joins them.
+//
+// What bounds it (32 + 8 heads, D 128, in a graph): few rows, the chain of a start and
+// two key blocks a CTA, and the join behind it: 64 tokens over 8,000 keys 20 us, of which
+// the pieces are known after 1.6, S of the first block after 3.6, a block takes 2, the
+// last piece ends at 13 and the join takes 5 (the plan and merge of eagle_prompt_attn
+// would be 12 in front and behind; the keys' bytes are 5 us).  4 tokens over 32,768 keys
+// 36 us, 3.8 TB/s.  Many rows, the chain S - softmax - P V: 1,885 rows of two
+// groups over 3,808 and 4,333 keys 128 us, 0.98 PFLOP/s (main kernel 115 from a cold L2,
+// join 24, of which half shows).
 struct __align__(16) Split {  // a unit that starts in a CTA's part and ends in CTA `last`'s
   int rows, last, h, tok0;   // rows: 0 if there is none
 };
@@ -2982,7 +2994,7 @@ int flat_join(const AttnParams& a, const Own& own, const FlatShape& sh, const Fl
   // Few chunks, two a SM at most: 20 pieces' loads at a time and all their CTAs at once,
   // since the chain of loads is what they wait for (64 tokens over 8,000 keys 20.0 us,
   // 4 over 32,768 35.3; the other way 22.0 and 38.6).  More: two pieces at a time, for
-  // more CTAs a SM (2,000 rows in 24 groups 128 us, 158 the first way).
+  // more CTAs a SM (1,885 rows in two groups 128 us, 158 the first way).
   constexpr int kFew = 2, kMany = 640 / D;
   if (chunks <= (long long)kFew * sms)
     launch(flat_join_kernel<D, T, 20, 256 / D>, (int)chunks + 1, 2 * D, 0, s, jp);

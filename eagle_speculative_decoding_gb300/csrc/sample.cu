@@ -448,11 +448,10 @@ struct Row {
     for (int w = 0; w < kNW; ++w) v += sh.wv[w];
     return v;
   }
-  // The bin at which the cluster's running measure (counts, or sums of weights) reaches
-  // goal(sum of all): before < goal <= before + bin's.  A CTA adds up an eighth of the
-  // bins over all the histograms.  False if the goal is not reached.
-  template <typename G>
-  __device__ __forceinline__ bool find_bin(bool weighted, G&& goal_of, unsigned long long& goal, Found& at) {
+  // Of the kBins bins the one at which the cluster's running measure (counts, or sums of
+  // weights) reaches goal (which some bin does): before < goal <= before + the bin's.  A
+  // CTA adds up an eighth of the bins over all the histograms.
+  __device__ __forceinline__ Found find_bin(bool weighted, unsigned long long goal) {
     cluster_sync();  // the histograms are complete
     constexpr int B = kBins / kNT;
     const int nb = kBins / C(), per = max(1, nb / kNT);
@@ -485,13 +484,7 @@ struct Row {
     uint32_t before_n, all_n;
     block_scan(mine, mine_n, before, before_n, sum, all_n);
     const Part* parts = tell(Part{sum, all_n, 0});
-    sum = 0;
-    for (int r = 0; r < C(); ++r) {
-      if (r < (int)blockIdx.x) before += parts[r].v, before_n += parts[r].n;
-      sum += parts[r].v;
-    }
-    goal = goal_of(sum);
-    if (goal > sum) return false;
+    for (int r = 0; r < (int)blockIdx.x; ++r) before += parts[r].v, before_n += parts[r].n;
 #pragma unroll
     for (int i = 0; i < B; ++i) {
       if (before < goal && goal <= before + v[i]) {
@@ -502,8 +495,7 @@ struct Row {
       before_n += n[i];
     }
     cluster_sync();
-    at = sh.found;
-    return true;
+    return sh.found;
   }
   // Of the kFine bins those in which the cluster's running measure passes the goal, top_k
   // or top_p's part of the sum, whose sums of weights are within kBinError of the true
@@ -970,9 +962,7 @@ __device__ __noinline__ void many_kept(const SampleParams& p, Shared& sh, int ph
       const int shift = max(0, 32 - __clz((int)(hi - lo)) - 9);
       row.clear();
       members([&](float f, int i) { row.add((int)((hi - order_key(f)) >> shift), by_w, row.weight(f)); });
-      unsigned long long g;
-      Found in;
-      row.find_bin(by_w, [&](unsigned long long) { return goal - before; }, g, in);
+      const Found in = row.find_bin(by_w, goal - before);
       before += in.before;
       n_bin = in.n;
       const uint32_t top = hi - (in.bin << shift), width = (1u << shift) - 1;

@@ -8,7 +8,10 @@
  * the token-embedding input FC, and eagle_draft_layer, its decoder layer,
  * built on eagle_linear; before the first round the prompt path fills the
  * paged caches: eagle_kv_append, eagle_prompt_attn and eagle_draft_prompt,
- * their 4-bit-page forms, which the tree calls do not read, beside them):
+ * their 4-bit-page forms, which the tree calls do not read, beside them;
+ * requests behind a prefix that they share: eagle_kv_append_axes and
+ * eagle_prefix_attn; tokens of a target without a draft, and truncated target
+ * distributions: eagle_sample and eagle_truncate_logits):
  *   eagle_fuse_proj             EAGLE-3 fused feature g = W_proj [h_low; h_mid; h_high]
  *   eagle_tree_attn             tree-masked attention vs a paged KV cache + the tree rows
  *   eagle_lmhead_topk           LM-head GEMM with fused per-row top-k and log-softmax
