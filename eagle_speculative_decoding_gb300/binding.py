@@ -758,6 +758,14 @@ def _own_rows(own_out, own_lse, out, T, Hq):
         raise ValueError("own_lse must be contiguous fp32 [T, Hq]")
 
 
+def _prefix_ws(ws, q, G, Hkv, stream):
+    """The caller's workspace, or one from the memory of the call's stream."""
+    if ws is None:
+        T, Hq, D = q.shape
+        ws = workspace(eagle_prefix_attn_workspace_size(G, T, Hq, Hkv, D), q.device, stream)
+    return ws
+
+
 def eagle_prefix_attn(q, k_cache, v_cache, prefix_table, cu_rows, prefix_lens, out, lse=None, own_out=None, own_lse=None,
                       scale=None, ws=None, status=None, stream=None):
     """Attention of groups of rows over the prefix that each group shares,
@@ -767,8 +775,9 @@ def eagle_prefix_attn(q, k_cache, v_cache, prefix_table, cu_rows, prefix_lens, o
     P = _pages16(k_cache, v_cache, Hkv, D, q.dtype)
     _own_rows(own_out, own_lse, out, T, Hq)
     G, pages = _lengths(q, cu_rows, prefix_lens, prefix_table, status)
-    if ws is None:
-        ws = workspace(eagle_prefix_attn_workspace_size(G, T, Hq, Hkv, D), q.device, stream)
+    if own_out is not None and not (own_out.is_cuda and own_lse.is_cuda):
+        raise ValueError("the arrays must be on the GPU")
+    ws = _prefix_ws(ws, q, G, Hkv, stream)
     _check("eagle_prefix_attn", lib().eagle_prefix_attn(
         q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), P, prefix_table.data_ptr(), pages, cu_rows.data_ptr(),
         prefix_lens.data_ptr(), _addr(own_out), _addr(own_lse), out.data_ptr(), _addr(lse), G, T, Hq, Hkv, D, page,
@@ -787,8 +796,9 @@ def eagle_prefix_attn_kv4(q, k_codes, k_scales, v_codes, v_scales, prefix_table,
     P = _pages4(k_codes, k_scales, v_codes, v_scales, Hkv, D)
     _own_rows(own_out, own_lse, out, T, Hq)
     G, pages = _lengths(q, cu_rows, prefix_lens, prefix_table, status)
-    if ws is None:
-        ws = workspace(eagle_prefix_attn_workspace_size(G, T, Hq, Hkv, D), q.device, stream)
+    if own_out is not None and not (own_out.is_cuda and own_lse.is_cuda):
+        raise ValueError("the arrays must be on the GPU")
+    ws = _prefix_ws(ws, q, G, Hkv, stream)
     _check("eagle_prefix_attn_kv4", lib().eagle_prefix_attn_kv4(
         q.data_ptr(), qs, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), k_scale,
         v_scale, P, prefix_table.data_ptr(), pages, cu_rows.data_ptr(), prefix_lens.data_ptr(), _addr(own_out),

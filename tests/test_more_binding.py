@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from eagle_speculative_decoding_gb300 import binding as eb
+from test_binding_streams import FakeStream, allocations  # noqa: F401 (a fixture)
 from test_prompt_binding import (B, CACHE, CODES, D, F32, HQ, I32, INDEX, OUT, ROPE, ROWS, T, W, attn_rows, lengths, pages4,
                                  pages16, rows, z)
 
@@ -108,3 +109,24 @@ def test_sampling_asks_for_a_gpu(call, base):
     some = {k: None if k in ("temperature", "top_k", "top_p", "min_p", "logprobs", "n_kept", "status") else v for k, v in base().items()}
     with pytest.raises(ValueError, match="on the GPU"):
         call(**some)
+
+
+@pytest.mark.parametrize("name", ["prefix", "prefix4"])
+def test_own_results_off_the_gpu_are_refused(name, monkeypatch):
+    call, base = CALLS[name]
+    on_gpu(monkeypatch)
+    with pytest.raises(ValueError, match="on the GPU"):
+        call(**base())
+
+
+@pytest.mark.parametrize("name", ["prefix", "prefix4"])
+@pytest.mark.parametrize("given", [False, True])
+def test_scratch_of_a_prefix_is_the_streams(allocations, name, given):  # noqa: F811
+    call, base = CALLS[name]
+    alone = dict(base(), own_out=None, own_lse=None)
+    s = FakeStream() if given else None
+    call(**alone, stream=s)
+    assert allocations == [(s, torch.uint8)]
+    allocations.clear()
+    call(**alone, stream=s, ws=torch.zeros(16, dtype=torch.uint8))
+    assert allocations == []
