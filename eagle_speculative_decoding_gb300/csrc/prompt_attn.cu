@@ -2654,17 +2654,45 @@ __global__ void __launch_bounds__(256, (CfgF32<D, RT>::kCtas)) prompt_attn_f32_k
 // threads takes eight rows of a unit at a time, whose partial results are 32 D
 // contiguous bytes of each piece: 16 bytes a thread, of 16-bit rows four rows of a
 // channel, of fp32 rows four channels of a row.  The pieces' weights are worked out
-// once, a thread a piece and row, while those are on their way.  The last CTA lets
-// rows of empty prefixes take their own result over.
+// once, a thread a piece and row, while those are on their way.  The last `extra` CTAs
+// let rows of empty prefixes take their own result over.
 struct JoinParams {
   AttnParams a;
-  int g, tpu, slot_rows, ctas;
+  int g, tpu, slot_rows, ctas, extra;
   const Split* splits;
   const float2* ml;
   const float* o;
   const void* own_out;
   const float* own_lse;
 };
+// Rows of empty prefixes, a warp a row; CTA c of p.extra.
+template <int D, typename T>
+__device__ __noinline__ void take_over(const JoinParams& p, int c) {
+  const AttnParams& a = p.a;
+  using V = typename std::conditional<sizeof(T) * D == 512, uint4, typename std::conditional<sizeof(T) * D == 256, uint2, uint32_t>::type>::type;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  bool falls = false;
+  for (int base = 0; base < a.B; base += 32) falls = __any_sync(0xffffffffu, load_groups(a, base, p.tpu, false).falls) || falls;
+  if (falls) return;
+  for (int base = 0; base < a.B; base += 32) {
+    const Groups g = load_groups(a, base, p.tpu, false);
+    unsigned m = __ballot_sync(0xffffffffu, g.n > 0 && g.len == 0);
+    if (a.B == 1) m &= 1u;
+    for (; m; m &= m - 1) {
+      const int src = __ffs((int)m) - 1;
+      const size_t r0 = (size_t)__shfl_sync(0xffffffffu, g.c0, src) * a.Hq, n = (size_t)__shfl_sync(0xffffffffu, g.n, src) * a.Hq;
+      for (size_t r = r0 + c * warps + warp; r < r0 + n; r += p.extra * warps) {
+        const float L = p.own_lse ? p.own_lse[r] : -INFINITY;
+        const size_t at = r * (sizeof(T) * D / sizeof(V)) + lane;
+        V v = {};
+        if (L != -INFINITY) v = static_cast<const V*>(p.own_out)[at];
+        static_cast<V*>(a.out)[at] = v;
+        __syncwarp();  // lse may be own_lse
+        if (a.lse && lane == 0) a.lse[r] = L;
+      }
+    }
+  }
+}
 constexpr int kMaxParts = 320;  // CTAs of a main kernel at most
 template <int D, typename T, int kBatch, int kCtas>
 __global__ void __launch_bounds__(2 * D, kCtas) flat_join_kernel(const JoinParams p) {
@@ -2707,37 +2735,13 @@ __global__ void __launch_bounds__(2 * D, kCtas) flat_join_kernel(const JoinParam
   };
   pdl_wait();
   pdl_trigger();
-  if (blockIdx.x == gridDim.x - 1) {
-    bool falls = false;
-    for (int base = 0; base < a.B; base += 32) falls = __any_sync(0xffffffffu, load_groups(a, base, p.tpu, false).falls) || falls;
-    if (falls) return;
-    const float none[4] = {};
-    for (int base = 0; base < a.B; base += 32) {
-      const Groups g = load_groups(a, base, p.tpu, false);
-      unsigned m = __ballot_sync(0xffffffffu, g.n > 0 && g.len == 0);
-      if (a.B == 1) m &= 1u;
-      for (; m; m &= m - 1) {
-        const int src = __ffs((int)m) - 1;
-        const size_t r0 = (size_t)__shfl_sync(0xffffffffu, g.c0, src) * a.Hq, n = (size_t)__shfl_sync(0xffffffffu, g.n, src) * a.Hq;
-        for (size_t r = r0; r < r0 + n; r += 8) {
-          const int rows = (int)min((size_t)8, r0 + n - r);
-          __syncthreads();
-          if (tid < rows) {
-            s_own[tid] = own_weight(-INFINITY, 0.f, p.own_lse ? p.own_lse[r + tid] : -INFINITY);
-            if (a.lse) a.lse[r + tid] = s_own[tid].lse;
-          }
-          __syncthreads();
-          float own[4];
-          auto same = [](int row) { return row; };
-          load_own(r, 0, rows, same, own);
-          store(r, 0, rows, same, none, own);
-        }
-      }
-    }
+  const int joining = (int)gridDim.x - p.extra;
+  if ((int)blockIdx.x >= joining) {
+    take_over<D, T>(p, (int)blockIdx.x - joining);
     return;
   }
   // this CTA's chunks of eight rows, of slot_rows / 8 of each split: numbers
-  // blockIdx.x, + gridDim.x - 1, ..
+  // blockIdx.x, + joining, ..
   const int of_split = p.slot_rows / 8;
   const int sets = (p.ctas + 31) / 32;
   for (int x = warp; x < sets; x += kWarps) {
@@ -2764,7 +2768,7 @@ __global__ void __launch_bounds__(2 * D, kCtas) flat_join_kernel(const JoinParam
   __syncthreads();
   const uint32_t g_inv = (65536u + (uint32_t)p.g - 1) / (uint32_t)p.g;
 #pragma unroll 1
-  for (int it = (int)blockIdx.x; it < splits * of_split; it += (int)gridDim.x - 1) {
+  for (int it = (int)blockIdx.x; it < splits * of_split; it += joining) {
     const int n = it / of_split, chunk = it - n * of_split, c0 = s_first[n];
     const Split u = s_split[c0];
     const int rows = u.rows, pieces = u.last - c0 + 1, h = u.h, tok0 = u.tok0;
@@ -2986,9 +2990,12 @@ struct Own {
 };
 template <int D, typename T>
 int flat_join(const AttnParams& a, const Own& own, const FlatShape& sh, const FlatWs& w, cudaStream_t s) {
-  const JoinParams jp = {a, sh.g, sh.tpu, sh.rows, sh.ctas, w.splits, w.ml, w.o, own.out, own.lse};
-  // CTAs for the chunks of eight rows that there can be
+  // CTAs for the chunks of eight rows that there can be, and one an SM at most for rows of
+  // empty prefixes, which are rare (64 tokens of which 32 have one: 21 us, and 106 with a
+  // single CTA for them; 4,096 tokens 76 us and 14,400)
   const int sms = std::max(1, sm_count());
+  const int extra = (int)std::min<long long>(sms, ((long long)a.T * a.Hq + 127) / 128);
+  const JoinParams jp = {a, sh.g, sh.tpu, sh.rows, sh.ctas, extra, w.splits, w.ml, w.o, own.out, own.lse};
   const long long units = ((long long)a.T + (long long)std::min(a.B, a.T) * (sh.tpu - 1)) / sh.tpu * a.Hkv;
   const long long chunks = std::min<long long>(units, sh.ctas) * (sh.rows / 8);
   // Few chunks, two a SM at most: 20 pieces' loads at a time and all their CTAs at once,
@@ -2997,9 +3004,9 @@ int flat_join(const AttnParams& a, const Own& own, const FlatShape& sh, const Fl
   // more CTAs a SM (1,885 rows in two groups 128 us, 158 the first way).
   constexpr int kFew = 2, kMany = 640 / D;
   if (chunks <= (long long)kFew * sms)
-    launch(flat_join_kernel<D, T, 20, 256 / D>, (int)chunks + 1, 2 * D, 0, s, jp);
+    launch(flat_join_kernel<D, T, 20, 256 / D>, (int)chunks + extra, 2 * D, 0, s, jp);
   else
-    launch(flat_join_kernel<D, T, 2, kMany>, (int)std::min<long long>(chunks, kMany * sms) + 1, 2 * D, 0, s, jp);
+    launch(flat_join_kernel<D, T, 2, kMany>, (int)std::min<long long>(chunks, kMany * sms) + extra, 2 * D, 0, s, jp);
   note_launch(2);
   return last_launch_status();
 }

@@ -361,3 +361,30 @@ def test_prefix_and_own_keys_are_the_whole_attention(kind):
     arith = (2 * (D + 9) * dot + 700 + 32) * 2.0 ** -24 + 2.0 ** -21
     assert (np.abs(f64(got) - want) <= half * np.abs(want) + (half + P_HALF[kind] + arith[..., None]) * mag).all()
     assert np.abs(f64(gl) - wl).max() <= 1e-4
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("Hq,Hkv,D", [(4, 2, 64), (32, 8, 128)])
+@pytest.mark.parametrize("own", [True, False])
+def test_many_rows_of_empty_prefixes(kind, Hq, Hkv, D, own):
+    """Their own results to the bit, by many CTAs; rows without keys of their own zeros, whatever
+    own_out holds; beside a group that has a prefix, and in place."""
+    b = need_gpu()
+    s = setup(kind, [0, 700, 3, 41, 0], [0, 0, 60, 0, 5], Hq, Hkv, D, 16, own=own)
+    if own:
+        s["own_lse"][::7] = -torch.inf
+        s["own_out"][::7] = torch.nan
+    out, lse = run(b, s, kind)
+    assert s["st"].item() == 0
+    rows = torch.cat([torch.arange(700), torch.arange(703, 744)]).cuda()
+    if not own:
+        assert (out[rows] == 0).all() and (lse[rows] == -torch.inf).all()
+        return
+    want = torch.where((s["own_lse"] == -torch.inf)[..., None], 0.0, s["own_out"])
+    assert torch.equal(out[rows], want[rows]) and torch.equal(lse[rows], s["own_lse"][rows])
+    args = dict(lse=s["own_lse"], own_out=s["own_out"], own_lse=s["own_lse"], status=s["st"])
+    if kind == "kv4":
+        b.eagle_prefix_attn_kv4(s["q"], s["k4"], s["ks"], s["v4"], s["vs"], s["table"], s["cu"], s["lens"], s["own_out"], **args)
+    else:
+        b.eagle_prefix_attn(s["q"], s["kc"], s["vc"], s["table"], s["cu"], s["lens"], s["own_out"], **args)
+    assert torch.equal(s["own_out"], out) and torch.equal(s["own_lse"], lse)
