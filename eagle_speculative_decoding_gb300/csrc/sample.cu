@@ -49,8 +49,8 @@
 // additions an entry, took as long.
 // Four CTAs an SM at 64 registers against three at 80: 64 rows of top-p 0.95 112 us and
 // 156, of top-k 50 29 and 35, 256 rows of mixed settings truncated 134 and 152; 17 rows
-// of 50,257 57.4 and 54.5.  Clusters of four CTAs took 16 % less for 256 rows, and a
-// half more for one row that keeps many.
+// of 50,257 57.4 and 54.5.  Clusters of two or four CTAs serve many rows
+// better, and take up to twice as long for one that keeps many (sample_launch).
 #include <float.h>
 #include <math.h>
 
@@ -1168,7 +1168,7 @@ __global__ void __launch_bounds__(kNT, 4) sample_kernel(const SampleParams p) {
         q = share < 0.2f ? min(kNT, (int)((1.f - __expf(-share * g * (float)E)) * (float)kNT) + 8) : 0;
       }
     } else if (use_p) {
-      q = kNT / 16;
+      q = 128 / row.C();  // (a nucleus of more takes the row's sums)
     }
   }
   float top = -INFINITY, group_top = -INFINITY;
@@ -1335,6 +1335,14 @@ int sample_launch(SampleParams p, void* stream) {
   const int total = (p.V + Unit<T>::E - 1) / Unit<T>::E + 1;  // and one for a start off its boundary
   int C = 1;
   while (C < kMaxCluster && total > C * kNT * 2) C *= 2;
+  // Many rows: two or four CTAs a row where a thread has 16 units at most then, for fewer
+  // barriers and first fetches a row; from four waves of CTAs on, or two where it has 8 (one
+  // row that keeps many takes longer).  bf16, mixed settings, fewer / eight: 256 rows of
+  // 32,000 104 us and 142, 512 147 and 264, 4,096 792 and 1,970 (one CTA a row 1,070);
+  // 512 rows of 128,256 332 and 402; 256 rows of 128,256 in fp32, of top-k up to 5,000,
+  // which four CTAs cannot hold, 190 and 133.
+  const long long slots = 4ll * std::max(1, sm_count());
+  while (C > 2 && total <= C / 2 * kNT * 16 && (long long)p.M * C > slots * (total <= C / 2 * kNT * 8 ? 2 : 4)) C /= 2;
   p.units = (total + C * kNW - 1) / (C * kNW);
   launch_cluster(sample_kernel<T>, dim3(C, p.M), dim3(kNT), dim3(C, 1, 1), 0, static_cast<cudaStream_t>(stream), p);
   note_launch();

@@ -259,3 +259,40 @@ def test_top_p_next_to_one_of_many(kind, V, dtype):
         e = V * 2.0 ** -45 + 2.0 ** -36 * run[-1]
         border = (1 - 2.0 ** -24) * run[-1]
         assert run[m - 1] < border + 2 * e and run[m] > border - 2 * e, (t, m, run[m - 1] - border, run[m] - border, e)
+
+
+@pytest.mark.parametrize("M,V,dtype", [(200, 32000, "bf16"), (400, 32001, "bf16"), (700, 20011, "fp32"), (640, 65539, "bf16")])
+def test_many_rows_in_smaller_clusters(M, V, dtype):
+    """Every kind of row among many, on the rows' own settings; those checked are the first of each setting."""
+    b = need_gpu()
+    rows = [SETTINGS[i % len(SETTINGS)] for i in range(M)]
+    first = len(SETTINGS)
+    x = make("power", 2 * first, V, dtype, V)
+    x[::3] = make("normal", 2 * first, V, dtype, V + 1)[::3]
+    x = x.repeat(-(-M // (2 * first)), 1)[:M].contiguous().cuda()
+    u = np.tile(uniforms(2 * first, M), -(-M // (2 * first)))[:M]
+    s = settings_of(rows)
+    tok, n, st = torch.zeros(M, dtype=torch.int32, device="cuda"), torch.zeros(M, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32).cuda()
+    b.eagle_sample(x, torch.from_numpy(u).cuda(), tok, n_kept=n, status=st, **s)
+    out = b.eagle_truncate_logits(x, torch.empty_like(x), status=st, **s)
+    assert st.item() == 0
+    per = 2 * first
+    want = oracle_rows(x[:per], rows[:per], u[:per])
+    tok, n = tok.cpu().numpy(), n.cpu().numpy()
+    for r in range(M):
+        assert (tok[r], n[r]) == want[r % per][:2], (r, rows[r])
+    for r in range(0, M, per):  # the same rows again
+        assert torch.equal(out[r:r + per], out[:min(per, M - r)])
+    for r in range(per):
+        assert np.array_equal(out[r].double().cpu().numpy(), want[r][2])
+
+
+def oracle_rows(x, rows, u):
+    """(token, entries kept, truncated row) of each row."""
+    result = []
+    for r, (t, k, p, m) in enumerate(rows):
+        row = x[r].double().cpu().numpy()
+        how = dict(temperature=float(F(t)), top_k=k, top_p=float(F(p)), min_p=float(F(m)))
+        token, _, kept = oracle.sample(row, float(u[r]), **how)
+        result.append((token, kept, np.where(oracle.truncate(row, **how)[0], row, -np.inf)))
+    return result
