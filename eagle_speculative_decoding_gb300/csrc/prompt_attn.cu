@@ -2654,20 +2654,20 @@ __global__ void __launch_bounds__(256, (CfgF32<D, RT>::kCtas)) prompt_attn_f32_k
 // threads takes eight rows of a unit at a time, whose partial results are 32 D
 // contiguous bytes of each piece: 16 bytes a thread, of 16-bit rows four rows of a
 // channel, of fp32 rows four channels of a row.  The pieces' weights are worked out
-// once, a thread a piece and row, while those are on their way.  The last `extra` CTAs
-// let rows of empty prefixes take their own result over.
+// once, a thread a piece and row, while those are on their way.  CTAs
+// that have none of that let rows of empty prefixes take their own result over.
 struct JoinParams {
   AttnParams a;
-  int g, tpu, slot_rows, ctas, extra;
+  int g, tpu, slot_rows, ctas;
   const Split* splits;
   const float2* ml;
   const float* o;
   const void* own_out;
   const float* own_lse;
 };
-// Rows of empty prefixes, a warp a row; CTA c of p.extra.
+// Rows of empty prefixes, a warp a row; CTA c of `ctas`.
 template <int D, typename T>
-__device__ __noinline__ void take_over(const JoinParams& p, int c) {
+__device__ __forceinline__ void take_over(const JoinParams& p, int c, int ctas) {
   const AttnParams& a = p.a;
   using V = typename std::conditional<sizeof(T) * D == 512, uint4, typename std::conditional<sizeof(T) * D == 256, uint2, uint32_t>::type>::type;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
@@ -2681,7 +2681,7 @@ __device__ __noinline__ void take_over(const JoinParams& p, int c) {
     for (; m; m &= m - 1) {
       const int src = __ffs((int)m) - 1;
       const size_t r0 = (size_t)__shfl_sync(0xffffffffu, g.c0, src) * a.Hq, n = (size_t)__shfl_sync(0xffffffffu, g.n, src) * a.Hq;
-      for (size_t r = r0 + c * warps + warp; r < r0 + n; r += p.extra * warps) {
+      for (size_t r = r0 + c * warps + warp; r < r0 + n; r += ctas * warps) {
         const float L = p.own_lse ? p.own_lse[r] : -INFINITY;
         const size_t at = r * (sizeof(T) * D / sizeof(V)) + lane;
         V v = {};
@@ -2694,7 +2694,7 @@ __device__ __noinline__ void take_over(const JoinParams& p, int c) {
   }
 }
 constexpr int kMaxParts = 320;  // CTAs of a main kernel at most
-template <int D, typename T, int kBatch, int kCtas>
+template <int D, typename T, int kBatch, int kCtas, bool kSpare>
 __global__ void __launch_bounds__(2 * D, kCtas) flat_join_kernel(const JoinParams p) {
   constexpr bool kByRow = sizeof(T) == 4;
   constexpr int kThreads_ = 2 * D, kWarps = kThreads_ / 32;
@@ -2735,14 +2735,9 @@ __global__ void __launch_bounds__(2 * D, kCtas) flat_join_kernel(const JoinParam
   };
   pdl_wait();
   pdl_trigger();
-  const int joining = (int)gridDim.x - p.extra;
-  if ((int)blockIdx.x >= joining) {
-    take_over<D, T>(p, (int)blockIdx.x - joining);
-    return;
-  }
   // this CTA's chunks of eight rows, of slot_rows / 8 of each split: numbers
-  // blockIdx.x, + joining, ..
-  const int of_split = p.slot_rows / 8;
+  // blockIdx.x, + stride, ..
+  const int of_split = p.slot_rows / 8, stride = (int)gridDim.x - (kSpare ? p.ctas : 1);
   const int sets = (p.ctas + 31) / 32;
   for (int x = warp; x < sets; x += kWarps) {
     const int c = x * 32 + lane;
@@ -2766,9 +2761,17 @@ __global__ void __launch_bounds__(2 * D, kCtas) flat_join_kernel(const JoinParam
     splits += s_count[x];
   }
   __syncthreads();
+  // CTAs without a chunk, one at least, let rows of empty prefixes take their own result
+  // over (64 tokens of which 32 have one 21 us, 4,096 tokens 21; with one CTA for them 106
+  // and 14,400)
+  const int joining = min(splits * of_split, stride);
+  if ((int)blockIdx.x >= joining) {
+    take_over<D, T>(p, (int)blockIdx.x - joining, (int)gridDim.x - joining);
+    return;
+  }
   const uint32_t g_inv = (65536u + (uint32_t)p.g - 1) / (uint32_t)p.g;
 #pragma unroll 1
-  for (int it = (int)blockIdx.x; it < splits * of_split; it += joining) {
+  for (int it = (int)blockIdx.x; it < splits * of_split; it += stride) {
     const int n = it / of_split, chunk = it - n * of_split, c0 = s_first[n];
     const Split u = s_split[c0];
     const int rows = u.rows, pieces = u.last - c0 + 1, h = u.h, tok0 = u.tok0;
@@ -2990,12 +2993,10 @@ struct Own {
 };
 template <int D, typename T>
 int flat_join(const AttnParams& a, const Own& own, const FlatShape& sh, const FlatWs& w, cudaStream_t s) {
-  // CTAs for the chunks of eight rows that there can be, and one an SM at most for rows of
-  // empty prefixes, which are rare (64 tokens of which 32 have one: 21 us, and 106 with a
-  // single CTA for them; 4,096 tokens 76 us and 14,400)
+  // CTAs for the chunks of eight rows that there can be, and one more (where they are more
+  // than the CTAs, one an SM more)
   const int sms = std::max(1, sm_count());
-  const int extra = (int)std::min<long long>(sms, ((long long)a.T * a.Hq + 127) / 128);
-  const JoinParams jp = {a, sh.g, sh.tpu, sh.rows, sh.ctas, extra, w.splits, w.ml, w.o, own.out, own.lse};
+  const JoinParams jp = {a, sh.g, sh.tpu, sh.rows, sh.ctas, w.splits, w.ml, w.o, own.out, own.lse};
   const long long units = ((long long)a.T + (long long)std::min(a.B, a.T) * (sh.tpu - 1)) / sh.tpu * a.Hkv;
   const long long chunks = std::min<long long>(units, sh.ctas) * (sh.rows / 8);
   // Few chunks, two a SM at most: 20 pieces' loads at a time and all their CTAs at once,
@@ -3004,9 +3005,9 @@ int flat_join(const AttnParams& a, const Own& own, const FlatShape& sh, const Fl
   // more CTAs a SM (1,885 rows in two groups 128 us, 158 the first way).
   constexpr int kFew = 2, kMany = 640 / D;
   if (chunks <= (long long)kFew * sms)
-    launch(flat_join_kernel<D, T, 20, 256 / D>, (int)chunks + extra, 2 * D, 0, s, jp);
+    launch(flat_join_kernel<D, T, 20, 256 / D, false>, (int)chunks + 1, 2 * D, 0, s, jp);
   else
-    launch(flat_join_kernel<D, T, 2, kMany>, (int)std::min<long long>(chunks, kMany * sms) + extra, 2 * D, 0, s, jp);
+    launch(flat_join_kernel<D, T, 2, kMany, true>, (int)std::min<long long>(chunks, kMany * sms) + sh.ctas, 2 * D, 0, s, jp);
   note_launch(2);
   return last_launch_status();
 }
