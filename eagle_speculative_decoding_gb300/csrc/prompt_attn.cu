@@ -1627,8 +1627,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         oph ^= 1u;
         tc_fence_after();
       }
+      const bool whole = w.slot < 0;
+      const size_t orow = ((size_t)w.c0 + tok) * a.Hq + w.h * p.g + row % p.g;
       float w0 = 1.f, w1 = 0.f;  // weights of this tile's O and of the other's
       const bool join = tw.twin && tw.n1 > 0;
+      const bool halves = FLAT && join;  // of the channels, one for each tile's warps
+      const bool writes = quad_live && (halves || !(tw.twin && t == 1));
+      // A row's own log-sum-exp, in whose place lse may be written.  With `halves` both tiles'
+      // warps read it, and tile 0's write lse: tile 1's read it in front of their arrivals
+      // on x_stat, all of which tile 0's have waited for by then, so that no read comes
+      // behind a write.  (Otherwise a row is one thread's.)
+      float own_lse = -INFINITY;
+      if (FLAT && writes && whole && row_ok && p.own_lse) own_lse = p.own_lse[orow];
       if (join) {
         if (t == 1) {
           sb.x_ml[row] = make_float2(m, l);
@@ -1666,17 +1676,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = mm;
         }
       }
-      const bool halves = FLAT && join;  // of the channels, one for each tile's warps
-      if (quad_live && (halves || !(tw.twin && t == 1))) {
-        const int head = w.h * p.g + row % p.g;
-        const size_t orow = ((size_t)w.c0 + tok) * a.Hq + head;
+      if (writes) {
         const int urow = (tw.twin ? 0 : t * p.tpt * p.g) + row;
-        const bool whole = w.slot < 0;
         const size_t prow = (size_t)max(w.slot, 0) * p.slot_rows + urow;
         float inv = whole ? (l == 0.f ? 0.f : a.v_scale / l) : 1.f, own = 0.f;
         if constexpr (FLAT) {
           if (whole && row_ok) {
-            const OwnWeight x = own_weight(m, l, p.own_lse ? p.own_lse[orow] : -INFINITY);
+            const OwnWeight x = own_weight(m, l, own_lse);
             inv = x.prefix * a.v_scale;
             own = x.own;
             m = x.lse;
