@@ -615,15 +615,18 @@ struct FlatWalk {
 // A row's own keys as one more term of its sums: their log-sum-exp L becomes the
 // weight 2^(L log2(e) - M) beside the prefix's sum l 2^(m - M), M the larger of the two
 // references.  L log2(e) is kept in two parts (as one it is off by 2^-24 of itself,
-// which is 2^-20 of a weight).
+// which is 2^-20 of a weight).  A side whose weight is zero does not count, whatever its
+// values are: with `prefix` 0 the own result is left as it is.
 struct OwnWeight {
   float prefix, own, lse;  // factors of O and of own_out, and the joined log-sum-exp
+  __device__ __forceinline__ float of_prefix(float o, float by) const { return prefix == 0.f ? 0.f : o * by; }
 };
 __device__ __forceinline__ OwnWeight own_weight(float m, float l, float L) {
   if (l == 0.f) return {0.f, L == -INFINITY ? 0.f : 1.f, L};  // the own result as it is
   if (L == -INFINITY) return {1.f / l, 0.f, (m + log2f(l)) * kLn2};
   const float hi = L * 1.44269502f, lo = fmaf(L, 1.44269502f, -hi) + L * 1.92596303e-8f, M = fmaxf(m, hi);
   const float p = ex2_approx(m - M), o = ex2_approx((hi - M) + lo), total = fmaf(l, p, o), f = 1.f / total;
+  if (l * p == 0.f) return {0.f, 1.f, L};
   return {p * f, o * f, (M + log2f(total)) * kLn2};
 }
 
@@ -1679,14 +1682,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (writes) {
         const int urow = (tw.twin ? 0 : t * p.tpt * p.g) + row;
         const size_t prow = (size_t)max(w.slot, 0) * p.slot_rows + urow;
-        float inv = whole ? (l == 0.f ? 0.f : a.v_scale / l) : 1.f, own = 0.f;
+        const float inv = whole ? (l == 0.f ? 0.f : a.v_scale / l) : 1.f;
+        OwnWeight x = {};
         if constexpr (FLAT) {
-          if (whole && row_ok) {
-            const OwnWeight x = own_weight(m, l, own_lse);
-            inv = x.prefix * a.v_scale;
-            own = x.own;
-            m = x.lse;
-          }
+          if (whole && row_ok) x = own_weight(m, l, own_lse);
         }
         const uint32_t o_first = halves ? tmem + lane_addr + C::kColO : o_addr;
 #pragma unroll 1
@@ -1711,8 +1710,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           float* f = reinterpret_cast<float*>(o);
           if (whole) {
             if constexpr (FLAT) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) f[k] = x.of_prefix(f[k], x.prefix * a.v_scale);
               // (a row without keys of its own may hold anything)
-              if (p.own_out && !(own == 0.f)) {
+              if (p.own_out && !(x.own == 0.f)) {
                 const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.own_out) + orow * D + c * 32);
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
@@ -1720,13 +1721,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const uint32_t e[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                   for (int k = 0; k < 4; ++k) {
-                    f[8 * u + 2 * k] = fmaf(__uint_as_float(e[k] << 16), own, f[8 * u + 2 * k] * inv);
-                    f[8 * u + 2 * k + 1] = fmaf(__uint_as_float(e[k] & 0xffff0000u), own, f[8 * u + 2 * k + 1] * inv);
+                    f[8 * u + 2 * k] = fmaf(__uint_as_float(e[k] << 16), x.own, f[8 * u + 2 * k]);
+                    f[8 * u + 2 * k + 1] = fmaf(__uint_as_float(e[k] & 0xffff0000u), x.own, f[8 * u + 2 * k + 1]);
                   }
                 }
-              } else {
-#pragma unroll
-                for (int k = 0; k < 32; ++k) f[k] *= inv;
               }
             }
             uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + c * 32);
@@ -1751,7 +1749,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (row_ok && !(halves && t == 1)) {
           if (whole) {
-            if (a.lse) a.lse[orow] = FLAT ? m : l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            if (a.lse) a.lse[orow] = FLAT ? x.lse : l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
           } else {
             p.part_ml[prow] = make_float2(m, l);
           }
@@ -2628,7 +2626,7 @@ __global__ void __launch_bounds__(256, (CfgF32<D, RT>::kCtas)) prompt_attn_f32_k
         f = 1.f;
         m[i] = x.lse;
 #pragma unroll
-        for (int c = 0; c < 4 * NC; ++c) o[i][c] *= x.prefix;
+        for (int c = 0; c < 4 * NC; ++c) o[i][c] = x.of_prefix(o[i][c], x.prefix);
         if (p.own_out && !(own == 0.f)) {
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
@@ -2730,8 +2728,8 @@ __global__ void __launch_bounds__(2 * D, kCtas) flat_join_kernel(const JoinParam
       const int row = row_of(e);
       if (first + row >= rows) continue;
       const OwnWeight w = s_own[row];
-      y[e] = o[e] * (w.prefix * a.v_scale);
-      if (w.own != 0.f) y[e] = w.prefix == 0.f ? own[e] : fmaf(own[e], w.own, y[e]);
+      y[e] = w.of_prefix(o[e], w.prefix * a.v_scale);
+      if (w.own != 0.f) y[e] = fmaf(own[e], w.own, y[e]);
       if constexpr (!kByRow) dst[at(first + row) * D + chan_of(e)] = (T)y[e];
     }
     if constexpr (kByRow) {

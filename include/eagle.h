@@ -886,7 +886,10 @@ int eagle_prompt_attn_kv4(const void* q, long long q_stride, const uint8_t* k_co
  *   out, lse (or NULL) : as eagle_prompt_attn; may be own_out and own_lse themselves
  * A group of an empty prefix takes own_out and own_lse over (zeros and -infinity
  * without them).  Rows whose keys, own ones included, all score -infinity give
- * zeros and -infinity.  T = 0 does nothing.
+ * zeros and -infinity.  A side whose weight is zero in fp32, because its scores are all
+ * -infinity or lie that far below the other's, does not count, whatever its values
+ * are (an infinity in the prefix's V, say): beside a prefix without weight the own
+ * result is left as it is.  T = 0 does nothing.
  * Device-detected: a cu_rows that falls somewhere -> EAGLE_ERR_INVALID_ARG (no
  * row is written); a group with an entry outside 0 .. T or a negative length ->
  * EAGLE_ERR_INVALID_ARG, a length beyond the table or 2^30 -> EAGLE_ERR_BAD_KV

@@ -42,3 +42,49 @@ def test_whole_units_in_place(rows, lens, Hq, Hkv, D, kind):
     for i in range(12):
         out, lse = in_place(b, s, kind, out=i % 3 != 2)
         assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
+# whole and cut units in one call; single blocks; cut alone; tiles of rows, whole
+SHARED_OUT = [([1] * 40, [300] * 40), ([9, 3], [100, 60]), ([64], [3000]), ([2000], [300])]
+
+
+def heads_of(kind, rows):
+    return (32, 8, 128) if kind != "fp32" or sum(rows) < 500 else (4, 2, 64)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows,lens", SHARED_OUT)
+def test_a_prefix_without_weight_does_not_count(rows, lens, kind):
+    """Where the own log-sum-exp lies so far above a prefix that the prefix weighs nothing, the own
+    result is taken over to the bit, whatever the prefix's values hold; beside it they are seen."""
+    b = need_gpu()
+    Hq, Hkv, D = heads_of(kind, rows)
+    s = setup(kind, rows, lens, Hq, Hkv, D, 21)
+    if kind == "kv4":
+        s["vs"][s["table"][:, 0].long(), :, 3] = 127  # a NaN as the scale of 16 values
+    else:
+        s["vc"][s["table"][:, 0].long(), 3] = torch.inf
+        s["vc"][s["table"][:, 0].long(), 5] = torch.nan
+    s["own_lse"][:, ::2] = 300.0
+    out, lse = run(b, s, kind)
+    assert torch.equal(out[:, ::2], s["own_out"][:, ::2]) and torch.equal(lse[:, ::2], s["own_lse"][:, ::2])
+    assert not out[:, 1::2].isfinite().any() and lse.isfinite().all() and s["st"].item() == 0
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("own", [True, False])
+@pytest.mark.parametrize("rows,lens", SHARED_OUT)
+def test_a_prefix_whose_scores_are_all_minus_infinity_does_not_count(rows, lens, own, kind):
+    """Nor does one without a score above -infinity: the own result, or zeros and -infinity."""
+    b = need_gpu()
+    s = setup(kind, rows, lens, *heads_of(kind, rows), 22, own=own)
+    s["q"].abs_()
+    s["kc"][:, :, 0] = -torch.inf
+    s["vc"][s["table"][:, 0].long(), 3] = torch.inf
+    out, lse = run(b, s, kind)
+    g = s["q"].shape[1] // s["kc"].shape[2]
+    if own:
+        assert torch.equal(out[:, :g], s["own_out"][:, :g]) and torch.equal(lse[:, :g], s["own_lse"][:, :g])
+    else:
+        assert (out[:, :g] == 0).all() and (lse[:, :g] == -torch.inf).all()
+    assert not out[:, g:, 0].isfinite().any() and lse[:, g:].isfinite().all() and s["st"].item() == 0
