@@ -623,8 +623,9 @@ struct OwnWeight {
 };
 __device__ __forceinline__ OwnWeight own_weight(float m, float l, float L) {
   if (l == 0.f) return {0.f, L == -INFINITY ? 0.f : 1.f, L};  // the own result as it is
-  if (L == -INFINITY) return {1.f / l, 0.f, (m + log2f(l)) * kLn2};
   const float hi = L * 1.44269502f, lo = fmaf(L, 1.44269502f, -hi) + L * 1.92596303e-8f, M = fmaxf(m, hi);
+  // (past fp32's range, as for a mask of the type's lowest value: nothing beside the other side)
+  if (isinf(hi)) return hi < 0.f ? OwnWeight{1.f / l, 0.f, (m + log2f(l)) * kLn2} : OwnWeight{0.f, 1.f, L};
   const float p = ex2_approx(m - M), o = ex2_approx((hi - M) + lo), total = fmaf(l, p, o), f = 1.f / total;
   if (l * p == 0.f) return {0.f, 1.f, L};
   return {p * f, o * f, (M + log2f(total)) * kLn2};

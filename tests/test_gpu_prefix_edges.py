@@ -88,3 +88,22 @@ def test_a_prefix_whose_scores_are_all_minus_infinity_does_not_count(rows, lens,
     else:
         assert (out[:, :g] == 0).all() and (lse[:, :g] == -torch.inf).all()
     assert not out[:, g:, 0].isfinite().any() and lse[:, g:].isfinite().all() and s["st"].item() == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows,lens", SHARED_OUT + [([5, 6], [0, 40])])
+def test_largest_and_lowest_own_sums(rows, lens, kind):
+    """The type's lowest value as an own log-sum-exp, as masks have it, weighs nothing beside a prefix;
+    its largest leaves the own result; the log-sum-exp in base 2 lies past fp32 in both."""
+    b = need_gpu()
+    s = setup(kind, rows, lens, *heads_of(kind, rows), 23)
+    none = dict(s, own_lse=torch.full_like(s["own_lse"], -torch.inf))
+    alone, al = run(b, none, kind)
+    empty = torch.repeat_interleave(s["lens"] == 0, torch.tensor(rows).cuda())
+    for low in (torch.finfo(torch.float32).min, -2.4e38, -2.3e38, -1e30):
+        out, lse = run(b, dict(s, own_lse=torch.full_like(s["own_lse"], low)), kind)
+        assert torch.equal(out[~empty], alone[~empty]) and torch.equal(lse[~empty], al[~empty])
+        assert torch.equal(out[empty], s["own_out"][empty]) and (lse[empty] == torch.tensor(low)).all()
+    for high in (torch.finfo(torch.float32).max, 2.4e38, 2.3e38, 1e30):
+        out, lse = run(b, dict(s, own_lse=torch.full_like(s["own_lse"], high)), kind)
+        assert torch.equal(out, s["own_out"]) and (lse == torch.tensor(high)).all()
