@@ -53,6 +53,7 @@
 // better, and take up to twice as long for one that keeps many (sample_launch).
 #include <float.h>
 #include <math.h>
+#include <stddef.h>
 
 #include <algorithm>
 
@@ -174,7 +175,7 @@ struct Weigh {
 
 
 // What a CTA holds of a row.
-struct Shared {
+struct alignas(16) Shared {
   // counts, and three limbs of sums of weights (a bin's four words apart: neighbouring
   // bins in all banks); or a word each of kFine bins
   uint32_t hist[4][kBins];
@@ -425,6 +426,7 @@ struct Row {
     all_n = an;
   }
   __device__ __forceinline__ void clear() {
+    static_assert(alignof(Shared) >= 16 && offsetof(Shared, hist) % 16 == 0 && sizeof(sh.hist) == 16 * kBins, "16 bytes a store");
     for (int i = threadIdx.x; i < kBins; i += kNT) reinterpret_cast<uint4*>(sh.hist)[i] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
   }
