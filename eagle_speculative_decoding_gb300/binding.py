@@ -516,9 +516,17 @@ _I32, _F32 = torch.int32, torch.float32
 _BYTES = (torch.uint8, torch.float8_e4m3fn)
 
 
+def _on_gpu(*arrays):
+    """That the arrays (those that are given) are on the GPU: a host address must not reach a kernel."""
+    for t in arrays:
+        if t is not None and not t.is_cuda:
+            raise ValueError("the arrays must be on the GPU")
+
+
 def _lengths(rows, cu_seqlens, ctx_lens, block_table, status):
     """Last of a call's checks, those of the index arrays, and that they (the
-    ones that are built on the host) and the rows are on the GPU: (B, max_pages)."""
+    ones that are built on the host), the status and `rows`, other arrays of the
+    call, are on the GPU: (B, max_pages)."""
     if not (cu_seqlens.dtype is _I32 and ctx_lens.dtype is _I32 and block_table.dtype is _I32
             and cu_seqlens.is_contiguous() and ctx_lens.is_contiguous() and block_table.is_contiguous()):
         raise ValueError("cu_seqlens, ctx_lens and block_table must be contiguous int32")
@@ -527,8 +535,9 @@ def _lengths(rows, cu_seqlens, ctx_lens, block_table, status):
         raise ValueError("cu_seqlens must be [B + 1], ctx_lens [B] and block_table [B, max_pages]")
     if status is not None and status.dtype is not _I32:
         raise ValueError("status must be int32")
-    if not (rows.is_cuda and cu_seqlens.is_cuda and ctx_lens.is_cuda and block_table.is_cuda):
+    if not (cu_seqlens.is_cuda and ctx_lens.is_cuda and block_table.is_cuda and (status is None or status.is_cuda)):
         raise ValueError("the arrays must be on the GPU")
+    _on_gpu(*rows)
     return B, pages
 
 
@@ -624,7 +633,7 @@ def eagle_kv_append(q, k, v, rope, cu_seqlens, ctx_lens, block_table, k_cache, v
     for no rotation."""
     T, Hkv, D, Hq, qs, ks, vs = _append_rows(q, k, v, q_out)
     P, max_pos = _pages16(k_cache, v_cache, Hkv, D, k.dtype), _rope_rows(rope, D)
-    B, pages = _lengths(k, cu_seqlens, ctx_lens, block_table, status)
+    B, pages = _lengths((k,), cu_seqlens, ctx_lens, block_table, status)
     _check("eagle_kv_append", lib().eagle_kv_append(
         _addr(q), k.data_ptr(), v.data_ptr(), qs, ks, vs, _addr(rope), max_pos, cu_seqlens.data_ptr(),
         ctx_lens.data_ptr(), B, T, Hq, Hkv, D, _dtype(k), _addr(q_out), k_cache.data_ptr(), v_cache.data_ptr(), P,
@@ -638,7 +647,7 @@ def eagle_kv_append_kv4(q, k, v, rope, cu_seqlens, ctx_lens, block_table, k_code
     if k.dtype != torch.bfloat16:
         raise ValueError("k and v must be bf16")
     P, max_pos = _pages4(k_codes, k_scales, v_codes, v_scales, Hkv, D), _rope_rows(rope, D)
-    B, pages = _lengths(k, cu_seqlens, ctx_lens, block_table, status)
+    B, pages = _lengths((k,), cu_seqlens, ctx_lens, block_table, status)
     _check("eagle_kv_append_kv4", lib().eagle_kv_append_kv4(
         _addr(q), k.data_ptr(), v.data_ptr(), qs, ks, vs, _addr(rope), max_pos, cu_seqlens.data_ptr(),
         ctx_lens.data_ptr(), B, T, Hq, Hkv, D, _addr(q_out), k_codes.data_ptr(), k_scales.data_ptr(),
@@ -653,8 +662,7 @@ def _axes(positions, pair_axis, T, D):
         raise ValueError("positions must be contiguous int32 [axes, T]")
     if pair_axis is not None and not (pair_axis.shape == (D // 2,) and pair_axis.dtype is _I32 and pair_axis.is_contiguous()):
         raise ValueError("pair_axis must be contiguous int32 [D / 2]")
-    if not (positions.is_cuda and (pair_axis is None or pair_axis.is_cuda)):
-        raise ValueError("the arrays must be on the GPU")
+    _on_gpu(positions, pair_axis)
     return shape[0]
 
 
@@ -664,7 +672,7 @@ def eagle_kv_append_axes(q, k, v, rope, positions, cu_seqlens, ctx_lens, block_t
     an axis for each channel pair, pair_axis [D / 2] (see include/eagle.h)."""
     T, Hkv, D, Hq, qs, ks, vs = _append_rows(q, k, v, q_out)
     P, max_pos = _pages16(k_cache, v_cache, Hkv, D, k.dtype), _rope_rows(rope, D)
-    B, pages = _lengths(k, cu_seqlens, ctx_lens, block_table, status)
+    B, pages = _lengths((k, q_out, k_cache, v_cache), cu_seqlens, ctx_lens, block_table, status)
     axes = _axes(positions, pair_axis, T, D)
     _check("eagle_kv_append_axes", lib().eagle_kv_append_axes(
         _addr(q), k.data_ptr(), v.data_ptr(), qs, ks, vs, _addr(rope), max_pos, positions.data_ptr(), axes,
@@ -680,7 +688,7 @@ def eagle_kv_append_axes_kv4(q, k, v, rope, positions, cu_seqlens, ctx_lens, blo
     if k.dtype != torch.bfloat16:
         raise ValueError("k and v must be bf16")
     P, max_pos = _pages4(k_codes, k_scales, v_codes, v_scales, Hkv, D), _rope_rows(rope, D)
-    B, pages = _lengths(k, cu_seqlens, ctx_lens, block_table, status)
+    B, pages = _lengths((k, q_out, k_codes, k_scales, v_codes, v_scales), cu_seqlens, ctx_lens, block_table, status)
     axes = _axes(positions, pair_axis, T, D)
     _check("eagle_kv_append_axes_kv4", lib().eagle_kv_append_axes_kv4(
         _addr(q), k.data_ptr(), v.data_ptr(), qs, ks, vs, _addr(rope), max_pos, positions.data_ptr(), axes,
@@ -712,7 +720,7 @@ def eagle_prompt_attn(q, k_cache, v_cache, block_table, cu_seqlens, ctx_lens, ou
     T, Hq, D, qs = _attn_rows(q, out, lse)
     _, page, Hkv, _ = k_cache.shape
     P = _pages16(k_cache, v_cache, Hkv, D, q.dtype)
-    B, pages = _lengths(q, cu_seqlens, ctx_lens, block_table, status)
+    B, pages = _lengths((q,), cu_seqlens, ctx_lens, block_table, status)
     if ws is None:
         ws = workspace(eagle_prompt_attn_workspace_size(B, T, Hq, Hkv, D), q.device, stream)
     _check("eagle_prompt_attn", lib().eagle_prompt_attn(
@@ -731,7 +739,7 @@ def eagle_prompt_attn_kv4(q, k_codes, k_scales, v_codes, v_scales, block_table, 
     T, Hq, D, qs = _attn_rows(q, out, lse)
     _, Hkv, page, _ = k_codes.shape
     P = _pages4(k_codes, k_scales, v_codes, v_scales, Hkv, D)
-    B, pages = _lengths(q, cu_seqlens, ctx_lens, block_table, status)
+    B, pages = _lengths((q,), cu_seqlens, ctx_lens, block_table, status)
     if ws is None:
         ws = workspace(eagle_prompt_attn_workspace_size(B, T, Hq, Hkv, D), q.device, stream)
     _check("eagle_prompt_attn_kv4", lib().eagle_prompt_attn_kv4(
@@ -774,9 +782,8 @@ def eagle_prefix_attn(q, k_cache, v_cache, prefix_table, cu_rows, prefix_lens, o
     _, page, Hkv, _ = k_cache.shape
     P = _pages16(k_cache, v_cache, Hkv, D, q.dtype)
     _own_rows(own_out, own_lse, out, T, Hq)
-    G, pages = _lengths(q, cu_rows, prefix_lens, prefix_table, status)
-    if own_out is not None and not (own_out.is_cuda and own_lse.is_cuda):
-        raise ValueError("the arrays must be on the GPU")
+    G, pages = _lengths((q, out, lse), cu_rows, prefix_lens, prefix_table, status)
+    _on_gpu(own_out, own_lse)
     ws = _prefix_ws(ws, q, G, Hkv, stream)
     _check("eagle_prefix_attn", lib().eagle_prefix_attn(
         q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), P, prefix_table.data_ptr(), pages, cu_rows.data_ptr(),
@@ -795,9 +802,8 @@ def eagle_prefix_attn_kv4(q, k_codes, k_scales, v_codes, v_scales, prefix_table,
     _, Hkv, page, _ = k_codes.shape
     P = _pages4(k_codes, k_scales, v_codes, v_scales, Hkv, D)
     _own_rows(own_out, own_lse, out, T, Hq)
-    G, pages = _lengths(q, cu_rows, prefix_lens, prefix_table, status)
-    if own_out is not None and not (own_out.is_cuda and own_lse.is_cuda):
-        raise ValueError("the arrays must be on the GPU")
+    G, pages = _lengths((q, out, lse), cu_rows, prefix_lens, prefix_table, status)
+    _on_gpu(own_out, own_lse)
     ws = _prefix_ws(ws, q, G, Hkv, stream)
     _check("eagle_prefix_attn_kv4", lib().eagle_prefix_attn_kv4(
         q.data_ptr(), qs, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), k_scale,
@@ -834,7 +840,7 @@ def eagle_draft_prompt(x, weights, rope, cu_seqlens, ctx_lens, k_cache, v_cache,
         raise ValueError("4-bit pages need k_scales and v_scales, and bf16 rows")
     else:
         P = _pages4(k_cache, k_scales, v_cache, v_scales, Hkv, D)
-    B, pages = _lengths(x, cu_seqlens, ctx_lens, block_table, status)
+    B, pages = _lengths((x,), cu_seqlens, ctx_lens, block_table, status)
     dt = _dtype(x)
     if ws is None:
         ws = workspace(eagle_draft_prompt_workspace_size(B, T, d, Hq, Hkv, D, I, dt), x.device, stream)
@@ -863,15 +869,13 @@ def _per_request(settings, M, rows_per_request):
     for (name, dtype), t in zip((("temperature", _F32), ("top_k", _I32), ("top_p", _F32), ("min_p", _F32)), settings):
         if t is not None and not (t.shape == (n,) and t.dtype is dtype and t.is_contiguous()):
             raise ValueError(f"{name} must be contiguous {dtype} [{n}], an entry per request")
-        if t is not None and not t.is_cuda:
-            raise ValueError("the arrays must be on the GPU")
+    _on_gpu(*settings)
 
 
 def _per_row(name, t, M, dtype):
     if t is not None and not (t.shape == (M,) and t.dtype is dtype and t.is_contiguous()):
         raise ValueError(f"{name} must be contiguous {dtype} [{M}], an entry per row")
-    if t is not None and not t.is_cuda:
-        raise ValueError("the arrays must be on the GPU")
+    _on_gpu(t)
 
 
 def eagle_sample(logits, uniforms, tokens, temperature=None, top_k=None, top_p=None, min_p=None, rows_per_request=1,
@@ -889,8 +893,7 @@ def eagle_sample(logits, uniforms, tokens, temperature=None, top_k=None, top_p=N
     _per_row("logprobs", logprobs, M, _F32)
     _per_row("n_kept", n_kept, M, _I32)
     _per_request((temperature, top_k, top_p, min_p), M, rows_per_request)
-    if not logits.is_cuda:
-        raise ValueError("the arrays must be on the GPU")
+    _on_gpu(logits, status)
     _check("eagle_sample", lib().eagle_sample(
         logits.data_ptr(), stride, M, V, _dtype(logits), _addr(temperature), _addr(top_k), _addr(top_p), _addr(min_p),
         rows_per_request, uniforms.data_ptr(), tokens.data_ptr(), _addr(logprobs), _addr(n_kept), _addr(status),
@@ -910,8 +913,7 @@ def eagle_truncate_logits(logits, out, temperature=None, top_k=None, top_p=None,
         raise ValueError("status must be int32")
     _per_row("n_kept", n_kept, M, _I32)
     _per_request((temperature, top_k, top_p, min_p), M, rows_per_request)
-    if not (logits.is_cuda and out.is_cuda):
-        raise ValueError("the arrays must be on the GPU")
+    _on_gpu(logits, out, status)
     _check("eagle_truncate_logits", lib().eagle_truncate_logits(
         logits.data_ptr(), stride, M, V, _dtype(logits), _addr(temperature), _addr(top_k), _addr(top_p), _addr(min_p),
         rows_per_request, out.data_ptr(), out_stride, _addr(n_kept), _addr(status), _raw_stream(stream, logits.device)))

@@ -130,3 +130,35 @@ def test_scratch_of_a_prefix_is_the_streams(allocations, name, given):  # noqa: 
     allocations.clear()
     call(**alone, stream=s, ws=torch.zeros(16, dtype=torch.uint8))
     assert allocations == []
+
+
+def every_array():
+    """(call, its arguments, the name of one array): the arrays that a kernel writes, and the host's usual slips."""
+    named = {**CALLS, "sample": (eb.eagle_sample, sampling), "truncate": (eb.eagle_truncate_logits, truncating)}
+    for name, (call, base) in named.items():
+        for array, value in base().items():
+            written = array in ("out", "lse", "status", "q_out", "k_cache", "v_cache", "k_codes", "k_scales", "v_codes", "v_scales")
+            if isinstance(value, torch.Tensor) and (name in ("sample", "truncate") or (written and not (
+                    name.startswith("prefix") and array.startswith(("k_", "v_"))))):
+                yield pytest.param(call, base, array, id=f"{name}-{array}")
+
+
+@pytest.mark.parametrize("call,base,array", list(every_array()))
+def test_one_array_off_the_gpu_is_refused(call, base, array, monkeypatch):
+    """Before the library is called: the others pass for the GPU's."""
+    args, called = base(), []
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: called.append(name) or 0
+
+    monkeypatch.setattr(eb, "_lib", Lib())
+    monkeypatch.setattr(eb, "_raw_stream", lambda stream, device: 0)
+    monkeypatch.setattr(eb, "workspace", lambda *a: torch.zeros(16, dtype=torch.uint8))
+    monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda t: t is not args[array]))
+    with pytest.raises(ValueError, match="on the GPU"):
+        call(**args)
+    assert not called
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True)
+    call(**args)
+    assert called
