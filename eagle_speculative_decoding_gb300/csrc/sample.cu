@@ -14,9 +14,10 @@
 //
 // Where a sum passes a border (p times the sum, u times the sum) decides the
 // result, and with 10^5 entries the borders lie closer than fp32's rounding of
-// such sums.  So weights are whole numbers, w = round(2^44 e^((x - max) / T)), good
-// to 2^-36 of themselves, and their sums are exact 64-bit integers: no order of
-// summation, no atomics' order and no split of a row changes any result.
+// such sums.  So weights are whole numbers, w = round(2^44 e^((x - max) / T)), off by
+// half a unit and 2^-36 of themselves at most (below 2^-9 of the largest the half unit is the
+// larger part), and their sums are exact 64-bit integers: no order of summation, no
+// atomics' order and no split of a row changes any result.
 //
 // A row belongs to a cluster of 1 to 8 CTAs: contiguous ranges by CTA and warp, so
 // that running sums by index are sums over ranges.  Passes after the first read the

@@ -899,7 +899,10 @@ int eagle_prompt_attn_kv4(const void* q, long long q_stride, const uint8_t* k_co
  * Arithmetic and limits as eagle_prompt_attn (own_out is read in `dtype`: where
  * it was rounded to bf16 by another call, that rounding stays in it); G <= 1024.
  * A workspace of G and T serves every call of at most that many groups and rows,
- * any dtype and 4-bit pages: 41 MB at most with 152 SMs and D 128. */
+ * any dtype and 4-bit pages: 41 MB at most with 152 SMs and D 128.
+ * It is for a caller that makes a layer's calls one by one: eagle_draft_prompt and
+ * eagle_draft_layer rotate by the slot and attend to one table per request, so a drafter
+ * run by them needs the prefix in each request's own pages. */
 size_t eagle_prefix_attn_workspace_size(int G, int T, int Hq, int Hkv, int D);
 int eagle_prefix_attn(const void* q, long long q_stride, const void* k_cache, const void* v_cache,
                       int num_pages, const int32_t* prefix_table, int max_pages,
@@ -964,8 +967,8 @@ int eagle_draft_prompt(const void* x, const void* w_norm1, const void* w_qkv, co
  *   logprob = log(w_token / sum of the kept weights);  n_kept = entries kept.
  * T = 0: the first entry (log-prob 0, one kept) whatever the others say.
  * Entries of minus infinity are never kept.  Weights are whole multiples of 2^-44
- * (good to 2^-36 of themselves) with exact sums, so a result does not depend on
- * the order of summation; entries below 2^-45 weigh nothing, nor does one that
+ * (off by half of that and 2^-36 of themselves) with exact sums, so a result does not
+ * depend on the order of summation; entries below 2^-45 weigh nothing, nor does one that
  * lies further below the maximum than fp32 reaches.  (Sums are off by V 2^-45 at
  * most: where a top_p next to 1 ends among weights as small as that, it may end a
  * few entries from where the formula does.)
@@ -995,7 +998,7 @@ int eagle_sample(const void* logits, long long row_stride, int M, int V, int dty
  *   out : rows of V entries, out_stride elements apart, dtype `dtype`; may be
  *         `logits` itself (in place, with one stride)
  * A row in error is not written.  T = 0 keeps the first entry alone.  Everything
- * else as eagle_sample. */
+ * else as eagle_sample, its limit of V, which eagle_tree_verify does not have, too. */
 int eagle_truncate_logits(const void* logits, long long row_stride, int M, int V, int dtype,
                           const float* temperature, const int32_t* top_k, const float* top_p,
                           const float* min_p, int rows_per_request, void* out,
